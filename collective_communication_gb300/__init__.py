@@ -8,7 +8,8 @@ so that `collective_communication_gb300.inputs` stays importable without it.
 """
 _BINDING_NAMES = (
     "RarError", "Status", "Dtype", "Proto", "load_library", "library_path", "allreduce", "oneshot",
-    "workspace_bytes", "Workspace", "get_status", "strerror",
+    "workspace_bytes", "Workspace", "get_status", "strerror", "OpWorkspace", "page_tables", "qk_norm_rope",
+    "qk_norm_rope_cached", "qk_norm_rope_backward", "decode_attention", "token_logprobs", "token_logprobs_backward",
 )
 
 

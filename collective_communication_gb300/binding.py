@@ -25,6 +25,7 @@ class Status(enum.IntEnum):
     ERR_TIMEOUT = 7
     ERR_ABORT = 8
     ERR_BOUNDS = 9
+    ERR_CAPACITY = 10
 
 
 class Dtype(enum.IntEnum):
@@ -44,7 +45,10 @@ EXPORTED = (
     "rar_strerror", "rar_set_spin_timeout_ns", "rar_debug_set_fault", "rar_describe_geometry",
     "rar_allreduce_static", "rar_allreduce_ex", "rar_reduce_scatter", "rar_all_gather",
     "rar_oneshot_workspace_bytes", "rar_oneshot_workspace_init", "rar_oneshot_staged",
-    "rar_debug_set_ll_flag_wrap",
+    "rar_debug_set_ll_flag_wrap", "rar_op_workspace_init", "rar_page_tables", "rar_qk_norm_rope",
+    "rar_qk_norm_rope_cached", "rar_qk_norm_rope_workspace_bytes", "rar_qk_norm_rope_backward",
+    "rar_decode_attention_workspace_bytes", "rar_decode_attention", "rar_token_logprobs_workspace_bytes",
+    "rar_token_logprobs", "rar_token_logprobs_backward",
 )
 
 
@@ -107,6 +111,27 @@ def load_library():
     L.rar_oneshot_staged.restype = I
     L.rar_debug_set_ll_flag_wrap.argtypes = [ctypes.c_uint32]
     L.rar_debug_set_ll_flag_wrap.restype = I
+    I64, F = ctypes.c_int64, ctypes.c_float
+    L.rar_op_workspace_init.argtypes = [P, SZ, P]
+    L.rar_page_tables.argtypes = [P, P, I, P, I, P, I, I, P, I64, I, P, P, P, P, I, P, P, SZ, P]
+    rope = [P, I, I64, I64, P, P, P, I, I, I, P]
+    heads = [I, I, I, I, F]
+    L.rar_qk_norm_rope.argtypes = rope + heads + [P, I64, P, I64, P, SZ, P]
+    L.rar_qk_norm_rope_cached.argtypes = rope + [P] + heads + [P, I64, P, P, I, I, P, SZ, P]
+    L.rar_qk_norm_rope_backward.argtypes = rope + heads + [P, I64, P, I64, P, I64, P, I64, P, P, P, SZ, P]
+    L.rar_qk_norm_rope_workspace_bytes.argtypes = [I, I]
+    L.rar_decode_attention_workspace_bytes.argtypes = [I, I, I, I, I]
+    L.rar_decode_attention.argtypes = [P, I64, P, P, I, I, I, I, I, I, I, I, P, I64, I, P, F, P, I64, P, P, SZ, P]
+    L.rar_token_logprobs_workspace_bytes.argtypes = [I64, I]
+    L.rar_token_logprobs.argtypes = [P, P, P, I, I64, I, P, P, P, P, I, P, P, P, SZ, P]
+    L.rar_token_logprobs_backward.argtypes = [P, P, P, I, I64, I, P, P, P, P, P, P, P, P, SZ, P]
+    for name in ("rar_qk_norm_rope_workspace_bytes", "rar_decode_attention_workspace_bytes",
+                 "rar_token_logprobs_workspace_bytes"):
+        getattr(L, name).restype = SZ
+    for name in ("rar_op_workspace_init", "rar_page_tables", "rar_qk_norm_rope", "rar_qk_norm_rope_cached",
+                 "rar_qk_norm_rope_backward", "rar_decode_attention", "rar_token_logprobs",
+                 "rar_token_logprobs_backward"):
+        getattr(L, name).restype = I
     _lib = L
     return L
 
@@ -294,6 +319,307 @@ def oneshot_staged(sendbufs: Sequence, recvbufs: Sequence, workspace: OneShotWor
                                            int(_dtype_of(sendbufs[0])), 0, workspace.ptr, workspace.nbytes,
                                            _stream_handle(stream))
     _check(st, "rar_oneshot_staged")
+
+
+# ---- operators of a tensor-parallel step (heads and vocabulary split over the virtual ranks) ----
+# A per-rank argument is a sequence of nranks alike tensors, or one tensor whose
+# first dimension is the rank.
+
+OP_WORKSPACE_MIN_BYTES = 20480
+
+
+class OpWorkspace:
+    """Device workspace of the operators: the status word, arrival counters and
+    scratch. One serves any of them, ordered on one stream; nbytes is the
+    largest of their *_workspace_bytes (0: the minimum, enough for those
+    without one)."""
+
+    def __init__(self, nbytes: int = 0, device=None, stream=None):
+        import torch
+        self.nbytes = max(int(nbytes), OP_WORKSPACE_MIN_BYTES)
+        self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        self._ptr = (self.buf.data_ptr() + 255) // 256 * 256
+        self.init(stream)
+
+    def init(self, stream=None):
+        _check(load_library().rar_op_workspace_init(self._ptr, self.nbytes, _stream_handle(stream)),
+               "rar_op_workspace_init")
+
+    @property
+    def ptr(self) -> int:
+        return self._ptr
+
+
+def _op_bytes(fn, *args) -> int:
+    n = int(getattr(load_library(), fn)(*args))
+    if n == 0:
+        raise RarError(Status.ERR_ARG, fn)
+    return n
+
+
+def qk_norm_rope_workspace_bytes(nranks: int, head_dim: int) -> int:
+    """Workspace of qk_norm_rope_backward."""
+    return _op_bytes("rar_qk_norm_rope_workspace_bytes", nranks, head_dim)
+
+
+def decode_attention_workspace_bytes(nranks: int, batch: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return _op_bytes("rar_decode_attention_workspace_bytes", nranks, batch, q_heads, kv_heads, head_dim)
+
+
+def token_logprobs_workspace_bytes(rows: int, top: int) -> int:
+    return _op_bytes("rar_token_logprobs_workspace_bytes", rows, top)
+
+
+_OP_DTYPES = {}
+
+
+def _op_dtype(dtype) -> int:
+    if not _OP_DTYPES:
+        import torch
+        _OP_DTYPES.update({torch.float32: 0, torch.bfloat16: 1})
+    d = _OP_DTYPES.get(dtype)
+    if d is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    return d
+
+
+def _need(ok, what):
+    if not ok:
+        raise RarError(Status.ERR_ARG, what)
+
+
+def _ranked(x, name, dims):
+    """(C array of the ranks' pointers, nranks, shape, strides, dtype) of a per-rank argument."""
+    if isinstance(x, (list, tuple)):
+        n, first = len(x), x[0]
+        shape, strides, dtype = first.shape, first.stride(), first.dtype
+        _need(all(t.shape == shape and t.stride() == strides and t.dtype == dtype for t in x),
+              f"{name}: the ranks' tensors differ")
+        ptrs = [t.data_ptr() for t in x]
+        cuda = all(t.is_cuda for t in x)
+    else:
+        full, strides, dtype, cuda = x.shape, x.stride(), x.dtype, x.is_cuda
+        n, base, step = full[0], x.data_ptr(), strides[0] * x.element_size()
+        ptrs = [base + r * step for r in range(n)] if base else [None] * n
+        shape, strides = full[1:], strides[1:]
+    _need(cuda and len(shape) == dims, f"{name}: {dims} dimensions a rank, in device memory")
+    return (ctypes.c_void_p * n)(*ptrs), n, shape, strides, dtype
+
+
+def _packed(shape, strides, first):
+    """Whether the dimensions from `first` on lie densely in their order."""
+    want = 1
+    for i in range(len(shape) - 1, first - 1, -1):
+        if shape[i] != 1 and strides[i] != want:
+            return False
+        want *= shape[i]
+    return True
+
+
+def _row_stride(shape, strides, width):
+    return strides[0] if shape[0] > 1 else width
+
+
+def _ints(t, name, numel):
+    import torch
+    _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == numel,
+          f"{name}: {numel} contiguous int32 in device memory")
+    return t.data_ptr()
+
+
+def _floats(t, name, shape):
+    import torch
+    _need(t.dtype == torch.float32 and t.is_cuda and t.is_contiguous() and tuple(t.shape) == tuple(shape),
+          f"{name}: contiguous float32 {tuple(shape)} in device memory")
+    return t.data_ptr()
+
+
+def page_tables(lens, new_tokens, free_pages, free_count, block_table, page_size: int, num_pages: int, lens_out, starts,
+                positions, slots, free_count_out, workspace: OpWorkspace, stream=None) -> None:
+    """Enqueue one step's page tables and slot maps, from the requests' lengths
+    (int32 tensors): new entries of block_table [requests, max_blocks] in place,
+    lens_out, starts [requests + 1], positions and slots [most tokens of a
+    step], free_count_out [1]."""
+    n = lens.numel()
+    _need(block_table.dim() == 2 and block_table.shape[0] == n and block_table.is_cuda
+          and block_table.dtype == lens.dtype and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
+          "block_table: int32 [requests, max_blocks]")
+    blocks = block_table.shape[1]
+    tokens = slots.numel()
+    st = load_library().rar_page_tables(
+        _ints(lens, "lens", n), _ints(new_tokens, "new_tokens", n), n,
+        _ints(free_pages, "free_pages", free_pages.numel()), free_pages.numel(), _ints(free_count, "free_count", 1),
+        page_size, num_pages, block_table.data_ptr(), block_table.stride(0) if n > 1 else blocks, blocks,
+        _ints(lens_out, "lens_out", n), _ints(starts, "starts", n + 1), _ints(positions, "positions", tokens),
+        _ints(slots, "slots", tokens), tokens, _ints(free_count_out, "free_count_out", 1), workspace.ptr,
+        workspace.nbytes, _stream_handle(stream))
+    _check(st, "rar_page_tables")
+
+
+def _rope_call(qkv, q_weight, k_weight, cos_sin, positions, q, kv_heads):
+    """What the forms of the norm and rotation share: qkv [tokens, (q + 2 kv heads) * head_dim] against
+    q [tokens, q_heads, head_dim]."""
+    import torch
+    qkv_p, n, shape, strides, dtype = qkv
+    q_p, qn, qshape, qstrides, qdtype = q
+    tokens, q_heads, dim = qshape
+    width = (q_heads + 2 * kv_heads) * dim
+    _need(qn == n and qdtype == dtype and shape[0] == tokens and shape[1] == width and _packed(shape, strides, 1)
+          and _packed(qshape, qstrides, 1), "qkv: [tokens, (q_heads + 2 kv_heads) head_dim], queries [tokens, q_heads, "
+          "head_dim], of one dtype")
+    for t in (q_weight, k_weight):
+        _need(t.dtype == dtype and t.is_cuda and t.is_contiguous() and t.numel() == dim,
+              "weights: head_dim elements of qkv's dtype")
+    _need(cos_sin.dtype == torch.float32 and cos_sin.is_cuda and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
+          "cos_sin: contiguous float32 [max_pos, rot_dim]")
+    return (qkv_p, n, tokens, _row_stride(shape, strides, width), q_weight.data_ptr(), k_weight.data_ptr(),
+            cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]), _ints(positions, "positions", tokens), \
+        (q_heads, kv_heads, dim, _op_dtype(dtype))
+
+
+def qk_norm_rope(qkv, q_weight, k_weight, cos_sin, positions, q_out, k_out, workspace: OpWorkspace, eps: float = 1e-6,
+                 interleaved: bool = False, stream=None) -> None:
+    """Enqueue the norm and rotation of every rank's queries and keys: q_out
+    [tokens, q_heads, head_dim] and k_out [tokens, kv_heads, head_dim] a rank."""
+    q, k = _ranked(q_out, "q_out", 3), _ranked(k_out, "k_out", 3)
+    head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, k[2][1])
+    _need(k[1] == q[1] and k[4] == q[4] and k[2][0] == q[2][0] and k[2][2] == q[2][2] and _packed(k[2], k[3], 1),
+          "k_out: [tokens, kv_heads, head_dim]")
+    st = load_library().rar_qk_norm_rope(
+        *head, int(interleaved), pos, *heads, eps, q[0], _row_stride(q[2], q[3], heads[0] * heads[2]), k[0],
+        _row_stride(k[2], k[3], heads[1] * heads[2]), workspace.ptr, workspace.nbytes, _stream_handle(stream))
+    _check(st, "rar_qk_norm_rope")
+
+
+def qk_norm_rope_cached(qkv, q_weight, k_weight, cos_sin, positions, slots, q_out, k_cache, v_cache,
+                        workspace: OpWorkspace, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """Enqueue the norm and rotation, keys and values into the paged caches
+    [num_pages, kv_heads, page_size, head_dim] a rank at slots."""
+    q, k, v = _ranked(q_out, "q_out", 3), _ranked(k_cache, "k_cache", 4), _ranked(v_cache, "v_cache", 4)
+    pages, kv_heads, page, dim = k[2]
+    head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, kv_heads)
+    _need(k[1] == v[1] == q[1] and k[4] == v[4] == q[4] and k[2] == v[2] and dim == heads[2]
+          and _packed(k[2], k[3], 0) and _packed(v[2], v[3], 0),
+          "k_cache, v_cache: contiguous [num_pages, kv_heads, page_size, head_dim]")
+    st = load_library().rar_qk_norm_rope_cached(
+        *head, int(interleaved), pos, _ints(slots, "slots", q[2][0]), *heads, eps, q[0],
+        _row_stride(q[2], q[3], heads[0] * dim), k[0], v[0], pages, page, workspace.ptr, workspace.nbytes,
+        _stream_handle(stream))
+    _check(st, "rar_qk_norm_rope_cached")
+
+
+def qk_norm_rope_backward(qkv, q_weight, k_weight, cos_sin, positions, dq, dk, dv, dqkv, dq_weight, dk_weight,
+                          workspace: OpWorkspace, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """Enqueue the gradient: dqkv (as qkv) and float32 dq_weight, dk_weight
+    [head_dim] a rank from dq [tokens, q_heads, head_dim], dk and dv [tokens,
+    kv_heads, head_dim]."""
+    import torch
+    q, k, v = _ranked(dq, "dq", 3), _ranked(dk, "dk", 3), _ranked(dv, "dv", 3)
+    x, d = _ranked(qkv, "qkv", 2), _ranked(dqkv, "dqkv", 2)
+    head, pos, heads = _rope_call(x, q_weight, k_weight, cos_sin, positions, q, k[2][1])
+    wide = heads[1] * heads[2]
+    _need(k[1] == v[1] == q[1] and k[4] == v[4] == q[4] and k[2] == v[2] and k[2][0] == q[2][0]
+          and k[2][2] == heads[2] and _packed(k[2], k[3], 1) and _packed(v[2], v[3], 1),
+          "dk, dv: [tokens, kv_heads, head_dim]")
+    _need(d[1] == x[1] and d[2] == x[2] and d[4] == x[4] and _packed(d[2], d[3], 1), "dqkv: as qkv")
+    wq, wk = _ranked(dq_weight, "dq_weight", 1), _ranked(dk_weight, "dk_weight", 1)
+    for w in (wq, wk):
+        _need(w[1] == x[1] and w[2][0] == heads[2] and w[4] == torch.float32 and _packed(w[2], w[3], 0),
+              "dq_weight, dk_weight: float32 [head_dim]")
+    st = load_library().rar_qk_norm_rope_backward(
+        *head, int(interleaved), pos, *heads, eps, q[0], _row_stride(q[2], q[3], heads[0] * heads[2]), k[0],
+        _row_stride(k[2], k[3], wide), v[0], _row_stride(v[2], v[3], wide), d[0],
+        _row_stride(d[2], d[3], d[2][1]), wq[0], wk[0], workspace.ptr, workspace.nbytes, _stream_handle(stream))
+    _check(st, "rar_qk_norm_rope_backward")
+
+
+def decode_attention(q, k_cache, v_cache, block_table, lens, out, lse, workspace: OpWorkspace,
+                     scale: Optional[float] = None, stream=None) -> None:
+    """Enqueue attention of one new token per request: q, out [batch, q_heads,
+    head_dim] a rank, caches as qk_norm_rope_cached writes them, int32
+    block_table [batch, max_blocks] and lens [batch]; lse float32 [batch,
+    q_heads] a rank, or None. scale: head_dim ** -0.5 by default."""
+    import torch
+    x, k, v, o = _ranked(q, "q", 3), _ranked(k_cache, "k_cache", 4), _ranked(v_cache, "v_cache", 4), \
+        _ranked(out, "out", 3)
+    batch, q_heads, dim = x[2]
+    pages, kv_heads, page, kdim = k[2]
+    _need(x[1] == k[1] == v[1] == o[1] and x[4] == k[4] == v[4] == o[4] and k[2] == v[2] and o[2] == x[2]
+          and kdim == dim and _packed(k[2], k[3], 0) and _packed(v[2], v[3], 0) and _packed(x[2], x[3], 1)
+          and _packed(o[2], o[3], 1),
+          "q, out: [batch, q_heads, head_dim]; caches: contiguous [num_pages, kv_heads, page_size, head_dim]")
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == batch
+          and block_table.is_cuda and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
+          "block_table: int32 [batch, max_blocks]")
+    blocks = block_table.shape[1]
+    lse_p = None
+    if lse is not None:
+        e = _ranked(lse, "lse", 2)
+        _need(e[1] == x[1] and e[2][0] == batch and e[2][1] == q_heads and e[4] == torch.float32
+              and _packed(e[2], e[3], 0), "lse: contiguous float32 [batch, q_heads]")
+        lse_p = e[0]
+    st = load_library().rar_decode_attention(
+        x[0], _row_stride(x[2], x[3], q_heads * dim), k[0], v[0], x[1], batch, q_heads, kv_heads, dim,
+        _op_dtype(x[4]), pages, page, block_table.data_ptr(), block_table.stride(0) if batch > 1 else blocks, blocks,
+        _ints(lens, "lens", batch), dim ** -0.5 if scale is None else scale, o[0],
+        _row_stride(o[2], o[3], q_heads * dim), lse_p, workspace.ptr, workspace.nbytes, _stream_handle(stream))
+    _check(st, "rar_decode_attention")
+
+
+def _shards(x, name):
+    """(pointers, vocabulary of each shard, row strides, nranks, rows, dtype); shards may differ in width."""
+    parts = list(x) if isinstance(x, (list, tuple)) else None
+    if parts is None:
+        p, n, shape, strides, dtype = _ranked(x, name, 2)
+        widths, steps = [shape[1]] * n, [_row_stride(shape, strides, shape[1])] * n
+        rows, dense = shape[0], shape[1] == 1 or strides[1] == 1
+    else:
+        n, rows, dtype = len(parts), parts[0].shape[0], parts[0].dtype
+        _need(all(t.dim() == 2 and t.shape[0] == rows and t.dtype == dtype and t.is_cuda for t in parts),
+              f"{name}: [rows, vocabulary of the shard], of one dtype, in device memory")
+        p = _ptrs(parts)
+        widths = [t.shape[1] for t in parts]
+        steps = [_row_stride(t.shape, t.stride(), t.shape[1]) for t in parts]
+        dense = all(t.shape[1] == 1 or t.stride(1) == 1 for t in parts)
+    _need(dense, f"{name}: the words of a row lie together")
+    return p, (ctypes.c_int64 * n)(*widths), (ctypes.c_int64 * n)(*steps), n, rows, dtype
+
+
+def token_logprobs(logits, tokens, logprob, entropy, lse, top_values, top_ids, workspace: OpWorkspace,
+                   stream=None) -> None:
+    """Enqueue log probabilities of int32 tokens [rows] over vocabulary shards
+    logits [rows, shard] a rank: float32 logprob, entropy, lse [rows] and the top
+    alternatives' float32 top_values and int32 top_ids [rows, top] (None, or top
+    0: none)."""
+    p, vocab, steps, n, rows, dtype = _shards(logits, "logits")
+    top = 0 if top_ids is None else top_ids.shape[1]
+    values_p = ids_p = None
+    if top:
+        values_p = _floats(top_values, "top_values", (rows, top))
+        ids_p = _ints(top_ids, "top_ids", rows * top)
+    one = (rows,)
+    st = load_library().rar_token_logprobs(
+        p, vocab, steps, n, rows, _op_dtype(dtype), _ints(tokens, "tokens", rows), _floats(logprob, "logprob", one),
+        _floats(entropy, "entropy", one), _floats(lse, "lse", one), top, values_p, ids_p, workspace.ptr,
+        workspace.nbytes, _stream_handle(stream))
+    _check(st, "rar_token_logprobs")
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_entropy, dlogits, workspace: OpWorkspace,
+                            stream=None) -> None:
+    """Enqueue the gradient with respect to the logits, from lse and entropy of
+    token_logprobs and float32 gradients [rows] (grad_entropy None: no such
+    term); dlogits as logits (in place is allowed)."""
+    p, vocab, steps, n, rows, dtype = _shards(logits, "logits")
+    dp, dvocab, dsteps, dn, drows, ddtype = _shards(dlogits, "dlogits")
+    _need(dn == n and drows == rows and ddtype == dtype and list(dvocab) == list(vocab), "dlogits: as logits")
+    one = (rows,)
+    st = load_library().rar_token_logprobs_backward(
+        p, vocab, steps, n, rows, _op_dtype(dtype), _ints(tokens, "tokens", rows), _floats(lse, "lse", one),
+        _floats(entropy, "entropy", one), _floats(grad_logprob, "grad_logprob", one),
+        None if grad_entropy is None else _floats(grad_entropy, "grad_entropy", one), dp, dsteps, workspace.ptr,
+        workspace.nbytes, _stream_handle(stream))
+    _check(st, "rar_token_logprobs_backward")
 
 
 def get_status(workspace, stream=None) -> Status:

@@ -17,8 +17,9 @@ LIB = os.path.join(HERE, "librar.so")
 # the debug variant: the same sources with RAR_DEBUG (device-side slice bounds checks)
 BUILD_DEBUG = os.path.join(HERE, "_build", "debug")
 LIB_DEBUG = os.path.join(HERE, "librar_debug.so")
-SOURCES = ["rar_api.cu", "ring_simple.cu", "ring_ll.cu", "oneshot.cu", "oneshot_staged.cu", "rar_static_ws.cu"]
-HEADERS = ["rar_device.cuh", "rar_geometry.h", "rar_launch.h"]
+SOURCES = ["rar_api.cu", "ring_simple.cu", "ring_ll.cu", "oneshot.cu", "oneshot_staged.cu", "rar_static_ws.cu",
+           "rar_ops_api.cu", "page_tables.cu", "qk_norm_rope.cu", "decode_attention.cu", "token_logprobs.cu"]
+HEADERS = ["rar_device.cuh", "rar_geometry.h", "rar_launch.h", "op_common.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [

@@ -62,7 +62,8 @@ typedef enum rar_status {
   RAR_ERR_CUDA = 6,        /* a CUDA runtime call failed */
   RAR_ERR_TIMEOUT = 7,     /* device: a wait ran past its time limit; the kernel gave up */
   RAR_ERR_ABORT = 8,       /* device: the workspace was aborted by an earlier failure */
-  RAR_ERR_BOUNDS = 9       /* device, debug library only: a slice fell outside its buffers */
+  RAR_ERR_BOUNDS = 9,      /* device, debug library only: a slice fell outside its buffers */
+  RAR_ERR_CAPACITY = 10    /* device, operators: a length, page, slot or position does not fit */
 } rar_status;
 
 typedef enum rar_dtype { RAR_F32 = 0, RAR_BF16 = 1 } rar_dtype;
@@ -385,6 +386,182 @@ RAR_API rar_status rar_debug_set_ll_flag_wrap(uint32_t flag_max);
  */
 RAR_API rar_status rar_describe_geometry(int nranks, size_t count, rar_dtype dtype, uint64_t channelMask,
                                  rar_proto proto, size_t buffSize, int chunkSteps, int64_t* out);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of a tensor-parallel model's step, around the collectives
+ * ---------------------------------------------------------------------------
+ * The virtual ranks of a tensor-parallel model each hold some heads of every
+ * attention layer and a range of the vocabulary. The operators below compute
+ * what the collectives then reduce, for all nranks ranks (1 to RAR_MAX_RANKS)
+ * in one launch: a rank's tensor is one entry of a host array of nranks device
+ * pointers; request lengths, page tables, positions and norm weights are shared
+ * by the ranks. The conventions at the head of this file hold: the caller owns
+ * all memory, argument errors return synchronously and enqueue nothing, the
+ * call does not wait. What only the device can see (lengths, positions, page
+ * and slot numbers) is checked there: nothing is read or written out of range,
+ * and rar_get_status() on the call's workspace reports RAR_ERR_CAPACITY. That
+ * status does not abort the workspace; later calls run.
+ *
+ * Layouts (strides count elements; the last dimension is contiguous; rows of
+ * tensors of RAR_F32 or RAR_BF16 start on 16-byte boundaries unless said
+ * otherwise):
+ *   qkv       [tokens, q_heads + 2 kv_heads, head_dim], tokens qkv_stride apart
+ *   k_cache,  [num_pages, kv_heads, page_size, head_dim] contiguous: a page
+ *   v_cache   holds page_size tokens (a power of two, 1 to 1024), and a head's
+ *             tokens of a page lie together. Slot s is token s % page_size of
+ *             page s / page_size; num_pages * page_size < 2^31.
+ *   block_table  int32 [requests, max_blocks], rows table_stride apart: entry c
+ *             is the page of the request's tokens c * page_size and up. Entries
+ *             past the request's length are not read.
+ * head_dim is a multiple of 8 up to 256; q_heads and kv_heads up to 1024. Sums,
+ * norms and softmax statistics are binary32; results are rounded once. A call's
+ * outputs may not overlap each other, its inputs or the workspace except where
+ * in place is allowed.
+ *
+ * Workspace: rar_op_workspace_init() prepares one (256-byte aligned, at least
+ * RAR_OP_WORKSPACE_MIN_BYTES, and what the *_workspace_bytes function of each
+ * operator used with it says; an operator without one needs the minimum). It
+ * serves any of these operators, at any sizes it has room for, in any order on
+ * one stream; nothing carries over from call to call.
+ */
+#define RAR_OP_WORKSPACE_MIN_BYTES 20480
+RAR_API rar_status rar_op_workspace_init(void* workspace, size_t workspaceBytes, void* stream);
+
+/*
+ * Block tables and slot maps of one step, from the requests' lengths. Request
+ * r has lens[r] tokens cached and adds new_tokens[r] (0 is allowed). It takes
+ * the pages that its new tokens need beyond those its table row already lists,
+ * in request order, from the end of the stack of free pages: the k-th page
+ * handed out is free_pages[*free_count - 1 - k]. Written:
+ *   block_table   the new entries of each row (in place; nothing else)
+ *   lens_out[r]   lens[r] + new_tokens[r]
+ *   starts[r]     first new token of request r in the step (num_requests + 1
+ *                 entries; the last is the total)
+ *   positions[t]  position of the step's token t in its request
+ *   slots[t]      its cache slot; for t past the total, up to max_tokens: slot
+ *                 -1, position 0, so a captured graph may run with any total
+ *   *free_count_out  pages left on the stack
+ * free_pages (num_free entries) is not changed: a caller that ends a request
+ * writes its pages back behind the new count. A request that does not fit
+ * whole -- free pages, its table row, max_tokens -- or whose length or count is
+ * negative gets nothing: its slots are -1, lens_out[r] is lens[r], and the
+ * status is RAR_ERR_CAPACITY; so are later requests that would need what it
+ * could not get. A negative or too long one also counts no tokens in starts.
+ * A page number outside 0..num_pages-1 gives slot -1 and the same status.
+ */
+RAR_API rar_status rar_page_tables(const int32_t* lens, const int32_t* new_tokens, int num_requests,
+                                   const int32_t* free_pages, int num_free, const int32_t* free_count, int page_size,
+                                   int num_pages, int32_t* block_table, int64_t table_stride, int max_blocks,
+                                   int32_t* lens_out, int32_t* starts, int32_t* positions, int32_t* slots,
+                                   int max_tokens, int32_t* free_count_out, void* workspace, size_t workspaceBytes,
+                                   void* stream);
+
+/*
+ * Root-mean-square norm of every query and key head and rotary positions, in
+ * one pass over qkv: y = R(x / sqrt(mean(x^2) + eps) * weight), where R turns
+ * the pairs (i, i + rot_dim/2) -- or (2i, 2i+1) if interleaved -- of the first
+ * rot_dim elements of a head by the angles of the token's position:
+ * (a, b) -> (a cos - b sin, b cos + a sin). cos_sin is float
+ * [max_pos, rot_dim], rot_dim/2 cosines then rot_dim/2 sines a row (any scaling
+ * for long contexts is in the table); rot_dim is a multiple of 16 up to
+ * head_dim. q_weight and k_weight: head_dim elements of dtype. positions:
+ * int32 [tokens]; one outside 0..max_pos-1 counts as 0 and reports
+ * RAR_ERR_CAPACITY.
+ *
+ * rar_qk_norm_rope: queries to q_out[r] [tokens, q_heads, head_dim] and keys to
+ *   k_out[r] [tokens, kv_heads, head_dim]; values are not touched.
+ * rar_qk_norm_rope_cached: queries to q_out[r]; keys and values to the cache
+ *   rows of slots (int32 [tokens]; a negative slot is a padding token, whose
+ *   query is written and whose key and value are not; one past the cache
+ *   reports RAR_ERR_CAPACITY and is not written). Two tokens of one slot: one
+ *   of them is kept.
+ * Both: q_out[r] == qkv[r] with q_stride == qkv_stride (queries in place) is
+ *   allowed. tokens 0 enqueues nothing.
+ * rar_qk_norm_rope_backward: from the gradients dq, dk, dv of y and of the
+ *   values, dqkv[r] (all of it; dv is copied) and the sums over the rank's
+ *   tokens and heads dq_weight[r], dk_weight[r] (float [head_dim]; the ranks'
+ *   sums are left for an AllReduce). The same bits every time. tokens 0 writes
+ *   zero weight gradients.
+ */
+RAR_API rar_status rar_qk_norm_rope(const void* const* qkv, int nranks, int64_t tokens, int64_t qkv_stride,
+                                    const void* q_weight, const void* k_weight, const float* cos_sin, int max_pos,
+                                    int rot_dim, int interleaved, const int32_t* positions, int q_heads, int kv_heads,
+                                    int head_dim, rar_dtype dtype, float eps, void* const* q_out, int64_t q_stride,
+                                    void* const* k_out, int64_t k_stride, void* workspace, size_t workspaceBytes,
+                                    void* stream);
+RAR_API rar_status rar_qk_norm_rope_cached(const void* const* qkv, int nranks, int64_t tokens, int64_t qkv_stride,
+                                           const void* q_weight, const void* k_weight, const float* cos_sin,
+                                           int max_pos, int rot_dim, int interleaved, const int32_t* positions,
+                                           const int32_t* slots, int q_heads, int kv_heads, int head_dim,
+                                           rar_dtype dtype, float eps, void* const* q_out, int64_t q_stride,
+                                           void* const* k_cache, void* const* v_cache, int num_pages, int page_size,
+                                           void* workspace, size_t workspaceBytes, void* stream);
+RAR_API size_t rar_qk_norm_rope_workspace_bytes(int nranks, int head_dim); /* of the backward call; 0: bad arguments */
+RAR_API rar_status rar_qk_norm_rope_backward(const void* const* qkv, int nranks, int64_t tokens, int64_t qkv_stride,
+                                             const void* q_weight, const void* k_weight, const float* cos_sin,
+                                             int max_pos, int rot_dim, int interleaved, const int32_t* positions,
+                                             int q_heads, int kv_heads, int head_dim, rar_dtype dtype, float eps,
+                                             const void* const* dq, int64_t dq_stride, const void* const* dk,
+                                             int64_t dk_stride, const void* const* dv, int64_t dv_stride,
+                                             void* const* dqkv, int64_t dqkv_stride, float* const* dq_weight,
+                                             float* const* dk_weight, void* workspace, size_t workspaceBytes,
+                                             void* stream);
+
+/*
+ * Attention of one new token per request over the paged cache. Query head h of
+ * request b (q[r], [batch, q_heads, head_dim]) attends to tokens 0..lens[b]-1
+ * of key head h / (q_heads / kv_heads) (q_heads a multiple of kv_heads):
+ *   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = log sum_t exp(scale * q . k_t)
+ * lens[b] counts the new token, whose key and value are in the cache already.
+ * A request of length 0 gives out 0 and lse -inf. Cache rows past a length may
+ * hold anything, infinities and NaN too. A key or value of a valid token that
+ * is infinite or NaN makes its heads' results infinite or NaN. A page number
+ * outside 0..num_pages-1 within a length, or a length past the table row,
+ * reports RAR_ERR_CAPACITY; the tokens concerned are left out.
+ * lse: host array of nranks pointers to float [batch, q_heads], or NULL.
+ * The work is split over the cache's length: the same bits every time for the
+ * same lengths on the same GPU model.
+ */
+RAR_API size_t rar_decode_attention_workspace_bytes(int nranks, int batch, int q_heads, int kv_heads, int head_dim);
+RAR_API rar_status rar_decode_attention(const void* const* q, int64_t q_stride, const void* const* k_cache,
+                                        const void* const* v_cache, int nranks, int batch, int q_heads, int kv_heads,
+                                        int head_dim, rar_dtype dtype, int num_pages, int page_size,
+                                        const int32_t* block_table, int64_t table_stride, int max_blocks,
+                                        const int32_t* lens, float scale, void* const* out, int64_t out_stride,
+                                        float* const* lse, void* workspace, size_t workspaceBytes, void* stream);
+
+/*
+ * Log probabilities over vocabulary shards that are never gathered. Rank r
+ * holds vocab[r] columns of every row, logits[r] [rows, vocab[r]], rows
+ * row_strides[r] apart (host arrays; a row may start on any element); column j
+ * of rank r is word vocab[0] + .. + vocab[r-1] + j. For each row x:
+ *   lse = log sum_i exp(x_i);  logprob = x[token] - lse;
+ *   entropy = -sum_i p_i log p_i, p = exp(x - lse), where p_i = 0 adds nothing;
+ *   the top (0 to 32, at most the vocabulary) words by x, the lower index first
+ *   among equal values: top_values[row, k] = x - lse, top_ids[row, k].
+ * tokens: int32 [rows]; one outside the vocabulary (-1, say) asks for nothing:
+ * logprob 0. Words of -inf have probability 0. A row with a NaN or +inf, or with
+ * nothing but -inf, has NaN results; a NaN ranks above every number.
+ *
+ * rar_token_logprobs_backward: the gradient with respect to the logits of
+ *   sum(grad_logprob * logprob) + sum(grad_entropy * entropy) from lse and
+ *   entropy of the forward call (grad_entropy NULL: no such term):
+ *   dx_i = grad_logprob ([i == token] - p_i) - grad_entropy p_i (log p_i + entropy).
+ *   grad_logprob of a row that asks for nothing is not read as a gradient.
+ *   dlogits[r] == logits[r] with one stride (in place) is allowed.
+ */
+RAR_API size_t rar_token_logprobs_workspace_bytes(int64_t rows, int top);
+RAR_API rar_status rar_token_logprobs(const void* const* logits, const int64_t* vocab, const int64_t* row_strides,
+                                      int nranks, int64_t rows, rar_dtype dtype, const int32_t* tokens, float* logprob,
+                                      float* entropy, float* lse, int top, float* top_values, int32_t* top_ids,
+                                      void* workspace, size_t workspaceBytes, void* stream);
+RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const int64_t* vocab,
+                                               const int64_t* row_strides, int nranks, int64_t rows, rar_dtype dtype,
+                                               const int32_t* tokens, const float* lse, const float* entropy,
+                                               const float* grad_logprob, const float* grad_entropy,
+                                               void* const* dlogits, const int64_t* drow_strides, void* workspace,
+                                               size_t workspaceBytes, void* stream);
 
 #ifdef __cplusplus
 }
