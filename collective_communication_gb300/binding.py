@@ -7,6 +7,7 @@ If the library is missing the binding raises -- there is no fallback path.
 import ctypes
 import enum
 import os
+import struct
 from typing import Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -338,16 +339,13 @@ class OpWorkspace:
         import torch
         self.nbytes = max(int(nbytes), OP_WORKSPACE_MIN_BYTES)
         self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
-        self._ptr = (self.buf.data_ptr() + 255) // 256 * 256
+        self.ptr = (self.buf.data_ptr() + 255) // 256 * 256
         self.init(stream)
 
     def init(self, stream=None):
-        _check(load_library().rar_op_workspace_init(self._ptr, self.nbytes, _stream_handle(stream)),
+        """(Re-)initialise: clear the status word and the counters."""
+        _check(load_library().rar_op_workspace_init(self.ptr, self.nbytes, _stream_handle(stream)),
                "rar_op_workspace_init")
-
-    @property
-    def ptr(self) -> int:
-        return self._ptr
 
 
 def _op_bytes(fn, *args) -> int:
@@ -370,68 +368,119 @@ def token_logprobs_workspace_bytes(rows: int, top: int) -> int:
     return _op_bytes("rar_token_logprobs_workspace_bytes", rows, top)
 
 
-_OP_DTYPES = {}
+# A decode step makes these calls once a layer, so their checks are written for
+# few Python operations: _op_setup binds once what each call needs of torch.
+_ops = None
+
+
+def _op_setup():
+    global _ops, _INT32, _FLOAT32, _OP_DTYPES, _raw_stream, _current_device
+    import torch
+    _INT32, _FLOAT32 = torch.int32, torch.float32
+    _OP_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+    if torch.cuda.is_available():
+        torch.cuda.init()
+        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _ops = load_library()
+    return _ops
+
+
+def _op_stream(stream) -> int:
+    return _raw_stream(_current_device()) if stream is None else _stream_handle(stream)
 
 
 def _op_dtype(dtype) -> int:
-    if not _OP_DTYPES:
-        import torch
-        _OP_DTYPES.update({torch.float32: 0, torch.bfloat16: 1})
     d = _OP_DTYPES.get(dtype)
     if d is None:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
     return d
 
 
-def _need(ok, what):
-    if not ok:
-        raise RarError(Status.ERR_ARG, what)
+def _refuse(what):
+    raise RarError(Status.ERR_ARG, what)
+
+
+_PACK = [struct.Struct(f"{n}Q").pack for n in range(33)]  # nranks pointers, or 64-bit counts, as a C array
+
+
+def _pack(values):
+    n = len(values)
+    return _PACK[n](*values) if n <= 32 else struct.pack(f"{n}Q", *values)
 
 
 def _ranked(x, name, dims):
-    """(C array of the ranks' pointers, nranks, shape, strides, dtype) of a per-rank argument."""
-    if isinstance(x, (list, tuple)):
-        n, first = len(x), x[0]
+    """A per-rank argument as (C array of the ranks' pointers, nranks, shape of
+    a rank's tensor, its row stride, dtype); the dimensions after a row's are
+    dense."""
+    if type(x) is list or type(x) is tuple:
+        first = x[0]
         shape, strides, dtype = first.shape, first.stride(), first.dtype
-        _need(all(t.shape == shape and t.stride() == strides and t.dtype == dtype for t in x),
-              f"{name}: the ranks' tensors differ")
-        ptrs = [t.data_ptr() for t in x]
-        cuda = all(t.is_cuda for t in x)
+        for t in x:
+            if t.shape != shape or t.stride() != strides or t.dtype is not dtype or not t.is_cuda:
+                _refuse(f"{name}: the ranks' tensors are alike and in device memory")
+        n, ptrs = len(x), _pack([t.data_ptr() for t in x])
     else:
-        full, strides, dtype, cuda = x.shape, x.stride(), x.dtype, x.is_cuda
-        n, base, step = full[0], x.data_ptr(), strides[0] * x.element_size()
-        ptrs = [base + r * step for r in range(n)] if base else [None] * n
-        shape, strides = full[1:], strides[1:]
-    _need(cuda and len(shape) == dims, f"{name}: {dims} dimensions a rank, in device memory")
-    return (ctypes.c_void_p * n)(*ptrs), n, shape, strides, dtype
+        full = x.shape
+        n, shape, dtype = full[0], full[1:], x.dtype
+        if not x.is_cuda or n == 0:
+            _refuse(f"{name}: a tensor in device memory for each rank")
+        base = x.data_ptr()
+        if x.is_contiguous():
+            if len(shape) != dims:
+                _refuse(f"{name}: {dims} dimensions a rank")
+            step = x.nbytes // n
+            ptrs = _pack(range(base, base + n * step, step) if step else [base] * n)
+            width = 1
+            for d in shape[1:]:
+                width *= d
+            return ptrs, n, shape, width, dtype
+        strides = x.stride()
+        step = strides[0] * x.element_size()
+        ptrs, strides = _pack([base + r * step for r in range(n)]), strides[1:]
+    if len(shape) != dims:
+        _refuse(f"{name}: {dims} dimensions a rank")
+    width = 1
+    for i in range(dims - 1, 0, -1):
+        if shape[i] != 1 and strides[i] != width:
+            _refuse(f"{name}: dense after its first dimension")
+        width *= shape[i]
+    return ptrs, n, shape, strides[0] if shape[0] > 1 else width, dtype
 
 
-def _packed(shape, strides, first):
-    """Whether the dimensions from `first` on lie densely in their order."""
-    want = 1
-    for i in range(len(shape) - 1, first - 1, -1):
-        if shape[i] != 1 and strides[i] != want:
-            return False
-        want *= shape[i]
-    return True
-
-
-def _row_stride(shape, strides, width):
-    return strides[0] if shape[0] > 1 else width
+def _ranked_dense(x, name, dims):
+    """_ranked of tensors without gaps."""
+    r = _ranked(x, name, dims)
+    width = 1
+    for d in r[2][1:]:
+        width *= d
+    if r[3] != width:
+        _refuse(f"{name}: contiguous")
+    return r
 
 
 def _ints(t, name, numel):
-    import torch
-    _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == numel,
-          f"{name}: {numel} contiguous int32 in device memory")
+    if t.dtype is not _INT32 or t.numel() != numel or not t.is_contiguous() or not t.is_cuda:
+        _refuse(f"{name}: {numel} contiguous int32 in device memory")
     return t.data_ptr()
 
 
-def _floats(t, name, shape):
-    import torch
-    _need(t.dtype == torch.float32 and t.is_cuda and t.is_contiguous() and tuple(t.shape) == tuple(shape),
-          f"{name}: contiguous float32 {tuple(shape)} in device memory")
+def _floats(t, name, numel):
+    if t.dtype is not _FLOAT32 or t.numel() != numel or not t.is_contiguous() or not t.is_cuda:
+        _refuse(f"{name}: {numel} contiguous float32 in device memory")
     return t.data_ptr()
+
+
+def _table(t, rows):
+    """(pointer, row stride, columns) of a block table."""
+    shape = t.shape
+    if t.dtype is not _INT32 or len(shape) != 2 or shape[0] != rows or not t.is_cuda:
+        _refuse("block_table: int32 [requests, max_blocks] in device memory")
+    blocks = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), blocks, blocks
+    if blocks != 1 and t.stride(1) != 1:
+        _refuse("block_table: dense rows")
+    return t.data_ptr(), t.stride(0) if rows > 1 else blocks, blocks
 
 
 def page_tables(lens, new_tokens, free_pages, free_count, block_table, page_size: int, num_pages: int, lens_out, starts,
@@ -440,72 +489,67 @@ def page_tables(lens, new_tokens, free_pages, free_count, block_table, page_size
     (int32 tensors): new entries of block_table [requests, max_blocks] in place,
     lens_out, starts [requests + 1], positions and slots [most tokens of a
     step], free_count_out [1]."""
-    n = lens.numel()
-    _need(block_table.dim() == 2 and block_table.shape[0] == n and block_table.is_cuda
-          and block_table.dtype == lens.dtype and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
-          "block_table: int32 [requests, max_blocks]")
-    blocks = block_table.shape[1]
-    tokens = slots.numel()
-    st = load_library().rar_page_tables(
-        _ints(lens, "lens", n), _ints(new_tokens, "new_tokens", n), n,
-        _ints(free_pages, "free_pages", free_pages.numel()), free_pages.numel(), _ints(free_count, "free_count", 1),
-        page_size, num_pages, block_table.data_ptr(), block_table.stride(0) if n > 1 else blocks, blocks,
+    lib = _ops or _op_setup()
+    n, tokens, free = lens.numel(), slots.numel(), free_pages.numel()
+    table, stride, blocks = _table(block_table, n)
+    st = lib.rar_page_tables(
+        _ints(lens, "lens", n), _ints(new_tokens, "new_tokens", n), n, _ints(free_pages, "free_pages", free), free,
+        _ints(free_count, "free_count", 1), page_size, num_pages, table, stride, blocks,
         _ints(lens_out, "lens_out", n), _ints(starts, "starts", n + 1), _ints(positions, "positions", tokens),
         _ints(slots, "slots", tokens), tokens, _ints(free_count_out, "free_count_out", 1), workspace.ptr,
-        workspace.nbytes, _stream_handle(stream))
-    _check(st, "rar_page_tables")
+        workspace.nbytes, _op_stream(stream))
+    if st:
+        _check(st, "rar_page_tables")
 
 
 def _rope_call(qkv, q_weight, k_weight, cos_sin, positions, q, kv_heads):
-    """What the forms of the norm and rotation share: qkv [tokens, (q + 2 kv heads) * head_dim] against
-    q [tokens, q_heads, head_dim]."""
-    import torch
-    qkv_p, n, shape, strides, dtype = qkv
-    q_p, qn, qshape, qstrides, qdtype = q
-    tokens, q_heads, dim = qshape
-    width = (q_heads + 2 * kv_heads) * dim
-    _need(qn == n and qdtype == dtype and shape[0] == tokens and shape[1] == width and _packed(shape, strides, 1)
-          and _packed(qshape, qstrides, 1), "qkv: [tokens, (q_heads + 2 kv_heads) head_dim], queries [tokens, q_heads, "
-          "head_dim], of one dtype")
-    for t in (q_weight, k_weight):
-        _need(t.dtype == dtype and t.is_cuda and t.is_contiguous() and t.numel() == dim,
-              "weights: head_dim elements of qkv's dtype")
-    _need(cos_sin.dtype == torch.float32 and cos_sin.is_cuda and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
-          "cos_sin: contiguous float32 [max_pos, rot_dim]")
-    return (qkv_p, n, tokens, _row_stride(shape, strides, width), q_weight.data_ptr(), k_weight.data_ptr(),
-            cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]), _ints(positions, "positions", tokens), \
-        (q_heads, kv_heads, dim, _op_dtype(dtype))
+    """What the forms of the norm and rotation share: qkv [tokens, (q + 2 kv
+    heads) * head_dim] against queries [tokens, q_heads, head_dim]."""
+    tokens, q_heads, dim = q[2]
+    dtype = qkv[4]
+    if qkv[1] != q[1] or q[4] is not dtype or qkv[2] != (tokens, (q_heads + 2 * kv_heads) * dim):
+        _refuse("qkv: [tokens, (q_heads + 2 kv_heads) head_dim], queries [tokens, q_heads, head_dim], of one dtype")
+    if q_weight.dtype is not dtype or k_weight.dtype is not dtype or q_weight.shape != (dim,) \
+            or k_weight.shape != (dim,) or not (q_weight.is_cuda and k_weight.is_cuda and q_weight.is_contiguous()
+                                                and k_weight.is_contiguous()):
+        _refuse("weights: head_dim contiguous elements of qkv's dtype in device memory")
+    table = cos_sin.shape
+    if cos_sin.dtype is not _FLOAT32 or len(table) != 2 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
+        _refuse("cos_sin: contiguous float32 [max_pos, rot_dim] in device memory")
+    return (qkv[0], q[1], tokens, qkv[3], q_weight.data_ptr(), k_weight.data_ptr(), cos_sin.data_ptr(), table[0],
+            table[1]), _ints(positions, "positions", tokens), (q_heads, kv_heads, dim, _op_dtype(dtype))
 
 
 def qk_norm_rope(qkv, q_weight, k_weight, cos_sin, positions, q_out, k_out, workspace: OpWorkspace, eps: float = 1e-6,
                  interleaved: bool = False, stream=None) -> None:
     """Enqueue the norm and rotation of every rank's queries and keys: q_out
     [tokens, q_heads, head_dim] and k_out [tokens, kv_heads, head_dim] a rank."""
+    lib = _ops or _op_setup()
     q, k = _ranked(q_out, "q_out", 3), _ranked(k_out, "k_out", 3)
     head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, k[2][1])
-    _need(k[1] == q[1] and k[4] == q[4] and k[2][0] == q[2][0] and k[2][2] == q[2][2] and _packed(k[2], k[3], 1),
-          "k_out: [tokens, kv_heads, head_dim]")
-    st = load_library().rar_qk_norm_rope(
-        *head, int(interleaved), pos, *heads, eps, q[0], _row_stride(q[2], q[3], heads[0] * heads[2]), k[0],
-        _row_stride(k[2], k[3], heads[1] * heads[2]), workspace.ptr, workspace.nbytes, _stream_handle(stream))
-    _check(st, "rar_qk_norm_rope")
+    if k[1] != q[1] or k[4] is not q[4] or k[2] != (q[2][0], heads[1], heads[2]):
+        _refuse("k_out: [tokens, kv_heads, head_dim]")
+    st = lib.rar_qk_norm_rope(*head, interleaved, pos, *heads, eps, q[0], q[3], k[0], k[3], workspace.ptr,
+                              workspace.nbytes, _op_stream(stream))
+    if st:
+        _check(st, "rar_qk_norm_rope")
 
 
 def qk_norm_rope_cached(qkv, q_weight, k_weight, cos_sin, positions, slots, q_out, k_cache, v_cache,
                         workspace: OpWorkspace, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """Enqueue the norm and rotation, keys and values into the paged caches
     [num_pages, kv_heads, page_size, head_dim] a rank at slots."""
-    q, k, v = _ranked(q_out, "q_out", 3), _ranked(k_cache, "k_cache", 4), _ranked(v_cache, "v_cache", 4)
+    lib = _ops or _op_setup()
+    q = _ranked(q_out, "q_out", 3)
+    k, v = _ranked_dense(k_cache, "k_cache", 4), _ranked_dense(v_cache, "v_cache", 4)
     pages, kv_heads, page, dim = k[2]
     head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, kv_heads)
-    _need(k[1] == v[1] == q[1] and k[4] == v[4] == q[4] and k[2] == v[2] and dim == heads[2]
-          and _packed(k[2], k[3], 0) and _packed(v[2], v[3], 0),
-          "k_cache, v_cache: contiguous [num_pages, kv_heads, page_size, head_dim]")
-    st = load_library().rar_qk_norm_rope_cached(
-        *head, int(interleaved), pos, _ints(slots, "slots", q[2][0]), *heads, eps, q[0],
-        _row_stride(q[2], q[3], heads[0] * dim), k[0], v[0], pages, page, workspace.ptr, workspace.nbytes,
-        _stream_handle(stream))
-    _check(st, "rar_qk_norm_rope_cached")
+    if k[1] != q[1] or v[1] != q[1] or k[4] is not q[4] or v[4] is not q[4] or v[2] != k[2] or dim != heads[2]:
+        _refuse("k_cache, v_cache: [num_pages, kv_heads, page_size, head_dim]")
+    st = lib.rar_qk_norm_rope_cached(*head, interleaved, pos, _ints(slots, "slots", q[2][0]), *heads, eps, q[0], q[3],
+                                     k[0], v[0], pages, page, workspace.ptr, workspace.nbytes, _op_stream(stream))
+    if st:
+        _check(st, "rar_qk_norm_rope_cached")
 
 
 def qk_norm_rope_backward(qkv, q_weight, k_weight, cos_sin, positions, dq, dk, dv, dqkv, dq_weight, dk_weight,
@@ -513,24 +557,23 @@ def qk_norm_rope_backward(qkv, q_weight, k_weight, cos_sin, positions, dq, dk, d
     """Enqueue the gradient: dqkv (as qkv) and float32 dq_weight, dk_weight
     [head_dim] a rank from dq [tokens, q_heads, head_dim], dk and dv [tokens,
     kv_heads, head_dim]."""
-    import torch
+    lib = _ops or _op_setup()
     q, k, v = _ranked(dq, "dq", 3), _ranked(dk, "dk", 3), _ranked(dv, "dv", 3)
     x, d = _ranked(qkv, "qkv", 2), _ranked(dqkv, "dqkv", 2)
     head, pos, heads = _rope_call(x, q_weight, k_weight, cos_sin, positions, q, k[2][1])
-    wide = heads[1] * heads[2]
-    _need(k[1] == v[1] == q[1] and k[4] == v[4] == q[4] and k[2] == v[2] and k[2][0] == q[2][0]
-          and k[2][2] == heads[2] and _packed(k[2], k[3], 1) and _packed(v[2], v[3], 1),
-          "dk, dv: [tokens, kv_heads, head_dim]")
-    _need(d[1] == x[1] and d[2] == x[2] and d[4] == x[4] and _packed(d[2], d[3], 1), "dqkv: as qkv")
+    if k[1] != q[1] or v[1] != q[1] or k[4] is not q[4] or v[4] is not q[4] or v[2] != k[2] \
+            or k[2] != (q[2][0], heads[1], heads[2]):
+        _refuse("dk, dv: [tokens, kv_heads, head_dim]")
+    if d[1] != x[1] or d[2] != x[2] or d[4] is not x[4]:
+        _refuse("dqkv: as qkv")
     wq, wk = _ranked(dq_weight, "dq_weight", 1), _ranked(dk_weight, "dk_weight", 1)
     for w in (wq, wk):
-        _need(w[1] == x[1] and w[2][0] == heads[2] and w[4] == torch.float32 and _packed(w[2], w[3], 0),
-              "dq_weight, dk_weight: float32 [head_dim]")
-    st = load_library().rar_qk_norm_rope_backward(
-        *head, int(interleaved), pos, *heads, eps, q[0], _row_stride(q[2], q[3], heads[0] * heads[2]), k[0],
-        _row_stride(k[2], k[3], wide), v[0], _row_stride(v[2], v[3], wide), d[0],
-        _row_stride(d[2], d[3], d[2][1]), wq[0], wk[0], workspace.ptr, workspace.nbytes, _stream_handle(stream))
-    _check(st, "rar_qk_norm_rope_backward")
+        if w[1] != x[1] or w[2] != (heads[2],) or w[4] is not _FLOAT32 or w[3] != 1:
+            _refuse("dq_weight, dk_weight: float32 [head_dim]")
+    st = lib.rar_qk_norm_rope_backward(*head, interleaved, pos, *heads, eps, q[0], q[3], k[0], k[3], v[0], v[3], d[0],
+                                       d[3], wq[0], wk[0], workspace.ptr, workspace.nbytes, _op_stream(stream))
+    if st:
+        _check(st, "rar_qk_norm_rope_backward")
 
 
 def decode_attention(q, k_cache, v_cache, block_table, lens, out, lse, workspace: OpWorkspace,
@@ -539,50 +582,42 @@ def decode_attention(q, k_cache, v_cache, block_table, lens, out, lse, workspace
     head_dim] a rank, caches as qk_norm_rope_cached writes them, int32
     block_table [batch, max_blocks] and lens [batch]; lse float32 [batch,
     q_heads] a rank, or None. scale: head_dim ** -0.5 by default."""
-    import torch
-    x, k, v, o = _ranked(q, "q", 3), _ranked(k_cache, "k_cache", 4), _ranked(v_cache, "v_cache", 4), \
-        _ranked(out, "out", 3)
+    lib = _ops or _op_setup()
+    x, o = _ranked(q, "q", 3), _ranked(out, "out", 3)
+    k, v = _ranked_dense(k_cache, "k_cache", 4), _ranked_dense(v_cache, "v_cache", 4)
+    n, dtype = x[1], x[4]
     batch, q_heads, dim = x[2]
     pages, kv_heads, page, kdim = k[2]
-    _need(x[1] == k[1] == v[1] == o[1] and x[4] == k[4] == v[4] == o[4] and k[2] == v[2] and o[2] == x[2]
-          and kdim == dim and _packed(k[2], k[3], 0) and _packed(v[2], v[3], 0) and _packed(x[2], x[3], 1)
-          and _packed(o[2], o[3], 1),
-          "q, out: [batch, q_heads, head_dim]; caches: contiguous [num_pages, kv_heads, page_size, head_dim]")
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == batch
-          and block_table.is_cuda and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
-          "block_table: int32 [batch, max_blocks]")
-    blocks = block_table.shape[1]
+    if k[1] != n or v[1] != n or o[1] != n or k[4] is not dtype or v[4] is not dtype or o[4] is not dtype \
+            or v[2] != k[2] or o[2] != x[2] or kdim != dim:
+        _refuse("q, out: [batch, q_heads, head_dim]; caches: [num_pages, kv_heads, page_size, head_dim]")
+    table, stride, blocks = _table(block_table, batch)
     lse_p = None
     if lse is not None:
-        e = _ranked(lse, "lse", 2)
-        _need(e[1] == x[1] and e[2][0] == batch and e[2][1] == q_heads and e[4] == torch.float32
-              and _packed(e[2], e[3], 0), "lse: contiguous float32 [batch, q_heads]")
+        e = _ranked_dense(lse, "lse", 2)
+        if e[1] != n or e[2] != (batch, q_heads) or e[4] is not _FLOAT32:
+            _refuse("lse: float32 [batch, q_heads]")
         lse_p = e[0]
-    st = load_library().rar_decode_attention(
-        x[0], _row_stride(x[2], x[3], q_heads * dim), k[0], v[0], x[1], batch, q_heads, kv_heads, dim,
-        _op_dtype(x[4]), pages, page, block_table.data_ptr(), block_table.stride(0) if batch > 1 else blocks, blocks,
-        _ints(lens, "lens", batch), dim ** -0.5 if scale is None else scale, o[0],
-        _row_stride(o[2], o[3], q_heads * dim), lse_p, workspace.ptr, workspace.nbytes, _stream_handle(stream))
-    _check(st, "rar_decode_attention")
+    st = lib.rar_decode_attention(
+        x[0], x[3], k[0], v[0], n, batch, q_heads, kv_heads, dim, _op_dtype(dtype), pages, page, table, stride, blocks,
+        _ints(lens, "lens", batch), dim ** -0.5 if scale is None else scale, o[0], o[3], lse_p, workspace.ptr,
+        workspace.nbytes, _op_stream(stream))
+    if st:
+        _check(st, "rar_decode_attention")
 
 
 def _shards(x, name):
     """(pointers, vocabulary of each shard, row strides, nranks, rows, dtype); shards may differ in width."""
-    parts = list(x) if isinstance(x, (list, tuple)) else None
-    if parts is None:
-        p, n, shape, strides, dtype = _ranked(x, name, 2)
-        widths, steps = [shape[1]] * n, [_row_stride(shape, strides, shape[1])] * n
-        rows, dense = shape[0], shape[1] == 1 or strides[1] == 1
-    else:
-        n, rows, dtype = len(parts), parts[0].shape[0], parts[0].dtype
-        _need(all(t.dim() == 2 and t.shape[0] == rows and t.dtype == dtype and t.is_cuda for t in parts),
-              f"{name}: [rows, vocabulary of the shard], of one dtype, in device memory")
-        p = _ptrs(parts)
-        widths = [t.shape[1] for t in parts]
-        steps = [_row_stride(t.shape, t.stride(), t.shape[1]) for t in parts]
-        dense = all(t.shape[1] == 1 or t.stride(1) == 1 for t in parts)
-    _need(dense, f"{name}: the words of a row lie together")
-    return p, (ctypes.c_int64 * n)(*widths), (ctypes.c_int64 * n)(*steps), n, rows, dtype
+    if type(x) is not list and type(x) is not tuple:
+        p, n, shape, stride, dtype = _ranked(x, name, 2)
+        return p, _pack([shape[1]] * n), _pack([stride] * n), n, shape[0], dtype
+    ones = [_ranked((t,), name, 2) for t in x]
+    rows, dtype = ones[0][2][0], ones[0][4]
+    for o in ones:
+        if o[2][0] != rows or o[4] is not dtype:
+            _refuse(f"{name}: [rows, vocabulary of the shard], of one dtype")
+    return (b"".join([o[0] for o in ones]), _pack([o[2][1] for o in ones]), _pack([o[3] for o in ones]), len(ones), rows,
+            dtype)
 
 
 def token_logprobs(logits, tokens, logprob, entropy, lse, top_values, top_ids, workspace: OpWorkspace,
@@ -591,18 +626,19 @@ def token_logprobs(logits, tokens, logprob, entropy, lse, top_values, top_ids, w
     logits [rows, shard] a rank: float32 logprob, entropy, lse [rows] and the top
     alternatives' float32 top_values and int32 top_ids [rows, top] (None, or top
     0: none)."""
-    p, vocab, steps, n, rows, dtype = _shards(logits, "logits")
+    lib = _ops or _op_setup()
+    p, vocab, strides, n, rows, dtype = _shards(logits, "logits")
     top = 0 if top_ids is None else top_ids.shape[1]
     values_p = ids_p = None
     if top:
-        values_p = _floats(top_values, "top_values", (rows, top))
+        values_p = _floats(top_values, "top_values", rows * top)
         ids_p = _ints(top_ids, "top_ids", rows * top)
-    one = (rows,)
-    st = load_library().rar_token_logprobs(
-        p, vocab, steps, n, rows, _op_dtype(dtype), _ints(tokens, "tokens", rows), _floats(logprob, "logprob", one),
-        _floats(entropy, "entropy", one), _floats(lse, "lse", one), top, values_p, ids_p, workspace.ptr,
-        workspace.nbytes, _stream_handle(stream))
-    _check(st, "rar_token_logprobs")
+    st = lib.rar_token_logprobs(
+        p, vocab, strides, n, rows, _op_dtype(dtype), _ints(tokens, "tokens", rows), _floats(logprob, "logprob", rows),
+        _floats(entropy, "entropy", rows), _floats(lse, "lse", rows), top, values_p, ids_p, workspace.ptr,
+        workspace.nbytes, _op_stream(stream))
+    if st:
+        _check(st, "rar_token_logprobs")
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_entropy, dlogits, workspace: OpWorkspace,
@@ -610,16 +646,18 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_ent
     """Enqueue the gradient with respect to the logits, from lse and entropy of
     token_logprobs and float32 gradients [rows] (grad_entropy None: no such
     term); dlogits as logits (in place is allowed)."""
-    p, vocab, steps, n, rows, dtype = _shards(logits, "logits")
-    dp, dvocab, dsteps, dn, drows, ddtype = _shards(dlogits, "dlogits")
-    _need(dn == n and drows == rows and ddtype == dtype and list(dvocab) == list(vocab), "dlogits: as logits")
-    one = (rows,)
-    st = load_library().rar_token_logprobs_backward(
-        p, vocab, steps, n, rows, _op_dtype(dtype), _ints(tokens, "tokens", rows), _floats(lse, "lse", one),
-        _floats(entropy, "entropy", one), _floats(grad_logprob, "grad_logprob", one),
-        None if grad_entropy is None else _floats(grad_entropy, "grad_entropy", one), dp, dsteps, workspace.ptr,
-        workspace.nbytes, _stream_handle(stream))
-    _check(st, "rar_token_logprobs_backward")
+    lib = _ops or _op_setup()
+    p, vocab, strides, n, rows, dtype = _shards(logits, "logits")
+    dp, dvocab, dstrides, dn, drows, ddtype = _shards(dlogits, "dlogits")
+    if dn != n or drows != rows or ddtype is not dtype or dvocab != vocab:
+        _refuse("dlogits: as logits")
+    st = lib.rar_token_logprobs_backward(
+        p, vocab, strides, n, rows, _op_dtype(dtype), _ints(tokens, "tokens", rows), _floats(lse, "lse", rows),
+        _floats(entropy, "entropy", rows), _floats(grad_logprob, "grad_logprob", rows),
+        None if grad_entropy is None else _floats(grad_entropy, "grad_entropy", rows), dp, dstrides, workspace.ptr,
+        workspace.nbytes, _op_stream(stream))
+    if st:
+        _check(st, "rar_token_logprobs_backward")
 
 
 def get_status(workspace, stream=None) -> Status:

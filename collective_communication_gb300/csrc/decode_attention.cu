@@ -3,8 +3,30 @@
 //
 //   s_t = scale * (q . k_t),  o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m)
 // over the t < len cached tokens of the request, with the running maximum m and
-// sum of the softmax in binary32; lse = m + log(sum). A request of length 0
-// gives o = 0 and lse = -inf.
+// sum l of the softmax in binary32; lse = m + log l. A request of length 0
+// gives o = 0 and lse = -inf. Results over parts of the cache (m, l, o
+// unnormalised) join by o = sum_i 2^(m_i - M) o_i, l likewise, M = max m_i.
+//
+// Every cached element is read once for up to 8 NT query heads, so the bytes of
+// the cache bound the kernel: about 4 NT flops a byte against the 250 at which
+// the tensor cores would.
+//
+// Split. An item is one (request, rank, key head, group of 8 NT query heads);
+// its tokens form tiles of 64. The tiles of all items in a row are cut into one
+// equal range per resident block, whatever the lengths are, so a block may
+// finish one item, do whole ones and start another. An item that a cut divides
+// is joined by the block that arrives last at it, in block order. A block's
+// four warps take 16 tokens of a tile each with a softmax of their own, and
+// join in shared memory at the end of an item.
+//
+// Registers instead of shared memory. With tokens (not query heads, of which
+// there are few) as the rows of the matrix instruction, S^T = K Q^T and
+// O^T = V^T P^T take their left operands straight from 16-byte loads: the order
+// of the contraction index of S^T and of the rows of O^T is free, so a lane's
+// chunk of consecutive elements supplies what its fragments need (for bf16
+// V^T one byte permute pairs two tokens). K of the next tile is loaded as soon
+// as S^T is done with its registers and V as soon as O^T is, so a warp always
+// has about a tile in flight and waits on no barrier.
 #include <cstdio>
 
 #include "op_common.cuh"
@@ -12,84 +34,701 @@
 
 namespace rar {
 
-constexpr int kDaThreads = 128;
-constexpr int kDaTile = 64;
+constexpr int kDaWarps = 4;
+constexpr int kDaThreads = 32 * kDaWarps;
+constexpr int kDaTile = 16 * kDaWarps;  // tokens of a tile
+constexpr int kDaMaxBlocks = 912;       // most blocks of a launch: partial results and counters for each
+static_assert(2 * kDaMaxBlocks <= kOpCounters, "two arrival counters per block");
 
-// One block per (query head, request, rank).
-template <typename T>
-__global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __grid_constant__ DecodeArgs a) {
-  __shared__ float s_q[256], s_s[kDaTile];
-  __shared__ int64_t s_row[kDaTile];
-  if (!op_workspace_ok(a.ws)) return;
-  const int h = blockIdx.x, b = blockIdx.y, rank = blockIdx.z, D = a.head_dim, tid = threadIdx.x;
-  const int kvh = h / (a.q_heads / a.kv_heads);
-  const T* q = reinterpret_cast<const T*>(a.q[rank]) + (int64_t)b * a.q_stride + (int64_t)h * D;
-  const T* kc = reinterpret_cast<const T*>(a.k_cache[rank]);
-  const T* vc = reinterpret_cast<const T*>(a.v_cache[rank]);
-  int len = a.lens[b];
-  bool bad = len < 0 || len > (int64_t)a.max_blocks << a.page_shift;
-  if (bad) len = len < 0 ? 0 : (int)((int64_t)a.max_blocks << a.page_shift);
-  for (int d = tid; d < D; d += kDaThreads) s_q[d] = to_float(q[d]) * a.scale;
-  float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
-  for (int t0 = 0; t0 < len; t0 += kDaTile) {
-    __syncthreads();
-    const int n = len - t0 < kDaTile ? len - t0 : kDaTile;
-    if (tid < n) {
-      const int t = t0 + tid;
-      const int page = a.table[(int64_t)b * a.table_stride + (t >> a.page_shift)];
-      const bool fine = page >= 0 && page < a.num_pages;
-      if (!fine) bad = true;
-      s_row[tid] = fine ? ((((int64_t)page * a.kv_heads + kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1))) * D
-                        : -1;
-    }
-    __syncthreads();
-    for (int i = tid >> 5; i < n; i += kDaThreads / 32) {
-      float s = 0.f;
-      const int64_t row = s_row[i];
-      if (row >= 0)
-        for (int d = tid & 31; d < D; d += 32) s += s_q[d] * to_float(kc[row + d]);
+namespace {
+
+// 16 bytes of the cache, or zeros where `live` is false. Volatile, as the matrix
+// instructions are: the order in which the loop asks for loads and uses them is
+// what keeps a tile in flight.
+__device__ __forceinline__ uint4 ldg_cache(const void* p, bool live) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)live));
+  return v;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t tf32_of(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+  return y;
+}
+// x = hi + lo + an error of at most 2^-22 |x|
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = tf32_of(x);
+  lo = tf32_of(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The running softmax of 8 NT query heads over a warp's tokens: query
+// 8 nt + 2c + j of the lane (g, c) = (lane / 4, lane % 4) at [nt][j]. l is the
+// lane's own part of the sum until the end.
+template <int NT>
+struct Softmax {
+  float m[NT][2], l[NT][2];
+};
+
+// Scores (C fragment of S^T: tokens g, g + 8 by queries 2c, 2c + 1, in units of
+// log 2) to weights. The maximum moves only if a score is more than 8 above it:
+// weights up to 2^8 lose nothing in binary32, and the rescaling of o and the
+// reduction over the lanes are skipped for almost every tile.
+template <int NT, int MT>
+__device__ __forceinline__ void softmax_step(float (&s)[NT][4], Softmax<NT>& st, float (&o)[MT][NT][4]) {
+  bool rise = false;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-      if ((tid & 31) == 0) s_s[i] = row >= 0 ? s : -INFINITY;
-    }
-    __syncthreads();
-    float top = m;
-    for (int i = 0; i < n; i++) top = fmaxf(top, s_s[i]);
-    if (top == -INFINITY) continue;
-    const float keep = expf(m - top);
-    m = top;
-    l *= keep;
-    acc[0] *= keep;
-    acc[1] *= keep;
-    for (int i = 0; i < n; i++) {
-      if (s_row[i] < 0) continue;
-      const float p = expf(s_s[i] - m);
-      l += p;
+  for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+    for (int j = 0; j < 2; j++) rise |= fmaxf(s[nt][j], s[nt][2 + j]) > st.m[nt][j] + 8.f;
+  if (__any_sync(~0u, rise)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
       for (int j = 0; j < 2; j++) {
-        const int d = tid + j * kDaThreads;
-        if (d < D) acc[j] += p * to_float(vc[s_row[i] + d]);
+        float top = fmaxf(s[nt][j], s[nt][2 + j]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        top = fmaxf(top, st.m[nt][j]);
+        const float keep = top == -INFINITY ? 1.f : exp2_fast(st.m[nt][j] - top);
+        st.m[nt][j] = top;
+        st.l[nt][j] *= keep;
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+          o[mt][nt][j] *= keep;
+          o[mt][nt][2 + j] *= keep;
+        }
       }
     }
   }
-  T* out = reinterpret_cast<T*>(a.out[rank]) + (int64_t)b * a.out_stride + (int64_t)h * D;
-  for (int j = 0; j < 2; j++) {
-    const int d = tid + j * kDaThreads;
-    if (d < D) from_float(out + d, len == 0 ? 0.f : acc[j] / l);
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const float m = st.m[nt][j] == -INFINITY ? 0.f : st.m[nt][j];  // no token yet: every weight is 0
+      s[nt][j] = exp2_fast(s[nt][j] - m);
+      s[nt][2 + j] = exp2_fast(s[nt][2 + j] - m);
+      st.l[nt][j] += s[nt][j] + s[nt][2 + j];
+    }
+}
+
+// What a tile needs per type. DP: head_dim rounded up to 64, 128 or 256 (the
+// chunks past head_dim are zero). Rows are cache rows, -1 for no token.
+template <typename T, int DP, int NT>
+struct Tile;
+
+template <int DP, int NT>
+struct Tile<uint16_t, DP, NT> {
+  static constexpr int KC = DP / 32, VC = DP / 64, MT = DP / 16;
+  static constexpr int kQueryBytes = NT * KC * 32 * 16;  // B fragments of Q^T in shared memory
+  uint4 k[2][KC];  // tokens g, g + 8; elements 32 i + 8 c
+  uint4 v[4][VC];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9; elements 64 h + 8 g
+
+  __device__ __forceinline__ static void load_queries(char* smem, const uint16_t* q, int queries, int D) {
+    for (int i = threadIdx.x; i < NT * KC * 32; i += kDaThreads) {
+      const int lane = i & 31, chunk = (i >> 5) % KC, nt = (i >> 5) / KC;
+      const int row = nt * 8 + (lane >> 2), d = chunk * 32 + (lane & 3) * 8;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (row < queries && d < D) u = *reinterpret_cast<const uint4*>(q + (int64_t)row * D + d);
+      reinterpret_cast<uint4*>(smem)[i] = u;
+    }
   }
-  if (tid == 0 && a.lse[rank] != nullptr) a.lse[rank][(int64_t)b * a.q_heads + h] = m + logf(l);
+  __device__ __forceinline__ void load_k(const uint16_t* base, int row, int D) {
+    const int lane = threadIdx.x & 31, c8 = (lane & 3) * 8;
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      const int r = __shfl_sync(~0u, row, (lane >> 2) + 8 * t);
+      const uint16_t* p = base + (int64_t)r * D + c8;
+#pragma unroll
+      for (int i = 0; i < KC; i++)
+        k[t][i] = ldg_cache(p + 32 * i, r >= 0 && 32 * i + c8 < D);
+    }
+  }
+  __device__ __forceinline__ void load_v(const uint16_t* base, int row, int D) {
+    const int lane = threadIdx.x & 31, g8 = (lane >> 2) * 8;
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+      const int r = __shfl_sync(~0u, row, 2 * (lane & 3) + (t & 1) + 8 * (t >> 1));
+      const uint16_t* p = base + (int64_t)r * D + g8;
+#pragma unroll
+      for (int h = 0; h < VC; h++)
+        v[t][h] = ldg_cache(p + 64 * h, r >= 0 && 64 * h + g8 < D);
+    }
+  }
+  __device__ __forceinline__ void scores(const char* smem, float (&s)[NT][4]) const {
+    const uint4* q = reinterpret_cast<const uint4*>(smem) + (threadIdx.x & 31);
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KC; i++) {
+        const uint4 b = q[(nt * KC + i) * 32];
+        mma_bf16(x, k[0][i].x, k[1][i].x, k[0][i].y, k[1][i].y, b.x, b.y);
+        mma_bf16(y, k[0][i].z, k[1][i].z, k[0][i].w, k[1][i].w, b.z, b.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) s[nt][j] = x[j] + y[j];
+    }
+  }
+  // O^T += V^T P^T. P goes in as a bf16 and the bf16 of its remainder, two
+  // instructions: P's own rounding (2^-9) would be as large as the result's.
+  __device__ __forceinline__ void accumulate(const float (&p)[NT][4], float (&o)[MT][NT][4]) const {
+    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        const float a = p[nt][2 * t], b = p[nt][2 * t + 1];
+        const uint32_t h = bf16_pair(a, b);
+        hi[nt][t] = transpose8x8(h);
+        lo[nt][t] = transpose8x8(bf16_pair(a - bf16_lo(h), b - bf16_hi(h)));
+      }
+#pragma unroll
+    for (int h = 0; h < VC; h++) {
+      const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&v[0][h]);
+      const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&v[1][h]);
+      const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&v[2][h]);
+      const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&v[3][h]);
+#pragma unroll
+      for (int jj = 0; jj < 4; jj++) {
+        const uint32_t a0 = __byte_perm(w0[jj], w1[jj], 0x5410), a1 = __byte_perm(w0[jj], w1[jj], 0x7632);
+        const uint32_t a2 = __byte_perm(w2[jj], w3[jj], 0x5410), a3 = __byte_perm(w2[jj], w3[jj], 0x7632);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          mma_bf16(o[h * 4 + jj][nt], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
+          mma_bf16(o[h * 4 + jj][nt], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
+        }
+      }
+    }
+  }
+  // Element of row g (or g + 8) of o's tile mt.
+  __device__ __forceinline__ static int dim_of(int mt, int g) { return (mt >> 2) * 64 + g * 8 + (mt & 3) * 2; }
+};
+
+// binary32: every operand as the sum of two tf32 values, three products
+// (hi hi, hi lo, lo hi); what is left out is below 2^-21 of a product.
+template <int DP, int NT>
+struct Tile<float, DP, NT> {
+  static constexpr int KC = DP / 16, VC = DP / 32, MT = DP / 16;
+  static constexpr int kQueryBytes = NT * 2 * KC * 32 * 16;
+  float4 k[2][KC];  // tokens g, g + 8; elements 16 i + 4 c
+  float4 v[4][VC];  // tokens c, c + 4, c + 8, c + 12; elements 32 h + 4 g
+
+  __device__ __forceinline__ static void load_queries(char* smem, const float* q, int queries, int D) {
+    for (int i = threadIdx.x; i < NT * 2 * KC * 32; i += kDaThreads) {
+      const int lane = i & 31, step = (i >> 5) % (2 * KC), nt = (i >> 5) / (2 * KC);
+      const int row = nt * 8 + (lane >> 2), d = (step >> 1) * 16 + (lane & 3) * 4 + (step & 1) * 2;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (row < queries && d < D) {
+        const float2 x = *reinterpret_cast<const float2*>(q + (int64_t)row * D + d);
+        split_tf32(x.x, u.x, u.z);
+        split_tf32(x.y, u.y, u.w);
+      }
+      reinterpret_cast<uint4*>(smem)[i] = u;
+    }
+  }
+  __device__ __forceinline__ static float4 load4(const float* p, bool live) {
+    const uint4 u = ldg_cache(p, live);
+    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  __device__ __forceinline__ void load_k(const float* base, int row, int D) {
+    const int lane = threadIdx.x & 31, c4 = (lane & 3) * 4;
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      const int r = __shfl_sync(~0u, row, (lane >> 2) + 8 * t);
+      const float* p = base + (int64_t)r * D + c4;
+#pragma unroll
+      for (int i = 0; i < KC; i++) k[t][i] = load4(p + 16 * i, r >= 0 && 16 * i + c4 < D);
+    }
+  }
+  __device__ __forceinline__ void load_v(const float* base, int row, int D) {
+    const int lane = threadIdx.x & 31, g4 = (lane >> 2) * 4;
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+      const int r = __shfl_sync(~0u, row, (lane & 3) + 4 * t);
+      const float* p = base + (int64_t)r * D + g4;
+#pragma unroll
+      for (int h = 0; h < VC; h++) v[t][h] = load4(p + 32 * h, r >= 0 && 32 * h + g4 < D);
+    }
+  }
+  __device__ __forceinline__ void scores(const char* smem, float (&s)[NT][4]) const {
+    const uint4* q = reinterpret_cast<const uint4*>(smem) + (threadIdx.x & 31);
+    float x[NT][4] = {}, y[NT][4] = {};
+#pragma unroll
+    for (int i = 0; i < KC; i++) {
+      const float* f0 = reinterpret_cast<const float*>(&k[0][i]);
+      const float* f1 = reinterpret_cast<const float*>(&k[1][i]);
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        uint32_t h[4], l[4];
+        split_tf32(f0[2 * e], h[0], l[0]);
+        split_tf32(f1[2 * e], h[1], l[1]);
+        split_tf32(f0[2 * e + 1], h[2], l[2]);
+        split_tf32(f1[2 * e + 1], h[3], l[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          const uint4 b = q[(nt * 2 * KC + 2 * i + e) * 32];
+          mma_tf32(x[nt], h[0], h[1], h[2], h[3], b.x, b.y);
+          mma_tf32(y[nt], h[0], h[1], h[2], h[3], b.z, b.w);
+          mma_tf32(y[nt], l[0], l[1], l[2], l[3], b.x, b.y);
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) s[nt][j] = x[nt][j] + y[nt][j];
+  }
+  __device__ __forceinline__ void accumulate(const float (&p)[NT][4], float (&o)[MT][NT][4]) const {
+    const int lane = threadIdx.x & 31, from = (lane & 3) * 4 + (lane >> 3);
+    const bool odd = (lane >> 2) & 1;
+    uint32_t ph[NT][2][2], pl[NT][2][2];  // [step of 8 tokens][token c, c + 4] of query g
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float a = __shfl_sync(~0u, p[nt][2 * t], from + 16 * e);
+          const float b = __shfl_sync(~0u, p[nt][2 * t + 1], from + 16 * e);
+          split_tf32(odd ? b : a, ph[nt][t][e], pl[nt][t][e]);
+        }
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+      for (int h = 0; h < VC; h++) {
+        const float* f0 = reinterpret_cast<const float*>(&v[2 * t][h]);
+        const float* f1 = reinterpret_cast<const float*>(&v[2 * t + 1][h]);
+#pragma unroll
+        for (int jj = 0; jj < 2; jj++) {
+          uint32_t a[4], b[4];
+          split_tf32(f0[2 * jj], a[0], b[0]);
+          split_tf32(f0[2 * jj + 1], a[1], b[1]);
+          split_tf32(f1[2 * jj], a[2], b[2]);
+          split_tf32(f1[2 * jj + 1], a[3], b[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            float(&acc)[4] = o[h * 2 + jj][nt];
+            mma_tf32(acc, a[0], a[1], a[2], a[3], ph[nt][t][0], ph[nt][t][1]);
+            mma_tf32(acc, a[0], a[1], a[2], a[3], pl[nt][t][0], pl[nt][t][1]);
+            mma_tf32(acc, b[0], b[1], b[2], b[3], ph[nt][t][0], ph[nt][t][1]);
+          }
+        }
+      }
+  }
+  __device__ __forceinline__ static int dim_of(int mt, int g) { return (mt >> 1) * 32 + g * 4 + (mt & 1) * 2; }
+};
+
+// A partial result of a block: 8 NT queries by DP values, then their m and l.
+template <int DP, int NT>
+__host__ __device__ constexpr int partial_floats() { return NT * 8 * (DP + 2); }
+
+}  // namespace
+
+// Whether K and V of a tile (DP elements of T, 16 tokens a warp) fit the
+// registers together; else V is loaded when K has been used.
+template <typename T, int DP>
+constexpr bool kDaAhead = DP * sizeof(T) <= 512;
+
+constexpr int kDaJoin = 16;  // partial results that one block joins before it hands on
+
+// Where the walk over the tiles stands: kept in shared memory so that the loop
+// over tiles has the registers.
+struct Part {
+  int64_t first;       // tiles before the request's, all items
+  int64_t item_first;  // first tile of the item
+  int request, t0, t1, tiles, len;  // tiles t0..t1 of the item's `tiles`
+  int rank, kvh, q0, queries;
+};
+
+template <typename T, int DP, int NT>
+__global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __grid_constant__ DecodeArgs a) {
+  using Tl = Tile<T, DP, NT>;
+  constexpr int MT = Tl::MT, Q = NT * 8, kRow = DP + 4;
+  constexpr int kMergeBytes = kDaWarps * Q * kRow * 4;
+  constexpr int kMostParts = kDaMaxBlocks / kDaJoin + 1;
+  __shared__ __align__(16) char s_buf[kMergeBytes > Tl::kQueryBytes ? kMergeBytes : Tl::kQueryBytes];
+  __shared__ float s_m[kDaWarps][Q], s_l[kDaWarps][Q];
+  __shared__ float s_w[kMostParts][Q], s_pl[kMostParts][Q], s_top[Q], s_sum_l[Q];
+  __shared__ int64_t s_sum[kDaWarps];
+  __shared__ Part s_part;
+  __shared__ bool s_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int D = a.head_dim;
+  const int longest = a.max_blocks << a.page_shift;
+  bool bad = false;
+
+  // Tiles of all requests: a segment of requests per thread, then a scan.
+  auto length = [&](int b) {
+    const int n = a.lens[b];
+    return n < 0 ? 0 : n > longest ? longest : n;
+  };
+  auto tiles_of = [](int n) { return (n + kDaTile - 1) / kDaTile; };
+  const int group = a.q_heads / a.kv_heads, qgroups = (group + Q - 1) / Q;
+  const int per_request = a.nranks * a.kv_heads * qgroups;  // items of a request
+  int64_t total;
+  {
+    const int seg = (a.batch + kDaThreads - 1) / kDaThreads;
+    const int b0 = min(tid * seg, a.batch), b1 = min(b0 + seg, a.batch);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; b++) {
+      const int n = a.lens[b];
+      if (n < 0 || n > longest) bad = true;
+      mine += tiles_of(length(b));
+    }
+    if (!op_workspace_ok(a.ws)) return;
+    int64_t scan = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, scan, d);
+      if (lane >= d) scan += x;
+    }
+    if (lane == 31) s_sum[warp] = scan;
+    __syncthreads();
+    int64_t before = scan - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kDaWarps; w++) {
+      if (w < warp) before += s_sum[w];
+      all += s_sum[w];
+    }
+    total = all * per_request;
+    const int64_t blocks = total < gridDim.x ? total : gridDim.x;
+    if (blockIdx.x < blocks) {
+      const int64_t at = blockIdx.x * total / blocks;
+      const int64_t t = at / per_request;  // lies in the same request, tiles counted once per item
+      if (t >= before && t < before + mine) {
+        int b = b0;
+        for (int n; t >= before + (n = tiles_of(length(b))); b++) before += n;
+        s_part.first = before * per_request;
+        s_part.request = b;
+      }
+    }
+  }
+  const int64_t blocks = total < gridDim.x ? total : gridDim.x;  // those with at least one tile
+  auto start_of = [&](int64_t block) { return block * total / blocks; };
+  auto block_of = [&](int64_t tile) { return ((tile + 1) * blocks - 1) / total; };
+
+  // Requests of length 0, shared out over the blocks.
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    if (length(b) != 0) continue;
+    for (int r = 0; r < a.nranks; r++) {
+      T* out = reinterpret_cast<T*>(a.out[r]) + (int64_t)b * a.out_stride;
+      for (int i = tid; i < a.q_heads * D; i += kDaThreads) from_float(out + i, 0.f);
+      if (a.lse[r] != nullptr)
+        for (int i = tid; i < a.q_heads; i += kDaThreads) a.lse[r][(int64_t)b * a.q_heads + i] = -INFINITY;
+    }
+  }
+  if (blockIdx.x >= blocks) {
+    if (bad) op_report(a.ws, kErrCapacity);
+    return;
+  }
+
+  for (int64_t at = start_of(blockIdx.x); at < start_of(blockIdx.x + 1);) {
+    __syncthreads();  // the last part's shared values have been read
+    if (tid == 0) {
+      const int64_t end = start_of(blockIdx.x + 1);
+      int b = s_part.request, n = tiles_of(length(b));
+      int64_t first = s_part.first;
+      while (at >= first + (int64_t)n * per_request) {
+        first += (int64_t)n * per_request;
+        n = tiles_of(length(++b));
+      }
+      const int item = (int)((at - first) / n), qg = item % qgroups;
+      s_part.first = first;
+      s_part.request = b;
+      s_part.tiles = n;
+      s_part.len = length(b);
+      s_part.item_first = first + (int64_t)item * n;
+      s_part.t0 = (int)(at - s_part.item_first);
+      s_part.t1 = (int)(end - s_part.item_first < n ? end - s_part.item_first : n);
+      s_part.kvh = item / qgroups % a.kv_heads;
+      s_part.rank = item / qgroups / a.kv_heads;
+      s_part.q0 = s_part.kvh * group + qg * Q;
+      s_part.queries = min(Q, group - qg * Q);
+    }
+    __syncthreads();
+    const int rank = s_part.rank, kvh = s_part.kvh, len = s_part.len, t1 = s_part.t1;
+    const T* kc = reinterpret_cast<const T*>(a.k_cache[rank]);
+    const T* vc = reinterpret_cast<const T*>(a.v_cache[rank]);
+    const int32_t* table = a.table + (int64_t)s_part.request * a.table_stride;
+
+    // the lane's token of the warp's 16 in a tile -> cache row
+    auto row_of = [&](int tile) {
+      const int t = tile * kDaTile + warp * 16 + (lane & 15);
+      if (tile >= t1 || t >= len) return -1;
+      const int page = table[t >> a.page_shift];
+      if (page < 0 || page >= a.num_pages) {
+        bad = true;
+        return -1;
+      }
+      return ((page * a.kv_heads + kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+    };
+    Tl tile;
+    float o[MT][NT][4];
+    Softmax<NT> st;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        st.m[nt][j] = -INFINITY;
+        st.l[nt][j] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) o[mt][nt][j] = 0.f;
+    }
+    {
+      const int t0 = s_part.t0;
+      int row = row_of(t0), next = row_of(t0 + 1);
+      tile.load_k(kc, row, D);
+      if (kDaAhead<T, DP>) tile.load_v(vc, row, D);
+      Tl::load_queries(s_buf,
+                       reinterpret_cast<const T*>(a.q[rank]) + (int64_t)s_part.request * a.q_stride +
+                           (int64_t)s_part.q0 * D,
+                       s_part.queries, D);
+      __syncthreads();
+      const float scale2 = a.scale * 1.4426950408889634f;  // scores in units of log 2
+      for (int t = t0; t < t1; t++) {
+        float s[NT][4];
+        tile.scores(s_buf, s);
+        const bool live0 = __shfl_sync(~0u, row, g) >= 0, live1 = __shfl_sync(~0u, row, g + 8) >= 0;
+        if (kDaAhead<T, DP>) tile.load_k(kc, next, D);
+        else tile.load_v(vc, row, D);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int j = 0; j < 2; j++) {
+            s[nt][j] = live0 ? s[nt][j] * scale2 : -INFINITY;
+            s[nt][2 + j] = live1 ? s[nt][2 + j] * scale2 : -INFINITY;
+          }
+        softmax_step<NT, MT>(s, st, o);
+        tile.accumulate(s, o);
+        if (kDaAhead<T, DP>) tile.load_v(vc, next, D);
+        else tile.load_k(kc, next, D);
+        row = next;
+        next = row_of(t + 2);
+      }
+    }
+
+    // the warps' results of this part of the item join in shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) st.l[nt][j] += __shfl_xor_sync(~0u, st.l[nt][j], d);
+        if (g == 0) {
+          s_m[warp][nt * 8 + 2 * c + j] = st.m[nt][j];
+          s_l[warp][nt * 8 + 2 * c + j] = st.l[nt][j];
+        }
+      }
+    __syncthreads();  // every warp is past the queries in s_buf
+    float* s_o = reinterpret_cast<float*>(s_buf);
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        const int q = nt * 8 + 2 * c + j;
+        float top = s_m[0][q];
+#pragma unroll
+        for (int w = 1; w < kDaWarps; w++) top = fmaxf(top, s_m[w][q]);
+        const float f = st.m[nt][j] == -INFINITY ? 0.f : exp2_fast(st.m[nt][j] - top);
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+          float2* p = reinterpret_cast<float2*>(s_o + (warp * Q + q) * kRow + Tl::dim_of(mt, g));
+          *p = make_float2(o[mt][nt][j] * f, o[mt][nt][2 + j] * f);
+        }
+      }
+    if (tid < Q) {
+      float m = s_m[0][tid], l = 0.f;
+#pragma unroll
+      for (int w = 1; w < kDaWarps; w++) m = fmaxf(m, s_m[w][tid]);
+#pragma unroll
+      for (int w = 0; w < kDaWarps; w++)
+        l += s_m[w][tid] == -INFINITY ? 0.f : s_l[w][tid] * exp2_fast(s_m[w][tid] - m);
+      s_top[tid] = m;
+      s_sum_l[tid] = l;
+    }
+    __syncthreads();
+    const int values = s_part.queries * (DP / 4);
+    auto sum4 = [&](int q, int d) {
+      float4 x = *reinterpret_cast<const float4*>(s_o + q * kRow + d);
+#pragma unroll
+      for (int w = 1; w < kDaWarps; w++) {
+        const float4 y = *reinterpret_cast<const float4*>(s_o + (w * Q + q) * kRow + d);
+        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+      }
+      return x;
+    };
+    T* out = reinterpret_cast<T*>(a.out[rank]) + (int64_t)s_part.request * a.out_stride + (int64_t)s_part.q0 * D;
+    float* lse = a.lse[rank] == nullptr ? nullptr : a.lse[rank] + (int64_t)s_part.request * a.q_heads + s_part.q0;
+    auto finish = [&](int q, int d, float4 x) {  // from s_top and s_sum_l
+      const float l = s_sum_l[q], f = l == 0.f ? 0.f : 1.f / l;  // no token with a weight: 0
+      T* p = out + (int64_t)q * D + d;
+      from_float(p, x.x * f);
+      from_float(p + 1, x.y * f);
+      from_float(p + 2, x.z * f);
+      from_float(p + 3, x.w * f);
+      if (d == 0 && lse != nullptr) lse[q] = l == 0.f ? -INFINITY : (s_top[q] + log2f(l)) * 0.6931471805599453f;
+    };
+    if (s_part.t0 == 0 && t1 == s_part.tiles) {
+      for (int i = tid; i < values; i += kDaThreads) {
+        const int q = i / (DP / 4), d = i % (DP / 4) * 4;
+        if (d < D) finish(q, d, sum4(q, d));
+      }
+    } else {
+      // The item is cut: its blocks cf..cl leave partial results, each run of kDaJoin blocks is joined by the one
+      // of them that arrives last, and the runs by the last of those, in block order both times.
+      float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset);
+      const int64_t item_first = s_part.item_first;
+      const int cf = (int)block_of(item_first), cl = (int)block_of(item_first + s_part.tiles - 1);
+      const bool starts_at_cf = start_of(cf) == item_first;
+      auto part_of = [&](int block) {  // a block leaves up to two: of its first item, and of the last that starts in it
+        return parts + (2 * block + (block == cf && !starts_at_cf)) * partial_floats<DP, NT>();
+      };
+      float* part = part_of(blockIdx.x);
+      for (int i = tid; i < values; i += kDaThreads) {
+        const int q = i / (DP / 4), d = i % (DP / 4) * 4;
+        *reinterpret_cast<float4*>(part + q * DP + d) = sum4(q, d);
+      }
+      if (tid < Q) {
+        part[Q * DP + tid] = s_top[tid];
+        part[Q * DP + Q + tid] = s_sum_l[tid];
+      }
+      uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
+      // a run's counter is that of its last block, which no other item's run ends with
+      int from = cf + (blockIdx.x - cf) / kDaJoin * kDaJoin, count = min(kDaJoin, cl + 1 - from), step = 1;
+      int counter = from + count - 1;
+      for (;;) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          s_last = atomicAdd(counters + counter, 1u) == (uint32_t)(count - 1);
+          if (s_last) counters[counter] = 0;
+        }
+        __syncthreads();
+        if (!s_last) break;
+        __threadfence();
+        for (int i = tid; i < count * Q; i += kDaThreads) {
+          const float* p = part_of(from + i / Q * step) + Q * DP + i % Q;
+          s_w[i / Q][i % Q] = __ldcg(p);
+          s_pl[i / Q][i % Q] = __ldcg(p + Q);
+        }
+        __syncthreads();
+        if (tid < Q) {
+          float m = -INFINITY, l = 0.f;
+          for (int p = 0; p < count; p++) m = fmaxf(m, s_w[p][tid]);
+          for (int p = 0; p < count; p++) {
+            const float f = s_w[p][tid] == -INFINITY ? 0.f : exp2_fast(s_w[p][tid] - m);
+            l += f * s_pl[p][tid];
+            s_w[p][tid] = f;
+          }
+          s_top[tid] = m;
+          s_sum_l[tid] = l;
+        }
+        __syncthreads();
+        const bool whole = step > 1 || count == cl + 1 - cf;  // nothing of the item is missing
+        float* to = part_of(from);
+        for (int i = tid; i < values; i += kDaThreads) {
+          const int q = i / (DP / 4), d = i % (DP / 4) * 4;
+          if (d >= D) continue;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int p = 0; p < count; p++) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(part_of(from + p * step) + q * DP + d));
+            const float f = s_w[p][q];
+            x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
+          }
+          if (whole) finish(q, d, x);
+          else *reinterpret_cast<float4*>(to + q * DP + d) = x;
+        }
+        if (whole) break;
+        if (tid < Q) {
+          to[Q * DP + tid] = s_top[tid];
+          to[Q * DP + Q + tid] = s_sum_l[tid];
+        }
+        step = kDaJoin;
+        count = (cl - cf) / kDaJoin + 1;
+        from = cf;
+        counter = kDaMaxBlocks + cf;  // one item at most starts in a block and leaves it
+      }
+    }
+    at = s_part.item_first + t1;
+  }
   if (bad) op_report(a.ws, kErrCapacity);
 }
 
-int64_t decode_attention_scratch_bytes(int, int, int, int, int) { return 0; }
+namespace {
+
+struct DecodeKernel {
+  const void* fn;
+  int partial;  // floats of a partial result
+};
+
+template <typename T, int DP, int NT>
+DecodeKernel kernel_of() { return {(const void*)decode_attention_kernel<T, DP, NT>, partial_floats<DP, NT>()}; }
+
+// 16 query heads share a pass over the cache where their accumulators fit the
+// registers beside K and V.
+template <typename T>
+DecodeKernel kernel_for(int head_dim, int group) {
+  const bool wide = group > 8;
+  if (head_dim <= 64) return wide ? kernel_of<T, 64, 2>() : kernel_of<T, 64, 1>();
+  if (head_dim <= 128) return wide && sizeof(T) == 2 ? kernel_of<T, 128, sizeof(T) == 2 ? 2 : 1>() : kernel_of<T, 128, 1>();
+  return kernel_of<T, 256, 1>();
+}
+
+}  // namespace
+
+int64_t decode_attention_scratch_bytes(int, int, int q_heads, int kv_heads, int head_dim) {
+  const int group = q_heads / kv_heads;
+  const int most = kernel_for<uint16_t>(head_dim, group).partial;
+  const int f32 = kernel_for<float>(head_dim, group).partial;
+  return 2ll * kDaMaxBlocks * (most > f32 ? most : f32) * (int64_t)sizeof(float);
+}
 
 cudaError_t launch_decode_attention(const DecodeArgs& a, cudaStream_t stream) {
-  dim3 grid((unsigned)a.q_heads, (unsigned)a.batch, (unsigned)a.nranks);
+  const int group = a.q_heads / a.kv_heads;
+  const DecodeKernel k = a.dtype == kF32 ? kernel_for<float>(a.head_dim, group) : kernel_for<uint16_t>(a.head_dim, group);
+  int device = 0, sms = 0, per_sm = 0;
+  cudaError_t e = current_device_sms(&device, &sms);
+  if (e != cudaSuccess) return e;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, kDaThreads, 0);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = imin((int64_t)sms * per_sm, kDaMaxBlocks);
   if (trace_on())
-    std::fprintf(stderr, "rar trace: decode_attention nranks=%d batch=%d heads=%d/%d dim=%d grid=%ux%ux%u\n", a.nranks,
-                 a.batch, a.q_heads, a.kv_heads, a.head_dim, grid.x, grid.y, grid.z);
-  if (a.dtype == kF32) decode_attention_kernel<float><<<grid, kDaThreads, 0, stream>>>(a);
-  else decode_attention_kernel<uint16_t><<<grid, kDaThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+    std::fprintf(stderr, "rar trace: decode_attention nranks=%d batch=%d heads=%d/%d dim=%d grid=%lld threads=%d\n",
+                 a.nranks, a.batch, a.q_heads, a.kv_heads, a.head_dim, (long long)grid, kDaThreads);
+  void* params[] = {const_cast<DecodeArgs*>(&a)};
+  return cudaLaunchKernel(k.fn, dim3((unsigned)grid), dim3(kDaThreads), params, 0, stream);
 }
 
 }  // namespace rar

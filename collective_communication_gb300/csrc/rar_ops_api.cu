@@ -96,7 +96,10 @@ int page_shift_of(int page_size) {
     if (page_size == 1 << s) return s;
   return -1;
 }
-bool pages_ok(int num_pages, int shift) { return num_pages >= 1 && ((int64_t)num_pages << shift) <= INT32_MAX; }
+// Slots, and the cache rows that they are for each key head, are 32-bit numbers.
+bool pages_ok(int num_pages, int shift, int64_t kv_heads) {
+  return num_pages >= 1 && ((int64_t)num_pages << shift) <= INT32_MAX / kv_heads;
+}
 
 bool heads_ok(int q_heads, int kv_heads, int head_dim) {
   return q_heads >= 1 && q_heads <= kMaxHeads && kv_heads >= 1 && kv_heads <= kMaxHeads && head_dim >= 8 &&
@@ -175,7 +178,7 @@ rar_status norm_rope_forward(const NormRopeCall& c, const void* const* qkv, int 
   if (cache) {
     if ((st = check_pointers((const void* const*)v_out, c.nranks, c.tokens, 16)) != RAR_OK) return st;
     shift = page_shift_of(page_size);
-    if (shift < 0 || !pages_ok(num_pages, shift) || (slots == nullptr && c.tokens > 0)) return RAR_ERR_ARG;
+    if (shift < 0 || !pages_ok(num_pages, shift, c.kv_heads) || (slots == nullptr && c.tokens > 0)) return RAR_ERR_ARG;
     if (!aligned(slots, 4)) return RAR_ERR_ALIGN;
     s.read(span(slots, c.tokens * 4));
   } else if ((st = check_stride(k_stride, c.kv_heads * D, c.tokens, es)) != RAR_OK) {
@@ -250,7 +253,7 @@ rar_status rar_page_tables(const int32_t* lens, const int32_t* new_tokens, int n
                            int32_t* positions, int32_t* slots, int max_tokens, int32_t* free_count_out, void* workspace,
                            size_t workspaceBytes, void* stream) {
   const int shift = page_shift_of(page_size);
-  if (num_requests < 0 || num_free < 0 || max_tokens < 0 || max_blocks < 1 || shift < 0 || !pages_ok(num_pages, shift))
+  if (num_requests < 0 || num_free < 0 || max_tokens < 0 || max_blocks < 1 || shift < 0 || !pages_ok(num_pages, shift, 1))
     return RAR_ERR_ARG;
   if (num_requests > 1 && table_stride < max_blocks) return RAR_ERR_ARG;
   if (table_stride < 0 || table_stride > INT64_MAX / 8 / (num_requests > 0 ? num_requests : 1)) return RAR_ERR_ARG;
@@ -420,7 +423,7 @@ rar_status rar_decode_attention(const void* const* q, int64_t q_stride, const vo
   const int shift = page_shift_of(page_size);
   const int64_t es = size_of(dtype), D = head_dim;
   if (!heads_ok(q_heads, kv_heads, head_dim) || q_heads % kv_heads != 0) return RAR_ERR_ARG;
-  if (batch < 0 || shift < 0 || !pages_ok(num_pages, shift) || max_blocks < 1) return RAR_ERR_ARG;
+  if (batch < 0 || shift < 0 || !pages_ok(num_pages, shift, kv_heads) || max_blocks < 1) return RAR_ERR_ARG;
   if ((int64_t)max_blocks << shift > INT32_MAX) return RAR_ERR_ARG;
   if (batch > 1 && table_stride < max_blocks) return RAR_ERR_ARG;
   if (table_stride < 0 || table_stride > INT64_MAX / 8 / (batch > 0 ? batch : 1)) return RAR_ERR_ARG;

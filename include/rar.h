@@ -410,7 +410,7 @@ RAR_API rar_status rar_describe_geometry(int nranks, size_t count, rar_dtype dty
  *   k_cache,  [num_pages, kv_heads, page_size, head_dim] contiguous: a page
  *   v_cache   holds page_size tokens (a power of two, 1 to 1024), and a head's
  *             tokens of a page lie together. Slot s is token s % page_size of
- *             page s / page_size; num_pages * page_size < 2^31.
+ *             page s / page_size; num_pages * page_size * kv_heads < 2^31.
  *   block_table  int32 [requests, max_blocks], rows table_stride apart: entry c
  *             is the page of the request's tokens c * page_size and up. Entries
  *             past the request's length are not read.
@@ -516,7 +516,8 @@ RAR_API rar_status rar_qk_norm_rope_backward(const void* const* qkv, int nranks,
  * lens[b] counts the new token, whose key and value are in the cache already.
  * A request of length 0 gives out 0 and lse -inf. Cache rows past a length may
  * hold anything, infinities and NaN too. A key or value of a valid token that
- * is infinite or NaN makes its heads' results infinite or NaN. A page number
+ * is infinite or NaN makes its heads' results infinite or NaN (a token whose
+ * score is -inf has no weight; no token with a weight gives 0 and -inf). A page number
  * outside 0..num_pages-1 within a length, or a length past the table row,
  * reports RAR_ERR_CAPACITY; the tokens concerned are left out.
  * lse: host array of nranks pointers to float [batch, q_heads], or NULL.
