@@ -50,14 +50,17 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 }
 
 // Eight consecutive elements of a row, widened to binary32 (T: float or
-// uint16_t holding bf16 bits; 16-byte aligned).
+// uint16_t holding bf16 bits; 16-byte aligned). load_stream: read once, past L1;
+// absent: -inf in all eight.
 template <typename T>
 struct Pack8;
 template <>
 struct Pack8<uint16_t> {
   uint4 u;
   __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_stream(const uint16_t* p) { u = ld_stream_v4(p); }
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void absent() { u = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
     v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
@@ -74,7 +77,13 @@ struct Pack8<float> {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
   }
+  __device__ __forceinline__ void load_stream(const float* p) {
+    const uint4 u = ld_stream_v4(p), v = ld_stream_v4(p + 4);
+    a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+    b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+  }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void absent() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }

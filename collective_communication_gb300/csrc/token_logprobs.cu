@@ -1,10 +1,25 @@
 // token_logprobs.cu -- log probabilities of given tokens, entropy and the top
 // alternatives over vocabulary shards of virtual ranks, and their gradient.
 //
-//   m = max x, s = sum exp(x - m), lse = m + log s, logprob = x[token] - lse
-//   entropy = log s - sum exp(x - m) (x - m) / s
+//   m = max x, s = sum 2^t, w = sum 2^t t, t = (x - m) log2(e)
+//   lse = m + ln s, logprob = x[token] - lse, entropy = ln 2 (log2 s - w / s)
 // over a row's shards in rank order; the top alternatives are the largest
-// values, the lower index first among equal ones.
+// values, the lower index first among equal ones. One pass: m only has to be
+// near the maximum, so a lane keeps its own and moves it when a value is more
+// than 8 above it (sums to 2^12 times larger lose nothing in binary32); sums
+// with their own m join exactly as partial softmaxes do.
+//
+// The bytes of the logits bound it; about 8 instructions a word leave room for
+// twice the words that memory delivers. Tiles of 2048 columns of all rows are
+// cut into one equal range per resident block, so few rows use all SMs and many
+// rows leave none idle; a row that a cut divides is joined by the block that
+// arrives last at it.
+//
+// Alternatives. Value and index make one 64-bit key. Each warp holds its 32
+// best keys sorted over its lanes and a bound below which nothing can matter:
+// the top-th best of any warp of the block. A value at or above the bound is
+// rare after the first few hundred words; it goes to a queue of the warp, and
+// 32 of those are sorted and merged into the list at a time.
 #include <cstdio>
 
 #include "op_common.cuh"
@@ -13,142 +28,447 @@
 namespace rar {
 
 constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpTile = kLpThreads * 8;   // columns of a tile
+constexpr int kLpAhead = 4;               // tiles' loads in flight
+constexpr int kLpMaxBlocks = 1216;        // most blocks of a forward launch: a partial result and a counter each
+constexpr int kLpQueue = 32 + 256;         // fewer than 32 keys wait; a warp's packs add up to 256
+constexpr int kLpPartFloats = 4 + 2 * 32;  // m, s, w, then 32 keys
+static_assert(kLpMaxBlocks <= kOpCounters, "one arrival counter per block");
 
 namespace {
 
-// The order of the alternatives as one number: the value's bits made monotonic
-// (a NaN above all), then the lower index first.
-__device__ __forceinline__ uint64_t top_key(float v, uint32_t index) {
-  uint32_t u = __float_as_uint(v);
-  u = v != v ? 0xffffffffu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return (uint64_t)u << 32 | (uint32_t)~index;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kFloorT = -1e4f;  // 2^t is 0 far above this; keeps 0 * t finite for words of -inf
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// A value's bits made monotonic, a NaN above all.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return v != v ? 0xffffffffu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+// Larger value first, then the lower index. 0 is below every key.
+__device__ __forceinline__ uint64_t top_key(float v, uint32_t index) { return (uint64_t)ordered(v) << 32 | (uint32_t)~index; }
 __device__ __forceinline__ float key_value(uint64_t key) {
   const uint32_t u = (uint32_t)(key >> 32);
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
+__device__ __forceinline__ int32_t key_index(uint64_t key) { return (int32_t)~(uint32_t)key; }
 
 struct Stat {
-  float m, s, w;  // maximum, sum of exp(x - m), sum of exp(x - m) (x - m)
+  float m, s, w;
 };
 __device__ __forceinline__ Stat join(Stat a, Stat b) {
-  if (a.m == -INFINITY) return b;
-  if (b.m == -INFINITY) return a;
-  if (a.m < b.m) { const Stat t = a; a = b; b = t; }
-  const float d = b.m - a.m, e = expf(d);
-  if (b.s > 0.f || b.s != b.s) {
-    a.w += e > 0.f ? e * (b.w + d * b.s) : e * b.s;
-    a.s += e * b.s;
+  if (a.m < b.m) {
+    const Stat t = a;
+    a = b;
+    b = t;
+  }
+  if (b.m == -INFINITY) {
+    // b has no word of probability: nothing to add, but a NaN among its words counts
+    if (b.s != b.s) a.s = b.s;
+    return a;
+  }
+  const float d = (b.m - a.m) * kLog2e, e = exp2_fast(d);
+  if (e > 0.f) a.w += e * (b.w + d * b.s);
+  a.s += e * b.s;
+  return a;
+}
+__device__ __forceinline__ Stat warp_join(Stat a) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    Stat b;
+    b.m = __shfl_xor_sync(~0u, a.m, d);
+    b.s = __shfl_xor_sync(~0u, a.s, d);
+    b.w = __shfl_xor_sync(~0u, a.w, d);
+    a = join(a, b);
   }
   return a;
 }
 
+// ---- 32 keys sorted over the lanes of a warp, largest in lane 0 ----
+__device__ __forceinline__ uint64_t exchange(uint64_t k, int d, bool keep_large) {
+  const uint64_t o = __shfl_xor_sync(~0u, k, d);
+  return (k > o) == keep_large ? k : o;
+}
+__device__ __forceinline__ uint64_t merge_bitonic(uint64_t k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) k = exchange(k, d, (lane & d) == 0);
+  return k;
+}
+__device__ __forceinline__ uint64_t sort32(uint64_t k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1) k = exchange(k, d, ((lane & d) == 0) == ((lane & size) == 0 || size == 32));
+  return k;
+}
+// The 32 best of two sorted lists, sorted.
+__device__ __forceinline__ uint64_t merge32(uint64_t a, uint64_t b) {
+  const uint64_t o = __shfl_sync(~0u, b, 31 - (threadIdx.x & 31));
+  return merge_bitonic(a > o ? a : o);
+}
+
+// One warp's alternatives.
+struct TopList {
+  uint64_t list, bound;  // sorted over the lanes; keys not above the bound cannot be among the top
+  float bound_value;     // value of the bound, for the quick test
+  int queued;
+};
+
 }  // namespace
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-  __shared__ Stat s_stat[kLpThreads];
-  __shared__ uint64_t s_key[kLpThreads];
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+  __shared__ Stat s_stat[kLpWarps];
+  __shared__ uint64_t s_queue[TOP ? kLpWarps : 1][TOP ? kLpQueue : 1];
+  __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];
+  __shared__ volatile uint64_t s_bound[kLpWarps];
+  __shared__ int s_tiles[kMaxRanks + 1];
+  __shared__ bool s_last;
   if (!op_workspace_ok(a.ws)) return;
-  const int row = blockIdx.x, tid = threadIdx.x;
-  Stat st = {-INFINITY, 0.f, 0.f};
-  for (int r = 0; r < a.nranks; r++) {
-    const T* x = reinterpret_cast<const T*>(a.logits[r]) + (int64_t)row * a.row_stride[r];
-    const int64_t n = a.first[r + 1] - a.first[r];
-    for (int64_t i = tid; i < n; i += kLpThreads) {
-      const float v = to_float(x[i]);
-      if (v == -INFINITY) continue;
-      st = join(st, Stat{v, 1.f, 0.f});
-    }
-  }
-  s_stat[tid] = st;
-  __syncthreads();
-  for (int d = kLpThreads / 2; d > 0; d >>= 1) {
-    if (tid < d) s_stat[tid] = join(s_stat[tid], s_stat[tid + d]);
-    __syncthreads();
-  }
-  st = s_stat[0];
-  if (st.m == INFINITY) st.s = NAN;  // exp(inf - inf)
-  const float log_s = logf(st.s), lse = st.m + log_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    const int64_t token = a.tokens[row];
-    float lp = 0.f;
-    for (int r = 0; r < a.nranks; r++)
-      if (token >= a.first[r] && token < a.first[r + 1])
-        lp = to_float(reinterpret_cast<const T*>(a.logits[r])[(int64_t)row * a.row_stride[r] + token - a.first[r]]) - lse;
-    a.logprob[row] = lp;
-    a.entropy[row] = log_s - st.w / st.s;
-    a.lse[row] = lse;
-  }
-  uint64_t below = ~0ull;
-  for (int k = 0; k < a.top; k++) {
-    uint64_t best = 0;
+    int n = 0;
     for (int r = 0; r < a.nranks; r++) {
-      const T* x = reinterpret_cast<const T*>(a.logits[r]) + (int64_t)row * a.row_stride[r];
-      const int64_t n = a.first[r + 1] - a.first[r];
-      for (int64_t i = tid; i < n; i += kLpThreads) {
-        const uint64_t key = top_key(to_float(x[i]), (uint32_t)(a.first[r] + i));
-        if (key < below && key > best) best = key;
+      s_tiles[r] = n;
+      n += (int)((a.first[r + 1] - a.first[r] + kLpTile - 1) / kLpTile);
+    }
+    s_tiles[a.nranks] = n;
+  }
+  __syncthreads();
+  const int per_row = s_tiles[a.nranks];
+  const int64_t total = (int64_t)a.rows * per_row;
+  const int64_t blocks = total < gridDim.x ? total : gridDim.x;
+  if (blockIdx.x >= blocks) return;
+  auto start_of = [&](int64_t block) { return block * total / blocks; };
+  auto block_of = [&](int64_t tile) { return ((tile + 1) * blocks - 1) / total; };
+  const int64_t end = start_of(blockIdx.x + 1);
+
+  for (int64_t at = start_of(blockIdx.x); at < end;) {
+    const int row = (int)(at / per_row);
+    const int64_t row_first = (int64_t)row * per_row;
+    const int t0 = (int)(at - row_first), t1 = (int)(end - row_first < per_row ? end - row_first : per_row);
+    Stat st = {-INFINITY, 0.f, 0.f};
+    TopList tl = {0, 0, -INFINITY, 0};
+    if (TOP && lane == 0) s_bound[warp] = 0;
+    __syncthreads();
+
+    auto set_bound = [&](uint64_t b) {
+      tl.bound = b;
+      // below every number while there is no bound; a NaN bound lets NaN alone pass the quick test
+      tl.bound_value = b == 0 ? -INFINITY : key_value(b);
+    };
+    auto flush = [&]() {  // up to 32 keys from the queue's end -> list, and a new bound for the block
+      const int first = tl.queued > 32 ? tl.queued - 32 : 0;
+      __syncwarp();
+      const uint64_t k = first + lane < tl.queued ? s_queue[warp][first + lane] : 0;
+      __syncwarp();
+      tl.queued = first;
+      tl.list = merge32(tl.list, sort32(k));
+      const uint64_t b = __shfl_sync(~0u, tl.list, a.top - 1);
+      if (b > tl.bound) {
+        set_bound(b);
+        if (lane == 0) s_bound[warp] = b;
+      }
+    };
+    // v[0..count) are the row's words index, index + 1, ..; count differs by lane
+    auto consider = [&](const float (&v)[8], uint32_t index, int count) {
+      uint64_t b = s_bound[lane & (kLpWarps - 1)];
+#pragma unroll
+      for (int d = kLpWarps / 2; d > 0; d >>= 1) {
+        const uint64_t o = __shfl_xor_sync(~0u, b, d);
+        b = o > b ? o : b;
+      }
+      if (b > tl.bound) set_bound(b);
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const uint64_t key = j < count ? top_key(v[j], index + j) : 0;
+        const bool in = key > tl.bound;
+        const uint32_t votes = __ballot_sync(~0u, in);
+        if (in) s_queue[warp][tl.queued + __popc(votes & ((1u << lane) - 1))] = key;
+        tl.queued += __popc(votes);
+      }
+      while (tl.queued >= 32) flush();
+    };
+    auto add = [&](const float (&v)[8], float pm, uint32_t index, int count) {
+      if (pm > st.m + 8.f) {
+        if (st.m != -INFINITY) {
+          const float d = (st.m - pm) * kLog2e, e = exp2_fast(d);
+          st.w = e > 0.f ? e * (st.w + d * st.s) : 0.f;
+          st.s *= e;
+        }
+        st.m = pm;
+      }
+      const float m = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float t = max_nan((v[j] - m) * kLog2e, kFloorT), e = exp2_fast(t);
+        st.s += e;
+        st.w = fmaf(e, t, st.w);
+      }
+      if (TOP) {
+        // !(<) so that a NaN word, which the maximum leaves out, is looked at through the sum
+        if (__any_sync(~0u, count > 0 && (pm >= tl.bound_value || tl.bound == 0 || st.s != st.s))) consider(v, index, count);
+      }
+    };
+    auto largest = [](const float (&v)[8]) {
+      return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+    };
+
+    bool fresh = true;  // no bound from this part's first words yet
+    for (int t = t0; t < t1;) {
+      int rank = 0;
+      while (t >= s_tiles[rank + 1]) rank++;
+      const int ts = t - s_tiles[rank], te = min(t1, s_tiles[rank + 1]) - s_tiles[rank];
+      const int64_t width = a.first[rank + 1] - a.first[rank];
+      const int64_t c0 = (int64_t)ts * kLpTile, c1 = imin((int64_t)te * kLpTile, width);
+      const T* x = reinterpret_cast<const T*>(a.logits[rank]) + (int64_t)row * a.row_stride[rank] + c0;
+      const int n = (int)(c1 - c0);
+      const uint32_t word = (uint32_t)(a.first[rank] + c0);
+      // words before the first and after the last 16-byte boundary go one to a lane
+      const int head = min(n, (int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T));
+      const int packs = (n - head) / 8, tail = n - head - packs * 8;
+      const T* body = x + head;
+      for (int p0 = 0; p0 < packs; p0 += kLpThreads * kLpAhead) {
+        Pack8<T> u[kLpAhead];
+#pragma unroll
+        for (int i = 0; i < kLpAhead; i++) {
+          const int p = p0 + i * kLpThreads + tid;
+          if (p < packs) u[i].load_stream(body + (int64_t)p * 8);
+          else u[i].absent();
+        }
+        if (TOP && fresh) {
+          // the top-th largest of the lanes' own maxima is a bound from the start
+          fresh = false;
+          float best = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kLpAhead; i++) {
+            float v[8];
+            u[i].widen(v);
+            best = fmaxf(best, largest(v));
+          }
+          const uint64_t k = sort32(best == -INFINITY ? 0 : (uint64_t)ordered(best) << 32);
+          const uint64_t b = __shfl_sync(~0u, k, a.top - 1);
+          if (b != 0) {
+            set_bound(b - 1);
+            tl.bound_value = key_value(b);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kLpAhead; i++) {
+          const int p = p0 + i * kLpThreads + tid;
+          if (p0 + i * kLpThreads >= packs) break;
+          float v[8];
+          u[i].widen(v);
+          add(v, largest(v), word + head + p * 8, p < packs ? 8 : 0);
+        }
+      }
+      if (head + tail > 0 && warp == 0) {
+        const int e = lane < head ? lane : lane - head < tail ? head + packs * 8 + lane - head : -1;
+        float v[8];
+        v[0] = e >= 0 ? to_float(x[e]) : -INFINITY;
+#pragma unroll
+        for (int j = 1; j < 8; j++) v[j] = -INFINITY;
+        add(v, v[0], word + e, e >= 0 ? 1 : 0);
+      }
+      t = te + s_tiles[rank];
+    }
+    if constexpr (TOP) {
+      while (tl.queued > 0) flush();
+    }
+
+    // the block's warps join
+    st = warp_join(st);
+    if (lane == 0) s_stat[warp] = st;
+    auto join_lists = [&]() {  // tl.list of all warps -> s_list[0]
+      if (!TOP) return;
+#pragma unroll
+      for (int d = kLpWarps / 2; d > 0; d >>= 1) {
+        if (warp >= d && warp < 2 * d) s_list[warp][lane] = tl.list;
+        __syncthreads();
+        if (warp < d) tl.list = merge32(tl.list, s_list[warp + d][lane]);
+      }
+    };
+    join_lists();
+    __syncthreads();
+    if (warp == 0) st = warp_join(lane < kLpWarps ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f});
+
+    bool mine = true;  // this block has the whole row's result
+    if (t0 != 0 || t1 != per_row) {
+      const int cf = (int)block_of(row_first), cl = (int)block_of(row_first + per_row - 1);
+      float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset);
+      const bool starts_at_cf = start_of(cf) == row_first;
+      auto part_of = [&](int block) {  // of its first row, or of the row that starts in it and goes on
+        return parts + (2 * block + (block == cf && !starts_at_cf)) * kLpPartFloats;
+      };
+      if (warp == 0) {
+        float* part = part_of(blockIdx.x);
+        if (lane == 0) {
+          part[0] = st.m;
+          part[1] = st.s;
+          part[2] = st.w;
+        }
+        if (TOP) reinterpret_cast<uint64_t*>(part + 4)[lane] = tl.list;
+        __threadfence();
+      }
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t* counter = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes) + cf;
+        s_last = atomicAdd(counter, 1u) == (uint32_t)(cl - cf);
+        if (s_last) *counter = 0;
+      }
+      __syncthreads();
+      mine = s_last;
+      if (mine) {
+        __threadfence();
+        st = {-INFINITY, 0.f, 0.f};
+        tl.list = 0;
+        for (int p = cf + tid; p <= cl; p += kLpThreads) {
+          const float* part = part_of(p);
+          st = join(st, Stat{__ldcg(part), __ldcg(part + 1), __ldcg(part + 2)});
+        }
+        if (TOP)
+          for (int p = cf + warp; p <= cl; p += kLpWarps)
+            tl.list = merge32(tl.list, __ldcg(reinterpret_cast<const unsigned long long*>(part_of(p) + 4) + lane));
+        st = warp_join(st);
+        if (lane == 0) s_stat[warp] = st;
+        join_lists();
+        __syncthreads();
+        if (warp == 0) st = warp_join(lane < kLpWarps ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f});
       }
     }
-    s_key[tid] = best;
-    __syncthreads();
-    for (int d = kLpThreads / 2; d > 0; d >>= 1) {
-      if (tid < d && s_key[tid + d] > s_key[tid]) s_key[tid] = s_key[tid + d];
-      __syncthreads();
+    if (mine && warp == 0) {
+      if (st.m == INFINITY) st.s = NAN;  // exp(inf - inf)
+      const float log2_s = log2f(st.s), lse = st.m + kLn2 * log2_s;
+      if (lane == 0) {
+        const int64_t token = a.tokens[row];
+        float lp = 0.f;
+        for (int r = 0; r < a.nranks; r++)
+          if (token >= a.first[r] && token < a.first[r + 1])
+            lp = to_float(reinterpret_cast<const T*>(a.logits[r])[(int64_t)row * a.row_stride[r] + token - a.first[r]]) - lse;
+        a.logprob[row] = lp;
+        a.entropy[row] = kLn2 * (log2_s - st.w / st.s);
+        a.lse[row] = lse;
+      }
+      if (TOP && lane < a.top) {
+        a.top_values[(int64_t)row * a.top + lane] = key_value(tl.list) - lse;
+        a.top_ids[(int64_t)row * a.top + lane] = key_index(tl.list);
+      }
     }
-    below = s_key[0];
-    __syncthreads();
-    if (tid == 0) {
-      a.top_values[(int64_t)row * a.top + k] = key_value(below) - lse;
-      a.top_ids[(int64_t)row * a.top + k] = (int32_t)~(uint32_t)below;
-    }
+    at = row_first + t1;
   }
 }
 
-// dx = g ([i == token] - p) - h p (log p + entropy), p = exp(x - lse); g counts
-// only if a token was asked for. One pass; a shard's row may start on any
-// element, so its ends up to the first 16-byte boundary go one by one.
+// dx = g ([i == token] - p) - h p (y + entropy), y = x - lse, p = exp(y); g counts
+// only if a token was asked for. One pass, read and written once; a block takes
+// kLpBwdTile columns of a row of a shard.
+constexpr int kLpBwdTile = kLpThreads * 8 * 8;
+
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a) {
+__global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a,
+                                                                       int tiles) {
   if (!op_workspace_ok(a.ws)) return;
-  const int row = blockIdx.x, rank = blockIdx.y, tid = threadIdx.x;
-  const T* x = reinterpret_cast<const T*>(a.logits[rank]) + (int64_t)row * a.row_stride[rank];
-  T* dx = reinterpret_cast<T*>(a.dlogits[rank]) + (int64_t)row * a.drow_stride[rank];
-  const int64_t n = a.first[rank + 1] - a.first[rank];
-  const float lse = a.lse[row], H = a.entropy[row];
+  const int row = (int)(blockIdx.x / (unsigned)tiles), tile = (int)(blockIdx.x % (unsigned)tiles);
+  const int rank = blockIdx.y, tid = threadIdx.x;
+  const int64_t width = a.first[rank + 1] - a.first[rank], c0 = (int64_t)tile * kLpBwdTile;
+  if (c0 >= width) return;
+  const int n = (int)imin(kLpBwdTile, width - c0);
+  const T* x = reinterpret_cast<const T*>(a.logits[rank]) + (int64_t)row * a.row_stride[rank] + c0;
+  T* dx = reinterpret_cast<T*>(a.dlogits[rank]) + (int64_t)row * a.drow_stride[rank] + c0;
+  const float lse = a.lse[row];
   const float h = a.grad_entropy != nullptr ? a.grad_entropy[row] : 0.f;
   const int64_t token = a.tokens[row];
   const bool asked = token >= 0 && token < a.first[a.nranks];
   const float g = asked ? a.grad_logprob[row] : 0.f;
-  const int64_t mine = token - a.first[rank];
-  for (int64_t i = tid; i < n; i += kLpThreads) {
-    const float y = to_float(x[i]) - lse, p = expf(y);
-    float d = p == 0.f ? 0.f : -p * (g + h * (y + H));
-    if (i == mine && asked) d += g;
-    from_float(dx + i, d);
+  const float base = g + h * a.entropy[row];
+  const int64_t at = token - a.first[rank] - c0;
+  const int mine = asked && at >= 0 && at < n ? (int)at : -1;
+  auto grad = [&](float v) {
+    const float y = max_nan(v - lse, kFloorT);
+    return -exp2_fast(y * kLog2e) * fmaf(h, y, base);
+  };
+  // rows that share a 16-byte phase go in packs, the ends one by one; others one by one altogether
+  const bool together = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;
+  const int head = together ? min(n, (int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T)) : n;
+  const int packs = (n - head) / 8, done = head + packs * 8;
+  for (int p0 = 0; p0 < packs; p0 += kLpThreads * kLpAhead) {
+    Pack8<T> u[kLpAhead];
+#pragma unroll
+    for (int i = 0; i < kLpAhead; i++) {
+      const int p = p0 + i * kLpThreads + tid;
+      if (p < packs) u[i].load_stream(x + head + (int64_t)p * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kLpAhead; i++) {
+      const int p = p0 + i * kLpThreads + tid;
+      if (p >= packs) break;
+      float v[8];
+      u[i].widen(v);
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[j] = grad(v[j]);
+      const int k = mine - head - p * 8;
+      if ((unsigned)k < 8u) {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+          if (j == k) v[j] += g;
+      }
+      u[i].narrow(v);
+      u[i].store(dx + head + (int64_t)p * 8);
+    }
+  }
+  for (int i = tid; i < head + n - done; i += kLpThreads) {
+    const int e = i < head ? i : done + i - head;
+    from_float(dx + e, grad(to_float(x[e])) + (e == mine ? g : 0.f));
   }
 }
 
-int64_t token_logprobs_scratch_bytes(int, int) { return 0; }
+int64_t token_logprobs_scratch_bytes(int, int) { return 2ll * kLpMaxBlocks * kLpPartFloats * (int64_t)sizeof(float); }
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
+  const void* fn = a.dtype == kF32 ? (a.top > 0 ? (const void*)token_logprobs_kernel<float, true>
+                                                : (const void*)token_logprobs_kernel<float, false>)
+                                   : (a.top > 0 ? (const void*)token_logprobs_kernel<uint16_t, true>
+                                                : (const void*)token_logprobs_kernel<uint16_t, false>);
+  int device = 0, sms = 0, per_sm = 0;
+  cudaError_t e = current_device_sms(&device, &sms);
+  if (e != cudaSuccess) return e;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kLpThreads, 0);
+  if (e != cudaSuccess) return e;
+  int64_t tiles = 0;
+  for (int r = 0; r < a.nranks; r++) tiles += div_up(a.first[r + 1] - a.first[r], kLpTile);
+  const int64_t grid = imin(imin((int64_t)sms * per_sm, kLpMaxBlocks), tiles * a.rows);
   if (trace_on())
-    std::fprintf(stderr, "rar trace: token_logprobs nranks=%d rows=%d vocab=%lld top=%d\n", a.nranks, a.rows,
-                 (long long)a.first[a.nranks], a.top);
-  if (a.dtype == kF32) token_logprobs_kernel<float><<<a.rows, kLpThreads, 0, stream>>>(a);
-  else token_logprobs_kernel<uint16_t><<<a.rows, kLpThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+    std::fprintf(stderr, "rar trace: token_logprobs nranks=%d rows=%d vocab=%lld top=%d grid=%lld\n", a.nranks, a.rows,
+                 (long long)a.first[a.nranks], a.top, (long long)grid);
+  void* params[] = {const_cast<LogprobArgs*>(&a)};
+  return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kLpThreads), params, 0, stream);
 }
 
 cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, cudaStream_t stream) {
+  int64_t widest = 0;
+  for (int r = 0; r < a.nranks; r++) widest = imax(widest, a.first[r + 1] - a.first[r]);
+  int tiles = (int)div_up(widest, kLpBwdTile);
   if (trace_on())
-    std::fprintf(stderr, "rar trace: token_logprobs_backward nranks=%d rows=%d vocab=%lld\n", a.nranks, a.rows,
-                 (long long)a.first[a.nranks]);
-  dim3 grid((unsigned)a.rows, (unsigned)a.nranks);
-  if (a.dtype == kF32) token_logprobs_bwd_kernel<float><<<grid, kLpThreads, 0, stream>>>(a);
-  else token_logprobs_bwd_kernel<uint16_t><<<grid, kLpThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+    std::fprintf(stderr, "rar trace: token_logprobs_backward nranks=%d rows=%d vocab=%lld tiles=%d\n", a.nranks, a.rows,
+                 (long long)a.first[a.nranks], tiles);
+  dim3 grid((unsigned)((int64_t)a.rows * tiles), (unsigned)a.nranks);
+  const void* fn = a.dtype == kF32 ? (const void*)token_logprobs_bwd_kernel<float>
+                                   : (const void*)token_logprobs_bwd_kernel<uint16_t>;
+  void* params[] = {const_cast<LogprobBwdArgs*>(&a), &tiles};
+  return cudaLaunchKernel(fn, grid, dim3(kLpThreads), params, 0, stream);
 }
 
 }  // namespace rar
