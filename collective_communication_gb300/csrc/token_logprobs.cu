@@ -17,9 +17,9 @@
 //
 // Alternatives. Value and index make one 64-bit key. Each warp holds its 32
 // best keys sorted over its lanes and a bound below which nothing can matter:
-// the top-th best of any warp of the block. A value at or above the bound is
-// rare after the first few hundred words; it goes to a queue of the warp, and
-// 32 of those are sorted and merged into the list at a time.
+// the top-th best of any warp of the block. The first words' bound is the
+// top-th largest of the lanes' own maxima; after that a word at or above the
+// bound is rare, and is read again and inserted where it belongs.
 #include <cstdio>
 
 #include "op_common.cuh"
@@ -30,9 +30,8 @@ namespace rar {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpTile = kLpThreads * 8;   // columns of a tile
-constexpr int kLpAhead = 4;               // tiles' loads in flight
+constexpr int kLpBytesAhead = 64;          // bytes a thread has in flight
 constexpr int kLpMaxBlocks = 1216;        // most blocks of a forward launch: a partial result and a counter each
-constexpr int kLpQueue = 32 + 256;         // fewer than 32 keys wait; a warp's packs add up to 256
 constexpr int kLpPartFloats = 4 + 2 * 32;  // m, s, w, then 32 keys
 static_assert(kLpMaxBlocks <= kOpCounters, "one arrival counter per block");
 
@@ -121,19 +120,29 @@ __device__ __forceinline__ uint64_t merge32(uint64_t a, uint64_t b) {
   return merge_bitonic(a > o ? a : o);
 }
 
-// One warp's alternatives.
-struct TopList {
-  uint64_t list, bound;  // sorted over the lanes; keys not above the bound cannot be among the top
-  float bound_value;     // value of the bound, for the quick test
-  int queued;
-};
+// The list with one more key, without its last.
+__device__ __forceinline__ uint64_t insert32(uint64_t list, uint64_t key) {
+  const int lane = threadIdx.x & 31, at = __popc(__ballot_sync(~0u, list > key));
+  const uint64_t up = __shfl_up_sync(~0u, list, 1);
+  return lane < at ? list : lane == at ? key : up;
+}
+
+// The largest of eight values, NaN left out.
+__device__ __forceinline__ float largest(const Pack8<uint16_t>& u) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u.u);
+  const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+  return fmaxf(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ float largest(const Pack8<float>& u) {
+  return fmaxf(fmaxf(fmaxf(u.a.x, u.a.y), fmaxf(u.a.z, u.a.w)), fmaxf(fmaxf(u.b.x, u.b.y), fmaxf(u.b.z, u.b.w)));
+}
 
 }  // namespace
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   __shared__ Stat s_stat[kLpWarps];
-  __shared__ uint64_t s_queue[TOP ? kLpWarps : 1][TOP ? kLpQueue : 1];
   __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];
   __shared__ volatile uint64_t s_bound[kLpWarps];
   __shared__ int s_tiles[kMaxRanks + 1];
@@ -162,48 +171,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
     const int64_t row_first = (int64_t)row * per_row;
     const int t0 = (int)(at - row_first), t1 = (int)(end - row_first < per_row ? end - row_first : per_row);
     Stat st = {-INFINITY, 0.f, 0.f};
-    TopList tl = {0, 0, -INFINITY, 0};
+    uint64_t list = 0, bound = 0;  // sorted over the lanes; keys not above the bound cannot be among the top
+    float bound_value = 0.f;       // value of the bound, for the quick test
     if (TOP && lane == 0) s_bound[warp] = 0;
     __syncthreads();
 
-    auto set_bound = [&](uint64_t b) {
-      tl.bound = b;
-      // below every number while there is no bound; a NaN bound lets NaN alone pass the quick test
-      tl.bound_value = b == 0 ? -INFINITY : key_value(b);
-    };
-    auto flush = [&]() {  // up to 32 keys from the queue's end -> list, and a new bound for the block
-      const int first = tl.queued > 32 ? tl.queued - 32 : 0;
-      __syncwarp();
-      const uint64_t k = first + lane < tl.queued ? s_queue[warp][first + lane] : 0;
-      __syncwarp();
-      tl.queued = first;
-      tl.list = merge32(tl.list, sort32(k));
-      const uint64_t b = __shfl_sync(~0u, tl.list, a.top - 1);
-      if (b > tl.bound) {
-        set_bound(b);
-        if (lane == 0) s_bound[warp] = b;
-      }
-    };
-    // v[0..count) are the row's words index, index + 1, ..; count differs by lane
-    auto consider = [&](const float (&v)[8], uint32_t index, int count) {
-      uint64_t b = s_bound[lane & (kLpWarps - 1)];
-#pragma unroll
-      for (int d = kLpWarps / 2; d > 0; d >>= 1) {
-        const uint64_t o = __shfl_xor_sync(~0u, b, d);
-        b = o > b ? o : b;
-      }
-      if (b > tl.bound) set_bound(b);
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const uint64_t key = j < count ? top_key(v[j], index + j) : 0;
-        const bool in = key > tl.bound;
-        const uint32_t votes = __ballot_sync(~0u, in);
-        if (in) s_queue[warp][tl.queued + __popc(votes & ((1u << lane) - 1))] = key;
-        tl.queued += __popc(votes);
-      }
-      while (tl.queued >= 32) flush();
-    };
-    auto add = [&](const float (&v)[8], float pm, uint32_t index, int count) {
+    auto add = [&](const Pack8<T>& u, float pm) {
       if (pm > st.m + 8.f) {
         if (st.m != -INFINITY) {
           const float d = (st.m - pm) * kLog2e, e = exp2_fast(d);
@@ -213,21 +186,49 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         st.m = pm;
       }
       const float m = st.m == -INFINITY ? 0.f : st.m;
+      float v[8];
+      u.widen(v);
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         const float t = max_nan((v[j] - m) * kLog2e, kFloorT), e = exp2_fast(t);
         st.s += e;
         st.w = fmaf(e, t, st.w);
       }
-      if (TOP) {
-        // !(<) so that a NaN word, which the maximum leaves out, is looked at through the sum
-        if (__any_sync(~0u, count > 0 && (pm >= tl.bound_value || tl.bound == 0 || st.s != st.s))) consider(v, index, count);
-      }
     };
-    auto largest = [](const float (&v)[8]) {
-      return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+    // Words that may be among the top: bit b of a lane's mask is word[8 kLpThreads (b / 8) + b % 8].
+    auto consider = [&](const T* word, uint32_t index, uint32_t mask) {
+      uint64_t b = s_bound[lane & (kLpWarps - 1)];
+#pragma unroll
+      for (int d = kLpWarps / 2; d > 0; d >>= 1) {
+        const uint64_t o = __shfl_xor_sync(~0u, b, d);
+        b = o > b ? o : b;
+      }
+      if (b > bound) bound = b;
+      bool grew = false;
+      while (__any_sync(~0u, mask != 0)) {
+        uint64_t key = 0;
+        if (mask != 0) {
+          const int bit = __ffs(mask) - 1, off = (bit >> 3) * (kLpThreads * 8) + (bit & 7);
+          key = top_key(to_float(word[off]), index + off);
+          mask &= mask - 1;
+        }
+        uint32_t votes = __ballot_sync(~0u, key > bound);
+        while (votes != 0) {
+          const int src = __ffs(votes) - 1;
+          list = insert32(list, __shfl_sync(~0u, key, src));
+          const uint64_t last = __shfl_sync(~0u, list, a.top - 1);
+          if (last > bound) {
+            bound = last;
+            grew = true;
+          }
+          votes = __ballot_sync(~0u, key > bound) & (~0u << src) << 1;
+        }
+      }
+      if (grew && lane == 0) s_bound[warp] = bound;
+      bound_value = bound == 0 ? -INFINITY : key_value(bound);
     };
 
+    constexpr int kAhead = kLpBytesAhead / (8 * (int)sizeof(T));
     bool fresh = true;  // no bound from this part's first words yet
     for (int t = t0; t < t1;) {
       int rank = 0;
@@ -242,64 +243,69 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
       const int head = min(n, (int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T));
       const int packs = (n - head) / 8, tail = n - head - packs * 8;
       const T* body = x + head;
-      for (int p0 = 0; p0 < packs; p0 += kLpThreads * kLpAhead) {
-        Pack8<T> u[kLpAhead];
+      // a thread's packs are kLpThreads apart
+      for (int p = tid; p - tid < packs; p += kLpThreads * kAhead) {
+        Pack8<T> u[kAhead];
+        float pm[kAhead], best = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kLpAhead; i++) {
-          const int p = p0 + i * kLpThreads + tid;
-          if (p < packs) u[i].load_stream(body + (int64_t)p * 8);
+        for (int i = 0; i < kAhead; i++) {
+          if (p + i * kLpThreads < packs) u[i].load_stream(body + (int64_t)(p + i * kLpThreads) * 8);
           else u[i].absent();
         }
-        if (TOP && fresh) {
-          // the top-th largest of the lanes' own maxima is a bound from the start
-          fresh = false;
-          float best = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < kLpAhead; i++) {
-            float v[8];
-            u[i].widen(v);
-            best = fmaxf(best, largest(v));
-          }
-          const uint64_t k = sort32(best == -INFINITY ? 0 : (uint64_t)ordered(best) << 32);
-          const uint64_t b = __shfl_sync(~0u, k, a.top - 1);
-          if (b != 0) {
-            set_bound(b - 1);
-            tl.bound_value = key_value(b);
-          }
+        for (int i = 0; i < kAhead; i++) {
+          pm[i] = largest(u[i]);
+          best = fmaxf(best, pm[i]);
+          add(u[i], pm[i]);
         }
+        if constexpr (TOP) {
+          if (fresh) {
+            fresh = false;
+            const uint64_t k = sort32(best == -INFINITY ? 0 : (uint64_t)ordered(best) << 32);
+            const uint64_t b = __shfl_sync(~0u, k, a.top - 1);
+            if (b != 0) bound = b - 1;
+            bound_value = b == 0 ? -INFINITY : key_value(b);
+          }
+          // a NaN, which the maxima leave out, shows in the sum; !(<) lets it, and all words under a NaN bound, in
+          if (__any_sync(~0u, !(best < bound_value) || st.s != st.s)) {
+            uint32_t mask = 0;
 #pragma unroll
-        for (int i = 0; i < kLpAhead; i++) {
-          const int p = p0 + i * kLpThreads + tid;
-          if (p0 + i * kLpThreads >= packs) break;
-          float v[8];
-          u[i].widen(v);
-          add(v, largest(v), word + head + p * 8, p < packs ? 8 : 0);
+            for (int i = 0; i < kAhead; i++) {
+              float v[8];
+              u[i].widen(v);
+              if (p + i * kLpThreads < packs)
+#pragma unroll
+                for (int j = 0; j < 8; j++) mask |= !(v[j] < bound_value) ? 1u << (8 * i + j) : 0u;
+            }
+            consider(body + (int64_t)p * 8, word + head + p * 8, mask);
+          }
         }
       }
       if (head + tail > 0 && warp == 0) {
         const int e = lane < head ? lane : lane - head < tail ? head + packs * 8 + lane - head : -1;
-        float v[8];
-        v[0] = e >= 0 ? to_float(x[e]) : -INFINITY;
-#pragma unroll
-        for (int j = 1; j < 8; j++) v[j] = -INFINITY;
-        add(v, v[0], word + e, e >= 0 ? 1 : 0);
+        const float v = e >= 0 ? to_float(x[e]) : -INFINITY;
+        Stat one = {v, v == -INFINITY ? 0.f : 1.f, 0.f};
+        if (v != v) one = {-INFINITY, v, 0.f};
+        st = join(st, one);
+        if constexpr (TOP) {
+          if (fresh) bound_value = -INFINITY;
+          consider(x + e, word + e, e >= 0 && !(v < bound_value) ? 1u : 0u);
+        }
       }
       t = te + s_tiles[rank];
-    }
-    if constexpr (TOP) {
-      while (tl.queued > 0) flush();
     }
 
     // the block's warps join
     st = warp_join(st);
     if (lane == 0) s_stat[warp] = st;
-    auto join_lists = [&]() {  // tl.list of all warps -> s_list[0]
-      if (!TOP) return;
+    auto join_lists = [&]() {  // list of all warps -> s_list[0]
+      if constexpr (TOP) {
 #pragma unroll
-      for (int d = kLpWarps / 2; d > 0; d >>= 1) {
-        if (warp >= d && warp < 2 * d) s_list[warp][lane] = tl.list;
-        __syncthreads();
-        if (warp < d) tl.list = merge32(tl.list, s_list[warp + d][lane]);
+        for (int d = kLpWarps / 2; d > 0; d >>= 1) {
+          if (warp >= d && warp < 2 * d) s_list[warp][lane] = list;
+          __syncthreads();
+          if (warp < d) list = merge32(list, s_list[warp + d][lane]);
+        }
       }
     };
     join_lists();
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
           part[1] = st.s;
           part[2] = st.w;
         }
-        if (TOP) reinterpret_cast<uint64_t*>(part + 4)[lane] = tl.list;
+        if (TOP) reinterpret_cast<uint64_t*>(part + 4)[lane] = list;
         __threadfence();
       }
       __syncthreads();
@@ -335,14 +341,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
       if (mine) {
         __threadfence();
         st = {-INFINITY, 0.f, 0.f};
-        tl.list = 0;
+        list = 0;
         for (int p = cf + tid; p <= cl; p += kLpThreads) {
           const float* part = part_of(p);
           st = join(st, Stat{__ldcg(part), __ldcg(part + 1), __ldcg(part + 2)});
         }
         if (TOP)
           for (int p = cf + warp; p <= cl; p += kLpWarps)
-            tl.list = merge32(tl.list, __ldcg(reinterpret_cast<const unsigned long long*>(part_of(p) + 4) + lane));
+            list = merge32(list, __ldcg(reinterpret_cast<const unsigned long long*>(part_of(p) + 4) + lane));
         st = warp_join(st);
         if (lane == 0) s_stat[warp] = st;
         join_lists();
@@ -364,8 +370,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         a.lse[row] = lse;
       }
       if (TOP && lane < a.top) {
-        a.top_values[(int64_t)row * a.top + lane] = key_value(tl.list) - lse;
-        a.top_ids[(int64_t)row * a.top + lane] = key_index(tl.list);
+        a.top_values[(int64_t)row * a.top + lane] = key_value(list) - lse;
+        a.top_ids[(int64_t)row * a.top + lane] = key_index(list);
       }
     }
     at = row_first + t1;
@@ -404,15 +410,16 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __
   const bool together = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;
   const int head = together ? min(n, (int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T)) : n;
   const int packs = (n - head) / 8, done = head + packs * 8;
-  for (int p0 = 0; p0 < packs; p0 += kLpThreads * kLpAhead) {
-    Pack8<T> u[kLpAhead];
+  constexpr int kAhead = kLpBytesAhead / (8 * (int)sizeof(T));
+  for (int p0 = 0; p0 < packs; p0 += kLpThreads * kAhead) {
+    Pack8<T> u[kAhead];
 #pragma unroll
-    for (int i = 0; i < kLpAhead; i++) {
+    for (int i = 0; i < kAhead; i++) {
       const int p = p0 + i * kLpThreads + tid;
       if (p < packs) u[i].load_stream(x + head + (int64_t)p * 8);
     }
 #pragma unroll
-    for (int i = 0; i < kLpAhead; i++) {
+    for (int i = 0; i < kAhead; i++) {
       const int p = p0 + i * kLpThreads + tid;
       if (p >= packs) break;
       float v[8];
