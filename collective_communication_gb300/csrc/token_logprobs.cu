@@ -16,10 +16,11 @@
 // arrives last at it.
 //
 // Alternatives. Value and index make one 64-bit key. Each warp holds its 32
-// best keys sorted over its lanes and a bound below which nothing can matter:
-// the top-th best of any warp of the block. The first words' bound is the
-// top-th largest of the lanes' own maxima; after that a word at or above the
-// bound is rare, and is read again and inserted where it belongs.
+// best keys sorted over its lanes and a bound below which nothing can matter.
+// The first words' bound is the top-th largest of the threads' own maxima; it
+// is renewed from all warps' lists whenever the words read have doubled. A word
+// at or above the bound is rare then (about top / (words read) of them), and is
+// read again and inserted where it belongs.
 #include <cstdio>
 
 #include "op_common.cuh"
@@ -127,6 +128,29 @@ __device__ __forceinline__ uint64_t insert32(uint64_t list, uint64_t key) {
   return lane < at ? list : lane == at ? key : up;
 }
 
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%6, %7};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+
 // The largest of eight values, NaN left out.
 __device__ __forceinline__ float largest(const Pack8<uint16_t>& u) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u.u);
@@ -144,7 +168,7 @@ template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   __shared__ Stat s_stat[kLpWarps];
   __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];
-  __shared__ volatile uint64_t s_bound[kLpWarps];
+  __shared__ uint64_t s_bound;
   __shared__ int s_tiles[kMaxRanks + 1];
   __shared__ bool s_last;
   if (!op_workspace_ok(a.ws)) return;
@@ -171,17 +195,15 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
     const int64_t row_first = (int64_t)row * per_row;
     const int t0 = (int)(at - row_first), t1 = (int)(end - row_first < per_row ? end - row_first : per_row);
     Stat st = {-INFINITY, 0.f, 0.f};
+    float2 s2 = make_float2(0.f, 0.f), w2 = s2;  // st.s and st.w in two halves, added at the end
     uint64_t list = 0, bound = 0;  // sorted over the lanes; keys not above the bound cannot be among the top
     float bound_value = 0.f;       // value of the bound, for the quick test
-    if (TOP && lane == 0) s_bound[warp] = 0;
-    __syncthreads();
-
     auto add = [&](const Pack8<T>& u, float pm) {
       if (pm > st.m + 8.f) {
         if (st.m != -INFINITY) {
           const float d = (st.m - pm) * kLog2e, e = exp2_fast(d);
-          st.w = e > 0.f ? e * (st.w + d * st.s) : 0.f;
-          st.s *= e;
+          w2 = e > 0.f ? make_float2(e * (w2.x + d * s2.x), e * (w2.y + d * s2.y)) : make_float2(0.f, 0.f);
+          s2 = make_float2(s2.x * e, s2.y * e);
         }
         st.m = pm;
       }
@@ -189,22 +211,28 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
       float v[8];
       u.widen(v);
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const float t = max_nan((v[j] - m) * kLog2e, kFloorT), e = exp2_fast(t);
-        st.s += e;
-        st.w = fmaf(e, t, st.w);
+      for (int j = 0; j < 8; j += 2) {
+        float2 t = mul2(add2(make_float2(v[j], v[j + 1]), make_float2(-m, -m)), make_float2(kLog2e, kLog2e));
+        t = make_float2(max_nan(t.x, kFloorT), max_nan(t.y, kFloorT));
+        const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+        s2 = add2(s2, e);
+        w2 = fma2(e, t, w2);
       }
+    };
+    // The top-th key of the warps' sorted keys together, for all threads; every thread of the block calls it.
+    auto block_bound = [&](uint64_t k) {
+#pragma unroll
+      for (int d = kLpWarps / 2; d > 0; d >>= 1) {
+        if (warp >= d && warp < 2 * d) s_list[warp][lane] = k;
+        __syncthreads();
+        if (warp < d) k = merge32(k, s_list[warp + d][lane]);
+      }
+      if (warp == 0 && lane == a.top - 1) s_bound = k;
+      __syncthreads();
+      return s_bound;
     };
     // Words that may be among the top: bit b of a lane's mask is word[8 kLpThreads (b / 8) + b % 8].
     auto consider = [&](const T* word, uint32_t index, uint32_t mask) {
-      uint64_t b = s_bound[lane & (kLpWarps - 1)];
-#pragma unroll
-      for (int d = kLpWarps / 2; d > 0; d >>= 1) {
-        const uint64_t o = __shfl_xor_sync(~0u, b, d);
-        b = o > b ? o : b;
-      }
-      if (b > bound) bound = b;
-      bool grew = false;
       while (__any_sync(~0u, mask != 0)) {
         uint64_t key = 0;
         if (mask != 0) {
@@ -217,19 +245,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
           const int src = __ffs(votes) - 1;
           list = insert32(list, __shfl_sync(~0u, key, src));
           const uint64_t last = __shfl_sync(~0u, list, a.top - 1);
-          if (last > bound) {
-            bound = last;
-            grew = true;
-          }
+          bound = last > bound ? last : bound;
           votes = __ballot_sync(~0u, key > bound) & (~0u << src) << 1;
         }
       }
-      if (grew && lane == 0) s_bound[warp] = bound;
       bound_value = bound == 0 ? -INFINITY : key_value(bound);
     };
 
     constexpr int kAhead = kLpBytesAhead / (8 * (int)sizeof(T));
-    bool fresh = true;  // no bound from this part's first words yet
+    int round = 0;  // of kAhead packs a thread
+    const bool alone = t1 - t0 <= kAhead;  // one round has all words: a bound of the warp will do
     for (int t = t0; t < t1;) {
       int rank = 0;
       while (t >= s_tiles[rank + 1]) rank++;
@@ -246,7 +271,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
       // a thread's packs are kLpThreads apart
       for (int p = tid; p - tid < packs; p += kLpThreads * kAhead) {
         Pack8<T> u[kAhead];
-        float pm[kAhead], best = -INFINITY;
+        float best = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
           if (p + i * kLpThreads < packs) u[i].load_stream(body + (int64_t)(p + i * kLpThreads) * 8);
@@ -254,28 +279,37 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         }
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
-          pm[i] = largest(u[i]);
-          best = fmaxf(best, pm[i]);
-          add(u[i], pm[i]);
+          const float pm = largest(u[i]);
+          best = fmaxf(best, pm);
+          add(u[i], pm);
         }
         if constexpr (TOP) {
-          if (fresh) {
-            fresh = false;
+          if (round == 0) {
             const uint64_t k = sort32(best == -INFINITY ? 0 : (uint64_t)ordered(best) << 32);
-            const uint64_t b = __shfl_sync(~0u, k, a.top - 1);
-            if (b != 0) bound = b - 1;
+            const uint64_t b = alone ? __shfl_sync(~0u, k, a.top - 1) : block_bound(k);
+            if (b > bound) bound = b - 1;
             bound_value = b == 0 ? -INFINITY : key_value(b);
+          } else if ((round & (round - 1)) == 0) {
+            const uint64_t b = block_bound(list);
+            if (b > bound) {
+              bound = b;
+              bound_value = key_value(b);
+            }
           }
+          round++;
           // a NaN, which the maxima leave out, shows in the sum; !(<) lets it, and all words under a NaN bound, in
-          if (__any_sync(~0u, !(best < bound_value) || st.s != st.s)) {
+          const bool nan = s2.x != s2.x || s2.y != s2.y;
+          if (__any_sync(~0u, !(best < bound_value) || nan)) {
             uint32_t mask = 0;
 #pragma unroll
             for (int i = 0; i < kAhead; i++) {
-              float v[8];
-              u[i].widen(v);
-              if (p + i * kLpThreads < packs)
+              const bool in = p + i * kLpThreads < packs && (!(largest(u[i]) < bound_value) || nan);
+              if (__any_sync(~0u, in)) {
+                float v[8];
+                u[i].widen(v);
 #pragma unroll
-                for (int j = 0; j < 8; j++) mask |= !(v[j] < bound_value) ? 1u << (8 * i + j) : 0u;
+                for (int j = 0; j < 8; j++) mask |= in && !(v[j] < bound_value) ? 1u << (8 * i + j) : 0u;
+              }
             }
             consider(body + (int64_t)p * 8, word + head + p * 8, mask);
           }
@@ -286,9 +320,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         const float v = e >= 0 ? to_float(x[e]) : -INFINITY;
         Stat one = {v, v == -INFINITY ? 0.f : 1.f, 0.f};
         if (v != v) one = {-INFINITY, v, 0.f};
-        st = join(st, one);
+        st = join(Stat{st.m, s2.x + s2.y, w2.x + w2.y}, one);
+        s2 = make_float2(st.s, 0.f);
+        w2 = make_float2(st.w, 0.f);
         if constexpr (TOP) {
-          if (fresh) bound_value = -INFINITY;
+          if (round == 0) bound_value = -INFINITY;
           consider(x + e, word + e, e >= 0 && !(v < bound_value) ? 1u : 0u);
         }
       }
@@ -296,7 +332,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
     }
 
     // the block's warps join
-    st = warp_join(st);
+    st = warp_join(Stat{st.m, s2.x + s2.y, w2.x + w2.y});
     if (lane == 0) s_stat[warp] = st;
     auto join_lists = [&]() {  // list of all warps -> s_list[0]
       if constexpr (TOP) {
