@@ -326,7 +326,7 @@ def oneshot_staged(sendbufs: Sequence, recvbufs: Sequence, workspace: OneShotWor
 # A per-rank argument is a sequence of nranks alike tensors, or one tensor whose
 # first dimension is the rank.
 
-OP_WORKSPACE_MIN_BYTES = 20480
+OP_WORKSPACE_MIN_BYTES = 36864
 
 
 class OpWorkspace:

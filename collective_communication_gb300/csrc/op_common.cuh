@@ -16,11 +16,11 @@ namespace rar {
 
 // Workspace of the operators (device memory owned by the caller):
 //   [0, 4096)        OpHeader (the status word where the ring header has it)
-//   [4096, 20480)    arrival counters, zero between calls: a block that arrives
-//                    last at a join sets its counter back to zero
-//   [20480, ...)     scratch of the call (partial results); nothing is kept
+//   [4096, 36864)    arrival counters, zero between calls: the block or warp that
+//                    arrives last at a join sets its counter back to zero
+//   [36864, ...)     scratch of the call (partial results); nothing is kept
 constexpr uint32_t kOpMagic = 0x31504f52u;  // "ROP1"
-constexpr int kOpCounters = 4096;
+constexpr int kOpCounters = 8192;
 constexpr int64_t kOpScratchOffset = kHeaderBytes + 4 * (int64_t)kOpCounters;
 
 struct OpHeader {
@@ -184,6 +184,9 @@ struct LogprobArgs {
   int32_t* top_ids;
   char* ws;
   int rows, nranks, dtype, top;
+  // set by the launcher: tiles before each shard's in a row, warps with work, tiles of each, and how many have one more
+  int first_tile[kMaxRanks + 1];
+  uint32_t workers, each, more;
 };
 
 struct LogprobBwdArgs {

@@ -9,18 +9,19 @@
 // than 8 above it (sums to 2^12 times larger lose nothing in binary32); sums
 // with their own m join exactly as partial softmaxes do.
 //
-// The bytes of the logits bound it; about 8 instructions a word leave room for
-// twice the words that memory delivers. Tiles of 2048 columns of all rows are
-// cut into one equal range per resident block, so few rows use all SMs and many
-// rows leave none idle; a row that a cut divides is joined by the block that
-// arrives last at it.
+// The bytes of the logits bound it; instructions come close, so they are
+// counted: about 7 a word, packed binary32 operations where there are any.
+// Tiles of 1024 columns of all rows are cut into one equal range per resident
+// warp, so few rows use all SMs and many rows leave none idle, and no warp
+// waits for another (blocks that joined their warps' results at the end of
+// every row spent a fifth of the time at barriers). A row that a cut divides is
+// joined by the warp that arrives last at it.
 //
-// Alternatives. Value and index make one 64-bit key. Each warp holds its 32
-// best keys sorted over its lanes and a bound below which nothing can matter.
-// The first words' bound is the top-th largest of the threads' own maxima; it
-// is renewed from all warps' lists whenever the words read have doubled. A word
-// at or above the bound is rare then (about top / (words read) of them), and is
-// read again and inserted where it belongs.
+// Alternatives. Value and index make one 64-bit key. A warp holds its 32 best
+// keys sorted over its lanes and a bound below which nothing can matter: first
+// the top-th largest of the lanes' own maxima, then the list's top-th key. A
+// word at or above the bound is rare after the first tile (about top / (words
+// read) of them), and is read again and inserted where it belongs.
 #include <cstdio>
 
 #include "op_common.cuh"
@@ -30,11 +31,10 @@ namespace rar {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpTile = kLpThreads * 8;   // columns of a tile
-constexpr int kLpBytesAhead = 64;          // bytes a thread has in flight
-constexpr int kLpMaxBlocks = 1216;        // most blocks of a forward launch: a partial result and a counter each
+constexpr int kLpTile = 1024;             // columns of a tile
+constexpr int kLpMaxWorkers = 4864;       // most warps of a forward launch: a counter and two partial results each
 constexpr int kLpPartFloats = 4 + 2 * 32;  // m, s, w, then 32 keys
-static_assert(kLpMaxBlocks <= kOpCounters, "one arrival counter per block");
+static_assert(kLpMaxWorkers <= kOpCounters, "one arrival counter per warp");
 
 namespace {
 
@@ -96,18 +96,17 @@ __device__ __forceinline__ Stat warp_join(Stat a) {
   return a;
 }
 
-// ---- 32 keys sorted over the lanes of a warp, largest in lane 0 ----
+// ---- 32 keys, or values without NaN, sorted over the lanes of a warp, largest in lane 0 ----
 __device__ __forceinline__ uint64_t exchange(uint64_t k, int d, bool keep_large) {
   const uint64_t o = __shfl_xor_sync(~0u, k, d);
   return (k > o) == keep_large ? k : o;
 }
-__device__ __forceinline__ uint64_t merge_bitonic(uint64_t k) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) k = exchange(k, d, (lane & d) == 0);
-  return k;
+__device__ __forceinline__ float exchange(float k, int d, bool keep_large) {
+  const float o = __shfl_xor_sync(~0u, k, d);
+  return keep_large ? fmaxf(k, o) : fminf(k, o);
 }
-__device__ __forceinline__ uint64_t sort32(uint64_t k) {
+template <typename K>
+__device__ __forceinline__ K sort32(K k) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int size = 2; size <= 32; size <<= 1)
@@ -115,12 +114,6 @@ __device__ __forceinline__ uint64_t sort32(uint64_t k) {
     for (int d = size >> 1; d > 0; d >>= 1) k = exchange(k, d, ((lane & d) == 0) == ((lane & size) == 0 || size == 32));
   return k;
 }
-// The 32 best of two sorted lists, sorted.
-__device__ __forceinline__ uint64_t merge32(uint64_t a, uint64_t b) {
-  const uint64_t o = __shfl_sync(~0u, b, 31 - (threadIdx.x & 31));
-  return merge_bitonic(a > o ? a : o);
-}
-
 // The list with one more key, without its last.
 __device__ __forceinline__ uint64_t insert32(uint64_t list, uint64_t key) {
   const int lane = threadIdx.x & 31, at = __popc(__ballot_sync(~0u, list > key));
@@ -164,235 +157,203 @@ __device__ __forceinline__ float largest(const Pack8<float>& u) {
 
 }  // namespace
 
+// A warp's alternatives.
+struct TopList {
+  uint64_t list = 0, bound = 0;  // sorted over the lanes; keys not above the bound cannot be among the top
+  float bound_value = -INFINITY;  // value of the bound, for quick tests: !(value < bound_value) lets a NaN in
+
+  // Every lane's key, 0 for none: those above the bound are inserted one after another.
+  __device__ __forceinline__ void offer(uint64_t key, int top) {
+    uint32_t votes = __ballot_sync(~0u, key > bound);
+    while (votes != 0) {
+      const int src = __ffs(votes) - 1;
+      list = insert32(list, __shfl_sync(~0u, key, src));
+      const uint64_t last = __shfl_sync(~0u, list, top - 1);
+      bound = last > bound ? last : bound;
+      votes = __ballot_sync(~0u, key > bound) & (~0u << src) << 1;
+    }
+    bound_value = bound == 0 ? -INFINITY : key_value(bound);
+  }
+  // `value` is in the top-th place of some values: no key of a smaller value matters.
+  __device__ __forceinline__ void start(float value) {
+    bound_value = value;
+    if (value != -INFINITY) bound = ((uint64_t)ordered(value) << 32) - 1;
+  }
+};
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-  __shared__ Stat s_stat[kLpWarps];
-  __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];
-  __shared__ uint64_t s_bound;
-  __shared__ int s_tiles[kMaxRanks + 1];
-  __shared__ bool s_last;
   if (!op_workspace_ok(a.ws)) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    int n = 0;
-    for (int r = 0; r < a.nranks; r++) {
-      s_tiles[r] = n;
-      n += (int)((a.first[r + 1] - a.first[r] + kLpTile - 1) / kLpTile);
-    }
-    s_tiles[a.nranks] = n;
-  }
-  __syncthreads();
-  const int per_row = s_tiles[a.nranks];
-  const int64_t total = (int64_t)a.rows * per_row;
-  const int64_t blocks = total < gridDim.x ? total : gridDim.x;
-  if (blockIdx.x >= blocks) return;
-  auto start_of = [&](int64_t block) { return block * total / blocks; };
-  auto block_of = [&](int64_t tile) { return ((tile + 1) * blocks - 1) / total; };
-  const int64_t end = start_of(blockIdx.x + 1);
+  const int lane = threadIdx.x & 31;
+  // neighbouring ranges go to different blocks, so that few workers still spread over the SMs
+  const uint32_t worker = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  if (worker >= a.workers) return;
+  // worker w's tiles start at w * each + min(w, more)
+  auto start_of = [&](uint32_t w) { return w * a.each + min(w, a.more); };
+  auto worker_of = [&](uint32_t tile) {
+    const uint32_t split = a.more * (a.each + 1);
+    return tile < split ? tile / (a.each + 1) : a.more + (tile - split) / a.each;
+  };
+  const uint32_t per_row = a.first_tile[a.nranks];
+  const uint32_t end = start_of(worker + 1);
 
-  for (int64_t at = start_of(blockIdx.x); at < end;) {
-    const int row = (int)(at / per_row);
-    const int64_t row_first = (int64_t)row * per_row;
-    const int t0 = (int)(at - row_first), t1 = (int)(end - row_first < per_row ? end - row_first : per_row);
-    Stat st = {-INFINITY, 0.f, 0.f};
-    float2 s2 = make_float2(0.f, 0.f), w2 = s2;  // st.s and st.w in two halves, added at the end
-    uint64_t list = 0, bound = 0;  // sorted over the lanes; keys not above the bound cannot be among the top
-    float bound_value = 0.f;       // value of the bound, for the quick test
-    auto add = [&](const Pack8<T>& u, float pm) {
-      if (pm > st.m + 8.f) {
-        if (st.m != -INFINITY) {
-          const float d = (st.m - pm) * kLog2e, e = exp2_fast(d);
-          w2 = e > 0.f ? make_float2(e * (w2.x + d * s2.x), e * (w2.y + d * s2.y)) : make_float2(0.f, 0.f);
-          s2 = make_float2(s2.x * e, s2.y * e);
-        }
-        st.m = pm;
-      }
-      const float m = st.m == -INFINITY ? 0.f : st.m;
-      float v[8];
-      u.widen(v);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        float2 t = mul2(add2(make_float2(v[j], v[j + 1]), make_float2(-m, -m)), make_float2(kLog2e, kLog2e));
-        t = make_float2(max_nan(t.x, kFloorT), max_nan(t.y, kFloorT));
-        const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
-        s2 = add2(s2, e);
-        w2 = fma2(e, t, w2);
-      }
-    };
-    // The top-th key of the warps' sorted keys together, for all threads; every thread of the block calls it.
-    auto block_bound = [&](uint64_t k) {
-#pragma unroll
-      for (int d = kLpWarps / 2; d > 0; d >>= 1) {
-        if (warp >= d && warp < 2 * d) s_list[warp][lane] = k;
-        __syncthreads();
-        if (warp < d) k = merge32(k, s_list[warp + d][lane]);
-      }
-      if (warp == 0 && lane == a.top - 1) s_bound = k;
-      __syncthreads();
-      return s_bound;
-    };
-    // Words that may be among the top: bit b of a lane's mask is word[8 kLpThreads (b / 8) + b % 8].
-    auto consider = [&](const T* word, uint32_t index, uint32_t mask) {
-      while (__any_sync(~0u, mask != 0)) {
-        uint64_t key = 0;
-        if (mask != 0) {
-          const int bit = __ffs(mask) - 1, off = (bit >> 3) * (kLpThreads * 8) + (bit & 7);
-          key = top_key(to_float(word[off]), index + off);
-          mask &= mask - 1;
-        }
-        uint32_t votes = __ballot_sync(~0u, key > bound);
-        while (votes != 0) {
-          const int src = __ffs(votes) - 1;
-          list = insert32(list, __shfl_sync(~0u, key, src));
-          const uint64_t last = __shfl_sync(~0u, list, a.top - 1);
-          bound = last > bound ? last : bound;
-          votes = __ballot_sync(~0u, key > bound) & (~0u << src) << 1;
-        }
-      }
-      bound_value = bound == 0 ? -INFINITY : key_value(bound);
-    };
+  for (uint32_t at = start_of(worker); at < end;) {
+    const uint32_t row = at / per_row, row_first = row * per_row;
+    const int t0 = (int)(at - row_first), t1 = (int)(min(end, row_first + per_row) - row_first);
+    float m = -INFINITY;                           // near the largest of the lane's words
+    float2 s2 = make_float2(0.f, 0.f), w2 = s2;  // its sums in two halves
+    TopList tops;
 
-    constexpr int kAhead = kLpBytesAhead / (8 * (int)sizeof(T));
-    int round = 0;  // of kAhead packs a thread
-    const bool alone = t1 - t0 <= kAhead;  // one round has all words: a bound of the warp will do
     for (int t = t0; t < t1;) {
+      // the part's words of one shard
       int rank = 0;
-      while (t >= s_tiles[rank + 1]) rank++;
-      const int ts = t - s_tiles[rank], te = min(t1, s_tiles[rank + 1]) - s_tiles[rank];
+      while (t >= a.first_tile[rank + 1]) rank++;
+      const int ts = t - a.first_tile[rank], te = min(t1, a.first_tile[rank + 1]) - a.first_tile[rank];
       const int64_t width = a.first[rank + 1] - a.first[rank];
       const int64_t c0 = (int64_t)ts * kLpTile, c1 = imin((int64_t)te * kLpTile, width);
       const T* x = reinterpret_cast<const T*>(a.logits[rank]) + (int64_t)row * a.row_stride[rank] + c0;
       const int n = (int)(c1 - c0);
-      const uint32_t word = (uint32_t)(a.first[rank] + c0);
-      // words before the first and after the last 16-byte boundary go one to a lane
+      const bool begins = t == t0;
+      t = te + a.first_tile[rank];
+      // up to the first and from the last 16-byte boundary one by one, 16-byte packs between
       const int head = min(n, (int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T));
       const int packs = (n - head) / 8, tail = n - head - packs * 8;
       const T* body = x + head;
-      // a thread's packs are kLpThreads apart
-      for (int p = tid; p - tid < packs; p += kLpThreads * kAhead) {
+      const uint32_t word = (uint32_t)(a.first[rank] + c0) + head;
+
+      // a round is kAhead packs a lane, 32 apart
+      constexpr int kAhead = 64 / (8 * (int)sizeof(T));
+      for (int p = lane; p - lane < packs; p += 32 * kAhead) {
         Pack8<T> u[kAhead];
-        float best = -INFINITY;
+        if (p - lane + 32 * kAhead <= packs) {
 #pragma unroll
-        for (int i = 0; i < kAhead; i++) {
-          if (p + i * kLpThreads < packs) u[i].load_stream(body + (int64_t)(p + i * kLpThreads) * 8);
-          else u[i].absent();
+          for (int i = 0; i < kAhead; i++) u[i].load_stream(body + (int64_t)(p + i * 32) * 8);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kAhead; i++) {
+            if (p + i * 32 < packs) u[i].load_stream(body + (int64_t)(p + i * 32) * 8);
+            else u[i].absent();
+          }
         }
+        float best = largest(u[0]);
+#pragma unroll
+        for (int i = 1; i < kAhead; i++) best = fmaxf(best, largest(u[i]));
+        if (best > m + 8.f) {
+          if (m != -INFINITY) {
+            const float d = (m - best) * kLog2e, e = exp2_fast(d);
+            w2 = e > 0.f ? make_float2(e * (w2.x + d * s2.x), e * (w2.y + d * s2.y)) : make_float2(0.f, 0.f);
+            s2 = make_float2(s2.x * e, s2.y * e);
+          }
+          m = best;
+        }
+        const float2 off = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
-          const float pm = largest(u[i]);
-          best = fmaxf(best, pm);
-          add(u[i], pm);
+          float v[8];
+          u[i].widen(v);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            float2 t2 = mul2(add2(make_float2(v[j], v[j + 1]), off), make_float2(kLog2e, kLog2e));
+            t2 = make_float2(max_nan(t2.x, kFloorT), max_nan(t2.y, kFloorT));
+            const float2 e = make_float2(exp2_fast(t2.x), exp2_fast(t2.y));
+            s2 = add2(s2, e);
+            w2 = fma2(e, t2, w2);
+          }
         }
         if constexpr (TOP) {
-          if (round == 0) {
-            const uint64_t k = sort32(best == -INFINITY ? 0 : (uint64_t)ordered(best) << 32);
-            const uint64_t b = alone ? __shfl_sync(~0u, k, a.top - 1) : block_bound(k);
-            if (b > bound) bound = b - 1;
-            bound_value = b == 0 ? -INFINITY : key_value(b);
-          } else if ((round & (round - 1)) == 0) {
-            const uint64_t b = block_bound(list);
-            if (b > bound) {
-              bound = b;
-              bound_value = key_value(b);
-            }
-          }
-          round++;
-          // a NaN, which the maxima leave out, shows in the sum; !(<) lets it, and all words under a NaN bound, in
-          const bool nan = s2.x != s2.x || s2.y != s2.y;
-          if (__any_sync(~0u, !(best < bound_value) || nan)) {
+          if (begins && p == lane) tops.start(__shfl_sync(~0u, sort32(best), a.top - 1));
+          const bool nan = s2.x != s2.x || s2.y != s2.y;  // which the maxima leave out
+          if (__any_sync(~0u, !(best < tops.bound_value) || nan)) {
             uint32_t mask = 0;
 #pragma unroll
             for (int i = 0; i < kAhead; i++) {
-              const bool in = p + i * kLpThreads < packs && (!(largest(u[i]) < bound_value) || nan);
+              const bool in = p + i * 32 < packs && (!(largest(u[i]) < tops.bound_value) || nan);
               if (__any_sync(~0u, in)) {
                 float v[8];
                 u[i].widen(v);
 #pragma unroll
-                for (int j = 0; j < 8; j++) mask |= in && !(v[j] < bound_value) ? 1u << (8 * i + j) : 0u;
+                for (int j = 0; j < 8; j++) mask |= in && !(v[j] < tops.bound_value) ? 1u << (8 * i + j) : 0u;
               }
             }
-            consider(body + (int64_t)p * 8, word + head + p * 8, mask);
+            while (__any_sync(~0u, mask != 0)) {
+              uint64_t key = 0;
+              if (mask != 0) {
+                const int bit = __ffs(mask) - 1, e = (p + (bit >> 3) * 32) * 8 + (bit & 7);
+                key = top_key(to_float(body[e]), word + e);
+                mask &= mask - 1;
+              }
+              tops.offer(key, a.top);
+            }
           }
         }
       }
-      if (head + tail > 0 && warp == 0) {
-        const int e = lane < head ? lane : lane - head < tail ? head + packs * 8 + lane - head : -1;
-        const float v = e >= 0 ? to_float(x[e]) : -INFINITY;
+      if (head + tail > 0) {
+        const bool mine = lane < head + tail;
+        const int e = lane < head ? lane - head : packs * 8 + lane - head;
+        const float v = mine ? to_float(body[e]) : -INFINITY;
         Stat one = {v, v == -INFINITY ? 0.f : 1.f, 0.f};
         if (v != v) one = {-INFINITY, v, 0.f};
-        st = join(Stat{st.m, s2.x + s2.y, w2.x + w2.y}, one);
-        s2 = make_float2(st.s, 0.f);
-        w2 = make_float2(st.w, 0.f);
-        if constexpr (TOP) {
-          if (round == 0) bound_value = -INFINITY;
-          consider(x + e, word + e, e >= 0 && !(v < bound_value) ? 1u : 0u);
-        }
+        one = join(Stat{m, s2.x + s2.y, w2.x + w2.y}, one);
+        m = one.m;
+        s2 = make_float2(one.s, 0.f);
+        w2 = make_float2(one.w, 0.f);
+        if constexpr (TOP) tops.offer(mine ? top_key(v, word + e) : 0, a.top);
       }
-      t = te + s_tiles[rank];
     }
+    Stat st = warp_join(Stat{m, s2.x + s2.y, w2.x + w2.y});
 
-    // the block's warps join
-    st = warp_join(Stat{st.m, s2.x + s2.y, w2.x + w2.y});
-    if (lane == 0) s_stat[warp] = st;
-    auto join_lists = [&]() {  // list of all warps -> s_list[0]
-      if constexpr (TOP) {
-#pragma unroll
-        for (int d = kLpWarps / 2; d > 0; d >>= 1) {
-          if (warp >= d && warp < 2 * d) s_list[warp][lane] = list;
-          __syncthreads();
-          if (warp < d) list = merge32(list, s_list[warp + d][lane]);
-        }
-      }
-    };
-    join_lists();
-    __syncthreads();
-    if (warp == 0) st = warp_join(lane < kLpWarps ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f});
-
-    bool mine = true;  // this block has the whole row's result
-    if (t0 != 0 || t1 != per_row) {
-      const int cf = (int)block_of(row_first), cl = (int)block_of(row_first + per_row - 1);
+    bool whole = t0 == 0 && t1 == (int)per_row;  // this warp has the row's result
+    if (!whole) {
+      const uint32_t wf = worker_of(row_first), wl = worker_of(row_first + per_row - 1);
+      const bool starts_at_wf = start_of(wf) == row_first;
       float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset);
-      const bool starts_at_cf = start_of(cf) == row_first;
-      auto part_of = [&](int block) {  // of its first row, or of the row that starts in it and goes on
-        return parts + (2 * block + (block == cf && !starts_at_cf)) * kLpPartFloats;
+      auto part_of = [&](uint32_t w) {  // of its first row, or of the row that starts in it and goes on
+        return parts + (2 * w + (w == wf && !starts_at_wf)) * kLpPartFloats;
       };
-      if (warp == 0) {
-        float* part = part_of(blockIdx.x);
-        if (lane == 0) {
-          part[0] = st.m;
-          part[1] = st.s;
-          part[2] = st.w;
-        }
-        if (TOP) reinterpret_cast<uint64_t*>(part + 4)[lane] = list;
-        __threadfence();
+      float* part = part_of(worker);
+      if (lane == 0) {
+        part[0] = st.m;
+        part[1] = st.s;
+        part[2] = st.w;
       }
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t* counter = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes) + cf;
-        s_last = atomicAdd(counter, 1u) == (uint32_t)(cl - cf);
-        if (s_last) *counter = 0;
+      if (TOP && lane < a.top) reinterpret_cast<uint64_t*>(part + 4)[lane] = tops.list;
+      __threadfence();
+      __syncwarp();
+      uint32_t arrived = 0;
+      if (lane == 0) {
+        uint32_t* counter = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes) + wf;
+        arrived = atomicAdd(counter, 1u);
+        if (arrived == wl - wf) *counter = 0;
       }
-      __syncthreads();
-      mine = s_last;
-      if (mine) {
+      whole = __shfl_sync(~0u, arrived, 0) == wl - wf;
+      if (whole) {
         __threadfence();
+        // in the workers' order, whoever joins: a lane's share first, then over the lanes
         st = {-INFINITY, 0.f, 0.f};
-        list = 0;
-        for (int p = cf + tid; p <= cl; p += kLpThreads) {
-          const float* part = part_of(p);
-          st = join(st, Stat{__ldcg(part), __ldcg(part + 1), __ldcg(part + 2)});
+        float head = -INFINITY;  // largest of the lane's parts' first alternatives
+        for (uint32_t w = wf + lane; w <= wl; w += 32) {
+          const float* q = part_of(w);
+          st = join(st, Stat{__ldcg(q), __ldcg(q + 1), __ldcg(q + 2)});
+          if (TOP) {
+            const uint64_t k = __ldcg(reinterpret_cast<const unsigned long long*>(q + 4));
+            if (k != 0) head = fmaxf(head, key_value(k));
+          }
         }
-        if (TOP)
-          for (int p = cf + warp; p <= cl; p += kLpWarps)
-            list = merge32(list, __ldcg(reinterpret_cast<const unsigned long long*>(part_of(p) + 4) + lane));
         st = warp_join(st);
-        if (lane == 0) s_stat[warp] = st;
-        join_lists();
-        __syncthreads();
-        if (warp == 0) st = warp_join(lane < kLpWarps ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f});
+        if constexpr (TOP) {
+          tops = TopList();
+          tops.start(__shfl_sync(~0u, sort32(head), a.top - 1));
+          const int keys = (int)(wl - wf + 1) * a.top;
+          for (int i = lane; i - lane < keys; i += 32) {
+            uint64_t key = 0;
+            if (i < keys)
+              key = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(wf + i / a.top) + 4) + i % a.top);
+            tops.offer(key, a.top);
+          }
+        }
       }
     }
-    if (mine && warp == 0) {
+    if (whole) {
       if (st.m == INFINITY) st.s = NAN;  // exp(inf - inf)
       const float log2_s = log2f(st.s), lse = st.m + kLn2 * log2_s;
       if (lane == 0) {
@@ -406,8 +367,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         a.lse[row] = lse;
       }
       if (TOP && lane < a.top) {
-        a.top_values[(int64_t)row * a.top + lane] = key_value(list) - lse;
-        a.top_ids[(int64_t)row * a.top + lane] = key_index(list);
+        a.top_values[(int64_t)row * a.top + lane] = key_value(tops.list) - lse;
+        a.top_ids[(int64_t)row * a.top + lane] = key_index(tops.list);
       }
     }
     at = row_first + t1;
@@ -446,7 +407,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __
   const bool together = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;
   const int head = together ? min(n, (int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T)) : n;
   const int packs = (n - head) / 8, done = head + packs * 8;
-  constexpr int kAhead = kLpBytesAhead / (8 * (int)sizeof(T));
+  constexpr int kAhead = 64 / (8 * (int)sizeof(T));
   for (int p0 = 0; p0 < packs; p0 += kLpThreads * kAhead) {
     Pack8<T> u[kAhead];
 #pragma unroll
@@ -478,9 +439,10 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __
   }
 }
 
-int64_t token_logprobs_scratch_bytes(int, int) { return 2ll * kLpMaxBlocks * kLpPartFloats * (int64_t)sizeof(float); }
+int64_t token_logprobs_scratch_bytes(int, int) { return 2ll * kLpMaxWorkers * kLpPartFloats * (int64_t)sizeof(float); }
 
-cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
+cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) {
+  LogprobArgs a = args;
   const void* fn = a.dtype == kF32 ? (a.top > 0 ? (const void*)token_logprobs_kernel<float, true>
                                                 : (const void*)token_logprobs_kernel<float, false>)
                                    : (a.top > 0 ? (const void*)token_logprobs_kernel<uint16_t, true>
@@ -490,13 +452,19 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kLpThreads, 0);
   if (e != cudaSuccess) return e;
-  int64_t tiles = 0;
-  for (int r = 0; r < a.nranks; r++) tiles += div_up(a.first[r + 1] - a.first[r], kLpTile);
-  const int64_t grid = imin(imin((int64_t)sms * per_sm, kLpMaxBlocks), tiles * a.rows);
+  for (int r = 0; r < a.nranks; r++)
+    a.first_tile[r + 1] = a.first_tile[r] + (int)div_up(a.first[r + 1] - a.first[r], kLpTile);
+  const int64_t tiles = (int64_t)a.rows * a.first_tile[a.nranks];
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  int64_t grid = imin((int64_t)sms * per_sm, kLpMaxWorkers / kLpWarps);
+  a.workers = (uint32_t)imin(grid * kLpWarps, tiles);
+  a.each = (uint32_t)(tiles / a.workers);
+  a.more = (uint32_t)(tiles % a.workers);
+  grid = imin(grid, a.workers);
   if (trace_on())
-    std::fprintf(stderr, "rar trace: token_logprobs nranks=%d rows=%d vocab=%lld top=%d grid=%lld\n", a.nranks, a.rows,
-                 (long long)a.first[a.nranks], a.top, (long long)grid);
-  void* params[] = {const_cast<LogprobArgs*>(&a)};
+    std::fprintf(stderr, "rar trace: token_logprobs nranks=%d rows=%d vocab=%lld top=%d grid=%lld workers=%u\n", a.nranks,
+                 a.rows, (long long)a.first[a.nranks], a.top, (long long)grid, a.workers);
+  void* params[] = {&a};
   return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kLpThreads), params, 0, stream);
 }
 

@@ -425,7 +425,7 @@ RAR_API rar_status rar_describe_geometry(int nranks, size_t count, rar_dtype dty
  * serves any of these operators, at any sizes it has room for, in any order on
  * one stream; nothing carries over from call to call.
  */
-#define RAR_OP_WORKSPACE_MIN_BYTES 20480
+#define RAR_OP_WORKSPACE_MIN_BYTES 36864
 RAR_API rar_status rar_op_workspace_init(void* workspace, size_t workspaceBytes, void* stream);
 
 /*

@@ -73,7 +73,7 @@ def test_norm_rope_refusals(lib, form):
            dict(max_pos=0), dict(wq=0), dict(wk=0), dict(cs=0), dict(pos=0), dict(qkv=None), dict(stride=632)]
     if form == "backward":
         bad += [dict(dq=None), dict(dx=ranks(1)), dict(dx=ranks(7)), dict(dwq=ranks(12)), dict(dvs=56), dict(dxs=632)]
-        assert rope(lib, form, bytes=20480) == S.ERR_WORKSPACE
+        assert rope(lib, form, bytes=B.OP_WORKSPACE_MIN_BYTES) == S.ERR_WORKSPACE
         assert rope(lib, form, dxs=644) == S.ERR_ALIGN
     else:
         bad += [dict(out=None), dict(outs=504), dict(out=ranks(1)), dict(k=ranks(1)), dict(k=ranks(7)),
