@@ -96,17 +96,12 @@ __device__ __forceinline__ Stat warp_join(Stat a) {
   return a;
 }
 
-// ---- 32 keys, or values without NaN, sorted over the lanes of a warp, largest in lane 0 ----
-__device__ __forceinline__ uint64_t exchange(uint64_t k, int d, bool keep_large) {
-  const uint64_t o = __shfl_xor_sync(~0u, k, d);
-  return (k > o) == keep_large ? k : o;
-}
+// 32 values without NaN sorted over the lanes of a warp, largest in lane 0.
 __device__ __forceinline__ float exchange(float k, int d, bool keep_large) {
   const float o = __shfl_xor_sync(~0u, k, d);
   return keep_large ? fmaxf(k, o) : fminf(k, o);
 }
-template <typename K>
-__device__ __forceinline__ K sort32(K k) {
+__device__ __forceinline__ float sort32(float k) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int size = 2; size <= 32; size <<= 1)
@@ -114,7 +109,7 @@ __device__ __forceinline__ K sort32(K k) {
     for (int d = size >> 1; d > 0; d >>= 1) k = exchange(k, d, ((lane & d) == 0) == ((lane & size) == 0 || size == 32));
   return k;
 }
-// The list with one more key, without its last.
+// 32 keys sorted over the lanes, largest in lane 0: with one more, without the last.
 __device__ __forceinline__ uint64_t insert32(uint64_t list, uint64_t key) {
   const int lane = threadIdx.x & 31, at = __popc(__ballot_sync(~0u, list > key));
   const uint64_t up = __shfl_up_sync(~0u, list, 1);
@@ -165,13 +160,10 @@ struct TopList {
   // Every lane's key, 0 for none: those above the bound are inserted one after another.
   __device__ __forceinline__ void offer(uint64_t key, int top) {
     uint32_t votes = __ballot_sync(~0u, key > bound);
-    while (votes != 0) {
-      const int src = __ffs(votes) - 1;
-      list = insert32(list, __shfl_sync(~0u, key, src));
-      const uint64_t last = __shfl_sync(~0u, list, top - 1);
-      bound = last > bound ? last : bound;
-      votes = __ballot_sync(~0u, key > bound) & (~0u << src) << 1;
-    }
+    if (votes == 0) return;
+    for (; votes != 0; votes &= votes - 1) list = insert32(list, __shfl_sync(~0u, key, __ffs(votes) - 1));
+    const uint64_t last = __shfl_sync(~0u, list, top - 1);
+    bound = last > bound ? last : bound;
     bound_value = bound == 0 ? -INFINITY : key_value(bound);
   }
   // `value` is in the top-th place of some values: no key of a smaller value matters.
@@ -183,6 +175,8 @@ struct TopList {
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+  constexpr int kAhead = 64 / (8 * (int)sizeof(T));  // packs of a lane in flight
+  __shared__ __align__(16) T s_words[TOP ? kLpWarps : 1][kAhead][32][8];
   if (!op_workspace_ok(a.ws)) return;
   const int lane = threadIdx.x & 31;
   // neighbouring ranges go to different blocks, so that few workers still spread over the SMs
@@ -222,7 +216,6 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
       const uint32_t word = (uint32_t)(a.first[rank] + c0) + head;
 
       // a round is kAhead packs a lane, 32 apart
-      constexpr int kAhead = 64 / (8 * (int)sizeof(T));
       for (int p = lane; p - lane < packs; p += 32 * kAhead) {
         Pack8<T> u[kAhead];
         if (p - lane + 32 * kAhead <= packs) {
@@ -262,28 +255,21 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         }
         if constexpr (TOP) {
           if (begins && p == lane) tops.start(__shfl_sync(~0u, sort32(best), a.top - 1));
-          const bool nan = s2.x != s2.x || s2.y != s2.y;  // which the maxima leave out
-          if (__any_sync(~0u, !(best < tops.bound_value) || nan)) {
-            uint32_t mask = 0;
+          // lanes with a word that may matter (a NaN, which the maxima leave out, shows in the sum): the warp looks at
+          // their words together, a word to a lane
+          uint32_t lanes = __ballot_sync(~0u, !(best < tops.bound_value) || s2.x != s2.x || s2.y != s2.y);
+          if (lanes != 0) {
+            T(*words)[32][8] = s_words[threadIdx.x >> 5];
 #pragma unroll
-            for (int i = 0; i < kAhead; i++) {
-              const bool in = p + i * 32 < packs && (!(largest(u[i]) < tops.bound_value) || nan);
-              if (__any_sync(~0u, in)) {
-                float v[8];
-                u[i].widen(v);
-#pragma unroll
-                for (int j = 0; j < 8; j++) mask |= in && !(v[j] < tops.bound_value) ? 1u << (8 * i + j) : 0u;
-              }
+            for (int i = 0; i < kAhead; i++) u[i].store(words[i][lane]);
+            __syncwarp();
+            for (; lanes != 0; lanes &= lanes - 1) {
+              const int l = __ffs(lanes) - 1, pack = p - lane + l + (lane >> 3) * 32;
+              const bool there = lane < 8 * kAhead && pack < packs;
+              const int i = there ? lane >> 3 : 0;
+              tops.offer(there ? top_key(to_float(words[i][l][lane & 7]), word + pack * 8 + (lane & 7)) : 0, a.top);
             }
-            while (__any_sync(~0u, mask != 0)) {
-              uint64_t key = 0;
-              if (mask != 0) {
-                const int bit = __ffs(mask) - 1, e = (p + (bit >> 3) * 32) * 8 + (bit & 7);
-                key = top_key(to_float(body[e]), word + e);
-                mask &= mask - 1;
-              }
-              tops.offer(key, a.top);
-            }
+            __syncwarp();
           }
         }
       }
@@ -331,12 +317,23 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         // in the workers' order, whoever joins: a lane's share first, then over the lanes
         st = {-INFINITY, 0.f, 0.f};
         float head = -INFINITY;  // largest of the lane's parts' first alternatives
-        for (uint32_t w = wf + lane; w <= wl; w += 32) {
-          const float* q = part_of(w);
-          st = join(st, Stat{__ldcg(q), __ldcg(q + 1), __ldcg(q + 2)});
-          if (TOP) {
-            const uint64_t k = __ldcg(reinterpret_cast<const unsigned long long*>(q + 4));
-            if (k != 0) head = fmaxf(head, key_value(k));
+        for (uint32_t w0 = wf + lane; w0 <= wl; w0 += 32 * 4) {
+          Stat q[4];
+          uint64_t k[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            q[j] = {-INFINITY, 0.f, 0.f};
+            k[j] = 0;
+            if (w0 + 32 * j <= wl) {
+              const float* from = part_of(w0 + 32 * j);
+              q[j] = {__ldcg(from), __ldcg(from + 1), __ldcg(from + 2)};
+              if (TOP) k[j] = __ldcg(reinterpret_cast<const unsigned long long*>(from + 4));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            st = join(st, q[j]);
+            if (TOP && k[j] != 0) head = fmaxf(head, key_value(k[j]));
           }
         }
         st = warp_join(st);
@@ -344,11 +341,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
           tops = TopList();
           tops.start(__shfl_sync(~0u, sort32(head), a.top - 1));
           const int keys = (int)(wl - wf + 1) * a.top;
-          for (int i = lane; i - lane < keys; i += 32) {
-            uint64_t key = 0;
-            if (i < keys)
-              key = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(wf + i / a.top) + 4) + i % a.top);
-            tops.offer(key, a.top);
+          for (int i0 = lane; i0 - lane < keys; i0 += 32 * 8) {
+            uint64_t key[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              const int i = i0 + 32 * j;
+              key[j] = 0;
+              if (i < keys)
+                key[j] = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(wf + i / a.top) + 4) + i % a.top);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++) tops.offer(key[j], a.top);
           }
         }
       }
