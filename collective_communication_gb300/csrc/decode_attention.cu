@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
   const int D = a.head_dim;
   const int longest = a.max_blocks << a.page_shift;
   bool bad = false;
+  const uint32_t magic = op_magic(a.ws);
 
   // Tiles of all requests: a segment of requests per thread, then a scan.
   auto length = [&](int b) {
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
       if (n < 0 || n > longest) bad = true;
       mine += tiles_of(length(b));
     }
-    if (!op_workspace_ok(a.ws)) return;
+    if (!op_ready(a.ws, magic)) return;
     int64_t scan = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {

@@ -34,9 +34,16 @@ constexpr uint32_t kErrCapacity = 10;  // mirrors RAR_ERR_CAPACITY
 __device__ __forceinline__ void op_report(char* ws, uint32_t code) {
   atomicCAS(&reinterpret_cast<OpHeader*>(ws)->status, 0u, code);
 }
+// The header's magic number. Kernels ask for it first, and test it before their
+// first store: the load then overlaps those of the inputs.
+__device__ __forceinline__ uint32_t op_magic(char* ws) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(&reinterpret_cast<OpHeader*>(ws)->magic));
+  return v;
+}
 // True if the workspace was initialised; else the status word says so.
-__device__ __forceinline__ bool op_workspace_ok(char* ws) {
-  if (reinterpret_cast<volatile OpHeader*>(ws)->magic == kOpMagic) return true;
+__device__ __forceinline__ bool op_ready(char* ws, uint32_t magic) {
+  if (magic == kOpMagic) return true;
   if (threadIdx.x == 0) op_report(ws, kErrWorkspace);
   return false;
 }
@@ -47,6 +54,29 @@ __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%6, %7};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
 }
 
 // Eight consecutive elements of a row, widened to binary32 (T: float or
@@ -156,7 +186,6 @@ struct NormRopeBwdArgs {
   float eps;
   int tokens, nranks, dtype, q_heads, kv_heads, head_dim, rot, max_pos, interleaved;
 };
-constexpr int kNormRopeBwdBlocks = 1216;  // most blocks of a backward launch, all ranks together
 
 struct DecodeArgs {
   const void* q[kMaxRanks];

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const __grid_co
   __shared__ int32_t s_start[kPtChunk];  // first token of the request, relative to the chunk's
   __shared__ int32_t s_off[kPtChunk];    // first page handed out to it; -1: the request gets nothing
   __shared__ int s_taken;
-  if (!op_workspace_ok(a.ws)) return;
+  const uint32_t magic = op_magic(a.ws);
   const int tid = threadIdx.x;
   const int P = 1 << a.page_shift;
   const int64_t width = (int64_t)a.max_blocks << a.page_shift;  // tokens that a table row can address
@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const __grid_co
   int count = *a.free_count;
   bool bad = count < 0 || count > a.num_free;
   count = count < 0 ? 0 : count > a.num_free ? a.num_free : count;
+  if (!op_ready(a.ws, magic)) return;
   if (tid == 0) s_taken = 0;
   int64_t need0 = 0, tok0 = 0;  // sums over the chunks before this one
   const int chunks = (int)div_up(a.requests, kPtChunk);

@@ -131,7 +131,7 @@ rar_status check_norm_rope(const NormRopeCall& c, const void* const* qkv, Spans*
   if (st != RAR_OK) return st;
   const int64_t es = size_of(c.dtype);
   if (!heads_ok(c.q_heads, c.kv_heads, c.head_dim)) return RAR_ERR_ARG;
-  if (c.rot_dim < 16 || c.rot_dim > c.head_dim || c.rot_dim % 16 != 0 || c.max_pos < 1) return RAR_ERR_ARG;
+  if (c.rot_dim < 8 || c.rot_dim > c.head_dim || c.rot_dim % 8 != 0 || c.max_pos < 1) return RAR_ERR_ARG;
   const int64_t heads = c.q_heads + 2 * (int64_t)c.kv_heads;
   if (c.tokens < 0 || c.tokens * heads > INT32_MAX) return RAR_ERR_ARG;
   if ((st = check_pointers(qkv, c.nranks, c.tokens, 16)) != RAR_OK) return st;

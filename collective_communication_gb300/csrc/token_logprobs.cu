@@ -116,29 +116,6 @@ __device__ __forceinline__ uint64_t insert32(uint64_t list, uint64_t key) {
   return lane < at ? list : lane == at ? key : up;
 }
 
-// Two binary32 operations in one instruction.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 y;
-  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 p, p, q;\n\t"
-      "mov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return y;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 y;
-  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 p, p, q;\n\t"
-      "mov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return y;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 y;
-  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%6, %7};\n\t"
-      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return y;
-}
-
 // The largest of eight values, NaN left out.
 __device__ __forceinline__ float largest(const Pack8<uint16_t>& u) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u.u);
@@ -177,7 +154,7 @@ template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int kAhead = 64 / (8 * (int)sizeof(T));  // packs of a lane in flight
   __shared__ __align__(16) T s_words[TOP ? kLpWarps : 1][kAhead][32][8];
-  if (!op_workspace_ok(a.ws)) return;
+  const uint32_t magic = op_magic(a.ws);
   const int lane = threadIdx.x & 31;
   // neighbouring ranges go to different blocks, so that few workers still spread over the SMs
   const uint32_t worker = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
@@ -287,6 +264,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
       }
     }
     Stat st = warp_join(Stat{m, s2.x + s2.y, w2.x + w2.y});
+    if (!op_ready(a.ws, magic)) return;
 
     bool whole = t0 == 0 && t1 == (int)per_row;  // this warp has the row's result
     if (!whole) {
@@ -386,7 +364,7 @@ constexpr int kLpBwdTile = kLpThreads * 8 * 8;
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a,
                                                                        int tiles) {
-  if (!op_workspace_ok(a.ws)) return;
+  const uint32_t magic = op_magic(a.ws);
   const int row = (int)(blockIdx.x / (unsigned)tiles), tile = (int)(blockIdx.x % (unsigned)tiles);
   const int rank = blockIdx.y, tid = threadIdx.x;
   const int64_t width = a.first[rank + 1] - a.first[rank], c0 = (int64_t)tile * kLpBwdTile;
@@ -409,6 +387,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __
   // rows that share a 16-byte phase go in packs, the ends one by one; others one by one altogether
   const bool together = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;
   const int head = together ? min(n, (int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T)) : n;
+  if (!op_ready(a.ws, magic)) return;
   const int packs = (n - head) / 8, done = head + packs * 8;
   constexpr int kAhead = 64 / (8 * (int)sizeof(T));
   for (int p0 = 0; p0 < packs; p0 += kLpThreads * kAhead) {

@@ -464,7 +464,7 @@ RAR_API rar_status rar_page_tables(const int32_t* lens, const int32_t* new_token
  * rot_dim elements of a head by the angles of the token's position:
  * (a, b) -> (a cos - b sin, b cos + a sin). cos_sin is float
  * [max_pos, rot_dim], rot_dim/2 cosines then rot_dim/2 sines a row (any scaling
- * for long contexts is in the table); rot_dim is a multiple of 16 up to
+ * for long contexts is in the table); rot_dim is a multiple of 8 up to
  * head_dim. q_weight and k_weight: head_dim elements of dtype. positions:
  * int32 [tokens]; one outside 0..max_pos-1 counts as 0 and reports
  * RAR_ERR_CAPACITY.

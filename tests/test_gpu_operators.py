@@ -217,7 +217,8 @@ ROPE = [  # n, tokens, q heads, kv heads, dim, rot, interleaved, dtype, extra co
     (3, 7, 3, 1, 80, 80, False, "f32", 8), (1, 130, 5, 5, 96, 48, True, "bf16", 16),
     (2, 33, 6, 2, 256, 64, True, "f32", 0), (8, 17, 4, 2, 192, 192, False, "bf16", 0),
     (1, 65, 2, 1, 8 * 9, 32, False, "bf16", 0), (2, 9, 1, 1, 8 * 31, 16, True, "bf16", 8),
-    (32, 3, 2, 1, 16, 16, False, "f32", 0), (1, 3, 1, 1, 24, 16, False, "bf16", 0)]
+    (32, 3, 2, 1, 16, 16, False, "f32", 0), (1, 3, 1, 1, 24, 16, False, "bf16", 0),
+    (2, 11, 3, 2, 80, 40, False, "bf16", 0), (1, 6, 9, 5, 8, 8, False, "f32", 0), (2, 5, 5, 3, 120, 24, True, "f32", 8)]
 
 
 @pytest.mark.parametrize("n,t,q,kv,d,rot,inter,dtype,extra", ROPE)

@@ -69,7 +69,7 @@ def rope(lib, form="plain", **kw):
 @pytest.mark.parametrize("form", ["plain", "cached", "backward"])
 def test_norm_rope_refusals(lib, form):
     bad = [dict(n=0), dict(n=33), dict(dtype=2), dict(tokens=-1), dict(tokens=1 << 31), dict(d=60), dict(d=264),
-           dict(d=0), dict(q=0), dict(kv=0), dict(q=1025), dict(rot=0), dict(rot=8), dict(rot=24), dict(rot=80),
+           dict(d=0), dict(q=0), dict(kv=0), dict(q=1025), dict(rot=0), dict(rot=4), dict(rot=20), dict(rot=72),
            dict(max_pos=0), dict(wq=0), dict(wk=0), dict(cs=0), dict(pos=0), dict(qkv=None), dict(stride=632)]
     if form == "backward":
         bad += [dict(dq=None), dict(dx=ranks(1)), dict(dx=ranks(7)), dict(dwq=ranks(12)), dict(dvs=56), dict(dxs=632)]
