@@ -24,7 +24,8 @@
 namespace rar {
 
 constexpr int kNrThreads = 256;
-constexpr int kStrip = 4;                 // heads of a forward strip
+template <typename T>
+constexpr int kStrip = 4;                 // rows of a forward strip
 constexpr int kBwdStrip = 2;              // heads of a backward strip: x and dy of each are in registers
 constexpr int kNormRopeBwdBlocks = 1216;  // most blocks of a backward launch, all ranks together
 
@@ -122,11 +123,18 @@ __device__ __forceinline__ void rotate(float (&v)[8], const Turn& t) {
   }
 }
 
+// Sum over a group; groups of a warp may be on different paths.
 template <int L>
 __device__ __forceinline__ float group_sum(float x) {
+  const uint32_t mask = L == 32 ? ~0u : ((1u << (L & 31)) - 1) << (threadIdx.x & 31 & ~(L - 1));
 #pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) x += __shfl_xor_sync(~0u, x, d, L);
+  for (int d = L / 2; d > 0; d >>= 1) x += __shfl_xor_sync(mask, x, d, L);
   return x;
+}
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
   float2 s = mul2(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
@@ -145,36 +153,37 @@ __device__ __forceinline__ void load_weight(float (&w)[8], const void* p, const 
 
 }  // namespace
 
-// A token's heads in strips: `q_strips` strips of per_q query heads, then strips
-// of per_kv key heads, with CACHE each with the same heads' values. Keys and
-// values go to the cache rows of slots, or keys to k_out. Block y is the rank.
+// Blocks below q_blocks take strips of per_q query heads, the others strips of
+// per_kv key heads, with CACHE each followed by the same heads' values; so a
+// warp's groups do the same. Keys and values go to the cache rows of slots, or
+// keys to k_out. Block y is the rank.
 template <typename T, int L, bool INTER, bool CACHE>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int strips,
-                                                               int q_strips, int per_q, int per_kv) {
+__global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int q_blocks,
+                                                               int q_strips, int per_q, int kv_strips, int per_kv) {
+  constexpr int kRows = kStrip<T>;
   const uint32_t magic = op_magic(a.ws);
   const int rank = blockIdx.y, D = a.head_dim;
   const Lane n = lane_of<INTER>(threadIdx.x & (L - 1), D, a.rot);
-  const uint32_t item = blockIdx.x * (kNrThreads / L) + threadIdx.x / L;
-  const bool live = item < (uint32_t)a.tokens * (uint32_t)strips;
-  const int token = live ? (int)(item / (uint32_t)strips) : 0;
-  const int strip = live ? (int)(item - (uint32_t)token * (uint32_t)strips) : 0;
-  const bool is_q = strip < q_strips, in = live && n.in;
-  const int h0 = is_q ? strip * per_q : (strip - q_strips) * per_kv;
+  const bool is_q = blockIdx.x < q_blocks;
+  const uint32_t strips = is_q ? q_strips : kv_strips;
+  const uint32_t item = (blockIdx.x - (is_q ? 0 : q_blocks)) * (kNrThreads / L) + threadIdx.x / L;
+  const bool live = item < (uint32_t)a.tokens * strips;
+  const int token = live ? (int)(item / strips) : 0;
+  const int strip = live ? (int)(item - (uint32_t)token * strips) : 0;
+  const bool in = live && n.in;
+  const int h0 = strip * (is_q ? per_q : per_kv);
   const int heads = is_q ? min(per_q, a.q_heads - h0) : min(per_kv, a.kv_heads - h0);
-  const int rows = heads * (CACHE && !is_q ? 2 : 1);  // with CACHE a key strip's values follow its keys
+  const int rows = heads * (CACHE && !is_q ? 2 : 1);
 
-  const T* x0 = reinterpret_cast<const T*>(a.qkv[rank]) + (int64_t)token * a.qkv_stride;
-  auto head_of = [&](int i) {  // place of the strip's row i among the token's heads
-    return is_q ? h0 + i : i < heads ? a.q_heads + h0 + i : a.q_heads + a.kv_heads + h0 + i - heads;
-  };
   int pos = live ? a.positions[token] : 0;
   int64_t slot = CACHE && live ? a.slots[token] : -1;  // below zero: a padding token, no cache row
-  Chunks<T> x[kStrip];
+  const T* x0 = reinterpret_cast<const T*>(a.qkv[rank]) + (int64_t)token * a.qkv_stride + (h0 + (is_q ? 0 : a.q_heads)) * D;
+  const int to_v = (a.kv_heads - heads) * D;  // from the place after a strip's keys to its values
+  Chunks<T> x[kRows];
 #pragma unroll
-  for (int i = 0; i < kStrip; i++) {
-    x[i].zero();
-    if (in && i < rows) x[i].load(x0 + head_of(i) * D, n);
-  }
+  for (int i = 0; i < kRows; i++)
+    if (in && i < rows) x[i].load(x0 + i * D + (CACHE && !is_q && i >= heads ? to_v : 0), n);
+    else x[i].zero();
   bool bad = false;
   if (pos < 0 || pos >= a.max_pos) { bad = true; pos = 0; }
   if (CACHE && slot >= a.num_slots) { bad = true; slot = -1; }
@@ -184,14 +193,30 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
   const float inv = 1.f / (float)D;
   if (!op_ready(a.ws, magic)) return;
 
+  // where the strip's first row goes and how far apart its rows are
+  T* out;
+  T* out_v = nullptr;
+  int64_t apart = D;
+  bool kept = true;  // false: a padding token's keys and values
+  if (is_q) {
+    out = reinterpret_cast<T*>(a.q_out[rank]) + (int64_t)token * a.q_stride + h0 * D;
+  } else if (!CACHE) {
+    out = reinterpret_cast<T*>(a.k_out[rank]) + (int64_t)token * a.k_stride + h0 * D;
+  } else {
+    kept = slot >= 0;
+    const int64_t page = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
+    const int64_t at = (((page * a.kv_heads + h0) << a.page_shift) + off) * D;
+    out = reinterpret_cast<T*>(a.k_out[rank]) + at;
+    out_v = reinterpret_cast<T*>(a.v_out[rank]) + at;
+    apart = (int64_t)D << a.page_shift;
+  }
 #pragma unroll
-  for (int i = 0; i < kStrip; i++) {
-    const bool is_v = CACHE && !is_q && i >= heads;
-    float v[8];
-    x[i].widen(v);
-    const float r = rsqrtf(group_sum<L>(dot8(v, v)) * inv + a.eps);
-    if (!in || i >= rows) continue;
-    if (!is_v) {
+  for (int i = 0; i < kRows; i++) {
+    if (i >= rows) break;
+    if (!CACHE || is_q || i < heads) {
+      float v[8];
+      x[i].widen(v);
+      const float r = rsqrt_fast(fmaf(group_sum<L>(dot8(v, v)), inv, a.eps));
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const float2 y = mul2(mul2(make_float2(v[j], v[j + 1]), make_float2(r, r)), make_float2(w[j], w[j + 1]));
@@ -200,15 +225,9 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
       }
       rotate<INTER, false>(v, turn);
       x[i].narrow(v);
-    }
-    if (is_q) {
-      x[i].store(reinterpret_cast<T*>(a.q_out[rank]) + (int64_t)token * a.q_stride + (h0 + i) * D, n);
-    } else if (!CACHE) {
-      x[i].store(reinterpret_cast<T*>(a.k_out[rank]) + (int64_t)token * a.k_stride + (h0 + i) * D, n);
-    } else if (slot >= 0) {
-      const int64_t page = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
-      T* cache = reinterpret_cast<T*>(is_v ? a.v_out[rank] : a.k_out[rank]);
-      x[i].store(cache + (((page * a.kv_heads + h0 + (is_v ? i - heads : i)) << a.page_shift) + off) * D, n);
+      if (in && kept) x[i].store(out + i * apart, n);
+    } else if (in && kept) {
+      x[i].store(out_v + (i - heads) * apart, n);
     }
   }
   if (bad) op_report(a.ws, kErrCapacity);
@@ -291,7 +310,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const __grid_
       float v[8], g[8];
       cur.x[i].widen(v);
       cur.dy[i].widen(g);
-      const float r = rsqrtf(group_sum<L>(dot8(v, v)) * inv + a.eps);
+      const float r = rsqrt_fast(fmaf(group_sum<L>(dot8(v, v)), inv, a.eps));
       rotate<INTER, true>(g, turn);
 #pragma unroll
       for (int j = 0; j < 8; j++) {
@@ -402,20 +421,21 @@ int64_t norm_rope_scratch_bytes(int nranks, int head_dim) {
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
   const int lanes = lanes_of(a.head_dim);
   const bool cache = a.slots != nullptr;
-  const int most_kv = cache ? kStrip / 2 : kStrip;
-  int q_strips = (int)div_up(a.q_heads, kStrip), kv_strips = (int)div_up(a.kv_heads, most_kv);
+  const int rows = a.dtype == kF32 ? kStrip<float> : kStrip<uint16_t>, most_kv = cache ? rows / 2 : rows;
+  int q_strips = (int)div_up(a.q_heads, rows), kv_strips = (int)div_up(a.kv_heads, most_kv);
   int per_q = (int)div_up(a.q_heads, q_strips), per_kv = (int)div_up(a.kv_heads, kv_strips);
   q_strips = (int)div_up(a.q_heads, per_q);
   kv_strips = (int)div_up(a.kv_heads, per_kv);
-  int strips = q_strips + kv_strips;
-  const int64_t items = (int64_t)a.tokens * strips;
-  dim3 grid((unsigned)div_up(items, kNrThreads / lanes), (unsigned)a.nranks);
+  const int groups = kNrThreads / lanes;
+  int q_blocks = (int)div_up((int64_t)a.tokens * q_strips, groups);
+  const int kv_blocks = (int)div_up((int64_t)a.tokens * kv_strips, groups);
+  dim3 grid((unsigned)(q_blocks + kv_blocks), (unsigned)a.nranks);
   if (trace_on())
     std::fprintf(stderr, "rar trace: qk_norm_rope nranks=%d tokens=%d heads=%d/%d dim=%d rot=%d grid=%ux%u cache=%d\n",
                  a.nranks, a.tokens, a.q_heads, a.kv_heads, a.head_dim, a.rot, grid.x, grid.y, cache ? 1 : 0);
   const void* fn = a.dtype == kF32 ? forward_of<float>(lanes, a.interleaved != 0, cache)
                                    : forward_of<uint16_t>(lanes, a.interleaved != 0, cache);
-  void* params[] = {const_cast<NormRopeArgs*>(&a), &strips, &q_strips, &per_q, &per_kv};
+  void* params[] = {const_cast<NormRopeArgs*>(&a), &q_blocks, &q_strips, &per_q, &kv_strips, &per_kv};
   return cudaLaunchKernel(fn, grid, dim3(kNrThreads), params, 0, stream);
 }
 
