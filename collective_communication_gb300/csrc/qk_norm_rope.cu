@@ -26,8 +26,12 @@ namespace rar {
 constexpr int kNrThreads = 256;
 template <typename T>
 constexpr int kStrip = 4;                 // rows of a forward strip
-constexpr int kBwdStrip = 2;              // heads of a backward strip: x and dy of each are in registers
+constexpr int kBwdThreads = 128;
+constexpr int kBwdStages = 4;             // rows of x and dy of a group in shared memory
+constexpr int kBwdJoin = 32;              // partial weight sums that one block joins
 constexpr int kNormRopeBwdBlocks = 1216;  // most blocks of a backward launch, all ranks together
+constexpr int kBwdCounters = 48;          // arrival counters of a rank: two kinds, then runs of blocks
+static_assert(kBwdCounters * kMaxRanks <= kOpCounters && kNormRopeBwdBlocks / kBwdJoin + 4 <= kBwdCounters, "counters");
 
 namespace {
 
@@ -48,44 +52,88 @@ __device__ __forceinline__ Lane lane_of(int l, int D, int rot) {
   return n;
 }
 
-// Two chunks of four elements.
-template <typename T>
+// A lane's eight elements in binary32, so that elements p[j] and p[j + 2] make
+// two pairs of the rotation in either layout.
+struct Row8 {
+  F2 p[4];
+};
+__device__ __forceinline__ Row8 operator*(const Row8& a, const Row8& b) {
+  Row8 r;
+#pragma unroll
+  for (int j = 0; j < 4; j++) r.p[j] = mul2(a.p[j], b.p[j]);
+  return r;
+}
+__device__ __forceinline__ Row8 operator*(const Row8& a, float f) {
+  const F2 ff = f2(f, f);
+  Row8 r;
+#pragma unroll
+  for (int j = 0; j < 4; j++) r.p[j] = mul2(a.p[j], ff);
+  return r;
+}
+__device__ __forceinline__ Row8 fma_row(const Row8& a, const Row8& b, const Row8& c) {
+  Row8 r;
+#pragma unroll
+  for (int j = 0; j < 4; j++) r.p[j] = fma2(a.p[j], b.p[j], c.p[j]);
+  return r;
+}
+__device__ __forceinline__ float dot8(const Row8& a, const Row8& b) {
+  F2 s = mul2(a.p[0], b.p[0]);
+#pragma unroll
+  for (int j = 1; j < 4; j++) s = fma2(a.p[j], b.p[j], s);
+  const float2 x = unpack(s);
+  return x.x + x.y;
+}
+
+// Two chunks of four elements as they are in memory. INTER: the even elements
+// of the eight make p[0], p[1], the odd ones p[2], p[3].
+template <typename T, bool INTER>
 struct Chunks;
-template <>
-struct Chunks<uint16_t> {
+template <bool INTER>
+struct Chunks<uint16_t, INTER> {
   uint2 a, b;
   __device__ __forceinline__ void load(const uint16_t* row, const Lane& n) {
     a = *reinterpret_cast<const uint2*>(row + n.o0);
     b = *reinterpret_cast<const uint2*>(row + n.o1);
   }
   __device__ __forceinline__ void zero() { a = b = make_uint2(0, 0); }
-  __device__ __forceinline__ void widen(float (&v)[8]) const {
-    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
-    v[4] = bf16_lo(b.x); v[5] = bf16_hi(b.x); v[6] = bf16_lo(b.y); v[7] = bf16_hi(b.y);
+  __device__ __forceinline__ Row8 widen() const {
+    if (INTER)
+      return Row8{{f2(bf16_lo(a.x), bf16_lo(a.y)), f2(bf16_lo(b.x), bf16_lo(b.y)), f2(bf16_hi(a.x), bf16_hi(a.y)),
+                   f2(bf16_hi(b.x), bf16_hi(b.y))}};
+    return Row8{{f2(bf16_lo(a.x), bf16_hi(a.x)), f2(bf16_lo(a.y), bf16_hi(a.y)), f2(bf16_lo(b.x), bf16_hi(b.x)),
+                 f2(bf16_lo(b.y), bf16_hi(b.y))}};
   }
-  __device__ __forceinline__ void narrow(const float (&v)[8]) {
-    a = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
-    b = make_uint2(bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+  __device__ __forceinline__ void narrow(const Row8& r) {
+    const float2 p = unpack(r.p[0]), q = unpack(r.p[1]), s = unpack(r.p[2]), t = unpack(r.p[3]);
+    if (INTER) {
+      a = make_uint2(bf16_pair(p.x, s.x), bf16_pair(p.y, s.y));
+      b = make_uint2(bf16_pair(q.x, t.x), bf16_pair(q.y, t.y));
+    } else {
+      a = make_uint2(bf16_pair(p.x, p.y), bf16_pair(q.x, q.y));
+      b = make_uint2(bf16_pair(s.x, s.y), bf16_pair(t.x, t.y));
+    }
   }
   __device__ __forceinline__ void store(uint16_t* row, const Lane& n) const {
     *reinterpret_cast<uint2*>(row + n.o0) = a;
     *reinterpret_cast<uint2*>(row + n.o1) = b;
   }
 };
-template <>
-struct Chunks<float> {
+template <bool INTER>
+struct Chunks<float, INTER> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* row, const Lane& n) {
     a = *reinterpret_cast<const float4*>(row + n.o0);
     b = *reinterpret_cast<const float4*>(row + n.o1);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void widen(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ __forceinline__ Row8 widen() const {
+    if (INTER) return Row8{{f2(a.x, a.z), f2(b.x, b.z), f2(a.y, a.w), f2(b.y, b.w)}};
+    return Row8{{f2(a.x, a.y), f2(a.z, a.w), f2(b.x, b.y), f2(b.z, b.w)}};
   }
-  __device__ __forceinline__ void narrow(const float (&v)[8]) {
-    a = make_float4(v[0], v[1], v[2], v[3]);
-    b = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ __forceinline__ void narrow(const Row8& r) {
+    const float2 p = unpack(r.p[0]), q = unpack(r.p[1]), s = unpack(r.p[2]), t = unpack(r.p[3]);
+    a = INTER ? make_float4(p.x, s.x, p.y, s.y) : make_float4(p.x, p.y, q.x, q.y);
+    b = INTER ? make_float4(q.x, t.x, q.y, t.y) : make_float4(s.x, s.y, t.x, t.y);
   }
   __device__ __forceinline__ void store(float* row, const Lane& n) const {
     *reinterpret_cast<float4*>(row + n.o0) = a;
@@ -95,7 +143,7 @@ struct Chunks<float> {
 
 // A lane's four angles; (1, 0) where nothing turns.
 struct Turn {
-  float c[4], s[4];
+  F2 c[2], s[2];
 };
 __device__ __forceinline__ Turn load_turn(const float* row, int rot, const Lane& n) {
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -103,24 +151,20 @@ __device__ __forceinline__ Turn load_turn(const float* row, int rot, const Lane&
     c = *reinterpret_cast<const float4*>(row + n.angle);
     s = *reinterpret_cast<const float4*>(row + (rot >> 1) + n.angle);
   }
-  return Turn{{c.x, c.y, c.z, c.w}, {s.x, s.y, s.z, s.w}};
+  return Turn{{f2(c.x, c.y), f2(c.z, c.w)}, {f2(s.x, s.y), f2(s.z, s.w)}};
 }
 
-// v <- R v, or R^T v with BACK.
-template <bool INTER, bool BACK>
-__device__ __forceinline__ void rotate(float (&v)[8], const Turn& t) {
+// R v, or R^T v with BACK.
+template <bool BACK>
+__device__ __forceinline__ Row8 rotate(const Row8& v, const Turn& t) {
+  Row8 r;
 #pragma unroll
-  for (int j = 0; j < 4; j += 2) {
-    const int x = INTER ? 2 * j : j, y = INTER ? 2 * j + 1 : j + 4, step = INTER ? 2 : 1;
-    const float2 c = make_float2(t.c[j], t.c[j + 1]);
-    const float2 s = BACK ? make_float2(-t.s[j], -t.s[j + 1]) : make_float2(t.s[j], t.s[j + 1]);
-    const float2 a = make_float2(v[x], v[x + step]), b = make_float2(v[y], v[y + step]);
-    const float2 ra = fma2(b, make_float2(-s.x, -s.y), mul2(a, c)), rb = fma2(a, s, mul2(b, c));
-    v[x] = ra.x;
-    v[x + step] = ra.y;
-    v[y] = rb.x;
-    v[y + step] = rb.y;
+  for (int j = 0; j < 2; j++) {
+    const F2 neg = mul2(t.s[j], f2(-1.f, -1.f));
+    r.p[j] = fma2(v.p[j + 2], BACK ? t.s[j] : neg, mul2(v.p[j], t.c[j]));
+    r.p[j + 2] = fma2(v.p[j], BACK ? neg : t.s[j], mul2(v.p[j + 2], t.c[j]));
   }
+  return r;
 }
 
 // Sum over a group; groups of a warp may be on different paths.
@@ -136,19 +180,13 @@ __device__ __forceinline__ float rsqrt_fast(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
-  float2 s = mul2(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
-#pragma unroll
-  for (int j = 2; j < 8; j += 2) s = fma2(make_float2(a[j], a[j + 1]), make_float2(b[j], b[j + 1]), s);
-  return s.x + s.y;
-}
 // The lane's weights of a head's kind.
-template <typename T>
-__device__ __forceinline__ void load_weight(float (&w)[8], const void* p, const Lane& n) {
-  Chunks<T> c;
+template <typename T, bool INTER>
+__device__ __forceinline__ Row8 load_weight(const void* p, const Lane& n) {
+  Chunks<T, INTER> c;
   c.zero();
   if (n.in) c.load(reinterpret_cast<const T*>(p), n);
-  c.widen(w);
+  return c.widen();
 }
 
 }  // namespace
@@ -179,7 +217,7 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
   int64_t slot = CACHE && live ? a.slots[token] : -1;  // below zero: a padding token, no cache row
   const T* x0 = reinterpret_cast<const T*>(a.qkv[rank]) + (int64_t)token * a.qkv_stride + (h0 + (is_q ? 0 : a.q_heads)) * D;
   const int to_v = (a.kv_heads - heads) * D;  // from the place after a strip's keys to its values
-  Chunks<T> x[kRows];
+  Chunks<T, INTER> x[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; i++)
     if (in && i < rows) x[i].load(x0 + i * D + (CACHE && !is_q && i >= heads ? to_v : 0), n);
@@ -188,8 +226,7 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
   if (pos < 0 || pos >= a.max_pos) { bad = true; pos = 0; }
   if (CACHE && slot >= a.num_slots) { bad = true; slot = -1; }
   const Turn turn = load_turn(a.cos_sin + (int64_t)pos * a.rot, a.rot, n);
-  float w[8];
-  load_weight<T>(w, is_q ? a.q_weight : a.k_weight, n);
+  const Row8 w = load_weight<T, INTER>(is_q ? a.q_weight : a.k_weight, n);
   const float inv = 1.f / (float)D;
   if (!op_ready(a.ws, magic)) return;
 
@@ -214,17 +251,9 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
   for (int i = 0; i < kRows; i++) {
     if (i >= rows) break;
     if (!CACHE || is_q || i < heads) {
-      float v[8];
-      x[i].widen(v);
+      const Row8 v = x[i].widen();
       const float r = rsqrt_fast(fmaf(group_sum<L>(dot8(v, v)), inv, a.eps));
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float2 y = mul2(mul2(make_float2(v[j], v[j + 1]), make_float2(r, r)), make_float2(w[j], w[j + 1]));
-        v[j] = y.x;
-        v[j + 1] = y.y;
-      }
-      rotate<INTER, false>(v, turn);
-      x[i].narrow(v);
+      x[i].narrow(rotate<false>(v * r * w, turn));
       if (in && kept) x[i].store(out + i * apart, n);
     } else if (in && kept) {
       x[i].store(out_v + (i - heads) * apart, n);
@@ -234,153 +263,210 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
 }
 
 // The gradient. z = R^T dy, dw = sum z x r, g = z w, xh = x r,
-// dx = r (g - xh mean(g xh)); dv is copied. The first q_blocks blocks of a rank
-// walk over strips of query heads, the others over key heads and the same
-// heads' values; so one set of weight sums stays in registers. They are added
-// over the block's groups in shared memory in group order, and the block that
-// arrives last for its rank adds the blocks' partial sums in block order: the
-// same bits every time.
+// dx = r (g - xh mean(g xh)); dv is copied. A rank's blocks are of three kinds,
+// for query heads, key heads and values, so one set of weights and weight sums
+// stays in registers. A group walks over tokens, head by head; rows of x and dy
+// come through a ring of kBwdStages rows in shared memory (16-byte asynchronous
+// copies of consecutive elements, read back as the lane's two chunks), so three
+// rows a group are in flight whatever the registers hold.
+//
+// Weight sums are added over the block's groups in group order, then over runs
+// of kBwdJoin blocks and over the runs in block order, each time by the block
+// that arrives last: the same bits every time.
+namespace {
+
+__device__ __forceinline__ void copy_async16(void* smem, const void* gmem, bool live) {  // zeros if not live
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem)), "l"(gmem), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+}  // namespace
+
 template <typename T, int L, bool INTER>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs a,
-                                                                   int q_blocks) {
-  constexpr int kGroups = kNrThreads / L;
-  __shared__ float sums[kNrThreads][9];
+__global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs a,
+                                                                    int q_blocks, int k_blocks) {
+  constexpr int kGroups = kBwdThreads / L, kRow = L * 8, kCopies = (int)sizeof(T) / 2;
+  __shared__ __align__(16) T ring[kGroups][kBwdStages][2][kRow];
+  __shared__ float sums[kBwdThreads][9];
   __shared__ bool s_last;
   const uint32_t magic = op_magic(a.ws);
-  const int rank = blockIdx.y, group = threadIdx.x / L, D = a.head_dim;
-  const Lane n = lane_of<INTER>(threadIdx.x & (L - 1), D, a.rot);
-  const bool is_q = blockIdx.x < q_blocks;
-  const uint32_t block = is_q ? blockIdx.x : blockIdx.x - q_blocks, blocks = is_q ? q_blocks : gridDim.x - q_blocks;
-  const int kind_heads = is_q ? a.q_heads : a.kv_heads;
-  const uint32_t strips = (uint32_t)(kind_heads + kBwdStrip - 1) / kBwdStrip;
-  float w[8], dw[8];
-  load_weight<T>(w, is_q ? a.q_weight : a.k_weight, n);
-#pragma unroll
-  for (int j = 0; j < 8; j++) dw[j] = 0.f;
-  const float inv = 1.f / (float)D;
-  const int64_t g_stride = is_q ? a.dq_stride : a.dk_stride;
-  const T* g0 = reinterpret_cast<const T*>(is_q ? a.dq[rank] : a.dk[rank]);
-  bool bad = false;
-  const uint32_t items = (uint32_t)a.tokens * strips;
-  // the next item is loaded while this one is worked on
-  struct Item {
-    Chunks<T> x[kBwdStrip], dy[kBwdStrip];
-    int token, h0, heads, pos;
-  };
-  const uint32_t step = blocks * kGroups;
+  const int rank = blockIdx.y, group = threadIdx.x / L, l = threadIdx.x & (L - 1), D = a.head_dim;
+  const Lane n = lane_of<INTER>(l, D, a.rot);
   const T* xs = reinterpret_cast<const T*>(a.qkv[rank]);
-  auto fetch = [&](uint32_t item) {
-    Item t;
-    const bool live = item < items;
-    t.token = live ? (int)(item / strips) : 0;
-    t.h0 = live ? (int)(item - (uint32_t)t.token * strips) * kBwdStrip : 0;
-    t.heads = live && n.in ? min(kBwdStrip, kind_heads - t.h0) : 0;
-    t.pos = live ? a.positions[t.token] : 0;
-    const T* xrow = xs + (int64_t)t.token * a.qkv_stride + (is_q ? t.h0 : a.q_heads + t.h0) * D;
-    const T* grow = g0 + (int64_t)t.token * g_stride + t.h0 * D;
+  T* ds = reinterpret_cast<T*>(a.dqkv[rank]);
+
+  if (blockIdx.x >= q_blocks + k_blocks) {  // values
+    const int block = blockIdx.x - q_blocks - k_blocks, blocks = gridDim.x - q_blocks - k_blocks;
+    const int place = (a.q_heads + a.kv_heads) * D, packs = a.kv_heads * D / 8;
+    const int64_t all = (int64_t)a.tokens * packs, step = (int64_t)blocks * kBwdThreads;
+    if (!op_ready(a.ws, magic)) return;
+    for (int64_t i = (int64_t)block * kBwdThreads + threadIdx.x; i < all; i += 4 * step) {
+      Pack8<T> u[4];
 #pragma unroll
-    for (int i = 0; i < kBwdStrip; i++) {
-      t.x[i].zero();
-      t.dy[i].zero();
-      if (i < t.heads) {
-        t.x[i].load(xrow + i * D, n);
-        t.dy[i].load(grow + i * D, n);
+      for (int j = 0; j < 4; j++) {
+        const int64_t e = i + j * step, token = e / packs;
+        if (e < all) u[j].load(reinterpret_cast<const T*>(a.dv[rank]) + token * a.dv_stride + (e - token * packs) * 8);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int64_t e = i + j * step, token = e / packs;
+        if (e < all) u[j].store(ds + token * a.dqkv_stride + place + (e - token * packs) * 8);
       }
     }
-    return t;
-  };
-  uint32_t item = block * kGroups + group;
-  Item cur = fetch(item);
-  if (!op_ready(a.ws, magic)) return;
-  for (; item - group < items; item += step) {
-    const Item nxt = fetch(item + step);
-    if (cur.pos < 0 || cur.pos >= a.max_pos) { bad = true; cur.pos = 0; }
-    const Turn turn = load_turn(a.cos_sin + (int64_t)cur.pos * a.rot, a.rot, n);
-    T* drow = reinterpret_cast<T*>(a.dqkv[rank]) + (int64_t)cur.token * a.dqkv_stride;
-    Chunks<T> dv[kBwdStrip];
-    if (!is_q) {
-      const T* vrow = reinterpret_cast<const T*>(a.dv[rank]) + (int64_t)cur.token * a.dv_stride + cur.h0 * D;
-#pragma unroll
-      for (int i = 0; i < kBwdStrip; i++)
-        if (i < cur.heads) dv[i].load(vrow + i * D, n);
-    }
-    const int place = is_q ? cur.h0 : a.q_heads + cur.h0;
-#pragma unroll
-    for (int i = 0; i < kBwdStrip; i++) {
-      float v[8], g[8];
-      cur.x[i].widen(v);
-      cur.dy[i].widen(g);
-      const float r = rsqrt_fast(fmaf(group_sum<L>(dot8(v, v)), inv, a.eps));
-      rotate<INTER, true>(g, turn);
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        v[j] *= r;
-        dw[j] = fmaf(g[j], v[j], dw[j]);  // rows that are not there are zeros
-        g[j] *= w[j];
-      }
-      const float mean = group_sum<L>(dot8(g, v)) * inv;
-#pragma unroll
-      for (int j = 0; j < 8; j++) g[j] = r * fmaf(-mean, v[j], g[j]);
-      if (i >= cur.heads) continue;
-      Chunks<T> dx;
-      dx.narrow(g);
-      dx.store(drow + (place + i) * D, n);
-      if (!is_q) dv[i].store(drow + (place + a.kv_heads + i) * D, n);
-    }
-    cur = nxt;
+    return;
   }
+
+  const bool is_q = blockIdx.x < q_blocks;
+  const int walkers = (is_q ? q_blocks : k_blocks) * kGroups;  // groups that share the tokens
+  const int walker = (is_q ? blockIdx.x : blockIdx.x - q_blocks) * kGroups + group;
+  const int heads = is_q ? a.q_heads : a.kv_heads, place = is_q ? 0 : a.q_heads * D;
+  const int64_t g_stride = is_q ? a.dq_stride : a.dk_stride;
+  const T* gs = reinterpret_cast<const T*>(is_q ? a.dq[rank] : a.dk[rank]);
+  const Row8 w = load_weight<T, INTER>(is_q ? a.q_weight : a.k_weight, n);
+  const F2 zero = f2(0.f, 0.f);
+  Row8 dw = {{zero, zero, zero, zero}};
+  const float inv = 1.f / (float)D;
+  bool bad = false;
+  // the warp's first group has the most tokens; the others run as long, with rows of zeros at the end
+  const int first_walker = walker - (threadIdx.x & 31) / L;
+  const int rows = first_walker < a.tokens ? ((a.tokens - 1 - first_walker) / walkers + 1) * heads : 0;
+  const int mine = walker < a.tokens ? ((a.tokens - 1 - walker) / walkers + 1) * heads : 0;
+
+  // Pointers walk along: one head on within a token, then to the group's next token.
+  const int64_t x_jump = (int64_t)walkers * a.qkv_stride - (int64_t)(heads - 1) * D;
+  const int64_t g_jump = (int64_t)walkers * g_stride - (int64_t)(heads - 1) * D;
+  const int64_t d_jump = (int64_t)walkers * a.dqkv_stride - (int64_t)(heads - 1) * D;
+  const int64_t w0 = walker < a.tokens ? walker : 0;
+  const T* fx = xs + w0 * a.qkv_stride + place + l * 8;  // of the next row to ask for
+  const T* fg = gs + w0 * g_stride + l * 8;
+  int f_left = n.in ? mine : 0, f_head = 0, f_slot = 0;
+  T* const cell = &ring[group][0][0][l * 8];
+  auto fetch = [&]() {
+    const bool live = f_left > 0;
+#pragma unroll
+    for (int c = 0; c < kCopies; c++) {
+      copy_async16(cell + f_slot * (2 * kRow) + c * (16 / (int)sizeof(T)), (live ? fx : xs) + c * (16 / (int)sizeof(T)), live);
+      copy_async16(cell + f_slot * (2 * kRow) + kRow + c * (16 / (int)sizeof(T)), (live ? fg : gs) + c * (16 / (int)sizeof(T)),
+                   live);
+    }
+    copy_async_commit();
+    f_slot = f_slot + 1 == kBwdStages ? 0 : f_slot + 1;
+    f_left--;
+    const bool wrap = ++f_head == heads;
+    fx += wrap ? x_jump : D;
+    fg += wrap ? g_jump : D;
+    f_head = wrap ? 0 : f_head;
+  };
+  auto position = [&](int token) {
+    const int pos = token < a.tokens ? a.positions[token] : 0;
+    if (pos >= 0 && pos < a.max_pos) return pos;
+    bad = true;
+    return 0;
+  };
+#pragma unroll
+  for (int s = 0; s < kBwdStages - 1; s++) fetch();
+  int token = walker, head = 0, slot = 0;
+  Turn turn = load_turn(a.cos_sin + (int64_t)position(token) * a.rot, a.rot, n);
+  int pos_next = position(token + walkers);
+  T* out = ds + w0 * a.dqkv_stride + place;
+  const int stores = n.in ? mine : 0;
+  if (!op_ready(a.ws, magic)) {
+    copy_async_wait<0>();
+    return;
+  }
+  for (int r = 0; r < rows; r++) {
+    copy_async_wait<kBwdStages - 2>();
+    __syncwarp();  // every lane's copies of this row are there, and every lane is past the last row's slot
+    Chunks<T, INTER> x, dy;
+    x.load(ring[group][slot][0], n);
+    dy.load(ring[group][slot][1], n);
+    fetch();
+    const Row8 v = x.widen(), z = rotate<true>(dy.widen(), turn);
+    const float root = rsqrt_fast(fmaf(group_sum<L>(dot8(v, v)), inv, a.eps));
+    const Row8 xh = v * root, g = z * w;
+    dw = fma_row(z, xh, dw);
+    const float mean = inv * group_sum<L>(dot8(g, xh));
+    const F2 down = f2(-mean, -mean);
+    dy.narrow(fma_row(xh, Row8{{down, down, down, down}}, g) * root);
+    if (r < stores) dy.store(out, n);
+    slot = slot + 1 == kBwdStages ? 0 : slot + 1;
+    const bool wrap = ++head == heads;
+    out += wrap ? d_jump : D;
+    if (wrap) {
+      head = 0;
+      token += walkers;
+      turn = load_turn(a.cos_sin + (int64_t)pos_next * a.rot, a.rot, n);
+      pos_next = position(token + walkers);
+    }
+  }
+  copy_async_wait<0>();
   if (bad) op_report(a.ws, kErrCapacity);
 
   // partial sums of the rank's blocks: [block][D], the query blocks first
   float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset) + (int64_t)rank * gridDim.x * D;
 #pragma unroll
-  for (int j = 0; j < 8; j++) sums[threadIdx.x][j] = dw[j];
+  for (int j = 0; j < 4; j++) {
+    sums[threadIdx.x][2 * j] = unpack(dw.p[j]).x;
+    sums[threadIdx.x][2 * j + 1] = unpack(dw.p[j]).y;
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e < D; e += kNrThreads) {
+  for (int e = threadIdx.x; e < D; e += kBwdThreads) {
     // the lane and chunk that hold element e
     const int half = a.rot >> 1;
     const bool turned = !INTER && e < a.rot;
-    const int l = turned ? (e < half ? e : e - half) >> 2 : e >> 3;
-    const int j = turned ? (e & 3) + (e < half ? 0 : 4) : e & 7;
+    const int from = turned ? (e < half ? e : e - half) >> 2 : e >> 3;
+    const int j = turned ? (e & 3) + (e < half ? 0 : 4) : INTER ? (e & 1) * 4 + ((e & 7) >> 1) : e & 7;
     float s = 0.f;
 #pragma unroll
-    for (int g = 0; g < kGroups; g++) s += sums[g * L + l][j];
+    for (int g = 0; g < kGroups; g++) s += sums[g * L + from][j];
     parts[(int64_t)blockIdx.x * D + e] = s;
   }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t* counter = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes) + rank;
-    s_last = atomicAdd(counter, 1u) == gridDim.x - 1;
-    if (s_last) *counter = 0;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  // four elements a thread; the threads that share them take every `many`-th block, then join in that order
-  const int quads = D >> 2, many = kNrThreads / quads, quad = threadIdx.x % quads, turn_of = threadIdx.x / quads;
-  for (int which = 0; which < 2; which++) {
-    const int b0 = which == 0 ? 0 : q_blocks, b1 = which == 0 ? q_blocks : (int)gridDim.x;
+  // join: runs of kBwdJoin blocks of one kind, then the kind's runs
+  const int k0 = is_q ? 0 : q_blocks, kind_blocks = is_q ? q_blocks : k_blocks;
+  const int quads = D >> 2, many = kBwdThreads / quads, quad = threadIdx.x % quads, turn_of = threadIdx.x / quads;
+  uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes) + rank * kBwdCounters;
+  int from = k0 + ((int)blockIdx.x - k0) / kBwdJoin * kBwdJoin, apart = 1;
+  int count = min(kBwdJoin, k0 + kind_blocks - from);
+  uint32_t* counter = counters + 2 + from / kBwdJoin + (is_q ? 0 : 1);  // runs of the two kinds do not share one
+  for (;;) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s_last = atomicAdd(counter, 1u) == (uint32_t)(count - 1);
+      if (s_last) *counter = 0;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    // four elements a thread; the threads that share them take every `many`-th partial, then join in that order
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (turn_of < many) {
 #pragma unroll 8
-      for (int b = b0 + turn_of; b < b1; b += many) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(parts + (int64_t)b * D + quad * 4));
+      for (int i = turn_of; i < count; i += many) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(parts + (int64_t)(from + i * apart) * D + quad * 4));
         s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
       }
     }
-    __syncthreads();
     sums[threadIdx.x][0] = s.x;
     sums[threadIdx.x][1] = s.y;
     sums[threadIdx.x][2] = s.z;
     sums[threadIdx.x][3] = s.w;
     __syncthreads();
-    float* out = which == 0 ? a.dq_weight[rank] : a.dk_weight[rank];
-    for (int e = threadIdx.x; e < D; e += kNrThreads) {
+    const bool whole = apart > 1 || count == kind_blocks;
+    float* out = whole ? (is_q ? a.dq_weight[rank] : a.dk_weight[rank]) : parts + (int64_t)from * D;
+    for (int e = threadIdx.x; e < D; e += kBwdThreads) {
       float t = 0.f;
-      for (int k = 0; k < many; k++) t += sums[k * quads + (e >> 2)][e & 3];
+      for (int k = 0; k < many && k < count; k++) t += sums[k * quads + (e >> 2)][e & 3];
       out[e] = t;
     }
+    if (whole) return;
+    from = k0;
+    apart = kBwdJoin;
+    count = (kind_blocks + kBwdJoin - 1) / kBwdJoin;
+    counter = counters + (is_q ? 0 : 1);
   }
 }
 
@@ -415,7 +501,7 @@ const void* backward_of(int lanes, bool inter) {
 }  // namespace
 
 int64_t norm_rope_scratch_bytes(int nranks, int head_dim) {
-  return (kNormRopeBwdBlocks + 2ll * nranks) * head_dim * (int64_t)sizeof(float);
+  return (kNormRopeBwdBlocks + 3ll * nranks) * head_dim * (int64_t)sizeof(float);
 }
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
@@ -440,27 +526,27 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, cudaStream_t stream) {
-  const int lanes = lanes_of(a.head_dim), groups = kNrThreads / lanes;
-  // blocks of the two kinds in proportion to their bytes: x, dy and dx of a query or key head, dv twice
+  const int lanes = lanes_of(a.head_dim), groups = kBwdThreads / lanes;
   const void* fn = a.dtype == kF32 ? backward_of<float>(lanes, a.interleaved != 0)
                                    : backward_of<uint16_t>(lanes, a.interleaved != 0);
   int device = 0, sms = 0, per_sm = 0;
   cudaError_t e = current_device_sms(&device, &sms);
   if (e != cudaSuccess) return e;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kNrThreads, 0);
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kBwdThreads, 0);
   if (e != cudaSuccess) return e;
+  // one resident wave, shared out in proportion to the kinds' bytes: x, dy and dx of query and key heads, dv twice
   const int64_t most = imin(kNormRopeBwdBlocks, (int64_t)sms * per_sm) / a.nranks;
-  const int64_t q_items = (int64_t)a.tokens * div_up(a.q_heads, kBwdStrip);
-  const int64_t kv_items = (int64_t)a.tokens * div_up(a.kv_heads, kBwdStrip);
-  const int64_t share = most * 3 * a.q_heads / (3 * a.q_heads + 5 * a.kv_heads);
-  int q_blocks = (int)imax(1, imin(div_up(q_items, groups), share));
-  const int kv_blocks = (int)imax(1, imin(div_up(kv_items, groups), most - share));
-  dim3 grid((unsigned)(q_blocks + kv_blocks), (unsigned)a.nranks);
+  const int64_t q = 3ll * a.q_heads, k = 3ll * a.kv_heads, v = 2ll * a.kv_heads;
+  const int64_t needed = div_up(a.tokens, groups);
+  auto blocks_of = [&](int64_t weight) { return (int)imax(1, imin(needed, most * weight / (q + k + v))); };
+  int q_blocks = blocks_of(q), k_blocks = blocks_of(k);
+  const int v_blocks = blocks_of(v);
+  dim3 grid((unsigned)(q_blocks + k_blocks + v_blocks), (unsigned)a.nranks);
   if (trace_on())
     std::fprintf(stderr, "rar trace: qk_norm_rope_backward nranks=%d tokens=%d heads=%d/%d dim=%d rot=%d grid=%ux%u\n",
                  a.nranks, a.tokens, a.q_heads, a.kv_heads, a.head_dim, a.rot, grid.x, grid.y);
-  void* params[] = {const_cast<NormRopeBwdArgs*>(&a), &q_blocks};
-  return cudaLaunchKernel(fn, grid, dim3(kNrThreads), params, 0, stream);
+  void* params[] = {const_cast<NormRopeBwdArgs*>(&a), &q_blocks, &k_blocks};
+  return cudaLaunchKernel(fn, grid, dim3(kBwdThreads), params, 0, stream);
 }
 
 }  // namespace rar

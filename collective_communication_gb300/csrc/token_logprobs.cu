@@ -52,6 +52,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
+__device__ __forceinline__ float sum_of(F2 a) {
+  const float2 p = unpack(a);
+  return p.x + p.y;
+}
+
 // A value's bits made monotonic, a NaN above all.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v);
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
     const uint32_t row = at / per_row, row_first = row * per_row;
     const int t0 = (int)(at - row_first), t1 = (int)(min(end, row_first + per_row) - row_first);
     float m = -INFINITY;                           // near the largest of the lane's words
-    float2 s2 = make_float2(0.f, 0.f), w2 = s2;  // its sums in two halves
+    F2 s2 = f2(0.f, 0.f), w2 = s2;            // its sums in two halves
     TopList tops;
 
     for (int t = t0; t < t1;) {
@@ -211,30 +216,31 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         if (best > m + 8.f) {
           if (m != -INFINITY) {
             const float d = (m - best) * kLog2e, e = exp2_fast(d);
-            w2 = e > 0.f ? make_float2(e * (w2.x + d * s2.x), e * (w2.y + d * s2.y)) : make_float2(0.f, 0.f);
-            s2 = make_float2(s2.x * e, s2.y * e);
+            w2 = e > 0.f ? mul2(f2(e, e), fma2(f2(d, d), s2, w2)) : f2(0.f, 0.f);
+            s2 = mul2(s2, f2(e, e));
           }
           m = best;
         }
-        const float2 off = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const F2 off = f2(neg, neg), log2e = f2(kLog2e, kLog2e);
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
           float v[8];
           u[i].widen(v);
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            float2 t2 = mul2(add2(make_float2(v[j], v[j + 1]), off), make_float2(kLog2e, kLog2e));
-            t2 = make_float2(max_nan(t2.x, kFloorT), max_nan(t2.y, kFloorT));
-            const float2 e = make_float2(exp2_fast(t2.x), exp2_fast(t2.y));
+            float2 t = unpack(mul2(add2(f2(v[j], v[j + 1]), off), log2e));
+            t = make_float2(max_nan(t.x, kFloorT), max_nan(t.y, kFloorT));
+            const F2 e = f2(exp2_fast(t.x), exp2_fast(t.y));
             s2 = add2(s2, e);
-            w2 = fma2(e, t2, w2);
+            w2 = fma2(e, f2(t.x, t.y), w2);
           }
         }
         if constexpr (TOP) {
           if (begins && p == lane) tops.start(__shfl_sync(~0u, sort32(best), a.top - 1));
           // lanes with a word that may matter (a NaN, which the maxima leave out, shows in the sum): the warp looks at
           // their words together, a word to a lane
-          uint32_t lanes = __ballot_sync(~0u, !(best < tops.bound_value) || s2.x != s2.x || s2.y != s2.y);
+          uint32_t lanes = __ballot_sync(~0u, !(best < tops.bound_value) || sum_of(s2) != sum_of(s2));
           if (lanes != 0) {
             T(*words)[32][8] = s_words[threadIdx.x >> 5];
 #pragma unroll
@@ -256,14 +262,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         const float v = mine ? to_float(body[e]) : -INFINITY;
         Stat one = {v, v == -INFINITY ? 0.f : 1.f, 0.f};
         if (v != v) one = {-INFINITY, v, 0.f};
-        one = join(Stat{m, s2.x + s2.y, w2.x + w2.y}, one);
+        one = join(Stat{m, sum_of(s2), sum_of(w2)}, one);
         m = one.m;
-        s2 = make_float2(one.s, 0.f);
-        w2 = make_float2(one.w, 0.f);
+        s2 = f2(one.s, 0.f);
+        w2 = f2(one.w, 0.f);
         if constexpr (TOP) tops.offer(mine ? top_key(v, word + e) : 0, a.top);
       }
     }
-    Stat st = warp_join(Stat{m, s2.x + s2.y, w2.x + w2.y});
+    Stat st = warp_join(Stat{m, sum_of(s2), sum_of(w2)});
     if (!op_ready(a.ws, magic)) return;
 
     bool whole = t0 == 0 && t1 == (int)per_row;  // this warp has the row's result
