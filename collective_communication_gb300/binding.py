@@ -400,43 +400,38 @@ def _refuse(what):
     raise RarError(Status.ERR_ARG, what)
 
 
-_PACK = [struct.Struct(f"{n}Q").pack for n in range(33)]  # nranks pointers, or 64-bit counts, as a C array
+_PACKS = {n: struct.Struct(f"{n}Q").pack for n in range(1, 33)}
 
 
 def _pack(values):
+    """nranks pointers, or 64-bit counts, as a C array."""
     n = len(values)
-    return _PACK[n](*values) if n <= 32 else struct.pack(f"{n}Q", *values)
+    return _PACKS[n](*values) if n in _PACKS else struct.pack(f"{n}Q", *values)
 
 
 def _ranked(x, name, dims):
-    """A per-rank argument as (C array of the ranks' pointers, nranks, shape of
-    a rank's tensor, its row stride, dtype); the dimensions after a row's are
-    dense."""
+    """A per-rank argument as (C array of the ranks' pointers, shape with the
+    rank first, row stride of a rank's tensor, dtype); the dimensions after a
+    row's are dense."""
     if type(x) is list or type(x) is tuple:
-        first = x[0]
-        shape, strides, dtype = first.shape, first.stride(), first.dtype
-        for t in x:
-            if t.shape != shape or t.stride() != strides or t.dtype is not dtype or not t.is_cuda:
-                _refuse(f"{name}: the ranks' tensors are alike and in device memory")
-        n, ptrs = len(x), _pack([t.data_ptr() for t in x])
-    else:
-        full = x.shape
-        n, shape, dtype = full[0], full[1:], x.dtype
-        if not x.is_cuda or n == 0:
-            _refuse(f"{name}: a tensor in device memory for each rank")
-        base = x.data_ptr()
-        if x.is_contiguous():
-            if len(shape) != dims:
-                _refuse(f"{name}: {dims} dimensions a rank")
-            step = x.nbytes // n
-            ptrs = _pack(range(base, base + n * step, step) if step else [base] * n)
-            width = 1
-            for d in shape[1:]:
-                width *= d
-            return ptrs, n, shape, width, dtype
-        strides = x.stride()
-        step = strides[0] * x.element_size()
-        ptrs, strides = _pack([base + r * step for r in range(n)]), strides[1:]
+        return _ranked_list(x, name, dims)
+    full = x.shape
+    n = full[0]
+    if len(full) != dims + 1 or not x.is_cuda or n == 0:
+        _refuse(f"{name}: {dims} dimensions a rank, in device memory")
+    if not x.is_contiguous():
+        return _ranked_list(x.unbind(0), name, dims)
+    base, step = x.data_ptr(), x.nbytes // n
+    width = 1 if dims == 1 else full[2] if dims == 2 else full[2] * full[3] if dims == 3 else full[2] * full[3] * full[4]
+    return (_pack(range(base, base + n * step, step)) if step else bytes(8 * n)), full, width, x.dtype
+
+
+def _ranked_list(x, name, dims):
+    first = x[0]
+    shape, strides, dtype = first.shape, first.stride(), first.dtype
+    for t in x:
+        if t.shape != shape or t.stride() != strides or t.dtype is not dtype or not t.is_cuda:
+            _refuse(f"{name}: the ranks' tensors are alike and in device memory")
     if len(shape) != dims:
         _refuse(f"{name}: {dims} dimensions a rank")
     width = 1
@@ -444,16 +439,16 @@ def _ranked(x, name, dims):
         if shape[i] != 1 and strides[i] != width:
             _refuse(f"{name}: dense after its first dimension")
         width *= shape[i]
-    return ptrs, n, shape, strides[0] if shape[0] > 1 else width, dtype
+    return _pack([t.data_ptr() for t in x]), (len(x), *shape), strides[0] if shape[0] > 1 else width, dtype
 
 
 def _ranked_dense(x, name, dims):
     """_ranked of tensors without gaps."""
     r = _ranked(x, name, dims)
     width = 1
-    for d in r[2][1:]:
+    for d in r[1][2:]:
         width *= d
-    if r[3] != width:
+    if r[2] != width:
         _refuse(f"{name}: contiguous")
     return r
 
@@ -505,19 +500,18 @@ def page_tables(lens, new_tokens, free_pages, free_count, block_table, page_size
 def _rope_call(qkv, q_weight, k_weight, cos_sin, positions, q, kv_heads):
     """What the forms of the norm and rotation share: qkv [tokens, (q + 2 kv
     heads) * head_dim] against queries [tokens, q_heads, head_dim]."""
-    tokens, q_heads, dim = q[2]
-    dtype = qkv[4]
-    if qkv[1] != q[1] or q[4] is not dtype or qkv[2] != (tokens, (q_heads + 2 * kv_heads) * dim):
+    n, tokens, q_heads, dim = q[1]
+    dtype = qkv[3]
+    if q[3] is not dtype or qkv[1] != (n, tokens, (q_heads + 2 * kv_heads) * dim):
         _refuse("qkv: [tokens, (q_heads + 2 kv_heads) head_dim], queries [tokens, q_heads, head_dim], of one dtype")
-    if q_weight.dtype is not dtype or k_weight.dtype is not dtype or q_weight.shape != (dim,) \
-            or k_weight.shape != (dim,) or not (q_weight.is_cuda and k_weight.is_cuda and q_weight.is_contiguous()
-                                                and k_weight.is_contiguous()):
-        _refuse("weights: head_dim contiguous elements of qkv's dtype in device memory")
-    table = cos_sin.shape
-    if cos_sin.dtype is not _FLOAT32 or len(table) != 2 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
+    for w in (q_weight, k_weight):
+        if w.dtype is not dtype or w.numel() != dim or not w.is_contiguous() or not w.is_cuda:
+            _refuse("weights: head_dim contiguous elements of qkv's dtype in device memory")
+    max_pos, rot = cos_sin.shape
+    if cos_sin.dtype is not _FLOAT32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
         _refuse("cos_sin: contiguous float32 [max_pos, rot_dim] in device memory")
-    return (qkv[0], q[1], tokens, qkv[3], q_weight.data_ptr(), k_weight.data_ptr(), cos_sin.data_ptr(), table[0],
-            table[1]), _ints(positions, "positions", tokens), (q_heads, kv_heads, dim, _op_dtype(dtype))
+    return (qkv[0], n, tokens, qkv[2], q_weight.data_ptr(), k_weight.data_ptr(), cos_sin.data_ptr(), max_pos, rot), \
+        _ints(positions, "positions", tokens), (q_heads, kv_heads, dim, _op_dtype(dtype))
 
 
 def qk_norm_rope(qkv, q_weight, k_weight, cos_sin, positions, q_out, k_out, workspace: OpWorkspace, eps: float = 1e-6,
@@ -526,10 +520,10 @@ def qk_norm_rope(qkv, q_weight, k_weight, cos_sin, positions, q_out, k_out, work
     [tokens, q_heads, head_dim] and k_out [tokens, kv_heads, head_dim] a rank."""
     lib = _ops or _op_setup()
     q, k = _ranked(q_out, "q_out", 3), _ranked(k_out, "k_out", 3)
-    head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, k[2][1])
-    if k[1] != q[1] or k[4] is not q[4] or k[2] != (q[2][0], heads[1], heads[2]):
+    head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, k[1][2])
+    if k[3] is not q[3] or k[1] != (*q[1][:2], heads[1], heads[2]):
         _refuse("k_out: [tokens, kv_heads, head_dim]")
-    st = lib.rar_qk_norm_rope(*head, interleaved, pos, *heads, eps, q[0], q[3], k[0], k[3], workspace.ptr,
+    st = lib.rar_qk_norm_rope(*head, interleaved, pos, *heads, eps, q[0], q[2], k[0], k[2], workspace.ptr,
                               workspace.nbytes, _op_stream(stream))
     if st:
         _check(st, "rar_qk_norm_rope")
@@ -542,11 +536,11 @@ def qk_norm_rope_cached(qkv, q_weight, k_weight, cos_sin, positions, slots, q_ou
     lib = _ops or _op_setup()
     q = _ranked(q_out, "q_out", 3)
     k, v = _ranked_dense(k_cache, "k_cache", 4), _ranked_dense(v_cache, "v_cache", 4)
-    pages, kv_heads, page, dim = k[2]
+    n, pages, kv_heads, page, dim = k[1]
     head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, kv_heads)
-    if k[1] != q[1] or v[1] != q[1] or k[4] is not q[4] or v[4] is not q[4] or v[2] != k[2] or dim != heads[2]:
+    if n != head[1] or v[1] != k[1] or k[3] is not q[3] or v[3] is not q[3] or dim != heads[2]:
         _refuse("k_cache, v_cache: [num_pages, kv_heads, page_size, head_dim]")
-    st = lib.rar_qk_norm_rope_cached(*head, interleaved, pos, _ints(slots, "slots", q[2][0]), *heads, eps, q[0], q[3],
+    st = lib.rar_qk_norm_rope_cached(*head, interleaved, pos, _ints(slots, "slots", head[2]), *heads, eps, q[0], q[2],
                                      k[0], v[0], pages, page, workspace.ptr, workspace.nbytes, _op_stream(stream))
     if st:
         _check(st, "rar_qk_norm_rope_cached")
@@ -560,18 +554,17 @@ def qk_norm_rope_backward(qkv, q_weight, k_weight, cos_sin, positions, dq, dk, d
     lib = _ops or _op_setup()
     q, k, v = _ranked(dq, "dq", 3), _ranked(dk, "dk", 3), _ranked(dv, "dv", 3)
     x, d = _ranked(qkv, "qkv", 2), _ranked(dqkv, "dqkv", 2)
-    head, pos, heads = _rope_call(x, q_weight, k_weight, cos_sin, positions, q, k[2][1])
-    if k[1] != q[1] or v[1] != q[1] or k[4] is not q[4] or v[4] is not q[4] or v[2] != k[2] \
-            or k[2] != (q[2][0], heads[1], heads[2]):
+    head, pos, heads = _rope_call(x, q_weight, k_weight, cos_sin, positions, q, k[1][2])
+    if k[3] is not q[3] or v[3] is not q[3] or v[1] != k[1] or k[1] != (*q[1][:2], heads[1], heads[2]):
         _refuse("dk, dv: [tokens, kv_heads, head_dim]")
-    if d[1] != x[1] or d[2] != x[2] or d[4] is not x[4]:
+    if d[1] != x[1] or d[3] is not x[3]:
         _refuse("dqkv: as qkv")
     wq, wk = _ranked(dq_weight, "dq_weight", 1), _ranked(dk_weight, "dk_weight", 1)
     for w in (wq, wk):
-        if w[1] != x[1] or w[2] != (heads[2],) or w[4] is not _FLOAT32 or w[3] != 1:
+        if w[1] != (head[1], heads[2]) or w[3] is not _FLOAT32 or w[2] != 1:
             _refuse("dq_weight, dk_weight: float32 [head_dim]")
-    st = lib.rar_qk_norm_rope_backward(*head, interleaved, pos, *heads, eps, q[0], q[3], k[0], k[3], v[0], v[3], d[0],
-                                       d[3], wq[0], wk[0], workspace.ptr, workspace.nbytes, _op_stream(stream))
+    st = lib.rar_qk_norm_rope_backward(*head, interleaved, pos, *heads, eps, q[0], q[2], k[0], k[2], v[0], v[2], d[0],
+                                       d[2], wq[0], wk[0], workspace.ptr, workspace.nbytes, _op_stream(stream))
     if st:
         _check(st, "rar_qk_norm_rope_backward")
 
@@ -585,22 +578,22 @@ def decode_attention(q, k_cache, v_cache, block_table, lens, out, lse, workspace
     lib = _ops or _op_setup()
     x, o = _ranked(q, "q", 3), _ranked(out, "out", 3)
     k, v = _ranked_dense(k_cache, "k_cache", 4), _ranked_dense(v_cache, "v_cache", 4)
-    n, dtype = x[1], x[4]
-    batch, q_heads, dim = x[2]
-    pages, kv_heads, page, kdim = k[2]
-    if k[1] != n or v[1] != n or o[1] != n or k[4] is not dtype or v[4] is not dtype or o[4] is not dtype \
-            or v[2] != k[2] or o[2] != x[2] or kdim != dim:
+    dtype = x[3]
+    n, batch, q_heads, dim = x[1]
+    kn, pages, kv_heads, page, kdim = k[1]
+    if kn != n or kdim != dim or v[1] != k[1] or o[1] != x[1] or k[3] is not dtype or v[3] is not dtype \
+            or o[3] is not dtype:
         _refuse("q, out: [batch, q_heads, head_dim]; caches: [num_pages, kv_heads, page_size, head_dim]")
     table, stride, blocks = _table(block_table, batch)
     lse_p = None
     if lse is not None:
         e = _ranked_dense(lse, "lse", 2)
-        if e[1] != n or e[2] != (batch, q_heads) or e[4] is not _FLOAT32:
+        if e[1] != (n, batch, q_heads) or e[3] is not _FLOAT32:
             _refuse("lse: float32 [batch, q_heads]")
         lse_p = e[0]
     st = lib.rar_decode_attention(
-        x[0], x[3], k[0], v[0], n, batch, q_heads, kv_heads, dim, _op_dtype(dtype), pages, page, table, stride, blocks,
-        _ints(lens, "lens", batch), dim ** -0.5 if scale is None else scale, o[0], o[3], lse_p, workspace.ptr,
+        x[0], x[2], k[0], v[0], n, batch, q_heads, kv_heads, dim, _op_dtype(dtype), pages, page, table, stride, blocks,
+        _ints(lens, "lens", batch), dim ** -0.5 if scale is None else scale, o[0], o[2], lse_p, workspace.ptr,
         workspace.nbytes, _op_stream(stream))
     if st:
         _check(st, "rar_decode_attention")
@@ -609,14 +602,14 @@ def decode_attention(q, k_cache, v_cache, block_table, lens, out, lse, workspace
 def _shards(x, name):
     """(pointers, vocabulary of each shard, row strides, nranks, rows, dtype); shards may differ in width."""
     if type(x) is not list and type(x) is not tuple:
-        p, n, shape, stride, dtype = _ranked(x, name, 2)
-        return p, _pack([shape[1]] * n), _pack([stride] * n), n, shape[0], dtype
-    ones = [_ranked((t,), name, 2) for t in x]
-    rows, dtype = ones[0][2][0], ones[0][4]
+        p, (n, rows, width), stride, dtype = _ranked(x, name, 2)
+        return p, _pack((width,) * n), _pack((stride,) * n), n, rows, dtype
+    ones = [_ranked_list((t,), name, 2) for t in x]
+    rows, dtype = ones[0][1][1], ones[0][3]
     for o in ones:
-        if o[2][0] != rows or o[4] is not dtype:
+        if o[1][1] != rows or o[3] is not dtype:
             _refuse(f"{name}: [rows, vocabulary of the shard], of one dtype")
-    return (b"".join([o[0] for o in ones]), _pack([o[2][1] for o in ones]), _pack([o[3] for o in ones]), len(ones), rows,
+    return (b"".join([o[0] for o in ones]), _pack([o[1][2] for o in ones]), _pack([o[2] for o in ones]), len(ones), rows,
             dtype)
 
 

@@ -719,12 +719,10 @@ int64_t decode_attention_scratch_bytes(int, int, int q_heads, int kv_heads, int 
 cudaError_t launch_decode_attention(const DecodeArgs& a, cudaStream_t stream) {
   const int group = a.q_heads / a.kv_heads;
   const DecodeKernel k = a.dtype == kF32 ? kernel_for<float>(a.head_dim, group) : kernel_for<uint16_t>(a.head_dim, group);
-  int device = 0, sms = 0, per_sm = 0;
-  cudaError_t e = current_device_sms(&device, &sms);
+  int resident = 0;
+  const cudaError_t e = resident_blocks(k.fn, kDaThreads, &resident);
   if (e != cudaSuccess) return e;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, kDaThreads, 0);
-  if (e != cudaSuccess) return e;
-  const int64_t grid = imin((int64_t)sms * per_sm, kDaMaxBlocks);
+  const int64_t grid = imin((int64_t)resident, kDaMaxBlocks);
   if (trace_on())
     std::fprintf(stderr, "rar trace: decode_attention nranks=%d batch=%d heads=%d/%d dim=%d grid=%lld threads=%d\n",
                  a.nranks, a.batch, a.q_heads, a.kv_heads, a.head_dim, (long long)grid, kDaThreads);

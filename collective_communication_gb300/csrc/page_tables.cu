@@ -7,12 +7,17 @@
 // Token j of r sits at position len + j and slot table[r][pos / P] * P + pos % P.
 //
 // One launch without a second pass: every block computes the two prefix sums
-// over all requests itself, kChunk requests at a time (8 bytes a request, from
-// L2), and writes the part of the outputs that is its own: the tokens
-// [b * kTokens, (b + 1) * kTokens), and the requests of every gridDim-th chunk.
-// A token's page that is new in this call is read from the free list, not from
-// the table that another block may still be writing. What bounds it is the
-// launch and the chain of dependent loads; the bytes are a few MB at most.
+// over all requests itself, a chunk of 4 requests a thread at a time (8 bytes a
+// request, from L2), and writes its share of the outputs: a run of the tokens,
+// and of every chunk's requests and new pages. (One block that wrote all
+// requests' new pages, a dependent load and store each, took 23 us for 4096
+// requests and 16000 pages; shared out it is 9.) A token's page that is new in
+// this call is read from the free list, not from the table that another block
+// may still be writing. What bounds it is the launch and the chain of dependent
+// loads; the bytes are a few MB at most. Blocks of 256 threads for up to 1024
+// requests, one chunk (3.4 us against 5.4 for 8 requests, where a larger block's
+// start and barriers are what there is to save), of 1024 above (one pass over
+// 4096 requests instead of four).
 #include <cstdio>
 
 #include "op_common.cuh"
@@ -20,10 +25,7 @@
 
 namespace rar {
 
-constexpr int kPtThreads = 1024;
-constexpr int kPtPer = 4;                     // consecutive requests of a thread
-constexpr int kPtChunk = kPtThreads * kPtPer;  // requests of a chunk
-constexpr int kPtTokens = 2048;               // tokens of a block
+constexpr int kPtPer = 4;  // consecutive requests of a thread
 
 namespace {
 
@@ -32,6 +34,7 @@ struct Sums {
 };
 
 // Exclusive prefix sum over the block's threads; `total` gets the sum of all.
+template <int THREADS>
 __device__ __forceinline__ Sums block_exclusive(Sums mine, Sums* warp_sums, Sums* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Sums s = mine;
@@ -43,7 +46,7 @@ __device__ __forceinline__ Sums block_exclusive(Sums mine, Sums* warp_sums, Sums
   __syncthreads();  // the last call's sums have been read
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  Sums w = warp_sums[lane];  // kPtThreads / 32 == 32 warps
+  Sums w = lane < THREADS / 32 ? warp_sums[lane] : Sums{0, 0};
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t a = __shfl_up_sync(~0u, w.need, d), b = __shfl_up_sync(~0u, w.tokens, d);
@@ -62,26 +65,29 @@ __device__ __forceinline__ int32_t clamp_i32(int64_t v) { return (int32_t)(v < I
 
 }  // namespace
 
-__global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const __grid_constant__ PageTablesArgs a) {
-  __shared__ Sums warp_sums[32];
-  __shared__ int32_t s_start[kPtChunk];  // first token of the request, relative to the chunk's
-  __shared__ int32_t s_off[kPtChunk];    // first page handed out to it; -1: the request gets nothing
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) page_tables_kernel(const __grid_constant__ PageTablesArgs a) {
+  constexpr int kChunk = THREADS * kPtPer, kTokens = 2 * THREADS;  // requests of a chunk, tokens of a block
+  __shared__ Sums warp_sums[THREADS / 32];
+  // of each request of the chunk, relative to the chunk: its first token; its first new page, with the bits
+  // inverted (so below zero) if the request gets nothing
+  __shared__ int32_t s_start[kChunk], s_off[kChunk];
   __shared__ int s_taken;
   const uint32_t magic = op_magic(a.ws);
   const int tid = threadIdx.x;
   const int P = 1 << a.page_shift;
   const int64_t width = (int64_t)a.max_blocks << a.page_shift;  // tokens that a table row can address
-  const int64_t t0 = (int64_t)blockIdx.x * kPtTokens;
-  const int64_t t1 = imin(t0 + kPtTokens, a.max_tokens);
+  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  const int64_t t1 = imin(t0 + kTokens, a.max_tokens);
   int count = *a.free_count;
   bool bad = count < 0 || count > a.num_free;
   count = count < 0 ? 0 : count > a.num_free ? a.num_free : count;
   if (!op_ready(a.ws, magic)) return;
   if (tid == 0) s_taken = 0;
   int64_t need0 = 0, tok0 = 0;  // sums over the chunks before this one
-  const int chunks = (int)div_up(a.requests, kPtChunk);
+  const int chunks = (int)div_up(a.requests, kChunk);
   for (int c = 0; c < chunks; c++) {
-    const int base = c * kPtChunk;
+    const int base = c * kChunk;
     int len[kPtPer], add[kPtPer], need[kPtPer];
     bool ok[kPtPer];
     Sums mine = {0, 0};
@@ -101,8 +107,10 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const __grid_co
       mine.tokens += add[i];
     }
     Sums total;
-    Sums at = block_exclusive(mine, warp_sums, &total);
-    const bool my_requests = c % (int)gridDim.x == (int)blockIdx.x;
+    Sums at = block_exclusive<THREADS>(mine, warp_sums, &total);
+    // the block's share of the chunk's requests
+    const int share = (kChunk + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int r0 = base + (int)blockIdx.x * share, r1 = min(min(r0 + share, base + kChunk), a.requests);
     int taken = 0;
 #pragma unroll
     for (int i = 0; i < kPtPer; i++) {
@@ -113,30 +121,39 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const __grid_co
       if (!served && add[i] > 0) bad = true;
       if (served && need[i] > 0) taken = (int)(off + need[i]);
       s_start[tid * kPtPer + i] = clamp_i32(at.tokens);
-      s_off[tid * kPtPer + i] = served ? (int)off : -1;
-      if (my_requests && r < a.requests) {
+      s_off[tid * kPtPer + i] = served ? clamp_i32(at.need) : ~clamp_i32(at.need);
+      if (r >= r0 && r < r1) {
         a.starts[r] = clamp_i32(start);
         a.lens_out[r] = served ? len[i] + add[i] : len[i];
-        if (served) {
-          const int have = (int)(((int64_t)len[i] + P - 1) >> a.page_shift);
-          for (int k = 0; k < need[i]; k++) {
-            const int page = a.free_pages[count - 1 - (off + k)];
-            const bool fine = page >= 0 && page < a.num_pages;
-            if (!fine) bad = true;
-            a.table[(int64_t)r * a.table_stride + have + k] = fine ? page : -1;
-          }
-        }
       }
       at.need += need[i];
       at.tokens += add[i];
     }
     if (taken > 0) atomicMax(&s_taken, taken);
     __syncthreads();
+    // The block's share of the chunk's new pages. The last request whose first page is not after p has page p.
+    auto first_page = [&](int i) { return s_off[i] < 0 ? ~s_off[i] : s_off[i]; };
+    const int64_t pages = imin(total.need, (int64_t)count - need0);  // those after it go to nobody
+    const int64_t p1 = pages * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t p = pages * blockIdx.x / gridDim.x + tid; p < p1; p += THREADS) {
+      int x = 0, y = kChunk;
+      while (y - x > 1) {
+        const int mid = (x + y) >> 1;
+        if (first_page(mid) <= p) x = mid; else y = mid;
+      }
+      const int r = base + x;
+      if (s_off[x] < 0) continue;
+      const int have = (int)(((int64_t)a.lens[r] + P - 1) >> a.page_shift);
+      const int page = a.free_pages[count - 1 - (need0 + p)];
+      const bool fine = page >= 0 && page < a.num_pages;
+      if (!fine) bad = true;
+      a.table[(int64_t)r * a.table_stride + have + (p - s_off[x])] = fine ? page : -1;
+    }
     // the block's tokens that belong to this chunk
     const int64_t lo = t0 > tok0 ? t0 : tok0, hi = imin(t1, tok0 + total.tokens);
-    for (int64_t t = lo + tid; t < hi; t += kPtThreads) {
+    for (int64_t t = lo + tid; t < hi; t += THREADS) {
       const int rel = (int)(t - tok0);
-      int x = 0, y = kPtChunk;  // the last request whose first token is not after t
+      int x = 0, y = kChunk;  // the last request whose first token is not after t
       while (y - x > 1) {
         const int mid = (x + y) >> 1;
         if (s_start[mid] <= rel) x = mid; else y = mid;
@@ -148,7 +165,7 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const __grid_co
         pos = len_r + (rel - s_start[x]);
         const int have = (int)(((int64_t)len_r + P - 1) >> a.page_shift), col = pos >> a.page_shift;
         const int page = col < have ? a.table[(int64_t)r * a.table_stride + col]
-                                    : a.free_pages[count - 1 - (s_off[x] + col - have)];
+                                    : a.free_pages[count - 1 - (need0 + s_off[x] + col - have)];
         if (page >= 0 && page < a.num_pages) slot = (page << a.page_shift) + (pos & (P - 1));
         else bad = true;
       }
@@ -159,7 +176,7 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const __grid_co
     tok0 += total.tokens;
     __syncthreads();  // s_start and s_off are written again
   }
-  for (int64_t t = (t0 > tok0 ? t0 : tok0) + tid; t < t1; t += kPtThreads) {
+  for (int64_t t = (t0 > tok0 ? t0 : tok0) + tid; t < t1; t += THREADS) {
     a.positions[t] = 0;
     a.slots[t] = -1;
   }
@@ -171,12 +188,13 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const __grid_co
 }
 
 cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream) {
-  int64_t grid = div_up(a.max_tokens, kPtTokens);
-  if (grid < 1) grid = 1;
+  const int threads = a.requests > 256 * kPtPer ? 1024 : 256;
+  const int64_t grid = imax(1, div_up(a.max_tokens, 2 * threads));
   if (trace_on())
     std::fprintf(stderr, "rar trace: page_tables requests=%d tokens=%d page=%d grid=%lld threads=%d\n", a.requests,
-                 a.max_tokens, 1 << a.page_shift, (long long)grid, kPtThreads);
-  page_tables_kernel<<<(unsigned)grid, kPtThreads, 0, stream>>>(a);
+                 a.max_tokens, 1 << a.page_shift, (long long)grid, threads);
+  if (threads == 1024) page_tables_kernel<1024><<<(unsigned)grid, 1024, 0, stream>>>(a);
+  else page_tables_kernel<256><<<(unsigned)grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

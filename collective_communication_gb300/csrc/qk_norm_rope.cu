@@ -529,13 +529,11 @@ cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, cudaStream_t stream) 
   const int lanes = lanes_of(a.head_dim), groups = kBwdThreads / lanes;
   const void* fn = a.dtype == kF32 ? backward_of<float>(lanes, a.interleaved != 0)
                                    : backward_of<uint16_t>(lanes, a.interleaved != 0);
-  int device = 0, sms = 0, per_sm = 0;
-  cudaError_t e = current_device_sms(&device, &sms);
-  if (e != cudaSuccess) return e;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kBwdThreads, 0);
+  int resident = 0;
+  const cudaError_t e = resident_blocks(fn, kBwdThreads, &resident);
   if (e != cudaSuccess) return e;
   // one resident wave, shared out in proportion to the kinds' bytes: x, dy and dx of query and key heads, dv twice
-  const int64_t most = imin(kNormRopeBwdBlocks, (int64_t)sms * per_sm) / a.nranks;
+  const int64_t most = imin(kNormRopeBwdBlocks, (int64_t)resident) / a.nranks;
   const int64_t q = 3ll * a.q_heads, k = 3ll * a.kv_heads, v = 2ll * a.kv_heads;
   const int64_t needed = div_up(a.tokens, groups);
   auto blocks_of = [&](int64_t weight) { return (int)imax(1, imin(needed, most * weight / (q + k + v))); };

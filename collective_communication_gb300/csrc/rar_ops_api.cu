@@ -2,6 +2,7 @@
 // in include/rar.h): argument checks, workspaces, launches. Nothing here waits
 // for the device; what only the device can see (lengths, positions, page and
 // slot numbers) is checked by the kernels and reported through the status word.
+#include <atomic>
 #include <cstring>
 
 #include "op_common.cuh"
@@ -147,7 +148,41 @@ rar_status check_norm_rope(const NormRopeCall& c, const void* const* qkv, Spans*
   return RAR_OK;
 }
 
+struct Residency {
+  std::atomic<const void*> fn;
+  std::atomic<int> device, blocks;
+};
+constexpr int kResidencies = 64;
+Residency g_residency[kResidencies];
+std::atomic<int> g_residencies{0};
+
 }  // namespace
+
+cudaError_t resident_blocks(const void* fn, int threads, int* blocks) {
+  int device = 0, sms = 0, per_sm = 0;
+  cudaError_t e = current_device_sms(&device, &sms);
+  if (e != cudaSuccess) return e;
+  const int known = g_residencies.load(std::memory_order_acquire);
+  for (int i = 0; i < known && i < kResidencies; i++) {
+    // an entry is complete once its kernel is set
+    if (g_residency[i].fn.load(std::memory_order_acquire) == fn && g_residency[i].device.load() == device) {
+      *blocks = g_residency[i].blocks.load();
+      return cudaSuccess;
+    }
+  }
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, 0);
+  if (e != cudaSuccess) return e;
+  *blocks = sms * per_sm;
+  const int slot = g_residencies.fetch_add(1);
+  if (slot < kResidencies) {
+    g_residency[slot].device.store(device);
+    g_residency[slot].blocks.store(*blocks);
+    g_residency[slot].fn.store(fn, std::memory_order_release);
+  } else {
+    g_residencies.store(kResidencies);
+  }
+  return cudaSuccess;
+}
 
 __global__ void init_op_header_kernel(char* ws) {
   OpHeader* h = reinterpret_cast<OpHeader*>(ws);

@@ -435,16 +435,14 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) 
                                                 : (const void*)token_logprobs_kernel<float, false>)
                                    : (a.top > 0 ? (const void*)token_logprobs_kernel<uint16_t, true>
                                                 : (const void*)token_logprobs_kernel<uint16_t, false>);
-  int device = 0, sms = 0, per_sm = 0;
-  cudaError_t e = current_device_sms(&device, &sms);
-  if (e != cudaSuccess) return e;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kLpThreads, 0);
+  int resident = 0;
+  const cudaError_t e = resident_blocks(fn, kLpThreads, &resident);
   if (e != cudaSuccess) return e;
   for (int r = 0; r < a.nranks; r++)
     a.first_tile[r + 1] = a.first_tile[r] + (int)div_up(a.first[r + 1] - a.first[r], kLpTile);
   const int64_t tiles = (int64_t)a.rows * a.first_tile[a.nranks];
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  int64_t grid = imin((int64_t)sms * per_sm, kLpMaxWorkers / kLpWarps);
+  int64_t grid = imin((int64_t)resident, kLpMaxWorkers / kLpWarps);
   a.workers = (uint32_t)imin(grid * kLpWarps, tiles);
   a.each = (uint32_t)(tiles / a.workers);
   a.more = (uint32_t)(tiles % a.workers);
