@@ -138,8 +138,8 @@ __device__ __forceinline__ void softmax_step(float (&s)[NT][4], Softmax<NT>& st,
     }
 }
 
-// What a tile needs per type. DP: head_dim rounded up to 64, 128 or 256 (the
-// chunks past head_dim are zero). Rows are cache rows, -1 for no token.
+// What a tile needs per type. DP: head_dim rounded up, to 64, 128, 192 or 256,
+// binary32 to 96 as well (the chunks past head_dim are zero). Rows are cache rows, -1 for no token.
 template <typename T, int DP, int NT>
 struct Tile;
 
@@ -279,7 +279,7 @@ struct Tile<float, DP, NT> {
   }
   __device__ __forceinline__ void scores(const char* smem, float (&s)[NT][4]) const {
     const uint4* q = reinterpret_cast<const uint4*>(smem) + (threadIdx.x & 31);
-    float x[NT][4] = {}, y[NT][4] = {};
+    float x[NT][4] = {}, y[NT][4] = {}, z[NT][4] = {};  // three chains of dependent instructions, not one
 #pragma unroll
     for (int i = 0; i < KC; i++) {
       const float* f0 = reinterpret_cast<const float*>(&k[0][i]);
@@ -296,14 +296,14 @@ struct Tile<float, DP, NT> {
           const uint4 b = q[(nt * 2 * KC + 2 * i + e) * 32];
           mma_tf32(x[nt], h[0], h[1], h[2], h[3], b.x, b.y);
           mma_tf32(y[nt], h[0], h[1], h[2], h[3], b.z, b.w);
-          mma_tf32(y[nt], l[0], l[1], l[2], l[3], b.x, b.y);
+          mma_tf32(z[nt], l[0], l[1], l[2], l[3], b.x, b.y);
         }
       }
     }
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) s[nt][j] = x[nt][j] + y[nt][j];
+      for (int j = 0; j < 4; j++) s[nt][j] = x[nt][j] + (y[nt][j] + z[nt][j]);
   }
   __device__ __forceinline__ void accumulate(const float (&p)[NT][4], float (&o)[MT][NT][4]) const {
     const int lane = threadIdx.x & 31, from = (lane & 3) * 4 + (lane >> 3);
@@ -394,9 +394,9 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
   auto tiles_of = [](int n) { return (n + kDaTile - 1) / kDaTile; };
   const int group = a.q_heads / a.kv_heads, qgroups = (group + Q - 1) / Q;
   const int per_request = a.nranks * a.kv_heads * qgroups;  // items of a request
-  int64_t total;
+  const int seg = (a.batch + kDaThreads - 1) / kDaThreads;
+  int64_t total, before_mine, tiles_mine;  // tiles of the requests before the thread's, and of its own
   {
-    const int seg = (a.batch + kDaThreads - 1) / kDaThreads;
     const int b0 = min(tid * seg, a.batch), b1 = min(b0 + seg, a.batch);
     int64_t mine = 0;
     for (int b = b0; b < b1; b++) {
@@ -420,21 +420,26 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
       all += s_sum[w];
     }
     total = all * per_request;
-    const int64_t blocks = total < gridDim.x ? total : gridDim.x;
-    if (blockIdx.x < blocks) {
-      const int64_t at = blockIdx.x * total / blocks;
-      const int64_t t = at / per_request;  // lies in the same request, tiles counted once per item
-      if (t >= before && t < before + mine) {
-        int b = b0;
-        for (int n; t >= before + (n = tiles_of(length(b))); b++) before += n;
-        s_part.first = before * per_request;
-        s_part.request = b;
-      }
+    before_mine = before;
+    tiles_mine = mine;
+  }
+  // the first `more` of the blocks with work have each + 1 tiles, the others each
+  const int64_t blocks = total < gridDim.x ? total : gridDim.x, each = blocks == 0 ? 0 : total / blocks;
+  const int64_t more = total - each * blocks;
+  auto start_of = [&](int64_t block) { return block * each + (block < more ? block : more); };
+  auto block_of = [&](int64_t tile) {
+    const int64_t split = more * (each + 1);
+    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
+  };
+  if (blockIdx.x < blocks) {
+    const int64_t t = start_of(blockIdx.x) / per_request;  // lies in the same request, tiles counted once per item
+    if (t >= before_mine && t < before_mine + tiles_mine) {
+      int b = tid * seg;
+      for (int n; t >= before_mine + (n = tiles_of(length(b))); b++) before_mine += n;
+      s_part.first = before_mine * per_request;
+      s_part.request = b;
     }
   }
-  const int64_t blocks = total < gridDim.x ? total : gridDim.x;  // those with at least one tile
-  auto start_of = [&](int64_t block) { return block * total / blocks; };
-  auto block_of = [&](int64_t tile) { return ((tile + 1) * blocks - 1) / total; };
 
   // Requests of length 0, shared out over the blocks.
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -703,8 +708,10 @@ template <typename T>
 DecodeKernel kernel_for(int head_dim, int group) {
   const bool wide = group > 8;
   if (head_dim <= 64) return wide ? kernel_of<T, 64, 2>() : kernel_of<T, 64, 1>();
+  // the padding that a rounder size brings costs binary32 instructions, of which it has few to spare
+  if (sizeof(T) == 4 && head_dim <= 96) return wide ? kernel_of<float, 96, 2>() : kernel_of<float, 96, 1>();
   if (head_dim <= 128) return wide && sizeof(T) == 2 ? kernel_of<T, 128, sizeof(T) == 2 ? 2 : 1>() : kernel_of<T, 128, 1>();
-  return kernel_of<T, 256, 1>();
+  return head_dim <= 192 ? kernel_of<T, 192, 1>() : kernel_of<T, 256, 1>();
 }
 
 }  // namespace
