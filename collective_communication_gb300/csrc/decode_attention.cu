@@ -34,10 +34,10 @@
 
 namespace rar {
 
-constexpr int kDaWarps = 4;
-constexpr int kDaThreads = 32 * kDaWarps;
+constexpr int kDaWarps = 4;        // warps that share a tile
 constexpr int kDaTile = 16 * kDaWarps;  // tokens of a tile
-constexpr int kDaMaxBlocks = 912;       // most blocks of a launch: partial results and counters for each
+constexpr int kDaMaxBlocks = 912;  // most blocks of a launch: partial results and counters for each
+constexpr int kDaJoin = 16;        // partial results that one block joins before it hands on
 static_assert(2 * kDaMaxBlocks <= kOpCounters, "two arrival counters per block");
 
 namespace {
@@ -150,8 +150,8 @@ struct Tile<uint16_t, DP, NT> {
   uint4 k[2][KC];  // tokens g, g + 8; elements 32 i + 8 c
   uint4 v[4][VC];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9; elements 64 h + 8 g
 
-  __device__ __forceinline__ static void load_queries(char* smem, const uint16_t* q, int queries, int D) {
-    for (int i = threadIdx.x; i < NT * KC * 32; i += kDaThreads) {
+  __device__ __forceinline__ static void load_queries(char* smem, const uint16_t* q, int queries, int D, int thread, int threads) {
+    for (int i = thread; i < NT * KC * 32; i += threads) {
       const int lane = i & 31, chunk = (i >> 5) % KC, nt = (i >> 5) / KC;
       const int row = nt * 8 + (lane >> 2), d = chunk * 32 + (lane & 3) * 8;
       uint4 u = make_uint4(0, 0, 0, 0);
@@ -240,8 +240,8 @@ struct Tile<float, DP, NT> {
   float4 k[2][KC];  // tokens g, g + 8; elements 16 i + 4 c
   float4 v[4][VC];  // tokens c, c + 4, c + 8, c + 12; elements 32 h + 4 g
 
-  __device__ __forceinline__ static void load_queries(char* smem, const float* q, int queries, int D) {
-    for (int i = threadIdx.x; i < NT * 2 * KC * 32; i += kDaThreads) {
+  __device__ __forceinline__ static void load_queries(char* smem, const float* q, int queries, int D, int thread, int threads) {
+    for (int i = thread; i < NT * 2 * KC * 32; i += threads) {
       const int lane = i & 31, step = (i >> 5) % (2 * KC), nt = (i >> 5) / (2 * KC);
       const int row = nt * 8 + (lane >> 2), d = (step >> 1) * 16 + (lane & 3) * 4 + (step & 1) * 2;
       uint4 u = make_uint4(0, 0, 0, 0);
@@ -345,10 +345,6 @@ struct Tile<float, DP, NT> {
   __device__ __forceinline__ static int dim_of(int mt, int g) { return (mt >> 1) * 32 + g * 4 + (mt & 1) * 2; }
 };
 
-// A partial result of a block: 8 NT queries by DP values, then their m and l.
-template <int DP, int NT>
-__host__ __device__ constexpr int partial_floats() { return NT * 8 * (DP + 2); }
-
 }  // namespace
 
 // Whether K and V of a tile (DP elements of T, 16 tokens a warp) fit the
@@ -356,10 +352,8 @@ __host__ __device__ constexpr int partial_floats() { return NT * 8 * (DP + 2); }
 template <typename T, int DP>
 constexpr bool kDaAhead = DP * sizeof(T) <= 512;
 
-constexpr int kDaJoin = 16;  // partial results that one block joins before it hands on
-
-// Where the walk over the tiles stands: kept in shared memory so that the loop
-// over tiles has the registers.
+// Where a block's walk over the tiles stands: kept in shared memory so that the
+// loop over tiles has the registers.
 struct Part {
   int64_t first;       // tiles before the request's, all items
   int64_t item_first;  // first tile of the item
@@ -367,20 +361,61 @@ struct Part {
   int rank, kvh, q0, queries;
 };
 
-template <typename T, int DP, int NT>
-__global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __grid_constant__ DecodeArgs a) {
+// The shapes of a kernel. Four warps take 16 tokens of a tile each, H times for
+// H groups of 8 NT query heads that read the same tiles at the same time (the
+// second from L2).
+template <typename T, int DP_, int NT, int H>
+struct Shape {
+  using Type = T;
+  static constexpr int DP = DP_;
   using Tl = Tile<T, DP, NT>;
-  constexpr int MT = Tl::MT, Q = NT * 8, kRow = DP + 4;
-  constexpr int kMergeBytes = kDaWarps * Q * kRow * 4;
-  constexpr int kMostParts = kDaMaxBlocks / kDaJoin + 1;
-  __shared__ __align__(16) char s_buf[kMergeBytes > Tl::kQueryBytes ? kMergeBytes : Tl::kQueryBytes];
-  __shared__ float s_m[kDaWarps][Q], s_l[kDaWarps][Q];
-  __shared__ float s_w[kMostParts][Q], s_pl[kMostParts][Q], s_top[Q], s_sum_l[Q];
-  __shared__ int64_t s_sum[kDaWarps];
-  __shared__ Part s_part;
-  __shared__ bool s_last;
+  static constexpr int kThreads = 32 * kDaWarps * H;
+  static constexpr int Q = NT * 8 * H;           // query heads of an item
+  static constexpr int kRow = DP + 4;
+  static constexpr int kPartial = Q * (DP + 2);  // floats of a partial result: DP values a query, m, l
+  static constexpr int kMostParts = kDaMaxBlocks / kDaJoin + 1;
+  static constexpr int kMergeBytes = kDaWarps * Q * kRow * 4, kQueryBytes = H * Tl::kQueryBytes;
+  struct Shared {
+    alignas(16) char buf[kMergeBytes > kQueryBytes ? kMergeBytes : kQueryBytes];
+    float m[kDaWarps][Q], l[kDaWarps][Q];
+    float weight[kMostParts][Q], sum[kMostParts][Q], top[Q], total[Q];
+    int64_t tiles[kDaWarps * H];
+    Part part;
+    int last;
+  };
+};
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+// Where an item's results go.
+template <typename T>
+struct Output {
+  T* out;
+  float* lse;  // null: not wanted
+  // four values of a query head, not yet divided by the sum l of the weights 2^(s - m)
+  __device__ __forceinline__ void write(int q, int d, int D, float4 x, float m, float l) const {
+    const float f = l == 0.f ? 0.f : 1.f / l;  // no token with a weight: 0
+    store4(out + (int64_t)q * D + d, x.x * f, x.y * f, x.z * f, x.w * f);
+    if (d == 0 && lse != nullptr) lse[q] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+};
+template <typename T>
+__device__ __forceinline__ Output<T> output_of(const DecodeArgs& a, const Part& p) {
+  Output<T> o;
+  o.out = reinterpret_cast<T*>(a.out[p.rank]) + (int64_t)p.request * a.out_stride + (int64_t)p.q0 * a.head_dim;
+  o.lse = a.lse[p.rank] == nullptr ? nullptr : a.lse[p.rank] + (int64_t)p.request * a.q_heads + p.q0;
+  return o;
+}
+
+template <typename T, int DP, int NT, int H>
+__global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attention_kernel(
+    const __grid_constant__ DecodeArgs a) {
+  using S = Shape<T, DP, NT, H>;
+  using Tl = Tile<T, DP, NT>;
+  constexpr int MT = Tl::MT, Q = S::Q, kRow = S::kRow, kThreads = S::kThreads;
+  extern __shared__ __align__(16) char smem[];
+  typename S::Shared& sh = *reinterpret_cast<typename S::Shared*>(smem);
+
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int warp = tid / 32 % kDaWarps, half = tid / 32 / kDaWarps, block = blockIdx.x;
   const int D = a.head_dim;
   const int longest = a.max_blocks << a.page_shift;
   bool bad = false;
@@ -394,11 +429,10 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
   auto tiles_of = [](int n) { return (n + kDaTile - 1) / kDaTile; };
   const int group = a.q_heads / a.kv_heads, qgroups = (group + Q - 1) / Q;
   const int per_request = a.nranks * a.kv_heads * qgroups;  // items of a request
-  const int seg = (a.batch + kDaThreads - 1) / kDaThreads;
-  int64_t total, before_mine, tiles_mine;  // tiles of the requests before the thread's, and of its own
+  const int seg = (a.batch + kThreads - 1) / kThreads;
+  int64_t before = 0, mine = 0, total = 0;  // tiles of the requests before the thread's, its own, all
   {
     const int b0 = min(tid * seg, a.batch), b1 = min(b0 + seg, a.batch);
-    int64_t mine = 0;
     for (int b = b0; b < b1; b++) {
       const int n = a.lens[b];
       if (n < 0 || n > longest) bad = true;
@@ -411,33 +445,31 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
       const int64_t x = __shfl_up_sync(~0u, scan, d);
       if (lane >= d) scan += x;
     }
-    if (lane == 31) s_sum[warp] = scan;
+    if (lane == 31) sh.tiles[tid >> 5] = scan;
     __syncthreads();
-    int64_t before = scan - mine, all = 0;
+    before = scan - mine;
 #pragma unroll
-    for (int w = 0; w < kDaWarps; w++) {
-      if (w < warp) before += s_sum[w];
-      all += s_sum[w];
+    for (int w = 0; w < kThreads / 32; w++) {
+      if (w < tid >> 5) before += sh.tiles[w];
+      total += sh.tiles[w];
     }
-    total = all * per_request;
-    before_mine = before;
-    tiles_mine = mine;
+    total *= per_request;
   }
   // the first `more` of the blocks with work have each + 1 tiles, the others each
   const int64_t blocks = total < gridDim.x ? total : gridDim.x, each = blocks == 0 ? 0 : total / blocks;
   const int64_t more = total - each * blocks;
-  auto start_of = [&](int64_t block) { return block * each + (block < more ? block : more); };
+  auto start_of = [&](int64_t w) { return w * each + (w < more ? w : more); };
   auto block_of = [&](int64_t tile) {
     const int64_t split = more * (each + 1);
-    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
+    return (int)(tile < split ? tile / (each + 1) : more + (tile - split) / each);
   };
-  if (blockIdx.x < blocks) {
-    const int64_t t = start_of(blockIdx.x) / per_request;  // lies in the same request, tiles counted once per item
-    if (t >= before_mine && t < before_mine + tiles_mine) {
+  if (block < blocks) {
+    const int64_t t = start_of(block) / per_request;  // lies in the same request, tiles counted once per item
+    if (t >= before && t < before + mine) {
       int b = tid * seg;
-      for (int n; t >= before_mine + (n = tiles_of(length(b))); b++) before_mine += n;
-      s_part.first = before_mine * per_request;
-      s_part.request = b;
+      for (int n; t >= before + (n = tiles_of(length(b))); b++) before += n;
+      sh.part.first = before * per_request;
+      sh.part.request = b;
     }
   }
 
@@ -446,44 +478,44 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
     if (length(b) != 0) continue;
     for (int r = 0; r < a.nranks; r++) {
       T* out = reinterpret_cast<T*>(a.out[r]) + (int64_t)b * a.out_stride;
-      for (int i = tid; i < a.q_heads * D; i += kDaThreads) from_float(out + i, 0.f);
+      for (int i = tid; i < a.q_heads * D; i += kThreads) from_float(out + i, 0.f);
       if (a.lse[r] != nullptr)
-        for (int i = tid; i < a.q_heads; i += kDaThreads) a.lse[r][(int64_t)b * a.q_heads + i] = -INFINITY;
+        for (int i = tid; i < a.q_heads; i += kThreads) a.lse[r][(int64_t)b * a.q_heads + i] = -INFINITY;
     }
   }
-  if (blockIdx.x >= blocks) {
+  if (block >= blocks) {
     if (bad) op_report(a.ws, kErrCapacity);
     return;
   }
 
-  for (int64_t at = start_of(blockIdx.x); at < start_of(blockIdx.x + 1);) {
+  for (int64_t at = start_of(block); at < start_of(block + 1);) {
     __syncthreads();  // the last part's shared values have been read
     if (tid == 0) {
-      const int64_t end = start_of(blockIdx.x + 1);
-      int b = s_part.request, n = tiles_of(length(b));
-      int64_t first = s_part.first;
+      const int64_t end = start_of(block + 1);
+      int b = sh.part.request, n = tiles_of(length(b));
+      int64_t first = sh.part.first;
       while (at >= first + (int64_t)n * per_request) {
         first += (int64_t)n * per_request;
         n = tiles_of(length(++b));
       }
       const int item = (int)((at - first) / n), qg = item % qgroups;
-      s_part.first = first;
-      s_part.request = b;
-      s_part.tiles = n;
-      s_part.len = length(b);
-      s_part.item_first = first + (int64_t)item * n;
-      s_part.t0 = (int)(at - s_part.item_first);
-      s_part.t1 = (int)(end - s_part.item_first < n ? end - s_part.item_first : n);
-      s_part.kvh = item / qgroups % a.kv_heads;
-      s_part.rank = item / qgroups / a.kv_heads;
-      s_part.q0 = s_part.kvh * group + qg * Q;
-      s_part.queries = min(Q, group - qg * Q);
+      sh.part.first = first;
+      sh.part.request = b;
+      sh.part.tiles = n;
+      sh.part.len = length(b);
+      sh.part.item_first = first + (int64_t)item * n;
+      sh.part.t0 = (int)(at - sh.part.item_first);
+      sh.part.t1 = (int)(end - sh.part.item_first < n ? end - sh.part.item_first : n);
+      sh.part.kvh = item / qgroups % a.kv_heads;
+      sh.part.rank = item / qgroups / a.kv_heads;
+      sh.part.q0 = sh.part.kvh * group + qg * Q;
+      sh.part.queries = min(Q, group - qg * Q);
     }
     __syncthreads();
-    const int rank = s_part.rank, kvh = s_part.kvh, len = s_part.len, t1 = s_part.t1;
+    const int rank = sh.part.rank, kvh = sh.part.kvh, len = sh.part.len, t1 = sh.part.t1;
     const T* kc = reinterpret_cast<const T*>(a.k_cache[rank]);
     const T* vc = reinterpret_cast<const T*>(a.v_cache[rank]);
-    const int32_t* table = a.table + (int64_t)s_part.request * a.table_stride;
+    const int32_t* table = a.table + (int64_t)sh.part.request * a.table_stride;
 
     // the lane's token of the warp's 16 in a tile -> cache row
     auto row_of = [&](int tile) {
@@ -512,19 +544,20 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
         for (int j = 0; j < 4; j++) o[mt][nt][j] = 0.f;
     }
     {
-      const int t0 = s_part.t0;
+      const int t0 = sh.part.t0;
       int row = row_of(t0), next = row_of(t0 + 1);
       tile.load_k(kc, row, D);
       if (kDaAhead<T, DP>) tile.load_v(vc, row, D);
-      Tl::load_queries(s_buf,
-                       reinterpret_cast<const T*>(a.q[rank]) + (int64_t)s_part.request * a.q_stride +
-                           (int64_t)s_part.q0 * D,
-                       s_part.queries, D);
+      const T* q = reinterpret_cast<const T*>(a.q[rank]) + (int64_t)sh.part.request * a.q_stride + (int64_t)sh.part.q0 * D;
+#pragma unroll
+      for (int h = 0; h < H; h++)
+        Tl::load_queries(sh.buf + h * Tl::kQueryBytes, q + h * NT * 8 * D, sh.part.queries - h * NT * 8, D, tid, kThreads);
+      const char* queries = sh.buf + half * Tl::kQueryBytes;
       __syncthreads();
       const float scale2 = a.scale * 1.4426950408889634f;  // scores in units of log 2
       for (int t = t0; t < t1; t++) {
         float s[NT][4];
-        tile.scores(s_buf, s);
+        tile.scores(queries, s);
         const bool live0 = __shfl_sync(~0u, row, g) >= 0, live1 = __shfl_sync(~0u, row, g + 8) >= 0;
         if (kDaAhead<T, DP>) tile.load_k(kc, next, D);
         else tile.load_v(vc, row, D);
@@ -552,20 +585,20 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) st.l[nt][j] += __shfl_xor_sync(~0u, st.l[nt][j], d);
         if (g == 0) {
-          s_m[warp][nt * 8 + 2 * c + j] = st.m[nt][j];
-          s_l[warp][nt * 8 + 2 * c + j] = st.l[nt][j];
+          sh.m[warp][half * NT * 8 + nt * 8 + 2 * c + j] = st.m[nt][j];
+          sh.l[warp][half * NT * 8 + nt * 8 + 2 * c + j] = st.l[nt][j];
         }
       }
-    __syncthreads();  // every warp is past the queries in s_buf
-    float* s_o = reinterpret_cast<float*>(s_buf);
+    __syncthreads();  // every warp is past the queries in sh.buf
+    float* s_o = reinterpret_cast<float*>(sh.buf);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
       for (int j = 0; j < 2; j++) {
-        const int q = nt * 8 + 2 * c + j;
-        float top = s_m[0][q];
+        const int q = half * NT * 8 + nt * 8 + 2 * c + j;
+        float top = sh.m[0][q];
 #pragma unroll
-        for (int w = 1; w < kDaWarps; w++) top = fmaxf(top, s_m[w][q]);
+        for (int w = 1; w < kDaWarps; w++) top = fmaxf(top, sh.m[w][q]);
         const float f = st.m[nt][j] == -INFINITY ? 0.f : exp2_fast(st.m[nt][j] - top);
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
@@ -574,17 +607,16 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
         }
       }
     if (tid < Q) {
-      float m = s_m[0][tid], l = 0.f;
+      float m = sh.m[0][tid], l = 0.f;
 #pragma unroll
-      for (int w = 1; w < kDaWarps; w++) m = fmaxf(m, s_m[w][tid]);
+      for (int w = 1; w < kDaWarps; w++) m = fmaxf(m, sh.m[w][tid]);
 #pragma unroll
-      for (int w = 0; w < kDaWarps; w++)
-        l += s_m[w][tid] == -INFINITY ? 0.f : s_l[w][tid] * exp2_fast(s_m[w][tid] - m);
-      s_top[tid] = m;
-      s_sum_l[tid] = l;
+      for (int w = 0; w < kDaWarps; w++) l += sh.m[w][tid] == -INFINITY ? 0.f : sh.l[w][tid] * exp2_fast(sh.m[w][tid] - m);
+      sh.top[tid] = m;
+      sh.total[tid] = l;
     }
     __syncthreads();
-    const int values = s_part.queries * (DP / 4);
+    const int values = sh.part.queries * (DP / 4);
     auto sum4 = [&](int q, int d) {
       float4 x = *reinterpret_cast<const float4*>(s_o + q * kRow + d);
 #pragma unroll
@@ -594,100 +626,96 @@ __global__ void __launch_bounds__(kDaThreads) decode_attention_kernel(const __gr
       }
       return x;
     };
-    T* out = reinterpret_cast<T*>(a.out[rank]) + (int64_t)s_part.request * a.out_stride + (int64_t)s_part.q0 * D;
-    float* lse = a.lse[rank] == nullptr ? nullptr : a.lse[rank] + (int64_t)s_part.request * a.q_heads + s_part.q0;
-    auto finish = [&](int q, int d, float4 x) {  // from s_top and s_sum_l
-      const float l = s_sum_l[q], f = l == 0.f ? 0.f : 1.f / l;  // no token with a weight: 0
-      T* p = out + (int64_t)q * D + d;
-      from_float(p, x.x * f);
-      from_float(p + 1, x.y * f);
-      from_float(p + 2, x.z * f);
-      from_float(p + 3, x.w * f);
-      if (d == 0 && lse != nullptr) lse[q] = l == 0.f ? -INFINITY : (s_top[q] + log2f(l)) * 0.6931471805599453f;
-    };
-    if (s_part.t0 == 0 && t1 == s_part.tiles) {
-      for (int i = tid; i < values; i += kDaThreads) {
+    const Output<T> out = output_of<T>(a, sh.part);
+    if (sh.part.t0 == 0 && t1 == sh.part.tiles) {
+      for (int i = tid; i < values; i += kThreads) {
         const int q = i / (DP / 4), d = i % (DP / 4) * 4;
-        if (d < D) finish(q, d, sum4(q, d));
+        if (d < D) out.write(q, d, D, sum4(q, d), sh.top[q], sh.total[q]);
       }
     } else {
       // The item is cut: its blocks cf..cl leave partial results, each run of kDaJoin blocks is joined by the one
       // of them that arrives last, and the runs by the last of those, in block order both times.
       float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset);
-      const int64_t item_first = s_part.item_first;
-      const int cf = (int)block_of(item_first), cl = (int)block_of(item_first + s_part.tiles - 1);
+      const int64_t item_first = sh.part.item_first;
+      const int cf = block_of(item_first), cl = block_of(item_first + sh.part.tiles - 1);
       const bool starts_at_cf = start_of(cf) == item_first;
-      auto part_of = [&](int block) {  // a block leaves up to two: of its first item, and of the last that starts in it
-        return parts + (2 * block + (block == cf && !starts_at_cf)) * partial_floats<DP, NT>();
+      auto part_of = [&](int b) {  // a block leaves up to two: of its first item, and of the last that starts in it
+        return parts + (2 * (int64_t)b + (b == cf && !starts_at_cf)) * S::kPartial;
       };
-      float* part = part_of(blockIdx.x);
-      for (int i = tid; i < values; i += kDaThreads) {
+      float* part = part_of(block);
+      for (int i = tid; i < values; i += kThreads) {
         const int q = i / (DP / 4), d = i % (DP / 4) * 4;
         *reinterpret_cast<float4*>(part + q * DP + d) = sum4(q, d);
       }
       if (tid < Q) {
-        part[Q * DP + tid] = s_top[tid];
-        part[Q * DP + Q + tid] = s_sum_l[tid];
+        part[Q * DP + tid] = sh.top[tid];
+        part[Q * DP + Q + tid] = sh.total[tid];
       }
       uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
       // a run's counter is that of its last block, which no other item's run ends with
-      int from = cf + (blockIdx.x - cf) / kDaJoin * kDaJoin, count = min(kDaJoin, cl + 1 - from), step = 1;
+      int from = cf + (block - cf) / kDaJoin * kDaJoin, count = min(kDaJoin, cl + 1 - from), step = 1;
       int counter = from + count - 1;
       for (;;) {
-        __threadfence();
         __syncthreads();
         if (tid == 0) {
-          s_last = atomicAdd(counters + counter, 1u) == (uint32_t)(count - 1);
-          if (s_last) counters[counter] = 0;
+          // releases the block's partial result, and acquires the others' if it is the last
+          sh.last = atom_add_acq_rel_u32(counters + counter, 1u) == (uint32_t)(count - 1);
+          if (sh.last) counters[counter] = 0;
         }
         __syncthreads();
-        if (!s_last) break;
-        __threadfence();
-        for (int i = tid; i < count * Q; i += kDaThreads) {
-          const float* p = part_of(from + i / Q * step) + Q * DP + i % Q;
-          s_w[i / Q][i % Q] = __ldcg(p);
-          s_pl[i / Q][i % Q] = __ldcg(p + Q);
-        }
-        __syncthreads();
-        if (tid < Q) {
+        if (!sh.last) break;
+        constexpr int kShare = kThreads / Q < 32 ? kThreads / Q : 32;  // lanes of a query head
+        if (tid < kShare * Q) {
+          const int q = tid / kShare, p0 = tid % kShare;
           float m = -INFINITY, l = 0.f;
-          for (int p = 0; p < count; p++) m = fmaxf(m, s_w[p][tid]);
-          for (int p = 0; p < count; p++) {
-            const float f = s_w[p][tid] == -INFINITY ? 0.f : exp2_fast(s_w[p][tid] - m);
-            l += f * s_pl[p][tid];
-            s_w[p][tid] = f;
+          for (int p = p0; p < count; p += kShare) {
+            const float* src = part_of(from + p * step) + Q * DP + q;
+            sh.weight[p][q] = __ldcg(src);
+            sh.sum[p][q] = __ldcg(src + Q);
           }
-          s_top[tid] = m;
-          s_sum_l[tid] = l;
+          for (int p = p0; p < count; p += kShare) m = fmaxf(m, sh.weight[p][q]);
+#pragma unroll
+          for (int d = kShare / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+          for (int p = p0; p < count; p += kShare) {
+            const float x = sh.weight[p][q], f = x == -INFINITY ? 0.f : exp2_fast(x - m);
+            l += f * sh.sum[p][q];
+            sh.weight[p][q] = f;
+          }
+#pragma unroll
+          for (int d = kShare / 2; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+          if (p0 == 0) {
+            sh.top[q] = m;
+            sh.total[q] = l;
+          }
         }
         __syncthreads();
         const bool whole = step > 1 || count == cl + 1 - cf;  // nothing of the item is missing
         float* to = part_of(from);
-        for (int i = tid; i < values; i += kDaThreads) {
+        for (int i = tid; i < values; i += kThreads) {
           const int q = i / (DP / 4), d = i % (DP / 4) * 4;
           if (d >= D) continue;
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
           for (int p = 0; p < count; p++) {
             const float4 y = __ldcg(reinterpret_cast<const float4*>(part_of(from + p * step) + q * DP + d));
-            const float f = s_w[p][q];
+            const float f = sh.weight[p][q];
             x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
           }
-          if (whole) finish(q, d, x);
+          if (whole) out.write(q, d, D, x, sh.top[q], sh.total[q]);
           else *reinterpret_cast<float4*>(to + q * DP + d) = x;
         }
         if (whole) break;
         if (tid < Q) {
-          to[Q * DP + tid] = s_top[tid];
-          to[Q * DP + Q + tid] = s_sum_l[tid];
+          to[Q * DP + tid] = sh.top[tid];
+          to[Q * DP + Q + tid] = sh.total[tid];
         }
         step = kDaJoin;
         count = (cl - cf) / kDaJoin + 1;
         from = cf;
-        counter = kDaMaxBlocks + cf;  // one item at most starts in a block and leaves it
+        counter = kDaMaxBlocks + cf;  // one item at most starts in a block's range and leaves it
       }
     }
-    at = s_part.item_first + t1;
+    at = sh.part.item_first + t1;
   }
   if (bad) op_report(a.ws, kErrCapacity);
 }
@@ -696,45 +724,53 @@ namespace {
 
 struct DecodeKernel {
   const void* fn;
-  int partial;  // floats of a partial result
+  int threads, shared, partial;  // bytes of shared memory, floats of a partial result
 };
 
-template <typename T, int DP, int NT>
-DecodeKernel kernel_of() { return {(const void*)decode_attention_kernel<T, DP, NT>, partial_floats<DP, NT>()}; }
+template <typename T, int DP, int NT, int H>
+DecodeKernel kernel_of() {
+  using S = Shape<T, DP, NT, H>;
+  return {(const void*)decode_attention_kernel<T, DP, NT, H>, S::kThreads, (int)sizeof(typename S::Shared), S::kPartial};
+}
 
-// 16 query heads share a pass over the cache where their accumulators fit the
-// registers beside K and V.
+// More than 8 query heads a key head (wide): two accumulators a tile where they
+// fit the registers beside K and V. Where they do not, bf16 takes two groups of
+// warps (head size 192, 16 heads on 8 ranks, 32 requests of 8192 tokens: 326 us
+// against 461 of two passes over the cache; 256: 534 against 614); binary32 is
+// bound by its instructions then, and two groups gave nothing (505 against 498).
 template <typename T>
-DecodeKernel kernel_for(int head_dim, int group) {
-  const bool wide = group > 8;
-  if (head_dim <= 64) return wide ? kernel_of<T, 64, 2>() : kernel_of<T, 64, 1>();
+DecodeKernel kernel_for(int head_dim, bool wide) {
+  constexpr bool half = sizeof(T) == 2;
+  if (head_dim <= 64) return wide ? kernel_of<T, 64, 2, 1>() : kernel_of<T, 64, 1, 1>();
   // the padding that a rounder size brings costs binary32 instructions, of which it has few to spare
-  if (sizeof(T) == 4 && head_dim <= 96) return wide ? kernel_of<float, 96, 2>() : kernel_of<float, 96, 1>();
-  if (head_dim <= 128) return wide && sizeof(T) == 2 ? kernel_of<T, 128, sizeof(T) == 2 ? 2 : 1>() : kernel_of<T, 128, 1>();
-  return head_dim <= 192 ? kernel_of<T, 192, 1>() : kernel_of<T, 256, 1>();
+  if (!half && head_dim <= 96) return wide ? kernel_of<float, 96, 2, 1>() : kernel_of<float, 96, 1, 1>();
+  if (head_dim <= 128) return half && wide ? kernel_of<T, 128, half ? 2 : 1, 1>() : kernel_of<T, 128, 1, 1>();
+  if (head_dim <= 192) return half && wide ? kernel_of<T, 192, 1, half ? 2 : 1>() : kernel_of<T, 192, 1, 1>();
+  return half && wide ? kernel_of<T, 256, 1, half ? 2 : 1>() : kernel_of<T, 256, 1, 1>();
+}
+DecodeKernel kernel_for(int dtype, int head_dim, int group) {
+  return dtype == kF32 ? kernel_for<float>(head_dim, group > 8) : kernel_for<uint16_t>(head_dim, group > 8);
 }
 
 }  // namespace
 
 int64_t decode_attention_scratch_bytes(int, int, int q_heads, int kv_heads, int head_dim) {
   const int group = q_heads / kv_heads;
-  const int most = kernel_for<uint16_t>(head_dim, group).partial;
-  const int f32 = kernel_for<float>(head_dim, group).partial;
-  return 2ll * kDaMaxBlocks * (most > f32 ? most : f32) * (int64_t)sizeof(float);
+  return 2ll * kDaMaxBlocks * imax(kernel_for(kF32, head_dim, group).partial, kernel_for(kBF16, head_dim, group).partial) *
+         (int64_t)sizeof(float);
 }
 
 cudaError_t launch_decode_attention(const DecodeArgs& a, cudaStream_t stream) {
-  const int group = a.q_heads / a.kv_heads;
-  const DecodeKernel k = a.dtype == kF32 ? kernel_for<float>(a.head_dim, group) : kernel_for<uint16_t>(a.head_dim, group);
+  const DecodeKernel k = kernel_for(a.dtype, a.head_dim, a.q_heads / a.kv_heads);
   int resident = 0;
-  const cudaError_t e = resident_blocks(k.fn, kDaThreads, &resident);
+  const cudaError_t e = resident_blocks(k.fn, k.threads, k.shared, &resident);
   if (e != cudaSuccess) return e;
   const int64_t grid = imin((int64_t)resident, kDaMaxBlocks);
   if (trace_on())
     std::fprintf(stderr, "rar trace: decode_attention nranks=%d batch=%d heads=%d/%d dim=%d grid=%lld threads=%d\n",
-                 a.nranks, a.batch, a.q_heads, a.kv_heads, a.head_dim, (long long)grid, kDaThreads);
+                 a.nranks, a.batch, a.q_heads, a.kv_heads, a.head_dim, (long long)grid, k.threads);
   void* params[] = {const_cast<DecodeArgs*>(&a)};
-  return cudaLaunchKernel(k.fn, dim3((unsigned)grid), dim3(kDaThreads), params, 0, stream);
+  return cudaLaunchKernel(k.fn, dim3((unsigned)grid), dim3(k.threads), params, (size_t)k.shared, stream);
 }
 
 }  // namespace rar

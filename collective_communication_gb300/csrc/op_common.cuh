@@ -48,6 +48,13 @@ __device__ __forceinline__ bool op_ready(char* ws, uint32_t magic) {
   return false;
 }
 
+// Returns the old value.
+__device__ __forceinline__ uint32_t atom_add_acq_rel_u32(uint32_t* p, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 // Two floats rounded to nearest even, a in the low half.
@@ -140,6 +147,13 @@ __device__ __forceinline__ void from_float(float* p, float v) { *p = v; }
 __device__ __forceinline__ void from_float(uint16_t* p, float v) {
   const __nv_bfloat16 b = __float2bfloat16_rn(v);
   *p = *reinterpret_cast<const uint16_t*>(&b);
+}
+// Four consecutive elements, 16-byte (f32) or 8-byte (bf16) aligned.
+__device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) {
+  *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
+}
+__device__ __forceinline__ void store4(uint16_t* p, float x, float y, float z, float w) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(x, y), bf16_pair(z, w));
 }
 
 // ---- kernel arguments ----

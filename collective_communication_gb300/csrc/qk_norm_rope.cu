@@ -530,7 +530,7 @@ cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, cudaStream_t stream) 
   const void* fn = a.dtype == kF32 ? backward_of<float>(lanes, a.interleaved != 0)
                                    : backward_of<uint16_t>(lanes, a.interleaved != 0);
   int resident = 0;
-  const cudaError_t e = resident_blocks(fn, kBwdThreads, &resident);
+  const cudaError_t e = resident_blocks(fn, kBwdThreads, 0, &resident);
   if (e != cudaSuccess) return e;
   // one resident wave, shared out in proportion to the kinds' bytes: x, dy and dx of query and key heads, dv twice
   const int64_t most = imin(kNormRopeBwdBlocks, (int64_t)resident) / a.nranks;

@@ -102,9 +102,10 @@ bool trace_on();
 // The current device and its SM count (cached per device; safe from several
 // host threads).
 cudaError_t current_device_sms(int* device, int* sms);
-// Blocks of `fn` (`threads` each, static shared memory only) that the current
-// device holds at once, cached per device and kernel.
-cudaError_t resident_blocks(const void* fn, int threads, int* blocks);
+// Blocks of `fn` (`threads` threads and `shared` bytes of dynamic shared memory
+// each) that the current device holds at once; cached per device and kernel.
+// Lets the kernel have that much shared memory.
+cudaError_t resident_blocks(const void* fn, int threads, int shared, int* blocks);
 // One-time host setup per device (kernel attributes): true once `key` has
 // been marked done on `device`; mark_setup_done records it. Setting an
 // attribute twice from racing threads is harmless, so no lock is taken.

@@ -158,7 +158,7 @@ std::atomic<int> g_residencies{0};
 
 }  // namespace
 
-cudaError_t resident_blocks(const void* fn, int threads, int* blocks) {
+cudaError_t resident_blocks(const void* fn, int threads, int shared, int* blocks) {
   int device = 0, sms = 0, per_sm = 0;
   cudaError_t e = current_device_sms(&device, &sms);
   if (e != cudaSuccess) return e;
@@ -170,7 +170,11 @@ cudaError_t resident_blocks(const void* fn, int threads, int* blocks) {
       return cudaSuccess;
     }
   }
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, 0);
+  if (shared > 0) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+    if (e != cudaSuccess) return e;
+  }
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, (size_t)shared);
   if (e != cudaSuccess) return e;
   *blocks = sms * per_sm;
   const int slot = g_residencies.fetch_add(1);

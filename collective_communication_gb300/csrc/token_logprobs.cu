@@ -436,7 +436,7 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) 
                                    : (a.top > 0 ? (const void*)token_logprobs_kernel<uint16_t, true>
                                                 : (const void*)token_logprobs_kernel<uint16_t, false>);
   int resident = 0;
-  const cudaError_t e = resident_blocks(fn, kLpThreads, &resident);
+  const cudaError_t e = resident_blocks(fn, kLpThreads, 0, &resident);
   if (e != cudaSuccess) return e;
   for (int r = 0; r < a.nranks; r++)
     a.first_tile[r + 1] = a.first_tile[r] + (int)div_up(a.first[r + 1] - a.first[r], kLpTile);
