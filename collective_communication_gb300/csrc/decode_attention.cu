@@ -380,7 +380,7 @@ struct Shape {
     float m[kDaWarps][Q], l[kDaWarps][Q];
     float weight[kMostParts][Q], sum[kMostParts][Q], top[Q], total[Q];
     int64_t tiles[kDaWarps * H];
-    Part part;
+    Part part[2];  // the one worked on and the one after it
     int last;
   };
 };
@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
     if (t >= before && t < before + mine) {
       int b = tid * seg;
       for (int n; t >= before + (n = tiles_of(length(b))); b++) before += n;
-      sh.part.first = before * per_request;
-      sh.part.request = b;
+      sh.part[1].first = before * per_request;
+      sh.part[1].request = b;
     }
   }
 
@@ -488,47 +488,65 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
     return;
   }
 
-  for (int64_t at = start_of(block); at < start_of(block + 1);) {
-    __syncthreads();  // the last part's shared values have been read
-    if (tid == 0) {
-      const int64_t end = start_of(block + 1);
-      int b = sh.part.request, n = tiles_of(length(b));
-      int64_t first = sh.part.first;
-      while (at >= first + (int64_t)n * per_request) {
-        first += (int64_t)n * per_request;
-        n = tiles_of(length(++b));
-      }
-      const int item = (int)((at - first) / n), qg = item % qgroups;
-      sh.part.first = first;
-      sh.part.request = b;
-      sh.part.tiles = n;
-      sh.part.len = length(b);
-      sh.part.item_first = first + (int64_t)item * n;
-      sh.part.t0 = (int)(at - sh.part.item_first);
-      sh.part.t1 = (int)(end - sh.part.item_first < n ? end - sh.part.item_first : n);
-      sh.part.kvh = item / qgroups % a.kv_heads;
-      sh.part.rank = item / qgroups / a.kv_heads;
-      sh.part.q0 = sh.part.kvh * group + qg * Q;
-      sh.part.queries = min(Q, group - qg * Q);
+  // The part that starts at tile `at` of the block's range, which lies in the request of `p` or after it.
+  auto describe = [&](Part& p, const Part& from, int64_t at) {
+    const int64_t end = start_of(block + 1);
+    p.t0 = p.t1 = 0;
+    if (at >= end) return;
+    int b = from.request, n = tiles_of(length(b));
+    int64_t first = from.first;
+    while (at >= first + (int64_t)n * per_request) {
+      first += (int64_t)n * per_request;
+      n = tiles_of(length(++b));
+    }
+    const int item = (int)((at - first) / n), qg = item % qgroups;
+    p.first = first;
+    p.request = b;
+    p.tiles = n;
+    p.len = length(b);
+    p.item_first = first + (int64_t)item * n;
+    p.t0 = (int)(at - p.item_first);
+    p.t1 = (int)(end - p.item_first < n ? end - p.item_first : n);
+    p.kvh = item / qgroups % a.kv_heads;
+    p.rank = item / qgroups / a.kv_heads;
+    p.q0 = p.kvh * group + qg * Q;
+    p.queries = min(Q, group - qg * Q);
+  };
+  // the lane's token of the warp's 16 in a tile of a part -> cache row
+  auto row_of = [&](const Part& p, int tile) {
+    const int t = tile * kDaTile + warp * 16 + (lane & 15);
+    if (tile >= p.t1 || t >= p.len) return -1;
+    const int page = a.table[(int64_t)p.request * a.table_stride + (t >> a.page_shift)];
+    if (page < 0 || page >= a.num_pages) {
+      bad = true;
+      return -1;
+    }
+    return ((page * a.kv_heads + p.kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+  };
+  __syncthreads();
+  if (tid == 0) describe(sh.part[0], sh.part[1], start_of(block));
+  __syncthreads();
+  Tl tile;
+  int row = row_of(sh.part[0], sh.part[0].t0);
+  tile.load_k(reinterpret_cast<const T*>(a.k_cache[sh.part[0].rank]), row, D);
+  if (kDaAhead<T, DP>) tile.load_v(reinterpret_cast<const T*>(a.v_cache[sh.part[0].rank]), row, D);
+
+  // At the end of a part the first tile of the next one is on its way already.
+  for (int i = 0;; i ^= 1) {
+    const Part& part = sh.part[i];
+    Part& after = sh.part[i ^ 1];
+    if (tid == 0) describe(after, part, part.item_first + part.t1);
+    {
+      const T* q = reinterpret_cast<const T*>(a.q[part.rank]) + (int64_t)part.request * a.q_stride + (int64_t)part.q0 * D;
+#pragma unroll
+      for (int h = 0; h < H; h++)
+        Tl::load_queries(sh.buf + h * Tl::kQueryBytes, q + h * NT * 8 * D, part.queries - h * NT * 8, D, tid, kThreads);
     }
     __syncthreads();
-    const int rank = sh.part.rank, kvh = sh.part.kvh, len = sh.part.len, t1 = sh.part.t1;
+    const int rank = part.rank, t1 = part.t1;
     const T* kc = reinterpret_cast<const T*>(a.k_cache[rank]);
     const T* vc = reinterpret_cast<const T*>(a.v_cache[rank]);
-    const int32_t* table = a.table + (int64_t)sh.part.request * a.table_stride;
-
-    // the lane's token of the warp's 16 in a tile -> cache row
-    auto row_of = [&](int tile) {
-      const int t = tile * kDaTile + warp * 16 + (lane & 15);
-      if (tile >= t1 || t >= len) return -1;
-      const int page = table[t >> a.page_shift];
-      if (page < 0 || page >= a.num_pages) {
-        bad = true;
-        return -1;
-      }
-      return ((page * a.kv_heads + kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-    };
-    Tl tile;
+    auto row_at = [&](int t) { return t < t1 ? row_of(part, t) : row_of(after, after.t0 + t - t1); };
     float o[MT][NT][4];
     Softmax<NT> st;
 #pragma unroll
@@ -544,23 +562,19 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
         for (int j = 0; j < 4; j++) o[mt][nt][j] = 0.f;
     }
     {
-      const int t0 = sh.part.t0;
-      int row = row_of(t0), next = row_of(t0 + 1);
-      tile.load_k(kc, row, D);
-      if (kDaAhead<T, DP>) tile.load_v(vc, row, D);
-      const T* q = reinterpret_cast<const T*>(a.q[rank]) + (int64_t)sh.part.request * a.q_stride + (int64_t)sh.part.q0 * D;
-#pragma unroll
-      for (int h = 0; h < H; h++)
-        Tl::load_queries(sh.buf + h * Tl::kQueryBytes, q + h * NT * 8 * D, sh.part.queries - h * NT * 8, D, tid, kThreads);
+      int next = row_at(part.t0 + 1);
       const char* queries = sh.buf + half * Tl::kQueryBytes;
-      __syncthreads();
       const float scale2 = a.scale * 1.4426950408889634f;  // scores in units of log 2
-      for (int t = t0; t < t1; t++) {
+      for (int t = part.t0; t < t1; t++) {
         float s[NT][4];
         tile.scores(queries, s);
         const bool live0 = __shfl_sync(~0u, row, g) >= 0, live1 = __shfl_sync(~0u, row, g + 8) >= 0;
+        if (!kDaAhead<T, DP>) tile.load_v(vc, row, D);
+        if (t + 1 == t1 && after.t1 > 0) {
+          kc = reinterpret_cast<const T*>(a.k_cache[after.rank]);
+          vc = reinterpret_cast<const T*>(a.v_cache[after.rank]);
+        }
         if (kDaAhead<T, DP>) tile.load_k(kc, next, D);
-        else tile.load_v(vc, row, D);
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -573,7 +587,7 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
         if (kDaAhead<T, DP>) tile.load_v(vc, next, D);
         else tile.load_k(kc, next, D);
         row = next;
-        next = row_of(t + 2);
+        next = row_at(t + 2);
       }
     }
 
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
       sh.total[tid] = l;
     }
     __syncthreads();
-    const int values = sh.part.queries * (DP / 4);
+    const int values = part.queries * (DP / 4);
     auto sum4 = [&](int q, int d) {
       float4 x = *reinterpret_cast<const float4*>(s_o + q * kRow + d);
 #pragma unroll
@@ -626,8 +640,8 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
       }
       return x;
     };
-    const Output<T> out = output_of<T>(a, sh.part);
-    if (sh.part.t0 == 0 && t1 == sh.part.tiles) {
+    const Output<T> out = output_of<T>(a, part);
+    if (part.t0 == 0 && t1 == part.tiles) {
       for (int i = tid; i < values; i += kThreads) {
         const int q = i / (DP / 4), d = i % (DP / 4) * 4;
         if (d < D) out.write(q, d, D, sum4(q, d), sh.top[q], sh.total[q]);
@@ -636,20 +650,20 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
       // The item is cut: its blocks cf..cl leave partial results, each run of kDaJoin blocks is joined by the one
       // of them that arrives last, and the runs by the last of those, in block order both times.
       float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset);
-      const int64_t item_first = sh.part.item_first;
-      const int cf = block_of(item_first), cl = block_of(item_first + sh.part.tiles - 1);
+      const int64_t item_first = part.item_first;
+      const int cf = block_of(item_first), cl = block_of(item_first + part.tiles - 1);
       const bool starts_at_cf = start_of(cf) == item_first;
       auto part_of = [&](int b) {  // a block leaves up to two: of its first item, and of the last that starts in it
         return parts + (2 * (int64_t)b + (b == cf && !starts_at_cf)) * S::kPartial;
       };
-      float* part = part_of(block);
+      float* mine_out = part_of(block);
       for (int i = tid; i < values; i += kThreads) {
         const int q = i / (DP / 4), d = i % (DP / 4) * 4;
-        *reinterpret_cast<float4*>(part + q * DP + d) = sum4(q, d);
+        *reinterpret_cast<float4*>(mine_out + q * DP + d) = sum4(q, d);
       }
       if (tid < Q) {
-        part[Q * DP + tid] = sh.top[tid];
-        part[Q * DP + Q + tid] = sh.total[tid];
+        mine_out[Q * DP + tid] = sh.top[tid];
+        mine_out[Q * DP + Q + tid] = sh.total[tid];
       }
       uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
       // a run's counter is that of its last block, which no other item's run ends with
@@ -715,7 +729,8 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
         counter = kDaMaxBlocks + cf;  // one item at most starts in a block's range and leaves it
       }
     }
-    at = sh.part.item_first + t1;
+    __syncthreads();  // the part's shared values have been read
+    if (after.t1 == 0) break;
   }
   if (bad) op_report(a.ws, kErrCapacity);
 }
