@@ -324,18 +324,24 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         if constexpr (TOP) {
           tops = TopList();
           tops.start(__shfl_sync(~0u, sort32(head), a.top - 1));
-          const int keys = (int)(wl - wf + 1) * a.top;
-          for (int i0 = lane; i0 - lane < keys; i0 += 32 * 8) {
-            uint64_t key[8];
+          // only parts whose first alternative is not below the bound have any to give: four at a time
+          for (uint32_t w0 = wf; w0 <= wl; w0 += 32) {
+            uint64_t first = 0;
+            if (w0 + lane <= wl) first = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(w0 + lane) + 4));
+            uint32_t votes = __ballot_sync(~0u, first > tops.bound);
+            while (votes != 0) {
+              uint64_t key[4];
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-              const int i = i0 + 32 * j;
-              key[j] = 0;
-              if (i < keys)
-                key[j] = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(wf + i / a.top) + 4) + i % a.top);
+              for (int j = 0; j < 4; j++) {
+                const int src = __ffs(votes) - 1;  // -1 when there are no more
+                votes &= votes - 1;
+                key[j] = 0;
+                if (src >= 0 && lane < a.top)
+                  key[j] = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(w0 + src) + 4) + lane);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; j++) tops.offer(key[j], a.top);
             }
-#pragma unroll
-            for (int j = 0; j < 8; j++) tops.offer(key[j], a.top);
           }
         }
       }
