@@ -167,12 +167,11 @@ __device__ __forceinline__ Row8 rotate(const Row8& v, const Turn& t) {
   return r;
 }
 
-// Sum over a group; groups of a warp may be on different paths.
+// Sum over a group; all lanes of the warp call it.
 template <int L>
 __device__ __forceinline__ float group_sum(float x) {
-  const uint32_t mask = L == 32 ? ~0u : ((1u << (L & 31)) - 1) << (threadIdx.x & 31 & ~(L - 1));
 #pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) x += __shfl_xor_sync(mask, x, d, L);
+  for (int d = L / 2; d > 0; d >>= 1) x += __shfl_xor_sync(~0u, x, d, L);
   return x;
 }
 __device__ __forceinline__ float rsqrt_fast(float x) {
@@ -210,18 +209,23 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
   const int strip = live ? (int)(item - (uint32_t)token * strips) : 0;
   const bool in = live && n.in;
   const int h0 = strip * (is_q ? per_q : per_kv);
-  const int heads = is_q ? min(per_q, a.q_heads - h0) : min(per_kv, a.kv_heads - h0);
-  const int rows = heads * (CACHE && !is_q ? 2 : 1);
+  const int heads = in ? min(is_q ? per_q : per_kv, (is_q ? a.q_heads : a.kv_heads) - h0) : 0;
+  // rows of the strip: its heads, and with CACHE from row per_kv the same heads' values (a shorter strip leaves gaps)
+  const int rows = is_q ? per_q : CACHE ? 2 * per_kv : per_kv, values = CACHE && !is_q ? per_kv : kRows;
 
   int pos = live ? a.positions[token] : 0;
   int64_t slot = CACHE && live ? a.slots[token] : -1;  // below zero: a padding token, no cache row
   const T* x0 = reinterpret_cast<const T*>(a.qkv[rank]) + (int64_t)token * a.qkv_stride + (h0 + (is_q ? 0 : a.q_heads)) * D;
-  const int to_v = (a.kv_heads - heads) * D;  // from the place after a strip's keys to its values
   Chunks<T, INTER> x[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; i++)
-    if (in && i < rows) x[i].load(x0 + i * D + (CACHE && !is_q && i >= heads ? to_v : 0), n);
-    else x[i].zero();
+  for (int i = 0; i < kRows; i++) {
+    x[i].zero();
+    if (i < values) {
+      if (i < heads) x[i].load(x0 + i * D, n);
+    } else if (i - values < heads) {
+      x[i].load(x0 + (a.kv_heads + i - values) * D, n);
+    }
+  }
   bool bad = false;
   if (pos < 0 || pos >= a.max_pos) { bad = true; pos = 0; }
   if (CACHE && slot >= a.num_slots) { bad = true; slot = -1; }
@@ -247,16 +251,19 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
     out_v = reinterpret_cast<T*>(a.v_out[rank]) + at;
     apart = (int64_t)D << a.page_shift;
   }
+  const int stores = kept ? heads : 0;
 #pragma unroll
   for (int i = 0; i < kRows; i++) {
     if (i >= rows) break;
-    if (!CACHE || is_q || i < heads) {
+    if (i < values) {
       const Row8 v = x[i].widen();
       const float r = rsqrt_fast(fmaf(group_sum<L>(dot8(v, v)), inv, a.eps));
       x[i].narrow(rotate<false>(v * r * w, turn));
-      if (in && kept) x[i].store(out + i * apart, n);
-    } else if (in && kept) {
-      x[i].store(out_v + (i - heads) * apart, n);
+      if (i < stores) x[i].store(out, n);
+      out += apart;
+    } else {
+      if (i - values < stores) x[i].store(out_v, n);
+      out_v += apart;
     }
   }
   if (bad) op_report(a.ws, kErrCapacity);
@@ -275,9 +282,11 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
 // that arrives last: the same bits every time.
 namespace {
 
-__device__ __forceinline__ void copy_async16(void* smem, const void* gmem, bool live) {  // zeros if not live
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem)), "l"(gmem), "r"(live ? 16 : 0)
-               : "memory");
+__device__ __forceinline__ void copy_async16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void store_zero16(uint32_t smem) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(smem), "r"(0) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -342,18 +351,27 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
   const int64_t w0 = walker < a.tokens ? walker : 0;
   const T* fx = xs + w0 * a.qkv_stride + place + l * 8;  // of the next row to ask for
   const T* fg = gs + w0 * g_stride + l * 8;
-  int f_left = n.in ? mine : 0, f_head = 0, f_slot = 0;
-  T* const cell = &ring[group][0][0][l * 8];
+  constexpr uint32_t kCell = kRow * sizeof(T), kSlot = 2 * kCell;  // bytes of a row of x or dy, of both
+  const uint32_t cell = smem_addr(&ring[group][0][0][l * 8]);
+  int f_left = mine, f_head = 0;
+  uint32_t f_cell = cell;
+  // the next row into the next slot; zeros after the group's last row, and always where a lane is past the head
   auto fetch = [&]() {
-    const bool live = f_left > 0;
+    if (n.in && f_left > 0) {
 #pragma unroll
-    for (int c = 0; c < kCopies; c++) {
-      copy_async16(cell + f_slot * (2 * kRow) + c * (16 / (int)sizeof(T)), (live ? fx : xs) + c * (16 / (int)sizeof(T)), live);
-      copy_async16(cell + f_slot * (2 * kRow) + kRow + c * (16 / (int)sizeof(T)), (live ? fg : gs) + c * (16 / (int)sizeof(T)),
-                   live);
+      for (int c = 0; c < kCopies; c++) {
+        copy_async16(f_cell + 16 * c, fx + c * (16 / (int)sizeof(T)));
+        copy_async16(f_cell + kCell + 16 * c, fg + c * (16 / (int)sizeof(T)));
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kCopies; c++) {
+        store_zero16(f_cell + 16 * c);
+        store_zero16(f_cell + kCell + 16 * c);
+      }
     }
     copy_async_commit();
-    f_slot = f_slot + 1 == kBwdStages ? 0 : f_slot + 1;
+    f_cell = f_cell == cell + (kBwdStages - 1) * kSlot ? cell : f_cell + kSlot;
     f_left--;
     const bool wrap = ++f_head == heads;
     fx += wrap ? x_jump : D;
