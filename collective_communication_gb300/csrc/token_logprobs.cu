@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
       const uint32_t word = (uint32_t)(a.first[rank] + c0) + head;
 
       // a round is kAhead packs a lane, 32 apart
-      for (int p = lane; p - lane < packs; p += 32 * kAhead) {
-        Pack8<T> u[kAhead];
+      Pack8<T> u[kAhead];
+      auto fetch = [&](int p) {
         if (p - lane + 32 * kAhead <= packs) {
 #pragma unroll
           for (int i = 0; i < kAhead; i++) u[i].load_stream(body + (int64_t)(p + i * 32) * 8);
@@ -210,6 +210,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
             else u[i].absent();
           }
         }
+      };
+      if (packs > 0) fetch(lane);
+      for (int p = lane; p - lane < packs; p += 32 * kAhead) {
         float best = largest(u[0]);
 #pragma unroll
         for (int i = 1; i < kAhead; i++) best = fmaxf(best, largest(u[i]));
@@ -236,15 +239,21 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
             w2 = fma2(e, f2(t.x, t.y), w2);
           }
         }
+        uint32_t lanes = 0;
         if constexpr (TOP) {
           if (begins && p == lane) tops.start(__shfl_sync(~0u, sort32(best), a.top - 1));
           // lanes with a word that may matter (a NaN, which the maxima leave out, shows in the sum): the warp looks at
-          // their words together, a word to a lane
-          uint32_t lanes = __ballot_sync(~0u, !(best < tops.bound_value) || sum_of(s2) != sum_of(s2));
+          // their words together, a word to a lane, with the next round's loads on their way
+          lanes = __ballot_sync(~0u, !(best < tops.bound_value) || sum_of(s2) != sum_of(s2));
+          if (lanes != 0) {
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) u[i].store(s_words[threadIdx.x >> 5][i][lane]);
+          }
+        }
+        if (p - lane + 32 * kAhead < packs) fetch(p + 32 * kAhead);
+        if constexpr (TOP) {
           if (lanes != 0) {
             T(*words)[32][8] = s_words[threadIdx.x >> 5];
-#pragma unroll
-            for (int i = 0; i < kAhead; i++) u[i].store(words[i][lane]);
             __syncwarp();
             for (; lanes != 0; lanes &= lanes - 1) {
               const int l = __ffs(lanes) - 1, pack = p - lane + l + (lane >> 3) * 32;
