@@ -96,23 +96,29 @@ struct Softmax {
   float m[NT][2], l[NT][2];
 };
 
-// Scores (C fragment of S^T: tokens g, g + 8 by queries 2c, 2c + 1, in units of
-// log 2) to weights. The maximum moves only if a score is more than 8 above it:
-// weights up to 2^8 lose nothing in binary32, and the rescaling of o and the
-// reduction over the lanes are skipped for almost every tile.
+// Scores (C fragment of S^T: tokens g, g + 8 by queries 2c, 2c + 1) to weights
+// 2^(scale2 s - m), scale2 = scale log2(e). The maximum moves only if a score is
+// more than 8 above it: weights up to 2^8 lose nothing in binary32, and the
+// rescaling of o and the reduction over the lanes are skipped for almost every
+// tile. The exponent is one fused operation, rounded once by its own size and
+// not by the score's: m's rounding is in every weight alike and cancels.
 template <int NT, int MT>
-__device__ __forceinline__ void softmax_step(float (&s)[NT][4], Softmax<NT>& st, float (&o)[MT][NT][4]) {
+__device__ __forceinline__ void softmax_step(float (&s)[NT][4], float scale2, bool live0, bool live1, Softmax<NT>& st,
+                                             float (&o)[MT][NT][4]) {
+  auto larger = [&](int nt, int j) {
+    return fmaxf(live0 ? s[nt][j] * scale2 : -INFINITY, live1 ? s[nt][2 + j] * scale2 : -INFINITY);
+  };
   bool rise = false;
 #pragma unroll
   for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-    for (int j = 0; j < 2; j++) rise |= fmaxf(s[nt][j], s[nt][2 + j]) > st.m[nt][j] + 8.f;
+    for (int j = 0; j < 2; j++) rise |= larger(nt, j) > st.m[nt][j] + 8.f;
   if (__any_sync(~0u, rise)) {
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
       for (int j = 0; j < 2; j++) {
-        float top = fmaxf(s[nt][j], s[nt][2 + j]);
+        float top = larger(nt, j);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
         top = fmaxf(top, st.m[nt][j]);
@@ -131,9 +137,9 @@ __device__ __forceinline__ void softmax_step(float (&s)[NT][4], Softmax<NT>& st,
   for (int nt = 0; nt < NT; nt++)
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-      const float m = st.m[nt][j] == -INFINITY ? 0.f : st.m[nt][j];  // no token yet: every weight is 0
-      s[nt][j] = exp2_fast(s[nt][j] - m);
-      s[nt][2 + j] = exp2_fast(s[nt][2 + j] - m);
+      const float m = st.m[nt][j] == -INFINITY ? 0.f : st.m[nt][j];  // scores of -inf alone so far: their weights are 0
+      s[nt][j] = live0 ? exp2_fast(fmaf(s[nt][j], scale2, -m)) : 0.f;
+      s[nt][2 + j] = live1 ? exp2_fast(fmaf(s[nt][2 + j], scale2, -m)) : 0.f;
       st.l[nt][j] += s[nt][j] + s[nt][2 + j];
     }
 }
@@ -232,7 +238,10 @@ struct Tile<uint16_t, DP, NT> {
 };
 
 // binary32: every operand as the sum of two tf32 values, three products
-// (hi hi, hi lo, lo hi); what is left out is below 2^-21 of a product.
+// (hi hi, hi lo, lo hi); what is left out is below 2^-21 of a product. The
+// instruction truncates its sum, which over a chain of them adds up to a bias
+// (5.7e-6 of the result after 36 tiles, where the operation in binary32 is
+// 1.7e-6 off): so chains are short, and their ends are added with rounding.
 template <int DP, int NT>
 struct Tile<float, DP, NT> {
   static constexpr int KC = DP / 16, VC = DP / 32, MT = DP / 16;
@@ -277,11 +286,25 @@ struct Tile<float, DP, NT> {
       for (int h = 0; h < VC; h++) v[t][h] = load4(p + 32 * h, r >= 0 && 32 * h + g4 < D);
     }
   }
+  __device__ __forceinline__ static void fold(float (&x)[NT][4], float (&s)[NT][4]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        s[nt][j] += x[nt][j];
+        x[nt][j] = 0.f;
+      }
+  }
   __device__ __forceinline__ void scores(const char* smem, float (&s)[NT][4]) const {
     const uint4* q = reinterpret_cast<const uint4*>(smem) + (threadIdx.x & 31);
     float x[NT][4] = {}, y[NT][4] = {}, z[NT][4] = {};  // three chains of dependent instructions, not one
 #pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) s[nt][j] = 0.f;
+#pragma unroll
     for (int i = 0; i < KC; i++) {
+      if (i % 2 == 0 && i > 0) fold(x, s);
       const float* f0 = reinterpret_cast<const float*>(&k[0][i]);
       const float* f1 = reinterpret_cast<const float*>(&k[1][i]);
 #pragma unroll
@@ -303,7 +326,7 @@ struct Tile<float, DP, NT> {
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) s[nt][j] = x[nt][j] + (y[nt][j] + z[nt][j]);
+      for (int j = 0; j < 4; j++) s[nt][j] += x[nt][j] + (y[nt][j] + z[nt][j]);
   }
   __device__ __forceinline__ void accumulate(const float (&p)[NT][4], float (&o)[MT][NT][4]) const {
     const int lane = threadIdx.x & 31, from = (lane & 3) * 4 + (lane >> 3);
@@ -334,10 +357,12 @@ struct Tile<float, DP, NT> {
           split_tf32(f1[2 * jj + 1], a[3], b[3]);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
-            float(&acc)[4] = o[h * 2 + jj][nt];
-            mma_tf32(acc, a[0], a[1], a[2], a[3], ph[nt][t][0], ph[nt][t][1]);
-            mma_tf32(acc, a[0], a[1], a[2], a[3], pl[nt][t][0], pl[nt][t][1]);
+            float acc[4] = {};
             mma_tf32(acc, b[0], b[1], b[2], b[3], ph[nt][t][0], ph[nt][t][1]);
+            mma_tf32(acc, a[0], a[1], a[2], a[3], pl[nt][t][0], pl[nt][t][1]);
+            mma_tf32(acc, a[0], a[1], a[2], a[3], ph[nt][t][0], ph[nt][t][1]);
+#pragma unroll
+            for (int j = 0; j < 4; j++) o[h * 2 + jj][nt][j] += acc[j];
           }
         }
       }
@@ -370,6 +395,16 @@ struct Shape {
   static constexpr int DP = DP_;
   using Tl = Tile<T, DP, NT>;
   static constexpr int kThreads = 32 * kDaWarps * H;
+  // Resident blocks that the registers have to leave room for: as many as K, V and the accumulators let, where the rest
+  // are temporaries that can wait (left to itself the compiler takes 215 registers at 128 elements of bf16: 329 us
+  // against 318 for 64 requests up to 16384 tokens; binary32 at 80: 43 us against 36 for 33 requests).
+  static constexpr int kBytes = DP * (int)sizeof(T);  // of a row of K, padded
+  static constexpr int kBlocks = H > 1                        ? 1
+                                 : kBytes * NT <= 128         ? 4
+                                 : kBytes == 256 && DP == 128 ? (NT == 1 ? 3 : 2)
+                                 : kBytes <= 256              ? 3
+                                 : DP == 96 && NT == 1        ? 3
+                                                              : 2;
   static constexpr int Q = NT * 8 * H;           // query heads of an item
   static constexpr int kRow = DP + 4;
   static constexpr int kPartial = Q * (DP + 2);  // floats of a partial result: DP values a query, m, l
@@ -406,7 +441,7 @@ __device__ __forceinline__ Output<T> output_of(const DecodeArgs& a, const Part& 
 }
 
 template <typename T, int DP, int NT, int H>
-__global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attention_kernel(
+__global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT, H>::kBlocks) decode_attention_kernel(
     const __grid_constant__ DecodeArgs a) {
   using S = Shape<T, DP, NT, H>;
   using Tl = Tile<T, DP, NT>;
@@ -564,7 +599,7 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
     {
       int next = row_at(part.t0 + 1);
       const char* queries = sh.buf + half * Tl::kQueryBytes;
-      const float scale2 = a.scale * 1.4426950408889634f;  // scores in units of log 2
+      const float scale2 = a.scale * 1.4426950408889634f;
       for (int t = part.t0; t < t1; t++) {
         float s[NT][4];
         tile.scores(queries, s);
@@ -575,14 +610,7 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads) decode_attentio
           vc = reinterpret_cast<const T*>(a.v_cache[after.rank]);
         }
         if (kDaAhead<T, DP>) tile.load_k(kc, next, D);
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int j = 0; j < 2; j++) {
-            s[nt][j] = live0 ? s[nt][j] * scale2 : -INFINITY;
-            s[nt][2 + j] = live1 ? s[nt][2 + j] * scale2 : -INFINITY;
-          }
-        softmax_step<NT, MT>(s, st, o);
+        softmax_step<NT, MT>(s, scale2, live0, live1, st, o);
         tile.accumulate(s, o);
         if (kDaAhead<T, DP>) tile.load_v(vc, next, D);
         else tile.load_k(kc, next, D);

@@ -408,7 +408,9 @@ ATTENTION = [  # n, lens, q heads, kv heads, dim, page, dtype
     (1, ODD, 5, 1, 256, 2, "f32"), (1, ODD, 32, 2, 64, 16, "f32"), (2, ODD, 2, 1, 24, 1024, "f32"),
     (1, [100000, 3, 0, 4097], 8, 1, 128, 16, "bf16"), (1, [50001], 3, 1, 64, 128, "f32"),
     (1, [0, 0], 8, 2, 128, 16, "bf16"), (32, [40, 1300], 4, 2, 64, 16, "bf16"),
-    (1, [i % 300 for i in range(1111)], 2, 1, 64, 16, "bf16")]
+    (1, [i % 300 for i in range(1111)], 2, 1, 64, 16, "bf16"), (1, ODD, 16, 1, 256, 16, "bf16"),
+    (1, ODD, 20, 2, 128, 16, "f32"), (1, ODD, 12, 1, 96, 16, "f32"), (1, ODD, 9, 1, 192, 8, "f32"),
+    (1, [30000, 5], 16, 1, 192, 64, "bf16"), (2, [0, 70001], 12, 1, 88, 32, "f32")]
 
 
 @pytest.mark.parametrize("n,lens,q,kv,d,page,dtype", ATTENTION)
@@ -422,6 +424,22 @@ def test_decode_attention(n, lens, q, kv, d, page, dtype):
     again = torch.empty_like(out)
     B.decode_attention(x, k, v, table, ln, again, None, ws)
     assert torch.equal(out, again), "not the same bits twice"
+
+
+def test_decode_attention_weights_sum_to_one():
+    """Values of 1: a result is the sum of the weights over itself. Each of the two sums adds up to 144 tiles a warp (512
+    requests and ranks of 128 tiles over 456 blocks), the block's warps and the joins, every addition rounded: at most u
+    each. A sum that truncates drifts by half of that in one direction for each of a tile's several products."""
+    g = gen(16)
+    n, batch, d, page, length = 8, 64, 64, 128, 8192
+    blocks = length // page
+    k = normal(g, n, batch * blocks, 1, page, d)
+    v = torch.ones_like(k)
+    table = torch.randperm(batch * blocks, generator=g, device="cuda").to(torch.int32).view(batch, blocks)
+    lens = torch.full((batch,), length, dtype=torch.int32, device="cuda")
+    out, _, status, _ = run_attention(normal(g, n, batch, 8, d), k, v, table, lens)
+    assert status == B.Status.OK
+    assert float((out.double() - 1).abs().max()) <= (2 * 144 + 32) * U / 2
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
