@@ -390,6 +390,7 @@ def _op_stream(stream) -> int:
 
 
 def _op_dtype(dtype) -> int:
+    """The C ABI's number of an operator's dtype."""
     d = _OP_DTYPES.get(dtype)
     if d is None:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
@@ -401,6 +402,9 @@ def _refuse(what):
 
 
 _PACKS = {n: struct.Struct(f"{n}Q").pack for n in range(1, 33)}
+
+
+_PACK1 = _PACKS[1]
 
 
 def _pack(values):
@@ -421,9 +425,18 @@ def _ranked(x, name, dims):
         _refuse(f"{name}: {dims} dimensions a rank, in device memory")
     if not x.is_contiguous():
         return _ranked_list(x.unbind(0), name, dims)
+    if dims == 3:
+        width = full[2] * full[3]
+    else:
+        width = 1 if dims == 1 else full[2] if dims == 2 else full[2] * full[3] * full[4]
     base, step = x.data_ptr(), x.nbytes // n
-    width = 1 if dims == 1 else full[2] if dims == 2 else full[2] * full[3] if dims == 3 else full[2] * full[3] * full[4]
-    return (_pack(range(base, base + n * step, step)) if step else bytes(8 * n)), full, width, x.dtype
+    if n == 1:
+        ptrs = _PACK1(base)
+    elif step and n <= 32:
+        ptrs = _PACKS[n](*range(base, base + n * step, step))
+    else:
+        ptrs = _pack((base,) * n)
+    return ptrs, full, width, x.dtype
 
 
 def _ranked_list(x, name, dims):
@@ -445,11 +458,11 @@ def _ranked_list(x, name, dims):
 def _ranked_dense(x, name, dims):
     """_ranked of tensors without gaps."""
     r = _ranked(x, name, dims)
-    width = 1
-    for d in r[1][2:]:
-        width *= d
-    if r[2] != width:
-        _refuse(f"{name}: contiguous")
+    if type(x) is list or type(x) is tuple:
+        if not all(t.is_contiguous() for t in x):
+            _refuse(f"{name}: contiguous")
+    elif not x.is_contiguous():
+        _ranked_dense(x.unbind(0), name, dims)
     return r
 
 
@@ -504,9 +517,10 @@ def _rope_call(qkv, q_weight, k_weight, cos_sin, positions, q, kv_heads):
     dtype = qkv[3]
     if q[3] is not dtype or qkv[1] != (n, tokens, (q_heads + 2 * kv_heads) * dim):
         _refuse("qkv: [tokens, (q_heads + 2 kv_heads) head_dim], queries [tokens, q_heads, head_dim], of one dtype")
-    for w in (q_weight, k_weight):
-        if w.dtype is not dtype or w.numel() != dim or not w.is_contiguous() or not w.is_cuda:
-            _refuse("weights: head_dim contiguous elements of qkv's dtype in device memory")
+    if q_weight.dtype is not dtype or k_weight.dtype is not dtype or q_weight.numel() != dim \
+            or k_weight.numel() != dim or not q_weight.is_contiguous() or not k_weight.is_contiguous() \
+            or not q_weight.is_cuda or not k_weight.is_cuda:
+        _refuse("weights: head_dim contiguous elements of qkv's dtype in device memory")
     max_pos, rot = cos_sin.shape
     if cos_sin.dtype is not _FLOAT32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
         _refuse("cos_sin: contiguous float32 [max_pos, rot_dim] in device memory")

@@ -141,9 +141,9 @@ struct Chunks<float, INTER> {
   }
 };
 
-// A lane's four angles; (1, 0) where nothing turns.
+// A lane's four angles (1, 0 where nothing turns): cosines, sines, negative sines.
 struct Turn {
-  F2 c[2], s[2];
+  F2 c[2], s[2], n[2];
 };
 __device__ __forceinline__ Turn load_turn(const float* row, int rot, const Lane& n) {
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -151,7 +151,7 @@ __device__ __forceinline__ Turn load_turn(const float* row, int rot, const Lane&
     c = *reinterpret_cast<const float4*>(row + n.angle);
     s = *reinterpret_cast<const float4*>(row + (rot >> 1) + n.angle);
   }
-  return Turn{{f2(c.x, c.y), f2(c.z, c.w)}, {f2(s.x, s.y), f2(s.z, s.w)}};
+  return Turn{{f2(c.x, c.y), f2(c.z, c.w)}, {f2(s.x, s.y), f2(s.z, s.w)}, {f2(-s.x, -s.y), f2(-s.z, -s.w)}};
 }
 
 // R v, or R^T v with BACK.
@@ -160,9 +160,8 @@ __device__ __forceinline__ Row8 rotate(const Row8& v, const Turn& t) {
   Row8 r;
 #pragma unroll
   for (int j = 0; j < 2; j++) {
-    const F2 neg = mul2(t.s[j], f2(-1.f, -1.f));
-    r.p[j] = fma2(v.p[j + 2], BACK ? t.s[j] : neg, mul2(v.p[j], t.c[j]));
-    r.p[j + 2] = fma2(v.p[j], BACK ? neg : t.s[j], mul2(v.p[j + 2], t.c[j]));
+    r.p[j] = fma2(v.p[j + 2], BACK ? t.s[j] : t.n[j], mul2(v.p[j], t.c[j]));
+    r.p[j + 2] = fma2(v.p[j], BACK ? t.n[j] : t.s[j], mul2(v.p[j + 2], t.c[j]));
   }
   return r;
 }
@@ -173,6 +172,16 @@ __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
   for (int d = L / 2; d > 0; d >>= 1) x += __shfl_xor_sync(~0u, x, d, L);
   return x;
+}
+template <int L>
+__device__ __forceinline__ float2 group_sum2(float x, float y) {  // two sums side by side
+  F2 s = f2(x, y);
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) {
+    const float2 p = unpack(s);
+    s = add2(s, f2(__shfl_xor_sync(~0u, p.x, d, L), __shfl_xor_sync(~0u, p.y, d, L)));
+  }
+  return unpack(s);
 }
 __device__ __forceinline__ float rsqrt_fast(float x) {
   float y;
@@ -269,8 +278,8 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
   if (bad) op_report(a.ws, kErrCapacity);
 }
 
-// The gradient. z = R^T dy, dw = sum z x r, g = z w, xh = x r,
-// dx = r (g - xh mean(g xh)); dv is copied. A rank's blocks are of three kinds,
+// The gradient. z = R^T dy, dw = sum z x r, u = z w,
+// dx = r u - r^3 mean(u x) x; dv is copied. A rank's blocks are of three kinds,
 // for query heads, key heads and values, so one set of weights and weight sums
 // stays in registers. A group walks over tokens, head by head; rows of x and dy
 // come through a ring of kBwdStages rows in shared memory (16-byte asynchronous
@@ -299,7 +308,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
                                                                     int q_blocks, int k_blocks) {
   constexpr int kGroups = kBwdThreads / L, kRow = L * 8, kCopies = (int)sizeof(T) / 2;
   __shared__ __align__(16) T ring[kGroups][kBwdStages][2][kRow];
-  __shared__ float sums[kBwdThreads][9];
+  __shared__ float s_dw[kBwdThreads][9];
   __shared__ bool s_last;
   const uint32_t magic = op_magic(a.ws);
   const int rank = blockIdx.y, group = threadIdx.x / L, l = threadIdx.x & (L - 1), D = a.head_dim;
@@ -344,13 +353,12 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
   const int rows = first_walker < a.tokens ? ((a.tokens - 1 - first_walker) / walkers + 1) * heads : 0;
   const int mine = walker < a.tokens ? ((a.tokens - 1 - walker) / walkers + 1) * heads : 0;
 
-  // Pointers walk along: one head on within a token, then to the group's next token.
-  const int64_t x_jump = (int64_t)walkers * a.qkv_stride - (int64_t)(heads - 1) * D;
-  const int64_t g_jump = (int64_t)walkers * g_stride - (int64_t)(heads - 1) * D;
-  const int64_t d_jump = (int64_t)walkers * a.dqkv_stride - (int64_t)(heads - 1) * D;
-  const int64_t w0 = walker < a.tokens ? walker : 0;
-  const T* fx = xs + w0 * a.qkv_stride + place + l * 8;  // of the next row to ask for
-  const T* fg = gs + w0 * g_stride + l * 8;
+  // Pointers go one head on within a token, and are set anew at the group's next token.
+  const T* fx = xs + place + l * 8;  // of the next row to ask for
+  const T* fg = gs + l * 8;
+  int f_token = walker < a.tokens ? walker : 0;
+  fx += f_token * a.qkv_stride;
+  fg += f_token * g_stride;
   constexpr uint32_t kCell = kRow * sizeof(T), kSlot = 2 * kCell;  // bytes of a row of x or dy, of both
   const uint32_t cell = smem_addr(&ring[group][0][0][l * 8]);
   int f_left = mine, f_head = 0;
@@ -373,10 +381,14 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
     copy_async_commit();
     f_cell = f_cell == cell + (kBwdStages - 1) * kSlot ? cell : f_cell + kSlot;
     f_left--;
-    const bool wrap = ++f_head == heads;
-    fx += wrap ? x_jump : D;
-    fg += wrap ? g_jump : D;
-    f_head = wrap ? 0 : f_head;
+    fx += D;
+    fg += D;
+    if (++f_head == heads) {
+      f_head = 0;
+      f_token += walkers;
+      fx = xs + f_token * a.qkv_stride + place + l * 8;
+      fg = gs + f_token * g_stride + l * 8;
+    }
   };
   auto position = [&](int token) {
     const int pos = token < a.tokens ? a.positions[token] : 0;
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
   int token = walker, head = 0, slot = 0;
   Turn turn = load_turn(a.cos_sin + (int64_t)position(token) * a.rot, a.rot, n);
   int pos_next = position(token + walkers);
-  T* out = ds + w0 * a.dqkv_stride + place;
+  T* out = ds + (walker < a.tokens ? walker : 0) * a.dqkv_stride + place;
   const int stores = n.in ? mine : 0;
   if (!op_ready(a.ws, magic)) {
     copy_async_wait<0>();
@@ -402,20 +414,21 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
     x.load(ring[group][slot][0], n);
     dy.load(ring[group][slot][1], n);
     fetch();
-    const Row8 v = x.widen(), z = rotate<true>(dy.widen(), turn);
-    const float root = rsqrt_fast(fmaf(group_sum<L>(dot8(v, v)), inv, a.eps));
-    const Row8 xh = v * root, g = z * w;
-    dw = fma_row(z, xh, dw);
-    const float mean = inv * group_sum<L>(dot8(g, xh));
-    const F2 down = f2(-mean, -mean);
-    dy.narrow(fma_row(xh, Row8{{down, down, down, down}}, g) * root);
+    // with u = z w: dw += z x r, dx = r u - (r^3 mean(u x)) x; both sums at once
+    const Row8 v = x.widen(), z = rotate<true>(dy.widen(), turn), u = z * w;
+    const float2 sums = group_sum2<L>(dot8(v, v), dot8(u, v));
+    const float root = rsqrt_fast(fmaf(sums.x, inv, a.eps));
+    dw = fma_row(z * root, v, dw);
+    const float down = -inv * sums.y * root * root * root;
+    const F2 down2 = f2(down, down);
+    dy.narrow(fma_row(v, Row8{{down2, down2, down2, down2}}, u * root));
     if (r < stores) dy.store(out, n);
     slot = slot + 1 == kBwdStages ? 0 : slot + 1;
-    const bool wrap = ++head == heads;
-    out += wrap ? d_jump : D;
-    if (wrap) {
+    out += D;
+    if (++head == heads) {
       head = 0;
       token += walkers;
+      out = ds + token * a.dqkv_stride + place;
       turn = load_turn(a.cos_sin + (int64_t)pos_next * a.rot, a.rot, n);
       pos_next = position(token + walkers);
     }
@@ -427,8 +440,8 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
   float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset) + (int64_t)rank * gridDim.x * D;
 #pragma unroll
   for (int j = 0; j < 4; j++) {
-    sums[threadIdx.x][2 * j] = unpack(dw.p[j]).x;
-    sums[threadIdx.x][2 * j + 1] = unpack(dw.p[j]).y;
+    s_dw[threadIdx.x][2 * j] = unpack(dw.p[j]).x;
+    s_dw[threadIdx.x][2 * j + 1] = unpack(dw.p[j]).y;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += kBwdThreads) {
@@ -439,7 +452,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
     const int j = turned ? (e & 3) + (e < half ? 0 : 4) : INTER ? (e & 1) * 4 + ((e & 7) >> 1) : e & 7;
     float s = 0.f;
 #pragma unroll
-    for (int g = 0; g < kGroups; g++) s += sums[g * L + from][j];
+    for (int g = 0; g < kGroups; g++) s += s_dw[g * L + from][j];
     parts[(int64_t)blockIdx.x * D + e] = s;
   }
   // join: runs of kBwdJoin blocks of one kind, then the kind's runs
@@ -468,16 +481,16 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
         s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
       }
     }
-    sums[threadIdx.x][0] = s.x;
-    sums[threadIdx.x][1] = s.y;
-    sums[threadIdx.x][2] = s.z;
-    sums[threadIdx.x][3] = s.w;
+    s_dw[threadIdx.x][0] = s.x;
+    s_dw[threadIdx.x][1] = s.y;
+    s_dw[threadIdx.x][2] = s.z;
+    s_dw[threadIdx.x][3] = s.w;
     __syncthreads();
     const bool whole = apart > 1 || count == kind_blocks;
     float* out = whole ? (is_q ? a.dq_weight[rank] : a.dk_weight[rank]) : parts + (int64_t)from * D;
     for (int e = threadIdx.x; e < D; e += kBwdThreads) {
       float t = 0.f;
-      for (int k = 0; k < many && k < count; k++) t += sums[k * quads + (e >> 2)][e & 3];
+      for (int k = 0; k < many && k < count; k++) t += s_dw[k * quads + (e >> 2)][e & 3];
       out[e] = t;
     }
     if (whole) return;
