@@ -11,9 +11,9 @@
 //
 // The bytes of the logits bound it; instructions come close, so they are
 // counted: about 7 a word, packed binary32 operations where there are any.
-// Tiles of 1024 columns of all rows are cut into one equal range per resident
-// warp, so few rows use all SMs and many rows leave none idle, and no warp
-// waits for another (blocks that joined their warps' results at the end of
+// Tiles of 1024 columns of all rows are cut into about one equal range per
+// resident warp, so few rows use all SMs and many rows leave none idle, and no
+// warp waits for another (blocks that joined their warps' results at the end of
 // every row spent a fifth of the time at barriers). A row that a cut divides is
 // joined by the warp that arrives last at it.
 //
@@ -164,13 +164,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
   // neighbouring ranges go to different blocks, so that few workers still spread over the SMs
   const uint32_t worker = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
   if (worker >= a.workers) return;
-  // worker w's tiles start at w * each + min(w, more)
-  auto start_of = [&](uint32_t w) { return w * a.each + min(w, a.more); };
-  auto worker_of = [&](uint32_t tile) {
-    const uint32_t split = a.more * (a.each + 1);
+  const uint32_t per_row = a.first_tile[a.nranks];
+  // rows in a.cuts equal parts each, or (a.cuts 0) all tiles in one equal range a worker: w's start at w * each + min(w, more)
+  auto start_of = [&](uint32_t w) {
+    return a.cuts > 0 ? w / a.cuts * per_row + (uint32_t)((uint64_t)(w % a.cuts) * per_row / a.cuts)
+                      : w * a.each + min(w, a.more);
+  };
+  auto worker_of = [&](uint32_t row, bool last) {  // the one with the row's first or last tile
+    if (a.cuts > 0) return row * a.cuts + (last ? a.cuts - 1 : 0);
+    const uint32_t tile = row * per_row + (last ? per_row - 1 : 0), split = a.more * (a.each + 1);
     return tile < split ? tile / (a.each + 1) : a.more + (tile - split) / a.each;
   };
-  const uint32_t per_row = a.first_tile[a.nranks];
   const uint32_t end = start_of(worker + 1);
 
   for (uint32_t at = start_of(worker); at < end;) {
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
 
     bool whole = t0 == 0 && t1 == (int)per_row;  // this warp has the row's result
     if (!whole) {
-      const uint32_t wf = worker_of(row_first), wl = worker_of(row_first + per_row - 1);
+      const uint32_t wf = worker_of(row, false), wl = worker_of(row, true);
       const bool starts_at_wf = start_of(wf) == row_first;
       float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset);
       auto part_of = [&](uint32_t w) {  // of its first row, or of the row that starts in it and goes on
@@ -458,7 +462,12 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) 
   const int64_t tiles = (int64_t)a.rows * a.first_tile[a.nranks];
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   int64_t grid = imin((int64_t)resident, kLpMaxWorkers / kLpWarps);
-  a.workers = (uint32_t)imin(grid * kLpWarps, tiles);
+  // With alternatives, rows in whole numbers of equal parts where that leaves few warps idle: a cut costs its row
+  // another start of the list (2048 rows of 131072 words, in 2 parts each against 2.4: top 20 147 against 175 us, top 5
+  // 106 against 109, none 90 against 87).
+  const int64_t most = grid * kLpWarps, cuts = imin(most / a.rows, a.first_tile[a.nranks]);
+  a.cuts = a.top > 0 && (a.rows * cuts * 5 >= most * 4 || cuts == a.first_tile[a.nranks]) ? (uint32_t)cuts : 0;
+  a.workers = a.cuts > 0 ? (uint32_t)(a.rows * cuts) : (uint32_t)imin(most, tiles);
   a.each = (uint32_t)(tiles / a.workers);
   a.more = (uint32_t)(tiles % a.workers);
   grid = imin(grid, a.workers);
