@@ -7,7 +7,6 @@ If the library is missing the binding raises -- there is no fallback path.
 import ctypes
 import enum
 import os
-import struct
 from typing import Optional, Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -368,127 +367,27 @@ def token_logprobs_workspace_bytes(rows: int, top: int) -> int:
     return _op_bytes("rar_token_logprobs_workspace_bytes", rows, top)
 
 
-# A decode step makes these calls once a layer, so their checks are written for
-# few Python operations: _op_setup binds once what each call needs of torch.
+# The tensors are read and checked, and the C ABI called, by the CPython module
+# _operands (csrc/operands.c): a decode step makes these calls once a layer.
 _ops = None
 
 
 def _op_setup():
-    global _ops, _INT32, _FLOAT32, _OP_DTYPES, _raw_stream, _current_device
+    global _ops
     import torch
-    _INT32, _FLOAT32 = torch.int32, torch.float32
-    _OP_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
-    if torch.cuda.is_available():
-        torch.cuda.init()
-        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _ops = load_library()
+    try:
+        from . import _operands
+    except ImportError as e:
+        raise RuntimeError(f"{os.path.join(HERE, '_operands.so')} is missing: build it with `python "
+                           "collective_communication_gb300/build.py` (or __graft_entry__.build())") from e
+    lib = load_library()
+    names = ("rar_page_tables", "rar_qk_norm_rope", "rar_qk_norm_rope_cached", "rar_qk_norm_rope_backward",
+             "rar_decode_attention", "rar_token_logprobs", "rar_token_logprobs_backward")
+    _operands.setup(RarError, (torch.float32, torch.bfloat16, torch.int32),
+                    tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in names),
+                    torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    _ops = _operands
     return _ops
-
-
-def _op_stream(stream) -> int:
-    return _raw_stream(_current_device()) if stream is None else _stream_handle(stream)
-
-
-def _op_dtype(dtype) -> int:
-    """The C ABI's number of an operator's dtype."""
-    d = _OP_DTYPES.get(dtype)
-    if d is None:
-        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
-    return d
-
-
-def _refuse(what):
-    raise RarError(Status.ERR_ARG, what)
-
-
-_PACKS = {n: struct.Struct(f"{n}Q").pack for n in range(1, 33)}
-
-
-_PACK1 = _PACKS[1]
-
-
-def _pack(values):
-    """nranks pointers, or 64-bit counts, as a C array."""
-    n = len(values)
-    return _PACKS[n](*values) if n in _PACKS else struct.pack(f"{n}Q", *values)
-
-
-def _ranked(x, name, dims):
-    """A per-rank argument as (C array of the ranks' pointers, shape with the
-    rank first, row stride of a rank's tensor, dtype); the dimensions after a
-    row's are dense."""
-    if type(x) is list or type(x) is tuple:
-        return _ranked_list(x, name, dims)
-    full = x.shape
-    n = full[0]
-    if len(full) != dims + 1 or not x.is_cuda or n == 0:
-        _refuse(f"{name}: {dims} dimensions a rank, in device memory")
-    if not x.is_contiguous():
-        return _ranked_list(x.unbind(0), name, dims)
-    if dims == 3:
-        width = full[2] * full[3]
-    else:
-        width = 1 if dims == 1 else full[2] if dims == 2 else full[2] * full[3] * full[4]
-    base, step = x.data_ptr(), x.nbytes // n
-    if n == 1:
-        ptrs = _PACK1(base)
-    elif step and n <= 32:
-        ptrs = _PACKS[n](*range(base, base + n * step, step))
-    else:
-        ptrs = _pack((base,) * n)
-    return ptrs, full, width, x.dtype
-
-
-def _ranked_list(x, name, dims):
-    first = x[0]
-    shape, strides, dtype = first.shape, first.stride(), first.dtype
-    for t in x:
-        if t.shape != shape or t.stride() != strides or t.dtype is not dtype or not t.is_cuda:
-            _refuse(f"{name}: the ranks' tensors are alike and in device memory")
-    if len(shape) != dims:
-        _refuse(f"{name}: {dims} dimensions a rank")
-    width = 1
-    for i in range(dims - 1, 0, -1):
-        if shape[i] != 1 and strides[i] != width:
-            _refuse(f"{name}: dense after its first dimension")
-        width *= shape[i]
-    return _pack([t.data_ptr() for t in x]), (len(x), *shape), strides[0] if shape[0] > 1 else width, dtype
-
-
-def _ranked_dense(x, name, dims):
-    """_ranked of tensors without gaps."""
-    r = _ranked(x, name, dims)
-    if type(x) is list or type(x) is tuple:
-        if not all(t.is_contiguous() for t in x):
-            _refuse(f"{name}: contiguous")
-    elif not x.is_contiguous():
-        _ranked_dense(x.unbind(0), name, dims)
-    return r
-
-
-def _ints(t, name, numel):
-    if t.dtype is not _INT32 or t.numel() != numel or not t.is_contiguous() or not t.is_cuda:
-        _refuse(f"{name}: {numel} contiguous int32 in device memory")
-    return t.data_ptr()
-
-
-def _floats(t, name, numel):
-    if t.dtype is not _FLOAT32 or t.numel() != numel or not t.is_contiguous() or not t.is_cuda:
-        _refuse(f"{name}: {numel} contiguous float32 in device memory")
-    return t.data_ptr()
-
-
-def _table(t, rows):
-    """(pointer, row stride, columns) of a block table."""
-    shape = t.shape
-    if t.dtype is not _INT32 or len(shape) != 2 or shape[0] != rows or not t.is_cuda:
-        _refuse("block_table: int32 [requests, max_blocks] in device memory")
-    blocks = shape[1]
-    if t.is_contiguous():
-        return t.data_ptr(), blocks, blocks
-    if blocks != 1 and t.stride(1) != 1:
-        _refuse("block_table: dense rows")
-    return t.data_ptr(), t.stride(0) if rows > 1 else blocks, blocks
 
 
 def page_tables(lens, new_tokens, free_pages, free_count, block_table, page_size: int, num_pages: int, lens_out, starts,
@@ -497,48 +396,20 @@ def page_tables(lens, new_tokens, free_pages, free_count, block_table, page_size
     (int32 tensors): new entries of block_table [requests, max_blocks] in place,
     lens_out, starts [requests + 1], positions and slots [most tokens of a
     step], free_count_out [1]."""
-    lib = _ops or _op_setup()
-    n, tokens, free = lens.numel(), slots.numel(), free_pages.numel()
-    table, stride, blocks = _table(block_table, n)
-    st = lib.rar_page_tables(
-        _ints(lens, "lens", n), _ints(new_tokens, "new_tokens", n), n, _ints(free_pages, "free_pages", free), free,
-        _ints(free_count, "free_count", 1), page_size, num_pages, table, stride, blocks,
-        _ints(lens_out, "lens_out", n), _ints(starts, "starts", n + 1), _ints(positions, "positions", tokens),
-        _ints(slots, "slots", tokens), tokens, _ints(free_count_out, "free_count_out", 1), workspace.ptr,
-        workspace.nbytes, _op_stream(stream))
+    st = (_ops or _op_setup()).page_tables(
+        lens, new_tokens, free_pages, free_count, block_table, page_size, num_pages, lens_out, starts, positions, slots,
+        free_count_out, workspace.ptr, workspace.nbytes, stream)
     if st:
         _check(st, "rar_page_tables")
-
-
-def _rope_call(qkv, q_weight, k_weight, cos_sin, positions, q, kv_heads):
-    """What the forms of the norm and rotation share: qkv [tokens, (q + 2 kv
-    heads) * head_dim] against queries [tokens, q_heads, head_dim]."""
-    n, tokens, q_heads, dim = q[1]
-    dtype = qkv[3]
-    if q[3] is not dtype or qkv[1] != (n, tokens, (q_heads + 2 * kv_heads) * dim):
-        _refuse("qkv: [tokens, (q_heads + 2 kv_heads) head_dim], queries [tokens, q_heads, head_dim], of one dtype")
-    if q_weight.dtype is not dtype or k_weight.dtype is not dtype or q_weight.numel() != dim \
-            or k_weight.numel() != dim or not q_weight.is_contiguous() or not k_weight.is_contiguous() \
-            or not q_weight.is_cuda or not k_weight.is_cuda:
-        _refuse("weights: head_dim contiguous elements of qkv's dtype in device memory")
-    max_pos, rot = cos_sin.shape
-    if cos_sin.dtype is not _FLOAT32 or not cos_sin.is_contiguous() or not cos_sin.is_cuda:
-        _refuse("cos_sin: contiguous float32 [max_pos, rot_dim] in device memory")
-    return (qkv[0], n, tokens, qkv[2], q_weight.data_ptr(), k_weight.data_ptr(), cos_sin.data_ptr(), max_pos, rot), \
-        _ints(positions, "positions", tokens), (q_heads, kv_heads, dim, _op_dtype(dtype))
 
 
 def qk_norm_rope(qkv, q_weight, k_weight, cos_sin, positions, q_out, k_out, workspace: OpWorkspace, eps: float = 1e-6,
                  interleaved: bool = False, stream=None) -> None:
     """Enqueue the norm and rotation of every rank's queries and keys: q_out
     [tokens, q_heads, head_dim] and k_out [tokens, kv_heads, head_dim] a rank."""
-    lib = _ops or _op_setup()
-    q, k = _ranked(q_out, "q_out", 3), _ranked(k_out, "k_out", 3)
-    head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, k[1][2])
-    if k[3] is not q[3] or k[1] != (*q[1][:2], heads[1], heads[2]):
-        _refuse("k_out: [tokens, kv_heads, head_dim]")
-    st = lib.rar_qk_norm_rope(*head, interleaved, pos, *heads, eps, q[0], q[2], k[0], k[2], workspace.ptr,
-                              workspace.nbytes, _op_stream(stream))
+    st = (_ops or _op_setup()).qk_norm_rope(
+        qkv, q_weight, k_weight, cos_sin, positions, q_out, eps, interleaved, k_out, workspace.ptr, workspace.nbytes,
+        stream)
     if st:
         _check(st, "rar_qk_norm_rope")
 
@@ -547,15 +418,9 @@ def qk_norm_rope_cached(qkv, q_weight, k_weight, cos_sin, positions, slots, q_ou
                         workspace: OpWorkspace, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """Enqueue the norm and rotation, keys and values into the paged caches
     [num_pages, kv_heads, page_size, head_dim] a rank at slots."""
-    lib = _ops or _op_setup()
-    q = _ranked(q_out, "q_out", 3)
-    k, v = _ranked_dense(k_cache, "k_cache", 4), _ranked_dense(v_cache, "v_cache", 4)
-    n, pages, kv_heads, page, dim = k[1]
-    head, pos, heads = _rope_call(_ranked(qkv, "qkv", 2), q_weight, k_weight, cos_sin, positions, q, kv_heads)
-    if n != head[1] or v[1] != k[1] or k[3] is not q[3] or v[3] is not q[3] or dim != heads[2]:
-        _refuse("k_cache, v_cache: [num_pages, kv_heads, page_size, head_dim]")
-    st = lib.rar_qk_norm_rope_cached(*head, interleaved, pos, _ints(slots, "slots", head[2]), *heads, eps, q[0], q[2],
-                                     k[0], v[0], pages, page, workspace.ptr, workspace.nbytes, _op_stream(stream))
+    st = (_ops or _op_setup()).qk_norm_rope_cached(
+        qkv, q_weight, k_weight, cos_sin, positions, q_out, eps, interleaved, slots, k_cache, v_cache, workspace.ptr,
+        workspace.nbytes, stream)
     if st:
         _check(st, "rar_qk_norm_rope_cached")
 
@@ -565,20 +430,9 @@ def qk_norm_rope_backward(qkv, q_weight, k_weight, cos_sin, positions, dq, dk, d
     """Enqueue the gradient: dqkv (as qkv) and float32 dq_weight, dk_weight
     [head_dim] a rank from dq [tokens, q_heads, head_dim], dk and dv [tokens,
     kv_heads, head_dim]."""
-    lib = _ops or _op_setup()
-    q, k, v = _ranked(dq, "dq", 3), _ranked(dk, "dk", 3), _ranked(dv, "dv", 3)
-    x, d = _ranked(qkv, "qkv", 2), _ranked(dqkv, "dqkv", 2)
-    head, pos, heads = _rope_call(x, q_weight, k_weight, cos_sin, positions, q, k[1][2])
-    if k[3] is not q[3] or v[3] is not q[3] or v[1] != k[1] or k[1] != (*q[1][:2], heads[1], heads[2]):
-        _refuse("dk, dv: [tokens, kv_heads, head_dim]")
-    if d[1] != x[1] or d[3] is not x[3]:
-        _refuse("dqkv: as qkv")
-    wq, wk = _ranked(dq_weight, "dq_weight", 1), _ranked(dk_weight, "dk_weight", 1)
-    for w in (wq, wk):
-        if w[1] != (head[1], heads[2]) or w[3] is not _FLOAT32 or w[2] != 1:
-            _refuse("dq_weight, dk_weight: float32 [head_dim]")
-    st = lib.rar_qk_norm_rope_backward(*head, interleaved, pos, *heads, eps, q[0], q[2], k[0], k[2], v[0], v[2], d[0],
-                                       d[2], wq[0], wk[0], workspace.ptr, workspace.nbytes, _op_stream(stream))
+    st = (_ops or _op_setup()).qk_norm_rope_backward(
+        qkv, q_weight, k_weight, cos_sin, positions, dq, eps, interleaved, dk, dv, dqkv, dq_weight, dk_weight,
+        workspace.ptr, workspace.nbytes, stream)
     if st:
         _check(st, "rar_qk_norm_rope_backward")
 
@@ -589,61 +443,20 @@ def decode_attention(q, k_cache, v_cache, block_table, lens, out, lse, workspace
     head_dim] a rank, caches as qk_norm_rope_cached writes them, int32
     block_table [batch, max_blocks] and lens [batch]; lse float32 [batch,
     q_heads] a rank, or None. scale: head_dim ** -0.5 by default."""
-    lib = _ops or _op_setup()
-    x, o = _ranked(q, "q", 3), _ranked(out, "out", 3)
-    k, v = _ranked_dense(k_cache, "k_cache", 4), _ranked_dense(v_cache, "v_cache", 4)
-    dtype = x[3]
-    n, batch, q_heads, dim = x[1]
-    kn, pages, kv_heads, page, kdim = k[1]
-    if kn != n or kdim != dim or v[1] != k[1] or o[1] != x[1] or k[3] is not dtype or v[3] is not dtype \
-            or o[3] is not dtype:
-        _refuse("q, out: [batch, q_heads, head_dim]; caches: [num_pages, kv_heads, page_size, head_dim]")
-    table, stride, blocks = _table(block_table, batch)
-    lse_p = None
-    if lse is not None:
-        e = _ranked_dense(lse, "lse", 2)
-        if e[1] != (n, batch, q_heads) or e[3] is not _FLOAT32:
-            _refuse("lse: float32 [batch, q_heads]")
-        lse_p = e[0]
-    st = lib.rar_decode_attention(
-        x[0], x[2], k[0], v[0], n, batch, q_heads, kv_heads, dim, _op_dtype(dtype), pages, page, table, stride, blocks,
-        _ints(lens, "lens", batch), dim ** -0.5 if scale is None else scale, o[0], o[2], lse_p, workspace.ptr,
-        workspace.nbytes, _op_stream(stream))
+    st = (_ops or _op_setup()).decode_attention(
+        q, k_cache, v_cache, block_table, lens, out, lse, scale, workspace.ptr, workspace.nbytes, stream)
     if st:
         _check(st, "rar_decode_attention")
-
-
-def _shards(x, name):
-    """(pointers, vocabulary of each shard, row strides, nranks, rows, dtype); shards may differ in width."""
-    if type(x) is not list and type(x) is not tuple:
-        p, (n, rows, width), stride, dtype = _ranked(x, name, 2)
-        return p, _pack((width,) * n), _pack((stride,) * n), n, rows, dtype
-    ones = [_ranked_list((t,), name, 2) for t in x]
-    rows, dtype = ones[0][1][1], ones[0][3]
-    for o in ones:
-        if o[1][1] != rows or o[3] is not dtype:
-            _refuse(f"{name}: [rows, vocabulary of the shard], of one dtype")
-    return (b"".join([o[0] for o in ones]), _pack([o[1][2] for o in ones]), _pack([o[2] for o in ones]), len(ones), rows,
-            dtype)
 
 
 def token_logprobs(logits, tokens, logprob, entropy, lse, top_values, top_ids, workspace: OpWorkspace,
                    stream=None) -> None:
     """Enqueue log probabilities of int32 tokens [rows] over vocabulary shards
-    logits [rows, shard] a rank: float32 logprob, entropy, lse [rows] and the top
-    alternatives' float32 top_values and int32 top_ids [rows, top] (None, or top
-    0: none)."""
-    lib = _ops or _op_setup()
-    p, vocab, strides, n, rows, dtype = _shards(logits, "logits")
-    top = 0 if top_ids is None else top_ids.shape[1]
-    values_p = ids_p = None
-    if top:
-        values_p = _floats(top_values, "top_values", rows * top)
-        ids_p = _ints(top_ids, "top_ids", rows * top)
-    st = lib.rar_token_logprobs(
-        p, vocab, strides, n, rows, _op_dtype(dtype), _ints(tokens, "tokens", rows), _floats(logprob, "logprob", rows),
-        _floats(entropy, "entropy", rows), _floats(lse, "lse", rows), top, values_p, ids_p, workspace.ptr,
-        workspace.nbytes, _op_stream(stream))
+    logits [rows, shard] a rank (shards may differ in width): float32 logprob,
+    entropy, lse [rows] and the top alternatives' float32 top_values and int32
+    top_ids [rows, top] (None, or top 0: none)."""
+    st = (_ops or _op_setup()).token_logprobs(
+        logits, tokens, logprob, entropy, lse, top_values, top_ids, workspace.ptr, workspace.nbytes, stream)
     if st:
         _check(st, "rar_token_logprobs")
 
@@ -653,16 +466,9 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_ent
     """Enqueue the gradient with respect to the logits, from lse and entropy of
     token_logprobs and float32 gradients [rows] (grad_entropy None: no such
     term); dlogits as logits (in place is allowed)."""
-    lib = _ops or _op_setup()
-    p, vocab, strides, n, rows, dtype = _shards(logits, "logits")
-    dp, dvocab, dstrides, dn, drows, ddtype = _shards(dlogits, "dlogits")
-    if dn != n or drows != rows or ddtype is not dtype or dvocab != vocab:
-        _refuse("dlogits: as logits")
-    st = lib.rar_token_logprobs_backward(
-        p, vocab, strides, n, rows, _op_dtype(dtype), _ints(tokens, "tokens", rows), _floats(lse, "lse", rows),
-        _floats(entropy, "entropy", rows), _floats(grad_logprob, "grad_logprob", rows),
-        None if grad_entropy is None else _floats(grad_entropy, "grad_entropy", rows), dp, dstrides, workspace.ptr,
-        workspace.nbytes, _op_stream(stream))
+    st = (_ops or _op_setup()).token_logprobs_backward(
+        logits, tokens, lse, entropy, grad_logprob, grad_entropy, dlogits, workspace.ptr, workspace.nbytes,
+        stream)
     if st:
         _check(st, "rar_token_logprobs_backward")
 

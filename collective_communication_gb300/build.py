@@ -1,13 +1,15 @@
 """Build librar.so (the C-ABI library of sm_103a CUDA kernels) in-tree.
 
 nvcc compiles each translation unit for sm_103a only, in parallel, then links
-the shared library next to this file. Run as a script or through
+the shared library next to this file; gcc compiles _operands.so, which reads the
+operators' tensors for the Python binding. Run as a script or through
 __graft_entry__.build().
 """
 import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -52,8 +54,24 @@ def _compile(src, verbose_ptxas=False, debug=False):
     return obj, r.stderr
 
 
+def build_operands(force: bool = False) -> str:
+    """Compile _operands.so, the CPython module that marshals the operators' calls."""
+    target, source = os.path.join(HERE, "_operands.so"), os.path.join(CSRC, "operands.c")
+    if force or _stale(target, [source, os.path.join(ROOT, "include", "rar.h")]):
+        tmp = target + ".tmp%d" % os.getpid()
+        cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-fPIC", "-shared", "-fvisibility=hidden", "-I",
+               sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), source, "-o", tmp, "-lm"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed on operands.c:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, target)
+    return target
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
     """Compile and link librar.so (debug=True: librar_debug.so); returns its path."""
+    if not debug:  # one module serves both variants
+        build_operands(force)
     build_dir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
     os.makedirs(build_dir, exist_ok=True)
     if force:

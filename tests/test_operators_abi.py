@@ -170,3 +170,80 @@ def test_binding_refuses_host_tensors_and_shapes(lib):
         B.page_tables(lens, lens, lens, lens[:1], table, 16, 64, lens, lens, lens, lens, lens[:1], Ws)
     with pytest.raises(B.RarError):
         B.qk_norm_rope(torch.zeros(2, 3, 640), x[0, 0, 0], x[0, 0, 0], torch.zeros(4, 64), lens, x, x[:, :, :1], Ws)
+
+
+class OnDevice:
+    """A host tensor that says it is in device memory: for calls that must be refused before any launch."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class Ws:
+    ptr, nbytes = at(0), MIB
+
+
+def attention_call(torch, **kw):
+    d = lambda *s, dtype=torch.float32: OnDevice(torch.zeros(*s, dtype=dtype))
+    i32 = torch.int32
+    a = dict(q=d(2, 3, 8, 64), k=d(2, 4, 2, 16, 64), v=d(2, 4, 2, 16, 64), table=d(3, 4, dtype=i32), lens=d(3, dtype=i32),
+             out=d(2, 3, 8, 64), lse=d(2, 3, 8))
+    a.update({k: v(d) if callable(v) else v for k, v in kw.items()})
+    B.decode_attention(*a.values(), Ws, stream=0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=lambda d: d(2, 3, 8, 32)), dict(q=lambda d: d(3, 8, 64)), dict(q=lambda d: d(2, 2, 8, 64)),
+    dict(q=lambda d: d(33, 3, 8, 64)), dict(q=lambda d: [d(3, 8, 64)]), dict(q=lambda d: [d(3, 8, 64), d(3, 8, 63)]),
+    dict(q=[]), dict(q=lambda d: [d(3, 8, 64)] * 33), dict(q=lambda d: d(1, 1, 1, 1, 2, 3, 8, 64)),
+    dict(q=lambda d: OnDevice(d(2, 3, 64, 8).t.transpose(2, 3))),
+    dict(k=lambda d: d(2, 4, 2, 16, 32)), dict(v=lambda d: d(2, 5, 2, 16, 64)),
+    dict(k=lambda d: OnDevice(d(2, 8, 2, 16, 64).t[:, ::2]), v=lambda d: OnDevice(d(2, 8, 2, 16, 64).t[:, ::2])),
+    dict(table=lambda d: d(3, 4)), dict(table=lambda d: OnDevice(d(4, 3).t.int().t())), dict(lens=lambda d: d(3)),
+    dict(out=lambda d: d(2, 3, 8, 32)), dict(lse=lambda d: d(2, 3, 4)), dict(lse=lambda d: OnDevice(d(2, 3, 16).t[..., ::2])),
+], ids=str)
+def test_binding_refuses_what_does_not_fit(lib, bad):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(B.RarError) as e:
+        attention_call(torch, **bad)
+    assert e.value.status == S.ERR_ARG
+
+
+def test_binding_refuses_dtypes(lib):
+    torch = pytest.importorskip("torch")
+    for dtype in (torch.float16, torch.int32, torch.float64):
+        with pytest.raises(TypeError):
+            attention_call(torch, q=lambda d: d(2, 3, 8, 64, dtype=dtype))
+        with pytest.raises(B.RarError):
+            attention_call(torch, k=lambda d: d(2, 4, 2, 16, 64, dtype=dtype))
+    with pytest.raises(AttributeError):
+        attention_call(torch, q=5)
+
+
+def test_binding_reads_a_list_that_shrinks(lib):
+    """Reading a tensor-like may run Python; the list it is in may change meanwhile."""
+    torch = pytest.importorskip("torch")
+    queries = []
+
+    class Shrinks(OnDevice):
+        def data_ptr(self):
+            del queries[1:]
+            return 0
+
+    queries += [Shrinks(torch.zeros(3, 8, 64)) for _ in range(4)]
+    with pytest.raises(IndexError):
+        attention_call(torch, q=queries)
+
+
+def test_binding_refuses_numbers_past_the_abi(lib):
+    torch = pytest.importorskip("torch")
+    i32 = lambda *s: OnDevice(torch.zeros(*s, dtype=torch.int32))
+    for page_size, pages in ((2**32 + 16, 64), (16, 2**32 + 64), (-16, 64), (16, -1), (12, 64)):
+        with pytest.raises(B.RarError) as e:
+            B.page_tables(i32(3), i32(3), i32(9), i32(1), i32(3, 4), page_size, pages, i32(3), i32(4), i32(5), i32(5), i32(1),
+                          Ws, stream=0)
+        assert e.value.status == S.ERR_ARG
