@@ -24,9 +24,10 @@
 // read) of them), and is read again and inserted where it belongs.
 // Measured: 2048 rows of 8 shards of 16003 words in bf16, 524 MB: 87 us without
 // alternatives (6.0 TB/s, 0.90 of the measured copy), 107 us with 5, 147 with 20:
-// the list's instructions. 3 rows of 131072 words, top 8: 13 us, a launch, a tile
-// and a join of 128 parts. The gradient, 2048 rows of 131072 words read and
-// written: 157 us, 6.8 TB/s (1.0 of the measured copy).
+// the list's instructions. 3 rows of 131072 words: 6.7 us without alternatives,
+// 11.4 with 8, 18.4 with 20: a launch, a tile and a join of 128 parts. The
+// gradient, 2048 rows of 131072 words read and written: 157 us, 6.8 TB/s (1.0 of
+// the measured copy).
 #include <cstdio>
 
 #include "op_common.cuh"
@@ -287,6 +288,15 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         if constexpr (TOP) tops.offer(mine ? top_key(v, word + e) : 0, a.top);
       }
     }
+    // the token's word, needed last, is on its way during the joins
+    const int64_t token = a.tokens[row];
+    float word_of_token = 0.f;
+    bool asked = false;
+    for (int r = 0; r < a.nranks; r++)
+      if (token >= a.first[r] && token < a.first[r + 1]) {
+        asked = true;
+        word_of_token = to_float(reinterpret_cast<const T*>(a.logits[r])[(int64_t)row * a.row_stride[r] + token - a.first[r]]);
+      }
     Stat st = warp_join(Stat{m, sum_of(s2), sum_of(w2)});
     if (!op_ready(a.ws, magic)) return;
 
@@ -305,60 +315,68 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         part[2] = st.w;
       }
       if (TOP && lane < a.top) reinterpret_cast<uint64_t*>(part + 4)[lane] = tops.list;
-      __threadfence();
       __syncwarp();
       uint32_t arrived = 0;
       if (lane == 0) {
+        // releases the warp's part, and acquires the others' if it is the last
         uint32_t* counter = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes) + wf;
-        arrived = atomicAdd(counter, 1u);
+        arrived = atom_add_acq_rel_u32(counter, 1u);
         if (arrived == wl - wf) *counter = 0;
       }
       whole = __shfl_sync(~0u, arrived, 0) == wl - wf;
+      __syncwarp();  // what lane 0 acquired is there for all lanes
       if (whole) {
-        __threadfence();
         // in the workers' order, whoever joins: a lane's share first, then over the lanes
         st = {-INFINITY, 0.f, 0.f};
         float head = -INFINITY;  // largest of the lane's parts' first alternatives
-        for (uint32_t w0 = wf + lane; w0 <= wl; w0 += 32 * 4) {
-          Stat q[4];
-          uint64_t k[4];
+        constexpr int kAt = 4;   // parts of a lane at a time
+        auto pair_of = [&](uint32_t w, int i) {
+          ulonglong2 v = make_ulonglong2(0, 0);
+          if (w <= wl) v = __ldcg(reinterpret_cast<const ulonglong2*>(part_of(w) + 4) + i / 2);
+          if (i + 1 >= a.top) v.y = 0;
+          return v;
+        };
+        for (uint32_t w0 = wf; w0 <= wl; w0 += 32 * kAt) {
+          Stat q[kAt];
+          uint64_t k[kAt];
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
+          for (int j = 0; j < kAt; j++) {
+            const uint32_t w = w0 + lane + 32 * j;
             q[j] = {-INFINITY, 0.f, 0.f};
-            k[j] = 0;
-            if (w0 + 32 * j <= wl) {
-              const float* from = part_of(w0 + 32 * j);
+            if (w <= wl) {
+              const float* from = part_of(w);
               q[j] = {__ldcg(from), __ldcg(from + 1), __ldcg(from + 2)};
-              if (TOP) k[j] = __ldcg(reinterpret_cast<const unsigned long long*>(from + 4));
             }
+            k[j] = 0;
+            if (TOP && w <= wl) k[j] = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(w) + 4));
           }
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
+          for (int j = 0; j < kAt; j++) {
             st = join(st, q[j]);
             if (TOP && k[j] != 0) head = fmaxf(head, key_value(k[j]));
           }
         }
         st = warp_join(st);
         if constexpr (TOP) {
+          // a lane offers its parts' alternatives in turn, until they fall below the bound
           tops = TopList();
           tops.start(__shfl_sync(~0u, sort32(head), a.top - 1));
-          // only parts whose first alternative is not below the bound have any to give: four at a time
-          for (uint32_t w0 = wf; w0 <= wl; w0 += 32) {
-            uint64_t first = 0;
-            if (w0 + lane <= wl) first = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(w0 + lane) + 4));
-            uint32_t votes = __ballot_sync(~0u, first > tops.bound);
-            while (votes != 0) {
-              uint64_t key[4];
+          for (uint32_t w0 = wf; w0 <= wl; w0 += 32 * kAt) {
+            ulonglong2 k[kAt];  // two alternatives of each
 #pragma unroll
-              for (int j = 0; j < 4; j++) {
-                const int src = __ffs(votes) - 1;  // -1 when there are no more
-                votes &= votes - 1;
-                key[j] = 0;
-                if (src >= 0 && lane < a.top)
-                  key[j] = __ldcg(reinterpret_cast<const unsigned long long*>(part_of(w0 + src) + 4) + lane);
+            for (int j = 0; j < kAt; j++) k[j] = pair_of(w0 + lane + 32 * j, 0);
+#pragma unroll 1
+            for (int j = 0; j < kAt; j++) {
+              ulonglong2 now = k[0];
+#pragma unroll
+              for (int i = 1; i < kAt; i++) k[i - 1] = k[i];
+              for (int i = 2;; i += 2) {
+                tops.offer(now.x, a.top);
+                tops.offer(now.y, a.top);
+                const bool more = i < a.top && now.y > tops.bound;
+                if (!__any_sync(~0u, more)) break;
+                now = more ? pair_of(w0 + lane + 32 * j, i) : make_ulonglong2(0, 0);
               }
-#pragma unroll
-              for (int j = 0; j < 4; j++) tops.offer(key[j], a.top);
             }
           }
         }
@@ -368,12 +386,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
       if (st.m == INFINITY) st.s = NAN;  // exp(inf - inf)
       const float log2_s = log2f(st.s), lse = st.m + kLn2 * log2_s;
       if (lane == 0) {
-        const int64_t token = a.tokens[row];
-        float lp = 0.f;
-        for (int r = 0; r < a.nranks; r++)
-          if (token >= a.first[r] && token < a.first[r + 1])
-            lp = to_float(reinterpret_cast<const T*>(a.logits[r])[(int64_t)row * a.row_stride[r] + token - a.first[r]]) - lse;
-        a.logprob[row] = lp;
+        a.logprob[row] = asked ? word_of_token - lse : 0.f;
         a.entropy[row] = kLn2 * (log2_s - st.w / st.s);
         a.lse[row] = lse;
       }
