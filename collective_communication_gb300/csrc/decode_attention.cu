@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
   const int D = a.head_dim;
   const int longest = a.max_blocks << a.page_shift;
   bool bad = false;
-  const uint32_t magic = op_magic(a.ws);
+  const uint32_t magic = op_start(a.ws);
 
   // Tiles of all requests: a segment of requests per thread, then a scan.
   auto length = [&](int b) {
@@ -824,7 +824,7 @@ cudaError_t launch_decode_attention(const DecodeArgs& a, cudaStream_t stream) {
     std::fprintf(stderr, "rar trace: decode_attention nranks=%d batch=%d heads=%d/%d dim=%d grid=%lld threads=%d\n",
                  a.nranks, a.batch, a.q_heads, a.kv_heads, a.head_dim, (long long)grid, k.threads);
   void* params[] = {const_cast<DecodeArgs*>(&a)};
-  return cudaLaunchKernel(k.fn, dim3((unsigned)grid), dim3(k.threads), params, (size_t)k.shared, stream);
+  return launch_op(k.fn, dim3((unsigned)grid), k.threads, k.shared, stream, params);
 }
 
 }  // namespace rar

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(THREADS) page_tables_kernel(const __grid_const
   // inverted (so below zero) if the request gets nothing
   __shared__ int32_t s_start[kChunk], s_off[kChunk];
   __shared__ int s_taken;
-  const uint32_t magic = op_magic(a.ws);
+  const uint32_t magic = op_start(a.ws);
   const int tid = threadIdx.x;
   const int P = 1 << a.page_shift;
   const int64_t width = (int64_t)a.max_blocks << a.page_shift;  // tokens that a table row can address
@@ -193,9 +193,9 @@ cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream) {
   if (trace_on())
     std::fprintf(stderr, "rar trace: page_tables requests=%d tokens=%d page=%d grid=%lld threads=%d\n", a.requests,
                  a.max_tokens, 1 << a.page_shift, (long long)grid, threads);
-  if (threads == 1024) page_tables_kernel<1024><<<(unsigned)grid, 1024, 0, stream>>>(a);
-  else page_tables_kernel<256><<<(unsigned)grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  void* params[] = {const_cast<PageTablesArgs*>(&a)};
+  const void* fn = threads == 1024 ? (const void*)page_tables_kernel<1024> : (const void*)page_tables_kernel<256>;
+  return launch_op(fn, dim3((unsigned)grid), threads, 0, stream, params);
 }
 
 }  // namespace rar

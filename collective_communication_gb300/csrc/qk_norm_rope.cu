@@ -211,7 +211,7 @@ template <typename T, int L, bool INTER, bool CACHE>
 __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int q_blocks,
                                                                int q_strips, int per_q, int kv_strips, int per_kv) {
   constexpr int kRows = kStrip<T>;
-  const uint32_t magic = op_magic(a.ws);
+  const uint32_t magic = op_start(a.ws);
   const int rank = blockIdx.y, D = a.head_dim;
   const Lane n = lane_of<INTER>(threadIdx.x & (L - 1), D, a.rot);
   const bool is_q = blockIdx.x < q_blocks;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
   __shared__ __align__(16) T ring[kGroups][kBwdStages][2][kRow];
   __shared__ float s_dw[kBwdThreads][9];
   __shared__ bool s_last;
-  const uint32_t magic = op_magic(a.ws);
+  const uint32_t magic = op_start(a.ws);
   const int rank = blockIdx.y, group = threadIdx.x / L, l = threadIdx.x & (L - 1), D = a.head_dim;
   const Lane n = lane_of<INTER>(l, D, a.rot);
   const T* xs = reinterpret_cast<const T*>(a.qkv[rank]);
@@ -562,7 +562,7 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
   const void* fn = a.dtype == kF32 ? forward_of<float>(lanes, a.interleaved != 0, cache)
                                    : forward_of<uint16_t>(lanes, a.interleaved != 0, cache);
   void* params[] = {const_cast<NormRopeArgs*>(&a), &q_blocks, &q_strips, &per_q, &kv_strips, &per_kv};
-  return cudaLaunchKernel(fn, grid, dim3(kNrThreads), params, 0, stream);
+  return launch_op(fn, grid, kNrThreads, 0, stream, params);
 }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, cudaStream_t stream) {
@@ -584,7 +584,7 @@ cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, cudaStream_t stream) 
     std::fprintf(stderr, "rar trace: qk_norm_rope_backward nranks=%d tokens=%d heads=%d/%d dim=%d rot=%d grid=%ux%u\n",
                  a.nranks, a.tokens, a.q_heads, a.kv_heads, a.head_dim, a.rot, grid.x, grid.y);
   void* params[] = {const_cast<NormRopeBwdArgs*>(&a), &q_blocks, &k_blocks};
-  return cudaLaunchKernel(fn, grid, dim3(kBwdThreads), params, 0, stream);
+  return launch_op(fn, grid, kBwdThreads, 0, stream, params);
 }
 
 }  // namespace rar

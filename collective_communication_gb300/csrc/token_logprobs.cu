@@ -165,7 +165,7 @@ template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int kAhead = 64 / (8 * (int)sizeof(T));  // packs of a lane in flight
   __shared__ __align__(16) T s_words[TOP ? kLpWarps : 1][kAhead][32][8];
-  const uint32_t magic = op_magic(a.ws);
+  const uint32_t magic = op_start(a.ws);
   const int lane = threadIdx.x & 31;
   // neighbouring ranges go to different blocks, so that few workers still spread over the SMs
   const uint32_t worker = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
@@ -407,7 +407,7 @@ constexpr int kLpBwdTile = kLpThreads * 8 * 8;
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a,
                                                                        int tiles) {
-  const uint32_t magic = op_magic(a.ws);
+  const uint32_t magic = op_start(a.ws);
   const int row = (int)(blockIdx.x / (unsigned)tiles), tile = (int)(blockIdx.x % (unsigned)tiles);
   const int rank = blockIdx.y, tid = threadIdx.x;
   const int64_t width = a.first[rank + 1] - a.first[rank], c0 = (int64_t)tile * kLpBwdTile;
@@ -493,7 +493,7 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) 
     std::fprintf(stderr, "rar trace: token_logprobs nranks=%d rows=%d vocab=%lld top=%d grid=%lld workers=%u\n", a.nranks,
                  a.rows, (long long)a.first[a.nranks], a.top, (long long)grid, a.workers);
   void* params[] = {&a};
-  return cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kLpThreads), params, 0, stream);
+  return launch_op(fn, dim3((unsigned)grid), kLpThreads, 0, stream, params);
 }
 
 cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, cudaStream_t stream) {
@@ -507,7 +507,7 @@ cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, cudaStream_t stre
   const void* fn = a.dtype == kF32 ? (const void*)token_logprobs_bwd_kernel<float>
                                    : (const void*)token_logprobs_bwd_kernel<uint16_t>;
   void* params[] = {const_cast<LogprobBwdArgs*>(&a), &tiles};
-  return cudaLaunchKernel(fn, grid, dim3(kLpThreads), params, 0, stream);
+  return launch_op(fn, grid, kLpThreads, 0, stream, params);
 }
 
 }  // namespace rar

@@ -726,3 +726,96 @@ def test_uninitialised_workspace_is_reported():
     out = torch.full_like(x, 7.0)
     B.decode_attention(x, k, v, table, ln, out, None, ws)
     assert B.get_status(ws) == B.Status.ERR_WORKSPACE and bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("way", ["one stream", "two streams", "graph", "torch between"])
+def test_operators_follow_one_another(way):
+    """A kernel may come up before the one ahead of it has ended, and has to wait for its results: steps whose
+    operators each read what the last one wrote, and write over what it read, give the bits of the same steps with
+    a synchronisation after every operator."""
+    n, rows, q, kv, d, page, steps = 4, 40, 8, 2, 64, 4, 18
+    g = gen(91)
+    qkv = normal(g, steps, n, rows, (q + 2 * kv) * d, dtype=torch.bfloat16)
+    weights = [normal(g, d, dtype=torch.bfloat16) for _ in range(2)]
+    angles = torch.rand((64, d // 2), generator=g, device="cuda") * 6
+    cos_sin = torch.cat([angles.cos(), angles.sin()], 1).contiguous()
+    tokens = torch.randint(0, n * q * d, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    blocks = -(-steps // page)
+    pages = rows * blocks + 3
+    ones = ints(rows, 1)
+    gradient = torch.full((rows,), 0.5, device="cuda")
+
+    def f32(*shape):
+        return torch.zeros(shape, device="cuda")
+
+    def bf16(*shape):
+        return torch.zeros(shape, device="cuda", dtype=torch.bfloat16)
+
+    def prepared():
+        return dict(lens=ints(2 * rows, 0).view(2, rows), count=i32(pages, 0).view(2, 1),
+                    free=torch.arange(pages, device="cuda", dtype=torch.int32),
+                    table=torch.zeros((rows, blocks), device="cuda", dtype=torch.int32), starts=ints(rows + 1),
+                    positions=ints(rows), slots=ints(rows), queries=bf16(n, rows, q, d), out=bf16(n, rows, q, d),
+                    k=bf16(n, pages, kv, page, d), v=bf16(n, pages, kv, page, d), dk=bf16(n, rows, kv, d),
+                    dqkv=bf16(n, rows, (q + 2 * kv) * d), logprob=f32(steps, rows), entropy=f32(steps, rows),
+                    lse=f32(steps, rows), values=f32(steps, rows, 5),
+                    ids=torch.zeros((steps, rows, 5), device="cuda", dtype=torch.int32), dw=f32(steps, 2, n, d),
+                    ws=B.OpWorkspace(max(B.decode_attention_workspace_bytes(n, rows, q, kv, d),
+                                         B.token_logprobs_workspace_bytes(rows, 5),
+                                         B.qk_norm_rope_workspace_bytes(n, d))))
+
+    def run(s, call):
+        for i in range(steps):
+            logits, now, next = s["out"].view(n, rows, q * d), i % 2, 1 - i % 2
+            lens = s["lens"][next]
+            call(B.page_tables, s["lens"][now], ones, s["free"], s["count"][now], s["table"], page, pages, lens, s["starts"],
+                 s["positions"], s["slots"], s["count"][next], s["ws"])
+            call(B.qk_norm_rope_cached, qkv[i], *weights, cos_sin, s["positions"], s["slots"], s["queries"], s["k"], s["v"],
+                 s["ws"])
+            call(B.decode_attention, s["queries"], s["k"], s["v"], s["table"], lens, s["out"], None, s["ws"])
+            call(B.token_logprobs, logits, tokens, s["logprob"][i], s["entropy"][i], s["lse"][i], s["values"][i],
+                 s["ids"][i], s["ws"])
+            call(B.token_logprobs_backward, logits, tokens, s["lse"][i], s["entropy"][i], gradient, None, logits, s["ws"])
+            call(B.qk_norm_rope_backward, qkv[i], *weights, cos_sin, s["positions"], s["out"], s["dk"], s["dk"], s["dqkv"],
+                 s["dw"][i, 0], s["dw"][i, 1], s["ws"])
+
+    def apart(f, *args):
+        f(*args)
+        torch.cuda.synchronize()
+
+    want = prepared()
+    run(want, apart)
+    got = prepared()
+    torch.cuda.synchronize()
+    if way == "one stream":
+        run(got, lambda f, *args: f(*args))
+    elif way == "two streams":
+        streams = [torch.cuda.Stream() for _ in range(2)]
+
+        def alternate(f, *args):
+            f(*args, stream=streams[0])
+            streams[1].wait_stream(streams[0])
+            streams.reverse()
+
+        run(got, alternate)
+    elif way == "graph":
+        first = {k: v.clone() for k, v in got.items() if k != "ws"}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(got, lambda f, *args: f(*args))
+        for _ in range(3):
+            for k, v in first.items():
+                got[k].copy_(v)
+            graph.replay()
+    else:
+        def between(f, *args):
+            f(*args)
+            got["dk"].add_(0)
+
+        run(got, between)
+    torch.cuda.synchronize()
+    assert B.get_status(want["ws"]) == B.Status.OK and B.get_status(got["ws"]) == B.Status.OK
+    assert want["lens"][steps % 2].tolist() == [steps] * rows
+    for k in want:
+        if k != "ws":
+            assert torch.equal(got[k], want[k]), k
