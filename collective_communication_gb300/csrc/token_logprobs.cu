@@ -23,9 +23,9 @@
 // word at or above the bound is rare after the first tile (about top / (words
 // read) of them), and is read again and inserted where it belongs.
 // Measured: 2048 rows of 8 shards of 16003 words in bf16, 524 MB: 87 us without
-// alternatives (6.0 TB/s, 0.90 of the measured copy), 107 us with 5, 147 with 20:
+// alternatives (6.0 TB/s, 0.90 of the measured copy), 107 us with 5, 136 with 20:
 // the list's instructions. 3 rows of 131072 words: 6.7 us without alternatives,
-// 11.4 with 8, 18.4 with 20: a launch, a tile and a join of 128 parts. The
+// 11 with 8, 16 with 20: a launch, a tile and a join of 128 parts. The
 // gradient, 2048 rows of 131072 words read and written: 157 us, 6.8 TB/s (1.0 of
 // the measured copy).
 #include <cstdio>
@@ -39,6 +39,12 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpTile = 1024;             // columns of a tile
 constexpr int kLpMaxWorkers = 4864;       // most warps of a forward launch: a counter and two partial results each
+// Alternatives are inserted one by one, and lanes' words looked at by the whole warp, where there are few; more are
+// sorted, and found by each lane on its own (3 rows of 24848 words in f32, top 20: 15.6 us against 22.1; 704 rows of
+// 80688 words in bf16, top 20: 56 against 66, top 5 no different).
+constexpr int kLpFewKeys = 6, kLpFewLanes = 4;
+// A row of few parts merges their lists, others pick from them (12 rows of 3381 words, top 20: 11.4 us against 15.5).
+constexpr int kLpFewParts = 8;
 constexpr int kLpPartFloats = 4 + 2 * 32;  // m, s, w, then 32 keys
 static_assert(kLpMaxWorkers <= kOpCounters, "one arrival counter per warp");
 
@@ -127,6 +133,21 @@ __device__ __forceinline__ uint64_t insert32(uint64_t list, uint64_t key) {
   return lane < at ? list : lane == at ? key : up;
 }
 
+// Sorts 32 keys over the lanes, largest in lane 0, from the stage whose runs have `size` lanes on (2: any keys;
+// 32: two runs, one falling and one rising).
+__device__ __forceinline__ uint64_t sort32(uint64_t k, int size) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (; size <= 32; size <<= 1)
+#pragma unroll 1
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      const uint64_t o = __shfl_xor_sync(~0u, k, d);
+      const bool large = ((lane & d) == 0) == ((lane & size) == 0 || size == 32);
+      k = (o > k) == large ? o : k;
+    }
+  return k;
+}
+
 // The largest of eight values, NaN left out.
 __device__ __forceinline__ float largest(const Pack8<uint16_t>& u) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u.u);
@@ -145,10 +166,20 @@ struct TopList {
   uint64_t list = 0, bound = 0;  // sorted over the lanes; keys not above the bound cannot be among the top
   float bound_value = -INFINITY;  // value of the bound, for quick tests: !(value < bound_value) lets a NaN in
 
-  // Every lane's key, 0 for none: those above the bound are inserted one after another.
+  // Another list, sorted likewise.
+  __device__ __forceinline__ void merge(uint64_t sorted) {
+    const uint64_t other = __shfl_xor_sync(~0u, sorted, 31);
+    list = sort32(other > list ? other : list, 32);
+  }
+  // Every lane's key, 0 for none: those above the bound are inserted one after another, or where there are many
+  // sorted (21 steps, about as long as 8 insertions) and merged.
   __device__ __forceinline__ void offer(uint64_t key, int top) {
     uint32_t votes = __ballot_sync(~0u, key > bound);
     if (votes == 0) return;
+    if (__popc(votes) > kLpFewKeys) {
+      merge(sort32(key > bound ? key : 0, 2));
+      votes = 0;
+    }
     for (; votes != 0; votes &= votes - 1) list = insert32(list, __shfl_sync(~0u, key, __ffs(votes) - 1));
     const uint64_t last = __shfl_sync(~0u, list, top - 1);
     bound = last > bound ? last : bound;
@@ -265,6 +296,26 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
           if (lanes != 0) {
             T(*words)[32][8] = s_words[threadIdx.x >> 5];
             __syncwarp();
+            if (__popc(lanes) > kLpFewLanes) {
+              // many, as in the first rounds: each lane walks through its own words
+              uint32_t mine = 0;
+#pragma unroll
+              for (int i = 0; i < kAhead; i++) {
+                Pack8<T> own;
+                own.load(words[i][lane]);
+                float v[8];
+                own.widen(v);
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                  if (p + i * 32 < packs && !(v[j] < tops.bound_value)) mine |= 1u << (i * 8 + j);
+              }
+              while (__any_sync(~0u, mine != 0)) {
+                const int b = __ffs(mine) - 1, i = b >> 3, j = b & 7;  // -1 when there are no more
+                tops.offer(mine != 0 ? top_key(to_float(words[i][lane][j]), word + (p + i * 32) * 8 + j) : 0, a.top);
+                mine &= mine - 1;
+              }
+              lanes = 0;
+            }
             for (; lanes != 0; lanes &= lanes - 1) {
               const int l = __ffs(lanes) - 1, pack = p - lane + l + (lane >> 3) * 32;
               const bool there = lane < 8 * kAhead && pack < packs;
@@ -358,10 +409,25 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         }
         st = warp_join(st);
         if constexpr (TOP) {
-          // a lane offers its parts' alternatives in turn, until they fall below the bound
+          // few parts: their lists one after another; many: a lane offers its parts' alternatives in turn, until they
+          // fall below the bound
           tops = TopList();
-          tops.start(__shfl_sync(~0u, sort32(head), a.top - 1));
-          for (uint32_t w0 = wf; w0 <= wl; w0 += 32 * kAt) {
+          const bool few = wl - wf < (uint32_t)min(kLpFewParts, a.top);
+          for (uint32_t w0 = wf; few && w0 <= wl; w0 += kAt) {
+            uint64_t k[kAt];
+#pragma unroll
+            for (int j = 0; j < kAt; j++)
+              k[j] = w0 + j <= wl && lane < a.top
+                         ? __ldcg(reinterpret_cast<const unsigned long long*>(part_of(w0 + j) + 4) + lane) : 0;
+#pragma unroll 1
+            for (int j = 0; j < kAt; j++) {
+              tops.merge(k[0]);
+#pragma unroll
+              for (int i = 1; i < kAt; i++) k[i - 1] = k[i];
+            }
+          }
+          if (!few) tops.start(__shfl_sync(~0u, sort32(head), a.top - 1));
+          for (uint32_t w0 = wf; !few && w0 <= wl; w0 += 32 * kAt) {
             ulonglong2 k[kAt];  // two alternatives of each
 #pragma unroll
             for (int j = 0; j < kAt; j++) k[j] = pair_of(w0 + lane + 32 * j, 0);

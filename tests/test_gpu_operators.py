@@ -819,3 +819,26 @@ def test_operators_follow_one_another(way):
     for k in want:
         if k != "ws":
             assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("top", [1, 2, 5, 6, 7, 8, 9, 31, 32])
+def test_token_logprobs_alternatives(top, dtype):
+    """One part a row to more than 128, words in rising and falling order, many alike, rows of -inf: every way in which
+    alternatives are found and joined gives the first of a stable sort."""
+    for seed, widths in enumerate(([40], [700, 900], [1024] * 5, [1700] * 4, [3000] * 5, [9000, 1], [16384] * 8,
+                                   [32768] * 5)):
+        total = sum(widths)
+        parts, tokens = logits_case(60 + seed, len(widths), 6, widths, dtype, seed % 3, ties=seed % 2 == 1)
+        ramp = torch.arange(total, device="cuda").float() * 0.125
+        at = 0
+        for p in parts:
+            p[0] = ramp[at:at + p.shape[1]]
+            p[1] = -ramp[at:at + p.shape[1]]
+            p[2] = 1.5
+            p[3] = float("-inf")
+            at += p.shape[1]
+        o, _ = run_logprobs(parts, tokens, top)
+        x = torch.cat([p.double() for p in parts], 1)
+        order = torch.sort(x, dim=1, descending=True, stable=True)
+        assert torch.equal(o["top_ids"].long(), order.indices[:, :top]), widths
