@@ -842,3 +842,11 @@ def test_token_logprobs_alternatives(top, dtype):
         x = torch.cat([p.double() for p in parts], 1)
         order = torch.sort(x, dim=1, descending=True, stable=True)
         assert torch.equal(o["top_ids"].long(), order.indices[:, :top]), widths
+
+
+@pytest.mark.parametrize("rows,widths,dtype,offset", [
+    (700, [501, 499], "bf16", 7), (1300, [2051], "f32", 1), (1217, [3071], "f32", 0), (409, [1, 700, 2049], "bf16", 0),
+    (2500, [8], "bf16", 0)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_token_logprobs_backward_of_many_narrow_rows(rows, widths, dtype, offset, in_place):
+    test_token_logprobs_backward(rows, widths, dtype, offset, True, in_place)
