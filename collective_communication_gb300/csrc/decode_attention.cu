@@ -15,7 +15,8 @@
 // for a product of 8 columns.
 //
 // Split. An item is one (request, rank, key head, group of 8 NT H query heads);
-// its tokens form tiles of 64. The tiles of all items in a row are cut into one
+// its tokens form tiles of 64. An item's units are its tiles and, ahead of them, one
+// or two for what it costs beside; the units of all items in a row are cut into one
 // equal range per resident block, whatever the lengths are, so a block may
 // finish one item, do whole ones and start another; the next item's first tile
 // is loaded before the last one's results are joined. An item that a cut divides
@@ -33,10 +34,10 @@
 // has about a tile in flight and waits on no barrier.
 //
 // Measured: 64 requests of up to 16384 tokens, 8 query heads and one key head of
-// 128 on each of 8 ranks, bf16, 2.15 GB: 317 us, 6.8 TB/s (1.0 of the measured
+// 128 on each of 8 ranks, bf16, 2.15 GB: 313 us, 6.9 TB/s (1.0 of the measured
 // copy). One request of 262145 tokens, 2 key heads: 55 us, 4.9 TB/s; 40 us are the
 // bytes, the rest the launch, the chain of lengths, tables and first tiles, and
-// two joins. 33 requests of up to 3001 tokens of 80 elements of f32: 37 us, 3.4
+// two joins. 33 requests of up to 3001 tokens of 80 elements of f32: 35 us, 3.6
 // TB/s: the same chain, and three products for one.
 #include <cstdio>
 
@@ -391,8 +392,8 @@ constexpr bool kDaAhead = DP * sizeof(T) <= 512;
 // Where a block's walk over the tiles stands: kept in shared memory so that the
 // loop over tiles has the registers.
 struct Part {
-  int64_t first;       // tiles before the request's, all items
-  int64_t item_first;  // first tile of the item
+  int64_t first;       // units before the request's, all items
+  int64_t tile_first;  // unit of the item's first tile
   int request, t0, t1, tiles, len;  // tiles t0..t1 of the item's `tiles`
   int rank, kvh, q0, queries;
 };
@@ -417,6 +418,10 @@ struct Shape {
                                  : DP == 96 && NT == 1        ? 3
                                                               : 2;
   static constexpr int Q = NT * 8 * H;           // query heads of an item
+  // What an item costs beside its tiles, in tiles: the start and the join of 8 query heads about one (232 requests of up to
+  // 448 tokens, 4 key heads of 128 on 8 ranks, bf16: 8 query heads a key head 147 us with one, 150 with 2, 201 with
+  // none; 16: 251, 211 and 377).
+  static constexpr int kStart = Q / 8;
   static constexpr int kRow = DP + 4;
   static constexpr int kPartial = Q * (DP + 2);  // floats of a partial result: DP values a query, m, l
   static constexpr int kMostParts = kDaMaxBlocks / kDaJoin + 1;
@@ -473,16 +478,17 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
     return n < 0 ? 0 : n > longest ? longest : n;
   };
   auto tiles_of = [](int n) { return (n + kDaTile - 1) / kDaTile; };
+  auto units_of = [&](int n) { return n == 0 ? 0 : S::kStart + tiles_of(n); };
   const int group = a.q_heads / a.kv_heads, qgroups = (group + Q - 1) / Q;
   const int per_request = a.nranks * a.kv_heads * qgroups;  // items of a request
   const int seg = (a.batch + kThreads - 1) / kThreads;
-  int64_t before = 0, mine = 0, total = 0;  // tiles of the requests before the thread's, its own, all
+  int64_t before = 0, mine = 0, total = 0;  // units of the requests before the thread's, its own, all
   {
     const int b0 = min(tid * seg, a.batch), b1 = min(b0 + seg, a.batch);
     for (int b = b0; b < b1; b++) {
       const int n = a.lens[b];
       if (n < 0 || n > longest) bad = true;
-      mine += tiles_of(length(b));
+      mine += units_of(length(b));
     }
     if (!op_ready(a.ws, magic)) return;
     int64_t scan = mine;
@@ -501,19 +507,19 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
     }
     total *= per_request;
   }
-  // the first `more` of the blocks with work have each + 1 tiles, the others each
+  // the first `more` of the blocks with work have each + 1 units, the others each
   const int64_t blocks = total < gridDim.x ? total : gridDim.x, each = blocks == 0 ? 0 : total / blocks;
   const int64_t more = total - each * blocks;
   auto start_of = [&](int64_t w) { return w * each + (w < more ? w : more); };
-  auto block_of = [&](int64_t tile) {
+  auto block_of = [&](int64_t unit) {
     const int64_t split = more * (each + 1);
-    return (int)(tile < split ? tile / (each + 1) : more + (tile - split) / each);
+    return (int)(unit < split ? unit / (each + 1) : more + (unit - split) / each);
   };
   if (block < blocks) {
-    const int64_t t = start_of(block) / per_request;  // lies in the same request, tiles counted once per item
+    const int64_t t = start_of(block) / per_request;  // lies in the same request, units counted once per item
     if (t >= before && t < before + mine) {
       int b = tid * seg;
-      for (int n; t >= before + (n = tiles_of(length(b))); b++) before += n;
+      for (int n; t >= before + (n = units_of(length(b))); b++) before += n;
       sh.part[1].first = before * per_request;
       sh.part[1].request = b;
     }
@@ -534,25 +540,26 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
     return;
   }
 
-  // The part that starts at tile `at` of the block's range, which lies in the request of `p` or after it.
+  // The part that starts at unit `at` of the block's range, which lies in the request of `from` or after it.
   auto describe = [&](Part& p, const Part& from, int64_t at) {
     const int64_t end = start_of(block + 1);
     p.t0 = p.t1 = 0;
     if (at >= end) return;
-    int b = from.request, n = tiles_of(length(b));
+    int b = from.request, n = units_of(length(b));
     int64_t first = from.first;
     while (at >= first + (int64_t)n * per_request) {
       first += (int64_t)n * per_request;
-      n = tiles_of(length(++b));
+      n = units_of(length(++b));
     }
     const int item = (int)((at - first) / n), qg = item % qgroups;
     p.first = first;
     p.request = b;
-    p.tiles = n;
+    p.tiles = n - S::kStart;
     p.len = length(b);
-    p.item_first = first + (int64_t)item * n;
-    p.t0 = (int)(at - p.item_first);
-    p.t1 = (int)(end - p.item_first < n ? end - p.item_first : n);
+    p.tile_first = first + (int64_t)item * n + S::kStart;
+    if (end <= p.tile_first) return;
+    p.t0 = (int)(at > p.tile_first ? at - p.tile_first : 0);
+    p.t1 = (int)(end - p.tile_first < p.tiles ? end - p.tile_first : p.tiles);
     p.kvh = item / qgroups % a.kv_heads;
     p.rank = item / qgroups / a.kv_heads;
     p.q0 = p.kvh * group + qg * Q;
@@ -572,6 +579,10 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
   __syncthreads();
   if (tid == 0) describe(sh.part[0], sh.part[1], start_of(block));
   __syncthreads();
+  if (sh.part[0].t1 == 0) {  // the range ends in an item's start
+    if (bad) op_report(a.ws, kErrCapacity);
+    return;
+  }
   Tl tile;
   int row = row_of(sh.part[0], sh.part[0].t0);
   tile.load_k(reinterpret_cast<const T*>(a.k_cache[sh.part[0].rank]), row, D);
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
   for (int i = 0;; i ^= 1) {
     const Part& part = sh.part[i];
     Part& after = sh.part[i ^ 1];
-    if (tid == 0) describe(after, part, part.item_first + part.t1);
+    if (tid == 0) describe(after, part, part.tile_first + part.t1);
     {
       const T* q = reinterpret_cast<const T*>(a.q[part.rank]) + (int64_t)part.request * a.q_stride + (int64_t)part.q0 * D;
 #pragma unroll
@@ -689,11 +700,9 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
       // The item is cut: its blocks cf..cl leave partial results, each run of kDaJoin blocks is joined by the one
       // of them that arrives last, and the runs by the last of those, in block order both times.
       float* parts = reinterpret_cast<float*>(a.ws + kOpScratchOffset);
-      const int64_t item_first = part.item_first;
-      const int cf = block_of(item_first), cl = block_of(item_first + part.tiles - 1);
-      const bool starts_at_cf = start_of(cf) == item_first;
-      auto part_of = [&](int b) {  // a block leaves up to two: of its first item, and of the last that starts in it
-        return parts + (2 * (int64_t)b + (b == cf && !starts_at_cf)) * S::kPartial;
+      const int cf = block_of(part.tile_first), cl = block_of(part.tile_first + part.tiles - 1);
+      auto part_of = [&](int b) {  // a block leaves up to two: of the item that it goes on with, and of one that it starts
+        return parts + (2 * (int64_t)b + (b == cf)) * S::kPartial;
       };
       float* mine_out = part_of(block);
       for (int i = tid; i < values; i += kThreads) {

@@ -850,3 +850,19 @@ def test_token_logprobs_alternatives(top, dtype):
 @pytest.mark.parametrize("in_place", [True, False])
 def test_token_logprobs_backward_of_many_narrow_rows(rows, widths, dtype, offset, in_place):
     test_token_logprobs_backward(rows, widths, dtype, offset, True, in_place)
+
+
+@pytest.mark.parametrize("q,d,dtype", [(8, 128, "bf16"), (16, 64, "bf16"), (9, 192, "bf16"), (5, 80, "f32")])
+def test_decode_attention_cuts(q, d, dtype):
+    """Lengths for which the blocks' ranges begin and end at every kind of place: in an item, at its first or last
+    tile, and between items."""
+    rng = torch.Generator().manual_seed(17)
+    for seed, (batch, longest) in enumerate([(1, 65), (2, 30000), (3, 64 * 500), (40, 700), (150, 130), (300, 64),
+                                             (450, 128), (700, 200), (911, 65), (913, 100)]):
+        lens = torch.randint(0, longest + 1, (batch,), generator=rng).tolist()
+        x, k, v, table, ln = attention_case(70 + seed, 1, lens, q, 1, d, 16, dtype)
+        out, lse, status, _ = run_attention(x, k, v, table, ln)
+        assert status == B.Status.OK
+        want, wlse, tol, ltol = attention64(x, k, v, table, ln, d ** -0.5, 16)
+        close(out, want, tol, "out")
+        close(lse, wlse, ltol, "lse")
