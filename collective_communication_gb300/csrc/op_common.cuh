@@ -257,10 +257,10 @@ struct LogprobArgs {
   int32_t* top_ids;
   char* ws;
   int rows, nranks, dtype, top;
-  // set by the launcher: tiles before each shard's in a row, warps with work; parts of a row, or 0 and the tiles of each
-  // warp and how many have one more
+  // set by the launcher: tiles before each shard's in a row, warps with work; parts of a row, or 0 and the units (of so
+  // many tiles: 1, or a row's) of each warp and how many have one more
   int first_tile[kMaxRanks + 1];
-  uint32_t workers, cuts, each, more;
+  uint32_t workers, cuts, unit, each, more;
 };
 
 struct LogprobBwdArgs {

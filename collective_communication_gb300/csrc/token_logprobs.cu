@@ -192,7 +192,8 @@ struct TopList {
   }
 };
 
-template <typename T, bool TOP>
+// NARROW: rows of few rounds, where it pays to look how much of a round there is.
+template <typename T, bool TOP, bool NARROW>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int kAhead = 64 / (8 * (int)sizeof(T));  // packs of a lane in flight
   __shared__ __align__(16) T s_words[TOP ? kLpWarps : 1][kAhead][32][8];
@@ -205,12 +206,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
   // rows in a.cuts equal parts each, or (a.cuts 0) all tiles in one equal range a worker: w's start at w * each + min(w, more)
   auto start_of = [&](uint32_t w) {
     return a.cuts > 0 ? w / a.cuts * per_row + (uint32_t)((uint64_t)(w % a.cuts) * per_row / a.cuts)
-                      : w * a.each + min(w, a.more);
+                      : (w * a.each + min(w, a.more)) * a.unit;
   };
   auto worker_of = [&](uint32_t row, bool last) {  // the one with the row's first or last tile
     if (a.cuts > 0) return row * a.cuts + (last ? a.cuts - 1 : 0);
-    const uint32_t tile = row * per_row + (last ? per_row - 1 : 0), split = a.more * (a.each + 1);
-    return tile < split ? tile / (a.each + 1) : a.more + (tile - split) / a.each;
+    const uint32_t at = (row * per_row + (last ? per_row - 1 : 0)) / a.unit, split = a.more * (a.each + 1);
+    return at < split ? at / (a.each + 1) : a.more + (at - split) / a.each;
   };
   const uint32_t end = start_of(worker + 1);
 
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         const F2 off = f2(neg, neg), log2e = f2(kLog2e, kLog2e);
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
+          if (NARROW && i > 0 && p - lane + i * 32 >= packs) break;
           float v[8];
           u[i].widen(v);
 #pragma unroll
@@ -536,10 +538,17 @@ int64_t token_logprobs_scratch_bytes(int, int) { return 2ll * kLpMaxWorkers * kL
 
 cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) {
   LogprobArgs a = args;
-  const void* fn = a.dtype == kF32 ? (a.top > 0 ? (const void*)token_logprobs_kernel<float, true>
-                                                : (const void*)token_logprobs_kernel<float, false>)
-                                   : (a.top > 0 ? (const void*)token_logprobs_kernel<uint16_t, true>
-                                                : (const void*)token_logprobs_kernel<uint16_t, false>);
+  int64_t widest = 0;
+  for (int r = 0; r < a.nranks; r++) widest = imax(widest, a.first[r + 1] - a.first[r]);
+  // bf16 (27691 rows of 2 shards of 1224 words: 45 us against 51; shards of 16003 words: 90 against 88). A round of f32 is
+  // half as many words and gained nothing.
+  const bool narrow = widest <= 8 * kLpTile;
+  const void* fn = a.dtype == kF32 ? (a.top > 0 ? (const void*)token_logprobs_kernel<float, true, false>
+                                                : (const void*)token_logprobs_kernel<float, false, false>)
+                   : narrow        ? (a.top > 0 ? (const void*)token_logprobs_kernel<uint16_t, true, true>
+                                                : (const void*)token_logprobs_kernel<uint16_t, false, true>)
+                                   : (a.top > 0 ? (const void*)token_logprobs_kernel<uint16_t, true, false>
+                                                : (const void*)token_logprobs_kernel<uint16_t, false, false>);
   int resident = 0;
   const cudaError_t e = resident_blocks(fn, kLpThreads, 0, &resident);
   if (e != cudaSuccess) return e;
@@ -554,8 +563,13 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) 
   const int64_t most = grid * kLpWarps, cuts = imin(most / a.rows, a.first_tile[a.nranks]);
   a.cuts = a.top > 0 && (a.rows * cuts * 5 >= most * 4 || cuts == a.first_tile[a.nranks]) ? (uint32_t)cuts : 0;
   a.workers = a.cuts > 0 ? (uint32_t)(a.rows * cuts) : (uint32_t)imin(most, tiles);
-  a.each = (uint32_t)(tiles / a.workers);
-  a.more = (uint32_t)(tiles % a.workers);
+  // More rows than warps stay whole if that leaves the warps few tiles apart, which cost less than the joins of two cut
+  // rows a warp (top 5, in us: 10046 rows of 8 tiles 52 against 64, 9000 of 30 112 against 122, 25000 of 16 equal, 16000
+  // of 30 205 against 201; none: 27691 of 4 41 against 45, 9000 of 30 equal, 5000 of 10 25 against 23).
+  const int64_t idle = (div_up(a.rows, most) * most - a.rows) * a.first_tile[a.nranks];
+  a.unit = a.rows >= most && idle <= most * (a.top > 0 ? 12 : 4) ? a.first_tile[a.nranks] : 1;
+  a.each = (uint32_t)(tiles / a.unit / a.workers);
+  a.more = (uint32_t)(tiles / a.unit % a.workers);
   grid = imin(grid, a.workers);
   if (trace_on())
     std::fprintf(stderr, "rar trace: token_logprobs nranks=%d rows=%d vocab=%lld top=%d grid=%lld workers=%u\n", a.nranks,

@@ -866,3 +866,10 @@ def test_decode_attention_cuts(q, d, dtype):
         want, wlse, tol, ltol = attention64(x, k, v, table, ln, d ** -0.5, 16)
         close(out, want, tol, "out")
         close(lse, wlse, ltol, "lse")
+
+
+@pytest.mark.parametrize("rows,widths,dtype,top", [
+    (5000, [1100, 30], "bf16", 5), (9731, [700], "f32", 20), (6000, [1030, 1027], "bf16", 0), (5001, [16400], "bf16", 1),
+    (4864, [333], "bf16", 2), (4865, [20, 1300], "f32", 3), (11000, [8200], "bf16", 0)])
+def test_token_logprobs_of_many_rows(rows, widths, dtype, top):
+    test_token_logprobs(rows, widths, dtype, top, 1, False)
