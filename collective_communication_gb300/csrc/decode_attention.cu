@@ -19,7 +19,9 @@
 // or two for what it costs beside; the units of all items in a row are cut into one
 // equal range per resident block, whatever the lengths are, so a block may
 // finish one item, do whole ones and start another; the next item's first tile
-// is loaded before the last one's results are joined. An item that a cut divides
+// and queries are loaded before the last one's results are joined (without the
+// queries 159 requests of 8 tokens, 4 key heads of 256 on 2 ranks, f32, took 41 us
+// instead of 34.5, 232 of up to 448 as below 148 instead of 143). An item that a cut divides
 // is joined by the blocks that arrive last at it, in two levels and in block
 // order. A block's four warps take 16 tokens of a tile each with a softmax of
 // their own, and join in shared memory at the end of an item.
@@ -34,10 +36,10 @@
 // has about a tile in flight and waits on no barrier.
 //
 // Measured: 64 requests of up to 16384 tokens, 8 query heads and one key head of
-// 128 on each of 8 ranks, bf16, 2.15 GB: 313 us, 6.9 TB/s (1.0 of the measured
+// 128 on each of 8 ranks, bf16, 2.15 GB: 317 us, 6.8 TB/s (1.0 of the measured
 // copy). One request of 262145 tokens, 2 key heads: 55 us, 4.9 TB/s; 40 us are the
 // bytes, the rest the launch, the chain of lengths, tables and first tiles, and
-// two joins. 33 requests of up to 3001 tokens of 80 elements of f32: 35 us, 3.6
+// two joins. 33 requests of up to 3001 tokens of 80 elements of f32: 33 us, 3.8
 // TB/s: the same chain, and three products for one.
 #include <cstdio>
 
@@ -168,15 +170,14 @@ struct Tile<uint16_t, DP, NT> {
   uint4 k[2][KC];  // tokens g, g + 8; elements 32 i + 8 c
   uint4 v[4][VC];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9; elements 64 h + 8 g
 
-  __device__ __forceinline__ static void load_queries(char* smem, const uint16_t* q, int queries, int D, int thread, int threads) {
-    for (int i = thread; i < NT * KC * 32; i += threads) {
-      const int lane = i & 31, chunk = (i >> 5) % KC, nt = (i >> 5) / KC;
-      const int row = nt * 8 + (lane >> 2), d = chunk * 32 + (lane & 3) * 8;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (row < queries && d < D) u = *reinterpret_cast<const uint4*>(q + (int64_t)row * D + d);
-      reinterpret_cast<uint4*>(smem)[i] = u;
-    }
+  // Piece i of the fragments, 16 bytes of shared memory, from the memory of the query heads.
+  using Piece = uint4;
+  __device__ __forceinline__ static Piece fetch_queries(int i, const uint16_t* q, int queries, int D) {
+    const int lane = i & 31, chunk = (i >> 5) % KC, nt = (i >> 5) / KC;
+    const int row = nt * 8 + (lane >> 2), d = chunk * 32 + (lane & 3) * 8;
+    return row < queries && d < D ? *reinterpret_cast<const uint4*>(q + (int64_t)row * D + d) : make_uint4(0, 0, 0, 0);
   }
+  __device__ __forceinline__ static uint4 fragment(Piece u) { return u; }
   __device__ __forceinline__ void load_k(const uint16_t* base, int row, int D) {
     const int lane = threadIdx.x & 31, c8 = (lane & 3) * 8;
 #pragma unroll
@@ -261,18 +262,17 @@ struct Tile<float, DP, NT> {
   float4 k[2][KC];  // tokens g, g + 8; elements 16 i + 4 c
   float4 v[4][VC];  // tokens c, c + 4, c + 8, c + 12; elements 32 h + 4 g
 
-  __device__ __forceinline__ static void load_queries(char* smem, const float* q, int queries, int D, int thread, int threads) {
-    for (int i = thread; i < NT * 2 * KC * 32; i += threads) {
-      const int lane = i & 31, step = (i >> 5) % (2 * KC), nt = (i >> 5) / (2 * KC);
-      const int row = nt * 8 + (lane >> 2), d = (step >> 1) * 16 + (lane & 3) * 4 + (step & 1) * 2;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (row < queries && d < D) {
-        const float2 x = *reinterpret_cast<const float2*>(q + (int64_t)row * D + d);
-        split_tf32(x.x, u.x, u.z);
-        split_tf32(x.y, u.y, u.w);
-      }
-      reinterpret_cast<uint4*>(smem)[i] = u;
-    }
+  using Piece = float2;
+  __device__ __forceinline__ static Piece fetch_queries(int i, const float* q, int queries, int D) {
+    const int lane = i & 31, step = (i >> 5) % (2 * KC), nt = (i >> 5) / (2 * KC);
+    const int row = nt * 8 + (lane >> 2), d = (step >> 1) * 16 + (lane & 3) * 4 + (step & 1) * 2;
+    return row < queries && d < D ? *reinterpret_cast<const float2*>(q + (int64_t)row * D + d) : make_float2(0.f, 0.f);
+  }
+  __device__ __forceinline__ static uint4 fragment(Piece x) {
+    uint4 u;
+    split_tf32(x.x, u.x, u.z);
+    split_tf32(x.y, u.y, u.w);
+    return u;
   }
   __device__ __forceinline__ static float4 load4(const float* p, bool live) {
     const uint4 u = ldg_cache(p, live);
@@ -392,10 +392,9 @@ constexpr bool kDaAhead = DP * sizeof(T) <= 512;
 // Where a block's walk over the tiles stands: kept in shared memory so that the
 // loop over tiles has the registers.
 struct Part {
-  int64_t first;       // units before the request's, all items
   int64_t tile_first;  // unit of the item's first tile
   int request, t0, t1, tiles, len;  // tiles t0..t1 of the item's `tiles`
-  int rank, kvh, q0, queries;
+  int rank, kvh, qg, queries;
 };
 
 // The shapes of a kernel. Four warps take 16 tokens of a tile each, H times for
@@ -427,7 +426,8 @@ struct Shape {
   static constexpr int kMostParts = kDaMaxBlocks / kDaJoin + 1;
   static constexpr int kMergeBytes = kDaWarps * Q * kRow * 4, kQueryBytes = H * Tl::kQueryBytes;
   struct Shared {
-    alignas(16) char buf[kMergeBytes > kQueryBytes ? kMergeBytes : kQueryBytes];
+    alignas(16) char buf[kMergeBytes];
+    uint4 queries[kQueryBytes / 16];
     float m[kDaWarps][Q], l[kDaWarps][Q];
     float weight[kMostParts][Q], sum[kMostParts][Q], top[Q], total[Q];
     int64_t tiles[kDaWarps * H];
@@ -449,10 +449,10 @@ struct Output {
   }
 };
 template <typename T>
-__device__ __forceinline__ Output<T> output_of(const DecodeArgs& a, const Part& p) {
+__device__ __forceinline__ Output<T> output_of(const DecodeArgs& a, const Part& p, int q0) {
   Output<T> o;
-  o.out = reinterpret_cast<T*>(a.out[p.rank]) + (int64_t)p.request * a.out_stride + (int64_t)p.q0 * a.head_dim;
-  o.lse = a.lse[p.rank] == nullptr ? nullptr : a.lse[p.rank] + (int64_t)p.request * a.q_heads + p.q0;
+  o.out = reinterpret_cast<T*>(a.out[p.rank]) + (int64_t)p.request * a.out_stride + (int64_t)q0 * a.head_dim;
+  o.lse = a.lse[p.rank] == nullptr ? nullptr : a.lse[p.rank] + (int64_t)p.request * a.q_heads + q0;
   return o;
 }
 
@@ -515,13 +515,30 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
     const int64_t split = more * (each + 1);
     return (int)(unit < split ? unit / (each + 1) : more + (unit - split) / each);
   };
+  auto place = [&](Part& p, int64_t item_first, int64_t at) {  // tiles of the item that are the block's, from unit `at` on
+    const int64_t end = start_of(block + 1);
+    p.tile_first = item_first + S::kStart;
+    p.t0 = p.t1 = 0;
+    if (at >= end || end <= p.tile_first) return;
+    p.t0 = (int)(at > p.tile_first ? at - p.tile_first : 0);
+    p.t1 = (int)(end - p.tile_first < p.tiles ? end - p.tile_first : p.tiles);
+    p.queries = min(Q, group - p.qg * Q);
+  };
   if (block < blocks) {
     const int64_t t = start_of(block) / per_request;  // lies in the same request, units counted once per item
     if (t >= before && t < before + mine) {
       int b = tid * seg;
       for (int n; t >= before + (n = units_of(length(b))); b++) before += n;
-      sh.part[1].first = before * per_request;
-      sh.part[1].request = b;
+      Part& p = sh.part[0];
+      const int64_t first = before * per_request, at = start_of(block);
+      const int n = units_of(length(b)), item = (int)((at - first) / n);
+      p.request = b;
+      p.len = length(b);
+      p.tiles = n - S::kStart;
+      p.qg = item % qgroups;
+      p.kvh = item / qgroups % a.kv_heads;
+      p.rank = item / qgroups / a.kv_heads;
+      place(p, first + (int64_t)item * n, at);
     }
   }
 
@@ -540,30 +557,33 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
     return;
   }
 
-  // The part that starts at unit `at` of the block's range, which lies in the request of `from` or after it.
-  auto describe = [&](Part& p, const Part& from, int64_t at) {
-    const int64_t end = start_of(block + 1);
+  // The part that follows `from`: of the next group of query heads, key head, rank or request.
+  auto describe_next = [&](Part& p, const Part& from) {
     p.t0 = p.t1 = 0;
-    if (at >= end) return;
-    int b = from.request, n = units_of(length(b));
-    int64_t first = from.first;
-    while (at >= first + (int64_t)n * per_request) {
-      first += (int64_t)n * per_request;
-      n = units_of(length(++b));
+    if (from.t1 < from.tiles) return;  // the block's range ends in it
+    const int64_t at = from.tile_first + from.tiles;
+    if (at >= start_of(block + 1)) return;
+    p.request = from.request;
+    p.tiles = from.tiles;
+    p.len = from.len;
+    p.rank = from.rank;
+    p.kvh = from.kvh;
+    p.qg = from.qg + 1;
+    if (p.qg == qgroups) {
+      p.qg = 0;
+      if (++p.kvh == a.kv_heads) {
+        p.kvh = 0;
+        if (++p.rank == a.nranks) {
+          p.rank = 0;
+          do {
+            if (++p.request >= a.batch) return;
+            p.len = length(p.request);
+          } while (p.len == 0);
+          p.tiles = tiles_of(p.len);
+        }
+      }
     }
-    const int item = (int)((at - first) / n), qg = item % qgroups;
-    p.first = first;
-    p.request = b;
-    p.tiles = n - S::kStart;
-    p.len = length(b);
-    p.tile_first = first + (int64_t)item * n + S::kStart;
-    if (end <= p.tile_first) return;
-    p.t0 = (int)(at > p.tile_first ? at - p.tile_first : 0);
-    p.t1 = (int)(end - p.tile_first < p.tiles ? end - p.tile_first : p.tiles);
-    p.kvh = item / qgroups % a.kv_heads;
-    p.rank = item / qgroups / a.kv_heads;
-    p.q0 = p.kvh * group + qg * Q;
-    p.queries = min(Q, group - qg * Q);
+    place(p, at, at);
   };
   // the lane's token of the warp's 16 in a tile of a part -> cache row
   auto row_of = [&](const Part& p, int tile) {
@@ -577,8 +597,6 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
     return ((page * a.kv_heads + p.kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
   };
   __syncthreads();
-  if (tid == 0) describe(sh.part[0], sh.part[1], start_of(block));
-  __syncthreads();
   if (sh.part[0].t1 == 0) {  // the range ends in an item's start
     if (bad) op_report(a.ws, kErrCapacity);
     return;
@@ -588,17 +606,28 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
   tile.load_k(reinterpret_cast<const T*>(a.k_cache[sh.part[0].rank]), row, D);
   if (kDaAhead<T, DP>) tile.load_v(reinterpret_cast<const T*>(a.v_cache[sh.part[0].rank]), row, D);
 
-  // At the end of a part the first tile of the next one is on its way already.
+  // queries of a part into registers, and from there into shared memory
+  constexpr int kPieces = S::kQueryBytes / 16, kEach = (kPieces + kThreads - 1) / kThreads;
+  typename Tl::Piece pieces[kEach];
+  auto fetch_queries = [&](const Part& p) {
+    const T* q = reinterpret_cast<const T*>(a.q[p.rank]) + (int64_t)p.request * a.q_stride + (int64_t)(p.kvh * group + p.qg * Q) * D;
+#pragma unroll
+    for (int j = 0; j < kEach; j++)
+      if (j * kThreads + tid < kPieces) pieces[j] = Tl::fetch_queries(j * kThreads + tid, q, p.queries, D);
+  };
+  auto put_queries = [&] {
+#pragma unroll
+    for (int j = 0; j < kEach; j++)
+      if (j * kThreads + tid < kPieces) sh.queries[j * kThreads + tid] = Tl::fragment(pieces[j]);
+  };
+  fetch_queries(sh.part[0]);
+  put_queries();
+
+  // At the end of a part the first tile of the next one is on its way already, and so are its queries.
   for (int i = 0;; i ^= 1) {
     const Part& part = sh.part[i];
     Part& after = sh.part[i ^ 1];
-    if (tid == 0) describe(after, part, part.tile_first + part.t1);
-    {
-      const T* q = reinterpret_cast<const T*>(a.q[part.rank]) + (int64_t)part.request * a.q_stride + (int64_t)part.q0 * D;
-#pragma unroll
-      for (int h = 0; h < H; h++)
-        Tl::load_queries(sh.buf + h * Tl::kQueryBytes, q + h * NT * 8 * D, part.queries - h * NT * 8, D, tid, kThreads);
-    }
+    if (tid == 0) describe_next(after, part);
     __syncthreads();
     const int rank = part.rank, t1 = part.t1;
     const T* kc = reinterpret_cast<const T*>(a.k_cache[rank]);
@@ -620,7 +649,7 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
     }
     {
       int next = row_at(part.t0 + 1);
-      const char* queries = sh.buf + half * Tl::kQueryBytes;
+      const char* queries = reinterpret_cast<const char*>(sh.queries) + half * Tl::kQueryBytes;
       const float scale2 = a.scale * 1.4426950408889634f;
       for (int t = part.t0; t < t1; t++) {
         float s[NT][4];
@@ -658,7 +687,7 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
           sh.l[warp][half * NT * 8 + nt * 8 + 2 * c + j] = st.l[nt][j];
         }
       }
-    __syncthreads();  // every warp is past the queries in sh.buf
+    __syncthreads();  // every warp is past the queries, and sh.m is there
     float* s_o = reinterpret_cast<float*>(sh.buf);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
@@ -695,8 +724,9 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
       }
       return x;
     };
-    const Output<T> out = output_of<T>(a, part);
+    const Output<T> out = output_of<T>(a, part, part.kvh * group + part.qg * Q);
     if (part.t0 == 0 && t1 == part.tiles) {
+      if (after.t1 > 0) fetch_queries(after);
       for (int i = tid; i < values; i += kThreads) {
         const int q = i / (DP / 4), d = i % (DP / 4) * 4;
         if (d < D) out.write(q, d, D, sum4(q, d), sh.top[q], sh.total[q]);
@@ -781,9 +811,11 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
         from = cf;
         counter = kDaMaxBlocks + cf;  // one item at most starts in a block's range and leaves it
       }
+      if (after.t1 > 0) fetch_queries(after);
     }
-    __syncthreads();  // the part's shared values have been read
     if (after.t1 == 0) break;
+    put_queries();
+    __syncthreads();  // the part's shared values have been read
   }
   if (bad) op_report(a.ws, kErrCapacity);
 }
