@@ -312,9 +312,11 @@ __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_
 
 }  // namespace
 
-template <typename T, int L, bool INTER>
+// SPLIT: few tokens, whose heads go to several groups (tested as it runs, it costs many tokens 2 to 9 %).
+template <typename T, int L, bool INTER, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs a,
-                                                                    int q_blocks, int k_blocks) {
+                                                                    int q_blocks, int k_blocks, int q_split,
+                                                                    int k_split) {
   constexpr int kGroups = kBwdThreads / L, kRow = L * 8, kCopies = (int)sizeof(T) / 2;
   __shared__ __align__(16) T ring[kGroups][kBwdStages][2][kRow];
   __shared__ float s_dw[kBwdThreads][9];
@@ -347,9 +349,13 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
   }
 
   const bool is_q = blockIdx.x < q_blocks;
-  const int walkers = (is_q ? q_blocks : k_blocks) * kGroups;  // groups that share the tokens
+  // a unit is a token's heads, or where there are few tokens the `split`-th part of them
+  const int split = !SPLIT ? 1 : is_q ? q_split : k_split, units = a.tokens * split;
+  const int walkers = (is_q ? q_blocks : k_blocks) * kGroups;  // groups that share the units
   const int walker = (is_q ? blockIdx.x : blockIdx.x - q_blocks) * kGroups + group;
-  const int heads = is_q ? a.q_heads : a.kv_heads, place = is_q ? 0 : a.q_heads * D;
+  const int heads = (is_q ? a.q_heads : a.kv_heads) / split, place = is_q ? 0 : a.q_heads * D;
+  auto token_of = [&](int unit) { return SPLIT ? unit / split : unit; };
+  auto part_of = [&](int unit, int token) { return SPLIT ? (unit - token * split) * heads * D : 0; };
   const int64_t g_stride = is_q ? a.dq_stride : a.dk_stride;
   const T* gs = reinterpret_cast<const T*>(is_q ? a.dq[rank] : a.dk[rank]);
   const Row8 w = load_weight<T, INTER>(is_q ? a.q_weight : a.k_weight, n);
@@ -357,17 +363,20 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
   Row8 dw = {{zero, zero, zero, zero}};
   const float inv = 1.f / (float)D;
   bool bad = false;
-  // the warp's first group has the most tokens; the others run as long, with rows of zeros at the end
+  // the warp's first group has the most units; the others run as long, with rows of zeros at the end
   const int first_walker = walker - (threadIdx.x & 31) / L;
-  const int rows = first_walker < a.tokens ? ((a.tokens - 1 - first_walker) / walkers + 1) * heads : 0;
-  const int mine = walker < a.tokens ? ((a.tokens - 1 - walker) / walkers + 1) * heads : 0;
+  const int rows = first_walker < units ? ((units - 1 - first_walker) / walkers + 1) * heads : 0;
+  const int mine = walker < units ? ((units - 1 - walker) / walkers + 1) * heads : 0;
 
-  // Pointers go one head on within a token, and are set anew at the group's next token.
+  // Pointers go one head on within a unit, and are set anew at the group's next one.
   const T* fx = xs + place + l * 8;  // of the next row to ask for
   const T* fg = gs + l * 8;
-  int f_token = walker < a.tokens ? walker : 0;
-  fx += f_token * a.qkv_stride;
-  fg += f_token * g_stride;
+  int f_unit = walker < units ? walker : 0;
+  {
+    const int f_token = token_of(f_unit), part = part_of(f_unit, f_token);
+    fx += f_token * a.qkv_stride + part;
+    fg += f_token * g_stride + part;
+  }
   constexpr uint32_t kCell = kRow * sizeof(T), kSlot = 2 * kCell;  // bytes of a row of x or dy, of both
   const uint32_t cell = smem_addr(&ring[group][0][0][l * 8]);
   int f_left = mine, f_head = 0;
@@ -394,23 +403,28 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
     fg += D;
     if (++f_head == heads) {
       f_head = 0;
-      f_token += walkers;
-      fx = xs + f_token * a.qkv_stride + place + l * 8;
-      fg = gs + f_token * g_stride + l * 8;
+      f_unit += walkers;
+      const int f_token = token_of(f_unit), part = part_of(f_unit, f_token);
+      fx = xs + f_token * a.qkv_stride + place + part + l * 8;
+      fg = gs + f_token * g_stride + part + l * 8;
     }
   };
-  auto position = [&](int token) {
-    const int pos = token < a.tokens ? a.positions[token] : 0;
+  auto position = [&](int unit) {
+    const int pos = unit < units ? a.positions[token_of(unit)] : 0;
     if (pos >= 0 && pos < a.max_pos) return pos;
     bad = true;
     return 0;
   };
 #pragma unroll
   for (int s = 0; s < kBwdStages - 1; s++) fetch();
-  int token = walker, head = 0, slot = 0;
-  Turn turn = load_turn(a.cos_sin + (int64_t)position(token) * a.rot, a.rot, n);
-  int pos_next = position(token + walkers);
-  T* out = ds + (walker < a.tokens ? walker : 0) * a.dqkv_stride + place;
+  int unit = walker, head = 0, slot = 0;
+  Turn turn = load_turn(a.cos_sin + (int64_t)position(unit) * a.rot, a.rot, n);
+  int pos_next = position(unit + walkers);
+  auto out_of = [&](int unit) {
+    const int token = token_of(unit);
+    return ds + token * a.dqkv_stride + place + part_of(unit, token);
+  };
+  T* out = out_of(walker < units ? walker : 0);
   const int stores = n.in ? mine : 0;
   if (!op_ready(a.ws, magic)) {
     copy_async_wait<0>();
@@ -436,10 +450,10 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
     out += D;
     if (++head == heads) {
       head = 0;
-      token += walkers;
-      out = ds + token * a.dqkv_stride + place;
+      unit += walkers;
+      out = out_of(unit);
       turn = load_turn(a.cos_sin + (int64_t)pos_next * a.rot, a.rot, n);
-      pos_next = position(token + walkers);
+      pos_next = position(unit + walkers);
     }
   }
   copy_async_wait<0>();
@@ -530,12 +544,15 @@ const void* forward_of(int lanes, bool inter, bool cache) {
                                                                    : forward_of<T, 32>(inter, cache);
 }
 template <typename T, int L>
-const void* backward_of(bool inter) {
-  return inter ? (const void*)norm_rope_bwd_kernel<T, L, true> : (const void*)norm_rope_bwd_kernel<T, L, false>;
+const void* backward_of(bool inter, bool split) {
+  return inter ? (split ? (const void*)norm_rope_bwd_kernel<T, L, true, true> : (const void*)norm_rope_bwd_kernel<T, L, true, false>)
+               : (split ? (const void*)norm_rope_bwd_kernel<T, L, false, true>
+                        : (const void*)norm_rope_bwd_kernel<T, L, false, false>);
 }
 template <typename T>
-const void* backward_of(int lanes, bool inter) {
-  return lanes == 8 ? backward_of<T, 8>(inter) : lanes == 16 ? backward_of<T, 16>(inter) : backward_of<T, 32>(inter);
+const void* backward_of(int lanes, bool inter, bool split) {
+  return lanes == 8 ? backward_of<T, 8>(inter, split) : lanes == 16 ? backward_of<T, 16>(inter, split)
+                                                                    : backward_of<T, 32>(inter, split);
 }
 
 }  // namespace
@@ -567,24 +584,38 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, cudaStream_t stream) {
   const int lanes = lanes_of(a.head_dim), groups = kBwdThreads / lanes;
-  const void* fn = a.dtype == kF32 ? backward_of<float>(lanes, a.interleaved != 0)
-                                   : backward_of<uint16_t>(lanes, a.interleaved != 0);
+  auto kernel = [&](bool split) {
+    return a.dtype == kF32 ? backward_of<float>(lanes, a.interleaved != 0, split)
+                           : backward_of<uint16_t>(lanes, a.interleaved != 0, split);
+  };
   int resident = 0;
-  const cudaError_t e = resident_blocks(fn, kBwdThreads, 0, &resident);
+  const cudaError_t e = resident_blocks(kernel(false), kBwdThreads, 0, &resident);
   if (e != cudaSuccess) return e;
   // one resident wave, shared out in proportion to the kinds' bytes: x, dy and dx of query and key heads, dv twice
   const int64_t most = imin(kNormRopeBwdBlocks, (int64_t)resident) / a.nranks;
   const int64_t q = 3ll * a.q_heads, k = 3ll * a.kv_heads, v = 2ll * a.kv_heads;
-  const int64_t needed = div_up(a.tokens, groups);
-  auto blocks_of = [&](int64_t weight) { return (int)imax(1, imin(needed, most * weight / (q + k + v))); };
-  int q_blocks = blocks_of(q), k_blocks = blocks_of(k);
-  const int v_blocks = blocks_of(v);
+  auto share = [&](int64_t weight) { return imax(1, most * weight / (q + k + v)); };
+  auto blocks_of = [&](int64_t weight, int64_t units) { return (int)imax(1, imin(div_up(units, groups), share(weight))); };
+  // Fewer tokens than groups: a token's heads go to several groups in equal parts, of 2 heads or more while the blocks join
+  // in one level, else of 8 or more (3 tokens of 32 and 4 heads of 192: 6.3 us against 14.6; 117 of 80 on 8 ranks in f32
+  // 15.7 against 18.5; 703 of 16 and 2 heads of 192 15.8 with 8 heads a part, 17.6 with 4, 16.5 undivided).
+  auto split_of = [&](int64_t weight, int heads) {
+    int split = 1;
+    for (int s = 2; s <= heads; s++) {
+      const int64_t units = (int64_t)a.tokens * s;
+      if (heads % s == 0 && units <= share(weight) * groups && heads / s >= (units <= kBwdJoin * groups ? 2 : 8)) split = s;
+    }
+    return split;
+  };
+  int q_split = split_of(q, a.q_heads), k_split = split_of(k, a.kv_heads);
+  int q_blocks = blocks_of(q, (int64_t)a.tokens * q_split), k_blocks = blocks_of(k, (int64_t)a.tokens * k_split);
+  const int v_blocks = blocks_of(v, a.tokens);
   dim3 grid((unsigned)(q_blocks + k_blocks + v_blocks), (unsigned)a.nranks);
   if (trace_on())
     std::fprintf(stderr, "rar trace: qk_norm_rope_backward nranks=%d tokens=%d heads=%d/%d dim=%d rot=%d grid=%ux%u\n",
                  a.nranks, a.tokens, a.q_heads, a.kv_heads, a.head_dim, a.rot, grid.x, grid.y);
-  void* params[] = {const_cast<NormRopeBwdArgs*>(&a), &q_blocks, &k_blocks};
-  return launch_op(fn, grid, kBwdThreads, 0, stream, params);
+  void* params[] = {const_cast<NormRopeBwdArgs*>(&a), &q_blocks, &k_blocks, &q_split, &k_split};
+  return launch_op(kernel(q_split * k_split > 1), grid, kBwdThreads, 0, stream, params);
 }
 
 }  // namespace rar

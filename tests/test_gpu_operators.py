@@ -873,3 +873,12 @@ def test_decode_attention_cuts(q, d, dtype):
     (4864, [333], "bf16", 2), (4865, [20, 1300], "f32", 3), (11000, [8200], "bf16", 0)])
 def test_token_logprobs_of_many_rows(rows, widths, dtype, top):
     test_token_logprobs(rows, widths, dtype, top, 1, False)
+
+
+@pytest.mark.parametrize("n,t,q,kv,d,rot,inter,dtype,extra", [
+    (1, 3, 32, 4, 192, 96, False, "bf16", 0), (4, 2, 32, 8, 64, 32, True, "bf16", 8), (1, 1, 7, 3, 128, 128, False, "f32", 0),
+    (8, 117, 32, 16, 80, 80, True, "f32", 0), (1, 703, 16, 2, 192, 192, False, "bf16", 0), (2, 64, 12, 9, 96, 48, False, "f32", 0),
+    (1, 40, 1024, 2, 8, 8, False, "bf16", 0)])
+def test_norm_rope_backward_of_few_tokens(n, t, q, kv, d, rot, inter, dtype, extra):
+    """A token's heads shared by several groups of threads."""
+    test_norm_rope_backward(n, t, q, kv, d, rot, inter, dtype, extra)
