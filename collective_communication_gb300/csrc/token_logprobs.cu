@@ -23,9 +23,9 @@
 // word at or above the bound is rare after the first tile (about top / (words
 // read) of them), and is read again and inserted where it belongs.
 // Measured: 2048 rows of 8 shards of 16003 words in bf16, 524 MB: 87 us without
-// alternatives (6.0 TB/s, 0.90 of the measured copy), 107 us with 5, 136 with 20:
+// alternatives (6.0 TB/s, 0.90 of the measured copy), 107 us with 5, 133 with 20:
 // the list's instructions. 3 rows of 131072 words: 6.7 us without alternatives,
-// 11 with 8, 16 with 20: a launch, a tile and a join of 128 parts. The
+// 11 with 8, 14 with 20: a launch, a tile and a join of 128 parts. The
 // gradient, 2048 rows of 131072 words read and written: 157 us, 6.8 TB/s (1.0 of
 // the measured copy).
 #include <cstdio>
@@ -40,8 +40,8 @@ constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpTile = 1024;             // columns of a tile
 constexpr int kLpMaxWorkers = 4864;       // most warps of a forward launch: a counter and two partial results each
 // Alternatives are inserted one by one, and lanes' words looked at by the whole warp, where there are few; more are
-// sorted, and found by each lane on its own (3 rows of 24848 words in f32, top 20: 15.6 us against 22.1; 704 rows of
-// 80688 words in bf16, top 20: 56 against 66, top 5 no different).
+// sorted, and found by each lane on its own (3 rows of 24848 words in f32, top 20: 14 us against 22; 704 rows of
+// 80688 words in bf16, top 20: 53 against 66, top 5 no different).
 constexpr int kLpFewKeys = 6, kLpFewLanes = 4;
 // A row of few parts merges their lists, others pick from them (12 rows of 3381 words, top 20: 11.4 us against 15.5).
 constexpr int kLpFewParts = 8;
@@ -133,13 +133,14 @@ __device__ __forceinline__ uint64_t insert32(uint64_t list, uint64_t key) {
   return lane < at ? list : lane == at ? key : up;
 }
 
-// Sorts 32 keys over the lanes, largest in lane 0, from the stage whose runs have `size` lanes on (2: any keys;
+// Sorts 32 keys over the lanes, largest in lane 0, from the stage whose runs have FROM lanes on (2: any keys;
 // 32: two runs, one falling and one rising).
-__device__ __forceinline__ uint64_t sort32(uint64_t k, int size) {
+template <int FROM>
+__device__ __forceinline__ uint64_t sort32(uint64_t k) {
   const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (; size <= 32; size <<= 1)
-#pragma unroll 1
+#pragma unroll
+  for (int size = FROM; size <= 32; size <<= 1)
+#pragma unroll
     for (int d = size >> 1; d > 0; d >>= 1) {
       const uint64_t o = __shfl_xor_sync(~0u, k, d);
       const bool large = ((lane & d) == 0) == ((lane & size) == 0 || size == 32);
@@ -169,15 +170,16 @@ struct TopList {
   // Another list, sorted likewise.
   __device__ __forceinline__ void merge(uint64_t sorted) {
     const uint64_t other = __shfl_xor_sync(~0u, sorted, 31);
-    list = sort32(other > list ? other : list, 32);
+    list = sort32<32>(other > list ? other : list);
   }
-  // Every lane's key, 0 for none: those above the bound are inserted one after another, or where there are many
-  // sorted (21 steps, about as long as 8 insertions) and merged.
+  // Every lane's key, 0 for none: those above the bound are inserted one after another, or where MANY are expected and
+  // there are many, sorted and merged.
+  template <bool MANY>
   __device__ __forceinline__ void offer(uint64_t key, int top) {
     uint32_t votes = __ballot_sync(~0u, key > bound);
     if (votes == 0) return;
-    if (__popc(votes) > kLpFewKeys) {
-      merge(sort32(key > bound ? key : 0, 2));
+    if (MANY && __popc(votes) > kLpFewKeys) {
+      merge(sort32<2>(key > bound ? key : 0));
       votes = 0;
     }
     for (; votes != 0; votes &= votes - 1) list = insert32(list, __shfl_sync(~0u, key, __ffs(votes) - 1));
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
               }
               while (__any_sync(~0u, mine != 0)) {
                 const int b = __ffs(mine) - 1, i = b >> 3, j = b & 7;  // -1 when there are no more
-                tops.offer(mine != 0 ? top_key(to_float(words[i][lane][j]), word + (p + i * 32) * 8 + j) : 0, a.top);
+                tops.offer<true>(mine != 0 ? top_key(to_float(words[i][lane][j]), word + (p + i * 32) * 8 + j) : 0, a.top);
                 mine &= mine - 1;
               }
               lanes = 0;
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
               const int l = __ffs(lanes) - 1, pack = p - lane + l + (lane >> 3) * 32;
               const bool there = lane < 8 * kAhead && pack < packs;
               const int i = there ? lane >> 3 : 0;
-              tops.offer(there ? top_key(to_float(words[i][l][lane & 7]), word + pack * 8 + (lane & 7)) : 0, a.top);
+              tops.offer<false>(there ? top_key(to_float(words[i][l][lane & 7]), word + pack * 8 + (lane & 7)) : 0, a.top);
             }
             __syncwarp();
           }
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
         m = one.m;
         s2 = f2(one.s, 0.f);
         w2 = f2(one.w, 0.f);
-        if constexpr (TOP) tops.offer(mine ? top_key(v, word + e) : 0, a.top);
+        if constexpr (TOP) tops.offer<false>(mine ? top_key(v, word + e) : 0, a.top);
       }
     }
     // the token's word, needed last, is on its way during the joins
@@ -439,8 +441,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
 #pragma unroll
               for (int i = 1; i < kAt; i++) k[i - 1] = k[i];
               for (int i = 2;; i += 2) {
-                tops.offer(now.x, a.top);
-                tops.offer(now.y, a.top);
+                tops.offer<true>(now.x, a.top);
+                tops.offer<false>(now.y, a.top);
                 const bool more = i < a.top && now.y > tops.bound;
                 if (!__any_sync(~0u, more)) break;
                 now = more ? pair_of(w0 + lane + 32 * j, i) : make_ulonglong2(0, 0);
