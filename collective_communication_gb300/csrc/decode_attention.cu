@@ -423,13 +423,12 @@ struct Shape {
   static constexpr int kStart = Q / 8;
   static constexpr int kRow = DP + 4;
   static constexpr int kPartial = Q * (DP + 2);  // floats of a partial result: DP values a query, m, l
-  static constexpr int kMostParts = kDaMaxBlocks / kDaJoin + 1;
   static constexpr int kMergeBytes = kDaWarps * Q * kRow * 4, kQueryBytes = H * Tl::kQueryBytes;
   struct Shared {
     alignas(16) char buf[kMergeBytes];
     uint4 queries[kQueryBytes / 16];
     float m[kDaWarps][Q], l[kDaWarps][Q];
-    float weight[kMostParts][Q], sum[kMostParts][Q], top[Q], total[Q];
+    float top[Q], total[Q];
     int64_t tiles[kDaWarps * H];
     Part part[2];  // the one worked on and the one after it
     int last;
@@ -761,47 +760,57 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
         }
         __syncthreads();
         if (!sh.last) break;
-        constexpr int kShare = kThreads / Q < 32 ? kThreads / Q : 32;  // lanes of a query head
-        if (tid < kShare * Q) {
-          const int q = tid / kShare, p0 = tid % kShare;
-          float m = -INFINITY, l = 0.f;
-          for (int p = p0; p < count; p += kShare) {
-            const float* src = part_of(from + p * step) + Q * DP + q;
-            sh.weight[p][q] = __ldcg(src);
-            sh.sum[p][q] = __ldcg(src + Q);
-          }
-          for (int p = p0; p < count; p += kShare) m = fmaxf(m, sh.weight[p][q]);
-#pragma unroll
-          for (int d = kShare / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-          for (int p = p0; p < count; p += kShare) {
-            const float x = sh.weight[p][q], f = x == -INFINITY ? 0.f : exp2_fast(x - m);
-            l += f * sh.sum[p][q];
-            sh.weight[p][q] = f;
-          }
-#pragma unroll
-          for (int d = kShare / 2; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-          if (p0 == 0) {
-            sh.top[q] = m;
-            sh.total[q] = l;
-          }
-        }
-        __syncthreads();
         const bool whole = step > 1 || count == cl + 1 - cf;  // nothing of the item is missing
         float* to = part_of(from);
+        // Every thread weighs the partial results of its query head itself, so that all loads of kAt of them are under way
+        // at once (4 requests of up to 5000 tokens, 7 query heads of 192: 17 us; 20.6 with the weights shared out first).
+        constexpr int kAt = 8;
         for (int i = tid; i < values; i += kThreads) {
           const int q = i / (DP / 4), d = i % (DP / 4) * 4;
           if (d >= D) continue;
+          float m = -INFINITY, l = 0.f;
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int p = 0; p < count; p++) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(part_of(from + p * step) + q * DP + d));
-            const float f = sh.weight[p][q];
-            x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
+          for (int p0 = 0; p0 < count; p0 += kAt) {
+            float pm[kAt], pl[kAt];
+            float4 y[kAt];
+#pragma unroll
+            for (int j = 0; j < kAt; j++) {
+              pm[j] = -INFINITY;
+              pl[j] = 0.f;
+              y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (p0 + j < count) {
+                const float* src = part_of(from + (p0 + j) * step);
+                pm[j] = __ldcg(src + Q * DP + q);
+                pl[j] = __ldcg(src + Q * DP + Q + q);
+                y[j] = __ldcg(reinterpret_cast<const float4*>(src + q * DP + d));
+              }
+            }
+            float top = m;
+#pragma unroll
+            for (int j = 0; j < kAt; j++) top = fmaxf(top, pm[j]);
+            const float keep = m == -INFINITY ? 0.f : exp2_fast(m - top);
+            l *= keep;
+            x.x *= keep; x.y *= keep; x.z *= keep; x.w *= keep;
+#pragma unroll
+            for (int j = 0; j < kAt; j++) {
+              const float f = pm[j] == -INFINITY ? 0.f : exp2_fast(pm[j] - top);
+              l += f * pl[j];
+              x.x += f * y[j].x; x.y += f * y[j].y; x.z += f * y[j].z; x.w += f * y[j].w;
+            }
+            m = top;
           }
-          if (whole) out.write(q, d, D, x, sh.top[q], sh.total[q]);
-          else *reinterpret_cast<float4*>(to + q * DP + d) = x;
+          if (whole) {
+            out.write(q, d, D, x, m, l);
+          } else {
+            *reinterpret_cast<float4*>(to + q * DP + d) = x;
+            if (d == 0) {
+              sh.top[q] = m;
+              sh.total[q] = l;
+            }
+          }
         }
         if (whole) break;
+        __syncthreads();  // every thread has read the weights that are overwritten now
         if (tid < Q) {
           to[Q * DP + tid] = sh.top[tid];
           to[Q * DP + Q + tid] = sh.total[tid];
