@@ -486,15 +486,14 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
   int count = min(kBwdJoin, k0 + kind_blocks - from);
   uint32_t* counter = counters + 2 + from / kBwdJoin + (is_q ? 0 : 1);  // runs of the two kinds do not share one
   for (;;) {
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-      s_last = atomicAdd(counter, 1u) == (uint32_t)(count - 1);
+      // releases the block's sums, and acquires the others' if it is the last
+      s_last = atom_add_acq_rel_u32(counter, 1u) == (uint32_t)(count - 1);
       if (s_last) *counter = 0;
     }
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
     // four elements a thread; the threads that share them take every `many`-th partial, then join in that order
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (turn_of < many) {
