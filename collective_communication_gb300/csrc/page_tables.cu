@@ -11,11 +11,12 @@
 // request, from L2), and writes its share of the outputs: a run of the tokens,
 // and of every chunk's requests and new pages. (One block that wrote all
 // requests' new pages, a dependent load and store each, took 23 us for 4096
-// requests and 16000 pages; shared out it is 9.) A token's page that is new in
+// requests and 16000 pages; shared out it is 7.5.) A token's page that is new in
 // this call is read from the free list, not from the table that another block
 // may still be writing. What bounds it is the launch and the chain of dependent
-// loads; the bytes are a few MB at most. Blocks of 256 threads for up to 1024
-// requests, one chunk (3.4 us against 5.4 for 8 requests, where a larger block's
+// loads, so a thread's two tokens go through theirs side by side (7.5 us against
+// 8.6 one after the other); the bytes are a few MB at most. Blocks of 256 threads for up to 1024
+// requests, one chunk (3.1 us against 5.4 for 8 requests, where a larger block's
 // start and barriers are what there is to save), of 1024 above (one pass over
 // 4096 requests instead of four).
 #include <cstdio>
@@ -151,26 +152,46 @@ __global__ void __launch_bounds__(THREADS) page_tables_kernel(const __grid_const
     }
     // the block's tokens that belong to this chunk
     const int64_t lo = t0 > tok0 ? t0 : tok0, hi = imin(t1, tok0 + total.tokens);
-    for (int64_t t = lo + tid; t < hi; t += THREADS) {
-      const int rel = (int)(t - tok0);
-      int x = 0, y = kChunk;  // the last request whose first token is not after t
-      while (y - x > 1) {
-        const int mid = (x + y) >> 1;
-        if (s_start[mid] <= rel) x = mid; else y = mid;
+    static_assert(kTokens == 2 * THREADS, "a thread's two tokens, whose searches and loads go side by side");
+    {
+      int x[2] = {0, 0}, rel[2], page[2], col[2], pos[2];
+      bool live[2], had[2];
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        const int64_t t = lo + tid + i * THREADS;
+        live[i] = t < hi;
+        rel[i] = live[i] ? (int)(t - tok0) : 0;
       }
-      const int r = base + x;
-      int slot = -1, pos = 0;
-      if (r < a.requests && s_off[x] >= 0) {
-        const int len_r = a.lens[r];
-        pos = len_r + (rel - s_start[x]);
-        const int have = (int)(((int64_t)len_r + P - 1) >> a.page_shift), col = pos >> a.page_shift;
-        const int page = col < have ? a.table[(int64_t)r * a.table_stride + col]
-                                    : a.free_pages[count - 1 - (need0 + s_off[x] + col - have)];
-        if (page >= 0 && page < a.num_pages) slot = (page << a.page_shift) + (pos & (P - 1));
-        else bad = true;
+      // the last request whose first token is not after the token
+      for (int step = kChunk / 2; step > 0; step >>= 1)
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+          if (s_start[x[i] + step] <= rel[i]) x[i] += step;
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        live[i] = live[i] && base + x[i] < a.requests;
+        had[i] = live[i] && s_off[x[i]] >= 0;
+        pos[i] = had[i] ? a.lens[base + x[i]] : 0;
       }
-      a.positions[t] = pos;
-      a.slots[t] = slot;
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        page[i] = -1;
+        if (!had[i]) continue;
+        const int r = base + x[i], have = (int)(((int64_t)pos[i] + P - 1) >> a.page_shift);
+        pos[i] += rel[i] - s_start[x[i]];
+        col[i] = pos[i] >> a.page_shift;
+        page[i] = col[i] < have ? a.table[(int64_t)r * a.table_stride + col[i]]
+                                : a.free_pages[count - 1 - (need0 + s_off[x[i]] + col[i] - have)];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        const int64_t t = lo + tid + i * THREADS;
+        if (t >= hi) continue;
+        const bool fine = page[i] >= 0 && page[i] < a.num_pages;
+        if (had[i] && !fine) bad = true;
+        a.positions[t] = pos[i];
+        a.slots[t] = fine ? (page[i] << a.page_shift) + (pos[i] & (P - 1)) : -1;
+      }
     }
     need0 += total.need;
     tok0 += total.tokens;
