@@ -844,9 +844,10 @@ DecodeKernel kernel_of() {
 
 // More than 8 query heads a key head (wide): two accumulators a tile where they
 // fit the registers beside K and V. Where they do not, bf16 takes two groups of
-// warps (head size 192, 16 heads on 8 ranks, 32 requests of 8192 tokens: 326 us
-// against 461 of two passes over the cache; 256: 534 against 614); binary32 is
-// bound by its instructions then, and two groups gave nothing (505 against 498).
+// warps (head size 192, 16 heads on 8 ranks, 32 requests of 8192 tokens: 323 us
+// against 461 of two passes over the cache; 256: 461 against 614); binary32 is
+// bound by its instructions then: two groups take 1025 us against 1011, 1342
+// against 1471, and a tenth more for short requests.
 template <typename T>
 DecodeKernel kernel_for(int head_dim, bool wide) {
   constexpr bool half = sizeof(T) == 2;
