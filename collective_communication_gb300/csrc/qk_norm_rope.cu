@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
 // copies of consecutive elements, read back as the lane's two chunks), so three
 // rows a group are in flight whatever the registers hold.
 //
-// 4097 tokens of 16 heads of 96 on 4 ranks, interleaved: 43 us, 4.1 TB/s (0.61 of
+// 4097 tokens of 16 heads of 96 on 4 ranks, interleaved: 44 us, 4.0 TB/s (0.60 of
 // the measured copy). Instruction issue bounds it (12 of a group's 16 lanes work
 // at 96 elements, and two sums a row go over the lanes), then the start and the
 // two joins, about 9 us together.

@@ -882,3 +882,36 @@ def test_token_logprobs_of_many_rows(rows, widths, dtype, top):
 def test_norm_rope_backward_of_few_tokens(n, t, q, kv, d, rot, inter, dtype, extra):
     """A token's heads shared by several groups of threads."""
     test_norm_rope_backward(n, t, q, kv, d, rot, inter, dtype, extra)
+
+
+def test_operators_follow_copies():
+    """A kernel that may come up early waits for a copy ahead of it all the same, and a copy behind it for its results."""
+    rows, vocab, n = 64, 40000, 12
+    g = torch.Generator().manual_seed(5)
+    given = [torch.randn((1, rows, vocab), generator=g).pin_memory() for _ in range(n)]
+    tokens = torch.randint(0, vocab, (rows,), generator=g, dtype=torch.int32).cuda()
+    x = torch.zeros((1, rows, vocab), device="cuda")
+    d = torch.zeros_like(x)
+    o = {k: torch.zeros((rows,), device="cuda") for k in ("logprob", "entropy", "lse")}
+    ws = B.OpWorkspace(B.token_logprobs_workspace_bytes(rows, 0))
+    read = [torch.zeros((2, rows)).pin_memory() for _ in range(n)]
+    grads = [torch.zeros((1, rows, vocab)).pin_memory() for _ in range(n)]
+    ones = torch.ones((rows,), device="cuda")
+    torch.cuda.synchronize()
+    for i in range(n):
+        B.token_logprobs(x, tokens, workspace=ws, top_values=None, top_ids=None, **o)  # of the last logits; overwritten
+        x.copy_(given[i], non_blocking=True)
+        B.token_logprobs(x, tokens, workspace=ws, top_values=None, top_ids=None, **o)
+        B.token_logprobs_backward(x, tokens, o["lse"], o["entropy"], ones, ones, d, ws)
+        grads[i].copy_(d, non_blocking=True)
+        read[i][0].copy_(o["logprob"], non_blocking=True)
+        read[i][1].copy_(o["lse"], non_blocking=True)
+    torch.cuda.synchronize()
+    for i in range(n):
+        want = {k: torch.zeros((rows,), device="cuda") for k in o}
+        x.copy_(given[i])
+        B.token_logprobs(x, tokens, workspace=ws, top_values=None, top_ids=None, **want)
+        torch.cuda.synchronize()
+        B.token_logprobs_backward(x, tokens, want["lse"], want["entropy"], ones, ones, d, ws)
+        assert torch.equal(read[i][0], want["logprob"].cpu()) and torch.equal(read[i][1], want["lse"].cpu())
+        assert torch.equal(grads[i], d.cpu())
