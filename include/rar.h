@@ -424,6 +424,12 @@ RAR_API rar_status rar_describe_geometry(int nranks, size_t count, rar_dtype dty
  * operator used with it says; an operator without one needs the minimum). It
  * serves any of these operators, at any sizes it has room for, in any order on
  * one stream; nothing carries over from call to call.
+ *
+ * Streams: calls are ordered as any kernel is. They are launched with
+ * programmatic stream serialization: an operator's blocks may come up while the
+ * kernel ahead of it in the stream runs its last ones, and wait for its end and
+ * its results before they read or write anything. A caller's own kernel that is
+ * launched with that attribute behind an operator has to wait likewise.
  */
 #define RAR_OP_WORKSPACE_MIN_BYTES 36864
 RAR_API rar_status rar_op_workspace_init(void* workspace, size_t workspaceBytes, void* stream);
