@@ -290,10 +290,10 @@ __global__ void __launch_bounds__(kNrThreads, sizeof(T) == 2 ? 4 : 3) norm_rope_
 // copies of consecutive elements, read back as the lane's two chunks), so three
 // rows a group are in flight whatever the registers hold.
 //
-// 4097 tokens of 16 heads of 96 on 4 ranks, interleaved: 44 us, 4.0 TB/s (0.60 of
+// 4097 tokens of 16 heads of 96 on 4 ranks, interleaved: 42.5 us, 4.2 TB/s (0.62 of
 // the measured copy). Instruction issue bounds it (12 of a group's 16 lanes work
 // at 96 elements, and two sums a row go over the lanes), then the start and the
-// two joins, about 9 us together.
+// two joins, about 7 us together.
 //
 // Weight sums are added over the block's groups in group order, then over runs
 // of kBwdJoin blocks and over the runs in block order, each time by the block
@@ -494,13 +494,23 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
     }
     __syncthreads();
     if (!s_last) return;
-    // four elements a thread; the threads that share them take every `many`-th partial, then join in that order
+    // four elements a thread; the threads that share them take every `many`-th partial, eight loads at a time whatever
+    // is left (loops over the rest cost up to 3 us), then join in that order
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (turn_of < many) {
-#pragma unroll 8
-      for (int i = turn_of; i < count; i += many) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(parts + (int64_t)(from + i * apart) * D + quad * 4));
-        s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
+      for (int i0 = turn_of; i0 < count; i0 += 8 * many) {
+        float4 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const int i = i0 + j * many;
+          y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < count)
+            y[j] = __ldcg(reinterpret_cast<const float4*>(parts + (int64_t)(from + i * apart) * D + quad * 4));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          s.x += y[j].x; s.y += y[j].y; s.z += y[j].z; s.w += y[j].w;
+        }
       }
     }
     s_dw[threadIdx.x][0] = s.x;
@@ -596,8 +606,8 @@ cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, cudaStream_t stream) 
   auto share = [&](int64_t weight) { return imax(1, most * weight / (q + k + v)); };
   auto blocks_of = [&](int64_t weight, int64_t units) { return (int)imax(1, imin(div_up(units, groups), share(weight))); };
   // Fewer tokens than groups: a token's heads go to several groups in equal parts, of 2 heads or more while the blocks join
-  // in one level, else of 8 or more (3 tokens of 32 and 4 heads of 192: 6.3 us against 14.6; 117 of 80 on 8 ranks in f32
-  // 15.7 against 18.5; 703 of 16 and 2 heads of 192 15.8 with 8 heads a part, 17.6 with 4, 16.5 undivided).
+  // in one level, else of 8 or more (3 tokens of 32 and 4 heads of 192: 5 us against 14; 2048 of 32 and 8 heads of 128
+  // 17.5 against 21.8; 235 of 16 and 2 heads of 256 in f32 11.8 with 8 heads a part, 13.2 with 4, 13.6 undivided).
   auto split_of = [&](int64_t weight, int heads) {
     int split = 1;
     for (int s = 2; s <= heads; s++) {
