@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(kBwdThreads) norm_rope_bwd_kernel(const __grid
     // with u = z w: dw += z x r, dx = r u - (r^3 mean(u x)) x; both sums at once
     const Row8 v = x.widen(), z = rotate<true>(dy.widen(), turn), u = z * w;
     const float2 sums = group_sum2<L>(dot8(v, v), dot8(u, v));
-    const float root = rsqrt_fast(fmaf(sums.x, inv, a.eps));
+    // a row of zeros at a group's end must not reach dw: with eps 0 its root would be infinite
+    const float root = r < mine ? rsqrt_fast(fmaf(sums.x, inv, a.eps)) : 0.f;
     dw = fma_row(z * root, v, dw);
     const float down = -inv * sums.y * root * root * root;
     const F2 down2 = f2(down, down);

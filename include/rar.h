@@ -471,9 +471,9 @@ RAR_API rar_status rar_page_tables(const int32_t* lens, const int32_t* new_token
  * (a, b) -> (a cos - b sin, b cos + a sin). cos_sin is float
  * [max_pos, rot_dim], rot_dim/2 cosines then rot_dim/2 sines a row (any scaling
  * for long contexts is in the table); rot_dim is a multiple of 8 up to
- * head_dim. q_weight and k_weight: head_dim elements of dtype. positions:
- * int32 [tokens]; one outside 0..max_pos-1 counts as 0 and reports
- * RAR_ERR_CAPACITY.
+ * head_dim. q_weight and k_weight: head_dim elements of dtype. eps may be 0; a
+ * head whose elements are all 0 has no norm then. positions: int32 [tokens]; one
+ * outside 0..max_pos-1 counts as 0 and reports RAR_ERR_CAPACITY.
  *
  * rar_qk_norm_rope: queries to q_out[r] [tokens, q_heads, head_dim] and keys to
  *   k_out[r] [tokens, kv_heads, head_dim]; values are not touched.

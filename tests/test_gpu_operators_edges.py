@@ -1,0 +1,115 @@
+"""GPU tests of the operators at the edges of their domain: vanishing values and no
+eps, sums that must neither miss nor repeat a row, zeros of both signs,
+infinities and NaN in valid places. Bounds as in test_gpu_operators.py, from
+binary32 roundings of the 64-bit computation's magnitudes, unless a test derives
+its own."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from collective_communication_gb300 import binding as B
+from test_gpu_operators import DT, U, close, gen, normal, turn64
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.load_library()
+    yield
+
+
+# ------------------------------------------------------------ norm and rotation
+def rope_inputs(seed, n, t, q, kv, d, rot, dtype, scale):
+    g = gen(seed)
+    qkv = normal(g, n, t, (q + 2 * kv) * d, dtype=DT[dtype], scale=scale)
+    wq, wk = normal(g, d, dtype=DT[dtype]), normal(g, d, dtype=DT[dtype])
+    angle = torch.rand((300, rot // 2), generator=g, device="cuda") * 6.3
+    pos = torch.randint(0, 300, (t,), generator=g, device="cuda", dtype=torch.int32)
+    grads = [normal(g, n, t, h, d, dtype=DT[dtype]) for h in (q, kv, kv)]
+    return qkv, wq, wk, torch.cat([angle.cos(), angle.sin()], 1), pos, grads
+
+
+def check_rope(qkv, wq, wk, cs, pos, grads, q, kv, d, inter, eps):
+    """Forward and gradient against 64 bits."""
+    n, t = qkv.shape[:2]
+    rot = cs.shape[1]
+    x = qkv.double().view(n, t, q + 2 * kv, d)[:, :, :q + kv]
+    r = (x.square().mean(-1, keepdim=True) + eps).rsqrt()
+    xh = x * r
+    w = torch.cat([wq.double().expand(q, d), wk.double().expand(kv, d)])
+    row = cs.double()[pos.long()][None, :, None]
+
+    def span(v):  # of the magnitudes that meet in a rotation
+        return v + turn64(v, row.abs(), rot, inter).abs() + turn64(v, -row.abs(), rot, inter).abs()
+
+    y = turn64(xh * w, row, rot, inter)
+    dy = torch.cat(grads[:2], 2).double()
+    z = turn64(dy, row, rot, inter, back=True)
+    zs = span(dy.abs())
+    a = z * w
+    dx = r * (a - xh * (a * xh).mean(-1, keepdim=True))
+    size = r * (zs * w.abs() + xh.abs() * (zs * w.abs() * xh.abs()).mean(-1, keepdim=True))
+    ws = B.OpWorkspace(B.qk_norm_rope_workspace_bytes(n, d))
+    yq, yk = (torch.full((n, t, h, d), NAN, dtype=qkv.dtype, device="cuda") for h in (q, kv))
+    B.qk_norm_rope(qkv, wq, wk, cs, pos, yq, yk, ws, eps=eps, interleaved=inter)
+    slack = (d / 2 + 12) * U * span((xh * w).abs())
+    close(yq, y[:, :, :q], slack[:, :, :q], "q")
+    close(yk, y[:, :, q:], slack[:, :, q:], "k")
+    dqkv = torch.full_like(qkv, NAN)
+    dwq, dwk = (torch.full((n, d), NAN, device="cuda") for _ in range(2))
+    B.qk_norm_rope_backward(qkv, wq, wk, cs, pos, *grads, dqkv, dwq, dwk, ws, eps=eps, interleaved=inter)
+    assert B.get_status(ws) == B.Status.OK
+    got = dqkv.view(n, t, q + 2 * kv, d)
+    close(got[:, :, :q + kv], dx, (2 * d + 24) * U * size, "dx")
+    assert torch.equal(got[:, :, q + kv:], grads[2])
+    for dw, heads in ((dwq, slice(0, q)), (dwk, slice(q, q + kv))):
+        mag = (zs * xh.abs())[:, :, heads].sum((1, 2))
+        close(dw, (z * xh)[:, :, heads].sum((1, 2)), (t * (q + kv) + d + 24) * U * mag, "dw")
+
+
+@pytest.mark.parametrize("n,t,q,kv,d,rot,inter,dtype", [
+    (1, 1, 1, 1, 64, 64, False, "f32"), (2, 1, 8, 1, 128, 128, False, "bf16"), (1, 3, 32, 4, 96, 48, True, "bf16"),
+    (1, 5, 3, 1, 8, 8, False, "f32"), (2, 701, 5, 3, 80, 40, False, "f32"), (1, 3001, 12, 4, 64, 64, True, "bf16"),
+    (1, 2, 4, 2, 256, 128, False, "bf16")])
+def test_norm_rope_without_eps(n, t, q, kv, d, rot, inter, dtype):
+    """Groups of threads that have fewer rows than their neighbours add nothing to the weights' gradient."""
+    check_rope(*rope_inputs(41, n, t, q, kv, d, rot, dtype, 1.0), q, kv, d, inter, 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [-45, -60])
+def test_norm_rope_of_vanishing_rows(power, dtype):
+    """Rows so small that the third power of 1 / rms, or the second, is past binary32, while the results are not."""
+    check_rope(*rope_inputs(42, 2, 9, 4, 2, 96, 48, dtype, 2.0 ** power), 4, 2, 96, False, 0.0)
+
+
+@pytest.mark.parametrize("n,t,q,kv,d,dtype", [
+    (1, 1500, 7, 3, 128, "f32"), (2, 4097, 4, 2, 64, "bf16"), (1, 20000, 2, 1, 256, "bf16"), (1, 130, 32, 4, 80, "f32")])
+def test_norm_rope_weight_gradient_counts_every_row_once(n, t, q, kv, d, dtype):
+    """Elements of +-1 and whole gradients, nothing turned: each weight's gradient is a sum of whole numbers from 1 to 4,
+    of either sign, that binary32 holds exactly, times a 1 / rms of 1 that is off by 4 u at most and rounded once more: less
+    than 1/2 in all, where a row that was left out or added twice is 1 or more."""
+    g = gen(44)
+
+    def signs(*shape):
+        return (torch.randint(0, 2, shape, generator=g, device="cuda") * 2 - 1).to(DT[dtype])
+
+    def whole(h):
+        return signs(n, t, h, d) * torch.randint(1, 5, (n, t, h, d), generator=g, device="cuda").to(DT[dtype])
+
+    qkv, dq, dk = signs(n, t, (q + 2 * kv) * d), whole(q), whole(kv)
+    w = torch.ones(d, dtype=DT[dtype], device="cuda")
+    cs = torch.cat([torch.ones(4, 8, device="cuda"), torch.zeros(4, 8, device="cuda")], 1)
+    pos = torch.zeros(t, dtype=torch.int32, device="cuda")
+    assert 4 * t * max(q, kv) * 6 * U < 0.5
+    ws = B.OpWorkspace(B.qk_norm_rope_workspace_bytes(n, d))
+    dwq, dwk = (torch.full((n, d), NAN, device="cuda") for _ in range(2))
+    B.qk_norm_rope_backward(qkv, w, w, cs, pos, dq, dk, dk, torch.empty_like(qkv), dwq, dwk, ws, eps=0.0)
+    x = qkv.double().view(n, t, q + 2 * kv, d)
+    for got, dy, heads in ((dwq, dq, slice(0, q)), (dwk, dk, slice(q, q + kv))):
+        assert float((got.double() - (dy.double() * x[:, :, heads]).sum((1, 2))).abs().max()) < 0.5
