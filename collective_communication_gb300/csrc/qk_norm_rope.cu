@@ -187,9 +187,10 @@ __device__ __forceinline__ float2 group_sum2(float x, float y) {  // two sums si
   }
   return unpack(s);
 }
+// Subnormal x counts as it is: a row of zeros with such an eps has a norm.
 __device__ __forceinline__ float rsqrt_fast(float x) {
   float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // The lane's weights of a head's kind.

@@ -88,6 +88,13 @@ def test_norm_rope_of_vanishing_rows(power, dtype):
     check_rope(*rope_inputs(42, 2, 9, 4, 2, 96, 48, dtype, 2.0 ** power), 4, 2, 96, False, 0.0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_rope_of_zero_rows_with_a_subnormal_eps(dtype):
+    inputs = rope_inputs(43, 1, 5, 4, 2, 64, 64, dtype, 1.0)
+    inputs[0][:, 2] = 0
+    check_rope(*inputs, 4, 2, 64, False, 2.0 ** -140)
+
+
 @pytest.mark.parametrize("n,t,q,kv,d,dtype", [
     (1, 1500, 7, 3, 128, "f32"), (2, 4097, 4, 2, 64, "bf16"), (1, 20000, 2, 1, 256, "bf16"), (1, 130, 32, 4, 80, "f32")])
 def test_norm_rope_weight_gradient_counts_every_row_once(n, t, q, kv, d, dtype):
