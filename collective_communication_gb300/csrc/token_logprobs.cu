@@ -69,9 +69,9 @@ __device__ __forceinline__ float sum_of(F2 a) {
   return p.x + p.y;
 }
 
-// A value's bits made monotonic, a NaN above all.
+// A value's bits made monotonic, a NaN above all, -0 as 0 (-0 + 0 is 0).
 __device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t u = __float_as_uint(v);
+  const uint32_t u = __float_as_uint(v + 0.f);
   return v != v ? 0xffffffffu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 // Larger value first, then the lower index. 0 is below every key.

@@ -8,7 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from collective_communication_gb300 import binding as B
-from test_gpu_operators import DT, U, close, gen, normal, turn64
+from test_gpu_operators import DT, U, close, gen, normal, run_logprobs, turn64
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,29 @@ def test_norm_rope_weight_gradient_counts_every_row_once(n, t, q, kv, d, dtype):
     x = qkv.double().view(n, t, q + 2 * kv, d)
     for got, dy, heads in ((dwq, dq, slice(0, q)), (dwk, dk, slice(q, q + kv))):
         assert float((got.double() - (dy.double() * x[:, :, heads]).sum((1, 2))).abs().max()) < 0.5
+
+
+# ------------------------------------------------------------ log probabilities
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("top", [1, 2, 5, 9, 32])
+def test_token_logprobs_alternatives_hold_both_zeros_equal(top, dtype):
+    """0 and -0 are one value, so the lower index comes first, wherever they lie in a row and its parts."""
+    g = gen(51)
+    for widths in ([40], [33, 700], [1024] * 5, [9000, 1], [16384] * 8, [131072]):
+        total = sum(widths)
+        rows = 6
+        x = -1 - torch.rand((rows, total), generator=g, device="cuda")
+        x[0, -1], x[0, 3] = 0.0, -0.0                 # two, the negative one first
+        x[1, 0], x[1, total // 2], x[1, -2] = -0.0, 0.0, -0.0
+        x[2] = torch.where(torch.rand(total, generator=g, device="cuda") < 0.5, 0.0, -0.0)
+        x[3] = -0.0
+        x[3, total // 3:] = 0.0                       # the negative ones first
+        many = torch.randperm(total, generator=g, device="cuda")[:40]
+        x[4, many] = torch.where(many % 2 == 0, 0.0, -0.0)
+        x[5, many] = torch.where(many % 3 == 0, 0.0, -0.0)
+        x[5, many[:3]] = 2.0
+        x = x.to(DT[dtype])
+        parts = [p.contiguous() for p in x.split(widths, 1)]
+        o, _ = run_logprobs(parts, torch.zeros(rows, dtype=torch.int32, device="cuda"), top)
+        order = torch.sort(x.double(), dim=1, descending=True, stable=True)
+        assert torch.equal(o["top_ids"].long(), order.indices[:, :top]), widths
