@@ -708,7 +708,8 @@ __global__ void __launch_bounds__(Shape<T, DP, NT, H>::kThreads, Shape<T, DP, NT
 #pragma unroll
       for (int w = 1; w < kDaWarps; w++) m = fmaxf(m, sh.m[w][tid]);
 #pragma unroll
-      for (int w = 0; w < kDaWarps; w++) l += sh.m[w][tid] == -INFINITY ? 0.f : sh.l[w][tid] * exp2_fast(sh.m[w][tid] - m);
+      for (int w = 0; w < kDaWarps; w++)  // without a maximum the sum is 0, or NaN if scores are, which shows in the total
+        l += sh.m[w][tid] == -INFINITY ? sh.l[w][tid] : sh.l[w][tid] * exp2_fast(sh.m[w][tid] - m);
       sh.top[tid] = m;
       sh.total[tid] = l;
     }

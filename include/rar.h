@@ -521,9 +521,11 @@ RAR_API rar_status rar_qk_norm_rope_backward(const void* const* qkv, int nranks,
  *   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = log sum_t exp(scale * q . k_t)
  * lens[b] counts the new token, whose key and value are in the cache already.
  * A request of length 0 gives out 0 and lse -inf. Cache rows past a length may
- * hold anything, infinities and NaN too. A key or value of a valid token that
- * is infinite or NaN makes its heads' results infinite or NaN (a token whose
- * score is -inf has no weight; no token with a weight gives 0 and -inf). A page number
+ * hold anything, infinities and NaN too. A valid token whose score comes out as
+ * +inf or NaN makes out and lse of that query head NaN; RAR_F32 gives any product
+ * with an infinity the score NaN. A score of -inf has no weight, and no token with
+ * a weight gives out 0 and lse -inf. A value of a valid token that is infinite or
+ * NaN makes out infinite or NaN, not lse. A page number
  * outside 0..num_pages-1 within a length, or a length past the table row,
  * reports RAR_ERR_CAPACITY; the tokens concerned are left out.
  * lse: host array of nranks pointers to float [batch, q_heads], or NULL.

@@ -8,11 +8,12 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from collective_communication_gb300 import binding as B
-from test_gpu_operators import DT, U, close, gen, normal, run_logprobs, turn64
+from test_gpu_operators import DT, U, attention64, attention_case, close, gen, i32, normal, run_attention, run_logprobs, \
+    turn64
 
 pytestmark = pytest.mark.gpu
 
-NAN = float("nan")
+INF, NAN = float("inf"), float("nan")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -146,3 +147,67 @@ def test_token_logprobs_alternatives_hold_both_zeros_equal(top, dtype):
         o, _ = run_logprobs(parts, torch.zeros(rows, dtype=torch.int32, device="cuda"), top)
         order = torch.sort(x.double(), dim=1, descending=True, stable=True)
         assert torch.equal(o["top_ids"].long(), order.indices[:, :top]), widths
+
+
+# -------------------------------------------------------------------- attention
+ATTENTION = [(q, kv, d, dtype) for dtype in ("f32", "bf16")
+             for q, kv, d in ((8, 2, 64), (16, 1, 128), (3, 1, 80), (12, 1, 192), (5, 1, 256))]
+
+
+@pytest.mark.parametrize("q,kv,d,dtype", ATTENTION)
+@pytest.mark.parametrize("length", [1, 16, 17, 65, 130, 5000])
+def test_decode_attention_nan_in_a_valid_key(length, q, kv, d, dtype):
+    """A NaN in the key of a valid token, wherever it lies among the tokens that a warp, a tile or a block takes, is in
+    out and lse of its head's queries, and nowhere else."""
+    lens = [length, 40, length]
+    places = sorted({0, length - 1, length // 2, min(length - 1, 16), min(length - 1, 64)})
+    x, k, v, table, ln = attention_case(61, 1, lens, q, kv, d, 16, dtype)
+    want, wlse, tol, ltol = attention64(x, k, v, table, ln, d ** -0.5, 16)
+    for t in places:
+        bad = k.clone()
+        bad[0, table[0, t // 16].long(), 0, t % 16, d // 2] = NAN
+        out, lse, status, _ = run_attention(x, bad, v, table, ln)
+        assert status == B.Status.OK
+        mine = slice(0, q // kv)
+        assert bool(out[0, 0, mine].isnan().all()) and bool(lse[0, 0, mine].isnan().all()), t
+        rest = torch.ones((1, 3, q), dtype=torch.bool, device="cuda")
+        rest[0, 0, mine] = False
+        close(out[rest], want[rest], tol[rest], "out of the others")
+        close(lse[rest], wlse[rest], ltol[rest], "lse of the others")
+
+
+@pytest.mark.parametrize("q,kv,d,dtype", ATTENTION)
+def test_decode_attention_nan_in_a_query(q, kv, d, dtype):
+    lens = [1, 17, 700, 5000, 0]
+    x, k, v, table, ln = attention_case(62, 1, lens, q, kv, d, 16, dtype)
+    want, wlse, tol, ltol = attention64(x, k, v, table, ln, d ** -0.5, 16)
+    x = x.clone()
+    x[:, :, q - 1, 3] = NAN
+    out, lse, status, _ = run_attention(x, k, v, table, ln)
+    assert status == B.Status.OK
+    assert bool(out[0, :4, q - 1].isnan().all()) and bool(lse[0, :4, q - 1].isnan().all())
+    assert not bool(out[0, 4].any()) and bool((lse[0, 4] == -INF).all())  # nothing to attend to
+    close(out[:, :4, :q - 1], want[:, :4, :q - 1], tol[:, :4, :q - 1], "out of the others")
+    close(lse[:, :4, :q - 1], wlse[:, :4, :q - 1], ltol[:, :4, :q - 1], "lse of the others")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("length", [1, 17, 3000])
+def test_decode_attention_infinite_key(length, dtype):
+    """A score of +inf, or in binary32 any product with an infinity, makes out and lse NaN; a score of -inf is one of no
+    weight."""
+    q, d = 8, 64
+    x, k, v, table, ln = attention_case(63, 1, [length], q, 1, d, 16, dtype)
+    t = length - 1
+    x[0, 0, :, 5] = x[0, 0, :, 5].abs() + 0.5
+    x[0, 0, :4, 5] *= -1
+    bad = k.clone()
+    bad[0, table[0, t // 16].long(), 0, t % 16, 5] = INF
+    out, lse, status, _ = run_attention(x, bad, v, table, ln)
+    assert status == B.Status.OK
+    nan = slice(4, q) if dtype == "bf16" else slice(0, q)
+    assert bool(out[0, 0, nan].isnan().all()) and bool(lse[0, 0, nan].isnan().all())
+    if dtype == "bf16":
+        want, wlse, tol, ltol = attention64(x, k, v, table, i32(length - 1), d ** -0.5, 16)
+        close(out[:, :, :4], want[:, :, :4], tol[:, :, :4], "without the token")
+        close(lse[:, :, :4], wlse[:, :, :4], ltol[:, :, :4], "lse without the token")
