@@ -470,8 +470,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const __g
 }
 
 // dx = g ([i == token] - p) - h p (y + entropy), y = x - lse, p = exp(y); g counts
-// only if a token was asked for. One pass, read and written once; SPAN threads (a
-// block, or a warp) take SPAN * 8 * kLpBwdPacks columns of a row of a shard.
+// only if a token was asked for, and without it and h dx is 0 even where p is not
+// a number. One pass, read and written once; SPAN threads (a block, or a warp) take
+// SPAN * 8 * kLpBwdPacks columns of a row of a shard.
 constexpr int kLpBwdPacks = 8;  // of a thread
 
 template <typename T, int SPAN>
@@ -492,12 +493,13 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __
   const int64_t token = a.tokens[row];
   const bool asked = token >= 0 && token < a.first[a.nranks];
   const float g = asked ? a.grad_logprob[row] : 0.f;
+  const bool nothing = !asked && h == 0.f;  // the row's terms are constants: gradient 0, whatever its logits are
   const float base = g + h * a.entropy[row];
   const int64_t at = token - a.first[rank] - c0;
   const int mine = asked && at >= 0 && at < n ? (int)at : -1;
   auto grad = [&](float v) {
-    const float y = max_nan(v - lse, kFloorT);
-    return -exp2_fast(y * kLog2e) * fmaf(h, y, base);
+    const float y = max_nan(v - lse, kFloorT), d = -exp2_fast(y * kLog2e) * fmaf(h, y, base);
+    return nothing ? 0.f : d;
   };
   // rows that share a 16-byte phase go in packs, the ends one by one; others one by one altogether
   const bool together = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;

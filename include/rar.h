@@ -557,7 +557,9 @@ RAR_API rar_status rar_decode_attention(const void* const* q, int64_t q_stride, 
  *   sum(grad_logprob * logprob) + sum(grad_entropy * entropy) from lse and
  *   entropy of the forward call (grad_entropy NULL: no such term):
  *   dx_i = grad_logprob ([i == token] - p_i) - grad_entropy p_i (log p_i + entropy).
- *   grad_logprob of a row that asks for nothing is not read as a gradient.
+ *   grad_logprob of a row that asks for nothing is not read as a gradient; if its
+ *   entropy term is absent or grad_entropy is 0, the row's gradient is 0 whatever
+ *   its logits are.
  *   dlogits[r] == logits[r] with one stride (in place) is allowed.
  */
 RAR_API size_t rar_token_logprobs_workspace_bytes(int64_t rows, int top);

@@ -149,6 +149,36 @@ def test_token_logprobs_alternatives_hold_both_zeros_equal(top, dtype):
         assert torch.equal(o["top_ids"].long(), order.indices[:, :top]), widths
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("widths", [[500, 499], [20001]])
+@pytest.mark.parametrize("entropy", ["none", "zero"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_token_logprobs_gradient_of_rows_without_a_token(widths, dtype, entropy, in_place):
+    """Their log probability is the constant 0, whatever the logits are: a padding row of NaN, or with nothing but -inf,
+    has the gradient 0."""
+    g = gen(52)
+    total = sum(widths)
+    x = normal(g, 5, total, dtype=DT[dtype], scale=3.0)
+    x[1] = -INF
+    x[2, 7], x[3, total - 1] = NAN, INF
+    tokens = i32(-1, -1, total, -5, 2)
+    parts = [p.clone() for p in x.split(widths, 1)]
+    o, ws = run_logprobs(parts, tokens, 0)
+    assert o["logprob"][:4].tolist() == [0] * 4
+    out = parts if in_place else [torch.full_like(p, NAN) for p in parts]
+    grad = torch.tensor([NAN, 1.0, 2.0, INF, 0.5], device="cuda")
+    h = None if entropy == "none" else torch.zeros(5, device="cuda")
+    B.token_logprobs_backward(parts, tokens, o["lse"], o["entropy"], grad, h, out, ws)
+    assert B.get_status(ws) == B.Status.OK
+    got = torch.cat(out, 1)
+    assert not bool(got[:4].any())  # NaN counts as true
+    p = torch.softmax(x[4].double(), 0)
+    want = 0.5 * ((torch.arange(total, device="cuda") == 2).double() - p)
+    size = x[4].double().abs() + abs(float(o["lse"][4]))
+    # p's exponent is off by 4 u of its terms and by lse's own error, of (4 total^(1/2) + 16) u and 4 u of its terms
+    close(got[4], want, 0.5 * (p + (want > 0)) * (8 * size + 4 * total ** 0.5 + 40) * U, "the row with a token")
+
+
 # -------------------------------------------------------------------- attention
 ATTENTION = [(q, kv, d, dtype) for dtype in ("f32", "bf16")
              for q, kv, d in ((8, 2, 64), (16, 1, 128), (3, 1, 80), (12, 1, 192), (5, 1, 256))]
