@@ -278,6 +278,7 @@ struct LogprobBwdArgs {
   int rows, nranks, dtype;
 };
 constexpr int kMaxTop = 32;
+constexpr int kLpTile = 1024;  // columns of a tile of the log probabilities; a call's tiles are counted in 32 bits
 
 cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);

@@ -539,6 +539,7 @@ rar_status rar_token_logprobs(const void* const* logits, const int64_t* vocab, c
   LogprobArgs a;
   std::memset(&a, 0, sizeof a);
   Spans s;
+  int64_t tiles = 0;  // of a row
   for (int r = 0; r < nranks; r++) {
     if (vocab[r] < 1 || vocab[r] > INT32_MAX) return RAR_ERR_ARG;
     if (rows > 1 && row_strides[r] < vocab[r]) return RAR_ERR_ARG;
@@ -546,9 +547,10 @@ rar_status rar_token_logprobs(const void* const* logits, const int64_t* vocab, c
     a.logits[r] = logits[r];
     a.row_stride[r] = row_strides[r];
     a.first[r + 1] = a.first[r] + vocab[r];
+    tiles += div_up(vocab[r], kLpTile);
     s.read(span(logits[r], rows, vocab[r] * es, row_strides[r] * es));
   }
-  if (a.first[nranks] > INT32_MAX || top > a.first[nranks]) return RAR_ERR_ARG;
+  if (a.first[nranks] > INT32_MAX || top > a.first[nranks] || rows * tiles > INT32_MAX) return RAR_ERR_ARG;
   if (rows > 0 && (tokens == nullptr || logprob == nullptr || entropy == nullptr || lse == nullptr)) return RAR_ERR_ARG;
   if (rows > 0 && top > 0 && (top_values == nullptr || top_ids == nullptr)) return RAR_ERR_ARG;
   const void* all[] = {tokens, logprob, entropy, lse, top_values, top_ids};

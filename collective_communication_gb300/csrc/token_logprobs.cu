@@ -37,7 +37,6 @@ namespace rar {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpTile = 1024;             // columns of a tile
 constexpr int kLpMaxWorkers = 4864;       // most warps of a forward launch: a counter and two partial results each
 // Alternatives are inserted one by one, and lanes' words looked at by the whole warp, where there are few; more are
 // sorted, and found by each lane on its own (3 rows of 24848 words in f32, top 20: 14 us against 22; 704 rows of
@@ -559,7 +558,6 @@ cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) 
   for (int r = 0; r < a.nranks; r++)
     a.first_tile[r + 1] = a.first_tile[r] + (int)div_up(a.first[r + 1] - a.first[r], kLpTile);
   const int64_t tiles = (int64_t)a.rows * a.first_tile[a.nranks];
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   int64_t grid = imin((int64_t)resident, kLpMaxWorkers / kLpWarps);
   // With alternatives, rows in whole numbers of equal parts where that leaves few warps idle: a cut costs its row
   // another start of the list (2048 rows of 131072 words, in 2 parts each against 2.4: top 20 147 against 175 us, top 5

@@ -549,6 +549,7 @@ RAR_API rar_status rar_decode_attention(const void* const* q, int64_t q_stride, 
  *   entropy = -sum_i p_i log p_i, p = exp(x - lse), where p_i = 0 adds nothing;
  *   the top (0 to 32, at most the vocabulary) words by x, the lower index first
  *   among equal values: top_values[row, k] = x - lse, top_ids[row, k].
+ * rows times the sum over the ranks of ceil(vocab[r] / 1024) is below 2^31.
  * tokens: int32 [rows]; one outside the vocabulary (-1, say) asks for nothing:
  * logprob 0. Words of -inf have probability 0. A row with a NaN or +inf, or with
  * nothing but -inf, has NaN results; a NaN ranks above every number.
