@@ -54,13 +54,22 @@ def _compile(src, verbose_ptxas=False, debug=False):
     return obj, r.stderr
 
 
-def build_operands(force: bool = False) -> str:
-    """Compile _operands.so, the CPython module that marshals the operators' calls."""
+def build_operands(force: bool = False):
+    """Compile _operands.so, the CPython module that marshals the operators' calls; returns its path. Without Python's
+    headers there is none, and the binding's operators say so when they are called: the C ABI and the collectives do
+    without."""
     target, source = os.path.join(HERE, "_operands.so"), os.path.join(CSRC, "operands.c")
     if force or _stale(target, [source, os.path.join(ROOT, "include", "rar.h")]):
+        python = sysconfig.get_paths()["include"]
+        if not os.path.exists(os.path.join(python, "Python.h")):
+            if os.path.exists(target):  # of another source
+                os.remove(target)
+            sys.stderr.write(f"_operands.so is not built, for {python} has no Python.h: the operators cannot be called "
+                             "from Python\n")
+            return None
         tmp = target + ".tmp%d" % os.getpid()
-        cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-fPIC", "-shared", "-fvisibility=hidden", "-I",
-               sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), source, "-o", tmp, "-lm"]
+        cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=gnu11", "-fPIC", "-shared", "-fvisibility=hidden", "-I", python,
+               "-I", os.path.join(ROOT, "include"), source, "-o", tmp, "-lm"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"{cmd[0]} failed on operands.c:\n{r.stdout}\n{r.stderr}")
@@ -70,8 +79,6 @@ def build_operands(force: bool = False) -> str:
 
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
     """Compile and link librar.so (debug=True: librar_debug.so); returns its path."""
-    if not debug:  # one module serves both variants
-        build_operands(force)
     build_dir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
     os.makedirs(build_dir, exist_ok=True)
     if force:
@@ -85,7 +92,10 @@ def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False)
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)
-    return _link(lib, objs, force)
+    _link(lib, objs, force)
+    if not debug:  # one module serves both variants
+        build_operands(force)
+    return lib
 
 
 def build_all(force: bool = False) -> list:
