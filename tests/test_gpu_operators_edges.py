@@ -150,6 +150,19 @@ def test_token_logprobs_alternatives_hold_both_zeros_equal(top, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_token_logprobs_of_a_word_that_holds_everything(dtype):
+    """A word above all others by 2e30 has the whole probability."""
+    x = torch.full((2, 3000), -1e30, device="cuda")
+    x[0, 5] = x[1, 2999] = 1e30
+    x = x.to(DT[dtype])
+    o, _ = run_logprobs([x[:, :1001].contiguous(), x[:, 1001:].contiguous()], i32(6, 2999), 2)
+    assert o["entropy"].tolist() == [0, 0]
+    assert float(o["logprob"][0]) <= -1e30 and float(o["logprob"][1]) == 0
+    assert o["top_ids"].tolist() == [[5, 0], [2999, 0]] and o["top_values"][:, 0].tolist() == [0, 0]
+    assert torch.equal(o["lse"], x.float().amax(1))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("widths", [[500, 499], [20001]])
 @pytest.mark.parametrize("entropy", ["none", "zero"])
 @pytest.mark.parametrize("in_place", [False, True])
