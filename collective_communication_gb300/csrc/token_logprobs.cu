@@ -586,7 +586,10 @@ cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, cudaStream_t stre
   // Narrow rows go a warp each, if there are more of them than the SMs hold blocks: 16777 rows of 8 shards of 500 words
   // in bf16 60 us against 242, of 2048 42 against 74, of 6007 44 against 45; wider ones the other way (8192: 42, 41), and
   // so 12 rows of 1500 (2.9, 2.3).
-  const bool narrow = widest * (a.dtype == kF32 ? 4 : 2) <= 12288 && (int64_t)a.rows * a.nranks > 8 * 152;
+  int device = 0, sms = 0;
+  const cudaError_t e = current_device_sms(&device, &sms);
+  if (e != cudaSuccess) return e;
+  const bool narrow = widest * (a.dtype == kF32 ? 4 : 2) <= 12288 && (int64_t)a.rows * a.nranks > 8 * sms;
   const int span = narrow ? 32 : kLpThreads;
   int tiles = (int)div_up(widest, span * 8 * kLpBwdPacks);
   if (trace_on())
