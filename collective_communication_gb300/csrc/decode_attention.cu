@@ -865,7 +865,8 @@ DecodeKernel kernel_for(int dtype, int head_dim, int group) {
 
 }  // namespace
 
-int64_t decode_attention_scratch_bytes(int, int, int q_heads, int kv_heads, int head_dim) {
+// Two partial results of each block that a launch may have, whatever the batch is.
+int64_t decode_attention_scratch_bytes(int q_heads, int kv_heads, int head_dim) {
   const int group = q_heads / kv_heads;
   return 2ll * kDaMaxBlocks * imax(kernel_for(kF32, head_dim, group).partial, kernel_for(kBF16, head_dim, group).partial) *
          (int64_t)sizeof(float);

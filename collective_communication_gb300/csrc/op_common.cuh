@@ -126,7 +126,6 @@ struct Pack8<uint16_t> {
   uint4 u;
   __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void load_stream(const uint16_t* p) { u = ld_stream_v4(p); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void absent() { u = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
@@ -149,7 +148,6 @@ struct Pack8<float> {
     a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
     b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void absent() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -288,7 +286,7 @@ cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream);
 cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, cudaStream_t stream);
 
 int64_t norm_rope_scratch_bytes(int nranks, int head_dim);
-int64_t decode_attention_scratch_bytes(int nranks, int batch, int q_heads, int kv_heads, int head_dim);
-int64_t token_logprobs_scratch_bytes(int rows, int top);
+int64_t decode_attention_scratch_bytes(int q_heads, int kv_heads, int head_dim);
+int64_t token_logprobs_scratch_bytes();
 
 }  // namespace rar

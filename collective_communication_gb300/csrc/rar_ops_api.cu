@@ -448,7 +448,7 @@ size_t rar_decode_attention_workspace_bytes(int nranks, int batch, int q_heads, 
   if (nranks < 1 || nranks > kMaxRanks || batch < 0 || !heads_ok(q_heads, kv_heads, head_dim) ||
       q_heads % kv_heads != 0)
     return 0;
-  return (size_t)(kOpScratchOffset + decode_attention_scratch_bytes(nranks, batch, q_heads, kv_heads, head_dim));
+  return (size_t)(kOpScratchOffset + decode_attention_scratch_bytes(q_heads, kv_heads, head_dim));
 }
 
 rar_status rar_decode_attention(const void* const* q, int64_t q_stride, const void* const* k_cache,
@@ -490,7 +490,7 @@ rar_status rar_decode_attention(const void* const* q, int64_t q_stride, const vo
   s.write(span(workspace, (int64_t)workspaceBytes));
   if (s.clash()) return RAR_ERR_ARG;
   if ((st = check_workspace(workspace, workspaceBytes,
-                            decode_attention_scratch_bytes(nranks, batch, q_heads, kv_heads, head_dim))) != RAR_OK)
+                            decode_attention_scratch_bytes(q_heads, kv_heads, head_dim))) != RAR_OK)
     return st;
   if (batch == 0) return RAR_OK;
   DecodeArgs a;
@@ -523,7 +523,7 @@ rar_status rar_decode_attention(const void* const* q, int64_t q_stride, const vo
 
 size_t rar_token_logprobs_workspace_bytes(int64_t rows, int top) {
   if (rows < 0 || rows > INT32_MAX || top < 0 || top > kMaxTop) return 0;
-  return (size_t)(kOpScratchOffset + token_logprobs_scratch_bytes((int)rows, top));
+  return (size_t)(kOpScratchOffset + token_logprobs_scratch_bytes());
 }
 
 rar_status rar_token_logprobs(const void* const* logits, const int64_t* vocab, const int64_t* row_strides, int nranks,
@@ -564,7 +564,7 @@ rar_status rar_token_logprobs(const void* const* logits, const int64_t* vocab, c
   s.write(span(top_ids, rows * top * 4));
   s.write(span(workspace, (int64_t)workspaceBytes));
   if (s.clash()) return RAR_ERR_ARG;
-  if ((st = check_workspace(workspace, workspaceBytes, token_logprobs_scratch_bytes((int)rows, top))) != RAR_OK)
+  if ((st = check_workspace(workspace, workspaceBytes, token_logprobs_scratch_bytes())) != RAR_OK)
     return st;
   if (rows == 0) return RAR_OK;
   a.tokens = tokens;

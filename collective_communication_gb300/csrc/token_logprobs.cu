@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_bwd_kernel(const __
   }
 }
 
-int64_t token_logprobs_scratch_bytes(int, int) { return 2ll * kLpMaxWorkers * kLpPartFloats * (int64_t)sizeof(float); }
+// Two partial results of each warp that a launch may have, whatever the rows are.
+int64_t token_logprobs_scratch_bytes() { return 2ll * kLpMaxWorkers * kLpPartFloats * (int64_t)sizeof(float); }
 
 cudaError_t launch_token_logprobs(const LogprobArgs& args, cudaStream_t stream) {
   LogprobArgs a = args;

@@ -423,7 +423,9 @@ RAR_API rar_status rar_describe_geometry(int nranks, size_t count, rar_dtype dty
  * RAR_OP_WORKSPACE_MIN_BYTES, and what the *_workspace_bytes function of each
  * operator used with it says; an operator without one needs the minimum). It
  * serves any of these operators, at any sizes it has room for, in any order on
- * one stream; nothing carries over from call to call.
+ * one stream; nothing carries over from call to call. Partial results are left
+ * per block, so the attention's bytes depend on the heads and their size alone,
+ * the log probabilities' on nothing: more requests or rows need no more.
  *
  * Streams: calls are ordered as any kernel is. They are launched with
  * programmatic stream serialization: an operator's blocks may come up while the
