@@ -412,12 +412,14 @@ RAR_API rar_status rar_describe_geometry(int nranks, size_t count, rar_dtype dty
  *             tokens of a page lie together. Slot s is token s % page_size of
  *             page s / page_size; num_pages * page_size * kv_heads < 2^31.
  *   block_table  int32 [requests, max_blocks], rows table_stride apart: entry c
- *             is the page of the request's tokens c * page_size and up. Entries
- *             past the request's length are not read.
- * head_dim is a multiple of 8 up to 256; q_heads and kv_heads up to 1024. Sums,
- * norms and softmax statistics are binary32; results are rounded once. A call's
- * outputs may not overlap each other, its inputs or the workspace except where
- * in place is allowed.
+ *             is the page of the request's tokens c * page_size and up; one or
+ *             more entries a row, max_blocks * page_size < 2^31. Entries past the
+ *             request's length are not read.
+ * head_dim is a multiple of 8 up to 256; q_heads and kv_heads up to 1024; in qkv
+ * tokens * (q_heads + 2 kv_heads) < 2^31. Sums, norms and softmax statistics are
+ * binary32, the squares of a norm too; results are rounded once. A call's outputs
+ * may not overlap each other, its inputs or the workspace except where in place
+ * is allowed.
  *
  * Workspace: rar_op_workspace_init() prepares one (256-byte aligned, at least
  * RAR_OP_WORKSPACE_MIN_BYTES, and what the *_workspace_bytes function of each
@@ -482,8 +484,8 @@ RAR_API rar_status rar_page_tables(const int32_t* lens, const int32_t* new_token
  * rar_qk_norm_rope_cached: queries to q_out[r]; keys and values to the cache
  *   rows of slots (int32 [tokens]; a negative slot is a padding token, whose
  *   query is written and whose key and value are not; one past the cache
- *   reports RAR_ERR_CAPACITY and is not written). Two tokens of one slot: one
- *   of them is kept.
+ *   reports RAR_ERR_CAPACITY and is not written). The tokens' slots differ: two
+ *   of one slot leave elements of both in it.
  * Both: q_out[r] == qkv[r] with q_stride == qkv_stride (queries in place) is
  *   allowed. tokens 0 enqueues nothing.
  * rar_qk_norm_rope_backward: from the gradients dq, dk, dv of y and of the
@@ -553,8 +555,9 @@ RAR_API rar_status rar_decode_attention(const void* const* q, int64_t q_stride, 
  *   among equal values: top_values[row, k] = x - lse, top_ids[row, k].
  * rows times the sum over the ranks of ceil(vocab[r] / 1024) is below 2^31.
  * tokens: int32 [rows]; one outside the vocabulary (-1, say) asks for nothing:
- * logprob 0. Words of -inf have probability 0. A row with a NaN or +inf, or with
- * nothing but -inf, has NaN results; a NaN ranks above every number.
+ * logprob 0. Words of -inf have probability 0. A row with a NaN or +inf has NaN
+ * results; so has one with nothing but -inf, except its lse, which is -inf. A NaN
+ * ranks above every number, and 0 and -0 are equal.
  *
  * rar_token_logprobs_backward: the gradient with respect to the logits of
  *   sum(grad_logprob * logprob) + sum(grad_entropy * entropy) from lse and
