@@ -216,7 +216,11 @@ struct Tile<uint16_t, DP, NT> {
     }
   }
   // O^T += V^T P^T. P goes in as a bf16 and the bf16 of its remainder, two
-  // instructions: P's own rounding (2^-9) would be as large as the result's.
+  // instructions: P's own rounding (2^-9) would be as large as the result's. The
+  // instruction truncates its sum, by about 2^-23 of it each time: 3e-5 after the
+  // 144 tiles that a warp has of 64 requests up to 16384 tokens, where the result's
+  // rounding takes up to 2e-3, so here the sum runs on, as the binary32 form's does
+  // not. 0.2 to 0.3 % of the results are rounded otherwise than in 64 bits.
   __device__ __forceinline__ void accumulate(const float (&p)[NT][4], float (&o)[MT][NT][4]) const {
     uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
