@@ -48,7 +48,9 @@ EXPORTED = (
     "rar_debug_set_ll_flag_wrap", "rar_op_workspace_init", "rar_page_tables", "rar_qk_norm_rope",
     "rar_qk_norm_rope_cached", "rar_qk_norm_rope_workspace_bytes", "rar_qk_norm_rope_backward",
     "rar_decode_attention_workspace_bytes", "rar_decode_attention", "rar_token_logprobs_workspace_bytes",
-    "rar_token_logprobs", "rar_token_logprobs_backward",
+    "rar_token_logprobs", "rar_token_logprobs_backward", "rar_prompt_attention_workspace_bytes",
+    "rar_prompt_attention", "rar_prompt_attention_cached", "rar_prompt_attention_backward", "rar_embed_tokens",
+    "rar_embed_tokens_workspace_bytes", "rar_embed_tokens_backward",
 )
 
 
@@ -125,12 +127,23 @@ def load_library():
     L.rar_token_logprobs_workspace_bytes.argtypes = [I64, I]
     L.rar_token_logprobs.argtypes = [P, P, P, I, I64, I, P, P, P, P, I, P, P, P, SZ, P]
     L.rar_token_logprobs_backward.argtypes = [P, P, P, I, I64, I, P, P, P, P, P, P, P, P, SZ, P]
+    L.rar_prompt_attention_workspace_bytes.argtypes = [I, I64, I, I, I]
+    rows = [P, I64]
+    L.rar_prompt_attention.argtypes = rows * 3 + [I, I64, I, I, I, I, P, I, F] + rows + [P, P, SZ, P]
+    L.rar_prompt_attention_cached.argtypes = rows + [P, P, I, I64, I, I, I, I, I, I, P, I64, I, P, P, I, F] + rows + \
+        [P, P, SZ, P]
+    L.rar_prompt_attention_backward.argtypes = rows * 3 + [I, I64, I, I, I, I, P, I, F] + rows + [P] + rows * 4 + [P, SZ, P]
+    L.rar_embed_tokens.argtypes = [P, I64, P, P, P, I, I, I, F, P, I64, P, SZ, P]
+    L.rar_embed_tokens_workspace_bytes.argtypes = [I64, I]
+    L.rar_embed_tokens_backward.argtypes = [P, I64, P, I64, I, F, P, P, P, I, I, I, P, SZ, P]
     for name in ("rar_qk_norm_rope_workspace_bytes", "rar_decode_attention_workspace_bytes",
-                 "rar_token_logprobs_workspace_bytes"):
+                 "rar_token_logprobs_workspace_bytes", "rar_prompt_attention_workspace_bytes",
+                 "rar_embed_tokens_workspace_bytes"):
         getattr(L, name).restype = SZ
     for name in ("rar_op_workspace_init", "rar_page_tables", "rar_qk_norm_rope", "rar_qk_norm_rope_cached",
                  "rar_qk_norm_rope_backward", "rar_decode_attention", "rar_token_logprobs",
-                 "rar_token_logprobs_backward"):
+                 "rar_token_logprobs_backward", "rar_prompt_attention", "rar_prompt_attention_cached",
+                 "rar_prompt_attention_backward", "rar_embed_tokens", "rar_embed_tokens_backward"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -367,6 +380,16 @@ def token_logprobs_workspace_bytes(rows: int, top: int) -> int:
     return _op_bytes("rar_token_logprobs_workspace_bytes", rows, top)
 
 
+def prompt_attention_workspace_bytes(nranks: int, tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Workspace of any form of the prompt attention."""
+    return _op_bytes("rar_prompt_attention_workspace_bytes", nranks, tokens, q_heads, kv_heads, head_dim)
+
+
+def embed_tokens_workspace_bytes(tokens: int, hidden: int) -> int:
+    """Workspace of embed_tokens_backward."""
+    return _op_bytes("rar_embed_tokens_workspace_bytes", tokens, hidden)
+
+
 # The tensors are read and checked, and the C ABI called, by the CPython module
 # _operands (csrc/operands.c): a decode step makes these calls once a layer.
 _ops = None
@@ -382,7 +405,8 @@ def _op_setup():
                            "collective_communication_gb300/build.py` (or __graft_entry__.build())") from e
     lib = load_library()
     names = ("rar_page_tables", "rar_qk_norm_rope", "rar_qk_norm_rope_cached", "rar_qk_norm_rope_backward",
-             "rar_decode_attention", "rar_token_logprobs", "rar_token_logprobs_backward")
+             "rar_decode_attention", "rar_token_logprobs", "rar_token_logprobs_backward", "rar_prompt_attention",
+             "rar_prompt_attention_cached", "rar_prompt_attention_backward", "rar_embed_tokens", "rar_embed_tokens_backward")
     _operands.setup(RarError, (torch.float32, torch.bfloat16, torch.int32),
                     tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in names),
                     torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
@@ -471,6 +495,56 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_ent
         stream)
     if st:
         _check(st, "rar_token_logprobs_backward")
+
+
+def prompt_attention(q, k, v, starts, out, lse, workspace: OpWorkspace, scale: Optional[float] = None,
+                     stream=None) -> None:
+    """Enqueue causal attention over packed sequences: q, out [tokens, q_heads,
+    head_dim] and k, v [tokens, kv_heads, head_dim] a rank (v may be a view of
+    the projection's output), int32 starts [sequences + 1]; lse float32 [tokens,
+    q_heads] a rank, or None. scale: head_dim ** -0.5 by default."""
+    st = (_ops or _op_setup()).prompt_attention(q, k, v, starts, out, lse, scale, workspace.ptr, workspace.nbytes, stream)
+    if st:
+        _check(st, "rar_prompt_attention")
+
+
+def prompt_attention_cached(q, k_cache, v_cache, block_table, starts, lens, out, lse, workspace: OpWorkspace,
+                            scale: Optional[float] = None, stream=None) -> None:
+    """Enqueue attention of each request's new tokens over the paged cache that
+    holds them and the ones before: q, out, lse and starts as prompt_attention
+    has them, caches, block_table and lens as decode_attention has them."""
+    st = (_ops or _op_setup()).prompt_attention_cached(
+        q, k_cache, v_cache, block_table, starts, lens, out, lse, scale, workspace.ptr, workspace.nbytes, stream)
+    if st:
+        _check(st, "rar_prompt_attention_cached")
+
+
+def prompt_attention_backward(q, k, v, starts, out, lse, dout, dq, dk, dv, workspace: OpWorkspace,
+                              scale: Optional[float] = None, stream=None) -> None:
+    """Enqueue the gradient of prompt_attention: dq as q, dk as k and dv as v (views
+    of one gradient of the projection, say) from dout, out and lse."""
+    st = (_ops or _op_setup()).prompt_attention_backward(
+        q, k, v, starts, out, lse, dout, dq, dk, dv, scale, workspace.ptr, workspace.nbytes, stream)
+    if st:
+        _check(st, "rar_prompt_attention_backward")
+
+
+def embed_tokens(tokens, tables, out, workspace: OpWorkspace, scale: float = 1.0, stream=None) -> None:
+    """Enqueue the embedding lookup of int32 tokens over vocabulary shards tables
+    [shard, hidden] a rank (shards may differ in rows): out [tokens, hidden]."""
+    st = (_ops or _op_setup()).embed_tokens(tokens, tables, out, scale, workspace.ptr, workspace.nbytes, stream)
+    if st:
+        _check(st, "rar_embed_tokens")
+
+
+def embed_tokens_backward(tokens, dout, dtables, workspace: OpWorkspace, scale: float = 1.0, accumulate: bool = False,
+                          stream=None) -> None:
+    """Enqueue the tables' gradient, float32 dtables [shard, hidden] a rank, from
+    dout [tokens, hidden]: written whole, or with accumulate added to."""
+    st = (_ops or _op_setup()).embed_tokens_backward(
+        tokens, dout, dtables, scale, accumulate, workspace.ptr, workspace.nbytes, stream)
+    if st:
+        _check(st, "rar_embed_tokens_backward")
 
 
 def get_status(workspace, stream=None) -> Status:

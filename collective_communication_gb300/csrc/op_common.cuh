@@ -118,7 +118,7 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 
 // Eight consecutive elements of a row, widened to binary32 (T: float or
 // uint16_t holding bf16 bits; 16-byte aligned). load_stream: read once, past L1;
-// absent: -inf in all eight.
+// absent: -inf in all eight; zero: 0.
 template <typename T>
 struct Pack8;
 template <>
@@ -126,6 +126,7 @@ struct Pack8<uint16_t> {
   uint4 u;
   __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void load_stream(const uint16_t* p) { u = ld_stream_v4(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void absent() { u = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
@@ -148,6 +149,7 @@ struct Pack8<float> {
     a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
     b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
   }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void absent() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -275,6 +277,36 @@ struct LogprobBwdArgs {
   char* ws;
   int rows, nranks, dtype;
 };
+
+struct EmbedArgs {
+  const void* tables[kMaxRanks];
+  int64_t row_stride[kMaxRanks];
+  int64_t first[kMaxRanks + 1];  // word of each shard's first row; the last entry is the total
+  const int32_t* tokens_in;
+  void* out;
+  char* ws;
+  int64_t tokens, out_stride;
+  float scale;
+  int nranks, dtype, hidden;
+  int spans;  // set by the launcher: warps of a row
+};
+
+struct EmbedBwdArgs {
+  float* dtables[kMaxRanks];
+  int64_t drow_stride[kMaxRanks];
+  int64_t first[kMaxRanks + 1];
+  const int32_t* tokens_in;
+  const void* dout;
+  char* ws;
+  int64_t tokens, dout_stride;
+  float scale;
+  int nranks, dtype, hidden, accumulate;
+  // set by the launcher: pairs (word, token) in tiles and in one row, parts of sums; tiles, warps of a row
+  uint64_t* sorted_tiles;
+  uint64_t* sorted;
+  float* parts;
+  int tiles, spans;
+};
 constexpr int kMaxTop = 32;
 constexpr int kLpTile = 1024;  // columns of a tile of the log probabilities; a call's tiles are counted in 32 bits
 
@@ -284,9 +316,12 @@ cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_attention(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream);
 cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, cudaStream_t stream);
+cudaError_t launch_embed_tokens(EmbedArgs& a, cudaStream_t stream);  // fills in what the launcher sets
+cudaError_t launch_embed_tokens_bwd(EmbedBwdArgs& a, cudaStream_t stream);
 
 int64_t norm_rope_scratch_bytes(int nranks, int head_dim);
 int64_t decode_attention_scratch_bytes(int q_heads, int kv_heads, int head_dim);
 int64_t token_logprobs_scratch_bytes();
+int64_t embed_tokens_scratch_bytes(int64_t tokens, int hidden);
 
 }  // namespace rar

@@ -33,6 +33,11 @@ static struct {
   __typeof__(&rar_decode_attention) decode_attention;
   __typeof__(&rar_token_logprobs) token_logprobs;
   __typeof__(&rar_token_logprobs_backward) token_logprobs_backward;
+  __typeof__(&rar_prompt_attention) prompt_attention;
+  __typeof__(&rar_prompt_attention_cached) prompt_attention_cached;
+  __typeof__(&rar_prompt_attention_backward) prompt_attention_backward;
+  __typeof__(&rar_embed_tokens) embed_tokens;
+  __typeof__(&rar_embed_tokens_backward) embed_tokens_backward;
 } abi;
 
 /* Raises RarError(RAR_ERR_ARG, "name: what"); false, for the callers' returns. */
@@ -511,14 +516,203 @@ static PyObject* token_logprobs_backward(PyObject* self, PyObject* const* v, Py_
                                    lse, entropy, gl, gh, d.data, d.row, w.data, w.bytes, w.stream));
 }
 
-/* setup(RarError, (float32, bfloat16, int32), addresses of the seven functions in the order of `abi`, function of the
+/* Queries, [tokens, heads, head_dim] a rank, and what the forms of the attention over prompts share. */
+typedef struct {
+  Ranked q;
+  void* starts;
+  int sequences;
+  float scale;
+} Prompt;
+
+/* q, starts, scale or None */
+static bool read_prompt(PyObject* q, PyObject* starts, PyObject* scale, Prompt* p) {
+  int64_t bounds;
+  if (!read_ranked(q, "q", 3, &p->q) || !floating(p->q.dtype, "q") ||
+      !read_flat(starts, "starts", I32, -1, &p->starts, &bounds) || !fits_int(bounds, "starts") ||
+      !fits_int(p->q.size[1], "q") || !fits_int(p->q.size[2], "q"))
+    return false;
+  if (bounds < 1) return refuse("starts", "one more than the sequences");
+  p->sequences = (int)(bounds - 1);
+  p->scale = (float)(scale == Py_None ? 1.0 / sqrt((double)p->q.size[2]) : PyFloat_AsDouble(scale));
+  return !PyErr_Occurred();
+}
+/* A tensor as the queries are. */
+static bool read_like(PyObject* x, const char* name, const Ranked* q, Ranked* out) {
+  if (!read_ranked(x, name, 3, out)) return false;
+  return (same_size(out, q) && out->dtype == q->dtype) || refuse(name, "as q");
+}
+/* Keys or values: [tokens, kv_heads, head_dim] with the queries' tokens and head_dim. */
+static bool read_keys(PyObject* x, const char* name, const Ranked* q, Ranked* out) {
+  if (!read_ranked(x, name, 3, out)) return false;
+  return (out->ranks == q->ranks && out->dtype == q->dtype && out->size[0] == q->size[0] && out->size[2] == q->size[2] &&
+          out->size[1] <= INT32_MAX) ||
+         refuse(name, "[tokens, kv_heads, head_dim] of q's tokens, head_dim and dtype");
+}
+static bool read_lse(PyObject* x, const Ranked* q, Ranked* out) {
+  if (!read_ranked(x, "lse", 2, out)) return false;
+  return (out->ranks == q->ranks && out->dtype == F32 && out->dense && out->size[0] == q->size[0] &&
+          out->size[1] == q->size[1]) ||
+         refuse("lse", "contiguous float32 [tokens, q_heads] for each rank");
+}
+
+/* q, k, v, starts, out, lse or None, scale or None, place */
+static PyObject* prompt_attention(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+  ARGUMENTS(10);
+  Prompt p;
+  Ranked k, c, out, lse;
+  Place w;
+  if (!read_prompt(v[0], v[3], v[6], &p) || !read_keys(v[1], "k", &p.q, &k) || !read_keys(v[2], "v", &p.q, &c) ||
+      !read_like(v[4], "out", &p.q, &out) || (v[5] != Py_None && !read_lse(v[5], &p.q, &lse)))
+    return NULL;
+  if (!same_size(&k, &c)) {
+    refuse("k, v", "alike");
+    return NULL;
+  }
+  if (!read_place(v + 7, &w)) return NULL;
+  CALL(abi.prompt_attention((const void* const*)p.q.data, p.q.row, (const void* const*)k.data, k.row,
+                            (const void* const*)c.data, c.row, p.q.ranks, p.q.size[0], (int)p.q.size[1], (int)k.size[1],
+                            (int)p.q.size[2], (rar_dtype)p.q.dtype, p.starts, p.sequences, p.scale, out.data, out.row,
+                            v[5] != Py_None ? (float* const*)lse.data : NULL, w.data, w.bytes, w.stream));
+}
+
+/* q, k_cache, v_cache, block_table, starts, lens, out, lse or None, scale or None, place */
+static PyObject* prompt_attention_cached(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+  ARGUMENTS(12);
+  Prompt p;
+  Ranked k, c, out, lse;
+  Table table;
+  Place w;
+  void* lens;
+  if (!read_prompt(v[0], v[4], v[8], &p) || !read_caches(v[1], v[2], &k, &c) || !read_table(v[3], p.sequences, &table) ||
+      !read_flat(v[5], "lens", I32, p.sequences, &lens, NULL) || !read_like(v[6], "out", &p.q, &out) ||
+      (v[7] != Py_None && !read_lse(v[7], &p.q, &lse)))
+    return NULL;
+  if (k.ranks != p.q.ranks || k.dtype != p.q.dtype || k.size[3] != p.q.size[2]) {
+    refuse("k_cache, v_cache", "[num_pages, kv_heads, page_size, head_dim] of q's dtype and head_dim for each rank");
+    return NULL;
+  }
+  if (!read_place(v + 9, &w)) return NULL;
+  CALL(abi.prompt_attention_cached((const void* const*)p.q.data, p.q.row, (const void* const*)k.data,
+                                   (const void* const*)c.data, p.q.ranks, p.q.size[0], (int)p.q.size[1], (int)k.size[1],
+                                   (int)p.q.size[2], (rar_dtype)p.q.dtype, (int)k.size[0], (int)k.size[2], table.data,
+                                   table.stride, table.columns, p.starts, lens, p.sequences, p.scale, out.data, out.row,
+                                   v[7] != Py_None ? (float* const*)lse.data : NULL, w.data, w.bytes, w.stream));
+}
+
+/* q, k, v, starts, out, lse, dout, dq, dk, dv, scale or None, place */
+static PyObject* prompt_attention_backward(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+  ARGUMENTS(14);
+  Prompt p;
+  Ranked k, c, out, lse, dout, dq, dk, dv;
+  Place w;
+  if (!read_prompt(v[0], v[3], v[10], &p) || !read_keys(v[1], "k", &p.q, &k) || !read_keys(v[2], "v", &p.q, &c) ||
+      !read_like(v[4], "out", &p.q, &out) || !read_lse(v[5], &p.q, &lse) || !read_like(v[6], "dout", &p.q, &dout) ||
+      !read_like(v[7], "dq", &p.q, &dq) || !read_keys(v[8], "dk", &p.q, &dk) || !read_keys(v[9], "dv", &p.q, &dv))
+    return NULL;
+  if (!same_size(&k, &c) || !same_size(&k, &dk) || !same_size(&k, &dv)) {
+    refuse("k, v, dk, dv", "alike");
+    return NULL;
+  }
+  if (!read_place(v + 11, &w)) return NULL;
+  CALL(abi.prompt_attention_backward((const void* const*)p.q.data, p.q.row, (const void* const*)k.data, k.row,
+                                     (const void* const*)c.data, c.row, p.q.ranks, p.q.size[0], (int)p.q.size[1],
+                                     (int)k.size[1], (int)p.q.size[2], (rar_dtype)p.q.dtype, p.starts, p.sequences, p.scale,
+                                     (const void* const*)out.data, out.row, (const float* const*)lse.data,
+                                     (const void* const*)dout.data, dout.row, dq.data, dq.row, dk.data, dk.row, dv.data,
+                                     dv.row, w.data, w.bytes, w.stream));
+}
+
+/* [tokens, width] rows that the ranks share. */
+static bool read_shared_rows(PyObject* x, const char* name, int dtype, int64_t rows, int64_t width, void** data,
+                             int64_t* stride) {
+  Tensor t;
+  if (!read_tensor(x, name, &t)) return false;
+  if (t.dims != 2 || t.dtype != dtype || t.size[0] != rows || t.size[1] != width || (width > 1 && t.stride[1] != 1))
+    return refuse(name, "[tokens, hidden] with dense rows");
+  *data = t.data;
+  *stride = rows > 1 ? t.stride[0] : width;
+  return true;
+}
+static bool one_width(const Shards* x, const char* name, int64_t* hidden) {
+  *hidden = x->width[0];
+  for (int r = 1; r < x->ranks; r++)
+    if (x->width[r] != *hidden) return refuse(name, "of one width");
+  return fits_int(*hidden, name);
+}
+
+/* Table shards: as read_shards, but alike in width and not in rows. */
+static bool read_tables(PyObject* x, const char* name, Shards* out, int64_t* vocab, int64_t* hidden) {
+  if (PyList_Check(x) || PyTuple_Check(x)) {
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(x);
+    if (n < 1 || n > RAR_MAX_RANKS) return refuse(name, "1 to 32 ranks");
+    Ranked r;
+    for (Py_ssize_t i = 0; i < n; i++) {
+      Tensor t;
+      if (!read_item(x, i, name, &t)) return false;
+      if (t.dims != 2 || !lay_out(t.size, t.stride, 2, name, &r))
+        return PyErr_Occurred() ? false : refuse(name, "[vocabulary of the shard, hidden]");
+      if (i == 0) out->dtype = t.dtype;
+      if (t.dtype != out->dtype) return refuse(name, "of one dtype");
+      vocab[i] = t.size[0];
+      out->width[i] = t.size[1];
+      out->row[i] = r.row;
+      out->data[i] = t.data;
+    }
+    out->ranks = (int)n;
+  } else {
+    if (!read_shards(x, name, out)) return false;
+    for (int r = 0; r < out->ranks; r++) vocab[r] = out->rows;
+  }
+  return one_width(out, name, hidden);
+}
+
+/* tokens, tables, out, scale, place */
+static PyObject* embed_tokens(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+  ARGUMENTS(7);
+  Shards x;
+  Place w;
+  void *tokens, *out;
+  int64_t count, hidden, stride, vocab[RAR_MAX_RANKS];
+  if (!read_flat(v[0], "tokens", I32, -1, &tokens, &count) || !read_tables(v[1], "tables", &x, vocab, &hidden) ||
+      !floating(x.dtype, "tables") || !read_shared_rows(v[2], "out", x.dtype, count, hidden, &out, &stride))
+    return NULL;
+  const float scale = (float)PyFloat_AsDouble(v[3]);
+  if (PyErr_Occurred() || !read_place(v + 4, &w)) return NULL;
+  CALL(abi.embed_tokens(tokens, count, (const void* const*)x.data, vocab, x.row, x.ranks, (int)hidden, (rar_dtype)x.dtype,
+                        scale, out, stride, w.data, w.bytes, w.stream));
+}
+
+/* tokens, dout, dtables, scale, accumulate, place */
+static PyObject* embed_tokens_backward(PyObject* self, PyObject* const* v, Py_ssize_t n) {
+  ARGUMENTS(8);
+  Shards x;
+  Place w;
+  Tensor t;
+  void *tokens, *dout;
+  int64_t count, hidden, stride, vocab[RAR_MAX_RANKS];
+  if (!read_flat(v[0], "tokens", I32, -1, &tokens, &count) || !read_tables(v[2], "dtables", &x, vocab, &hidden) ||
+      !read_tensor(v[1], "dout", &t) || !floating(t.dtype, "dout") ||
+      !read_shared_rows(v[1], "dout", t.dtype, count, hidden, &dout, &stride))
+    return NULL;
+  if (x.dtype != F32) {
+    refuse("dtables", "float32 [vocabulary of the shard, hidden] for each rank");
+    return NULL;
+  }
+  const float scale = (float)PyFloat_AsDouble(v[3]);
+  const int accumulate = PyObject_IsTrue(v[4]);
+  if (PyErr_Occurred() || !read_place(v + 5, &w)) return NULL;
+  CALL(abi.embed_tokens_backward(tokens, count, dout, stride, (rar_dtype)t.dtype, scale, (float* const*)x.data, vocab, x.row,
+                                 x.ranks, (int)hidden, accumulate, w.data, w.bytes, w.stream));
+}
+
+/* setup(RarError, (float32, bfloat16, int32), addresses of the functions in the order of `abi`, function of the
    current device, function of a device's current stream handle) */
 static PyObject* setup(PyObject* self, PyObject* args) {
   PyObject *cls, *dtypes, *addresses, *device, *stream;
   if (!PyArg_ParseTuple(args, "OO!O!OO", &cls, &PyTuple_Type, &dtypes, &PyTuple_Type, &addresses, &device, &stream))
     return NULL;
   if (PyTuple_GET_SIZE(dtypes) != 3 || PyTuple_GET_SIZE(addresses) * sizeof(void*) != sizeof abi)
-    return PyErr_Format(PyExc_TypeError, "three dtypes and seven addresses are wanted");
+    return PyErr_Format(PyExc_TypeError, "three dtypes and an address for each function are wanted");
   void** to = (void**)&abi;
   for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(addresses); i++) to[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(addresses, i));
   if (PyErr_Occurred()) return NULL;
@@ -533,6 +727,8 @@ static PyObject* setup(PyObject* self, PyObject* args) {
 static PyMethodDef methods[] = {
     {"setup", setup, METH_VARARGS, NULL}, FAST(page_tables), FAST(qk_norm_rope), FAST(qk_norm_rope_cached),
     FAST(qk_norm_rope_backward), FAST(decode_attention), FAST(token_logprobs), FAST(token_logprobs_backward),
+    FAST(prompt_attention), FAST(prompt_attention_cached), FAST(prompt_attention_backward), FAST(embed_tokens),
+    FAST(embed_tokens_backward),
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operands", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

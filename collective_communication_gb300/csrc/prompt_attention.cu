@@ -1,0 +1,474 @@
+// prompt_attention.cu -- attention over whole prompts and its gradient on the
+// ordinary arithmetic units, for any type, head size and group.
+//
+//   s = scale q . k over the keys at or before the query's position, p = exp(s - lse),
+//   out = sum p v;   with delta = out . dout:   ds = p (dout . v - delta),
+//   dq = scale sum ds k,  dk = scale sum ds q,  dv = sum p dout
+//
+// A block of 256 threads holds BT rows (prompt_attention.cuh) as binary32 in shared
+// memory, and reads tiles of BT keys after one another, with the running maximum and
+// sum of the softmax in registers. The gradient is two kernels: one by rows, which
+// leaves delta behind and sums dq over the keys, one by keys, which sums dk and dv over
+// the rows of all query heads of the group. Both recompute p from lse; no sum
+// crosses blocks, so results are the same bits every time.
+//
+// Threads are 16 by 16; thread (ty, tx) has rows ty + 16 i and columns tx + 16 j of a
+// tile's scores, and elements 4 tx + 64 c of the rows' results: operands come as
+// 16-byte loads that half a warp shares or that fall on all banks. Products run two
+// at a time along the head (scores) or across it (results).
+#include "op_common.cuh"
+#include "prompt_attention.cuh"
+#include "rar_launch.h"
+
+namespace rar {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int DP, int BT>
+struct Shape {
+  static constexpr int MT = BT / 16;   // rows, and columns, of a thread
+  static constexpr int NC = DP / 64;   // groups of four elements of a result row
+  static constexpr int LD = DP + 4;    // floats from row to row: 16-byte loads of 16 rows fall on different banks
+  static constexpr int LP = BT + 4;
+  static constexpr int kRows = BT * LD, kScores = BT * LP;
+};
+
+// BT rows of D elements, widened, zeros past D and where at(row) is null.
+template <typename T, int DP, int BT, typename At>
+__device__ __forceinline__ void load_rows(float* to, int D, At at) {
+  constexpr int C = DP / 8;
+  for (int i = threadIdx.x; i < BT * C; i += kThreads) {
+    const int row = i / C, d = (i % C) * 8;
+    float v[8] = {};
+    const T* p = at(row);
+    if (p != nullptr && d < D) {
+      Pack8<T> x;
+      x.load(p + d);
+      x.widen(v);
+    }
+    float* o = to + row * Shape<DP, BT>::LD + d;
+    store4(o, v[0], v[1], v[2], v[3]);
+    store4(o + 4, v[4], v[5], v[6], v[7]);
+  }
+}
+
+// s[i][j] = x[ty + 16 i] . y[tx + 16 j]
+template <int DP, int BT>
+__device__ __forceinline__ void dots(const float* x, const float* y, float (&s)[BT / 16][BT / 16]) {
+  using S = Shape<DP, BT>;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  F2 acc[S::MT][S::MT];
+#pragma unroll
+  for (int i = 0; i < S::MT; i++)
+#pragma unroll
+    for (int j = 0; j < S::MT; j++) acc[i][j] = f2(0.f, 0.f);
+#pragma unroll 4
+  for (int d = 0; d < DP; d += 4) {
+    float4 a[S::MT], b[S::MT];
+#pragma unroll
+    for (int i = 0; i < S::MT; i++) {
+      a[i] = *reinterpret_cast<const float4*>(x + (ty + 16 * i) * S::LD + d);
+      b[i] = *reinterpret_cast<const float4*>(y + (tx + 16 * i) * S::LD + d);
+    }
+#pragma unroll
+    for (int i = 0; i < S::MT; i++)
+#pragma unroll
+      for (int j = 0; j < S::MT; j++) {
+        acc[i][j] = fma2(f2(a[i].x, a[i].y), f2(b[j].x, b[j].y), acc[i][j]);
+        acc[i][j] = fma2(f2(a[i].z, a[i].w), f2(b[j].z, b[j].w), acc[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < S::MT; i++)
+#pragma unroll
+    for (int j = 0; j < S::MT; j++) {
+      const float2 u = unpack(acc[i][j]);
+      s[i][j] = u.x + u.y;
+    }
+}
+
+template <int DP, int BT>
+struct Sums {  // elements 4 tx + 64 c of rows ty + 16 i
+  F2 v[BT / 16][DP / 64][2];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < BT / 16; i++)
+#pragma unroll
+      for (int c = 0; c < DP / 64; c++) v[i][c][0] = v[i][c][1] = f2(0.f, 0.f);
+  }
+  __device__ __forceinline__ void scale_row(int i, float by) {
+#pragma unroll
+    for (int c = 0; c < DP / 64; c++) {
+      v[i][c][0] = mul2(v[i][c][0], f2(by, by));
+      v[i][c][1] = mul2(v[i][c][1], f2(by, by));
+    }
+  }
+  // += sum over t of w[ty + 16 i][t] x[t]
+  __device__ __forceinline__ void add(const float* w, const float* x) {
+    using S = Shape<DP, BT>;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
+    for (int t = 0; t < BT; t += 4) {
+      float4 u[BT / 16];
+#pragma unroll
+      for (int i = 0; i < BT / 16; i++) u[i] = *reinterpret_cast<const float4*>(w + (ty + 16 * i) * S::LP + t);
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int c = 0; c < DP / 64; c++) {
+          const float4 y = *reinterpret_cast<const float4*>(x + (t + k) * S::LD + 4 * tx + 64 * c);
+#pragma unroll
+          for (int i = 0; i < BT / 16; i++) {
+            const float z = k == 0 ? u[i].x : k == 1 ? u[i].y : k == 2 ? u[i].z : u[i].w;
+            v[i][c][0] = fma2(f2(z, z), f2(y.x, y.y), v[i][c][0]);
+            v[i][c][1] = fma2(f2(z, z), f2(y.z, y.w), v[i][c][1]);
+          }
+        }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store_row(int i, T* row, int D, float by) const {
+    const int tx = threadIdx.x & 15;
+#pragma unroll
+    for (int c = 0; c < DP / 64; c++) {
+      if (4 * tx + 64 * c >= D) continue;
+      const float2 a = unpack(v[i][c][0]), b = unpack(v[i][c][1]);
+      store4(row + 4 * tx + 64 * c, a.x * by, a.y * by, b.x * by, b.y * by);
+    }
+  }
+};
+
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) x += __shfl_xor_sync(~0u, x, d);
+  return x;
+}
+
+// Cache rows of the keys j0 .. j0 + BT - 1 (-1: no key, or a page that is none).
+template <int BT>
+__device__ __forceinline__ void find_keys(const PromptArgs& a, const PromptSequence& seq, int head, int j0, int64_t* rows) {
+  for (int i = threadIdx.x; i < BT; i += kThreads) {
+    const int j = j0 + i;
+    int64_t row = -1;
+    if (j < seq.keys) {
+      const int page = a.table[seq.index * a.table_stride + (j >> a.page_shift)];
+      if ((unsigned)page < (unsigned)a.num_pages)
+        row = (((int64_t)page * a.kv_heads + head) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
+      else
+        op_report(a.ws, kErrCapacity);
+    }
+    rows[i] = row;
+  }
+}
+
+template <typename T, int DP, int BT>
+__global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant__ PromptArgs a) {
+  using S = Shape<DP, BT>;
+  extern __shared__ __align__(16) float shared[];
+  float *sq = shared, *sk = sq + S::kRows, *sv = sk + S::kRows, *sp = sv + S::kRows;
+  __shared__ int64_t key_row[BT];
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
+  const int group = a.q_heads / a.kv_heads, head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
+  PromptSequence seq;
+  int tile;
+  // the last tiles of a sequence see the most keys: they start first
+  if (!find_sequence(a.starts, a.sequences, a.tokens, group, BT, (int64_t)gridDim.x - 1 - blockIdx.x, &seq, &tile)) return;
+  const bool paged = a.table != nullptr;
+  if (paged) cached_sequence(a, &seq);
+  const int row0 = tile * BT;  // of the sequence: tokens * group stays below 2^31 (checked)
+  const int rows = min(BT, seq.length * group - row0);
+  const T* q = (const T*)a.q[rank];
+  auto token_of = [&](int r) { return seq.first + (row0 + r) / group; };
+  auto head_of = [&](int r) { return head * group + (row0 + r) % group; };
+  load_rows<T, DP, BT>(sq, D, [&](int r) {
+    return r < rows ? q + (int64_t)token_of(r) * a.q_stride + (int64_t)head_of(r) * D : nullptr;
+  });
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  int sees[S::MT];  // keys that the row sees
+  float m[S::MT], l[S::MT];
+  Sums<DP, BT> o;
+  o.zero();
+#pragma unroll
+  for (int i = 0; i < S::MT; i++) {
+    const int r = ty + 16 * i;
+    sees[i] = r < rows ? min(seq.before + (row0 + r) / group + 1, seq.keys) : 0;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+  const int most = min(seq.before + (row0 + rows - 1) / group + 1, seq.keys);
+  const float scale2 = a.scale * kLog2e;
+  for (int j0 = 0; j0 < most; j0 += BT) {
+    __syncthreads();
+    if (paged) {
+      find_keys<BT>(a, seq, head, j0, key_row);
+      __syncthreads();
+    }
+    auto key = [&](const void* base, int64_t stride, int r) -> const T* {
+      if (paged) return key_row[r] < 0 ? nullptr : (const T*)base + key_row[r] * D;
+      return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
+    };
+    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
+    load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
+    __syncthreads();
+    float s[S::MT][S::MT];
+    dots<DP, BT>(sq, sk, s);
+#pragma unroll
+    for (int i = 0; i < S::MT; i++) {
+      float top = m[i];
+#pragma unroll
+      for (int j = 0; j < S::MT; j++) {
+        const int c = tx + 16 * j;
+        s[i][j] = j0 + c < sees[i] && (!paged || key_row[c] >= 0) ? s[i][j] * scale2 : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      const float keep = top == -INFINITY ? 1.f : exp2_fast(m[i] - top);
+      const float by = top == -INFINITY ? 0.f : top;  // nothing seen so far: the weights are 0
+      m[i] = top;
+      l[i] *= keep;
+      o.scale_row(i, keep);
+#pragma unroll
+      for (int j = 0; j < S::MT; j++) {
+        const float p = exp2_fast(s[i][j] - by);
+        l[i] += p;
+        sp[(ty + 16 * i) * S::LP + tx + 16 * j] = p;
+      }
+    }
+    __syncwarp();  // a row's weights are written and read by the same half warp
+    o.add(sp, sv);
+  }
+#pragma unroll
+  for (int i = 0; i < S::MT; i++) {
+    const int r = ty + 16 * i;
+    const float sum = sum16(l[i]);
+    if (r >= rows) continue;
+    o.store_row(i, (T*)a.out[rank] + (int64_t)token_of(r) * a.out_stride + (int64_t)head_of(r) * D, D,
+                sum == 0.f ? 0.f : 1.f / sum);
+    if (a.lse[rank] != nullptr && tx == 0)
+      a.lse[rank][(int64_t)token_of(r) * a.q_heads + head_of(r)] = (m[i] + log2f(sum)) / kLog2e;
+  }
+}
+
+// Weight and score gradient of a score s that the row sees.
+__device__ __forceinline__ void weigh(float s, float dp, bool seen, float scale2, float lse2, float delta, float* p, float* ds) {
+  *p = seen ? exp2_fast(fmaf(s, scale2, -lse2)) : 0.f;
+  *ds = seen ? *p * (dp - delta) : 0.f;
+}
+
+// dq of BT rows, and delta of each for the other kernel.
+template <typename T, int DP, int BT>
+__global__ void __launch_bounds__(kThreads) prompt_bwd_rows_kernel(const __grid_constant__ PromptBwdArgs a) {
+  using S = Shape<DP, BT>;
+  extern __shared__ __align__(16) float shared[];
+  float *sq = shared, *sg = sq + S::kRows, *sk = sg + S::kRows, *sv = sk + S::kRows, *sp = sv + S::kRows;
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
+  const int group = a.q_heads / a.kv_heads, head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
+  PromptSequence seq;
+  int tile;
+  if (!find_sequence(a.starts, a.sequences, a.tokens, group, BT, (int64_t)gridDim.x - 1 - blockIdx.x, &seq, &tile)) return;
+  const int row0 = tile * BT, rows = min(BT, seq.length * group - row0);
+  auto token_of = [&](int r) { return (int64_t)(seq.first + (row0 + r) / group); };
+  auto head_of = [&](int r) { return (int64_t)(head * group + (row0 + r) % group); };
+  auto row_of = [&](const void* base, int64_t stride, int r) {
+    return r < rows ? (const T*)base + token_of(r) * stride + head_of(r) * D : nullptr;
+  };
+  load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
+  load_rows<T, DP, BT>(sk, D, [&](int r) { return row_of(a.out[rank], a.out_stride, r); });
+  load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
+  __syncthreads();
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  int sees[S::MT];
+  float lse2[S::MT], delta[S::MT];
+  Sums<DP, BT> dq;
+  dq.zero();
+#pragma unroll
+  for (int i = 0; i < S::MT; i++) {
+    const int r = ty + 16 * i;
+    float x = 0.f;
+    for (int d = tx; d < DP; d += 16) x = fmaf(sg[r * S::LD + d], sk[r * S::LD + d], x);
+    delta[i] = sum16(x);
+    sees[i] = r < rows ? (row0 + r) / group + 1 : 0;
+    lse2[i] = 0.f;
+    if (r < rows) {
+      const int64_t at = token_of(r) * a.q_heads + head_of(r);
+      lse2[i] = a.lse[rank][at] * kLog2e;
+      if (tx == 0)
+        reinterpret_cast<float*>(a.ws + kOpScratchOffset)[(int64_t)rank * a.tokens * a.q_heads + at] = delta[i];
+    }
+  }
+  const int most = (row0 + rows - 1) / group + 1;
+  const float scale2 = a.scale * kLog2e;
+  for (int j0 = 0; j0 < most; j0 += BT) {
+    __syncthreads();
+    auto key = [&](const void* base, int64_t stride, int r) {
+      return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
+    };
+    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
+    load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
+    __syncthreads();
+    float s[S::MT][S::MT], dp[S::MT][S::MT];
+    dots<DP, BT>(sq, sk, s);
+    dots<DP, BT>(sg, sv, dp);
+#pragma unroll
+    for (int i = 0; i < S::MT; i++)
+#pragma unroll
+      for (int j = 0; j < S::MT; j++) {
+        float p, ds;
+        weigh(s[i][j], dp[i][j], j0 + tx + 16 * j < sees[i], scale2, lse2[i], delta[i], &p, &ds);
+        sp[(ty + 16 * i) * S::LP + tx + 16 * j] = ds;
+      }
+    __syncwarp();
+    dq.add(sp, sk);
+  }
+#pragma unroll
+  for (int i = 0; i < S::MT; i++) {
+    const int r = ty + 16 * i;
+    if (r < rows) dq.store_row(i, (T*)a.dq[rank] + token_of(r) * a.dq_stride + head_of(r) * D, D, a.scale);
+  }
+}
+
+// dk and dv of BT keys, over the rows of all query heads of the group that see them.
+template <typename T, int DP, int BT>
+__global__ void __launch_bounds__(kThreads) prompt_bwd_keys_kernel(const __grid_constant__ PromptBwdArgs a) {
+  using S = Shape<DP, BT>;
+  extern __shared__ __align__(16) float shared[];
+  float *sk = shared, *sv = sk + S::kRows, *sq = sv + S::kRows, *sg = sq + S::kRows, *sp = sg + S::kRows,
+        *sd = sp + S::kScores;
+  __shared__ float slse[BT], sdelta[BT];
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  const int group = a.q_heads / a.kv_heads, head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
+  PromptSequence seq;
+  int tile;
+  // the first keys of a sequence are seen by the most rows: they start first
+  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, BT, blockIdx.x, &seq, &tile)) return;
+  const int j0 = tile * BT, keys = min(BT, seq.length - j0);
+  auto key = [&](const void* base, int64_t stride, int r) {
+    return r < keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
+  };
+  load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
+  load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  Sums<DP, BT> dk, dv;
+  dk.zero();
+  dv.zero();
+  const float scale2 = a.scale * kLog2e;
+  const float* deltas = reinterpret_cast<const float*>(a.ws + kOpScratchOffset) + (int64_t)rank * a.tokens * a.q_heads;
+  for (int row0 = j0 * group; row0 < seq.length * group; row0 += BT) {
+    const int rows = min(BT, seq.length * group - row0);
+    auto token_of = [&](int r) { return (int64_t)(seq.first + (row0 + r) / group); };
+    auto head_of = [&](int r) { return (int64_t)(head * group + (row0 + r) % group); };
+    auto row_of = [&](const void* base, int64_t stride, int r) {
+      return r < rows ? (const T*)base + token_of(r) * stride + head_of(r) * D : nullptr;
+    };
+    __syncthreads();
+    load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
+    load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
+    for (int r = threadIdx.x; r < BT; r += kThreads) {
+      const int64_t at = r < rows ? token_of(r) * a.q_heads + head_of(r) : 0;
+      slse[r] = r < rows ? a.lse[rank][at] * kLog2e : 0.f;
+      sdelta[r] = r < rows ? deltas[at] : 0.f;
+    }
+    __syncthreads();
+    float s[S::MT][S::MT], dp[S::MT][S::MT];  // rows of the tile are keys here, columns the queries
+    dots<DP, BT>(sk, sq, s);
+    dots<DP, BT>(sv, sg, dp);
+#pragma unroll
+    for (int i = 0; i < S::MT; i++)
+#pragma unroll
+      for (int j = 0; j < S::MT; j++) {
+        const int r = tx + 16 * j, c = ty + 16 * i;
+        const bool seen = r < rows && c < keys && j0 + c <= (row0 + r) / group;
+        float p, ds;
+        weigh(s[i][j], dp[i][j], seen, scale2, slse[r], sdelta[r], &p, &ds);
+        sp[c * S::LP + r] = p;
+        sd[c * S::LP + r] = ds;
+      }
+    __syncwarp();
+    dv.add(sp, sg);
+    dk.add(sd, sq);
+  }
+#pragma unroll
+  for (int i = 0; i < S::MT; i++) {
+    const int r = ty + 16 * i;
+    if (r >= keys) continue;
+    const int64_t token = seq.first + j0 + r, at = (int64_t)head * D;
+    dk.store_row(i, (T*)a.dk[rank] + token * a.dk_stride + at, D, a.scale);
+    dv.store_row(i, (T*)a.dv[rank] + token * a.dv_stride + at, D, 1.f);
+  }
+}
+
+template <int DP, int BT>
+constexpr int shared_bytes(int rows, int scores) {
+  return (rows * Shape<DP, BT>::kRows + scores * Shape<DP, BT>::kScores) * 4;
+}
+
+template <typename Args>
+cudaError_t launch(const void* fn, const Args& a, int64_t slots, int shared, cudaStream_t stream) {
+  int blocks = 0;
+  const cudaError_t e = resident_blocks(fn, kThreads, shared, &blocks);  // lets the kernel have its shared memory
+  if (e != cudaSuccess) return e;
+  Args copy = a;
+  void* params[] = {&copy};
+  return launch_op(fn, dim3((unsigned)slots, (unsigned)a.kv_heads, (unsigned)a.nranks), kThreads, shared, stream, params);
+}
+
+template <typename T, int DP, int BT>
+cudaError_t forward(const PromptArgs& a, cudaStream_t stream) {
+  return launch((const void*)prompt_kernel<T, DP, BT>, a, prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT),
+                shared_bytes<DP, BT>(3, 1), stream);
+}
+
+template <typename T, int DP, int BT>
+cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
+  const cudaError_t e =
+      launch((const void*)prompt_bwd_rows_kernel<T, DP, BT>, a,
+             prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT), shared_bytes<DP, BT>(4, 1), stream);
+  if (e != cudaSuccess) return e;
+  return launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>, a, prompt_slots(a.tokens, a.sequences, 1, BT),
+                shared_bytes<DP, BT>(4, 2), stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream) {
+  if (a.dtype == 0) {
+    if (a.head_dim <= 64) return forward<float, 64, 64>(a, stream);
+    if (a.head_dim <= 128) return forward<float, 128, 64>(a, stream);
+    return forward<float, 256, 32>(a, stream);
+  }
+  if (a.head_dim <= 64) return forward<uint16_t, 64, 64>(a, stream);
+  if (a.head_dim <= 128) return forward<uint16_t, 128, 64>(a, stream);
+  return forward<uint16_t, 256, 32>(a, stream);
+}
+
+cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t stream) {
+  if (a.dtype == 0) {
+    if (a.head_dim <= 64) return backward<float, 64, 64>(a, stream);
+    if (a.head_dim <= 128) return backward<float, 128, 64>(a, stream);
+    return backward<float, 256, 32>(a, stream);
+  }
+  if (a.head_dim <= 64) return backward<uint16_t, 64, 64>(a, stream);
+  if (a.head_dim <= 128) return backward<uint16_t, 128, 64>(a, stream);
+  return backward<uint16_t, 256, 32>(a, stream);
+}
+
+int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
+  return align_up((int64_t)nranks * tokens * q_heads * 4, 256);
+}
+
+}  // namespace rar

@@ -1,0 +1,107 @@
+// prompt_attention.cuh -- what the forms of the attention over whole prompts share:
+// arguments, and the way from a block's number to its rows.
+//
+// The query heads that share a key head are rows of one tile: row r of a sequence is
+// head r % group of its token r / group. Sequences are packed along the tokens, and
+// only the device knows where they start. A tile holds `unit` of something that a
+// sequence has `per` of a token (rows, or tokens); sequence s takes the numbers from
+// slot(s) = floor(starts[s] per / unit) + s on. That leaves it at least
+// ceil(length per / unit) numbers, since floor(x + y) >= floor(x) + ceil(y) - 1, so a
+// grid of slot(last) + 1 blocks, whose size the host knows, covers any starts, and a
+// block finds its sequence by bisection with no sums over the lengths.
+#pragma once
+
+#include "op_common.cuh"
+
+namespace rar {
+
+struct PromptArgs {
+  const void* q[kMaxRanks];
+  const void* k[kMaxRanks];  // [tokens, kv_heads, head_dim], or the paged cache if table is set
+  const void* v[kMaxRanks];
+  void* out[kMaxRanks];
+  float* lse[kMaxRanks];  // null: not wanted
+  const int32_t* starts;
+  const int32_t* lens;   // of the cached form
+  const int32_t* table;  // null: dense keys
+  char* ws;
+  int64_t q_stride, k_stride, v_stride, out_stride, table_stride;
+  float scale;
+  int nranks, dtype, tokens, sequences, q_heads, kv_heads, head_dim, page_shift, num_pages, max_blocks;
+};
+
+struct PromptBwdArgs {
+  const void* q[kMaxRanks];
+  const void* k[kMaxRanks];
+  const void* v[kMaxRanks];
+  const void* out[kMaxRanks];
+  const void* dout[kMaxRanks];
+  const float* lse[kMaxRanks];
+  void* dq[kMaxRanks];
+  void* dk[kMaxRanks];
+  void* dv[kMaxRanks];
+  const int32_t* starts;
+  char* ws;  // scratch: delta, float [ranks, tokens, q_heads]
+  int64_t q_stride, k_stride, v_stride, out_stride, dout_stride, dq_stride, dk_stride, dv_stride;
+  float scale;
+  int nranks, dtype, tokens, sequences, q_heads, kv_heads, head_dim;
+};
+
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream);
+cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t stream);
+int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim);
+
+// Numbers that cover any starts of `tokens` tokens in `sequences` sequences.
+inline int64_t prompt_slots(int64_t tokens, int sequences, int per, int unit) {
+  return tokens * per / unit + sequences;
+}
+
+// A sequence as its starts and lengths say, with what does not fit left out.
+struct PromptSequence {
+  int index, first, length;  // its number, first token and tokens in the step
+  int before;                // position of its first token; negative where lens is below the step's tokens
+  int keys;                  // tokens with a key
+};
+
+// Every pair of starts, by the threads of one block; true if they are in order.
+__device__ __forceinline__ void check_starts(const int32_t* starts, int sequences, int tokens, char* ws) {
+  bool bad = false;
+  for (int s = threadIdx.x; s < sequences; s += blockDim.x) {
+    const int a = starts[s], b = starts[s + 1];
+    bad |= a < 0 || b < a || b > tokens;
+  }
+  if (bad) op_report(ws, kErrCapacity);
+}
+
+// The sequence that number `slot` belongs to, and which of its tiles it is; false for none.
+__device__ __forceinline__ bool find_sequence(const int32_t* starts, int sequences, int tokens, int per, int unit,
+                                              int64_t slot, PromptSequence* seq, int* tile) {
+  int lo = 0, hi = sequences;  // the last s with slot(s) <= slot
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    const int a = starts[mid];
+    if (a <= tokens && (int64_t)(a > 0 ? a : 0) * per / unit + mid <= slot) lo = mid;
+    else hi = mid;
+  }
+  const int a = starts[lo], b = starts[lo + 1];
+  if (a < 0 || b < a || b > tokens) return false;
+  const int64_t t = slot - ((int64_t)a * per / unit + lo);
+  if (t < 0 || t * unit >= (int64_t)(b - a) * per) return false;
+  seq->index = lo;
+  seq->first = a;
+  seq->length = seq->keys = b - a;
+  seq->before = 0;
+  *tile = (int)t;
+  return true;
+}
+
+// The cached form: positions and keys from the request's length, of which the step's tokens are the last.
+__device__ __forceinline__ void cached_sequence(const PromptArgs& a, PromptSequence* seq) {
+  const int len = a.lens[seq->index];
+  const int room = a.max_blocks << a.page_shift;
+  if (threadIdx.x == 0 && (len < 0 || len > room)) op_report(a.ws, kErrCapacity);
+  seq->before = (len < 0 ? 0 : len) - seq->length;
+  seq->keys = len < 0 ? 0 : len < room ? len : room;
+}
+
+}  // namespace rar

@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "op_common.cuh"
+#include "prompt_attention.cuh"
 #include "rar.h"
 #include "rar_launch.h"
 
@@ -51,7 +52,7 @@ bool meet(const Span& a, const Span& b) {
 
 // Inputs and outputs of a call: an output may meet nothing else.
 struct Spans {
-  Span in[5 * kMaxRanks + 16];
+  Span in[6 * kMaxRanks + 16];
   Span out[3 * kMaxRanks + 16];
   int nin = 0, nout = 0;
   void read(const Span& s) { in[nin++] = s; }
@@ -271,6 +272,76 @@ rar_status norm_rope_forward(const NormRopeCall& c, const void* const* qkv, int 
   a.interleaved = interleaved != 0;
   a.page_shift = shift;
   return from_cuda(launch_norm_rope(a, (cudaStream_t)stream));
+}
+
+// Sizes that the forms of the attention over prompts share.
+bool prompt_sizes_ok(int64_t tokens, int q_heads, int kv_heads, int head_dim) {
+  return heads_ok(q_heads, kv_heads, head_dim) && q_heads % kv_heads == 0 && tokens >= 0 &&
+         tokens <= INT32_MAX / q_heads;
+}
+rar_status check_prompt(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim, rar_dtype dtype,
+                        const int32_t* starts, int sequences, Spans* s) {
+  const rar_status st = check_ranks(nranks, dtype);
+  if (st != RAR_OK) return st;
+  if (!prompt_sizes_ok(tokens, q_heads, kv_heads, head_dim) || sequences < 0 || sequences > INT32_MAX / 2) return RAR_ERR_ARG;
+  if (starts == nullptr && sequences > 0) return RAR_ERR_ARG;
+  if (!aligned(starts, 4)) return RAR_ERR_ALIGN;
+  s->read(span(starts, sequences > 0 ? ((int64_t)sequences + 1) * 4 : 0));
+  return RAR_OK;
+}
+// Rows [tokens, heads, head_dim] of each rank.
+rar_status check_rows(const void* const* p, int nranks, int64_t tokens, int64_t width, int64_t stride, int64_t es, bool out,
+                      Spans* s) {
+  rar_status st = check_pointers(p, nranks, tokens, 16);
+  if (st != RAR_OK || (st = check_stride(stride, width, tokens, es)) != RAR_OK) return st;
+  for (int r = 0; r < nranks; r++) {
+    const Span x = span(p[r], tokens, width * es, stride * es);
+    if (out) s->write(x);
+    else s->read(x);
+  }
+  return RAR_OK;
+}
+
+rar_status prompt_forward(PromptArgs& a, void* const* out, float* const* lse, size_t ws_bytes, Spans& s, void* stream) {
+  const int64_t es = a.dtype == RAR_F32 ? 4 : 2, width = (int64_t)a.q_heads * a.head_dim;
+  rar_status st = check_rows((const void* const*)out, a.nranks, a.tokens, width, a.out_stride, es, true, &s);
+  if (st != RAR_OK) return st;
+  if (lse != nullptr) {
+    if ((st = check_pointers((const void* const*)lse, a.nranks, a.tokens, 4)) != RAR_OK) return st;
+    for (int r = 0; r < a.nranks; r++) s.write(span(lse[r], (int64_t)a.tokens * a.q_heads * 4));
+  }
+  s.write(span(a.ws, (int64_t)ws_bytes));
+  if (s.clash()) return RAR_ERR_ARG;
+  if ((st = check_workspace(a.ws, ws_bytes,
+                            prompt_attention_scratch_bytes(a.nranks, a.tokens, a.q_heads, a.kv_heads, a.head_dim))) != RAR_OK)
+    return st;
+  if (a.tokens == 0 || a.sequences == 0) return RAR_OK;
+  for (int r = 0; r < a.nranks; r++) {
+    a.out[r] = out[r];
+    a.lse[r] = lse != nullptr ? lse[r] : nullptr;
+  }
+  return RAR_OK;
+}
+
+// Vocabulary shards of rows: the first word of each, and their spans.
+rar_status check_tables(const void* const* tables, const int64_t* vocab, const int64_t* strides, int nranks, int hidden,
+                        int64_t es, bool out, int64_t* first, Spans* s) {
+  if (vocab == nullptr || strides == nullptr || hidden < 8 || hidden > 1 << 20 || hidden % 8 != 0) return RAR_ERR_ARG;
+  rar_status st = check_pointers(tables, nranks, 1, 16);
+  if (st != RAR_OK) return st;
+  first[0] = 0;
+  for (int r = 0; r < nranks; r++) {
+    if (vocab[r] < 1 || vocab[r] > INT32_MAX) return RAR_ERR_ARG;
+    if ((st = check_stride(strides[r], hidden, vocab[r], es)) != RAR_OK) return st;
+    first[r + 1] = first[r] + vocab[r];
+    const Span x = span(tables[r], vocab[r], hidden * es, strides[r] * es);
+    if (out) s->write(x);
+    else s->read(x);
+  }
+  return first[nranks] <= INT32_MAX ? RAR_OK : RAR_ERR_ARG;
+}
+bool embed_sizes_ok(int64_t tokens, int hidden) {
+  return hidden >= 8 && hidden <= 1 << 20 && hidden % 8 == 0 && tokens >= 0 && tokens <= INT32_MAX / div_up(hidden, 256);
 }
 
 }  // namespace
@@ -636,6 +707,247 @@ rar_status rar_token_logprobs_backward(const void* const* logits, const int64_t*
   a.nranks = nranks;
   a.dtype = (int)dtype;
   return from_cuda(launch_token_logprobs_bwd(a, (cudaStream_t)stream));
+}
+
+size_t rar_prompt_attention_workspace_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
+  if (nranks < 1 || nranks > kMaxRanks || !prompt_sizes_ok(tokens, q_heads, kv_heads, head_dim)) return 0;
+  return (size_t)(kOpScratchOffset + prompt_attention_scratch_bytes(nranks, tokens, q_heads, kv_heads, head_dim));
+}
+
+rar_status rar_prompt_attention(const void* const* q, int64_t q_stride, const void* const* k, int64_t k_stride,
+                                const void* const* v, int64_t v_stride, int nranks, int64_t tokens, int q_heads,
+                                int kv_heads, int head_dim, rar_dtype dtype, const int32_t* starts, int num_sequences,
+                                float scale, void* const* out, int64_t out_stride, float* const* lse, void* workspace,
+                                size_t workspaceBytes, void* stream) {
+  Spans s;
+  rar_status st = check_prompt(nranks, tokens, q_heads, kv_heads, head_dim, dtype, starts, num_sequences, &s);
+  if (st != RAR_OK) return st;
+  const int64_t es = size_of(dtype), D = head_dim;
+  if ((st = check_rows(q, nranks, tokens, q_heads * D, q_stride, es, false, &s)) != RAR_OK ||
+      (st = check_rows(k, nranks, tokens, kv_heads * D, k_stride, es, false, &s)) != RAR_OK ||
+      (st = check_rows(v, nranks, tokens, kv_heads * D, v_stride, es, false, &s)) != RAR_OK)
+    return st;
+  PromptArgs a;
+  std::memset(&a, 0, sizeof a);
+  for (int r = 0; r < nranks; r++) {
+    a.q[r] = q[r];
+    a.k[r] = k[r];
+    a.v[r] = v[r];
+  }
+  a.starts = starts;
+  a.ws = (char*)workspace;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.out_stride = out_stride;
+  a.scale = scale;
+  a.nranks = nranks;
+  a.dtype = (int)dtype;
+  a.tokens = (int)tokens;
+  a.sequences = num_sequences;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  if ((st = prompt_forward(a, out, lse, workspaceBytes, s, stream)) != RAR_OK || tokens == 0 || num_sequences == 0) return st;
+  return from_cuda(launch_prompt_attention(a, (cudaStream_t)stream));
+}
+
+rar_status rar_prompt_attention_cached(const void* const* q, int64_t q_stride, const void* const* k_cache,
+                                       const void* const* v_cache, int nranks, int64_t tokens, int q_heads, int kv_heads,
+                                       int head_dim, rar_dtype dtype, int num_pages, int page_size,
+                                       const int32_t* block_table, int64_t table_stride, int max_blocks,
+                                       const int32_t* starts, const int32_t* lens, int num_sequences, float scale,
+                                       void* const* out, int64_t out_stride, float* const* lse, void* workspace,
+                                       size_t workspaceBytes, void* stream) {
+  Spans s;
+  rar_status st = check_prompt(nranks, tokens, q_heads, kv_heads, head_dim, dtype, starts, num_sequences, &s);
+  if (st != RAR_OK) return st;
+  const int shift = page_shift_of(page_size);
+  const int64_t es = size_of(dtype), D = head_dim, n = num_sequences;
+  if (shift < 0 || !pages_ok(num_pages, shift, kv_heads) || max_blocks < 1 || (int64_t)max_blocks << shift > INT32_MAX)
+    return RAR_ERR_ARG;
+  if ((n > 1 && table_stride < max_blocks) || table_stride < 0 || table_stride > INT64_MAX / 8 / (n > 0 ? n : 1))
+    return RAR_ERR_ARG;
+  if ((st = check_rows(q, nranks, tokens, q_heads * D, q_stride, es, false, &s)) != RAR_OK ||
+      (st = check_pointers(k_cache, nranks, tokens, 16)) != RAR_OK ||
+      (st = check_pointers(v_cache, nranks, tokens, 16)) != RAR_OK)
+    return st;
+  if (n > 0 && (block_table == nullptr || lens == nullptr)) return RAR_ERR_ARG;
+  if (!aligned(block_table, 4) || !aligned(lens, 4)) return RAR_ERR_ALIGN;
+  s.read(span(block_table, n, (int64_t)max_blocks * 4, table_stride * 4));
+  s.read(span(lens, n * 4));
+  PromptArgs a;
+  std::memset(&a, 0, sizeof a);
+  for (int r = 0; r < nranks; r++) {
+    const int64_t cache = ((int64_t)num_pages << shift) * kv_heads * D * es;
+    s.read(span(k_cache[r], cache));
+    s.read(span(v_cache[r], cache));
+    a.q[r] = q[r];
+    a.k[r] = k_cache[r];
+    a.v[r] = v_cache[r];
+  }
+  a.starts = starts;
+  a.lens = lens;
+  a.table = block_table;
+  a.ws = (char*)workspace;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.table_stride = table_stride;
+  a.scale = scale;
+  a.nranks = nranks;
+  a.dtype = (int)dtype;
+  a.tokens = (int)tokens;
+  a.sequences = num_sequences;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  a.page_shift = shift;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  if ((st = prompt_forward(a, out, lse, workspaceBytes, s, stream)) != RAR_OK || tokens == 0 || n == 0) return st;
+  return from_cuda(launch_prompt_attention(a, (cudaStream_t)stream));
+}
+
+rar_status rar_prompt_attention_backward(const void* const* q, int64_t q_stride, const void* const* k, int64_t k_stride,
+                                         const void* const* v, int64_t v_stride, int nranks, int64_t tokens, int q_heads,
+                                         int kv_heads, int head_dim, rar_dtype dtype, const int32_t* starts,
+                                         int num_sequences, float scale, const void* const* out, int64_t out_stride,
+                                         const float* const* lse, const void* const* dout, int64_t dout_stride,
+                                         void* const* dq, int64_t dq_stride, void* const* dk, int64_t dk_stride,
+                                         void* const* dv, int64_t dv_stride, void* workspace, size_t workspaceBytes,
+                                         void* stream) {
+  Spans s;
+  rar_status st = check_prompt(nranks, tokens, q_heads, kv_heads, head_dim, dtype, starts, num_sequences, &s);
+  if (st != RAR_OK) return st;
+  const int64_t es = size_of(dtype), D = head_dim, qw = q_heads * D, kw = kv_heads * D;
+  if ((st = check_rows(q, nranks, tokens, qw, q_stride, es, false, &s)) != RAR_OK ||
+      (st = check_rows(k, nranks, tokens, kw, k_stride, es, false, &s)) != RAR_OK ||
+      (st = check_rows(v, nranks, tokens, kw, v_stride, es, false, &s)) != RAR_OK ||
+      (st = check_rows(out, nranks, tokens, qw, out_stride, es, false, &s)) != RAR_OK ||
+      (st = check_rows(dout, nranks, tokens, qw, dout_stride, es, false, &s)) != RAR_OK ||
+      (st = check_rows((const void* const*)dq, nranks, tokens, qw, dq_stride, es, true, &s)) != RAR_OK ||
+      (st = check_rows((const void* const*)dk, nranks, tokens, kw, dk_stride, es, true, &s)) != RAR_OK ||
+      (st = check_rows((const void* const*)dv, nranks, tokens, kw, dv_stride, es, true, &s)) != RAR_OK ||
+      (st = check_pointers((const void* const*)lse, nranks, tokens, 4)) != RAR_OK)
+    return st;
+  PromptBwdArgs a;
+  std::memset(&a, 0, sizeof a);
+  for (int r = 0; r < nranks; r++) {
+    s.read(span(lse[r], tokens * q_heads * 4));
+    a.q[r] = q[r];
+    a.k[r] = k[r];
+    a.v[r] = v[r];
+    a.out[r] = out[r];
+    a.dout[r] = dout[r];
+    a.lse[r] = lse[r];
+    a.dq[r] = dq[r];
+    a.dk[r] = dk[r];
+    a.dv[r] = dv[r];
+  }
+  s.write(span(workspace, (int64_t)workspaceBytes));
+  if (s.clash()) return RAR_ERR_ARG;
+  if ((st = check_workspace(workspace, workspaceBytes,
+                            prompt_attention_scratch_bytes(nranks, tokens, q_heads, kv_heads, head_dim))) != RAR_OK)
+    return st;
+  if (tokens == 0 || num_sequences == 0) return RAR_OK;
+  a.starts = starts;
+  a.ws = (char*)workspace;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.out_stride = out_stride;
+  a.dout_stride = dout_stride;
+  a.dq_stride = dq_stride;
+  a.dk_stride = dk_stride;
+  a.dv_stride = dv_stride;
+  a.scale = scale;
+  a.nranks = nranks;
+  a.dtype = (int)dtype;
+  a.tokens = (int)tokens;
+  a.sequences = num_sequences;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.head_dim = head_dim;
+  return from_cuda(launch_prompt_attention_bwd(a, (cudaStream_t)stream));
+}
+
+rar_status rar_embed_tokens(const int32_t* tokens, int64_t num_tokens, const void* const* tables, const int64_t* vocab,
+                            const int64_t* row_strides, int nranks, int hidden, rar_dtype dtype, float scale, void* out,
+                            int64_t out_stride, void* workspace, size_t workspaceBytes, void* stream) {
+  rar_status st = check_ranks(nranks, dtype);
+  if (st != RAR_OK) return st;
+  const int64_t es = size_of(dtype);
+  if (!embed_sizes_ok(num_tokens, hidden)) return RAR_ERR_ARG;
+  Spans s;
+  EmbedArgs a;
+  std::memset(&a, 0, sizeof a);
+  if ((st = check_tables(tables, vocab, row_strides, nranks, hidden, es, false, a.first, &s)) != RAR_OK) return st;
+  if (num_tokens > 0 && (tokens == nullptr || out == nullptr)) return RAR_ERR_ARG;
+  if (!aligned(tokens, 4) || !aligned(out, 16)) return RAR_ERR_ALIGN;
+  if ((st = check_stride(out_stride, hidden, num_tokens, es)) != RAR_OK) return st;
+  s.read(span(tokens, num_tokens * 4));
+  s.write(span(out, num_tokens, hidden * es, out_stride * es));
+  s.write(span(workspace, (int64_t)workspaceBytes));
+  if (s.clash()) return RAR_ERR_ARG;
+  if ((st = check_workspace(workspace, workspaceBytes, 0)) != RAR_OK) return st;
+  if (num_tokens == 0) return RAR_OK;
+  for (int r = 0; r < nranks; r++) {
+    a.tables[r] = tables[r];
+    a.row_stride[r] = row_strides[r];
+  }
+  a.tokens_in = tokens;
+  a.out = out;
+  a.ws = (char*)workspace;
+  a.tokens = num_tokens;
+  a.out_stride = out_stride;
+  a.scale = scale;
+  a.nranks = nranks;
+  a.dtype = (int)dtype;
+  a.hidden = hidden;
+  return from_cuda(launch_embed_tokens(a, (cudaStream_t)stream));
+}
+
+size_t rar_embed_tokens_workspace_bytes(int64_t num_tokens, int hidden) {
+  if (!embed_sizes_ok(num_tokens, hidden)) return 0;
+  return (size_t)(kOpScratchOffset + embed_tokens_scratch_bytes(num_tokens, hidden));
+}
+
+rar_status rar_embed_tokens_backward(const int32_t* tokens, int64_t num_tokens, const void* dout, int64_t dout_stride,
+                                     rar_dtype dtype, float scale, float* const* dtables, const int64_t* vocab,
+                                     const int64_t* drow_strides, int nranks, int hidden, int accumulate, void* workspace,
+                                     size_t workspaceBytes, void* stream) {
+  rar_status st = check_ranks(nranks, dtype);
+  if (st != RAR_OK) return st;
+  const int64_t es = size_of(dtype);
+  if (!embed_sizes_ok(num_tokens, hidden)) return RAR_ERR_ARG;
+  Spans s;
+  EmbedBwdArgs a;
+  std::memset(&a, 0, sizeof a);
+  if ((st = check_tables((const void* const*)dtables, vocab, drow_strides, nranks, hidden, 4, true, a.first, &s)) != RAR_OK)
+    return st;
+  if (num_tokens > 0 && (tokens == nullptr || dout == nullptr)) return RAR_ERR_ARG;
+  if (!aligned(tokens, 4) || !aligned(dout, 16)) return RAR_ERR_ALIGN;
+  if ((st = check_stride(dout_stride, hidden, num_tokens, es)) != RAR_OK) return st;
+  s.read(span(tokens, num_tokens * 4));
+  s.read(span(dout, num_tokens, hidden * es, dout_stride * es));
+  s.write(span(workspace, (int64_t)workspaceBytes));
+  if (s.clash()) return RAR_ERR_ARG;
+  if ((st = check_workspace(workspace, workspaceBytes, embed_tokens_scratch_bytes(num_tokens, hidden))) != RAR_OK) return st;
+  for (int r = 0; r < nranks; r++) {
+    a.dtables[r] = dtables[r];
+    a.drow_stride[r] = drow_strides[r];
+  }
+  a.tokens_in = tokens;
+  a.dout = dout;
+  a.ws = (char*)workspace;
+  a.tokens = num_tokens;
+  a.dout_stride = dout_stride;
+  a.scale = scale;
+  a.nranks = nranks;
+  a.dtype = (int)dtype;
+  a.hidden = hidden;
+  a.accumulate = accumulate != 0;
+  return from_cuda(launch_embed_tokens_bwd(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

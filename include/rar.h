@@ -426,8 +426,9 @@ RAR_API rar_status rar_describe_geometry(int nranks, size_t count, rar_dtype dty
  * operator used with it says; an operator without one needs the minimum). It
  * serves any of these operators, at any sizes it has room for, in any order on
  * one stream; nothing carries over from call to call. Partial results are left
- * per block, so the attention's bytes depend on the heads and their size alone,
- * the log probabilities' on nothing: more requests or rows need no more.
+ * per block, so the decode attention's bytes depend on the heads and their size alone,
+ * the log probabilities' on nothing: more requests or rows need no more. The prompt
+ * attention's and the embedding gradient's grow with the tokens.
  *
  * Streams: calls are ordered as any kernel is. They are launched with
  * programmatic stream serialization: an operator's blocks may come up while the
@@ -579,6 +580,82 @@ RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const 
                                                const float* grad_logprob, const float* grad_entropy,
                                                void* const* dlogits, const int64_t* drow_strides, void* workspace,
                                                size_t workspaceBytes, void* stream);
+
+/*
+ * Causal attention over whole prompts, packed along the tokens. Sequence s of
+ * num_sequences holds the tokens starts[s] to starts[s + 1] - 1 (int32, num_sequences
+ * + 1 entries, in order, none above tokens; a sequence may be empty). Query head h of a
+ * token attends to key head h / (q_heads / kv_heads) of the tokens of its sequence up
+ * to and including itself (q_heads a multiple of kv_heads):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = log sum_j exp(scale * q . k_j)
+ * q[r], out[r] are [tokens, q_heads, head_dim]; tokens * q_heads < 2^31. lse: host array
+ * of nranks pointers to float [tokens, q_heads], or NULL. Rows of tokens in no sequence
+ * (ahead of the first, behind the last) are left as they were. Starts that are out of
+ * order or range report RAR_ERR_CAPACITY, and the rows concerned are left or written
+ * with no meaning.
+ *
+ * rar_prompt_attention: k[r], v[r] are [tokens, kv_heads, head_dim].
+ * rar_prompt_attention_cached: the keys and values are in the paged cache, as
+ *   rar_qk_norm_rope_cached writes them: lens[s] tokens of sequence s, of which the
+ *   starts[s + 1] - starts[s] tokens of the call are the last (rar_page_tables gives
+ *   starts and lens_out), so its i-th sees those up to position
+ *   lens[s] - (starts[s + 1] - starts[s]) + i. A row whose position is negative sees
+ *   nothing: out 0, lse -inf. What is past a length or in a page that is none is not
+ *   read, and reports as in rar_decode_attention.
+ * rar_prompt_attention_backward: dq, dk and dv from the gradient dout of out, with
+ *   out and lse of the forward call. dk and dv are sums over the query heads of a group.
+ *   No gradient goes through lse. The same bits every time.
+ * A key or value of a sequence that is infinite or NaN makes the rows that see it
+ * infinite or NaN, and may make those of its earlier tokens NaN; other sequences' rows
+ * do not depend on it.
+ */
+RAR_API size_t rar_prompt_attention_workspace_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads,
+                                                    int head_dim); /* for all three; 0: bad arguments */
+RAR_API rar_status rar_prompt_attention(const void* const* q, int64_t q_stride, const void* const* k, int64_t k_stride,
+                                        const void* const* v, int64_t v_stride, int nranks, int64_t tokens, int q_heads,
+                                        int kv_heads, int head_dim, rar_dtype dtype, const int32_t* starts,
+                                        int num_sequences, float scale, void* const* out, int64_t out_stride,
+                                        float* const* lse, void* workspace, size_t workspaceBytes, void* stream);
+RAR_API rar_status rar_prompt_attention_cached(const void* const* q, int64_t q_stride, const void* const* k_cache,
+                                               const void* const* v_cache, int nranks, int64_t tokens, int q_heads,
+                                               int kv_heads, int head_dim, rar_dtype dtype, int num_pages, int page_size,
+                                               const int32_t* block_table, int64_t table_stride, int max_blocks,
+                                               const int32_t* starts, const int32_t* lens, int num_sequences, float scale,
+                                               void* const* out, int64_t out_stride, float* const* lse, void* workspace,
+                                               size_t workspaceBytes, void* stream);
+RAR_API rar_status rar_prompt_attention_backward(const void* const* q, int64_t q_stride, const void* const* k,
+                                                 int64_t k_stride, const void* const* v, int64_t v_stride, int nranks,
+                                                 int64_t tokens, int q_heads, int kv_heads, int head_dim, rar_dtype dtype,
+                                                 const int32_t* starts, int num_sequences, float scale,
+                                                 const void* const* out, int64_t out_stride, const float* const* lse,
+                                                 const void* const* dout, int64_t dout_stride, void* const* dq,
+                                                 int64_t dq_stride, void* const* dk, int64_t dk_stride, void* const* dv,
+                                                 int64_t dv_stride, void* workspace, size_t workspaceBytes, void* stream);
+
+/*
+ * Embedding lookup over vocabulary shards that are never gathered: rank r holds the
+ * rows of vocab[r] words, tables[r] [vocab[r], hidden], rows row_strides[r] apart (host
+ * arrays); row j of rank r is word vocab[0] + .. + vocab[r-1] + j.
+ *   out_t = scale * table[tokens[t]]
+ * tokens: int32 [num_tokens]; one outside the vocabulary (-1, say) gives a row of 0.
+ * out: [num_tokens, hidden], shared by the ranks. hidden is a multiple of 8 up to 2^20;
+ * num_tokens * ceil(hidden / 256) < 2^31.
+ *
+ * rar_embed_tokens_backward: the tables' gradient, scale times the sum of dout over
+ *   the tokens of a word, in the tokens' order: the same bits every time. dtables[r] is
+ *   float [vocab[r], hidden] whatever dtype, that of dout, is. accumulate 0: every row
+ *   is written, with 0 where no token asks for it; else the sums are added to what
+ *   dtables holds, and rows that no token asks for are not touched.
+ */
+RAR_API rar_status rar_embed_tokens(const int32_t* tokens, int64_t num_tokens, const void* const* tables,
+                                    const int64_t* vocab, const int64_t* row_strides, int nranks, int hidden,
+                                    rar_dtype dtype, float scale, void* out, int64_t out_stride, void* workspace,
+                                    size_t workspaceBytes, void* stream);
+RAR_API size_t rar_embed_tokens_workspace_bytes(int64_t num_tokens, int hidden); /* of the backward call; 0: bad arguments */
+RAR_API rar_status rar_embed_tokens_backward(const int32_t* tokens, int64_t num_tokens, const void* dout,
+                                             int64_t dout_stride, rar_dtype dtype, float scale, float* const* dtables,
+                                             const int64_t* vocab, const int64_t* drow_strides, int nranks, int hidden,
+                                             int accumulate, void* workspace, size_t workspaceBytes, void* stream);
 
 #ifdef __cplusplus
 }
