@@ -443,6 +443,16 @@ cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
                 shared_bytes<DP, BT>(4, 2), stream);
 }
 
+// Whether the tensor core form takes the call: a group of heads fills no more than the
+// 128 rows of a tile, sums of 128 elements a row fit tensor memory beside the scores,
+// and strides are what a TMA map can say.
+template <typename Args>
+bool tensor_cores(const Args& a, int64_t k_stride, int64_t v_stride) {
+  const int64_t most = (int64_t)1 << 38;
+  return a.dtype != 0 && a.head_dim <= 128 && a.q_heads / a.kv_heads <= 128 && a.q_stride < most && k_stride < most &&
+         v_stride < most;
+}
+
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream) {
@@ -451,6 +461,7 @@ cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream) {
     if (a.head_dim <= 128) return forward<float, 128, 64>(a, stream);
     return forward<float, 256, 32>(a, stream);
   }
+  if (tensor_cores(a, a.k_stride, a.v_stride)) return launch_prompt_attention_tc(a, stream);
   if (a.head_dim <= 64) return forward<uint16_t, 64, 64>(a, stream);
   if (a.head_dim <= 128) return forward<uint16_t, 128, 64>(a, stream);
   return forward<uint16_t, 256, 32>(a, stream);
@@ -468,7 +479,14 @@ cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t str
 }
 
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
-  return align_up((int64_t)nranks * tokens * q_heads * 4, 256);
+  const int64_t delta = align_up((int64_t)nranks * tokens * q_heads * 4, 256);
+  // the parts of few tiles' keys, where they may be split: 2 x 128 rows of O, m and l a block
+  const int group = q_heads / kv_heads;
+  int64_t parts = 0;
+  if (group <= 128 && head_dim <= 128 &&
+      (tokens / (2 * (128 / group)) + 1) * kv_heads * nranks * 2 <= kPromptSplitBlocks)
+    parts = (int64_t)kPromptSplitBlocks * 256 * ((head_dim <= 64 ? 64 : 128) + 2) * 4;
+  return delta > parts ? delta : parts;
 }
 
 }  // namespace rar

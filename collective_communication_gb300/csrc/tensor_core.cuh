@@ -1,0 +1,197 @@
+// tensor_core.cuh -- fifth-generation tensor cores, tensor memory, TMA copies and
+// mbarriers for the operators that are products of tiles: PTX wrappers and the waits'
+// limits. One block per SM (its shared memory sees to that) uses all of its
+// tensor memory.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "op_common.cuh"
+
+namespace rar {
+namespace tc {
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
+// ---- mbarriers ----
+__device__ __forceinline__ void barrier_init(uint64_t* b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_address(b)), "r"(count) : "memory");
+}
+// Barriers that one thread has initialised, for the copies and products that will arrive on them.
+__device__ __forceinline__ void barriers_ready() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+__device__ __forceinline__ void arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_address(b)) : "memory");
+}
+__device__ __forceinline__ void arrive_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_address(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint64_t* b, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(shared_address(b)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+constexpr uint64_t kWaitNs = 2000000000ull;  // no tile takes a thousandth of that
+
+// Waits for the phase of `parity` to end. False once any wait of the block has run
+// past the limit: every role then leaves its loops.
+__device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile int* dead) {
+  const uint64_t until = global_timer_ns() + kWaitNs;
+  while (!try_wait(b, parity)) {
+    if (*dead) return false;
+    if (global_timer_ns() > until) {
+      *dead = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int* dead) {
+#pragma unroll 1
+  for (int i = 0; i < 16; i++)
+    if (try_wait(b, parity)) return true;
+  return wait_long(b, parity, dead);
+}
+
+// ---- TMA ----
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+__device__ __forceinline__ void copy_3d(void* to, const CUtensorMap* m, int x, int y, int z, uint64_t* b) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          shared_address(to)),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(shared_address(b))
+      : "memory");
+}
+// Ordinary stores to shared memory, for products that read it afterwards.
+__device__ __forceinline__ void stores_to_products() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---- tensor memory ----
+__device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t columns) {  // one warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_address(where)), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {  // the same warp
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void loads_done() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define RAR_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define RAR_V8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+// 32 columns of the lane's row of the warp's quarter; valid after loads_done().
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : RAR_R8(r, 0), RAR_R8(r, 8), RAR_R8(r, 16), RAR_R8(r, 24)
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : RAR_R8(r, 0), RAR_R8(r, 8)
+               : "r"(at));
+}
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      RAR_V8(r, 0), RAR_V8(r, 8), RAR_V8(r, 16), RAR_V8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+               RAR_V8(r, 0), RAR_V8(r, 8)
+               : "memory");
+}
+
+// ---- registers of a warpgroup ----
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- products ----
+// Operands in shared memory are slabs of 64 elements (128 bytes) a row, rows side by
+// side, swizzled by 128 bytes as TMA writes them: groups of eight rows are 1024 bytes.
+// along: the contraction runs along the rows' elements (next 16: 32 bytes on, next 64:
+// the next slab). across: it runs across the rows (next 16: 2048 bytes on), and `next`
+// bytes lie between slabs of 64 results.
+constexpr uint64_t kSlabBits = 1ull << 46 | 2ull << 61;
+__device__ __forceinline__ uint64_t operand_along(uint32_t at) {
+  return (uint64_t)((at >> 4) & 0x3fff) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | kSlabBits;
+}
+__device__ __forceinline__ uint64_t operand_across(uint32_t at, uint32_t next) {
+  return (uint64_t)((at >> 4) & 0x3fff) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | kSlabBits;
+}
+// bf16 operands, binary32 sums, 128 rows by n columns (a multiple of 16).
+__device__ __forceinline__ uint32_t product_of(int n, bool right_across) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (right_across ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+// d (+)= a b over 16 elements; one thread. a in shared memory, or in tensor memory
+// (two elements a column).
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void multiply_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      : "memory");
+}
+// Arrives on b once the thread's products so far are done.
+__device__ __forceinline__ void commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(shared_address(b))
+               : "memory");
+}
+
+// d (+)= x y^T: 128 rows of x by n rows of y, `steps` times 16 elements along both; slab bytes from slab to slab.
+__device__ __forceinline__ void rows_by_rows(uint32_t d, uint32_t x, uint32_t y, uint32_t slab_x, uint32_t slab_y, int n,
+                                             int steps, bool add) {
+  const uint32_t kind = product_of(n, false);
+  for (int k = 0; k < steps; k++)
+    multiply(d, operand_along(x + (k >> 2) * slab_x + (k & 3) * 32), operand_along(y + (k >> 2) * slab_y + (k & 3) * 32), kind,
+             add || k > 0);
+}
+// d (+)= w z: w in tensor memory, 128 rows by 16 `steps`; z has as many rows, n elements each.
+__device__ __forceinline__ void weights_by_rows(uint32_t d, uint32_t w, uint32_t z, uint32_t slab, int n, int steps, bool add) {
+  const uint32_t kind = product_of(n, true);
+  for (int k = 0; k < steps; k++) multiply_tmem(d, w + 8 * k, operand_across(z + k * 2048, slab), kind, add || k > 0);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace tc
+
+// A tensor of three dimensions of 2-byte elements, the innermost dense, for copies of
+// boxes of 64 elements by `rows` by `planes`, swizzled by 128 bytes; zeros outside.
+cudaError_t make_map(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t stride1_bytes,
+                     int64_t stride2_bytes, int rows, int planes);
+
+}  // namespace rar

@@ -543,8 +543,8 @@ def test_two_streams():
 
 
 def test_nothing_to_do():
-    ws = B.OpWorkspace(1 << 20)
     q, k, v, starts = prompt_inputs(1, [], 4, 2, 64, "bf16", behind=10)
+    ws = workspace(q, 2)
     out = torch.full_like(q, MARK)
     B.prompt_attention(q, k, v, starts, out, None, ws)          # no sequences
     B.prompt_attention(q[:, :0], k[:, :0], v[:, :0], starts, out[:, :0], None, ws)  # no tokens
