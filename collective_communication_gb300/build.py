@@ -21,7 +21,8 @@ BUILD_DEBUG = os.path.join(HERE, "_build", "debug")
 LIB_DEBUG = os.path.join(HERE, "librar_debug.so")
 SOURCES = ["rar_api.cu", "ring_simple.cu", "ring_ll.cu", "oneshot.cu", "oneshot_staged.cu", "rar_static_ws.cu",
            "rar_ops_api.cu", "page_tables.cu", "qk_norm_rope.cu", "decode_attention.cu", "token_logprobs.cu",
-           "prompt_attention.cu", "prompt_attention_tc.cu", "tensor_map.cu", "embed_tokens.cu"]
+           "prompt_attention.cu", "prompt_attention_tc.cu", "prompt_attention_bwd_tc.cu",
+           "tensor_map.cu", "embed_tokens.cu"]
 HEADERS = ["rar_device.cuh", "rar_geometry.h", "rar_launch.h", "op_common.cuh", "prompt_attention.cuh",
            "tensor_core.cuh"]
 

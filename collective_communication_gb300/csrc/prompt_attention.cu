@@ -473,6 +473,8 @@ cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t str
     if (a.head_dim <= 128) return backward<float, 128, 64>(a, stream);
     return backward<float, 256, 32>(a, stream);
   }
+  if (tensor_cores(a, a.k_stride, a.v_stride) && a.dout_stride < (int64_t)1 << 38)
+    return launch_prompt_attention_bwd_tc(a, stream);
   if (a.head_dim <= 64) return backward<uint16_t, 64, 64>(a, stream);
   if (a.head_dim <= 128) return backward<uint16_t, 128, 64>(a, stream);
   return backward<uint16_t, 256, 32>(a, stream);

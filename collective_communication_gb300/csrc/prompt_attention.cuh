@@ -48,8 +48,9 @@ struct PromptBwdArgs {
 };
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream);
-// The form of bf16 with head sizes up to 128 and groups up to 128 (prompt_attention_tc.cu).
+// The forms of bf16 with head sizes up to 128 and groups up to 128 (prompt_attention_tc.cu, prompt_attention_bwd_tc.cu).
 cudaError_t launch_prompt_attention_tc(const PromptArgs& a, cudaStream_t stream);
+cudaError_t launch_prompt_attention_bwd_tc(const PromptBwdArgs& a, cudaStream_t stream);
 constexpr int kPromptSplitBlocks = 152;  // blocks among which few tiles' keys are split: the SMs
 cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t stream);
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim);
