@@ -51,14 +51,6 @@ struct Layout {
   static constexpr int kKeysShared = (2 + 2 * kRowStages) * kBytes + 1024;
 };
 
-// d += w z, w in tensor memory as the two warpgroups leave it: 64 columns of elements from column 0 on, 64 from 64 on.
-__device__ __forceinline__ void halves_by_rows(uint32_t d, uint32_t w, uint32_t z, uint32_t slab, int n, bool add) {
-  const uint32_t kind = product_of(n, true);
-#pragma unroll
-  for (int k = 0; k < kTile / 16; k++)
-    multiply_tmem(d, w + 8 * k + (k >> 2) * 32, operand_across(z + k * 2048, slab), kind, add || k > 0);
-}
-
 // Rows from `first` on of a tile in shared memory become 0, before products run over them; one warp.
 template <int DP>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int first) {
@@ -118,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   __shared__ int dead_flag;
   __shared__ float half_delta[kTile];
   volatile int* const dead = &dead_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     dead_flag = 0;
     barrier_init(&q_full, 1);
@@ -148,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   const int tiles = (token0 + tokens + kTile - 1) / kTile;
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
-  const uint32_t tmem = tmem_at;
-  const uint32_t s_at = tmem, dp_at = tmem + 256, dq_at = tmem + 384;  // S: two buffers of 128 columns
+  constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
+  constexpr uint32_t s_at = tmem, dp_at = tmem + 256, dq_at = tmem + 384;  // S: two buffers of 128 columns
   uint8_t *const q_tile = smem, *const g_tile = smem + L::kBytes, *const k_ring = smem + 2 * L::kBytes,
           *const v_ring = k_ring + KS * L::kBytes;
   const int steps = (D + 15) / 16;
@@ -175,42 +167,37 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   } else if (warp == kProductWarp) {
     const uint32_t q_at = shared_address(q_tile), g_at = shared_address(g_tile), k_at = shared_address(k_ring),
                    v_at = shared_address(v_ring);
-    bool fine = wait(&q_full, 0, dead);
+    const uint32_t lead = elect_one();
+    const int count = uniform(tiles), keys_of = uniform(seq.length);
     auto score = [&](int j) {  // S of key tile j; keys that are none are 0, for the product with dS
-      if (!wait(&k_full[j % KS], j / KS & 1, dead)) return false;
-      if (seq.length - j * kTile < kTile) {
-        clear_rows<DP>(k_ring + j % KS * L::kBytes, seq.length - j * kTile);
+      if (!wait_warp(&k_full[j % KS], j / KS & 1, dead)) return false;
+      if (keys_of - j * kTile < kTile) {
+        clear_rows<DP>(k_ring + j % KS * L::kBytes, keys_of - j * kTile);
         stores_to_products();
         __syncwarp();
       }
       fence_after();
-      if (lane == 0)
-        rows_by_rows(s_at + (j & 1) * 128, q_at, k_at + j % KS * L::kBytes, L::kSlab, L::kSlab, kTile, steps, false);
+      rows_by_rows<DP / 16, L::kSlab>(lead, s_at + (j & 1) * 128, q_at, k_at + j % KS * L::kBytes, kTile, steps);
       return true;
     };
     auto value = [&](int j) {  // dO V^T
-      if (!wait(&v_full[j % VS], j / VS & 1, dead)) return false;
+      if (!wait_warp(&v_full[j % VS], j / VS & 1, dead)) return false;
       fence_after();
-      if (lane == 0) {
-        rows_by_rows(dp_at, g_at, v_at + j % VS * L::kBytes, L::kSlab, L::kSlab, kTile, steps, false);
-        commit(&dp_full);
-        commit(&v_empty[j % VS]);
-      }
+      rows_by_rows<DP / 16, L::kSlab>(lead, dp_at, g_at, v_at + j % VS * L::kBytes, kTile, steps);
+      commit(lead, &dp_full);
+      commit(lead, &v_empty[j % VS]);
       return true;
     };
-    fine = fine && score(0) && value(0);
-    for (int j = 0; j < tiles && fine; j++) {
-      const bool more = j + 1 < tiles;
+    bool fine = wait_warp(&q_full, 0, dead) && score(0) && value(0);
+    for (int j = 0; j < count && fine; j++) {
+      const bool more = j + 1 < count;
       if (more && !(fine = score(j + 1))) break;
-      if (!(fine = wait(&ds_ready, j & 1, dead))) break;
+      if (!(fine = wait_warp(&ds_ready, j & 1, dead))) break;
       fence_after();
       if (more && !(fine = value(j + 1))) break;
-      if (lane == 0) {
-        halves_by_rows(dq_at, s_at + (j & 1) * 128, k_at + j % KS * L::kBytes, L::kSlab, steps * 16, j > 0);
-        commit(&k_empty[j % KS]);
-        if (!more) commit(&dq_full);
-      }
-      __syncwarp();
+      weights_by_rows<L::kSlab, 32>(lead, dq_at, s_at + (j & 1) * 128, k_at + j % KS * L::kBytes, steps * 16, j > 0);
+      commit(lead, &k_empty[j % KS]);
+      if (!more) commit(lead, &dq_full);
     }
   } else if (warp < kCopyWarp) {
     const int half = warp >> 2;
@@ -301,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   __shared__ __align__(16) float numbers[NS][2][kTile];  // -lse log2(e) and -delta of a tile's rows
   __shared__ uint8_t token_of[kTile];
   volatile int* const dead = &dead_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int group = a.q_heads / a.kv_heads;
   if (threadIdx.x == 0) {
     dead_flag = 0;
@@ -330,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   const int begin = key0 / per_tile, end = (seq.length + per_tile - 1) / per_tile;  // tiles of rows
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
-  const uint32_t tmem = tmem_at;
-  const uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 384;
+  constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
+  constexpr uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 384;
   uint8_t *const k_tile = smem, *const v_tile = smem + L::kBytes, *const ring = smem + 2 * L::kBytes;  // a stage: Q, dO
   const int steps = (D + 15) / 16;
 
@@ -381,11 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
     }
   } else if (warp == kProductWarp) {
     const uint32_t k_at = shared_address(k_tile), v_at = shared_address(v_tile), ring_at = shared_address(ring);
-    bool fine = wait(&kv_full, 0, dead);
+    const uint32_t lead = elect_one();
+    const int from = uniform(begin), to = uniform(end), tokens_of = uniform(seq.length);
     auto score = [&](int i) {  // S^T of a tile of rows; rows that are none are 0, for the products with P and dS
-      const int n = i - begin, stage = n % NS;
-      if (!wait(&full[stage], n / NS & 1, dead)) return false;
-      const int rows = min(per_tile, seq.length - i * per_tile) * group;
+      const int n = i - from, stage = n % NS;
+      if (!wait_warp(&full[stage], n / NS & 1, dead)) return false;
+      const int rows = min(per_tile, tokens_of - i * per_tile) * group;
       if (rows < kTile) {
         clear_rows<DP>(ring + stage * 2 * L::kBytes, rows);
         clear_rows<DP>(ring + (stage * 2 + 1) * L::kBytes, rows);
@@ -393,36 +381,29 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         __syncwarp();
       }
       fence_after();
-      if (lane == 0) {
-        rows_by_rows(s_at, k_at, ring_at + stage * 2 * L::kBytes, L::kSlab, L::kSlab, kTile, steps, false);
-        commit(&s_full);
-      }
+      rows_by_rows<DP / 16, L::kSlab>(lead, s_at, k_at, ring_at + stage * 2 * L::kBytes, kTile, steps);
+      commit(lead, &s_full);
       return true;
     };
     auto value = [&](int i) {  // V dO^T
-      if (lane == 0) {
-        rows_by_rows(dp_at, v_at, ring_at + ((i - begin) % NS * 2 + 1) * L::kBytes, L::kSlab, L::kSlab, kTile, steps, false);
-        commit(&dp_full);
-      }
+      rows_by_rows<DP / 16, L::kSlab>(lead, dp_at, v_at, ring_at + ((i - from) % NS * 2 + 1) * L::kBytes, kTile, steps);
+      commit(lead, &dp_full);
     };
-    if (fine && (fine = score(begin))) value(begin);
-    for (int i = begin; i < end && fine; i++) {
-      const int n = i - begin, stage = n % NS;
-      const bool more = i + 1 < end;
-      if (!(fine = wait(&p_ready, n & 1, dead))) break;
+    bool fine = wait_warp(&kv_full, 0, dead) && score(from);
+    if (fine) value(from);
+    for (int i = from; i < to && fine; i++) {
+      const int n = i - from, stage = n % NS;
+      const bool more = i + 1 < to;
+      if (!(fine = wait_warp(&p_ready, n & 1, dead))) break;
       fence_after();
-      if (lane == 0)
-        halves_by_rows(dv_at, s_at, ring_at + (stage * 2 + 1) * L::kBytes, L::kSlab, steps * 16, n > 0);
+      weights_by_rows<L::kSlab, 32>(lead, dv_at, s_at, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, n > 0);
       if (more && !(fine = score(i + 1))) break;
-      if (!(fine = wait(&ds_ready, n & 1, dead))) break;
+      if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
       fence_after();
-      if (lane == 0) {
-        halves_by_rows(dk_at, dp_at, ring_at + stage * 2 * L::kBytes, L::kSlab, steps * 16, n > 0);
-        commit(&empty[stage]);
-        if (!more) commit(&done);
-      }
+      weights_by_rows<L::kSlab, 32>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, n > 0);
+      commit(lead, &empty[stage]);
+      if (!more) commit(lead, &done);
       if (more) value(i + 1);
-      __syncwarp();
     }
   } else if (warp < kCopyWarp) {
     const int half = warp >> 2;

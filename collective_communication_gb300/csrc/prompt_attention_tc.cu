@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
   __shared__ uint32_t tmem_at, lost[4][4];
   __shared__ int dead_flag, last_flag;
   volatile int* const dead = &dead_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     dead_flag = 0;
     barrier_init(&q_full, 1);
@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
   const int begin = (int)((int64_t)tiles * part / split.parts), end = (int)((int64_t)tiles * (part + 1) / split.parts);
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
-  const uint32_t tmem = tmem_at;
-  const uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 384};
+  constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
+  constexpr uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 384};
   uint8_t* const ring = smem + 2 * L::kTile;
   const int steps = (D + 15) / 16;
   const int last[2] = {min(tiles_of[0], end), min(tiles_of[1], end)};  // a tile of rows walks from begin to here
@@ -197,75 +197,70 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       }
     }
   } else if (warp == kProductWarp) {
-    if (begin < end) {
-      int stage = 0;
-      uint32_t phase = 0;
+    const int from = uniform(begin), to = uniform(end), upto[2] = {uniform(last[0]), uniform(last[1])}, keys_of = uniform(seq.keys);
+    if (from < to) {
+      const uint32_t lead = elect_one();
       const int n_out = steps * 16;
       const uint32_t q_at = shared_address(smem), ring_at = shared_address(ring);
-      bool fine = wait(&q_full, 0, dead);
-      // the S of key tile j for each tile of rows that sees it; K is in `stage`
+      // the S of a key tile for a tile of rows that sees it
       auto score = [&](int t, uint32_t k_at) {
-        rows_by_rows(s_at[t], q_at + t * L::kTile, k_at, L::kSlab, L::kSlab, kKeys, steps, false);
-        commit(&s_full[t]);
+        rows_by_rows<DP / 16, L::kSlab>(lead, s_at[t], q_at + t * L::kTile, k_at, kKeys, steps);
+        commit(lead, &s_full[t]);
       };
-      fine = fine && wait(&full[0], 0, dead);
-      if (fine) {
-        fence_after();
-        if (lane == 0) {
-          for (int t = 0; t < 2; t++)
-            if (last[t] > begin) score(t, ring_at);
-          commit(&empty[0]);
-        }
-        stage = 1;
-      }
-      for (int j = begin; j < end && fine; j++) {
-        const int v_stage = stage;
-        const uint32_t v_phase = phase;
-        if (++stage == NS) {
-          stage = 0;
-          phase ^= 1;
-        }
-        const int k_stage = stage;
-        const uint32_t k_phase = phase;
-        const bool more = j + 1 < end;
-        if (!(fine = wait(&full[v_stage], v_phase, dead))) break;
-        // rows of V with no key would be multiplied by weights of 0, and may hold a NaN
-        const int keys = seq.keys - j * kKeys;
-        const bool holes = PAGED && (lost[j & 3][0] | lost[j & 3][1] | lost[j & 3][2] | lost[j & 3][3]) != 0;
+      // V of key tile j is there; rows with no key would be multiplied by weights of 0, and may hold a NaN
+      auto values = [&](int j, int stage, uint32_t phase) {
+        if (!wait_warp(&full[stage], phase, dead)) return false;
+        const int keys = keys_of - j * kKeys;
+        const bool holes = PAGED && __any_sync(~0u, lane < 4 && lost[j & 3][lane & 3] != 0);
         if (keys < kKeys || holes) {
           for (int r = lane; r < kKeys; r += 32)
             if (r >= keys || (holes && (lost[j & 3][r >> 5] >> (r & 31) & 1)))
               for (int h = 0; h < DP / 64; h++)
                 for (int c = 0; c < 8; c++)
-                  *reinterpret_cast<uint4*>(ring + v_stage * L::kTile + h * L::kSlab + r * 128 + c * 16) =
-                      make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(ring + stage * L::kTile + h * L::kSlab + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
           stores_to_products();
           __syncwarp();
         }
+        return true;
+      };
+      // stages: K of the first tile, then V of a tile and K of the next in turn
+      bool fine = wait_warp(&q_full, 0, dead) && wait_warp(&full[0], 0, dead);
+      if (fine) {
+        fence_after();
+        for (int t = 0; t < 2; t++)
+          if (upto[t] > from) score(t, ring_at);
+        commit(lead, &empty[0]);
+        fine = values(from, 1, 0);
+      }
+      int v_stage = 1;
+      uint32_t v_phase = 0;
+      for (int j = from; j < to && fine; j++) {
+        const bool more = j + 1 < to;
+        const int k_stage = v_stage + 1 == NS ? 0 : v_stage + 1;
+        const uint32_t k_phase = v_phase ^ (k_stage == 0);
+        const int next_stage = k_stage + 1 == NS ? 0 : k_stage + 1;
+        const uint32_t next_phase = k_phase ^ (next_stage == 0);
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-          if (j >= last[t]) continue;
-          if (!(fine = wait(&p_full[t], (j - begin) & 1, dead))) break;
-          fence_after();
-          if (lane == 0) {
-            weights_by_rows(o_at[t], s_at[t], ring_at + v_stage * L::kTile, L::kSlab, n_out, kKeys / 16, j > begin);
-            if (j + 1 >= last[t]) commit(&o_full[t]);
-          }
-          if (j + 1 < last[t]) {
-            if (!(fine = wait(&full[k_stage], k_phase, dead))) break;
+          if (j < upto[t]) {
+            if (!(fine = wait_warp(&p_full[t], (j - from) & 1, dead))) break;
             fence_after();
-            if (lane == 0) score(t, ring_at + k_stage * L::kTile);
+            weights_by_rows<L::kSlab, 0>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > from);
+            if (j + 1 >= upto[t]) commit(lead, &o_full[t]);
           }
-          __syncwarp();
+          // what the warp waits for beside the weights, it waits for while products run
+          if (more && t == 0 && !(fine = wait_warp(&full[k_stage], k_phase, dead))) break;
+          if (more && t == 1 && !(fine = values(j + 1, next_stage, next_phase))) break;
+          if (j + 1 < upto[t]) {
+            fence_after();
+            score(t, ring_at + k_stage * L::kTile);
+          }
         }
-        if (fine && lane == 0) {
-          commit(&empty[v_stage]);
-          if (more) commit(&empty[k_stage]);
-        }
-        if (more && ++stage == NS) {
-          stage = 0;
-          phase ^= 1;
-        }
+        if (!fine) break;
+        commit(lead, &empty[v_stage]);
+        if (more) commit(lead, &empty[k_stage]);
+        v_stage = next_stage;
+        v_phase = next_phase;
       }
     }
   } else if (warp < kCopyWarp) {

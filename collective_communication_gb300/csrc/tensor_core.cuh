@@ -64,6 +64,21 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int*
   return wait_long(b, parity, dead);
 }
 
+// The same for a whole warp, that goes on together: what follows is uniform to the compiler.
+__device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* dead) {
+  if (__all_sync(~0u, try_wait(b, parity))) return true;
+  const uint64_t until = global_timer_ns() + kWaitNs;
+#pragma unroll 1
+  while (true) {
+    if (__all_sync(~0u, try_wait(b, parity))) return true;
+    const bool late = global_timer_ns() > until;
+    if (late) *dead = 1;
+    if (__any_sync(~0u, late || *dead)) return false;
+  }
+}
+// A number that all lanes of a warp have, as one that the compiler knows they have.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(~0u, x); }
+
 // ---- TMA ----
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
@@ -136,49 +151,63 @@ __device__ __forceinline__ void take_registers() {
 // along: the contraction runs along the rows' elements (next 16: 32 bytes on, next 64:
 // the next slab). across: it runs across the rows (next 16: 2048 bytes on), and `next`
 // bytes lie between slabs of 64 results.
-constexpr uint64_t kSlabBits = 1ull << 46 | 2ull << 61;
-__device__ __forceinline__ uint64_t operand_along(uint32_t at) {
-  return (uint64_t)((at >> 4) & 0x3fff) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | kSlabBits;
-}
-__device__ __forceinline__ uint64_t operand_across(uint32_t at, uint32_t next) {
-  return (uint64_t)((at >> 4) & 0x3fff) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | kSlabBits;
-}
+// The upper half of a descriptor is the same for both; the lower one holds the address
+// and the bytes between slabs in units of 16, so a step is an addition to it.
+constexpr uint32_t kOperandHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t operand_along(uint32_t at) { return at >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t operand_across(uint32_t at, uint32_t next) { return at >> 4 | (next >> 4) << 16; }
 // bf16 operands, binary32 sums, 128 rows by n columns (a multiple of 16).
 __device__ __forceinline__ uint32_t product_of(int n, bool right_across) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (right_across ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
 }
-// d (+)= a b over 16 elements; one thread. a in shared memory, or in tensor memory
-// (two elements a column).
-__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+// d (+)= a b over 16 elements, issued by the lane that leads; the whole warp comes here
+// together. a in shared memory, or in tensor memory (two elements a column).
+__device__ __forceinline__ void multiply(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kind), "r"((uint32_t)add), "r"(kOperandHigh), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void multiply_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void multiply_tmem(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kind), "r"((uint32_t)add), "r"(kOperandHigh), "r"(lead)
       : "memory");
 }
-// Arrives on b once the thread's products so far are done.
-__device__ __forceinline__ void commit(uint64_t* b) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(shared_address(b))
-               : "memory");
+// Arrives on b once the leading lane's products so far are done.
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* b) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(shared_address(b)),
+      "r"(lead)
+      : "memory");
 }
 
-// d (+)= x y^T: 128 rows of x by n rows of y, `steps` times 16 elements along both; slab bytes from slab to slab.
-__device__ __forceinline__ void rows_by_rows(uint32_t d, uint32_t x, uint32_t y, uint32_t slab_x, uint32_t slab_y, int n,
-                                             int steps, bool add) {
-  const uint32_t kind = product_of(n, false);
-  for (int k = 0; k < steps; k++)
-    multiply(d, operand_along(x + (k >> 2) * slab_x + (k & 3) * 32), operand_along(y + (k >> 2) * slab_y + (k & 3) * 32), kind,
-             add || k > 0);
+// One lane issues all products of a tile, so the instructions around each count: in a
+// branch of that lane alone, with descriptors worked out anew, a product took 108 cycles
+// to issue and 64 to run. Hence additions to the lower halves only, loops unrolled to
+// MOST, and a warp that stays together, whose numbers the compiler keeps in uniform
+// registers, where the products want them.
+// d = x y^T: 128 rows of x by n rows of y, `steps` times 16 elements along both; SLAB bytes from slab to slab.
+template <int MOST, int SLAB>
+__device__ __forceinline__ void rows_by_rows(uint32_t lead, uint32_t d, uint32_t x, uint32_t y, int n, int steps) {
+  const uint32_t kind = product_of(n, false), a = operand_along(x), b = operand_along(y);
+#pragma unroll
+  for (int k = 0; k < MOST; k++) {
+    const uint32_t on = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
+    if (k < steps) multiply(lead, d, a + on, b + on, kind, k > 0);
+  }
 }
-// d (+)= w z: w in tensor memory, 128 rows by 16 `steps`; z has as many rows, n elements each.
-__device__ __forceinline__ void weights_by_rows(uint32_t d, uint32_t w, uint32_t z, uint32_t slab, int n, int steps, bool add) {
-  const uint32_t kind = product_of(n, true);
-  for (int k = 0; k < steps; k++) multiply_tmem(d, w + 8 * k, operand_across(z + k * 2048, slab), kind, add || k > 0);
+// d (+)= w z: w in tensor memory, 128 rows by 128, the second half GAP columns behind the first; z has as many rows, n elements each.
+template <int SLAB, int GAP>
+__device__ __forceinline__ void weights_by_rows(uint32_t lead, uint32_t d, uint32_t w, uint32_t z, int n, bool add) {
+  const uint32_t kind = product_of(n, true), b = operand_across(z, SLAB);
+#pragma unroll
+  for (int k = 0; k < 8; k++) multiply_tmem(lead, d, w + 8 * k + (k >> 2) * GAP, b + k * (2048 >> 4), kind, add || k > 0);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
