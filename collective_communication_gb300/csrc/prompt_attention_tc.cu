@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
   constexpr int NS = L::kStages;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (shared_address(raw) & 1023));
-  __shared__ uint64_t q_full, full[NS], empty[NS], s_full[2], p_full[2], o_full[2];
+  __shared__ uint64_t q_full, full[NS], empty[NS], s_full[2], p_half[2], p_full[2], o_full[2];
   __shared__ uint32_t tmem_at, lost[4][4];
   __shared__ int dead_flag, last_flag;
   volatile int* const dead = &dead_flag;
@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     }
     for (int i = 0; i < 2; i++) {
       barrier_init(&s_full[i], 1);
+      barrier_init(&p_half[i], kRows);
       barrier_init(&p_full[i], kRows);
       barrier_init(&o_full[i], 1);
     }
@@ -243,9 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
 #pragma unroll
         for (int t = 0; t < 2; t++) {
           if (j < upto[t]) {
+            if (!(fine = wait_warp(&p_half[t], (j - from) & 1, dead))) break;
+            fence_after();
+            weights_by_rows<L::kSlab, 0, 0, 4>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > from);
             if (!(fine = wait_warp(&p_full[t], (j - from) & 1, dead))) break;
             fence_after();
-            weights_by_rows<L::kSlab, 0>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > from);
+            weights_by_rows<L::kSlab, 0, 4, 8>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, true);
             if (j + 1 >= upto[t]) commit(lead, &o_full[t]);
           }
           // what the warp waits for beside the weights, it waits for while products run
@@ -331,26 +335,29 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       const float by = m == -INFINITY ? 0.f : m;  // nothing seen so far: the weights are 0
       F2 sum = f2(0.f, 0.f), more = f2(0.f, 0.f);
       const F2 scale_pair = f2(scale2, scale2), by_pair = f2(-by, -by);
+      // products with the first half of the weights run while the second half is worked out
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 4) {
-        float2 x = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, by_pair));
-        float2 y = unpack(fma2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale_pair, by_pair));
-        x.x = exp2_fast(x.x);
-        x.y = exp2_fast(x.y);
-        y.x = exp2_fast(y.x);
-        y.y = exp2_fast(y.y);
-        sum = add2(sum, f2(x.x, x.y));
-        more = add2(more, f2(y.x, y.y));
-        s[c / 2] = bf16_pair(x.x, x.y);
-        s[c / 2 + 1] = bf16_pair(y.x, y.y);
+      for (int h = 0; h < 2; h++) {
+#pragma unroll
+        for (int c = h * 64; c < h * 64 + 64; c += 4) {
+          float2 x = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, by_pair));
+          float2 y = unpack(fma2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale_pair, by_pair));
+          x.x = exp2_fast(x.x);
+          x.y = exp2_fast(x.y);
+          y.x = exp2_fast(y.x);
+          y.y = exp2_fast(y.y);
+          sum = add2(sum, f2(x.x, x.y));
+          more = add2(more, f2(y.x, y.y));
+          s[c / 2] = bf16_pair(x.x, x.y);
+          s[c / 2 + 1] = bf16_pair(y.x, y.y);
+        }
+        tmem_store32(s_at[t] + quarter + 32 * h, s + 32 * h);
+        stores_done();
+        fence_before();
+        arrive(h == 0 ? &p_half[t] : &p_full[t]);
       }
-      tmem_store32(s_at[t] + quarter, s);
-      tmem_store32(s_at[t] + quarter + 32, s + 32);
       const float2 u = unpack(add2(sum, more));
       l += u.x + u.y;
-      stores_done();
-      fence_before();
-      arrive(&p_full[t]);
     }
     const bool some = last[t] > begin;  // O has been written
     if (fine && some) {

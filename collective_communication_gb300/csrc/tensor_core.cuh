@@ -203,11 +203,12 @@ __device__ __forceinline__ void rows_by_rows(uint32_t lead, uint32_t d, uint32_t
   }
 }
 // d (+)= w z: w in tensor memory, 128 rows by 128, the second half GAP columns behind the first; z has as many rows, n elements each.
-template <int SLAB, int GAP>
+// The part of them from step FIRST to LAST.
+template <int SLAB, int GAP, int FIRST = 0, int LAST = 8>
 __device__ __forceinline__ void weights_by_rows(uint32_t lead, uint32_t d, uint32_t w, uint32_t z, int n, bool add) {
   const uint32_t kind = product_of(n, true), b = operand_across(z, SLAB);
 #pragma unroll
-  for (int k = 0; k < 8; k++) multiply_tmem(lead, d, w + 8 * k + (k >> 2) * GAP, b + k * (2048 >> 4), kind, add || k > 0);
+  for (int k = FIRST; k < LAST; k++) multiply_tmem(lead, d, w + 8 * k + (k >> 2) * GAP, b + k * (2048 >> 4), kind, add || k > 0);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
