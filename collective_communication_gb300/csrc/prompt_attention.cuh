@@ -78,14 +78,20 @@ __device__ __forceinline__ void check_starts(const int32_t* starts, int sequence
 }
 
 // The sequence that number `slot` belongs to, and which of its tiles it is; false for none.
+// A whole warp looks, 32 sequences at a time.
 __device__ __forceinline__ bool find_sequence(const int32_t* starts, int sequences, int tokens, int per, int unit,
                                               int64_t slot, PromptSequence* seq, int* tile) {
   int lo = 0, hi = sequences;  // the last s with slot(s) <= slot
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    const int a = starts[mid];
-    if (a <= tokens && (int64_t)(a > 0 ? a : 0) * per / unit + mid <= slot) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + 31) >> 5, probe = lo + (int)(threadIdx.x & 31) * step;
+    bool below = false;
+    if (probe < hi) {
+      const int a = starts[probe];
+      below = a <= tokens && (int64_t)(a > 0 ? a : 0) * per / unit + probe <= slot;
+    }
+    const int count = __popc(__ballot_sync(~0u, below));
+    lo += (count > 1 ? count - 1 : 0) * step;
+    hi = min(hi, lo + step);
   }
   const int a = starts[lo], b = starts[lo + 1];
   if (a < 0 || b < a || b > tokens) return false;
@@ -103,7 +109,7 @@ __device__ __forceinline__ bool find_sequence(const int32_t* starts, int sequenc
 __device__ __forceinline__ void cached_sequence(const PromptArgs& a, PromptSequence* seq) {
   const int len = a.lens[seq->index];
   const int room = a.max_blocks << a.page_shift;
-  if (threadIdx.x == 0 && (len < 0 || len > room)) op_report(a.ws, kErrCapacity);
+  if ((threadIdx.x & 31) == 0 && (len < 0 || len > room)) op_report(a.ws, kErrCapacity);
   seq->before = (len < 0 ? 0 : len) - seq->length;
   seq->keys = len < 0 ? 0 : len < room ? len : room;
 }

@@ -7,14 +7,20 @@
 // query head of the group of a token, so a tile's 128 rows are floor(128 / group)
 // tokens, and K and V are read once for all heads of the group.
 //
-// A block has two tiles of rows and walks over tiles of 128 keys. One warp copies (TMA),
-// one issues products, and a warpgroup for each tile of rows turns S into P: a thread a
-// row, so that the softmax needs no exchange between threads. While one tile's weights
-// are being worked out, the other's products run. S and O are in tensor memory (2 x 128
-// and 2 x head size columns); P takes the place of the S that it came from, as bf16, and
-// is the left operand of P V from there. Weights are rounded to bf16 (2^-8 of
-// themselves, in both directions): their sum l is of the unrounded ones, so the
-// roundings average out over the keys and stay below the result's own.
+// A block has two tiles of rows (an item) and walks over tiles of 128 keys. One warp
+// copies (TMA), one issues products, and a warpgroup for each tile of rows turns S into
+// P: a thread a row, so that the softmax needs no exchange between threads. While one
+// tile's weights are being worked out, the other's products run. S and O are in tensor
+// memory (2 x 128 and 2 x head size columns); P takes the place of the S that it came
+// from, as bf16, and is the left operand of P V from there; products with the first half
+// of a tile's weights run while the second half is worked out. Weights are rounded to
+// bf16 (2^-8 of themselves, in both directions): their sum l is of the unrounded ones,
+// so the roundings average out over the keys and stay below the result's own.
+//
+// Blocks stay, one an SM, and take items from a counter, those with the most keys first
+// within a sequence. A fourth warp takes them ahead and finds out what they are, so
+// that queries, keys and values of the next item are copied, and its scores worked out,
+// while the last one's results are still being stored.
 //
 // m moves only if a score is more than 8 above it (in base 2): weights up to 2^8 lose
 // nothing in binary32, and O is read and rescaled for almost no tile. Products run in
@@ -22,9 +28,9 @@
 // sees says that P V of the last one has been added too.
 //
 // Few rows over many keys (the verification of drafted tokens behind a long context)
-// would leave most SMs idle: where the blocks would be fewer than half of the SMs, each
-// tile's keys are split over several, which leave O, m and l unscaled as binary32, and
-// the one that arrives last adds them up in the order of the keys.
+// would leave most SMs idle: where the items would be at most half of the SMs, each
+// one's keys are split over several, which leave O, m and l unscaled as binary32, and a
+// second kernel adds them up in the order of the keys, a warp a row.
 #include <cstdio>
 
 #include "prompt_attention.cuh"
@@ -41,7 +47,10 @@ constexpr int kThreads = 384;  // two softmax warpgroups, and one of which a war
 constexpr int kFewRegisters = 72, kManyRegisters = 216;
 static_assert(kFewRegisters + 2 * kManyRegisters <= 3 * 168, "no more than the block was launched with");
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kCopyWarp = 8, kProductWarp = 9;
+constexpr int kCopyWarp = 8, kProductWarp = 9, kItemWarp = 10;
+constexpr int kItemSlots = 4, kLostSlots = 8;
+constexpr int kNextItem = kOpCounters - 1, kDoneBlocks = kOpCounters - 2;  // counters of the workspace
+constexpr int kNotWanted = INT32_MIN;  // for a page number: a box past the keys
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Maps {
@@ -52,32 +61,90 @@ template <int DP>
 struct Layout {
   static constexpr int kSlab = kRows * 128;              // 64 elements of 128 rows
   static constexpr int kTile = kSlab * (DP / 64);
+  static constexpr int kQueries = 3;                     // tiles of queries: the item's, and one of the next
   static constexpr int kStages = DP == 64 ? 8 : 4;       // tiles of keys or values
-  static constexpr int kShared = (2 + kStages) * kTile + 1024;
+  static constexpr int kShared = (kQueries + kStages) * kTile + 1024;
 };
-
-__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(2 * kRows) : "memory"); }
 
 struct Split {
-  int parts;      // blocks that share a tile's keys
-  float* sums;    // per block: 2 x 128 rows of DP binary32, then m and l of each
+  int64_t slots, items;
+  int parts;    // that an item's keys are split into
+  float* sums;  // per item and part: 2 x 128 rows of DP binary32, then m and l of each
 };
+template <int DP>
+constexpr int64_t kPartFloats = 2 * kRows * (DP + 2);
+
+struct Item {
+  int there;        // 0: no more
+  int rank, head;   // key head
+  int sequence, keys;
+  int first, before;  // the first row's token in the step, and its position
+  int tokens[2];    // of each tile of rows
+  int begin, end;   // tiles of keys
+  int last[2];      // a tile of rows walks from begin to here
+  int part;
+  int64_t index;    // of the item, parts aside
+};
+
+// Item number n in order; false if there is none (a whole warp).
+template <bool PAGED>
+__device__ __forceinline__ bool find_item(const PromptArgs& a, const Split& split, int64_t n, Item* item) {
+  const int per_tile = kRows / (a.q_heads / a.kv_heads);
+  item->part = (int)(n % split.parts);
+  const int64_t whole = n / split.parts, lanes = (int64_t)a.kv_heads * a.nranks;
+  const int lane_of = (int)(whole % lanes);
+  item->head = lane_of % a.kv_heads;
+  item->rank = lane_of / a.kv_heads;
+  // the last tokens of a sequence see the most keys: they come first
+  const int64_t slot = split.slots - 1 - whole / lanes;
+  item->index = slot * lanes + lane_of;
+  PromptSequence seq;
+  int pair;
+  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, slot, &seq, &pair)) return false;
+  if (PAGED) cached_sequence(a, &seq);
+  const int token0 = pair * 2 * per_tile;  // of the sequence
+  item->sequence = seq.index;
+  item->keys = seq.keys;
+  item->first = seq.first + token0;
+  item->before = seq.before + token0;
+  int tiles[2];
+#pragma unroll
+  for (int t = 0; t < 2; t++) {
+    const int tokens = max(0, min(per_tile, seq.length - token0 - t * per_tile));
+    const int sees = min(item->before + t * per_tile + tokens, seq.keys);
+    tiles[t] = tokens > 0 && sees > 0 ? (sees + kKeys - 1) / kKeys : 0;
+    item->tokens[t] = tokens;
+  }
+  const int most = max(tiles[0], tiles[1]);
+  item->begin = (int)((int64_t)most * item->part / split.parts);
+  item->end = (int)((int64_t)most * (item->part + 1) / split.parts);
+#pragma unroll
+  for (int t = 0; t < 2; t++) item->last[t] = max(item->begin, min(tiles[t], item->end));
+  item->there = 1;
+  return true;
+}
 
 template <int DP, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_constant__ PromptArgs a,
-                                                                const __grid_constant__ Maps maps, Split split) {
+                                                                const __grid_constant__ Maps maps,
+                                                                const __grid_constant__ Split split) {
   using L = Layout<DP>;
-  constexpr int NS = L::kStages;
+  constexpr int NS = L::kStages, NQ = L::kQueries;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (shared_address(raw) & 1023));
-  __shared__ uint64_t q_full, full[NS], empty[NS], s_full[2], p_half[2], p_full[2], o_full[2];
-  __shared__ uint32_t tmem_at, lost[4][4];
-  __shared__ int dead_flag, last_flag;
+  __shared__ uint64_t q_full[NQ], q_empty[NQ], full[NS], empty[NS], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2],
+      item_full[kItemSlots], item_empty[kItemSlots];
+  __shared__ Item items[kItemSlots];
+  __shared__ uint32_t tmem_at, lost[kLostSlots][4];
+  __shared__ int dead_flag;
   volatile int* const dead = &dead_flag;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     dead_flag = 0;
-    barrier_init(&q_full, 1);
+    for (int i = 0; i < NQ; i++) {
+      barrier_init(&q_full[i], 1);
+      barrier_init(&q_empty[i], 4);  // the warps that store a tile's results by way of its queries' place
+    }
     for (int i = 0; i < NS; i++) {
       barrier_init(&full[i], 1);
       barrier_init(&empty[i], 1);
@@ -87,135 +154,202 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       barrier_init(&p_half[i], kRows);
       barrier_init(&p_full[i], kRows);
       barrier_init(&o_full[i], 1);
+      barrier_init(&o_free[i], kRows);
+    }
+    for (int i = 0; i < kItemSlots; i++) {
+      barrier_init(&item_full[i], 1);
+      barrier_init(&item_empty[i], 10);  // the warps that read it: copies, products, eight of the softmax
     }
     barriers_ready();
   }
+  if (warp == kCopyWarp && lane == 0) {  // the descriptors of the first item
+    const int first = (int)(blockIdx.x / split.parts % (a.kv_heads * a.nranks)) / a.kv_heads;
+    prefetch_map(&maps.q[first]);
+    prefetch_map(&maps.k[first]);
+    prefetch_map(&maps.v[first]);
+  }
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
-  const int group = a.q_heads / a.kv_heads, head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
-  const int per_tile = kRows / group;  // tokens of a tile
-  PromptSequence seq;
-  int pair;
-  // the last tokens of a sequence see the most keys: their blocks start first
-  const int part = (int)(blockIdx.x % (unsigned)split.parts);
-  const int64_t slot = (gridDim.x / (unsigned)split.parts) - 1 - blockIdx.x / (unsigned)split.parts;
-  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, slot, &seq, &pair)) return;
-  if (PAGED) cached_sequence(a, &seq);
-  const int token0 = pair * 2 * per_tile;  // of the sequence
-  int rows_of[2], tiles_of[2];             // tokens of each tile, and tiles of keys that its last one sees
-#pragma unroll
-  for (int t = 0; t < 2; t++) {
-    rows_of[t] = max(0, min(per_tile, seq.length - token0 - t * per_tile));
-    const int sees = min(seq.before + token0 + t * per_tile + rows_of[t], seq.keys);
-    tiles_of[t] = rows_of[t] > 0 && sees > 0 ? (sees + kKeys - 1) / kKeys : 0;
-  }
-  const int tiles = max(tiles_of[0], tiles_of[1]);
-  const int begin = (int)((int64_t)tiles * part / split.parts), end = (int)((int64_t)tiles * (part + 1) / split.parts);
+  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
   constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
   constexpr uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 384};
-  uint8_t* const ring = smem + 2 * L::kTile;
+  uint8_t* const ring = smem + NQ * L::kTile;
+  const int group = a.q_heads / a.kv_heads, D = a.head_dim;
+  const int per_tile = kRows / group;  // tokens of a tile
   const int steps = (D + 15) / 16;
-  const int last[2] = {min(tiles_of[0], end), min(tiles_of[1], end)};  // a tile of rows walks from begin to here
 
   if (warp >= kCopyWarp) give_registers<kFewRegisters>();
-  if (warp == kCopyWarp) {
-    if (begin < end) {
-      if (lane == 0) {
-        prefetch_map(&maps.k[rank]);
-        prefetch_map(&maps.v[rank]);
-        const int boxes = (last[0] > begin) + (last[1] > begin);
-        arrive_expect(&q_full, (uint32_t)(boxes * per_tile * group * 128 * (DP / 64)));
-        for (int t = 0; t < 2; t++)
-          if (last[t] > begin)
-            for (int h = 0; h < DP / 64; h++)
-              copy_3d(smem + t * L::kTile + h * L::kSlab, &maps.q[rank], h * 64, head * group,
-                      seq.first + token0 + t * per_tile, &q_full);
+  if (warp == kItemWarp) {
+    uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
+    const int64_t all = split.items * split.parts;
+    int64_t n = blockIdx.x;
+    for (int i = 0;;) {
+      Item item;
+      const bool more = n < all;
+      if (!more) item.there = 0;
+      if (!more || find_item<PAGED>(a, split, n, &item)) {
+        if (!wait_warp(&item_empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, dead)) break;
+        if (lane == 0) {
+          items[i % kItemSlots] = item;
+          arrive(&item_full[i % kItemSlots]);
+        }
+        i++;
       }
-      int stage = 0;
-      uint32_t phase = 0;
+      if (!more) break;
+      uint32_t next = 0;
+      if (lane == 0) next = atomicAdd(&counters[kNextItem], 1);
+      n = (int64_t)gridDim.x + __shfl_sync(~0u, next, 0);
+    }
+    // the last block to have no more sets the counters back
+    if (lane == 0 && atom_add_acq_rel_u32(&counters[kDoneBlocks], 1) == gridDim.x - 1) {
+      counters[kNextItem] = 0;
+      counters[kDoneBlocks] = 0;
+    }
+  } else if (warp == kCopyWarp) {
+    int stage = 0, queries = 0, seen = 0;  // seen: tiles of keys of the items before
+    uint32_t phase = 0;
+    for (int i = 0;; i++) {
+      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      const Item& item = items[i % kItemSlots];
+      const int there = uniform(item.there);
+      if (!there) break;
+      const int rank = uniform(item.rank), head = uniform(item.head), first = uniform(item.first), keys = uniform(item.keys),
+                begin = uniform(item.begin), end = uniform(item.end), sequence = uniform(item.sequence),
+                before = uniform(item.before);
+      const int last[2] = {uniform(item.last[0]), uniform(item.last[1])};
+      __syncwarp();
+      if (lane == 0) arrive(&item_empty[i % kItemSlots]);
+      const CUtensorMap *const map_q = &maps.q[rank], *const map_k = &maps.k[rank], *const map_v = &maps.v[rank];
+      auto query = [&](int t) {
+        const int at = queries % NQ;
+        if (!wait_warp(&q_empty[at], (queries / NQ & 1) ^ 1, dead)) return false;
+        if (lane == 0) {
+          arrive_expect(&q_full[at], (uint32_t)(per_tile * group * 128 * (DP / 64)));
+          for (int h = 0; h < DP / 64; h++)
+            copy_3d(smem + at * L::kTile + h * L::kSlab, map_q, h * 64, head * group, first + t * per_tile, &q_full[at]);
+        }
+        queries++;
+        return true;
+      };
       bool fine = true;
+      if (last[0] > begin) fine = query(0);
+      const int base = first - before;  // of the sequence, if its keys are dense
+      // pages of a tile's boxes, lane by lane, read a tile ahead
+      const int box = PAGED ? min(kKeys, 1 << a.page_shift) : kKeys, boxes = kKeys / box;
+      int page[4], ahead[4];
+      auto pages_of = [&](int j) {
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          const int b = lane + 32 * x, key = j * kKeys + b * box;
+          ahead[x] = kNotWanted;
+          if (b < boxes && j < end && key < keys) ahead[x] = a.table[sequence * a.table_stride + (key >> a.page_shift)];
+        }
+      };
+      if (PAGED) pages_of(begin);
       for (int j = begin; j < end && fine; j++) {
-        int page = 0, box = kKeys;
-        bool there = true;
-        if (PAGED) box = min(kKeys, 1 << a.page_shift);
-        uint32_t bad[4];
+        if (PAGED) {
+#pragma unroll
+          for (int x = 0; x < 4; x++) page[x] = ahead[x];
+          pages_of(j + 1);
+        }
         for (int which = 0; which < 2 && fine; which++) {
-          fine = wait(&empty[stage], phase ^ 1, dead);
+          if (!(fine = wait_warp(&empty[stage], phase ^ 1, dead))) break;
           uint8_t* to = ring + stage * L::kTile;
-          const CUtensorMap* map = which == 0 ? &maps.k[rank] : &maps.v[rank];
+          const CUtensorMap* map = which == 0 ? map_k : map_v;
           if (!PAGED) {
-            if (fine && lane == 0) {
+            if (lane == 0) {
               arrive_expect(&full[stage], L::kTile);
               for (int h = 0; h < DP / 64; h++)
-                copy_3d(to + h * L::kSlab, map, h * 64, head, seq.first + j * kKeys, &full[stage]);
+                copy_3d(to + h * L::kSlab, map, h * 64, head, base + j * kKeys, &full[stage]);
             }
-          } else if (fine) {
+          } else {
             // a box a page (or 128 tokens of a larger one); boxes past the keys, and pages that are none, are not copied
-            const int boxes = kKeys / box;
-            if (which == 0) bad[0] = bad[1] = bad[2] = bad[3] = 0;
             int count = 0;
-            for (int b0 = 0; b0 < boxes; b0 += 32) {
-              const int b = b0 + lane, key = j * kKeys + b * box;
-              const bool wanted = b < boxes && key < seq.keys;
-              page = wanted ? a.table[seq.index * a.table_stride + (key >> a.page_shift)] : 0;
-              there = wanted && (unsigned)page < (unsigned)a.num_pages;
-              if (wanted && !there) op_report(a.ws, kErrCapacity);
-              count += __popc(__ballot_sync(~0u, there));
-              if (which == 0 && __any_sync(~0u, wanted && !there)) {
-                for (int r = 0; r < 4; r++) {  // rows of the tile that such a page would have filled
-                  uint32_t mine = 0;
-                  if (wanted && !there)
-                    for (int x = b * box; x < (b + 1) * box; x++)
-                      if (x >> 5 == r) mine |= 1u << (x & 31);
-                  bad[r] |= __reduce_or_sync(~0u, mine);
+#pragma unroll
+            for (int x = 0; x < 4; x++) count += __popc(__ballot_sync(~0u, (unsigned)page[x] < (unsigned)a.num_pages));
+            if (which == 0) {
+              uint32_t bad[4] = {0, 0, 0, 0};
+              bool none = false;
+#pragma unroll
+              for (int x = 0; x < 4; x++) none |= page[x] != kNotWanted && (unsigned)page[x] >= (unsigned)a.num_pages;
+              if (__any_sync(~0u, none)) {
+                if (none) op_report(a.ws, kErrCapacity);
+                for (int x = 0; x < 4; x++) {
+                  const bool mine = page[x] != kNotWanted && (unsigned)page[x] >= (unsigned)a.num_pages;
+#pragma unroll
+                  for (int r = 0; r < 4; r++) {  // rows of the tile that such a page would have filled
+                    uint32_t bits = 0;
+                    if (mine)
+                      for (int y = (lane + 32 * x) * box; y < (lane + 32 * x + 1) * box; y++)
+                        if (y >> 5 == r) bits |= 1u << (y & 31);
+                    bad[r] |= __reduce_or_sync(~0u, bits);
+                  }
                 }
               }
+              if (lane == 0) {
+#pragma unroll
+                for (int r = 0; r < 4; r++) lost[(seen + j - begin) % kLostSlots][r] = bad[r];
+              }
             }
-            if (which == 0 && lane == 0)
-              for (int r = 0; r < 4; r++) lost[j & 3][r] = bad[r];
             __syncwarp();
             if (lane == 0) arrive_expect(&full[stage], (uint32_t)(count * box * 128 * (DP / 64)));
             __syncwarp();
-            for (int b0 = 0; b0 < boxes; b0 += 32) {
-              const int b = b0 + lane, key = j * kKeys + b * box;
-              const bool wanted = b < boxes && key < seq.keys;
-              if (!wanted) continue;
-              page = a.table[seq.index * a.table_stride + (key >> a.page_shift)];
-              if ((unsigned)page >= (unsigned)a.num_pages) continue;
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+              if ((unsigned)page[x] >= (unsigned)a.num_pages) continue;
+              const int b = lane + 32 * x;
               for (int h = 0; h < DP / 64; h++)
-                copy_3d(to + h * L::kSlab + b * box * 128, map, h * 64, key & ((1 << a.page_shift) - 1),
-                        page * a.kv_heads + head, &full[stage]);
+                copy_3d(to + h * L::kSlab + b * box * 128, map, h * 64, (j * kKeys + b * box) & ((1 << a.page_shift) - 1),
+                        page[x] * a.kv_heads + head, &full[stage]);
             }
+            __syncwarp();
           }
           if (++stage == NS) {
             stage = 0;
             phase ^= 1;
           }
+          if (j == begin && which == 0 && last[1] > begin) fine = query(1);
         }
       }
+      if (!fine) break;
+      seen += end - begin;
     }
   } else if (warp == kProductWarp) {
-    const int from = uniform(begin), to = uniform(end), upto[2] = {uniform(last[0]), uniform(last[1])}, keys_of = uniform(seq.keys);
-    if (from < to) {
-      const uint32_t lead = elect_one();
-      const int n_out = steps * 16;
-      const uint32_t q_at = shared_address(smem), ring_at = shared_address(ring);
+    const uint32_t lead = elect_one();
+    const int n_out = steps * 16;
+    const uint32_t q_at = shared_address(smem), ring_at = shared_address(ring);
+    int stage = 0, queries = 0, seen = 0;
+    int walked[2] = {0, 0}, results[2] = {0, 0};  // tiles of keys, and items, of each tile of rows so far
+    uint32_t phase = 0;
+    for (int i = 0;; i++) {
+      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      const Item& item = items[i % kItemSlots];
+      const int there = uniform(item.there);
+      if (!there) break;
+      const int begin = uniform(item.begin), end = uniform(item.end), keys = uniform(item.keys);
+      const int last[2] = {uniform(item.last[0]), uniform(item.last[1])};
+      __syncwarp();
+      if (lane == 0) arrive(&item_empty[i % kItemSlots]);
+      if (begin >= end) continue;
+      int q_slot[2];
+#pragma unroll
+      for (int t = 0; t < 2; t++) q_slot[t] = last[t] > begin ? queries++ : 0;
       // the S of a key tile for a tile of rows that sees it
       auto score = [&](int t, uint32_t k_at) {
-        rows_by_rows<DP / 16, L::kSlab>(lead, s_at[t], q_at + t * L::kTile, k_at, kKeys, steps);
+        rows_by_rows<DP / 16, L::kSlab>(lead, s_at[t], q_at + (uint32_t)(q_slot[t] % NQ) * L::kTile, k_at, kKeys, steps);
         commit(lead, &s_full[t]);
       };
       // V of key tile j is there; rows with no key would be multiplied by weights of 0, and may hold a NaN
       auto values = [&](int j, int stage, uint32_t phase) {
         if (!wait_warp(&full[stage], phase, dead)) return false;
-        const int keys = keys_of - j * kKeys;
-        const bool holes = PAGED && __any_sync(~0u, lane < 4 && lost[j & 3][lane & 3] != 0);
-        if (keys < kKeys || holes) {
+        const int left = keys - j * kKeys;
+        const uint32_t* holes_of = lost[(seen + j - begin) % kLostSlots];
+        const bool holes = PAGED && __any_sync(~0u, lane < 4 && holes_of[lane & 3] != 0);
+        if (left < kKeys || holes) {
           for (int r = lane; r < kKeys; r += 32)
-            if (r >= keys || (holes && (lost[j & 3][r >> 5] >> (r & 31) & 1)))
+            if (r >= left || (holes && (holes_of[r >> 5] >> (r & 31) & 1)))
               for (int h = 0; h < DP / 64; h++)
                 for (int c = 0; c < 8; c++)
                   *reinterpret_cast<uint4*>(ring + stage * L::kTile + h * L::kSlab + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
@@ -225,37 +359,51 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         return true;
       };
       // stages: K of the first tile, then V of a tile and K of the next in turn
-      bool fine = wait_warp(&q_full, 0, dead) && wait_warp(&full[0], 0, dead);
-      if (fine) {
+      bool fine = wait_warp(&full[stage], phase, dead);
+      const int first_stage = stage;
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        if (!fine || last[t] <= begin) continue;
+        if (!(fine = wait_warp(&q_full[q_slot[t] % NQ], q_slot[t] / NQ & 1, dead))) break;
         fence_after();
-        for (int t = 0; t < 2; t++)
-          if (upto[t] > from) score(t, ring_at);
-        commit(lead, &empty[0]);
-        fine = values(from, 1, 0);
+        score(t, ring_at + first_stage * L::kTile);
       }
-      int v_stage = 1;
-      uint32_t v_phase = 0;
-      for (int j = from; j < to && fine; j++) {
-        const bool more = j + 1 < to;
+      if (!fine) break;
+      commit(lead, &empty[first_stage]);
+      if (++stage == NS) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (!values(begin, stage, phase)) break;
+      int v_stage = stage;
+      uint32_t v_phase = phase;
+      for (int j = begin; j < end && fine; j++) {
+        const bool more = j + 1 < end;
         const int k_stage = v_stage + 1 == NS ? 0 : v_stage + 1;
         const uint32_t k_phase = v_phase ^ (k_stage == 0);
         const int next_stage = k_stage + 1 == NS ? 0 : k_stage + 1;
         const uint32_t next_phase = k_phase ^ (next_stage == 0);
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-          if (j < upto[t]) {
-            if (!(fine = wait_warp(&p_half[t], (j - from) & 1, dead))) break;
+          if (j < last[t]) {
+            // O of the item before has been read
+            if (j == begin && results[t] > 0 && !(fine = wait_warp(&o_free[t], (results[t] - 1) & 1, dead))) break;
+            if (!(fine = wait_warp(&p_half[t], walked[t] & 1, dead))) break;
             fence_after();
-            weights_by_rows<L::kSlab, 0, 0, 4>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > from);
-            if (!(fine = wait_warp(&p_full[t], (j - from) & 1, dead))) break;
+            weights_by_rows<L::kSlab, 0, 0, 4>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > begin);
+            if (!(fine = wait_warp(&p_full[t], walked[t] & 1, dead))) break;
             fence_after();
             weights_by_rows<L::kSlab, 0, 4, 8>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, true);
-            if (j + 1 >= upto[t]) commit(lead, &o_full[t]);
+            walked[t]++;
+            if (j + 1 == last[t]) {
+              commit(lead, &o_full[t]);
+              results[t]++;
+            }
           }
           // what the warp waits for beside the weights, it waits for while products run
           if (more && t == 0 && !(fine = wait_warp(&full[k_stage], k_phase, dead))) break;
           if (more && t == 1 && !(fine = values(j + 1, next_stage, next_phase))) break;
-          if (j + 1 < upto[t]) {
+          if (j + 1 < last[t]) {
             fence_after();
             score(t, ring_at + k_stage * L::kTile);
           }
@@ -263,138 +411,168 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         if (!fine) break;
         commit(lead, &empty[v_stage]);
         if (more) commit(lead, &empty[k_stage]);
+        // behind the item's last V: the next item's first K
+        stage = more ? next_stage : k_stage;
+        phase = more ? next_phase : k_phase;
         v_stage = next_stage;
         v_phase = next_phase;
       }
+      if (!fine) break;
+      seen += end - begin;
     }
   } else if (warp < kCopyWarp) {
     take_registers<kManyRegisters>();
     const int t = warp >> 2;
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
-    const int row = threadIdx.x & 127, token = row / group, query = head * group + row % group;
-    const bool mine = token < rows_of[t];
-    const int64_t at_token = (int64_t)seq.first + token0 + t * per_tile + token;
-    // rows that are none see what the tile's first row sees: they hold anything, and nobody reads them
-    const int sees = min(seq.before + token0 + t * per_tile + (mine ? token : 0) + 1, seq.keys);
-    int least = sees;  // of the warp
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) least = min(least, __shfl_xor_sync(~0u, least, d));
+    const int row = threadIdx.x & 127, token = row / group;
     // of a negative scale or none, the scores are turned or cleared first, so that the largest is the one that counts
     const float scale2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
     const uint32_t turn = a.scale < 0.f ? 0x80000000u : 0u, keep_bits = a.scale == 0.f ? 0u : ~0u;
-    float m = -INFINITY, l = 0.f;
-    bool fine = true;
-    for (int j = begin; j < last[t] && fine; j++) {
-      if (!(fine = wait(&s_full[t], (j - begin) & 1, dead))) break;
-      fence_after();
-      uint32_t s[kKeys];
+    int walked = 0, results = 0, seen = 0, queries = 0;  // queries: tiles of queries of both tiles of rows
+    for (int i = 0;; i++) {
+      if (!wait(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      const Item& item = items[i % kItemSlots];
+      if (!item.there) break;
+      const int begin = item.begin, end = item.end, last = item.last[t];
+      const int q_slot = (queries + (t == 1 && item.last[0] > begin)) % NQ;
+      queries += (item.last[0] > begin) + (item.last[1] > begin);
+      const bool mine = token < item.tokens[t];
+      // rows that are none see what the tile's first row sees: they hold anything, and nobody reads them
+      const int sees = min(item.before + t * per_tile + (mine ? token : 0) + 1, item.keys);
+      const int query = item.head * group + row % group, rank = item.rank, part = item.part;
+      const int64_t at_token = (int64_t)item.first + t * per_tile + token, index = item.index;
+      __syncwarp();
+      if (lane == 0) arrive(&item_empty[i % kItemSlots]);
+      int least = sees;  // of the warp
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 32) tmem_load32(s_at[t] + quarter + c, s + c);
-      loads_done();
-      if (!(a.scale > 0.f)) {
+      for (int d = 16; d > 0; d >>= 1) least = min(least, __shfl_xor_sync(~0u, least, d));
+      float m = -INFINITY, l = 0.f;
+      bool fine = true;
+      for (int j = begin; j < last; j++) {
+        if (!(fine = wait(&s_full[t], walked & 1, dead))) break;
+        walked++;
+        fence_after();
+        uint32_t s[kKeys];
 #pragma unroll
-        for (int c = 0; c < kKeys; c++) s[c] = (s[c] ^ turn) & keep_bits;
-      }
-      const bool holes = PAGED && (lost[j & 3][0] | lost[j & 3][1] | lost[j & 3][2] | lost[j & 3][3]) != 0;
-      if ((j + 1) * kKeys > least || holes) {
-        const int upto = sees - j * kKeys;
+        for (int c = 0; c < kKeys; c += 32) tmem_load32(s_at[t] + quarter + c, s + c);
+        loads_done();
+        if (!(a.scale > 0.f)) {
 #pragma unroll
-        for (int c = 0; c < kKeys; c++) {
-          bool seen = c < upto;
-          if (PAGED && holes) seen = seen && !(lost[j & 3][c >> 5] >> (c & 31) & 1);
-          if (!seen) s[c] = 0xff800000u;
+          for (int c = 0; c < kKeys; c++) s[c] = (s[c] ^ turn) & keep_bits;
         }
-      }
-      float top[4];
+        const uint32_t* holes_of = lost[(seen + j - begin) % kLostSlots];
+        const bool holes = PAGED && (holes_of[0] | holes_of[1] | holes_of[2] | holes_of[3]) != 0;
+        if ((j + 1) * kKeys > least || holes) {
+          const int upto = sees - j * kKeys;
 #pragma unroll
-      for (int i = 0; i < 4; i++) top[i] = __uint_as_float(s[i]);
-#pragma unroll
-      for (int c = 4; c < kKeys; c += 4)
-#pragma unroll
-        for (int i = 0; i < 4; i++) top[i] = fmaxf(top[i], __uint_as_float(s[c + i]));
-      const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      const float high = best * scale2;
-      // (rows that are none have no say: what they hold would change how the others are rounded)
-      if (__any_sync(~0u, mine && high > m + 8.f)) {
-        const float next = fmaxf(m, high);
-        const float keep = next == -INFINITY ? 1.f : exp2_fast(m - next);
-        m = next;
-        l *= keep;
-        if (j > begin) {
-          uint32_t o[16];
-#pragma unroll 1
-          for (int c = 0; c < DP; c += 16) {
-            tmem_load16(o_at[t] + quarter + c, o);
-            loads_done();
-#pragma unroll
-            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-            tmem_store16(o_at[t] + quarter + c, o);
+          for (int c = 0; c < kKeys; c++) {
+            bool there = c < upto;
+            if (PAGED && holes) there = there && !(holes_of[c >> 5] >> (c & 31) & 1);
+            if (!there) s[c] = 0xff800000u;
           }
         }
-      }
-      const float by = m == -INFINITY ? 0.f : m;  // nothing seen so far: the weights are 0
-      F2 sum = f2(0.f, 0.f), more = f2(0.f, 0.f);
-      const F2 scale_pair = f2(scale2, scale2), by_pair = f2(-by, -by);
-      // products with the first half of the weights run while the second half is worked out
+        float top[4];
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
+        for (int i = 0; i < 4; i++) top[i] = __uint_as_float(s[i]);
 #pragma unroll
-        for (int c = h * 64; c < h * 64 + 64; c += 4) {
-          float2 x = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, by_pair));
-          float2 y = unpack(fma2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale_pair, by_pair));
-          x.x = exp2_fast(x.x);
-          x.y = exp2_fast(x.y);
-          y.x = exp2_fast(y.x);
-          y.y = exp2_fast(y.y);
-          sum = add2(sum, f2(x.x, x.y));
-          more = add2(more, f2(y.x, y.y));
-          s[c / 2] = bf16_pair(x.x, x.y);
-          s[c / 2 + 1] = bf16_pair(y.x, y.y);
+        for (int c = 4; c < kKeys; c += 4)
+#pragma unroll
+          for (int i = 0; i < 4; i++) top[i] = fmaxf(top[i], __uint_as_float(s[c + i]));
+        const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const float high = best * scale2;
+        // (rows that are none have no say: what they hold would change how the others are rounded)
+        if (__any_sync(~0u, mine && high > m + 8.f)) {
+          const float next = fmaxf(m, high);
+          const float keep = next == -INFINITY ? 1.f : exp2_fast(m - next);
+          m = next;
+          l *= keep;
+          if (j > begin) {
+            uint32_t o[16];
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              tmem_load16(o_at[t] + quarter + c, o);
+              loads_done();
+#pragma unroll
+              for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+              tmem_store16(o_at[t] + quarter + c, o);
+            }
+          }
         }
-        tmem_store32(s_at[t] + quarter + 32 * h, s + 32 * h);
-        stores_done();
-        fence_before();
-        arrive(h == 0 ? &p_half[t] : &p_full[t]);
+        const float by = m == -INFINITY ? 0.f : m;  // nothing seen so far: the weights are 0
+        F2 sum = f2(0.f, 0.f), more = f2(0.f, 0.f);
+        const F2 scale_pair = f2(scale2, scale2), by_pair = f2(-by, -by);
+        // products with the first half of the weights run while the second half is worked out
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+#pragma unroll
+          for (int c = h * 64; c < h * 64 + 64; c += 4) {
+            float2 x = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, by_pair));
+            float2 y = unpack(fma2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale_pair, by_pair));
+            x.x = exp2_fast(x.x);
+            x.y = exp2_fast(x.y);
+            y.x = exp2_fast(y.x);
+            y.y = exp2_fast(y.y);
+            sum = add2(sum, f2(x.x, x.y));
+            more = add2(more, f2(y.x, y.y));
+            s[c / 2] = bf16_pair(x.x, x.y);
+            s[c / 2 + 1] = bf16_pair(y.x, y.y);
+          }
+          tmem_store32(s_at[t] + quarter + 32 * h, s + 32 * h);
+          stores_done();
+          fence_before();
+          arrive(h == 0 ? &p_half[t] : &p_full[t]);
+        }
+        const float2 u = unpack(add2(sum, more));
+        l += u.x + u.y;
       }
-      const float2 u = unpack(add2(sum, more));
-      l += u.x + u.y;
-    }
-    const bool some = last[t] > begin;  // O has been written
-    if (fine && some) {
-      fine = wait(&o_full[t], 0, dead);
-      fence_after();
-    }
-    if (fine && split.parts == 1) {
+      if (!fine) break;
+      seen += end - begin;
+      const bool some = last > begin;  // O has been written
+      if (some) {
+        if (!wait(&o_full[t], results & 1, dead)) break;
+        results++;
+        fence_after();
+      }
       const float by = l == 0.f ? 0.f : 1.f / l;
       uint16_t* out = (uint16_t*)a.out[rank] + at_token * a.out_stride + (int64_t)query * D;
+      float* sums = split.sums + (index * split.parts + part) * kPartFloats<DP> + t * kRows * (DP + 2);
+      if (!some) {
+        for (int c = 0; c < D && mine && split.parts == 1; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+      } else if (split.parts == 1) {
+        // A warp's 32 rows go by way of their queries' place in shared memory, with 16-byte
+        // pieces swizzled, so that stores cover whole lines: a row a thread took 6400 cycles
+        // a tile for the addresses of its 32 lines a store.
+        uint8_t* const place = smem + q_slot * L::kTile + row * 128;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (some) {
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
           tmem_load32(o_at[t] + quarter + c, o);
           loads_done();
-        }
-        if (mine) {
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
-            if (c + i >= D) continue;
             Pack8<uint16_t> x;
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; k++) v[k] = l == 0.f ? 0.f : __uint_as_float(o[i + k]) * by;
             x.narrow(v);
-            x.store(out + c + i);
+            const int piece = (c + i) / 8;
+            *reinterpret_cast<uint4*>(place + (piece >> 3) * L::kSlab + (((piece & 7) ^ (row & 7)) << 4)) = x.u;
           }
         }
-      }
-      if (mine && a.lse[rank] != nullptr) a.lse[rank][at_token * a.q_heads + query] = (m + log2f(l)) / kLog2e;
-    } else if (fine) {
-      // a part of the keys: O, m and l as they are
-      const int64_t item = ((int64_t)rank * a.kv_heads + head) * (gridDim.x / (unsigned)split.parts) + slot;
-      float* mine_at = split.sums + (item * split.parts + part) * (int64_t)(2 * kRows * (DP + 2)) + t * kRows * (DP + 2);
-      mine_at[kRows * DP + row] = m;
-      mine_at[kRows * (DP + 1) + row] = l;
-      if (some) {
+        fence_before();
+        arrive(&o_free[t]);
+        __syncwarp();
+        constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // lanes of a row, rows of an instruction
+        const int piece = lane % kPieces;
+        const uint8_t* from = smem + q_slot * L::kTile + (row - lane) * 128 + (piece >> 3) * L::kSlab;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+          const int r = r0 + lane / kPieces;
+          uint16_t* const to = (uint16_t*)__shfl_sync(~0u, mine ? (unsigned long long)out : 0ull, r);
+          const uint4 x = *reinterpret_cast<const uint4*>(from + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+          if (to != nullptr && piece * 8 < D) *reinterpret_cast<uint4*>(to + piece * 8) = x;
+        }
+      } else {  // a part of the keys: O as it is
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -403,54 +581,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
           if (!mine) continue;
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            if (c + i < D)
-              *reinterpret_cast<uint4*>(mine_at + row * DP + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            if (c + i < D) *reinterpret_cast<uint4*>(sums + row * DP + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
+        fence_before();
+        arrive(&o_free[t]);
       }
-    }
-    fence_before();
-    if (split.parts > 1) {
-      // the block that arrives last has every part of the tile
-      const int64_t item = ((int64_t)rank * a.kv_heads + head) * (gridDim.x / (unsigned)split.parts) + slot;
-      __threadfence();
-      softmax_barrier();
-      if (threadIdx.x == 0) {
-        uint32_t* counter = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes) + item;
-        last_flag = atom_add_acq_rel_u32(counter, 1) == (uint32_t)split.parts - 1;
-        if (last_flag) *counter = 0;
+      if (some) {
+        stores_to_products();  // copies write there next
+        __syncwarp();
+        if (lane == 0) arrive(&q_empty[q_slot]);
       }
-      softmax_barrier();
-      if (last_flag && !*dead) {
-        __threadfence();
-        const float* parts = split.sums + item * split.parts * (int64_t)(2 * kRows * (DP + 2));
-        const int chunks = D / 8;
-        for (int i = threadIdx.x; i < 2 * kRows * chunks; i += 2 * kRows) {
-          const int r = i / chunks, d = (i % chunks) * 8, u = r / kRows, row = r % kRows, token = row / group;
-          if (token >= rows_of[u]) continue;
-          float top = -INFINITY, sum = 0.f, v[8] = {};
-          for (int k = 0; k < split.parts; k++)
-            top = fmaxf(top, parts[(int64_t)(2 * k + u) * kRows * (DP + 2) + kRows * DP + row]);
-          for (int k = 0; k < split.parts && top != -INFINITY; k++) {
-            const float* p = parts + (int64_t)(2 * k + u) * kRows * (DP + 2);
-            const float m = p[kRows * DP + row];
-            if (m == -INFINITY) continue;
-            const float w = exp2_fast(m - top);
-            sum = fmaf(p[kRows * (DP + 1) + row], w, sum);
-#pragma unroll
-            for (int x = 0; x < 8; x++) v[x] = fmaf(p[row * DP + d + x], w, v[x]);
-          }
-          const int64_t at_token = (int64_t)seq.first + token0 + u * per_tile + token;
-          const int query = head * group + row % group;
-#pragma unroll
-          for (int x = 0; x < 8; x++) v[x] = sum == 0.f ? 0.f : v[x] / sum;
-          Pack8<uint16_t> out;
-          out.narrow(v);
-          out.store((uint16_t*)a.out[rank] + at_token * a.out_stride + (int64_t)query * D + d);
-          if (d == 0 && a.lse[rank] != nullptr) a.lse[rank][at_token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
-        }
+      if (mine && split.parts > 1) {
+        sums[kRows * DP + row] = m;
+        sums[kRows * (DP + 1) + row] = l;
+      } else if (mine && a.lse[rank] != nullptr) {
+        a.lse[rank][at_token * a.q_heads + query] = (m + log2f(l)) / kLog2e;
       }
     }
   }
+  __syncwarp();
+  fence_before();
   __syncthreads();
   if (*dead) {
     // a wait ran out: copies and products that are still under way have ended by the time this has passed
@@ -463,6 +613,71 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     fence_after();
     tmem_free(tmem, 512);
   }
+}
+
+// The parts of a row's keys, in their order; a warp a row, 16 parts' loads under way.
+template <int DP, bool PAGED>
+__global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a,
+                                                          const __grid_constant__ Split split) {
+  constexpr int E = DP / 32;  // elements of a lane
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  const int lane = threadIdx.x & 31, r = (int)(blockIdx.x % 64) * 4 + (threadIdx.x >> 5), t = r / kRows, row = r % kRows;
+  const int group = a.q_heads / a.kv_heads, D = a.head_dim, token = row / group;
+  Item item;
+  if (!find_item<PAGED>(a, split, (int64_t)(blockIdx.x / 64) * split.parts, &item) || token >= item.tokens[t]) return;
+  const float* sums = split.sums + item.index * split.parts * kPartFloats<DP> + t * kRows * (DP + 2);
+  float m[kPromptSplitBlocks / 32 + 1], top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
+    const int k = i * 32 + lane;
+    m[i] = k < split.parts ? sums[k * kPartFloats<DP> + kRows * DP + row] : -INFINITY;
+    top = fmaxf(top, m[i]);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+#pragma unroll
+  for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
+    const int k = i * 32 + lane;
+    m[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - top);  // now the part's weight
+    if (k < split.parts) sum = fmaf(sums[k * kPartFloats<DP> + kRows * (DP + 1) + row], m[i], sum);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  float v[E] = {};
+#pragma unroll
+  for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
+#pragma unroll
+    for (int k0 = 0; k0 < 32; k0 += 16) {
+      if (i * 32 + k0 >= split.parts) continue;
+      float x[16][E], w[16];
+#pragma unroll
+      for (int k = 0; k < 16; k++) {
+        w[k] = __shfl_sync(~0u, m[i], k0 + k);
+        // a part that saw nothing has left nothing
+        const float* p = sums + (i * 32 + k0 + k) * kPartFloats<DP> + row * DP + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          float2 y = make_float2(0.f, 0.f);
+          if (w[k] != 0.f) y = *reinterpret_cast<const float2*>(p + e);
+          x[k][e] = y.x;
+          x[k][e + 1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 16; k++)
+#pragma unroll
+        for (int e = 0; e < E; e++) v[e] = fmaf(x[k][e], w[k], v[e]);
+    }
+  }
+  const int64_t at_token = (int64_t)item.first + t * (kRows / group) + token;
+  const int query = item.head * group + row % group;
+  uint16_t* out = (uint16_t*)a.out[item.rank] + at_token * a.out_stride + (int64_t)query * D + lane * E;
+  const float by = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    if (lane * E + e < D) *reinterpret_cast<uint32_t*>(out + e) = bf16_pair(sum == 0.f ? 0.f : v[e] * by, sum == 0.f ? 0.f : v[e + 1] * by);
+  if (lane == 0 && a.lse[item.rank] != nullptr) a.lse[item.rank][at_token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
 
 template <int DP, bool PAGED>
@@ -485,20 +700,24 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
     }
   }
   if (e != cudaSuccess) return e;
-  const int64_t slots = prompt_slots(a.tokens, a.sequences, 1, 2 * per_tile);
-  const int64_t items = slots * a.kv_heads * a.nranks;
-  // most keys that a tile may see, in tiles
+  Split split;
+  split.slots = prompt_slots(a.tokens, a.sequences, 1, 2 * per_tile);
+  split.items = split.slots * a.kv_heads * a.nranks;
+  split.sums = (float*)(a.ws + kOpScratchOffset);
+  split.parts = 1;
+  // tiles of keys that an item may have
   const int64_t most = div_up(PAGED ? (int64_t)a.max_blocks << a.page_shift : a.tokens, kKeys);
-  Split split = {1, (float*)(a.ws + kOpScratchOffset)};
-  if (items * 2 <= kPromptSplitBlocks) {
-    const int64_t room = kPromptSplitBlocks / items;
-    split.parts = (int)(room < div_up(most, 2) ? room : div_up(most, 2));
-    if (split.parts < 1) split.parts = 1;
+  if (split.items * 2 <= kPromptSplitBlocks) {
+    const int64_t room = kPromptSplitBlocks / split.items, wanted = div_up(most, 2);
+    split.parts = (int)(room < wanted ? room : wanted);
   }
+  const int64_t all = split.items * split.parts;
   PromptArgs copy = a;
   void* params[] = {&copy, &maps, &split};
-  return launch_op(fn, dim3((unsigned)(slots * split.parts), (unsigned)a.kv_heads, (unsigned)a.nranks), kThreads,
-                   Layout<DP>::kShared, stream, params);
+  e = launch_op(fn, dim3((unsigned)(all < blocks ? all : blocks)), kThreads, Layout<DP>::kShared, stream, params);
+  if (e != cudaSuccess || split.parts == 1) return e;
+  void* join_params[] = {&copy, &split};
+  return launch_op((const void*)prompt_join_kernel<DP, PAGED>, dim3((unsigned)(split.items * 64)), 128, 0, stream, join_params);
 }
 
 }  // namespace
