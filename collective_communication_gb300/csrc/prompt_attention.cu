@@ -449,8 +449,8 @@ cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
 template <typename Args>
 bool tensor_cores(const Args& a, int64_t k_stride, int64_t v_stride) {
   const int64_t most = (int64_t)1 << 38;
-  return a.dtype != 0 && a.head_dim <= 128 && a.q_heads / a.kv_heads <= 128 && a.q_stride < most && k_stride < most &&
-         v_stride < most;
+  return a.dtype != 0 && a.head_dim <= 128 && a.q_heads / a.kv_heads <= 128 && a.q_stride < most && a.out_stride < most &&
+         k_stride < most && v_stride < most;
 }
 
 }  // namespace

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
       if (!(fine = wait_warp(&ds_ready, j & 1, dead))) break;
       fence_after();
       if (more && !(fine = value(j + 1))) break;
-      weights_by_rows<L::kSlab, 32>(lead, dq_at, s_at + (j & 1) * 128, k_at + j % KS * L::kBytes, steps * 16, j > 0);
+      weights_by_rows<32>(lead, dq_at, s_at + (j & 1) * 128, k_at + j % KS * L::kBytes, steps * 16, j > 0, L::kSlab);
       commit(lead, &k_empty[j % KS]);
       if (!more) commit(lead, &dq_full);
     }
@@ -396,11 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       const bool more = i + 1 < to;
       if (!(fine = wait_warp(&p_ready, n & 1, dead))) break;
       fence_after();
-      weights_by_rows<L::kSlab, 32>(lead, dv_at, s_at, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, n > 0);
+      weights_by_rows<32>(lead, dv_at, s_at, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, n > 0, L::kSlab);
       if (more && !(fine = score(i + 1))) break;
       if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
       fence_after();
-      weights_by_rows<L::kSlab, 32>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, n > 0);
+      weights_by_rows<32>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, n > 0, L::kSlab);
       commit(lead, &empty[stage]);
       if (!more) commit(lead, &done);
       if (more) value(i + 1);

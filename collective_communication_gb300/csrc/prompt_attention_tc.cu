@@ -42,19 +42,29 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;  // two softmax warpgroups, and one of which a warp copies and one issues products
-// Registers: 384 threads start with 168 each, the third warpgroup leaves 96 of its own to the two others.
-constexpr int kFewRegisters = 72, kManyRegisters = 216;
-static_assert(kFewRegisters + 2 * kManyRegisters <= 3 * 168, "no more than the block was launched with");
+// Where keys and values are, and how they are copied: dense, in pages by TMA, or in
+// pages by the lanes of a fourth warpgroup. TMA takes a box or two a page: with pages of
+// fewer than 8 tokens a tile's boxes took longer to issue than its products to run
+// (chunks of 2048 tokens of the largest case, 6.2 GB of copies: pages of 1, 4, 16 and 64
+// tokens 3170, 932, 447 and 350 us by TMA in boxes of 64 elements, 403 us by lanes).
+enum Form { kDense, kPages, kLanes };
+// Two softmax warpgroups, one of which each warp has a part of its own, and the one that
+// copies keys and values. The registers that a block starts with (168 a thread of 384,
+// 128 of 512) are shared out anew: what the others leave, the softmax takes.
+template <int FORM>
+struct Threads {
+  static constexpr int kCount = FORM == kLanes ? 512 : 384, kStart = FORM == kLanes ? 128 : 168;
+  static constexpr int kFew = FORM == kLanes ? 48 : 72, kMany = FORM == kLanes ? 208 : 216;
+  static_assert(kFew * (kCount / 128 - 2) + 2 * kMany <= kStart * (kCount / 128), "no more than the block was launched with");
+};
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kCopyWarp = 8, kProductWarp = 9, kItemWarp = 10;
+constexpr int kCopyWarp = 8, kProductWarp = 9, kItemWarp = 10, kStoreWarp = 11, kCacheWarp = 12;
 constexpr int kItemSlots = 4, kLostSlots = 8;
 constexpr int kNextItem = kOpCounters - 1, kDoneBlocks = kOpCounters - 2;  // counters of the workspace
-constexpr int kNotWanted = INT32_MIN;  // for a page number: a box past the keys
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Maps {
-  CUtensorMap q[kMaxRanks], k[kMaxRanks], v[kMaxRanks];
+  CUtensorMap q[kMaxRanks], k[kMaxRanks], v[kMaxRanks], out[kMaxRanks];  // k, v: of dense keys
 };
 
 template <int DP>
@@ -87,7 +97,7 @@ struct Item {
 };
 
 // Item number n in order; false if there is none (a whole warp).
-template <bool PAGED>
+template <int FORM>
 __device__ __forceinline__ bool find_item(const PromptArgs& a, const Split& split, int64_t n, Item* item) {
   const int per_tile = kRows / (a.q_heads / a.kv_heads);
   item->part = (int)(n % split.parts);
@@ -101,7 +111,7 @@ __device__ __forceinline__ bool find_item(const PromptArgs& a, const Split& spli
   PromptSequence seq;
   int pair;
   if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, slot, &seq, &pair)) return false;
-  if (PAGED) cached_sequence(a, &seq);
+  if (FORM != kDense) cached_sequence(a, &seq);
   const int token0 = pair * 2 * per_tile;  // of the sequence
   item->sequence = seq.index;
   item->keys = seq.keys;
@@ -124,15 +134,15 @@ __device__ __forceinline__ bool find_item(const PromptArgs& a, const Split& spli
   return true;
 }
 
-template <int DP, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_constant__ PromptArgs a,
+template <int DP, int FORM>
+__global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(const __grid_constant__ PromptArgs a,
                                                                 const __grid_constant__ Maps maps,
                                                                 const __grid_constant__ Split split) {
   using L = Layout<DP>;
   constexpr int NS = L::kStages, NQ = L::kQueries;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (shared_address(raw) & 1023));
-  __shared__ uint64_t q_full[NQ], q_empty[NQ], full[NS], empty[NS], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2],
+  __shared__ uint64_t q_full[NQ], q_empty[NQ], full[NS], empty[NS], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], out_ready[2],
       item_full[kItemSlots], item_empty[kItemSlots];
   __shared__ Item items[kItemSlots];
   __shared__ uint32_t tmem_at, lost[kLostSlots][4];
@@ -143,10 +153,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
     dead_flag = 0;
     for (int i = 0; i < NQ; i++) {
       barrier_init(&q_full[i], 1);
-      barrier_init(&q_empty[i], 4);  // the warps that store a tile's results by way of its queries' place
+      barrier_init(&q_empty[i], 1);
     }
     for (int i = 0; i < NS; i++) {
-      barrier_init(&full[i], 1);
+      barrier_init(&full[i], FORM == kLanes ? 4 : 1);
       barrier_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; i++) {
@@ -155,18 +165,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       barrier_init(&p_full[i], kRows);
       barrier_init(&o_full[i], 1);
       barrier_init(&o_free[i], kRows);
+      barrier_init(&out_ready[i], kRows);
     }
     for (int i = 0; i < kItemSlots; i++) {
       barrier_init(&item_full[i], 1);
-      barrier_init(&item_empty[i], 10);  // the warps that read it: copies, products, eight of the softmax
+      barrier_init(&item_empty[i], FORM == kLanes ? 15 : 11);  // the warps that read it: all but the one that writes it
     }
     barriers_ready();
   }
   if (warp == kCopyWarp && lane == 0) {  // the descriptors of the first item
     const int first = (int)(blockIdx.x / split.parts % (a.kv_heads * a.nranks)) / a.kv_heads;
     prefetch_map(&maps.q[first]);
-    prefetch_map(&maps.k[first]);
-    prefetch_map(&maps.v[first]);
+    prefetch_map(&maps.out[first]);
+    if (FORM != kLanes) {
+      prefetch_map(&maps.k[first]);
+      prefetch_map(&maps.v[first]);
+    }
   }
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
@@ -178,9 +192,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
   uint8_t* const ring = smem + NQ * L::kTile;
   const int group = a.q_heads / a.kv_heads, D = a.head_dim;
   const int per_tile = kRows / group;  // tokens of a tile
+  // a tile of keys is slab by slab, or where a box holds whole rows of pages, eight rows of both slabs after one another
+  const bool grouped = FORM == kPages && DP == 128 && D == DP;
+  const uint32_t kv_slab = grouped ? kGroup : L::kSlab, kv_group = grouped ? kGroup * (DP / 64) : kGroup;
   const int steps = (D + 15) / 16;
 
-  if (warp >= kCopyWarp) give_registers<kFewRegisters>();
+  if (warp >= kCopyWarp) give_registers<Threads<FORM>::kFew>();
   if (warp == kItemWarp) {
     uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
     const int64_t all = split.items * split.parts;
@@ -189,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       Item item;
       const bool more = n < all;
       if (!more) item.there = 0;
-      if (!more || find_item<PAGED>(a, split, n, &item)) {
+      if (!more || find_item<FORM>(a, split, n, &item)) {
         if (!wait_warp(&item_empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, dead)) break;
         if (lane == 0) {
           items[i % kItemSlots] = item;
@@ -215,77 +232,66 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       const Item& item = items[i % kItemSlots];
       const int there = uniform(item.there);
       if (!there) break;
-      const int rank = uniform(item.rank), head = uniform(item.head), first = uniform(item.first), keys = uniform(item.keys),
-                begin = uniform(item.begin), end = uniform(item.end), sequence = uniform(item.sequence),
-                before = uniform(item.before);
+      const int rank = uniform(item.rank), head = uniform(item.head), first = uniform(item.first), begin = uniform(item.begin),
+                end = uniform(item.end), keys = uniform(item.keys),
+                base = first - uniform(item.before);  // of the sequence, if its keys are dense
+      const int32_t* const row_pages = a.table + uniform(item.sequence) * a.table_stride;
       const int last[2] = {uniform(item.last[0]), uniform(item.last[1])};
       __syncwarp();
       if (lane == 0) arrive(&item_empty[i % kItemSlots]);
-      const CUtensorMap *const map_q = &maps.q[rank], *const map_k = &maps.k[rank], *const map_v = &maps.v[rank];
       auto query = [&](int t) {
         const int at = queries % NQ;
         if (!wait_warp(&q_empty[at], (queries / NQ & 1) ^ 1, dead)) return false;
         if (lane == 0) {
           arrive_expect(&q_full[at], (uint32_t)(per_tile * group * 128 * (DP / 64)));
           for (int h = 0; h < DP / 64; h++)
-            copy_3d(smem + at * L::kTile + h * L::kSlab, map_q, h * 64, head * group, first + t * per_tile, &q_full[at]);
+            copy_3d(smem + at * L::kTile + h * L::kSlab, &maps.q[rank], h * 64, head * group, first + t * per_tile, &q_full[at]);
         }
         queries++;
         return true;
       };
       bool fine = true;
       if (last[0] > begin) fine = query(0);
-      const int base = first - before;  // of the sequence, if its keys are dense
-      // pages of a tile's boxes, lane by lane, read a tile ahead
-      const int box = PAGED ? min(kKeys, 1 << a.page_shift) : kKeys, boxes = kKeys / box;
-      int page[4], ahead[4];
-      auto pages_of = [&](int j) {
-#pragma unroll
-        for (int x = 0; x < 4; x++) {
-          const int b = lane + 32 * x, key = j * kKeys + b * box;
-          ahead[x] = kNotWanted;
-          if (b < boxes && j < end && key < keys) ahead[x] = a.table[sequence * a.table_stride + (key >> a.page_shift)];
-        }
+      if (FORM == kLanes) {
+        if (fine && last[1] > begin) fine = query(1);
+        if (!fine) break;
+        continue;
+      }
+      // a page, or 128 tokens of a larger one, is a lane's; read a tile ahead, INT32_MIN where there is no key
+      const int box = FORM == kPages ? min(kKeys, 1 << a.page_shift) : kKeys;
+      auto page_of = [&](int j) {
+        const int key = j * kKeys + lane * box;
+        return FORM == kPages && lane * box < kKeys && j < end && key < keys ? row_pages[key >> a.page_shift] : INT32_MIN;
       };
-      if (PAGED) pages_of(begin);
+      int next_page = page_of(begin);
       for (int j = begin; j < end && fine; j++) {
-        if (PAGED) {
-#pragma unroll
-          for (int x = 0; x < 4; x++) page[x] = ahead[x];
-          pages_of(j + 1);
-        }
-        for (int which = 0; which < 2 && fine; which++) {
+        const int page = next_page;
+        next_page = page_of(j + 1);
+        const bool copied = (unsigned)page < (unsigned)a.num_pages;
+        const int count = FORM == kPages ? __popc(__ballot_sync(~0u, copied)) : 0;
+        for (int which = 0; which < 2; which++) {
           if (!(fine = wait_warp(&empty[stage], phase ^ 1, dead))) break;
-          uint8_t* to = ring + stage * L::kTile;
-          const CUtensorMap* map = which == 0 ? map_k : map_v;
-          if (!PAGED) {
+          uint8_t* const to = ring + stage * L::kTile;
+          const CUtensorMap* const map = which == 0 ? &maps.k[rank] : &maps.v[rank];
+          if (FORM == kDense) {
             if (lane == 0) {
               arrive_expect(&full[stage], L::kTile);
               for (int h = 0; h < DP / 64; h++)
                 copy_3d(to + h * L::kSlab, map, h * 64, head, base + j * kKeys, &full[stage]);
             }
           } else {
-            // a box a page (or 128 tokens of a larger one); boxes past the keys, and pages that are none, are not copied
-            int count = 0;
-#pragma unroll
-            for (int x = 0; x < 4; x++) count += __popc(__ballot_sync(~0u, (unsigned)page[x] < (unsigned)a.num_pages));
             if (which == 0) {
+              const bool none = page != INT32_MIN && !copied;
               uint32_t bad[4] = {0, 0, 0, 0};
-              bool none = false;
-#pragma unroll
-              for (int x = 0; x < 4; x++) none |= page[x] != kNotWanted && (unsigned)page[x] >= (unsigned)a.num_pages;
               if (__any_sync(~0u, none)) {
                 if (none) op_report(a.ws, kErrCapacity);
-                for (int x = 0; x < 4; x++) {
-                  const bool mine = page[x] != kNotWanted && (unsigned)page[x] >= (unsigned)a.num_pages;
 #pragma unroll
-                  for (int r = 0; r < 4; r++) {  // rows of the tile that such a page would have filled
-                    uint32_t bits = 0;
-                    if (mine)
-                      for (int y = (lane + 32 * x) * box; y < (lane + 32 * x + 1) * box; y++)
-                        if (y >> 5 == r) bits |= 1u << (y & 31);
-                    bad[r] |= __reduce_or_sync(~0u, bits);
-                  }
+                for (int r = 0; r < 4; r++) {  // rows of the tile that such a page would have filled
+                  uint32_t bits = 0;
+                  if (none)
+                    for (int y = lane * box; y < (lane + 1) * box; y++)
+                      if (y >> 5 == r) bits |= 1u << (y & 31);
+                  bad[r] = __reduce_or_sync(~0u, bits);
                 }
               }
               if (lane == 0) {
@@ -296,13 +302,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             __syncwarp();
             if (lane == 0) arrive_expect(&full[stage], (uint32_t)(count * box * 128 * (DP / 64)));
             __syncwarp();
-#pragma unroll
-            for (int x = 0; x < 4; x++) {
-              if ((unsigned)page[x] >= (unsigned)a.num_pages) continue;
-              const int b = lane + 32 * x;
-              for (int h = 0; h < DP / 64; h++)
-                copy_3d(to + h * L::kSlab + b * box * 128, map, h * 64, (j * kKeys + b * box) & ((1 << a.page_shift) - 1),
-                        page[x] * a.kv_heads + head, &full[stage]);
+            if (copied) {
+              const int off = (j * kKeys + lane * box) & ((1 << a.page_shift) - 1), plane = page * a.kv_heads + head;
+              if (grouped)
+                copy_4d(to + lane * box * (128 * (DP / 64)), map, 0, 0, 0, ((plane << a.page_shift) + off) >> 3, &full[stage]);
+              else
+                for (int h = 0; h < DP / 64; h++)
+                  copy_3d(to + h * L::kSlab + lane * box * 128, map, h * 64, off, plane, &full[stage]);
             }
             __syncwarp();
           }
@@ -310,12 +316,126 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             stage = 0;
             phase ^= 1;
           }
-          if (j == begin && which == 0 && last[1] > begin) fine = query(1);
+          if (j == begin && which == 0 && last[1] > begin && !(fine = query(1))) break;
         }
       }
       if (!fine) break;
       seen += end - begin;
     }
+  } else if (FORM == kLanes && warp >= kCacheWarp) {
+    // Keys and values of a cache's pages, 32 rows of a tile a warp, 16 bytes a lane, in the
+    // places where TMA would put them. Rows of no key, or of a page that is none, are 0; so
+    // are elements past the head.
+    constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // lanes of a row, rows of an instruction
+    const int mine = (warp - kCacheWarp) * 32, piece = lane % kPieces;
+    const bool inside = piece * 8 < D;
+    // (rows of an instruction differ in the bits of a row's swizzle below those of its first one)
+    const uint32_t to = shared_address(ring) + (piece >> 3) * L::kSlab + (mine + lane / kPieces) * 128 +
+                        (((piece & 7) ^ (lane / kPieces)) << 4);
+    int stage = 0, oldest = 0, pending = 0, seen = 0;  // pending: tiles from `oldest` on whose copies are under way
+    uint32_t phase = 0;
+    auto hand_over = [&] {  // the oldest of them, which has come in
+      stores_to_products();
+      __syncwarp();
+      if (lane == 0) arrive(&full[oldest]);
+      oldest = oldest + 1 == NS ? 0 : oldest + 1;
+      pending--;
+    };
+    auto drain = [&] {
+      if (pending == 2) {
+        copies_done<1>();
+        hand_over();
+      }
+      if (pending == 1) {
+        copies_done<0>();
+        hand_over();
+      }
+    };
+    for (int i = 0;; i++) {
+      if (pending > 0 && !__all_sync(~0u, ended(&item_full[i % kItemSlots], i / kItemSlots & 1))) drain();
+      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      const Item& item = items[i % kItemSlots];
+      const int there = uniform(item.there);
+      if (!there) break;
+      const int head = uniform(item.head), keys = uniform(item.keys), begin = uniform(item.begin), end = uniform(item.end);
+      const int32_t* row_pages = a.table + uniform(item.sequence) * a.table_stride;
+      const uint16_t *const k = (const uint16_t*)a.k[uniform(item.rank)], *const v = (const uint16_t*)a.v[uniform(item.rank)];
+      __syncwarp();
+      if (lane == 0) arrive(&item_empty[i % kItemSlots]);
+      auto page_of = [&](int j) {  // of the lane's row, a tile ahead
+        const int key = j * kKeys + mine + lane;
+        return j < end && key < keys ? row_pages[key >> a.page_shift] : 0;
+      };
+      bool fine = true;
+      int next_page = page_of(begin);
+      for (int j = begin; j < end && fine; j++) {
+        const int key = j * kKeys + mine + lane, page = next_page;
+        next_page = page_of(j + 1);
+        const bool there = (unsigned)page < (unsigned)a.num_pages;
+        const int row = key < keys && there
+                            ? ((page * a.kv_heads + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))
+                            : -1;
+        const uint32_t bad = __ballot_sync(~0u, key < keys && !there);
+        if (bad != 0 && lane == 0) op_report(a.ws, kErrCapacity);
+        for (int which = 0; which < 2; which++) {
+          if (!__all_sync(~0u, ended(&empty[stage], phase ^ 1))) {
+            drain();  // nobody would make room for what is not there yet
+            if (!(fine = wait_warp(&empty[stage], phase ^ 1, dead))) break;
+          }
+          if (which == 0 && lane == 0) lost[(seen + j - begin) % kLostSlots][warp - kCacheWarp] = bad;
+          const uint16_t* const from = (which == 0 ? k : v) + piece * 8;
+          const uint32_t place = to + stage * L::kTile;
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+            const int at = __shfl_sync(~0u, row, r0 + lane / kPieces);
+            copy_16((place + r0 * 128) ^ ((r0 & 7) << 4), from + (int64_t)max(at, 0) * D, at >= 0 && inside ? 16 : 0);
+          }
+          copies_of_a_tile();
+          if (++pending == 3) {
+            copies_done<2>();
+            hand_over();
+          }
+          if (++stage == NS) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!fine) break;
+      seen += end - begin;
+    }
+    drain();
+  } else if (warp == kStoreWarp) {
+    int queries = 0, results[2] = {0, 0};
+    for (int i = 0;; i++) {
+      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      const Item& item = items[i % kItemSlots];
+      const int there = uniform(item.there);
+      if (!there) break;
+      const int rank = uniform(item.rank), head = uniform(item.head), first = uniform(item.first), begin = uniform(item.begin);
+      const int last[2] = {uniform(item.last[0]), uniform(item.last[1])},
+                tokens[2] = {uniform(item.tokens[0]), uniform(item.tokens[1])};
+      __syncwarp();
+      if (lane == 0) arrive(&item_empty[i % kItemSlots]);
+      bool fine = true;
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        if (!fine || last[t] <= begin) continue;
+        const int at = queries++ % NQ;
+        if (!(fine = wait_warp(&out_ready[t], results[t]++ & 1, dead))) break;
+        if (lane == 0) {
+          if (tokens[t] == per_tile && split.parts == 1) {
+            for (int h = 0; h < DP / 64 && h * 64 < D; h++)
+              store_3d(&maps.out[rank], h * 64, head * group, first + t * per_tile, smem + at * L::kTile + h * L::kSlab);
+            stores_read();
+          }
+          arrive(&q_empty[at]);
+        }
+        __syncwarp();
+      }
+      if (!fine) break;
+    }
+    if (lane == 0) stores_written();
   } else if (warp == kProductWarp) {
     const uint32_t lead = elect_one();
     const int n_out = steps * 16;
@@ -338,21 +458,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       for (int t = 0; t < 2; t++) q_slot[t] = last[t] > begin ? queries++ : 0;
       // the S of a key tile for a tile of rows that sees it
       auto score = [&](int t, uint32_t k_at) {
-        rows_by_rows<DP / 16, L::kSlab>(lead, s_at[t], q_at + (uint32_t)(q_slot[t] % NQ) * L::kTile, k_at, kKeys, steps);
+        rows_by_rows<DP / 16, L::kSlab>(lead, s_at[t], q_at + (uint32_t)(q_slot[t] % NQ) * L::kTile, k_at, kKeys, steps, kv_slab, kv_group);
         commit(lead, &s_full[t]);
       };
       // V of key tile j is there; rows with no key would be multiplied by weights of 0, and may hold a NaN
       auto values = [&](int j, int stage, uint32_t phase) {
         if (!wait_warp(&full[stage], phase, dead)) return false;
         const int left = keys - j * kKeys;
-        const uint32_t* holes_of = lost[(seen + j - begin) % kLostSlots];
-        const bool holes = PAGED && __any_sync(~0u, lane < 4 && holes_of[lane & 3] != 0);
-        if (left < kKeys || holes) {
+        const uint32_t* const holes_of = lost[(seen + j - begin) % kLostSlots];
+        const bool holes = FORM == kPages && __any_sync(~0u, lane < 4 && holes_of[lane & 3] != 0);
+        if (FORM != kLanes && (left < kKeys || holes)) {
           for (int r = lane; r < kKeys; r += 32)
             if (r >= left || (holes && (holes_of[r >> 5] >> (r & 31) & 1)))
               for (int h = 0; h < DP / 64; h++)
                 for (int c = 0; c < 8; c++)
-                  *reinterpret_cast<uint4*>(ring + stage * L::kTile + h * L::kSlab + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(ring + stage * L::kTile + h * kv_slab + (r >> 3) * kv_group + (r & 7) * 128 + c * 16) =
+                      make_uint4(0, 0, 0, 0);
           stores_to_products();
           __syncwarp();
         }
@@ -390,10 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
             if (j == begin && results[t] > 0 && !(fine = wait_warp(&o_free[t], (results[t] - 1) & 1, dead))) break;
             if (!(fine = wait_warp(&p_half[t], walked[t] & 1, dead))) break;
             fence_after();
-            weights_by_rows<L::kSlab, 0, 0, 4>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > begin);
+            weights_by_rows<0, 0, 4>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > begin, kv_slab, kv_group);
             if (!(fine = wait_warp(&p_full[t], walked[t] & 1, dead))) break;
             fence_after();
-            weights_by_rows<L::kSlab, 0, 4, 8>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, true);
+            weights_by_rows<0, 4, 8>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
             walked[t]++;
             if (j + 1 == last[t]) {
               commit(lead, &o_full[t]);
@@ -421,10 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       seen += end - begin;
     }
   } else if (warp < kCopyWarp) {
-    take_registers<kManyRegisters>();
+    take_registers<Threads<FORM>::kMany>();
     const int t = warp >> 2;
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
-    const int row = threadIdx.x & 127, token = row / group;
+    const int row = threadIdx.x & 127, token = row / group, in_group = row % group;
     // of a negative scale or none, the scores are turned or cleared first, so that the largest is the one that counts
     const float scale2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
     const uint32_t turn = a.scale < 0.f ? 0x80000000u : 0u, keep_bits = a.scale == 0.f ? 0u : ~0u;
@@ -436,10 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
       const int begin = item.begin, end = item.end, last = item.last[t];
       const int q_slot = (queries + (t == 1 && item.last[0] > begin)) % NQ;
       queries += (item.last[0] > begin) + (item.last[1] > begin);
-      const bool mine = token < item.tokens[t];
+      const int tokens = item.tokens[t];
+      const bool mine = token < tokens;
       // rows that are none see what the tile's first row sees: they hold anything, and nobody reads them
       const int sees = min(item.before + t * per_tile + (mine ? token : 0) + 1, item.keys);
-      const int query = item.head * group + row % group, rank = item.rank, part = item.part;
+      const int query = item.head * group + in_group, rank = item.rank, part = item.part;
       const int64_t at_token = (int64_t)item.first + t * per_tile + token, index = item.index;
       __syncwarp();
       if (lane == 0) arrive(&item_empty[i % kItemSlots]);
@@ -461,13 +583,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
           for (int c = 0; c < kKeys; c++) s[c] = (s[c] ^ turn) & keep_bits;
         }
         const uint32_t* holes_of = lost[(seen + j - begin) % kLostSlots];
-        const bool holes = PAGED && (holes_of[0] | holes_of[1] | holes_of[2] | holes_of[3]) != 0;
+        const bool holes = FORM != kDense && (holes_of[0] | holes_of[1] | holes_of[2] | holes_of[3]) != 0;
         if ((j + 1) * kKeys > least || holes) {
           const int upto = sees - j * kKeys;
 #pragma unroll
           for (int c = 0; c < kKeys; c++) {
             bool there = c < upto;
-            if (PAGED && holes) there = there && !(holes_of[c >> 5] >> (c & 31) & 1);
+            if (FORM != kDense && holes) there = there && !(holes_of[c >> 5] >> (c & 31) & 1);
             if (!there) s[c] = 0xff800000u;
           }
         }
@@ -534,62 +656,59 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
         fence_after();
       }
       const float by = l == 0.f ? 0.f : 1.f / l;
-      uint16_t* out = (uint16_t*)a.out[rank] + at_token * a.out_stride + (int64_t)query * D;
-      float* sums = split.sums + (index * split.parts + part) * kPartFloats<DP> + t * kRows * (DP + 2);
+      uint16_t* const out = (uint16_t*)a.out[rank] + at_token * a.out_stride + (int64_t)query * D;
+      float* const sums = split.sums + (index * split.parts + part) * kPartFloats<DP> + t * kRows * (DP + 2);
       if (!some) {
         for (int c = 0; c < D && mine && split.parts == 1; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
-      } else if (split.parts == 1) {
-        // A warp's 32 rows go by way of their queries' place in shared memory, with 16-byte
-        // pieces swizzled, so that stores cover whole lines: a row a thread took 6400 cycles
-        // a tile for the addresses of its 32 lines a store.
-        uint8_t* const place = smem + q_slot * L::kTile + row * 128;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_load32(o_at[t] + quarter + c, o);
-          loads_done();
+      } else {
+        uint32_t o[DP];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            Pack8<uint16_t> x;
-            float v[8];
+        for (int c = 0; c < DP; c += 32) tmem_load32(o_at[t] + quarter + c, o + c);
+        loads_done();
+        fence_before();
+        arrive(&o_free[t]);
+        if (split.parts > 1) {  // a part of the keys: O as it is
+          if (mine) {
 #pragma unroll
-            for (int k = 0; k < 8; k++) v[k] = l == 0.f ? 0.f : __uint_as_float(o[i + k]) * by;
-            x.narrow(v);
-            const int piece = (c + i) / 8;
-            *reinterpret_cast<uint4*>(place + (piece >> 3) * L::kSlab + (((piece & 7) ^ (row & 7)) << 4)) = x.u;
+            for (int c = 0; c < DP; c += 4)
+              if (c < D) *reinterpret_cast<uint4*>(sums + row * DP + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+          }
+        } else {
+          // to the queries' place in shared memory, from where the store warp's TMA takes a
+          // whole tile; a warp stores its rows of one that the sequence does not fill itself
+          if (l == 0.f) {  // no weight at all: 0, whatever the values are
+#pragma unroll
+            for (int c = 0; c < DP; c++) o[c] = 0;
+          }
+          uint8_t* const place = smem + q_slot * L::kTile + row * 128;
+          const F2 by_pair = f2(by, by);
+#pragma unroll
+          for (int c = 0; c < DP; c += 8) {
+            uint4 x;
+            uint32_t* to = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+              const float2 v = unpack(mul2(f2(__uint_as_float(o[c + 2 * k]), __uint_as_float(o[c + 2 * k + 1])), by_pair));
+              to[k] = bf16_pair(v.x, v.y);
+            }
+            *reinterpret_cast<uint4*>(place + (c >> 6) * L::kSlab + (((c >> 3 & 7) ^ (row & 7)) << 4)) = x;
+          }
+          stores_to_products();
+          if (tokens != per_tile) {
+            __syncwarp();
+            constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // lanes of a row, rows of an instruction
+            const int piece = lane % kPieces;
+            const uint8_t* from = smem + q_slot * L::kTile + (row - lane) * 128 + (piece >> 3) * L::kSlab;
+#pragma unroll 4
+            for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+              const int r = r0 + lane / kPieces;
+              uint16_t* const to = (uint16_t*)__shfl_sync(~0u, mine ? (unsigned long long)out : 0ull, r);
+              const uint4 x = *reinterpret_cast<const uint4*>(from + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+              if (to != nullptr && piece * 8 < D) *reinterpret_cast<uint4*>(to + piece * 8) = x;
+            }
           }
         }
-        fence_before();
-        arrive(&o_free[t]);
-        __syncwarp();
-        constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // lanes of a row, rows of an instruction
-        const int piece = lane % kPieces;
-        const uint8_t* from = smem + q_slot * L::kTile + (row - lane) * 128 + (piece >> 3) * L::kSlab;
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
-          const int r = r0 + lane / kPieces;
-          uint16_t* const to = (uint16_t*)__shfl_sync(~0u, mine ? (unsigned long long)out : 0ull, r);
-          const uint4 x = *reinterpret_cast<const uint4*>(from + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
-          if (to != nullptr && piece * 8 < D) *reinterpret_cast<uint4*>(to + piece * 8) = x;
-        }
-      } else {  // a part of the keys: O as it is
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_load32(o_at[t] + quarter + c, o);
-          loads_done();
-          if (!mine) continue;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            if (c + i < D) *reinterpret_cast<uint4*>(sums + row * DP + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        }
-        fence_before();
-        arrive(&o_free[t]);
-      }
-      if (some) {
-        stores_to_products();  // copies write there next
-        __syncwarp();
-        if (lane == 0) arrive(&q_empty[q_slot]);
+        arrive(&out_ready[t]);
       }
       if (mine && split.parts > 1) {
         sums[kRows * DP + row] = m;
@@ -616,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_tc_kernel(const __grid_con
 }
 
 // The parts of a row's keys, in their order; a warp a row, 16 parts' loads under way.
-template <int DP, bool PAGED>
+template <int DP, int FORM>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a,
                                                           const __grid_constant__ Split split) {
   constexpr int E = DP / 32;  // elements of a lane
@@ -625,7 +744,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, r = (int)(blockIdx.x % 64) * 4 + (threadIdx.x >> 5), t = r / kRows, row = r % kRows;
   const int group = a.q_heads / a.kv_heads, D = a.head_dim, token = row / group;
   Item item;
-  if (!find_item<PAGED>(a, split, (int64_t)(blockIdx.x / 64) * split.parts, &item) || token >= item.tokens[t]) return;
+  if (!find_item<FORM>(a, split, (int64_t)(blockIdx.x / 64) * split.parts, &item) || token >= item.tokens[t]) return;
   const float* sums = split.sums + item.index * split.parts * kPartFloats<DP> + t * kRows * (DP + 2);
   float m[kPromptSplitBlocks / 32 + 1], top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -680,23 +799,27 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   if (lane == 0 && a.lse[item.rank] != nullptr) a.lse[item.rank][at_token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
 
-template <int DP, bool PAGED>
+template <int DP, int FORM>
 cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   const int group = a.q_heads / a.kv_heads, per_tile = kRows / group, D = a.head_dim;
-  const void* fn = (const void*)prompt_tc_kernel<DP, PAGED>;
+  const void* fn = (const void*)prompt_tc_kernel<DP, FORM>;
   int blocks = 0;
-  cudaError_t e = resident_blocks(fn, kThreads, Layout<DP>::kShared, &blocks);
+  cudaError_t e = resident_blocks(fn, Threads<FORM>::kCount, Layout<DP>::kShared, &blocks);
   if (e != cudaSuccess) return e;
   static thread_local Maps maps;
   for (int r = 0; r < a.nranks && e == cudaSuccess; r++) {
     e = make_map(&maps.q[r], a.q[r], D, a.q_heads, a.tokens, D * 2, a.q_stride * 2, group, per_tile);
+    if (e == cudaSuccess) e = make_map(&maps.out[r], a.out[r], D, a.q_heads, a.tokens, D * 2, a.out_stride * 2, group, per_tile);
     for (int which = 0; which < 2 && e == cudaSuccess; which++) {
       CUtensorMap* map = which == 0 ? &maps.k[r] : &maps.v[r];
       const void* base = which == 0 ? a.k[r] : a.v[r];
-      const int page = 1 << a.page_shift;
-      e = PAGED ? make_map(map, base, D, page, (int64_t)a.num_pages * a.kv_heads, D * 2, (int64_t)page * D * 2,
-                           page < kKeys ? page : kKeys, 1)
-                : make_map(map, base, D, a.kv_heads, a.tokens, D * 2, (which == 0 ? a.k_stride : a.v_stride) * 2, 1, kKeys);
+      const int64_t page = (int64_t)1 << a.page_shift, planes = (int64_t)a.num_pages * a.kv_heads, box = page < kKeys ? page : kKeys;
+      if (FORM == kDense)
+        e = make_map(map, base, D, a.kv_heads, a.tokens, D * 2, (which == 0 ? a.k_stride : a.v_stride) * 2, 1, kKeys);
+      else if (FORM == kPages && DP == 128 && D == DP)
+        e = make_grouped_map(map, base, D, planes * page, (int)box / 8);
+      else if (FORM == kPages)
+        e = make_map(map, base, D, page, planes, D * 2, page * D * 2, (int)box, 1);
     }
   }
   if (e != cudaSuccess) return e;
@@ -706,7 +829,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   split.sums = (float*)(a.ws + kOpScratchOffset);
   split.parts = 1;
   // tiles of keys that an item may have
-  const int64_t most = div_up(PAGED ? (int64_t)a.max_blocks << a.page_shift : a.tokens, kKeys);
+  const int64_t most = div_up(FORM != kDense ? (int64_t)a.max_blocks << a.page_shift : a.tokens, kKeys);
   if (split.items * 2 <= kPromptSplitBlocks) {
     const int64_t room = kPromptSplitBlocks / split.items, wanted = div_up(most, 2);
     split.parts = (int)(room < wanted ? room : wanted);
@@ -714,18 +837,19 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   const int64_t all = split.items * split.parts;
   PromptArgs copy = a;
   void* params[] = {&copy, &maps, &split};
-  e = launch_op(fn, dim3((unsigned)(all < blocks ? all : blocks)), kThreads, Layout<DP>::kShared, stream, params);
+  e = launch_op(fn, dim3((unsigned)(all < blocks ? all : blocks)), Threads<FORM>::kCount, Layout<DP>::kShared, stream, params);
   if (e != cudaSuccess || split.parts == 1) return e;
   void* join_params[] = {&copy, &split};
-  return launch_op((const void*)prompt_join_kernel<DP, PAGED>, dim3((unsigned)(split.items * 64)), 128, 0, stream, join_params);
+  return launch_op((const void*)prompt_join_kernel<DP, FORM>, dim3((unsigned)(split.items * 64)), 128, 0, stream, join_params);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention_tc(const PromptArgs& a, cudaStream_t stream) {
-  const bool paged = a.table != nullptr;
-  if (a.head_dim <= 64) return paged ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
-  return paged ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+  const bool small = a.head_dim <= 64;
+  if (a.table == nullptr) return small ? launch<64, kDense>(a, stream) : launch<128, kDense>(a, stream);
+  if (a.page_shift >= 3) return small ? launch<64, kPages>(a, stream) : launch<128, kPages>(a, stream);
+  return small ? launch<64, kLanes>(a, stream) : launch<128, kLanes>(a, stream);
 }
 
 }  // namespace rar

@@ -42,6 +42,17 @@ __device__ __forceinline__ bool try_wait(uint64_t* b, uint32_t parity) {
   return done != 0;
 }
 
+// try_wait may hold the thread for microseconds before it says no; this does not.
+__device__ __forceinline__ bool ended(uint64_t* b, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(shared_address(b)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 constexpr uint64_t kWaitNs = 2000000000ull;  // no tile takes a thousandth of that
 
 // Waits for the phase of `parity` to end. False once any wait of the block has run
@@ -90,6 +101,34 @@ __device__ __forceinline__ void copy_3d(void* to, const CUtensorMap* m, int x, i
       "l"(m), "r"(x), "r"(y), "r"(z), "r"(shared_address(b))
       : "memory");
 }
+__device__ __forceinline__ void copy_4d(void* to, const CUtensorMap* m, int x, int y, int z, int w, uint64_t* b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          shared_address(to)),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(shared_address(b))
+      : "memory");
+}
+__device__ __forceinline__ void store_3d(const CUtensorMap* m, int x, int y, int z, const void* from) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x), "r"(y),
+               "r"(z), "r"(shared_address(from))
+               : "memory");
+}
+// The thread's stores so far have read shared memory, or have been written as well.
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void stores_written() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// ---- copies of 16 bytes, the last 16 - bytes of them 0 ----
+__device__ __forceinline__ void copy_16(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_of_a_tile() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_done() {  // but for those of the last LEFT tiles
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 // Ordinary stores to shared memory, for products that read it afterwards.
 __device__ __forceinline__ void stores_to_products() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -146,36 +185,42 @@ __device__ __forceinline__ void take_registers() {
 }
 
 // ---- products ----
-// Operands in shared memory are slabs of 64 elements (128 bytes) a row, rows side by
-// side, swizzled by 128 bytes as TMA writes them: groups of eight rows are 1024 bytes.
+// Operands in shared memory are slabs of 64 elements (128 bytes) a row, swizzled by 128
+// bytes as TMA writes them: eight rows are 1024 bytes in a row, `group` bytes lie
+// between them and the next eight, `slab` bytes between slabs. A tile is slab by slab
+// (groups 1024 bytes apart), or eight rows of all slabs after one another.
 // along: the contraction runs along the rows' elements (next 16: 32 bytes on, next 64:
-// the next slab). across: it runs across the rows (next 16: 2048 bytes on), and `next`
-// bytes lie between slabs of 64 results.
-// The upper half of a descriptor is the same for both; the lower one holds the address
-// and the bytes between slabs in units of 16, so a step is an addition to it.
-constexpr uint32_t kOperandHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+// the next slab). across: it runs across the rows (next 16: two groups on), with results
+// along the elements.
+// The upper half of a descriptor holds the group's bytes and is the same for both; the
+// lower one the address and the bytes between slabs in units of 16, so a step is an
+// addition to it.
+constexpr uint32_t kGroup = 1024;
+__device__ __forceinline__ uint32_t operand_high(uint32_t group) { return group >> 4 | 1u << 14 | 2u << 29; }
 __device__ __forceinline__ uint32_t operand_along(uint32_t at) { return at >> 4 | 1u << 16; }
-__device__ __forceinline__ uint32_t operand_across(uint32_t at, uint32_t next) { return at >> 4 | (next >> 4) << 16; }
+__device__ __forceinline__ uint32_t operand_across(uint32_t at, uint32_t slab) { return at >> 4 | (slab >> 4) << 16; }
 // bf16 operands, binary32 sums, 128 rows by n columns (a multiple of 16).
 __device__ __forceinline__ uint32_t product_of(int n, bool right_across) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (right_across ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
 }
 // d (+)= a b over 16 elements, issued by the lane that leads; the whole warp comes here
 // together. a in shared memory, or in tensor memory (two elements a column).
-__device__ __forceinline__ void multiply(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void multiply(uint32_t lead, uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high,
+                                         uint32_t kind, bool add) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
-      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %7};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(kind), "r"((uint32_t)add), "r"(kOperandHigh), "r"(lead)
+      "r"(a), "r"(b), "r"(kind), "r"((uint32_t)add), "r"(a_high), "r"(lead), "r"(b_high)
       : "memory");
 }
-__device__ __forceinline__ void multiply_tmem(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void multiply_tmem(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t b_high, uint32_t kind,
+                                              bool add) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
       "mov.b64 y, {%2, %5};\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(kind), "r"((uint32_t)add), "r"(kOperandHigh), "r"(lead)
+      "r"(a), "r"(b), "r"(kind), "r"((uint32_t)add), "r"(b_high), "r"(lead)
       : "memory");
 }
 // Arrives on b once the leading lane's products so far are done.
@@ -192,23 +237,26 @@ __device__ __forceinline__ void commit(uint32_t lead, uint64_t* b) {
 // to issue and 64 to run. Hence additions to the lower halves only, loops unrolled to
 // MOST, and a warp that stays together, whose numbers the compiler keeps in uniform
 // registers, where the products want them.
-// d = x y^T: 128 rows of x by n rows of y, `steps` times 16 elements along both; SLAB bytes from slab to slab.
+// d = x y^T: 128 rows of x, slab by slab, by n rows of y, `steps` times 16 elements along both.
 template <int MOST, int SLAB>
-__device__ __forceinline__ void rows_by_rows(uint32_t lead, uint32_t d, uint32_t x, uint32_t y, int n, int steps) {
-  const uint32_t kind = product_of(n, false), a = operand_along(x), b = operand_along(y);
+__device__ __forceinline__ void rows_by_rows(uint32_t lead, uint32_t d, uint32_t x, uint32_t y, int n, int steps,
+                                             uint32_t slab = SLAB, uint32_t group = kGroup) {
+  const uint32_t kind = product_of(n, false), a = operand_along(x), b = operand_along(y), high = operand_high(group);
 #pragma unroll
-  for (int k = 0; k < MOST; k++) {
-    const uint32_t on = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
-    if (k < steps) multiply(lead, d, a + on, b + on, kind, k > 0);
-  }
+  for (int k = 0; k < MOST; k++)
+    if (k < steps)
+      multiply(lead, d, a + (((k >> 2) * SLAB + (k & 3) * 32) >> 4), operand_high(kGroup), b + (((k >> 2) * slab + (k & 3) * 32) >> 4),
+               high, kind, k > 0);
 }
 // d (+)= w z: w in tensor memory, 128 rows by 128, the second half GAP columns behind the first; z has as many rows, n elements each.
 // The part of them from step FIRST to LAST.
-template <int SLAB, int GAP, int FIRST = 0, int LAST = 8>
-__device__ __forceinline__ void weights_by_rows(uint32_t lead, uint32_t d, uint32_t w, uint32_t z, int n, bool add) {
-  const uint32_t kind = product_of(n, true), b = operand_across(z, SLAB);
+template <int GAP, int FIRST = 0, int LAST = 8>
+__device__ __forceinline__ void weights_by_rows(uint32_t lead, uint32_t d, uint32_t w, uint32_t z, int n, bool add, uint32_t slab,
+                                                uint32_t group = kGroup) {
+  const uint32_t kind = product_of(n, true), b = operand_across(z, slab), high = operand_high(group);
 #pragma unroll
-  for (int k = FIRST; k < LAST; k++) multiply_tmem(lead, d, w + 8 * k + (k >> 2) * GAP, b + k * (2048 >> 4), kind, add || k > 0);
+  for (int k = FIRST; k < LAST; k++)
+    multiply_tmem(lead, d, w + 8 * k + (k >> 2) * GAP, b + k * (group >> 3), high, kind, add || k > 0);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -219,9 +267,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 }  // namespace tc
 
-// A tensor of three dimensions of 2-byte elements, the innermost dense, for copies of
-// boxes of 64 elements by `rows` by `planes`, swizzled by 128 bytes; zeros outside.
+// TMA descriptors of 2-byte elements, boxes 64 elements wide, swizzled by 128 bytes, zeros outside.
+// Three dimensions, the innermost dense: boxes of 64 by `rows` by `planes`.
 cudaError_t make_map(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t stride1_bytes,
                      int64_t stride2_bytes, int rows, int planes);
+// Dense rows of a multiple of 64 elements, eight by eight: boxes of 64 elements by 8 rows by all slabs by `groups`.
+cudaError_t make_grouped_map(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int groups);
 
 }  // namespace rar
