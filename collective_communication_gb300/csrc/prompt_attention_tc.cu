@@ -59,7 +59,7 @@ struct Threads {
 };
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kCopyWarp = 8, kProductWarp = 9, kItemWarp = 10, kStoreWarp = 11, kCacheWarp = 12;
-constexpr int kItemSlots = 4, kLostSlots = 8;
+constexpr int kItemSlots = 2, kLostSlots = 8;
 constexpr int kNextItem = kOpCounters - 1, kDoneBlocks = kOpCounters - 2;  // counters of the workspace
 constexpr float kLog2e = 1.4426950408889634f;
 
