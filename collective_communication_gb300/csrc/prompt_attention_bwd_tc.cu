@@ -5,8 +5,8 @@
 //   P = 2^(scale log2(e) Q K^T - lse log2(e)),  dS = P (dO V^T - delta),  delta = O . dO
 //   dQ = scale dS K,   dK = scale dS^T Q,   dV = P^T dO
 //
-// Two kernels that both recompute P: one by rows for dQ (three products a tile, and
-// delta, which it leaves for the other), one by keys for dK and dV (four). One kernel
+// Two kernels that both recompute P: one by rows for dQ (three products a tile), one by
+// keys for dK and dV (four); a small one ahead of them works out delta. One kernel
 // with five products would have to add dQ up across blocks, in an order that changes
 // from run to run, or in passes over partial sums of dQ in memory.
 //
@@ -17,10 +17,18 @@
 // came from, and are left operands from there. The keys' kernel has S transposed, keys
 // as rows, so that P^T and dS^T come out as left operands too.
 //
-// Two warpgroups work out the weights, half of the columns each: a thread has 64
-// columns of a row. The products' order keeps the tensor cores busy meanwhile:
+// O is rounded to bf16, and its rounding goes into delta: over few keys, where O is as
+// large as the values, by as much as the result's own rounding. Rows whose whole tile
+// sees one tile of keys take delta from sum P (dO V^T) instead, which is at hand there.
+//
+// Four warpgroups work out the weights, a quarter of the columns each: a thread has 32
+// columns of a row (with two, of 64 columns a thread, the two steps of a tile of keys
+// took 3900 cycles of latency where its products take 2048). The products' order keeps
+// the tensor cores busy meanwhile:
 //   rows:  S(j+1) | dS(j) ready: dP(j+1), dQ += dS(j) K(j) | ...
 //   keys:  P(i) ready: dV += P(i) dO, S(i+1) | dS(i) ready: dK += dS(i) Q, dP(i+1) | ...
+// Blocks stay, one an SM, and take items (a tile of rows, or of keys) from a counter;
+// a warp finds the next one while the last is under way, and its first tiles are copied.
 #include <cstdio>
 
 #include "prompt_attention.cuh"
@@ -32,9 +40,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;  // two warpgroups for the weights; warps for copies, products, rows' numbers; one is idle
-constexpr int kTile = 128;     // rows, and keys
-constexpr int kCopyWarp = 8, kProductWarp = 9, kNumbersWarp = 10;
+constexpr int kWeightWarps = 16, kThreads = 32 * (kWeightWarps + 4);
+constexpr int kTile = 128;   // rows, and keys
+constexpr int kColumns = 32;  // of a thread
+constexpr int kCopyWarp = kWeightWarps, kProductWarp = kCopyWarp + 1, kItemWarp = kCopyWarp + 2, kNumbersWarp = kCopyWarp + 3;
+constexpr int kItemSlots = 2;
+constexpr int kNextItem = kOpCounters - 1, kDoneBlocks = kOpCounters - 2;  // counters of the workspace
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Maps {
@@ -51,6 +62,89 @@ struct Layout {
   static constexpr int kKeysShared = (2 + 2 * kRowStages) * kBytes + 1024;
 };
 
+struct Item {
+  int there;             // 0: no more
+  int rank, head;        // key head
+  int sequence, length;  // the sequence's first token in the step, and its tokens
+  int from, count;       // first token or key of the item in the sequence, and how many
+};
+
+// Numbers of items, in tiles of `unit` tokens.
+struct Work {
+  int64_t slots;
+  int unit;
+};
+
+// Item number n in order, from the last tiles of a sequence on, or from the first; false if there is none (a whole warp).
+__device__ __forceinline__ bool find_item(const PromptBwdArgs& a, const Work& work, bool last_first, int64_t n, Item* item) {
+  const int64_t lanes = (int64_t)a.kv_heads * a.nranks, slot = n / lanes;
+  const int lane_of = (int)(n % lanes);
+  item->head = lane_of % a.kv_heads;
+  item->rank = lane_of / a.kv_heads;
+  PromptSequence seq;
+  int tile;
+  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, work.unit, last_first ? work.slots - 1 - slot : slot, &seq, &tile))
+    return false;
+  item->sequence = seq.first;
+  item->length = seq.length;
+  item->from = tile * work.unit;
+  item->count = min(work.unit, seq.length - item->from);
+  item->there = 1;
+  return true;
+}
+
+// The warp that finds items for the others.
+__device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& work, bool last_first, Item* items,
+                                            uint64_t* full, uint64_t* empty, volatile int* dead) {
+  const int lane = threadIdx.x & 31;
+  uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
+  const int64_t all = work.slots * a.kv_heads * a.nranks;
+  int64_t n = blockIdx.x;
+  for (int i = 0;;) {
+    Item item;
+    const bool more = n < all;
+    if (!more) item.there = 0;
+    if (!more || find_item(a, work, last_first, n, &item)) {
+      if (!wait_warp(&empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, dead)) break;
+      if (lane == 0) {
+        items[i % kItemSlots] = item;
+        arrive(&full[i % kItemSlots]);
+      }
+      i++;
+    }
+    if (!more) break;
+    uint32_t next = 0;
+    if (lane == 0) next = atomicAdd(&counters[kNextItem], 1);
+    n = (int64_t)gridDim.x + __shfl_sync(~0u, next, 0);
+  }
+  // the last block to have no more sets the counters back
+  if (lane == 0 && atom_add_acq_rel_u32(&counters[kDoneBlocks], 1) == gridDim.x - 1) {
+    counters[kNextItem] = 0;
+    counters[kDoneBlocks] = 0;
+  }
+}
+
+// What another warp reads of item i; false at the end.
+struct Taken {
+  int rank, head, sequence, length, from, count;
+};
+__device__ __forceinline__ bool take_item(int i, const Item* items, uint64_t* full, uint64_t* empty, volatile int* dead, Taken* t) {
+  if (!wait_warp(&full[i % kItemSlots], i / kItemSlots & 1, dead)) return false;
+  const Item& item = items[i % kItemSlots];
+  const int there = uniform(item.there);
+  if (there) {
+    t->rank = uniform(item.rank);
+    t->head = uniform(item.head);
+    t->sequence = uniform(item.sequence);
+    t->length = uniform(item.length);
+    t->from = uniform(item.from);
+    t->count = uniform(item.count);
+  }
+  __syncwarp();
+  if (there && (threadIdx.x & 31) == 0) arrive(&empty[i % kItemSlots]);
+  return there != 0;
+}
+
 // Rows from `first` on of a tile in shared memory become 0, before products run over them; one warp.
 template <int DP>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int first) {
@@ -58,29 +152,40 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int first) {
     for (int h = 0; h < DP / 64; h++) *reinterpret_cast<uint4*>(tile + h * Layout<DP>::kSlab + r * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// A row of sums from tensor memory, half of its elements each for the two warpgroups, scaled and rounded.
+// Sums of a row from tensor memory: the slice's quarter of its elements.
 template <int DP>
-__device__ __forceinline__ void store_half(uint32_t at, int half, float by, bool mine, uint16_t* row, int D) {
-#pragma unroll 1
-  for (int c = half * (DP / 2); c < (half + 1) * (DP / 2) && c < D; c += 32) {
-    uint32_t o[32];
-    tmem_load32(at + c, o);
-    loads_done();
-    if (!mine) continue;
+struct Quarter {
+  uint32_t o[DP / 4];
+  __device__ __forceinline__ void load(uint32_t at, int slice) {
+    if (DP == 128) tmem_load32(at + slice * 32, o);
+    else tmem_load16(at + slice * 16, o);
+  }
+  __device__ __forceinline__ void store(uint16_t* row, int slice, float by, int D) const {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      if (c + i >= D) continue;
+    for (int i = 0; i < DP / 4; i += 8) {
+      const int d = slice * (DP / 4) + i;
+      if (d >= D) continue;
       Pack8<uint16_t> x;
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; k++) v[k] = __uint_as_float(o[i + k]) * by;
       x.narrow(v);
-      x.store(row + c + i);
+      x.store(row + d);
     }
   }
+};
+
+__device__ __forceinline__ void weights_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWeightWarps) : "memory"); }
+// One arrival of the warp, after its lanes' stores to tensor memory.
+__device__ __forceinline__ void arrive_warp(uint64_t* b) {
+  stores_done();
+  fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(b);
 }
 
-__device__ __forceinline__ void end_block(char* ws, volatile int* dead, int warp, uint32_t tmem) {
+__device__ __forceinline__ void end_block(char* ws, volatile int* dead, int warp) {
+  __syncwarp();
   fence_before();
   __syncthreads();
   if (*dead) {
@@ -92,28 +197,69 @@ __device__ __forceinline__ void end_block(char* ws, volatile int* dead, int warp
   __syncthreads();
   if (warp == kCopyWarp) {
     fence_after();
-    tmem_free(tmem, 512);
+    tmem_free(0, 512);
   }
 }
 
-__device__ __forceinline__ void weights_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ float* deltas_of(const PromptBwdArgs& a, int rank) {
+  return reinterpret_cast<float*>(a.ws + kOpScratchOffset) + (int64_t)rank * a.tokens * a.q_heads;
+}
+
+// delta of every row: DP / 8 lanes a row, 16 bytes a lane of each tensor.
+template <int DP>
+__global__ void __launch_bounds__(256) prompt_delta_kernel(const __grid_constant__ PromptBwdArgs a) {
+  constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes, kUnroll = 4;
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  const int lane = threadIdx.x & 31, rank = blockIdx.y, d = lane % kLanes * 8, D = a.head_dim;
+  const int rows = a.tokens * a.q_heads;
+  const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * (kAtOnce * kUnroll) + lane / kLanes;
+  Pack8<uint16_t> x[kUnroll], y[kUnroll];
+#pragma unroll
+  for (int i = 0; i < kUnroll; i++) {
+    const int64_t r = first + i * kAtOnce;
+    x[i].zero();
+    y[i].zero();
+    if (r < rows && d < D) {
+      const int64_t token = r / a.q_heads, in_token = r % a.q_heads * D + d;
+      x[i].load_stream((const uint16_t*)a.out[rank] + token * a.out_stride + in_token);
+      y[i].load_stream((const uint16_t*)a.dout[rank] + token * a.dout_stride + in_token);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; i++) {
+    float u[8], v[8], sum = 0.f;
+    x[i].widen(u);
+    y[i].widen(v);
+#pragma unroll
+    for (int k = 0; k < 8; k++) sum = fmaf(u[k], v[k], sum);
+#pragma unroll
+    for (int k = 1; k < kLanes; k *= 2) sum += __shfl_xor_sync(~0u, sum, k);
+    const int64_t r = first + i * kAtOnce;
+    if (d == 0 && r < rows) deltas_of(a, rank)[r] = sum;
+  }
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __grid_constant__ PromptBwdArgs a,
-                                                                     const __grid_constant__ Maps maps) {
+                                                                     const __grid_constant__ Maps maps,
+                                                                     const __grid_constant__ Work work) {
   using L = Layout<DP>;
   constexpr int KS = L::kKeyStages, VS = L::kValueStages;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (shared_address(raw) & 1023));
-  __shared__ uint64_t q_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], dp_full, ds_ready, dq_full;
+  __shared__ uint64_t q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], dp_full, ds_ready, dq_full, dq_free,
+      item_full[kItemSlots], item_empty[kItemSlots];
+  __shared__ Item items[kItemSlots];
   __shared__ uint32_t tmem_at;
   __shared__ int dead_flag;
-  __shared__ float half_delta[kTile];
+  __shared__ float sums[2][kTile];
   volatile int* const dead = &dead_flag;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     dead_flag = 0;
     barrier_init(&q_full, 1);
+    barrier_init(&q_empty, 1);
     for (int i = 0; i < KS; i++) {
       barrier_init(&k_full[i], 1);
       barrier_init(&k_empty[i], 1);
@@ -123,166 +269,200 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
       barrier_init(&v_empty[i], 1);
     }
     barrier_init(&dp_full, 1);
-    barrier_init(&ds_ready, 2 * kTile);
+    barrier_init(&ds_ready, kWeightWarps);
     barrier_init(&dq_full, 1);
+    barrier_init(&dq_free, kWeightWarps);
+    for (int i = 0; i < kItemSlots; i++) {
+      barrier_init(&item_full[i], 1);
+      barrier_init(&item_empty[i], kWeightWarps + 2);
+    }
     barriers_ready();
   }
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
-  const int group = a.q_heads / a.kv_heads, head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
-  const int per_tile = kTile / group;
-  PromptSequence seq;
-  int tile;
-  // the last rows of a sequence see the most keys: they start first
-  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, per_tile, (int64_t)gridDim.x - 1 - blockIdx.x, &seq, &tile)) return;
-  const int token0 = tile * per_tile, tokens = min(per_tile, seq.length - token0);
-  const int tiles = (token0 + tokens + kTile - 1) / kTile;
+  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
-  constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
-  constexpr uint32_t s_at = tmem, dp_at = tmem + 256, dq_at = tmem + 384;  // S: two buffers of 128 columns
+  constexpr uint32_t s_at = 0, dp_at = 256, dq_at = 384;  // all of tensor memory, from 0 on; S: two buffers of 128 columns
   uint8_t *const q_tile = smem, *const g_tile = smem + L::kBytes, *const k_ring = smem + 2 * L::kBytes,
           *const v_ring = k_ring + KS * L::kBytes;
-  const int steps = (D + 15) / 16;
+  const int group = a.q_heads / a.kv_heads, D = a.head_dim, per_tile = kTile / group, steps = (D + 15) / 16;
 
-  if (warp == kCopyWarp) {
-    if (lane == 0) {
-      arrive_expect(&q_full, (uint32_t)(2 * per_tile * group * 128 * (DP / 64)));
-      for (int h = 0; h < DP / 64; h++) {
-        copy_3d(q_tile + h * L::kSlab, &maps.q[rank], h * 64, head * group, seq.first + token0, &q_full);
-        copy_3d(g_tile + h * L::kSlab, &maps.dout[rank], h * 64, head * group, seq.first + token0, &q_full);
+  if (warp == kItemWarp) {
+    serve_items(a, work, true, items, item_full, item_empty, dead);  // the last rows see the most keys
+  } else if (warp == kCopyWarp) {
+    int n = 0;  // tiles of keys so far
+    for (int i = 0;; i++) {
+      Taken t;
+      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      const int tiles = (t.from + t.count + kTile - 1) / kTile;
+      bool fine = true;
+      for (int j = 0; j < tiles && fine; j++, n++) {
+        const int k = n % KS, v = n % VS;
+        if (!(fine = wait_warp(&k_empty[k], (n / KS & 1) ^ 1, dead))) break;
+        if (lane == 0) {
+          arrive_expect(&k_full[k], L::kBytes);
+          for (int h = 0; h < DP / 64; h++)
+            copy_3d(k_ring + k * L::kBytes + h * L::kSlab, &maps.k[t.rank], h * 64, t.head, t.sequence + j * kTile, &k_full[k]);
+        }
+        if (!(fine = wait_warp(&v_empty[v], (n / VS & 1) ^ 1, dead))) break;
+        if (lane == 0) {
+          arrive_expect(&v_full[v], L::kBytes);
+          for (int h = 0; h < DP / 64; h++)
+            copy_3d(v_ring + v * L::kBytes + h * L::kSlab, &maps.v[t.rank], h * 64, t.head, t.sequence + j * kTile, &v_full[v]);
+        }
+        if (j == 0) {
+          if (!(fine = wait_warp(&q_empty, (i & 1) ^ 1, dead))) break;
+          if (lane == 0) {
+            arrive_expect(&q_full, (uint32_t)(2 * per_tile * group * 128 * (DP / 64)));
+            for (int h = 0; h < DP / 64; h++) {
+              copy_3d(q_tile + h * L::kSlab, &maps.q[t.rank], h * 64, t.head * group, t.sequence + t.from, &q_full);
+              copy_3d(g_tile + h * L::kSlab, &maps.dout[t.rank], h * 64, t.head * group, t.sequence + t.from, &q_full);
+            }
+          }
+        }
       }
-      for (int j = 0; j < tiles; j++) {
-        if (!wait(&k_empty[j % KS], (j / KS & 1) ^ 1, dead)) break;
-        arrive_expect(&k_full[j % KS], L::kBytes);
-        for (int h = 0; h < DP / 64; h++)
-          copy_3d(k_ring + j % KS * L::kBytes + h * L::kSlab, &maps.k[rank], h * 64, head, seq.first + j * kTile, &k_full[j % KS]);
-        if (!wait(&v_empty[j % VS], (j / VS & 1) ^ 1, dead)) break;
-        arrive_expect(&v_full[j % VS], L::kBytes);
-        for (int h = 0; h < DP / 64; h++)
-          copy_3d(v_ring + j % VS * L::kBytes + h * L::kSlab, &maps.v[rank], h * 64, head, seq.first + j * kTile, &v_full[j % VS]);
-      }
+      if (!fine) break;
     }
   } else if (warp == kProductWarp) {
     const uint32_t q_at = shared_address(q_tile), g_at = shared_address(g_tile), k_at = shared_address(k_ring),
                    v_at = shared_address(v_ring);
     const uint32_t lead = elect_one();
-    const int count = uniform(tiles), keys_of = uniform(seq.length);
-    auto score = [&](int j) {  // S of key tile j; keys that are none are 0, for the product with dS
-      if (!wait_warp(&k_full[j % KS], j / KS & 1, dead)) return false;
-      if (keys_of - j * kTile < kTile) {
-        clear_rows<DP>(k_ring + j % KS * L::kBytes, keys_of - j * kTile);
-        stores_to_products();
-        __syncwarp();
+    int base = 0;  // tiles of keys of the items before
+    for (int i = 0;; i++) {
+      Taken t;
+      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      const int tiles = (t.from + t.count + kTile - 1) / kTile;
+      auto score = [&](int j) {  // S of key tile j; keys that are none are 0, for the product with dS
+        const int n = base + j, stage = n % KS;
+        if (!wait_warp(&k_full[stage], n / KS & 1, dead)) return false;
+        if (t.length - j * kTile < kTile) {
+          clear_rows<DP>(k_ring + stage * L::kBytes, t.length - j * kTile);
+          stores_to_products();
+          __syncwarp();
+        }
+        fence_after();
+        rows_by_rows<DP / 16, L::kSlab>(lead, s_at + (n & 1) * 128, q_at, k_at + stage * L::kBytes, kTile, steps);
+        return true;
+      };
+      auto value = [&](int j) {  // dO V^T
+        const int n = base + j, stage = n % VS;
+        if (!wait_warp(&v_full[stage], n / VS & 1, dead)) return false;
+        fence_after();
+        rows_by_rows<DP / 16, L::kSlab>(lead, dp_at, g_at, v_at + stage * L::kBytes, kTile, steps);
+        commit(lead, &dp_full);
+        commit(lead, &v_empty[stage]);
+        if (j + 1 == tiles) commit(lead, &q_empty);
+        return true;
+      };
+      bool fine = wait_warp(&q_full, i & 1, dead) && score(0) && value(0);
+      for (int j = 0; j < tiles && fine; j++) {
+        const int n = base + j;
+        const bool more = j + 1 < tiles;
+        if (more && !(fine = score(j + 1))) break;
+        if (j == 0 && i > 0 && !(fine = wait_warp(&dq_free, (i - 1) & 1, dead))) break;  // dQ of the item before has been read
+        if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
+        fence_after();
+        if (more && !(fine = value(j + 1))) break;
+        weights_by_rows<2, kColumns>(lead, dq_at, s_at + (n & 1) * 128, k_at + n % KS * L::kBytes, steps * 16, j > 0, L::kSlab);
+        commit(lead, &k_empty[n % KS]);
+        if (!more) commit(lead, &dq_full);
       }
-      fence_after();
-      rows_by_rows<DP / 16, L::kSlab>(lead, s_at + (j & 1) * 128, q_at, k_at + j % KS * L::kBytes, kTile, steps);
-      return true;
-    };
-    auto value = [&](int j) {  // dO V^T
-      if (!wait_warp(&v_full[j % VS], j / VS & 1, dead)) return false;
-      fence_after();
-      rows_by_rows<DP / 16, L::kSlab>(lead, dp_at, g_at, v_at + j % VS * L::kBytes, kTile, steps);
-      commit(lead, &dp_full);
-      commit(lead, &v_empty[j % VS]);
-      return true;
-    };
-    bool fine = wait_warp(&q_full, 0, dead) && score(0) && value(0);
-    for (int j = 0; j < count && fine; j++) {
-      const bool more = j + 1 < count;
-      if (more && !(fine = score(j + 1))) break;
-      if (!(fine = wait_warp(&ds_ready, j & 1, dead))) break;
-      fence_after();
-      if (more && !(fine = value(j + 1))) break;
-      weights_by_rows<32>(lead, dq_at, s_at + (j & 1) * 128, k_at + j % KS * L::kBytes, steps * 16, j > 0, L::kSlab);
-      commit(lead, &k_empty[j % KS]);
-      if (!more) commit(lead, &dq_full);
+      if (!fine) break;
+      base += tiles;
     }
-  } else if (warp < kCopyWarp) {
-    const int half = warp >> 2;
-    const uint32_t quarter = (uint32_t)(warp & 3) << 21;
-    const int row = threadIdx.x & 127, token = row / group, query = head * group + row % group;
-    const bool mine = token < tokens;
-    const int64_t at_token = (int64_t)seq.first + token0 + token, at = at_token * a.q_heads + query;
-    // delta, half of the elements each
-    float delta = 0.f, lse2 = 0.f;
-    if (mine) {
-      const uint16_t* o = (const uint16_t*)a.out[rank] + at_token * a.out_stride + (int64_t)query * D;
-      const uint16_t* g = (const uint16_t*)a.dout[rank] + at_token * a.dout_stride + (int64_t)query * D;
-#pragma unroll 4
-      for (int d = half * (DP / 2); d < (half + 1) * (DP / 2); d += 8) {
-        if (d >= D) break;
-        Pack8<uint16_t> x, y;
-        float u[8], v[8];
-        x.load(o + d);
-        y.load(g + d);
-        x.widen(u);
-        y.widen(v);
-#pragma unroll
-        for (int i = 0; i < 8; i++) delta = fmaf(u[i], v[i], delta);
+  } else if (warp < kWeightWarps) {
+    const int slice = warp >> 2;
+    const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
+    const int row = threadIdx.x & 127, token = row / group, in_group = row % group;
+    const float scale2 = a.scale * kLog2e;
+    int n = 0;
+    for (int i = 0;; i++) {
+      Taken t;
+      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      const int tiles = (t.from + t.count + kTile - 1) / kTile, query = t.head * group + in_group;
+      const bool mine = token < t.count;
+      const int64_t at_token = (int64_t)t.sequence + t.from + token, at = at_token * a.q_heads + query;
+      float lse2 = 0.f, delta = 0.f;
+      if (mine) {
+        lse2 = a.lse[t.rank][at] * kLog2e;
+        delta = deltas_of(a, t.rank)[at];
       }
-      lse2 = a.lse[rank][at] * kLog2e;
-    }
-    if (half == 1) half_delta[row] = delta;
-    weights_barrier();
-    if (half == 0) {
-      delta += half_delta[row];
-      if (mine) reinterpret_cast<float*>(a.ws + kOpScratchOffset)[(int64_t)rank * a.tokens * a.q_heads + at] = delta;
-    }
-    weights_barrier();
-    if (half == 0) half_delta[row] = delta;
-    weights_barrier();
-    delta = half_delta[row];
-    const int sees = token0 + (mine ? token : 0) + 1;
-    int least = sees;
+      const int sees = t.from + (mine ? token : 0) + 1;
+      const int least = __reduce_min_sync(~0u, sees);
+      bool fine = true;
+      for (int j = 0; j < tiles; j++, n++) {
+        if (!(fine = wait(&dp_full, n & 1, dead))) break;  // S of the tile was issued ahead of it
+        fence_after();
+        const uint32_t from = s_at + (n & 1) * 128 + quarter + slice * kColumns;
+        uint32_t s[kColumns], dp[kColumns];
+        tmem_load32(from, s);
+        tmem_load32(dp_at + quarter + slice * kColumns, dp);
+        loads_done();
+        const int upto = sees - j * kTile - slice * kColumns;
+        const bool cut = (j + 1) * kTile > least;
+        const F2 scale_pair = f2(scale2, scale2), lse_pair = f2(-lse2, -lse2);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) least = min(least, __shfl_xor_sync(~0u, least, d));
-    const F2 scale_pair = f2(a.scale * kLog2e, a.scale * kLog2e), lse_pair = f2(-lse2, -lse2), delta_pair = f2(-delta, -delta);
-    bool fine = true;
-    for (int j = 0; j < tiles; j++) {
-      if (!(fine = wait(&dp_full, j & 1, dead))) break;  // S of the tile was issued ahead of it
+        for (int c = 0; c < kColumns; c += 2) {
+          float2 p = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, lse_pair));
+          s[c] = __float_as_uint(exp2_fast(p.x));
+          s[c + 1] = __float_as_uint(exp2_fast(p.y));
+        }
+        if (cut) {
+#pragma unroll
+          for (int c = 0; c < kColumns; c++) {
+            if (c >= upto) s[c] = dp[c] = 0;
+          }
+        }
+        if (tiles == 1) {  // all keys of the rows are here
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < kColumns; c++) sum = fmaf(__uint_as_float(s[c]), __uint_as_float(dp[c]), sum);
+          if (slice >= 2) sums[slice - 2][row] = sum;
+          weights_barrier();
+          if (slice < 2) sum += sums[slice][row];
+          weights_barrier();
+          if (slice < 2) sums[slice][row] = sum;
+          weights_barrier();
+          delta = sums[0][row] + sums[1][row];
+          if (mine && slice == 0) deltas_of(a, t.rank)[at] = delta;
+          weights_barrier();
+        }
+        const F2 delta_pair = f2(-delta, -delta);
+#pragma unroll
+        for (int c = 0; c < kColumns; c += 2) {
+          const F2 d = add2(f2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), delta_pair);
+          const float2 ds = unpack(mul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), d));
+          s[c / 2] = bf16_pair(ds.x, ds.y);
+        }
+        tmem_store16(from, s);
+        arrive_warp(&ds_ready);
+      }
+      if (!fine || !wait(&dq_full, i & 1, dead)) break;
       fence_after();
-      const uint32_t from = s_at + (j & 1) * 128 + quarter + half * 64;
-      uint32_t s[64], dp[64];
-      tmem_load32(from, s);
-      tmem_load32(from + 32, s + 32);
-      tmem_load32(dp_at + quarter + half * 64, dp);
-      tmem_load32(dp_at + quarter + half * 64 + 32, dp + 32);
+      Quarter<DP> o;
+      o.load(dq_at + quarter, slice);
       loads_done();
-      const int upto = sees - j * kTile - half * 64;
-      const bool cut = (j + 1) * kTile > least;
-#pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        float2 p = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, lse_pair));
-        p.x = exp2_fast(p.x);
-        p.y = exp2_fast(p.y);
-        const F2 d = add2(f2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), delta_pair);
-        const float2 ds = unpack(mul2(f2(p.x, p.y), d));
-        s[c / 2] = bf16_pair(!cut || c < upto ? ds.x : 0.f, !cut || c + 1 < upto ? ds.y : 0.f);
-      }
-      tmem_store32(from, s);
-      stores_done();
       fence_before();
-      arrive(&ds_ready);
-    }
-    if (fine && wait(&dq_full, 0, dead)) {
-      fence_after();
-      store_half<DP>(dq_at + quarter, half, a.scale, mine, (uint16_t*)a.dq[rank] + at_token * a.dq_stride + (int64_t)query * D, D);
+      __syncwarp();
+      if (lane == 0) arrive(&dq_free);
+      if (mine) o.store((uint16_t*)a.dq[t.rank] + at_token * a.dq_stride + (int64_t)query * D, slice, a.scale, D);
     }
   }
-  __syncwarp();
-  end_block(a.ws, dead, warp, tmem);
+  end_block(a.ws, dead, warp);
 }
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __grid_constant__ PromptBwdArgs a,
-                                                                     const __grid_constant__ Maps maps) {
+                                                                     const __grid_constant__ Maps maps,
+                                                                     const __grid_constant__ Work work) {
   using L = Layout<DP>;
   constexpr int NS = L::kRowStages;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (shared_address(raw) & 1023));
-  __shared__ uint64_t kv_full, full[NS], empty[NS], s_full, p_ready, dp_full, ds_ready, done;
+  __shared__ uint64_t kv_full, kv_empty, full[NS], empty[NS], s_full, p_ready, dp_full, ds_ready, sums_full, sums_free,
+      item_full[kItemSlots], item_empty[kItemSlots];
+  __shared__ Item items[kItemSlots];
   __shared__ uint32_t tmem_at;
   __shared__ int dead_flag;
   __shared__ __align__(16) float numbers[NS][2][kTile];  // -lse log2(e) and -delta of a tile's rows
@@ -293,203 +473,232 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   if (threadIdx.x == 0) {
     dead_flag = 0;
     barrier_init(&kv_full, 1);
+    barrier_init(&kv_empty, 1);
     for (int i = 0; i < NS; i++) {
-      barrier_init(&full[i], 1 + 32);
-      barrier_init(&empty[i], 1 + 2 * kTile);
+      barrier_init(&full[i], 2);
+      barrier_init(&empty[i], 1 + kWeightWarps);
     }
     barrier_init(&s_full, 1);
-    barrier_init(&p_ready, 2 * kTile);
+    barrier_init(&p_ready, kWeightWarps);
     barrier_init(&dp_full, 1);
-    barrier_init(&ds_ready, 2 * kTile);
-    barrier_init(&done, 1);
+    barrier_init(&ds_ready, kWeightWarps);
+    barrier_init(&sums_full, 1);
+    barrier_init(&sums_free, kWeightWarps);
+    for (int i = 0; i < kItemSlots; i++) {
+      barrier_init(&item_full[i], 1);
+      barrier_init(&item_empty[i], kWeightWarps + 3);
+    }
     barriers_ready();
   }
   if (threadIdx.x < kTile) token_of[threadIdx.x] = (uint8_t)(threadIdx.x / group);
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  const int head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
-  const int per_tile = kTile / group;
-  PromptSequence seq;
-  int tile;
-  // the first keys of a sequence are seen by the most rows: they start first
-  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, kTile, blockIdx.x, &seq, &tile)) return;
-  const int key0 = tile * kTile, keys = min(kTile, seq.length - key0);
-  const int begin = key0 / per_tile, end = (seq.length + per_tile - 1) / per_tile;  // tiles of rows
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
-  constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
-  constexpr uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 384;
+  constexpr uint32_t s_at = 0, dp_at = 128, dv_at = 256, dk_at = 384;  // all of tensor memory, from 0 on
   uint8_t *const k_tile = smem, *const v_tile = smem + L::kBytes, *const ring = smem + 2 * L::kBytes;  // a stage: Q, dO
-  const int steps = (D + 15) / 16;
+  const int D = a.head_dim, per_tile = kTile / group, steps = (D + 15) / 16;
+  auto first_tile = [&](const Taken& t) { return t.from / per_tile; };  // of rows
+  auto last_tile = [&](const Taken& t) { return (t.length + per_tile - 1) / per_tile; };
 
-  if (warp == kCopyWarp) {
-    if (lane == 0) {
-      arrive_expect(&kv_full, 2 * L::kBytes);
-      for (int h = 0; h < DP / 64; h++) {
-        copy_3d(k_tile + h * L::kSlab, &maps.k[rank], h * 64, head, seq.first + key0, &kv_full);
-        copy_3d(v_tile + h * L::kSlab, &maps.v[rank], h * 64, head, seq.first + key0, &kv_full);
-      }
-      for (int i = begin; i < end; i++) {
-        const int n = i - begin, stage = n % NS;
-        if (!wait(&empty[stage], (n / NS & 1) ^ 1, dead)) break;
-        arrive_expect(&full[stage], (uint32_t)(2 * per_tile * group * 128 * (DP / 64)));
-        for (int h = 0; h < DP / 64; h++) {
-          copy_3d(ring + stage * 2 * L::kBytes + h * L::kSlab, &maps.q[rank], h * 64, head * group, seq.first + i * per_tile,
-                  &full[stage]);
-          copy_3d(ring + (stage * 2 + 1) * L::kBytes + h * L::kSlab, &maps.dout[rank], h * 64, head * group,
-                  seq.first + i * per_tile, &full[stage]);
+  if (warp == kItemWarp) {
+    serve_items(a, work, false, items, item_full, item_empty, dead);  // the first keys are seen by the most rows
+  } else if (warp == kCopyWarp) {
+    int n = 0;  // tiles of rows so far
+    for (int i = 0;; i++) {
+      Taken t;
+      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      const int begin = first_tile(t), end = last_tile(t);
+      bool fine = true;
+      for (int x = begin; x < end && fine; x++, n++) {
+        const int stage = n % NS;
+        if (!(fine = wait_warp(&empty[stage], (n / NS & 1) ^ 1, dead))) break;
+        if (lane == 0) {
+          arrive_expect(&full[stage], (uint32_t)(2 * per_tile * group * 128 * (DP / 64)));
+          for (int h = 0; h < DP / 64; h++) {
+            copy_3d(ring + stage * 2 * L::kBytes + h * L::kSlab, &maps.q[t.rank], h * 64, t.head * group,
+                    t.sequence + x * per_tile, &full[stage]);
+            copy_3d(ring + (stage * 2 + 1) * L::kBytes + h * L::kSlab, &maps.dout[t.rank], h * 64, t.head * group,
+                    t.sequence + x * per_tile, &full[stage]);
+          }
+        }
+        if (x == begin) {
+          if (!(fine = wait_warp(&kv_empty, (i & 1) ^ 1, dead))) break;
+          if (lane == 0) {
+            arrive_expect(&kv_full, 2 * L::kBytes);
+            for (int h = 0; h < DP / 64; h++) {
+              copy_3d(k_tile + h * L::kSlab, &maps.k[t.rank], h * 64, t.head, t.sequence + t.from, &kv_full);
+              copy_3d(v_tile + h * L::kSlab, &maps.v[t.rank], h * 64, t.head, t.sequence + t.from, &kv_full);
+            }
+          }
         }
       }
+      if (!fine) break;
     }
   } else if (warp == kNumbersWarp) {
-    const float* deltas = reinterpret_cast<const float*>(a.ws + kOpScratchOffset) + (int64_t)rank * a.tokens * a.q_heads;
-    float l[4], d[4];
-    auto read = [&](int i) {
+    int n = 0;
+    for (int i = 0;; i++) {
+      Taken t;
+      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      const int begin = first_tile(t), end = last_tile(t);
+      const float *const lse = a.lse[t.rank], *const deltas = deltas_of(a, t.rank);
+      float l[4], d[4];
+      auto read = [&](int x) {  // a tile ahead
 #pragma unroll
-      for (int x = 0; x < 4; x++) {
-        const int r = lane + 32 * x, token = i * per_tile + r / group;
-        const bool there = r / group < per_tile && token < seq.length && i < end;
-        const int64_t at = ((int64_t)seq.first + token) * a.q_heads + head * group + r % group;
-        l[x] = there ? a.lse[rank][at] * -kLog2e : 0.f;
-        d[x] = there ? -deltas[at] : 0.f;
-      }
-    };
-    read(begin);
-    for (int i = begin; i < end; i++) {
-      const int n = i - begin, stage = n % NS;
-      if (!wait(&empty[stage], (n / NS & 1) ^ 1, dead)) break;
+        for (int y = 0; y < 4; y++) {
+          const int r = lane + 32 * y, token = x * per_tile + token_of[r];
+          const bool there = token_of[r] < per_tile && token < t.length && x < end;
+          const int64_t at = ((int64_t)t.sequence + token) * a.q_heads + t.head * group + r - token_of[r] * group;
+          l[y] = there ? lse[at] * -kLog2e : 0.f;
+          d[y] = there ? -deltas[at] : 0.f;
+        }
+      };
+      read(begin);
+      bool fine = true;
+      for (int x = begin; x < end; x++, n++) {
+        const int stage = n % NS;
+        if (!(fine = wait_warp(&empty[stage], (n / NS & 1) ^ 1, dead))) break;
 #pragma unroll
-      for (int x = 0; x < 4; x++) {
-        numbers[stage][0][lane + 32 * x] = l[x];
-        numbers[stage][1][lane + 32 * x] = d[x];
+        for (int y = 0; y < 4; y++) {
+          numbers[stage][0][lane + 32 * y] = l[y];
+          numbers[stage][1][lane + 32 * y] = d[y];
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&full[stage]);
+        read(x + 1);
       }
-      arrive(&full[stage]);
-      read(i + 1);
+      if (!fine) break;
     }
   } else if (warp == kProductWarp) {
     const uint32_t k_at = shared_address(k_tile), v_at = shared_address(v_tile), ring_at = shared_address(ring);
     const uint32_t lead = elect_one();
-    const int from = uniform(begin), to = uniform(end), tokens_of = uniform(seq.length);
-    auto score = [&](int i) {  // S^T of a tile of rows; rows that are none are 0, for the products with P and dS
-      const int n = i - from, stage = n % NS;
-      if (!wait_warp(&full[stage], n / NS & 1, dead)) return false;
-      const int rows = min(per_tile, tokens_of - i * per_tile) * group;
-      if (rows < kTile) {
-        clear_rows<DP>(ring + stage * 2 * L::kBytes, rows);
-        clear_rows<DP>(ring + (stage * 2 + 1) * L::kBytes, rows);
-        stores_to_products();
-        __syncwarp();
+    int base = 0;  // tiles of rows of the items before
+    for (int i = 0;; i++) {
+      Taken t;
+      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      const int begin = first_tile(t), end = last_tile(t);
+      auto score = [&](int x) {  // S^T of a tile of rows; rows that are none are 0, for the products with P and dS
+        const int n = base + x - begin, stage = n % NS;
+        if (!wait_warp(&full[stage], n / NS & 1, dead)) return false;
+        const int rows = min(per_tile, t.length - x * per_tile) * group;
+        if (rows < kTile) {
+          clear_rows<DP>(ring + stage * 2 * L::kBytes, rows);
+          clear_rows<DP>(ring + (stage * 2 + 1) * L::kBytes, rows);
+          stores_to_products();
+          __syncwarp();
+        }
+        fence_after();
+        rows_by_rows<DP / 16, L::kSlab>(lead, s_at, k_at, ring_at + stage * 2 * L::kBytes, kTile, steps);
+        commit(lead, &s_full);
+        return true;
+      };
+      auto value = [&](int x) {  // V dO^T
+        rows_by_rows<DP / 16, L::kSlab>(lead, dp_at, v_at, ring_at + ((base + x - begin) % NS * 2 + 1) * L::kBytes, kTile, steps);
+        commit(lead, &dp_full);
+        if (x + 1 == end) commit(lead, &kv_empty);
+      };
+      bool fine = wait_warp(&kv_full, i & 1, dead) && score(begin);
+      if (!fine) break;
+      value(begin);
+      // sums of the item before have been read
+      if (i > 0 && !wait_warp(&sums_free, (i - 1) & 1, dead)) break;
+      for (int x = begin; x < end; x++) {
+        const int n = base + x - begin, stage = n % NS;
+        const bool more = x + 1 < end;
+        if (!(fine = wait_warp(&p_ready, n & 1, dead))) break;
+        fence_after();
+        weights_by_rows<2, kColumns>(lead, dv_at, s_at, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, x > begin, L::kSlab);
+        if (more && !(fine = score(x + 1))) break;
+        if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
+        fence_after();
+        weights_by_rows<2, kColumns>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, x > begin, L::kSlab);
+        commit(lead, &empty[stage]);
+        if (!more) commit(lead, &sums_full);
+        if (more) value(x + 1);
       }
-      fence_after();
-      rows_by_rows<DP / 16, L::kSlab>(lead, s_at, k_at, ring_at + stage * 2 * L::kBytes, kTile, steps);
-      commit(lead, &s_full);
-      return true;
-    };
-    auto value = [&](int i) {  // V dO^T
-      rows_by_rows<DP / 16, L::kSlab>(lead, dp_at, v_at, ring_at + ((i - from) % NS * 2 + 1) * L::kBytes, kTile, steps);
-      commit(lead, &dp_full);
-    };
-    bool fine = wait_warp(&kv_full, 0, dead) && score(from);
-    if (fine) value(from);
-    for (int i = from; i < to && fine; i++) {
-      const int n = i - from, stage = n % NS;
-      const bool more = i + 1 < to;
-      if (!(fine = wait_warp(&p_ready, n & 1, dead))) break;
-      fence_after();
-      weights_by_rows<32>(lead, dv_at, s_at, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, n > 0, L::kSlab);
-      if (more && !(fine = score(i + 1))) break;
-      if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
-      fence_after();
-      weights_by_rows<32>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, n > 0, L::kSlab);
-      commit(lead, &empty[stage]);
-      if (!more) commit(lead, &done);
-      if (more) value(i + 1);
+      if (!fine) break;
+      base += end - begin;
     }
-  } else if (warp < kCopyWarp) {
-    const int half = warp >> 2;
+  } else if (warp < kWeightWarps) {
+    const int slice = warp >> 2, c0 = slice * kColumns;
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;
     const int row = threadIdx.x & 127;
-    const bool mine = row < keys;
-    const int key = key0 + row;
     const F2 scale_pair = f2(a.scale * kLog2e, a.scale * kLog2e);
-    bool fine = true;
-    for (int i = begin; i < end; i++) {
-      const int n = i - begin, stage = n % NS;
-      if (!(fine = wait(&full[stage], n / NS & 1, dead))) break;  // the rows' numbers
-      if (!(fine = wait(&s_full, n & 1, dead))) break;
-      fence_after();
-      const uint32_t from = s_at + quarter + half * 64, dp_from = dp_at + quarter + half * 64;
-      uint32_t s[64], w[32];
-      tmem_load32(from, s);
-      tmem_load32(from + 32, s + 32);
-      loads_done();
-      const int rows = min(per_tile, seq.length - i * per_tile) * group;
-      const bool cut = rows < kTile || i * per_tile < key0 + kTile - 1;
-      const float4* l = reinterpret_cast<const float4*>(numbers[stage][0] + half * 64);
-      const float4* d = reinterpret_cast<const float4*>(numbers[stage][1] + half * 64);
+    int n = 0;
+    for (int i = 0;; i++) {
+      Taken t;
+      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      const int begin = first_tile(t), end = last_tile(t), key = t.from + row;
+      bool fine = true;
+      for (int x = begin; x < end; x++, n++) {
+        const int stage = n % NS;
+        if (!(fine = wait(&full[stage], n / NS & 1, dead))) break;  // the rows' numbers
+        if (!(fine = wait(&s_full, n & 1, dead))) break;
+        fence_after();
+        const uint32_t from = s_at + quarter + c0, dp_from = dp_at + quarter + c0;
+        uint32_t s[kColumns], w[kColumns / 2];
+        tmem_load32(from, s);
+        loads_done();
+        const int rows = min(per_tile, t.length - x * per_tile) * group;
+        const bool cut = rows < kTile || x * per_tile < t.from + kTile - 1;
+        const float4* l = reinterpret_cast<const float4*>(numbers[stage][0] + c0);
+        const float4* d = reinterpret_cast<const float4*>(numbers[stage][1] + c0);
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 x = l[c / 4];
-        float2 p = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, f2(x.x, x.y)));
-        float2 q = unpack(fma2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale_pair, f2(x.z, x.w)));
-        p.x = exp2_fast(p.x);
-        p.y = exp2_fast(p.y);
-        q.x = exp2_fast(q.x);
-        q.y = exp2_fast(q.y);
-        if (cut) {
-          auto seen = [&](int u) {
-            const int r = half * 64 + c + u;
-            return r < rows && i * per_tile + token_of[r] >= key;
-          };
-          p.x = seen(0) ? p.x : 0.f;
-          p.y = seen(1) ? p.y : 0.f;
-          q.x = seen(2) ? q.x : 0.f;
-          q.y = seen(3) ? q.y : 0.f;
+        for (int c = 0; c < kColumns; c += 4) {
+          const float4 y = l[c / 4];
+          const float2 p = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, f2(y.x, y.y)));
+          const float2 q = unpack(fma2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), scale_pair, f2(y.z, y.w)));
+          s[c] = __float_as_uint(exp2_fast(p.x));
+          s[c + 1] = __float_as_uint(exp2_fast(p.y));
+          s[c + 2] = __float_as_uint(exp2_fast(q.x));
+          s[c + 3] = __float_as_uint(exp2_fast(q.y));
         }
-        s[c] = __float_as_uint(p.x);
-        s[c + 1] = __float_as_uint(p.y);
-        s[c + 2] = __float_as_uint(q.x);
-        s[c + 3] = __float_as_uint(q.y);
-        w[c / 2] = bf16_pair(p.x, p.y);
-        w[c / 2 + 1] = bf16_pair(q.x, q.y);
-      }
-      tmem_store32(from, w);
-      stores_done();
-      fence_before();
-      arrive(&p_ready);
-      if (!(fine = wait(&dp_full, n & 1, dead))) break;
-      fence_after();
+        if (cut) {
+          const int before = key - x * per_tile;  // tokens of the tile ahead of the key
 #pragma unroll
-      for (int b = 0; b < 64; b += 32) {
-        uint32_t g[32];
-        tmem_load32(dp_from + b, g);
+          for (int c = 0; c < kColumns; c++)
+            if (c0 + c >= rows || (int)token_of[c0 + c] < before) s[c] = 0;
+        }
+#pragma unroll
+        for (int c = 0; c < kColumns; c += 2) w[c / 2] = bf16_pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        tmem_store16(from, w);
+        arrive_warp(&p_ready);
+        if (!(fine = wait(&dp_full, n & 1, dead))) break;
+        fence_after();
+        uint32_t g[kColumns];
+        tmem_load32(dp_from, g);
         loads_done();
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 x = d[(b + c) / 4];
-          const float2 u = unpack(mul2(f2(__uint_as_float(s[b + c]), __uint_as_float(s[b + c + 1])),
-                                       add2(f2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), f2(x.x, x.y))));
-          const float2 v = unpack(mul2(f2(__uint_as_float(s[b + c + 2]), __uint_as_float(s[b + c + 3])),
-                                       add2(f2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), f2(x.z, x.w))));
-          w[(b + c) / 2] = bf16_pair(u.x, u.y);
-          w[(b + c) / 2 + 1] = bf16_pair(v.x, v.y);
+        for (int c = 0; c < kColumns; c += 4) {
+          const float4 y = d[c / 4];
+          const float2 u = unpack(mul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                       add2(f2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), f2(y.x, y.y))));
+          const float2 v = unpack(mul2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                       add2(f2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), f2(y.z, y.w))));
+          w[c / 2] = bf16_pair(u.x, u.y);
+          w[c / 2 + 1] = bf16_pair(v.x, v.y);
         }
+        tmem_store16(dp_from, w);
+        arrive_warp(&ds_ready);
+        if (lane == 0) arrive(&empty[stage]);  // the rows' numbers have been read
       }
-      tmem_store32(dp_from, w);
-      stores_done();
-      fence_before();
-      arrive(&ds_ready);
-      arrive(&empty[stage]);  // the rows' numbers have been read
-    }
-    if (fine && wait(&done, 0, dead)) {
+      if (!fine || !wait(&sums_full, i & 1, dead)) break;
       fence_after();
-      const int64_t token = (int64_t)seq.first + key, at = (int64_t)head * D;
-      store_half<DP>(dk_at + quarter, half, a.scale, mine, (uint16_t*)a.dk[rank] + token * a.dk_stride + at, D);
-      store_half<DP>(dv_at + quarter, half, 1.f, mine, (uint16_t*)a.dv[rank] + token * a.dv_stride + at, D);
+      Quarter<DP> dk, dv;
+      dk.load(dk_at + quarter, slice);
+      dv.load(dv_at + quarter, slice);
+      loads_done();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&sums_free);
+      if (row < t.count) {
+        const int64_t token = (int64_t)t.sequence + key, at = (int64_t)t.head * D;
+        dk.store((uint16_t*)a.dk[t.rank] + token * a.dk_stride + at, slice, a.scale, D);
+        dv.store((uint16_t*)a.dv[t.rank] + token * a.dv_stride + at, slice, 1.f, D);
+      }
     }
   }
-  __syncwarp();
-  end_block(a.ws, dead, warp, tmem);
+  end_block(a.ws, dead, warp);
 }
 
 template <int DP>
@@ -509,12 +718,20 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
   }
   if (e != cudaSuccess) return e;
   PromptBwdArgs copy = a;
-  void* params[] = {&copy, &maps};
-  e = launch_op(rows, dim3((unsigned)prompt_slots(a.tokens, a.sequences, 1, per_tile), (unsigned)a.kv_heads, (unsigned)a.nranks),
-                kThreads, Layout<DP>::kRowsShared, stream, params);
-  if (e != cudaSuccess) return e;
-  return launch_op(keys, dim3((unsigned)prompt_slots(a.tokens, a.sequences, 1, kTile), (unsigned)a.kv_heads, (unsigned)a.nranks),
-                   kThreads, Layout<DP>::kKeysShared, stream, params);
+  void* delta_params[] = {&copy};
+  const int64_t a_block = 8 * 4 * (32 / (DP / 8));  // rows
+  e = launch_op((const void*)prompt_delta_kernel<DP>,
+                dim3((unsigned)div_up((int64_t)a.tokens * a.q_heads, a_block), (unsigned)a.nranks), 256, 0, stream, delta_params);
+  for (int which = 0; which < 2 && e == cudaSuccess; which++) {
+    Work work;
+    work.unit = which == 0 ? per_tile : kTile;
+    work.slots = prompt_slots(a.tokens, a.sequences, 1, work.unit);
+    const int64_t all = work.slots * a.kv_heads * a.nranks;
+    void* params[] = {&copy, &maps, &work};
+    e = launch_op(which == 0 ? rows : keys, dim3((unsigned)(all < blocks ? all : blocks)), kThreads,
+                  which == 0 ? Layout<DP>::kRowsShared : Layout<DP>::kKeysShared, stream, params);
+  }
+  return e;
 }
 
 }  // namespace

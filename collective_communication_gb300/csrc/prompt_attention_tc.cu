@@ -511,10 +511,10 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
             if (j == begin && results[t] > 0 && !(fine = wait_warp(&o_free[t], (results[t] - 1) & 1, dead))) break;
             if (!(fine = wait_warp(&p_half[t], walked[t] & 1, dead))) break;
             fence_after();
-            weights_by_rows<0, 0, 4>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > begin, kv_slab, kv_group);
+            weights_by_rows<8, 0, 0, 4>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > begin, kv_slab, kv_group);
             if (!(fine = wait_warp(&p_full[t], walked[t] & 1, dead))) break;
             fence_after();
-            weights_by_rows<0, 4, 8>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
+            weights_by_rows<8, 0, 4, 8>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
             walked[t]++;
             if (j + 1 == last[t]) {
               commit(lead, &o_full[t]);

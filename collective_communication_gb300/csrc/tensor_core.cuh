@@ -252,15 +252,15 @@ __device__ __forceinline__ void rows_by_rows(uint32_t lead, uint32_t d, uint32_t
       multiply(lead, d, a + (((k >> 2) * SLAB + (k & 3) * 32) >> 4), operand_high(kGroup), b + (((k >> 2) * slab + (k & 3) * 32) >> 4),
                high, kind, k > 0);
 }
-// d (+)= w z: w in tensor memory, 128 rows by 128, the second half GAP columns behind the first; z has as many rows, n elements each.
-// The part of them from step FIRST to LAST.
-template <int GAP, int FIRST = 0, int LAST = 8>
+// d (+)= w z: w in tensor memory, 128 rows by 128, its columns in slices of 16 PER elements that begin STRIDE columns
+// apart; z has as many rows, n elements each. The part of them from step FIRST to LAST.
+template <int PER, int STRIDE, int FIRST = 0, int LAST = 8>
 __device__ __forceinline__ void weights_by_rows(uint32_t lead, uint32_t d, uint32_t w, uint32_t z, int n, bool add, uint32_t slab,
                                                 uint32_t group = kGroup) {
   const uint32_t kind = product_of(n, true), b = operand_across(z, slab), high = operand_high(group);
 #pragma unroll
   for (int k = FIRST; k < LAST; k++)
-    multiply_tmem(lead, d, w + 8 * k + (k >> 2) * GAP, b + k * (group >> 3), high, kind, add || k > 0);
+    multiply_tmem(lead, d, w + k / PER * STRIDE + k % PER * 8, b + k * (group >> 3), high, kind, add || k > 0);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

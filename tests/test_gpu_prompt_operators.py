@@ -10,7 +10,10 @@ of binary32 are rounded: among the 4), and exp(s - lse) relatively by E plus the
 roundings of the exponent, 4 u (|s| + |lse|), and a few u for the exponential: `weight`
 below is the largest of that over a row's keys. Weights and score gradients of bf16
 inputs may be rounded to bf16, by 2^-8 of themselves, before they meet values, queries
-or keys. A weight below the smallest normal number, 2^-126, may count as 0. A result is the rounding to its type of a sum that is within these relative
+or keys. A weight below the smallest normal number, 2^-126, may count as 0. The gradient's
+delta may be out . dout, of the out that the call is given, or the sum of p (dout . v) that
+it stands for: they differ by out's rounding and what the forward call leaves, and by the
+errors of p and dout . v. A result is the rounding to its type of a sum that is within these relative
 errors of the magnitudes of the 64-bit computation.
 """
 import itertools
@@ -346,7 +349,11 @@ def check_backward(q, k, v, starts, out, lse, dout, dq, dk, dv, scale=None):
             lsize = (g * o).abs().sum(-1).permute(1, 2, 0)[..., None]
             ds = p * (dp - delta)
             tiny = torch.where(sees, TINY, 0.0)
-            eds = p * (2 * (d + 4) * U * (dsize + lsize)) + ds.abs() * (err + cut(q) + 4 * U) + tiny * (dp - delta).abs()
+            mass = torch.einsum("hgts,shd->thgd", p, value.abs())
+            left = (torch.where(sees, err, 0.0).amax(-1) * 2 + cut(q) + 2 * (b - a + 8) * U).permute(2, 0, 1)[..., None] * mass
+            ddelta = (g.abs() * (left + ROUND[q.dtype] * o.abs())).sum(-1).permute(1, 2, 0)[..., None] + \
+                (p * (dp.abs() * err + 2 * (d + 4) * U * dsize)).sum(-1, keepdim=True)
+            eds = p * (2 * (d + 4) * U * (dsize + lsize) + ddelta) + ds.abs() * (err + cut(q) + 4 * U) + tiny * (dp - delta).abs()
             ep = p * (err + cut(q)) + tiny
             rows, cols = 2 * (b - a + 8) * U, 2 * ((b - a) * (heads // kv) + 8) * U
             want = torch.einsum("hgts,shd->thgd", ds, key).flatten(1, 2) * scale
