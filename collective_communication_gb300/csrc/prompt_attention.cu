@@ -487,7 +487,7 @@ int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, 
   int64_t parts = 0;
   if (group <= 128 && head_dim <= 128 &&
       (tokens / (2 * (128 / group)) + 1) * kv_heads * nranks * 2 <= kPromptSplitBlocks)
-    parts = (int64_t)kPromptSplitBlocks * 256 * ((head_dim <= 64 ? 64 : 128) + 2) * 4;
+    parts = (int64_t)kPromptSplitBlocks * (256 * ((head_dim <= 64 ? 64 : 128) + 2) + kPromptPartInfo) * 4;
   return delta > parts ? delta : parts;
 }
 

@@ -79,10 +79,11 @@ struct Layout {
 struct Split {
   int64_t slots, items;
   int parts;    // that an item's keys are split into
-  float* sums;  // per item and part: 2 x 128 rows of DP binary32, then m and l of each
+  float* sums;  // per item and part: 2 x 128 rows of DP binary32, then m and l of each, then the item (of part 0)
 };
+// of 2 x 128 rows with m and l, and 32 numbers behind them
 template <int DP>
-constexpr int64_t kPartFloats = 2 * kRows * (DP + 2);
+constexpr int64_t kPartFloats = 2 * kRows * (DP + 2) + kPromptPartInfo;
 
 struct Item {
   int there;        // 0: no more
@@ -562,7 +563,8 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       // rows that are none see what the tile's first row sees: they hold anything, and nobody reads them
       const int sees = min(item.before + t * per_tile + (mine ? token : 0) + 1, item.keys);
       const int query = item.head * group + in_group, rank = item.rank, part = item.part;
-      const int64_t at_token = (int64_t)item.first + t * per_tile + token, index = item.index;
+      const int token0 = item.first, both_tokens = item.tokens[0] + item.tokens[1];
+      const int64_t at_token = (int64_t)token0 + t * per_tile + token, index = item.index;
       __syncwarp();
       if (lane == 0) arrive(&item_empty[i % kItemSlots]);
       int least = sees;  // of the warp
@@ -710,6 +712,11 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         }
         arrive(&out_ready[t]);
       }
+      if (split.parts > 1 && part == 0 && threadIdx.x == 0) {
+        int* const info = reinterpret_cast<int*>(sums + 2 * kRows * (DP + 2));
+        info[0] = token0;
+        info[1] = both_tokens;
+      }
       if (mine && split.parts > 1) {
         sums[kRows * DP + row] = m;
         sums[kRows * (DP + 1) + row] = l;
@@ -734,69 +741,90 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
   }
 }
 
-// The parts of a row's keys, in their order; a warp a row, 16 parts' loads under way.
-template <int DP, int FORM>
+// The parts of a row's keys, a block a row: each of its four warps adds up every fourth
+// part, all their loads under way at once, and the four sums join in the warps' order.
+template <int DP>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a,
                                                           const __grid_constant__ Split split) {
-  constexpr int E = DP / 32;  // elements of a lane
+  constexpr int E = DP / 32, kMost = kPromptSplitBlocks / 4, kBatch = 20;  // elements of a lane, parts of a warp
+  __shared__ float partial[4][DP];
   const uint32_t magic = op_start(a.ws);
-  if (!op_ready(a.ws, magic)) return;
-  const int lane = threadIdx.x & 31, r = (int)(blockIdx.x % 64) * 4 + (threadIdx.x >> 5), t = r / kRows, row = r % kRows;
-  const int group = a.q_heads / a.kv_heads, D = a.head_dim, token = row / group;
-  Item item;
-  if (!find_item<FORM>(a, split, (int64_t)(blockIdx.x / 64) * split.parts, &item) || token >= item.tokens[t]) return;
-  const float* sums = split.sums + item.index * split.parts * kPartFloats<DP> + t * kRows * (DP + 2);
-  float m[kPromptSplitBlocks / 32 + 1], top = -INFINITY, sum = 0.f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = (int)(blockIdx.x % (2 * kRows)), t = r / kRows, row = r % kRows;
+  const int group = a.q_heads / a.kv_heads, D = a.head_dim, per_tile = kRows / group, token = row / group;
+  const int64_t index = blockIdx.x / (2 * kRows), lanes = (int64_t)a.kv_heads * a.nranks;
+  const float* const sums = split.sums + index * split.parts * kPartFloats<DP> + t * kRows * (DP + 2);
+  // an item of no tokens has left nothing: whether this is one, only the starts say
+  const int* const info = reinterpret_cast<const int*>(split.sums + index * split.parts * kPartFloats<DP> + 2 * kRows * (DP + 2));
+  float m[kPromptSplitBlocks / 32 + 1], l[kPromptSplitBlocks / 32 + 1];
 #pragma unroll
   for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
     const int k = i * 32 + lane;
     m[i] = k < split.parts ? sums[k * kPartFloats<DP> + kRows * DP + row] : -INFINITY;
-    top = fmaxf(top, m[i]);
+    l[i] = k < split.parts ? sums[k * kPartFloats<DP> + kRows * (DP + 1) + row] : 0.f;
   }
+  const int first = info[0], tokens = info[1];
+  PromptSequence seq;
+  int pair;
+  if (!op_ready(a.ws, magic) || token >= per_tile) return;
+  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, index / lanes, &seq, &pair)) return;
+  if (t * per_tile + token >= tokens) return;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i <= kPromptSplitBlocks / 32; i++) top = fmaxf(top, m[i]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
 #pragma unroll
   for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
-    const int k = i * 32 + lane;
     m[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - top);  // now the part's weight
-    if (k < split.parts) sum = fmaf(sums[k * kPartFloats<DP> + kRows * (DP + 1) + row], m[i], sum);
+    if (m[i] != 0.f) sum = fmaf(l[i], m[i], sum);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   float v[E] = {};
+#pragma unroll 1
+  for (int k0 = 0; k0 < kMost && k0 * 4 < split.parts; k0 += kBatch) {
+    float x[kBatch][E], w[kBatch];
 #pragma unroll
-  for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
+    for (int k = 0; k < kBatch; k++) {
+      const int part = (k0 + k) * 4 + warp;
+      w[k] = 0.f;
 #pragma unroll
-    for (int k0 = 0; k0 < 32; k0 += 16) {
-      if (i * 32 + k0 >= split.parts) continue;
-      float x[16][E], w[16];
-#pragma unroll
-      for (int k = 0; k < 16; k++) {
-        w[k] = __shfl_sync(~0u, m[i], k0 + k);
-        // a part that saw nothing has left nothing
-        const float* p = sums + (i * 32 + k0 + k) * kPartFloats<DP> + row * DP + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          float2 y = make_float2(0.f, 0.f);
-          if (w[k] != 0.f) y = *reinterpret_cast<const float2*>(p + e);
-          x[k][e] = y.x;
-          x[k][e + 1] = y.y;
-        }
+      for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
+        const float y = __shfl_sync(~0u, m[i], part & 31);
+        if (part >> 5 == i) w[k] = y;
       }
+      // a part that saw nothing has left nothing
+      const float* p = sums + part * kPartFloats<DP> + row * DP + lane * E;
 #pragma unroll
-      for (int k = 0; k < 16; k++)
-#pragma unroll
-        for (int e = 0; e < E; e++) v[e] = fmaf(x[k][e], w[k], v[e]);
+      for (int e = 0; e < E; e += 2) {
+        float2 y = make_float2(0.f, 0.f);
+        if (w[k] != 0.f && part < split.parts) y = *reinterpret_cast<const float2*>(p + e);
+        x[k][e] = y.x;
+        x[k][e + 1] = y.y;
+      }
     }
-  }
-  const int64_t at_token = (int64_t)item.first + t * (kRows / group) + token;
-  const int query = item.head * group + row % group;
-  uint16_t* out = (uint16_t*)a.out[item.rank] + at_token * a.out_stride + (int64_t)query * D + lane * E;
-  const float by = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    if (lane * E + e < D) *reinterpret_cast<uint32_t*>(out + e) = bf16_pair(sum == 0.f ? 0.f : v[e] * by, sum == 0.f ? 0.f : v[e + 1] * by);
-  if (lane == 0 && a.lse[item.rank] != nullptr) a.lse[item.rank][at_token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
+    for (int k = 0; k < kBatch; k++)
+#pragma unroll
+      for (int e = 0; e < E; e++) v[e] = fmaf(x[k][e], w[k], v[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; e++) partial[warp][lane * E + e] = v[e];
+  __syncthreads();
+  const int lane_of = (int)(index % lanes), head = lane_of % a.kv_heads, rank = lane_of / a.kv_heads;
+  const int64_t at_token = (int64_t)first + t * per_tile + token;
+  const int query = head * group + row % group, d = threadIdx.x * 2;
+  const float by = sum == 0.f ? 0.f : 1.f / sum;
+  if (d < D) {
+    float y[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      const float z = (partial[0][d + e] + partial[1][d + e]) + (partial[2][d + e] + partial[3][d + e]);
+      y[e] = sum == 0.f ? 0.f : z * by;
+    }
+    *reinterpret_cast<uint32_t*>((uint16_t*)a.out[rank] + at_token * a.out_stride + (int64_t)query * D + d) = bf16_pair(y[0], y[1]);
+  }
+  if (threadIdx.x == 0 && a.lse[rank] != nullptr) a.lse[rank][at_token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
 
 template <int DP, int FORM>
@@ -840,7 +868,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   e = launch_op(fn, dim3((unsigned)(all < blocks ? all : blocks)), Threads<FORM>::kCount, Layout<DP>::kShared, stream, params);
   if (e != cudaSuccess || split.parts == 1) return e;
   void* join_params[] = {&copy, &split};
-  return launch_op((const void*)prompt_join_kernel<DP, FORM>, dim3((unsigned)(split.items * 64)), 128, 0, stream, join_params);
+  return launch_op((const void*)prompt_join_kernel<DP>, dim3((unsigned)(split.items * 2 * kRows)), 128, 0, stream, join_params);
 }
 
 }  // namespace
