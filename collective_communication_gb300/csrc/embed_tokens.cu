@@ -12,10 +12,13 @@
 // in one chunk is stored at once; of others each chunk leaves its part, and the
 // chunk where such a word begins adds the parts up, in order, in a kernel behind.
 // A pair is one 64-bit number, no two alike, so any way of sorting gives the same
-// order: blocks sort tiles of 8192 in shared memory, and if there are several, each
+// order: blocks sort tiles in shared memory (32 pairs in a warp's lanes, then runs merge by
+// bisection), and if there are several, each
 // pair's place is its place in its tile and its places by bisection in the others.
-// Where the tables are not added to, the blocks beside the sorting ones fill them
-// with zeros meanwhile; rows of words that occur are written once more.
+// Where the tables are not added to, further warps of that kernel look their words up
+// in the sorted pairs and fill the rows of those that do not occur with zeros: every
+// row is written once. (Filling whole tables beside the sorting blocks took 187 us
+// where this takes TIME_16385, 16385 tokens of 4096 elements into tables of 32008 words.)
 #include "op_common.cuh"
 #include "rar_launch.h"
 
@@ -23,7 +26,10 @@ namespace rar {
 namespace {
 
 constexpr int kSortThreads = 512;
-constexpr int kTile = 8192;  // pairs of a tile: 64 KiB
+// Pairs of a tile: bisection in shared memory bounds its sort (8192 took 80 us), and the
+// number of tiles the merge's.
+constexpr int kSmallTile = 1024, kLargeTile = 4096;
+constexpr int64_t kManyPairs = 65536;  // with small tiles no more than 64 of them
 constexpr uint64_t kNone = ~0ull;
 
 __device__ __forceinline__ int shard_of(const int64_t* first, int nranks, int64_t word) {
@@ -69,47 +75,54 @@ __global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ Embe
   }
 }
 
-// Blocks 0 .. tiles - 1 sort a tile each; the others fill the tables with zeros.
+// A block sorts a tile.
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_constant__ EmbedBwdArgs a) {
   extern __shared__ uint64_t pair[];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  if ((int)blockIdx.x >= a.tiles) {
-    const int64_t warps = (int64_t)(gridDim.x - a.tiles) * (kSortThreads / 32);
-    const int lane = threadIdx.x & 31;
-    int r = 0;
-    for (int64_t w = (int64_t)(blockIdx.x - a.tiles) * (kSortThreads / 32) + (threadIdx.x >> 5); w < a.first[a.nranks];
-         w += warps) {
-      while (a.first[r + 1] <= w) r++;
-      float* row = a.dtables[r] + (w - a.first[r]) * a.drow_stride[r];
-      for (int d = lane * 4; d < a.hidden; d += 128) *reinterpret_cast<float4*>(row + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    return;
-  }
-  const int64_t at = (int64_t)blockIdx.x * kTile;
-  const int count = (int)min((int64_t)kTile, a.tokens - at);
-  int size = 2;
-  while (size < count) size *= 2;
-  for (int i = threadIdx.x; i < size; i += kSortThreads) {
+  const int64_t at = (int64_t)blockIdx.x * a.tile;
+  const int count = (int)min((int64_t)a.tile, a.tokens - at);
+  // warps sort 32 pairs each, by exchanges between lanes; then runs merge two by two
+  uint64_t *from = pair, *into = pair + a.tile;
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i - lane < count; i += kSortThreads) {
     const int64_t word = i < count ? a.tokens_in[at + i] : -1;
-    pair[i] = word >= 0 && word < a.first[a.nranks] ? (uint64_t)word << 32 | (uint64_t)(at + i) : kNone;
-  }
-  for (int k = 2; k <= size; k *= 2) {
-    for (int j = k / 2; j > 0; j /= 2) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < size / 2; i += kSortThreads) {
-        const int lo = (i & ~(j - 1)) * 2 | (i & (j - 1)), hi = lo | j;
-        const uint64_t x = pair[lo], y = pair[hi];
-        if ((x > y) == ((lo & k) == 0)) {
-          pair[lo] = y;
-          pair[hi] = x;
-        }
+    uint64_t x = word >= 0 && word < a.first[a.nranks] ? (uint64_t)word << 32 | (uint64_t)(at + i) : kNone;
+#pragma unroll
+    for (int k = 2; k <= 32; k *= 2) {
+#pragma unroll
+      for (int j = k / 2; j > 0; j /= 2) {
+        const uint64_t y = __shfl_xor_sync(~0u, x, j);
+        const bool low = (lane & j) == 0, up = (lane & k) == 0;
+        if (low == up ? y < x : y > x) x = y;
       }
     }
+    from[i] = x;
+  }
+  for (int run = 32; run < count; run *= 2) {
+    __syncthreads();
+    // a pair's place among both runs: its own, and by bisection how many of the other run are ahead of it
+#pragma unroll 4
+    for (int i = threadIdx.x; i < count; i += kSortThreads) {
+      const uint64_t x = from[i];
+      const bool second = (i & run) != 0;
+      const int base = i & ~(2 * run - 1), other = second ? base : base + run;
+      int lo = 0, hi = max(0, min(run, count - other));
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        const uint64_t y = from[other + mid];
+        if (second ? y <= x : y < x) lo = mid + 1;
+        else hi = mid;
+      }
+      into[base + (i & (run - 1)) + lo] = x;
+    }
+    uint64_t* const t = from;
+    from = into;
+    into = t;
   }
   __syncthreads();
   uint64_t* to = a.tiles == 1 ? a.sorted : a.sorted_tiles;
-  for (int i = threadIdx.x; i < count; i += kSortThreads) to[at + i] = pair[i];
+  for (int i = threadIdx.x; i < count; i += kSortThreads) to[at + i] = from[i];
 }
 
 // Tiles to one row of pairs. Tokens that ask for nothing are alike: their order is of no matter, they stay behind.
@@ -119,19 +132,22 @@ __global__ void __launch_bounds__(256) embed_merge_kernel(const __grid_constant_
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= a.tokens) return;
   const uint64_t x = a.sorted_tiles[i];
-  const int mine = (int)(i / kTile);
-  int64_t place = i % kTile;
-  for (int t = 0; t < a.tiles; t++) {
-    if (t == mine) continue;
-    const uint64_t* tile = a.sorted_tiles + (int64_t)t * kTile;
-    int lo = 0, hi = (int)min((int64_t)kTile, a.tokens - (int64_t)t * kTile);
-    while (lo < hi) {  // pairs of the tile below x; of those alike (none's) the ones in tiles ahead
-      const int mid = (lo + hi) >> 1;
-      const uint64_t y = tile[mid];
-      if (y < x || (y == x && t < mine)) lo = mid + 1;
-      else hi = mid;
+  const int mine = (int)(i / a.tile), last = a.tiles - 1, left = (int)(a.tokens - (int64_t)last * a.tile);
+  int64_t place = i - (int64_t)mine * a.tile;
+  constexpr int kAtOnce = 8;  // tiles that are searched side by side
+  for (int t0 = 0; t0 < a.tiles; t0 += kAtOnce) {
+    int below[kAtOnce] = {};  // pairs of the tile below x; of those alike (none's) the ones in tiles ahead
+    for (int step = a.tile; step > 0; step >>= 1) {
+#pragma unroll
+      for (int k = 0; k < kAtOnce; k++) {
+        const int t = t0 + k, at = below[k] + step, count = t < last ? a.tile : t == last ? left : 0;
+        if (t == mine || at > count) continue;
+        const uint64_t y = a.sorted_tiles[(int64_t)t * a.tile + at - 1];
+        if (y < x || (y == x && t < mine)) below[k] = at;
+      }
     }
-    place += lo;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; k++) place += below[k];
   }
   a.sorted[place] = x;
 }
@@ -158,6 +174,29 @@ __device__ __forceinline__ float* part_of(const EmbedBwdArgs& a, int64_t c, int 
   return a.parts + (c * 2 + side) * a.hidden + d;
 }
 
+// Rows of 0 for the words from `first` on that no token asks for, at most 32; a warp.
+__device__ __forceinline__ void clear_words(const EmbedBwdArgs& a, int64_t first, int count) {
+  const int lane = threadIdx.x & 31;
+  const int64_t mine = first + lane;
+  bool absent = false;
+  if (lane < count && mine < a.first[a.nranks]) {
+    int64_t lo = 0, hi = a.tokens;  // the first pair of the word or a later one
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (word_of(a.sorted[mid]) < (uint32_t)mine) lo = mid + 1;
+      else hi = mid;
+    }
+    absent = lo >= a.tokens || word_of(a.sorted[lo]) != (uint32_t)mine;
+  }
+  for (uint32_t left = __ballot_sync(~0u, absent); left != 0; left &= left - 1) {
+    const int64_t word = first + __ffs(left) - 1;
+    const int r = shard_of(a.first, a.nranks, word);
+    float4* const row = reinterpret_cast<float4*>(a.dtables[r] + (word - a.first[r]) * a.drow_stride[r]);
+#pragma unroll 8
+    for (int d = lane; d < a.hidden / 4; d += 32) row[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
 template <typename T, int C>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ EmbedBwdArgs a) {
   constexpr int kAhead = 8;
@@ -165,6 +204,11 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
   if (!op_ready(a.ws, magic)) return;
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (unit >= a.sum_units) {
+    const int64_t first = (unit - a.sum_units) * a.clear_rows;
+    if (first < a.first[a.nranks]) clear_words(a, first, a.clear_rows);
+    return;
+  }
   const int64_t c = unit / a.spans, i0 = c * C;
   const int d = (int)(unit % a.spans) * 256 + lane * 8;
   if (i0 >= a.tokens) return;
@@ -228,20 +272,37 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
   const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t c = unit / a.spans, end = (c + 1) * C;
   const int d = (int)(unit % a.spans) * 256 + lane * 8;
-  if (end >= a.tokens || d >= a.hidden) return;
+  if (end >= a.tokens) return;
   const uint32_t word = word_of(a.sorted[end - 1]);
   if (word == ~0u || word_of(a.sorted[end]) != word) return;
   if (word_of(a.sorted[c * C]) == word && c > 0 && word_of(a.sorted[c * C - 1]) == word) return;  // it began ahead
   float sum[8], v[8];
   Pack8<float> x;
-  x.load(part_of(a, c, 1, d));
+  x.zero();
+  if (d < a.hidden) x.load(part_of(a, c, 1, d));
   x.widen(sum);
-  for (int64_t k = c + 1; k * C < a.tokens && word_of(a.sorted[k * C]) == word; k++) {
-    x.load(part_of(a, k, 0, d));
-    x.widen(v);
+  // 32 chunks at a time: how many of them begin with the word, then their parts, eight under way
+  for (int64_t k0 = c + 1;; k0 += 32) {
+    const int64_t k = k0 + lane;
+    const uint32_t on = __ballot_sync(~0u, k * C < a.tokens && word_of(a.sorted[k * C]) == word);
+    const int count = __popc(on);
+    for (int i0 = 0; i0 < count; i0 += 8) {
+      Pack8<float> y[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) sum[j] += v[j];
+      for (int i = 0; i < 8; i++) {
+        y[i].zero();
+        if (i0 + i < count && d < a.hidden) y[i].load(part_of(a, k0 + i0 + i, 0, d));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        y[i].widen(v);
+#pragma unroll
+        for (int j = 0; j < 8; j++) sum[j] += v[j];
+      }
+    }
+    if (count < 32) break;
   }
+  if (d >= a.hidden) return;
   store_sum(a, word, d, sum);
 }
 
@@ -249,10 +310,14 @@ template <typename T, int C>
 cudaError_t sums(EmbedBwdArgs& a, cudaStream_t stream) {
   void* params[] = {&a};
   const int64_t units = div_up(a.tokens, C) * a.spans;
-  const dim3 grid((unsigned)div_up(units, 8));
-  const cudaError_t e = launch_op((const void*)embed_sum_kernel<T, C>, grid, 256, 0, stream, params);
+  a.sum_units = div_up(units, 8) * 8;
+  // a warp's rows: 32 KiB of them, one at least
+  a.clear_rows = (int)(8192 / a.hidden < 1 ? 1 : 8192 / a.hidden > 32 ? 32 : 8192 / a.hidden);
+  const int64_t clears = a.accumulate ? 0 : div_up(a.first[a.nranks], a.clear_rows);
+  const cudaError_t e = launch_op((const void*)embed_sum_kernel<T, C>, dim3((unsigned)(a.sum_units / 8 + div_up(clears, 8))), 256, 0,
+                                  stream, params);
   if (e != cudaSuccess || a.tokens <= C) return e;
-  return launch_op((const void*)embed_join_kernel<C>, grid, 256, 0, stream, params);
+  return launch_op((const void*)embed_join_kernel<C>, dim3((unsigned)div_up(units, 8)), 256, 0, stream, params);
 }
 
 // Chunks of 32 tokens leave less to join; of 8, where they would make too few warps.
@@ -278,16 +343,18 @@ cudaError_t launch_embed_tokens_bwd(EmbedBwdArgs& a, cudaStream_t stream) {
   a.sorted = (uint64_t*)scratch;
   a.sorted_tiles = (uint64_t*)(scratch + align_up(a.tokens * 8, 256));
   a.parts = (float*)(scratch + 2 * align_up(a.tokens * 8, 256));
-  a.tiles = (int)div_up(a.tokens, kTile);
+  a.tile = a.tokens <= kManyPairs ? kSmallTile : kLargeTile;
+  a.tiles = (int)div_up(a.tokens, a.tile);
   a.spans = (int)div_up(a.hidden, 256);
   int blocks = 0;
-  cudaError_t e = resident_blocks((const void*)embed_sort_kernel, kSortThreads, kTile * 8, &blocks);
+  cudaError_t e = resident_blocks((const void*)embed_sort_kernel, kSortThreads, 2 * kLargeTile * 8, &blocks);
   if (e != cudaSuccess) return e;
-  const int zeros = a.accumulate ? 0 : (int)(a.first[a.nranks] < blocks * 16 ? div_up(a.first[a.nranks], 16) : blocks);
-  if (a.tiles + zeros == 0) return cudaSuccess;
+  if (a.accumulate && a.tokens == 0) return cudaSuccess;
   void* params[] = {&a};
-  e = launch_op((const void*)embed_sort_kernel, dim3((unsigned)(a.tiles + zeros)), kSortThreads, kTile * 8, stream, params);
-  if (e != cudaSuccess || a.tokens == 0) return e;
+  if (a.tokens > 0) {
+    e = launch_op((const void*)embed_sort_kernel, dim3((unsigned)a.tiles), kSortThreads, 2 * a.tile * 8, stream, params);
+    if (e != cudaSuccess) return e;
+  }
   if (a.tiles > 1) {
     e = launch_op((const void*)embed_merge_kernel, dim3((unsigned)div_up(a.tokens, 256)), 256, 0, stream, params);
     if (e != cudaSuccess) return e;

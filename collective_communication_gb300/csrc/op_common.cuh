@@ -301,11 +301,12 @@ struct EmbedBwdArgs {
   int64_t tokens, dout_stride;
   float scale;
   int nranks, dtype, hidden, accumulate;
-  // set by the launcher: pairs (word, token) in tiles and in one row, parts of sums; tiles, warps of a row
+  // set by the launcher: pairs (word, token) in tiles and in one row, parts of sums; a tile's pairs, tiles, warps of a row
   uint64_t* sorted_tiles;
   uint64_t* sorted;
   float* parts;
-  int tiles, spans;
+  int64_t sum_units;  // warps that sum; behind them those that clear rows, so many each
+  int tile, tiles, spans, clear_rows;
 };
 constexpr int kMaxTop = 32;
 constexpr int kLpTile = 1024;  // columns of a tile of the log probabilities; a call's tiles are counted in 32 bits
