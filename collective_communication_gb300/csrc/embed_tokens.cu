@@ -9,8 +9,8 @@
 // The gradient sums in an order that no run changes, with no atomics on values: the
 // pairs (word, t) are sorted, and a warp sums a chunk of 32 (few tokens: 8) sorted
 // tokens by 256 columns, its loads in flight eight at a time. A word whose tokens lie
-// in one chunk is stored at once; of others each chunk leaves its part, and the
-// chunk where such a word begins adds the parts up, in order, in a kernel behind.
+// in one chunk is stored at once; the parts of others meet in shared memory, eight
+// chunks a block, and of words of several blocks in a kernel behind, always in order.
 // A pair is one 64-bit number, no two alike, so any way of sorting gives the same
 // order: blocks sort tiles in shared memory (32 pairs in a warp's lanes, then runs merge by
 // bisection), and if there are several, each
@@ -25,12 +25,13 @@
 namespace rar {
 namespace {
 
+constexpr int kChunks = 8;  // of a block, a warp each
 constexpr int kSortThreads = 512;
 // Pairs of a tile: bisection in shared memory bounds its sort (8192 took 80 us), and the
 // number of tiles the merge's.
 constexpr int kSmallTile = 1024, kLargeTile = 4096;
 constexpr int64_t kManyPairs = 65536;  // with small tiles no more than 64 of them
-constexpr uint64_t kNone = ~0ull;
+constexpr uint64_t kNone = ~0ull, kAbove = ~0ull - 1;  // no word; no pair, above every word's
 
 __device__ __forceinline__ int shard_of(const int64_t* first, int nranks, int64_t word) {
   int r = 0;
@@ -126,10 +127,10 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
 }
 
 // Tiles to one row of pairs. Tokens that ask for nothing are alike: their order is of no matter, they stay behind.
-__global__ void __launch_bounds__(256) embed_merge_kernel(const __grid_constant__ EmbedBwdArgs a) {
+__global__ void __launch_bounds__(128) embed_merge_kernel(const __grid_constant__ EmbedBwdArgs a) {
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
   if (i >= a.tokens) return;
   const uint64_t x = a.sorted_tiles[i];
   const int mine = (int)(i / a.tile), last = a.tiles - 1, left = (int)(a.tokens - (int64_t)last * a.tile);
@@ -138,13 +139,16 @@ __global__ void __launch_bounds__(256) embed_merge_kernel(const __grid_constant_
   for (int t0 = 0; t0 < a.tiles; t0 += kAtOnce) {
     int below[kAtOnce] = {};  // pairs of the tile below x; of those alike (none's) the ones in tiles ahead
     for (int step = a.tile; step > 0; step >>= 1) {
+      uint64_t y[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; k++) {
-        const int t = t0 + k, at = below[k] + step, count = t < last ? a.tile : t == last ? left : 0;
-        if (t == mine || at > count) continue;
-        const uint64_t y = a.sorted_tiles[(int64_t)t * a.tile + at - 1];
-        if (y < x || (y == x && t < mine)) below[k] = at;
+        const int t = t0 + k, at = below[k] + step, count = t == mine ? 0 : t < last ? a.tile : t == last ? left : 0;
+        y[k] = kAbove;
+        if (at <= count) y[k] = a.sorted_tiles[(int64_t)t * a.tile + at - 1];
       }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; k++)
+        if (y[k] != kAbove && (y[k] < x || (y[k] == x && t0 + k < mine))) below[k] += step;
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; k++) place += below[k];
@@ -169,7 +173,7 @@ __device__ __forceinline__ void store_sum(const EmbedBwdArgs& a, uint32_t word, 
   x.store(row);
 }
 
-// Where chunk c leaves its part of a word that began ahead of it (side 0) or goes on behind it (side 1).
+// Where block c's chunks leave their part of a word that began ahead of them (side 0) or goes on behind them (side 1).
 __device__ __forceinline__ float* part_of(const EmbedBwdArgs& a, int64_t c, int side, int d) {
   return a.parts + (c * 2 + side) * a.hidden + d;
 }
@@ -203,25 +207,30 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (unit >= a.sum_units) {
-    const int64_t first = (unit - a.sum_units) * a.clear_rows;
+  const int warp = threadIdx.x >> 5;
+  if (blockIdx.x >= a.sum_blocks) {
+    const int64_t first = ((int64_t)(blockIdx.x - a.sum_blocks) * kChunks + warp) * a.clear_rows;
     if (first < a.first[a.nranks]) clear_words(a, first, a.clear_rows);
     return;
   }
-  const int64_t c = unit / a.spans, i0 = c * C;
-  const int d = (int)(unit % a.spans) * 256 + lane * 8;
-  if (i0 >= a.tokens) return;
+  // parts of a word that began ahead of a warp's chunk, and of one that begins in it and goes on behind it; whether the
+  // first is the whole chunk and goes on
+  __shared__ __align__(16) float head_part[kChunks][256], tail_part[kChunks][256];
+  __shared__ int goes_on[kChunks];
+  const int64_t block = blockIdx.x / a.spans, c = block * kChunks + warp, i0 = c * C;
+  const int d = (int)(blockIdx.x % a.spans) * 256 + lane * 8;
   // the chunk's pairs, a lane each, and the words next to it
   const uint64_t mine = lane < C && i0 + lane < a.tokens ? a.sorted[i0 + lane] : kNone;
-  const uint32_t before = i0 > 0 ? word_of(a.sorted[i0 - 1]) : ~0u;
+  const uint32_t before = i0 > 0 && i0 <= a.tokens ? word_of(a.sorted[i0 - 1]) : ~0u;
   const uint32_t behind = i0 + C < a.tokens ? word_of(a.sorted[i0 + C]) : ~0u;
   float sum[8] = {};
   uint32_t word = word_of(__shfl_sync(~0u, mine, 0));
-  bool head = word == before;  // the present word began in a chunk ahead
-  if (word == ~0u) return;
+  const bool began_ahead = word != ~0u && word == before;
+  bool head = began_ahead;  // the present word did
+  Pack8<float> y;
 #pragma unroll
   for (int b = 0; b < C; b += kAhead) {
+    if (word == ~0u) break;
     Pack8<T> x[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; i++) {
@@ -233,12 +242,11 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
     for (int i = 0; i < kAhead; i++) {
       const uint32_t next = word_of(__shfl_sync(~0u, mine, b + i));
       if (next != word) {
-        if (d < a.hidden && word != ~0u) {
+        if (word != ~0u) {
           if (head) {
-            Pack8<float> y;
             y.narrow(sum);
-            y.store(part_of(a, c, 0, d));
-          } else {
+            y.store(&head_part[warp][lane * 8]);
+          } else if (d < a.hidden) {
             store_sum(a, word, d, sum);
           }
         }
@@ -253,38 +261,66 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
       for (int j = 0; j < 8; j++) sum[j] += v[j];
     }
   }
-  if (word == ~0u || d >= a.hidden) return;
-  if (head || word == behind) {
-    Pack8<float> y;
+  const bool on = word != ~0u && word == behind;  // the last word goes on
+  if (head || on) {
     y.narrow(sum);
-    y.store(part_of(a, c, head ? 0 : 1, d));
-  } else {
+    y.store(head ? &head_part[warp][lane * 8] : &tail_part[warp][lane * 8]);
+  } else if (word != ~0u && d < a.hidden) {
     store_sum(a, word, d, sum);
+  }
+  if (lane == 0) goes_on[warp] = head && on;
+  __syncthreads();
+  if (d >= a.hidden) return;
+  // the block's parts of a word, one after another
+  const bool begins = on && !head;  // here, and goes on
+  if (!begins && !(warp == 0 && began_ahead)) return;
+  for (int which = 0; which < 2; which++) {
+    if (which == 0 ? !(warp == 0 && began_ahead) : !begins) continue;
+    float v[8];
+    y.load(which == 0 ? &head_part[0][lane * 8] : &tail_part[warp][lane * 8]);
+    y.widen(sum);
+    int w = warp;
+    bool more = which == 0 ? goes_on[0] != 0 : true;
+    while (more && w + 1 < kChunks) {
+      w++;
+      y.load(&head_part[w][lane * 8]);
+      y.widen(v);
+#pragma unroll
+      for (int j = 0; j < 8; j++) sum[j] += v[j];
+      more = goes_on[w] != 0;
+    }
+    if (which == 0 || more) {
+      y.narrow(sum);
+      y.store(part_of(a, block, which, d));
+    } else {
+      store_sum(a, word, d, sum);
+    }
   }
 }
 
-// The parts of each word that lies in several chunks, by the chunk in which it begins.
-template <int C>
+// The parts of each word that lies in several blocks' chunks of B tokens, by the block in which it begins.
+template <int B>
 __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__ EmbedBwdArgs a) {
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t c = unit / a.spans, end = (c + 1) * C;
+  const int64_t c = unit / a.spans, end = (c + 1) * B;
   const int d = (int)(unit % a.spans) * 256 + lane * 8;
   if (end >= a.tokens) return;
-  const uint32_t word = word_of(a.sorted[end - 1]);
-  if (word == ~0u || word_of(a.sorted[end]) != word) return;
-  if (word_of(a.sorted[c * C]) == word && c > 0 && word_of(a.sorted[c * C - 1]) == word) return;  // it began ahead
+  const uint32_t word = word_of(a.sorted[end - 1]), next = word_of(a.sorted[end]), first = word_of(a.sorted[c * B]),
+                 ahead = c > 0 ? word_of(a.sorted[c * B - 1]) : ~0u;
+  if (word == ~0u || next != word) return;
+  if (first == word && ahead == word) return;  // it began ahead
   float sum[8], v[8];
   Pack8<float> x;
   x.zero();
   if (d < a.hidden) x.load(part_of(a, c, 1, d));
   x.widen(sum);
-  // 32 chunks at a time: how many of them begin with the word, then their parts, eight under way
+  // 32 blocks at a time: how many of them begin with the word, then their parts, eight under way
   for (int64_t k0 = c + 1;; k0 += 32) {
     const int64_t k = k0 + lane;
-    const uint32_t on = __ballot_sync(~0u, k * C < a.tokens && word_of(a.sorted[k * C]) == word);
+    const uint32_t on = __ballot_sync(~0u, k * B < a.tokens && word_of(a.sorted[k * B]) == word);
     const int count = __popc(on);
     for (int i0 = 0; i0 < count; i0 += 8) {
       Pack8<float> y[8];
@@ -309,15 +345,16 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
 template <typename T, int C>
 cudaError_t sums(EmbedBwdArgs& a, cudaStream_t stream) {
   void* params[] = {&a};
-  const int64_t units = div_up(a.tokens, C) * a.spans;
-  a.sum_units = div_up(units, 8) * 8;
+  constexpr int B = C * kChunks;
+  const int64_t units = div_up(a.tokens, B) * a.spans;
+  a.sum_blocks = units;
   // a warp's rows: 32 KiB of them, one at least
   a.clear_rows = (int)(8192 / a.hidden < 1 ? 1 : 8192 / a.hidden > 32 ? 32 : 8192 / a.hidden);
-  const int64_t clears = a.accumulate ? 0 : div_up(a.first[a.nranks], a.clear_rows);
-  const cudaError_t e = launch_op((const void*)embed_sum_kernel<T, C>, dim3((unsigned)(a.sum_units / 8 + div_up(clears, 8))), 256, 0,
-                                  stream, params);
-  if (e != cudaSuccess || a.tokens <= C) return e;
-  return launch_op((const void*)embed_join_kernel<C>, dim3((unsigned)div_up(units, 8)), 256, 0, stream, params);
+  const int64_t clears = a.accumulate ? 0 : div_up(a.first[a.nranks], (int64_t)a.clear_rows * kChunks);
+  const cudaError_t e =
+      launch_op((const void*)embed_sum_kernel<T, C>, dim3((unsigned)(units + clears)), 32 * kChunks, 0, stream, params);
+  if (e != cudaSuccess || a.tokens <= B) return e;
+  return launch_op((const void*)embed_join_kernel<B>, dim3((unsigned)div_up(units, 8)), 256, 0, stream, params);
 }
 
 // Chunks of 32 tokens leave less to join; of 8, where they would make too few warps.
@@ -327,7 +364,7 @@ bool short_chunks(int64_t tokens, int hidden) { return div_up(tokens, 32) * div_
 
 int64_t embed_tokens_scratch_bytes(int64_t tokens, int hidden) {
   const int chunk = short_chunks(tokens, hidden) ? 8 : 32;
-  return 2 * align_up(tokens * 8, 256) + div_up(tokens, chunk) * 2 * hidden * 4;
+  return 2 * align_up(tokens * 8, 256) + div_up(tokens, chunk * kChunks) * 2 * hidden * 4;
 }
 
 cudaError_t launch_embed_tokens(EmbedArgs& a, cudaStream_t stream) {
@@ -356,7 +393,7 @@ cudaError_t launch_embed_tokens_bwd(EmbedBwdArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   if (a.tiles > 1) {
-    e = launch_op((const void*)embed_merge_kernel, dim3((unsigned)div_up(a.tokens, 256)), 256, 0, stream, params);
+    e = launch_op((const void*)embed_merge_kernel, dim3((unsigned)div_up(a.tokens, 128)), 128, 0, stream, params);
     if (e != cudaSuccess) return e;
   }
   const bool few = short_chunks(a.tokens, a.hidden);

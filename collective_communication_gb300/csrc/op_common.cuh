@@ -305,7 +305,7 @@ struct EmbedBwdArgs {
   uint64_t* sorted_tiles;
   uint64_t* sorted;
   float* parts;
-  int64_t sum_units;  // warps that sum; behind them those that clear rows, so many each
+  int64_t sum_blocks;  // blocks that sum; the warps of those behind them clear rows, so many each
   int tile, tiles, spans, clear_rows;
 };
 constexpr int kMaxTop = 32;
