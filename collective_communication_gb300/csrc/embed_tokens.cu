@@ -26,12 +26,13 @@ namespace rar {
 namespace {
 
 constexpr int kChunks = 8;  // of a block, a warp each
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 512, kMergeThreads = 512;
+constexpr int kMergePairs = 16384;  // of whole tiles, in a merging block's shared memory
 // Pairs of a tile: bisection in shared memory bounds its sort (8192 took 80 us), and the
 // number of tiles the merge's.
 constexpr int kSmallTile = 1024, kLargeTile = 4096;
 constexpr int64_t kManyPairs = 65536;  // with small tiles no more than 64 of them
-constexpr uint64_t kNone = ~0ull, kAbove = ~0ull - 1;  // no word; no pair, above every word's
+constexpr uint64_t kNone = (uint64_t)~0u << 32;  // with the token's number: a token of no word
 
 __device__ __forceinline__ int shard_of(const int64_t* first, int nranks, int64_t word) {
   int r = 0;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
   const int lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i - lane < count; i += kSortThreads) {
     const int64_t word = i < count ? a.tokens_in[at + i] : -1;
-    uint64_t x = word >= 0 && word < a.first[a.nranks] ? (uint64_t)word << 32 | (uint64_t)(at + i) : kNone;
+    uint64_t x = (word >= 0 && word < a.first[a.nranks] ? (uint64_t)word << 32 : kNone) | (uint64_t)(at + i);
 #pragma unroll
     for (int k = 2; k <= 32; k *= 2) {
 #pragma unroll
@@ -106,13 +107,12 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
 #pragma unroll 4
     for (int i = threadIdx.x; i < count; i += kSortThreads) {
       const uint64_t x = from[i];
-      const bool second = (i & run) != 0;
-      const int base = i & ~(2 * run - 1), other = second ? base : base + run;
+      const int base = i & ~(2 * run - 1), other = (i & run) != 0 ? base : base + run;
       int lo = 0, hi = max(0, min(run, count - other));
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         const uint64_t y = from[other + mid];
-        if (second ? y <= x : y < x) lo = mid + 1;
+        if (y < x) lo = mid + 1;
         else hi = mid;
       }
       into[base + (i & (run - 1)) + lo] = x;
@@ -126,34 +126,42 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
   for (int i = threadIdx.x; i < count; i += kSortThreads) to[at + i] = from[i];
 }
 
-// Tiles to one row of pairs. Tokens that ask for nothing are alike: their order is of no matter, they stay behind.
-__global__ void __launch_bounds__(128) embed_merge_kernel(const __grid_constant__ EmbedBwdArgs a) {
+// Tiles to one row of pairs, a thread a pair; tokens that ask for nothing stay behind.
+// Blocks bisect in shared memory, 128 KiB of tiles at a time: in global memory, with a
+// tenth of the pairs in L1 at first, 17 tiles took 36 us.
+__global__ void __launch_bounds__(kMergeThreads) embed_merge_kernel(const __grid_constant__ EmbedBwdArgs a) {
+  extern __shared__ uint64_t pair[];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  if (i >= a.tokens) return;
-  const uint64_t x = a.sorted_tiles[i];
-  const int mine = (int)(i / a.tile), last = a.tiles - 1, left = (int)(a.tokens - (int64_t)last * a.tile);
-  int64_t place = i - (int64_t)mine * a.tile;
-  constexpr int kAtOnce = 8;  // tiles that are searched side by side
-  for (int t0 = 0; t0 < a.tiles; t0 += kAtOnce) {
-    int below[kAtOnce] = {};  // pairs of the tile below x; of those alike (none's) the ones in tiles ahead
-    for (int step = a.tile; step > 0; step >>= 1) {
-      uint64_t y[kAtOnce];
+  const int64_t i = (int64_t)blockIdx.x * kMergeThreads + threadIdx.x;
+  const bool live = i < a.tokens;
+  const uint64_t x = live ? a.sorted_tiles[i] : 0;
+  const int64_t mine = i / a.tile;
+  int64_t place = i - mine * a.tile;
+  for (int64_t from = 0; from < a.tokens; from += kMergePairs) {
+    const int count = (int)min((int64_t)kMergePairs, a.tokens - from);
+    __syncthreads();
+#pragma unroll 8
+    for (int j = threadIdx.x; j < count; j += kMergeThreads) pair[j] = a.sorted_tiles[from + j];
+    __syncthreads();
+    constexpr int kAtOnce = 4;  // tiles that are searched side by side
+    for (int t0 = 0; t0 < count; t0 += kAtOnce * a.tile) {
+      int at[kAtOnce], end[kAtOnce], start[kAtOnce];  // the tiles' pairs below x end before `at`
 #pragma unroll
       for (int k = 0; k < kAtOnce; k++) {
-        const int t = t0 + k, at = below[k] + step, count = t == mine ? 0 : t < last ? a.tile : t == last ? left : 0;
-        y[k] = kAbove;
-        if (at <= count) y[k] = a.sorted_tiles[(int64_t)t * a.tile + at - 1];
+        start[k] = at[k] = min(t0 + k * a.tile, count);
+        end[k] = (from + start[k]) / a.tile == mine ? start[k] : min(start[k] + a.tile, count);
+      }
+      for (int step = a.tile; step > 0; step >>= 1) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++)
+          if (at[k] + step <= end[k] && pair[at[k] + step - 1] < x) at[k] += step;
       }
 #pragma unroll
-      for (int k = 0; k < kAtOnce; k++)
-        if (y[k] != kAbove && (y[k] < x || (y[k] == x && t0 + k < mine))) below[k] += step;
+      for (int k = 0; k < kAtOnce; k++) place += at[k] - start[k];
     }
-#pragma unroll
-    for (int k = 0; k < kAtOnce; k++) place += below[k];
   }
-  a.sorted[place] = x;
+  if (live) a.sorted[place] = x;
 }
 
 __device__ __forceinline__ uint32_t word_of(uint64_t pair) { return (uint32_t)(pair >> 32); }
@@ -393,7 +401,10 @@ cudaError_t launch_embed_tokens_bwd(EmbedBwdArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   if (a.tiles > 1) {
-    e = launch_op((const void*)embed_merge_kernel, dim3((unsigned)div_up(a.tokens, 128)), 128, 0, stream, params);
+    e = resident_blocks((const void*)embed_merge_kernel, kMergeThreads, kMergePairs * 8, &blocks);
+    if (e != cudaSuccess) return e;
+    e = launch_op((const void*)embed_merge_kernel, dim3((unsigned)div_up(a.tokens, kMergeThreads)), kMergeThreads, kMergePairs * 8,
+                  stream, params);
     if (e != cudaSuccess) return e;
   }
   const bool few = short_chunks(a.tokens, a.hidden);
