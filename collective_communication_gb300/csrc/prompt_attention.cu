@@ -13,9 +13,13 @@
 // crosses blocks, so results are the same bits every time.
 //
 // Threads are 16 by 16; thread (ty, tx) has rows ty + 16 i and columns tx + 16 j of a
-// tile's scores, and elements 4 tx + 64 c of the rows' results: operands come as
-// 16-byte loads that half a warp shares or that fall on all banks. Products run two
-// at a time along the head (scores) or across it (results).
+// tile's scores, and elements 2 tx + 32 c and the next of the rows' results: operands
+// come as loads that half a warp shares or that fall on all banks. Products run two at a
+// time along the head (scores) or across it (results). What bounds them is the two
+// multiply-adds a lane and cycle, and the latency of a tile's loads: keys and values take
+// turns in one buffer, so that two blocks fit an SM up to a head size of 128 and one
+// works while the other waits (a buffer each and head sizes padded to 64 or 128: 340 us
+// for 2777 tokens of 12 heads of 80 where this takes TIME_F32).
 #include "op_common.cuh"
 #include "prompt_attention.cuh"
 #include "rar_launch.h"
@@ -33,28 +37,36 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(uint16_t* p, float x, float y) { *reinterpret_cast<uint32_t*>(p) = bf16_pair(x, y); }
+
 template <int DP, int BT>
 struct Shape {
   static constexpr int MT = BT / 16;   // rows, and columns, of a thread
-  static constexpr int NC = DP / 64;   // groups of four elements of a result row
+  static constexpr int NC = DP / 32;   // pairs of elements of a result row
   static constexpr int LD = DP + 4;    // floats from row to row: 16-byte loads of 16 rows fall on different banks
   static constexpr int LP = BT + 4;
   static constexpr int kRows = BT * LD, kScores = BT * LP;
 };
 
-// BT rows of D elements, widened, zeros past D and where at(row) is null.
+// BT rows of D elements, widened, zeros past D and where at(row) is null; loads first, then stores.
 template <typename T, int DP, int BT, typename At>
 __device__ __forceinline__ void load_rows(float* to, int D, At at) {
-  constexpr int C = DP / 8;
-  for (int i = threadIdx.x; i < BT * C; i += kThreads) {
-    const int row = i / C, d = (i % C) * 8;
-    float v[8] = {};
+  constexpr int C = DP / 8, N = BT * C / kThreads;
+  static_assert(BT * C % kThreads == 0, "pieces of a thread");
+  Pack8<T> x[N];
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const int k = threadIdx.x + i * kThreads, row = k / C, d = (k % C) * 8;
     const T* p = at(row);
-    if (p != nullptr && d < D) {
-      Pack8<T> x;
-      x.load(p + d);
-      x.widen(v);
-    }
+    x[i].zero();
+    if (p != nullptr && d < D) x[i].load(p + d);
+  }
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const int k = threadIdx.x + i * kThreads, row = k / C, d = (k % C) * 8;
+    float v[8];
+    x[i].widen(v);
     float* o = to + row * Shape<DP, BT>::LD + d;
     store4(o, v[0], v[1], v[2], v[3]);
     store4(o + 4, v[4], v[5], v[6], v[7]);
@@ -63,7 +75,7 @@ __device__ __forceinline__ void load_rows(float* to, int D, At at) {
 
 // s[i][j] = x[ty + 16 i] . y[tx + 16 j]
 template <int DP, int BT>
-__device__ __forceinline__ void dots(const float* x, const float* y, float (&s)[BT / 16][BT / 16]) {
+__device__ __forceinline__ void dots(const float* x, const float* y, int D, float (&s)[BT / 16][BT / 16]) {
   using S = Shape<DP, BT>;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   F2 acc[S::MT][S::MT];
@@ -71,8 +83,8 @@ __device__ __forceinline__ void dots(const float* x, const float* y, float (&s)[
   for (int i = 0; i < S::MT; i++)
 #pragma unroll
     for (int j = 0; j < S::MT; j++) acc[i][j] = f2(0.f, 0.f);
-#pragma unroll 4
-  for (int d = 0; d < DP; d += 4) {
+#pragma unroll 2
+  for (int d = 0; d < D; d += 4) {
     float4 a[S::MT], b[S::MT];
 #pragma unroll
     for (int i = 0; i < S::MT; i++) {
@@ -97,40 +109,36 @@ __device__ __forceinline__ void dots(const float* x, const float* y, float (&s)[
 }
 
 template <int DP, int BT>
-struct Sums {  // elements 4 tx + 64 c of rows ty + 16 i
-  F2 v[BT / 16][DP / 64][2];
+struct Sums {  // elements 2 tx + 32 c and the next of rows ty + 16 i
+  using S = Shape<DP, BT>;
+  F2 v[S::MT][S::NC];
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < BT / 16; i++)
+    for (int i = 0; i < S::MT; i++)
 #pragma unroll
-      for (int c = 0; c < DP / 64; c++) v[i][c][0] = v[i][c][1] = f2(0.f, 0.f);
+      for (int c = 0; c < S::NC; c++) v[i][c] = f2(0.f, 0.f);
   }
   __device__ __forceinline__ void scale_row(int i, float by) {
 #pragma unroll
-    for (int c = 0; c < DP / 64; c++) {
-      v[i][c][0] = mul2(v[i][c][0], f2(by, by));
-      v[i][c][1] = mul2(v[i][c][1], f2(by, by));
-    }
+    for (int c = 0; c < S::NC; c++) v[i][c] = mul2(v[i][c], f2(by, by));
   }
   // += sum over t of w[ty + 16 i][t] x[t]
   __device__ __forceinline__ void add(const float* w, const float* x) {
-    using S = Shape<DP, BT>;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll 2
     for (int t = 0; t < BT; t += 4) {
-      float4 u[BT / 16];
+      float4 u[S::MT];
 #pragma unroll
-      for (int i = 0; i < BT / 16; i++) u[i] = *reinterpret_cast<const float4*>(w + (ty + 16 * i) * S::LP + t);
+      for (int i = 0; i < S::MT; i++) u[i] = *reinterpret_cast<const float4*>(w + (ty + 16 * i) * S::LP + t);
 #pragma unroll
       for (int k = 0; k < 4; k++)
 #pragma unroll
-        for (int c = 0; c < DP / 64; c++) {
-          const float4 y = *reinterpret_cast<const float4*>(x + (t + k) * S::LD + 4 * tx + 64 * c);
+        for (int c = 0; c < S::NC; c++) {
+          const float2 y = *reinterpret_cast<const float2*>(x + (t + k) * S::LD + 2 * tx + 32 * c);
 #pragma unroll
-          for (int i = 0; i < BT / 16; i++) {
+          for (int i = 0; i < S::MT; i++) {
             const float z = k == 0 ? u[i].x : k == 1 ? u[i].y : k == 2 ? u[i].z : u[i].w;
-            v[i][c][0] = fma2(f2(z, z), f2(y.x, y.y), v[i][c][0]);
-            v[i][c][1] = fma2(f2(z, z), f2(y.z, y.w), v[i][c][1]);
+            v[i][c] = fma2(f2(z, z), f2(y.x, y.y), v[i][c]);
           }
         }
     }
@@ -139,10 +147,10 @@ struct Sums {  // elements 4 tx + 64 c of rows ty + 16 i
   __device__ __forceinline__ void store_row(int i, T* row, int D, float by) const {
     const int tx = threadIdx.x & 15;
 #pragma unroll
-    for (int c = 0; c < DP / 64; c++) {
-      if (4 * tx + 64 * c >= D) continue;
-      const float2 a = unpack(v[i][c][0]), b = unpack(v[i][c][1]);
-      store4(row + 4 * tx + 64 * c, a.x * by, a.y * by, b.x * by, b.y * by);
+    for (int c = 0; c < S::NC; c++) {
+      if (2 * tx + 32 * c >= D) continue;
+      const float2 a = unpack(v[i][c]);
+      store2(row + 2 * tx + 32 * c, a.x * by, a.y * by);
     }
   }
 };
@@ -171,10 +179,10 @@ __device__ __forceinline__ void find_keys(const PromptArgs& a, const PromptSeque
 }
 
 template <typename T, int DP, int BT>
-__global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(const __grid_constant__ PromptArgs a) {
   using S = Shape<DP, BT>;
   extern __shared__ __align__(16) float shared[];
-  float *sq = shared, *sk = sq + S::kRows, *sv = sk + S::kRows, *sp = sv + S::kRows;
+  float *sq = shared, *sk = sq + S::kRows, *sp = sk + S::kRows;  // sk: keys, then values
   __shared__ int64_t key_row[BT];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
@@ -219,10 +227,11 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant_
       return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
     };
     load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
-    load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
     __syncthreads();
     float s[S::MT][S::MT];
-    dots<DP, BT>(sq, sk, s);
+    dots<DP, BT>(sq, sk, D, s);
+    __syncthreads();
+    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
 #pragma unroll
     for (int i = 0; i < S::MT; i++) {
       float top = m[i];
@@ -246,8 +255,8 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant_
         sp[(ty + 16 * i) * S::LP + tx + 16 * j] = p;
       }
     }
-    __syncwarp();  // a row's weights are written and read by the same half warp
-    o.add(sp, sv);
+    __syncthreads();
+    o.add(sp, sk);
   }
 #pragma unroll
   for (int i = 0; i < S::MT; i++) {
@@ -269,10 +278,10 @@ __device__ __forceinline__ void weigh(float s, float dp, bool seen, float scale2
 
 // dq of BT rows, and delta of each for the other kernel.
 template <typename T, int DP, int BT>
-__global__ void __launch_bounds__(kThreads) prompt_bwd_rows_kernel(const __grid_constant__ PromptBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_kernel(const __grid_constant__ PromptBwdArgs a) {
   using S = Shape<DP, BT>;
   extern __shared__ __align__(16) float shared[];
-  float *sq = shared, *sg = sq + S::kRows, *sk = sg + S::kRows, *sv = sk + S::kRows, *sp = sv + S::kRows;
+  float *sq = shared, *sg = sq + S::kRows, *sk = sg + S::kRows, *sp = sk + S::kRows;  // sk: values, then keys
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
@@ -317,12 +326,14 @@ __global__ void __launch_bounds__(kThreads) prompt_bwd_rows_kernel(const __grid_
     auto key = [&](const void* base, int64_t stride, int r) {
       return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
     };
-    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
-    load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
-    __syncthreads();
     float s[S::MT][S::MT], dp[S::MT][S::MT];
-    dots<DP, BT>(sq, sk, s);
-    dots<DP, BT>(sg, sv, dp);
+    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
+    __syncthreads();
+    dots<DP, BT>(sg, sk, D, dp);
+    __syncthreads();
+    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
+    __syncthreads();
+    dots<DP, BT>(sq, sk, D, s);
 #pragma unroll
     for (int i = 0; i < S::MT; i++)
 #pragma unroll
@@ -343,11 +354,10 @@ __global__ void __launch_bounds__(kThreads) prompt_bwd_rows_kernel(const __grid_
 
 // dk and dv of BT keys, over the rows of all query heads of the group that see them.
 template <typename T, int DP, int BT>
-__global__ void __launch_bounds__(kThreads) prompt_bwd_keys_kernel(const __grid_constant__ PromptBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_kernel(const __grid_constant__ PromptBwdArgs a) {
   using S = Shape<DP, BT>;
   extern __shared__ __align__(16) float shared[];
-  float *sk = shared, *sv = sk + S::kRows, *sq = sv + S::kRows, *sg = sq + S::kRows, *sp = sg + S::kRows,
-        *sd = sp + S::kScores;
+  float *sk = shared, *sv = sk + S::kRows, *sq = sv + S::kRows, *sp = sq + S::kRows, *sd = sp + S::kScores;  // sq: Q, dO, Q
   __shared__ float slse[BT], sdelta[BT];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
@@ -377,7 +387,6 @@ __global__ void __launch_bounds__(kThreads) prompt_bwd_keys_kernel(const __grid_
     };
     __syncthreads();
     load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
-    load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
     for (int r = threadIdx.x; r < BT; r += kThreads) {
       const int64_t at = r < rows ? token_of(r) * a.q_heads + head_of(r) : 0;
       slse[r] = r < rows ? a.lse[rank][at] * kLog2e : 0.f;
@@ -385,8 +394,11 @@ __global__ void __launch_bounds__(kThreads) prompt_bwd_keys_kernel(const __grid_
     }
     __syncthreads();
     float s[S::MT][S::MT], dp[S::MT][S::MT];  // rows of the tile are keys here, columns the queries
-    dots<DP, BT>(sk, sq, s);
-    dots<DP, BT>(sv, sg, dp);
+    dots<DP, BT>(sk, sq, D, s);
+    __syncthreads();
+    load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
+    __syncthreads();
+    dots<DP, BT>(sv, sq, D, dp);
 #pragma unroll
     for (int i = 0; i < S::MT; i++)
 #pragma unroll
@@ -398,8 +410,11 @@ __global__ void __launch_bounds__(kThreads) prompt_bwd_keys_kernel(const __grid_
         sp[c * S::LP + r] = p;
         sd[c * S::LP + r] = ds;
       }
-    __syncwarp();
-    dv.add(sp, sg);
+    __syncwarp();  // a row's weights are written and read by the same half warp
+    dv.add(sp, sq);
+    __syncthreads();
+    load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
+    __syncthreads();
     dk.add(sd, sq);
   }
 #pragma unroll
@@ -430,17 +445,17 @@ cudaError_t launch(const void* fn, const Args& a, int64_t slots, int shared, cud
 template <typename T, int DP, int BT>
 cudaError_t forward(const PromptArgs& a, cudaStream_t stream) {
   return launch((const void*)prompt_kernel<T, DP, BT>, a, prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT),
-                shared_bytes<DP, BT>(3, 1), stream);
+                shared_bytes<DP, BT>(2, 1), stream);
 }
 
 template <typename T, int DP, int BT>
 cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
   const cudaError_t e =
       launch((const void*)prompt_bwd_rows_kernel<T, DP, BT>, a,
-             prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT), shared_bytes<DP, BT>(4, 1), stream);
+             prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT), shared_bytes<DP, BT>(3, 1), stream);
   if (e != cudaSuccess) return e;
   return launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>, a, prompt_slots(a.tokens, a.sequences, 1, BT),
-                shared_bytes<DP, BT>(4, 2), stream);
+                shared_bytes<DP, BT>(3, 2), stream);
 }
 
 // Whether the tensor core form takes the call: a group of heads fills no more than the
@@ -455,29 +470,33 @@ bool tensor_cores(const Args& a, int64_t k_stride, int64_t v_stride) {
 
 }  // namespace
 
+// By head size, padded to 64, 96, 128 or 256.
+template <typename T>
+cudaError_t by_size(const PromptArgs& a, cudaStream_t stream) {
+  if (a.head_dim <= 64) return forward<T, 64, 64>(a, stream);
+  if (a.head_dim <= 96) return forward<T, 96, 64>(a, stream);
+  if (a.head_dim <= 128) return forward<T, 128, 64>(a, stream);
+  return forward<T, 256, 32>(a, stream);
+}
+template <typename T>
+cudaError_t by_size(const PromptBwdArgs& a, cudaStream_t stream) {
+  if (a.head_dim <= 64) return backward<T, 64, 64>(a, stream);
+  if (a.head_dim <= 96) return backward<T, 96, 64>(a, stream);
+  if (a.head_dim <= 128) return backward<T, 128, 64>(a, stream);
+  return backward<T, 256, 32>(a, stream);
+}
+
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream) {
-  if (a.dtype == 0) {
-    if (a.head_dim <= 64) return forward<float, 64, 64>(a, stream);
-    if (a.head_dim <= 128) return forward<float, 128, 64>(a, stream);
-    return forward<float, 256, 32>(a, stream);
-  }
+  if (a.dtype == 0) return by_size<float>(a, stream);
   if (tensor_cores(a, a.k_stride, a.v_stride)) return launch_prompt_attention_tc(a, stream);
-  if (a.head_dim <= 64) return forward<uint16_t, 64, 64>(a, stream);
-  if (a.head_dim <= 128) return forward<uint16_t, 128, 64>(a, stream);
-  return forward<uint16_t, 256, 32>(a, stream);
+  return by_size<uint16_t>(a, stream);
 }
 
 cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t stream) {
-  if (a.dtype == 0) {
-    if (a.head_dim <= 64) return backward<float, 64, 64>(a, stream);
-    if (a.head_dim <= 128) return backward<float, 128, 64>(a, stream);
-    return backward<float, 256, 32>(a, stream);
-  }
+  if (a.dtype == 0) return by_size<float>(a, stream);
   if (tensor_cores(a, a.k_stride, a.v_stride) && a.dout_stride < (int64_t)1 << 38)
     return launch_prompt_attention_bwd_tc(a, stream);
-  if (a.head_dim <= 64) return backward<uint16_t, 64, 64>(a, stream);
-  if (a.head_dim <= 128) return backward<uint16_t, 128, 64>(a, stream);
-  return backward<uint16_t, 256, 32>(a, stream);
+  return by_size<uint16_t>(a, stream);
 }
 
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
