@@ -178,8 +178,17 @@ __device__ __forceinline__ void find_keys(const PromptArgs& a, const PromptSeque
   }
 }
 
+// An item's keys may be split over several blocks, which then leave O, m and l.
+struct Split {
+  int parts;
+  float* sums;  // per item and part: BT rows of DP, then m and l of each
+};
+template <int DP, int BT>
+constexpr int64_t kPartFloats = BT * (DP + 2);
+
 template <typename T, int DP, int BT>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(const __grid_constant__ PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(const __grid_constant__ PromptArgs a,
+                                                                           const __grid_constant__ Split split) {
   using S = Shape<DP, BT>;
   extern __shared__ __align__(16) float shared[];
   float *sq = shared, *sk = sq + S::kRows, *sp = sk + S::kRows;  // sk: keys, then values
@@ -191,7 +200,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(con
   PromptSequence seq;
   int tile;
   // the last tiles of a sequence see the most keys: they start first
-  if (!find_sequence(a.starts, a.sequences, a.tokens, group, BT, (int64_t)gridDim.x - 1 - blockIdx.x, &seq, &tile)) return;
+  const int part = (int)(blockIdx.x % (unsigned)split.parts);
+  const int64_t slots = gridDim.x / (unsigned)split.parts, slot = slots - 1 - blockIdx.x / (unsigned)split.parts;
+  if (!find_sequence(a.starts, a.sequences, a.tokens, group, BT, slot, &seq, &tile)) return;
   const bool paged = a.table != nullptr;
   if (paged) cached_sequence(a, &seq);
   const int row0 = tile * BT;  // of the sequence: tokens * group stays below 2^31 (checked)
@@ -216,7 +227,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(con
   }
   const int most = min(seq.before + (row0 + rows - 1) / group + 1, seq.keys);
   const float scale2 = a.scale * kLog2e;
-  for (int j0 = 0; j0 < most; j0 += BT) {
+  const int64_t tiles = most > 0 ? div_up(most, BT) : 0;
+  const int begin = (int)(tiles * part / split.parts) * BT, end = (int)min(tiles * (part + 1) / split.parts * BT, (int64_t)most);
+  for (int j0 = begin; j0 < end; j0 += BT) {
     __syncthreads();
     if (paged) {
       find_keys<BT>(a, seq, head, j0, key_row);
@@ -263,11 +276,89 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(con
     const int r = ty + 16 * i;
     const float sum = sum16(l[i]);
     if (r >= rows) continue;
+    if (split.parts > 1) {
+      float* const to =
+          split.sums + ((((int64_t)rank * a.kv_heads + head) * slots + slot) * split.parts + part) * kPartFloats<DP, BT>;
+      o.store_row(i, to + r * DP, DP, 1.f);
+      if (tx == 0) {
+        to[BT * DP + r] = m[i];
+        to[BT * (DP + 1) + r] = sum;
+      }
+      continue;
+    }
     o.store_row(i, (T*)a.out[rank] + (int64_t)token_of(r) * a.out_stride + (int64_t)head_of(r) * D, D,
                 sum == 0.f ? 0.f : 1.f / sum);
     if (a.lse[rank] != nullptr && tx == 0)
       a.lse[rank][(int64_t)token_of(r) * a.q_heads + head_of(r)] = (m[i] + log2f(sum)) / kLog2e;
   }
+}
+
+// The parts of a row's keys, a block a row: groups of threads take every G-th part, a
+// pair of elements a thread, and join in order.
+template <typename T, int DP, int BT>
+__global__ void __launch_bounds__(128) prompt_join_rows_kernel(const __grid_constant__ PromptArgs a,
+                                                               const __grid_constant__ Split split, int64_t slots) {
+  constexpr int G = 128 / (DP / 2);
+  __shared__ float weight[kPromptParts], reduced[8];
+  __shared__ float2 partial[G][DP / 2];
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  const int group = a.q_heads / a.kv_heads, D = a.head_dim, r = (int)(blockIdx.x % BT), lane = threadIdx.x & 31,
+            warp = threadIdx.x >> 5;
+  const int64_t item = blockIdx.x / BT, slot = item % slots;
+  const int head = (int)(item / slots % a.kv_heads), rank = (int)(item / slots / a.kv_heads);
+  PromptSequence seq;
+  int tile;
+  if (!find_sequence(a.starts, a.sequences, a.tokens, group, BT, slot, &seq, &tile)) return;
+  const int row = tile * BT + r;
+  if (row >= seq.length * group) return;
+  const float* const sums = split.sums + item * split.parts * kPartFloats<DP, BT>;
+  float top = -INFINITY, sum = 0.f;
+  for (int k = threadIdx.x; k < split.parts; k += 128) top = fmaxf(top, sums[k * kPartFloats<DP, BT> + BT * DP + r]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  if (lane == 0) reduced[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(reduced[0], reduced[1]), fmaxf(reduced[2], reduced[3]));
+  for (int k = threadIdx.x; k < split.parts; k += 128) {
+    const float* p = sums + k * kPartFloats<DP, BT> + BT * DP + r;
+    // below 0: a part with no weight at all has left nothing. (One of NaN scores alone has a sum of NaN, and no maximum.)
+    const float w = p[BT] == 0.f ? -1.f : exp2_fast(p[0] - top);
+    weight[k] = w;
+    if (!(w < 0.f)) sum = fmaf(p[BT], w, sum);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  if (lane == 0) reduced[4 + warp] = sum;
+  __syncthreads();
+  sum = (reduced[4] + reduced[5]) + (reduced[6] + reduced[7]);
+  const int g = threadIdx.x / (DP / 2), d = threadIdx.x % (DP / 2) * 2;
+  if (g < G) {
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll 8
+    for (int k = g; k < split.parts; k += G) {
+      const float w = weight[k];
+      const float2 x = *reinterpret_cast<const float2*>(sums + k * kPartFloats<DP, BT> + r * DP + d);
+      if (!(w < 0.f)) {
+        v.x = fmaf(x.x, w, v.x);
+        v.y = fmaf(x.y, w, v.y);
+      }
+    }
+    partial[g][d / 2] = v;
+  }
+  __syncthreads();
+  const int64_t token = seq.first + row / group, query = head * group + row % group;
+  if (g == 0 && d < D) {
+    float2 v = partial[0][d / 2];
+#pragma unroll
+    for (int k = 1; k < G; k++) {
+      v.x += partial[k][d / 2].x;
+      v.y += partial[k][d / 2].y;
+    }
+    const float by = sum == 0.f ? 0.f : 1.f / sum;
+    store2((T*)a.out[rank] + token * a.out_stride + query * D + d, sum == 0.f ? 0.f : v.x * by, sum == 0.f ? 0.f : v.y * by);
+  }
+  if (threadIdx.x == 0 && a.lse[rank] != nullptr) a.lse[rank][token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
 
 // Weight and score gradient of a score s that the row sees.
@@ -432,30 +523,43 @@ constexpr int shared_bytes(int rows, int scores) {
   return (rows * Shape<DP, BT>::kRows + scores * Shape<DP, BT>::kScores) * 4;
 }
 
-template <typename Args>
-cudaError_t launch(const void* fn, const Args& a, int64_t slots, int shared, cudaStream_t stream) {
+cudaError_t launch(const void* fn, dim3 grid, int shared, cudaStream_t stream, void** params) {
   int blocks = 0;
   const cudaError_t e = resident_blocks(fn, kThreads, shared, &blocks);  // lets the kernel have its shared memory
-  if (e != cudaSuccess) return e;
-  Args copy = a;
-  void* params[] = {&copy};
-  return launch_op(fn, dim3((unsigned)slots, (unsigned)a.kv_heads, (unsigned)a.nranks), kThreads, shared, stream, params);
+  return e != cudaSuccess ? e : launch_op(fn, grid, kThreads, shared, stream, params);
 }
 
+// Few items' keys are split so that every block of two an SM has some, two tiles at least.
 template <typename T, int DP, int BT>
 cudaError_t forward(const PromptArgs& a, cudaStream_t stream) {
-  return launch((const void*)prompt_kernel<T, DP, BT>, a, prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT),
-                shared_bytes<DP, BT>(2, 1), stream);
+  int64_t slots = prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT);
+  const int64_t items = slots * a.kv_heads * a.nranks;
+  Split split = {1, (float*)(a.ws + kOpScratchOffset)};
+  if (items * 2 <= kPromptParts) {
+    const int64_t most = a.table != nullptr ? (int64_t)a.max_blocks << a.page_shift : a.tokens;
+    const int64_t room = kPromptParts / items, wanted = div_up(most, 2 * BT);
+    split.parts = (int)(room < wanted ? room : wanted);
+  }
+  PromptArgs copy = a;
+  void* params[] = {&copy, &split, &slots};
+  const cudaError_t e = launch((const void*)prompt_kernel<T, DP, BT>,
+                               dim3((unsigned)(slots * split.parts), (unsigned)a.kv_heads, (unsigned)a.nranks),
+                               shared_bytes<DP, BT>(2, 1), stream, params);
+  if (e != cudaSuccess || split.parts == 1) return e;
+  return launch_op((const void*)prompt_join_rows_kernel<T, DP, BT>, dim3((unsigned)(items * BT)), 128, 0, stream, params);
 }
 
 template <typename T, int DP, int BT>
 cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
-  const cudaError_t e =
-      launch((const void*)prompt_bwd_rows_kernel<T, DP, BT>, a,
-             prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT), shared_bytes<DP, BT>(3, 1), stream);
+  PromptBwdArgs copy = a;
+  void* params[] = {&copy};
+  const unsigned kv = (unsigned)a.kv_heads, n = (unsigned)a.nranks;
+  const cudaError_t e = launch((const void*)prompt_bwd_rows_kernel<T, DP, BT>,
+                               dim3((unsigned)prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT), kv, n),
+                               shared_bytes<DP, BT>(3, 1), stream, params);
   if (e != cudaSuccess) return e;
-  return launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>, a, prompt_slots(a.tokens, a.sequences, 1, BT),
-                shared_bytes<DP, BT>(3, 2), stream);
+  return launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>,
+                dim3((unsigned)prompt_slots(a.tokens, a.sequences, 1, BT), kv, n), shared_bytes<DP, BT>(3, 2), stream, params);
 }
 
 // Whether the tensor core form takes the call: a group of heads fills no more than the
@@ -501,11 +605,12 @@ cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t str
 
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
   const int64_t delta = align_up((int64_t)nranks * tokens * q_heads * 4, 256);
-  // the parts of few tiles' keys, where they may be split: 2 x 128 rows of O, m and l a block
-  const int group = q_heads / kv_heads;
+  // the parts of few items' keys, where they may be split: rows of O, m and l, in either form
+  const int group = q_heads / kv_heads, rows = head_dim <= 128 ? 64 : 32;
+  const int64_t lanes = (int64_t)kv_heads * nranks, padded = head_dim <= 64 ? 64 : head_dim <= 96 ? 96 : head_dim <= 128 ? 128 : 256;
   int64_t parts = 0;
-  if (group <= 128 && head_dim <= 128 &&
-      (tokens / (2 * (128 / group)) + 1) * kv_heads * nranks * 2 <= kPromptSplitBlocks)
+  if ((tokens * group / rows + 1) * lanes * 2 <= kPromptParts) parts = kPromptParts * rows * (padded + 2) * 4;
+  if (group <= 128 && head_dim <= 128 && (tokens / (2 * (128 / group)) + 1) * lanes * 2 <= kPromptSplitBlocks)
     parts = (int64_t)kPromptSplitBlocks * (256 * ((head_dim <= 64 ? 64 : 128) + 2) + kPromptPartInfo) * 4;
   return delta > parts ? delta : parts;
 }

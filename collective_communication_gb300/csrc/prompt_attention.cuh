@@ -52,6 +52,7 @@ cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream);
 cudaError_t launch_prompt_attention_tc(const PromptArgs& a, cudaStream_t stream);
 cudaError_t launch_prompt_attention_bwd_tc(const PromptBwdArgs& a, cudaStream_t stream);
 constexpr int kPromptSplitBlocks = 152;  // blocks among which few tiles' keys are split: the SMs
+constexpr int kPromptParts = 304;        // the same in the form on the ordinary arithmetic units: two blocks an SM
 constexpr int kPromptPartInfo = 32;      // numbers behind a part's sums
 cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t stream);
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim);

@@ -775,8 +775,10 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
 #pragma unroll
   for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
-    m[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - top);  // now the part's weight
-    if (m[i] != 0.f) sum = fmaf(l[i], m[i], sum);
+    // now the part's weight; below 0: a part with no weight at all has left nothing. (One of NaN scores alone has a
+    // sum of NaN, and no maximum.)
+    m[i] = l[i] == 0.f ? -1.f : exp2_fast(m[i] - top);
+    if (!(m[i] < 0.f)) sum = fmaf(l[i], m[i], sum);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
@@ -787,18 +789,17 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < kBatch; k++) {
       const int part = (k0 + k) * 4 + warp;
-      w[k] = 0.f;
+      w[k] = -1.f;
 #pragma unroll
       for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
         const float y = __shfl_sync(~0u, m[i], part & 31);
         if (part >> 5 == i) w[k] = y;
       }
-      // a part that saw nothing has left nothing
       const float* p = sums + part * kPartFloats<DP> + row * DP + lane * E;
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         float2 y = make_float2(0.f, 0.f);
-        if (w[k] != 0.f && part < split.parts) y = *reinterpret_cast<const float2*>(p + e);
+        if (!(w[k] < 0.f) && part < split.parts) y = *reinterpret_cast<const float2*>(p + e);
         x[k][e] = y.x;
         x[k][e + 1] = y.y;
       }
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < kBatch; k++)
 #pragma unroll
-      for (int e = 0; e < E; e++) v[e] = fmaf(x[k][e], w[k], v[e]);
+      for (int e = 0; e < E; e++) v[e] = fmaf(x[k][e], w[k] < 0.f ? 0.f : w[k], v[e]);
   }
 #pragma unroll
   for (int e = 0; e < E; e++) partial[warp][lane * E + e] = v[e];
