@@ -40,6 +40,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
 __device__ __forceinline__ void store2(uint16_t* p, float x, float y) { *reinterpret_cast<uint32_t*>(p) = bf16_pair(x, y); }
 
+// Whether the gradient's tiles have buffers of their own and two blocks fit an SM all the same.
+template <int DP>
+constexpr bool kApart = DP <= 64;
+
 template <int DP, int BT>
 struct Shape {
   static constexpr int MT = BT / 16;   // rows, and columns, of a thread
@@ -372,7 +376,8 @@ template <typename T, int DP, int BT>
 __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_kernel(const __grid_constant__ PromptBwdArgs a) {
   using S = Shape<DP, BT>;
   extern __shared__ __align__(16) float shared[];
-  float *sq = shared, *sg = sq + S::kRows, *sk = sg + S::kRows, *sp = sk + S::kRows;  // sk: values, then keys
+  float *sq = shared, *sg = sq + S::kRows, *sk = sg + S::kRows, *sv = kApart<DP> ? sk + S::kRows : sk,
+        *sp = sv + S::kRows;  // values and keys may take turns
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
@@ -418,12 +423,15 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
       return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
     };
     float s[S::MT][S::MT], dp[S::MT][S::MT];
-    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
+    load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
+    if (kApart<DP>) load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
     __syncthreads();
-    dots<DP, BT>(sg, sk, D, dp);
-    __syncthreads();
-    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
-    __syncthreads();
+    dots<DP, BT>(sg, sv, D, dp);
+    if (!kApart<DP>) {
+      __syncthreads();
+      load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
+      __syncthreads();
+    }
     dots<DP, BT>(sq, sk, D, s);
 #pragma unroll
     for (int i = 0; i < S::MT; i++)
@@ -445,10 +453,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
 
 // dk and dv of BT keys, over the rows of all query heads of the group that see them.
 template <typename T, int DP, int BT>
-__global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_kernel(const __grid_constant__ PromptBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_kernel(const __grid_constant__ PromptBwdArgs a,
+                                                                                     const __grid_constant__ KeyParts split) {
   using S = Shape<DP, BT>;
   extern __shared__ __align__(16) float shared[];
-  float *sk = shared, *sv = sk + S::kRows, *sq = sv + S::kRows, *sp = sq + S::kRows, *sd = sp + S::kScores;  // sq: Q, dO, Q
+  float *sk = shared, *sv = sk + S::kRows, *sq = sv + S::kRows, *sg = kApart<DP> ? sq + S::kRows : sq,
+        *sp = sg + S::kRows, *sd = sp + S::kScores;  // Q and dO may take turns
   __shared__ float slse[BT], sdelta[BT];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
@@ -456,7 +466,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
   PromptSequence seq;
   int tile;
   // the first keys of a sequence are seen by the most rows: they start first
-  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, BT, blockIdx.x, &seq, &tile)) return;
+  const int part = (int)(blockIdx.x % (unsigned)split.parts);
+  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, BT, blockIdx.x / (unsigned)split.parts, &seq, &tile)) return;
   const int j0 = tile * BT, keys = min(BT, seq.length - j0);
   auto key = [&](const void* base, int64_t stride, int r) {
     return r < keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
@@ -469,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
   dv.zero();
   const float scale2 = a.scale * kLog2e;
   const float* deltas = reinterpret_cast<const float*>(a.ws + kOpScratchOffset) + (int64_t)rank * a.tokens * a.q_heads;
-  for (int row0 = j0 * group; row0 < seq.length * group; row0 += BT) {
+  const int64_t tiles = div_up((int64_t)(seq.length - j0) * group, BT);
+  const int first = j0 * group + (int)(tiles * part / split.parts) * BT, last = j0 * group + (int)(tiles * (part + 1) / split.parts) * BT;
+  for (int row0 = first; row0 < min(last, seq.length * group); row0 += BT) {
     const int rows = min(BT, seq.length * group - row0);
     auto token_of = [&](int r) { return (int64_t)(seq.first + (row0 + r) / group); };
     auto head_of = [&](int r) { return (int64_t)(head * group + (row0 + r) % group); };
@@ -478,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
     };
     __syncthreads();
     load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
+    if (kApart<DP>) load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
     for (int r = threadIdx.x; r < BT; r += kThreads) {
       const int64_t at = r < rows ? token_of(r) * a.q_heads + head_of(r) : 0;
       slse[r] = r < rows ? a.lse[rank][at] * kLog2e : 0.f;
@@ -486,10 +500,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
     __syncthreads();
     float s[S::MT][S::MT], dp[S::MT][S::MT];  // rows of the tile are keys here, columns the queries
     dots<DP, BT>(sk, sq, D, s);
-    __syncthreads();
-    load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
-    __syncthreads();
-    dots<DP, BT>(sv, sq, D, dp);
+    if (!kApart<DP>) {
+      __syncthreads();
+      load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
+      __syncthreads();
+    }
+    dots<DP, BT>(sv, sg, D, dp);
 #pragma unroll
     for (int i = 0; i < S::MT; i++)
 #pragma unroll
@@ -502,10 +518,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
         sd[c * S::LP + r] = ds;
       }
     __syncwarp();  // a row's weights are written and read by the same half warp
-    dv.add(sp, sq);
-    __syncthreads();
-    load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
-    __syncthreads();
+    dv.add(sp, sg);
+    if (!kApart<DP>) {
+      __syncthreads();
+      load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
+      __syncthreads();
+    }
     dk.add(sd, sq);
   }
 #pragma unroll
@@ -513,8 +531,44 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
     const int r = ty + 16 * i;
     if (r >= keys) continue;
     const int64_t token = seq.first + j0 + r, at = (int64_t)head * D;
+    if (split.parts > 1) {
+      const int64_t each = key_part_floats(a.nranks, a.tokens, a.kv_heads, D);
+      float* const to = split.sums + 2 * part * each + (((int64_t)rank * a.tokens + token) * a.kv_heads + head) * D;
+      dk.store_row(i, to, D, a.scale);
+      dv.store_row(i, to + each, D, 1.f);
+      continue;
+    }
     dk.store_row(i, (T*)a.dk[rank] + token * a.dk_stride + at, D, a.scale);
     dv.store_row(i, (T*)a.dv[rank] + token * a.dv_stride + at, D, 1.f);
+  }
+}
+
+// dk and dv of eight elements a thread, from the parts' sums.
+template <typename T>
+__global__ void __launch_bounds__(256) prompt_key_parts_kernel(const __grid_constant__ PromptBwdArgs a,
+                                                               const __grid_constant__ KeyParts split) {
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  const int width = a.kv_heads * a.head_dim, rank = blockIdx.y;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, token = at / width;
+  // tokens in no sequence have no sums
+  if (token < a.starts[0] || token >= a.starts[a.sequences] || token >= a.tokens) return;
+  const int64_t each = key_part_floats(a.nranks, a.tokens, a.kv_heads, a.head_dim);
+#pragma unroll
+  for (int which = 0; which < 2; which++) {
+    float sum[8] = {}, v[8];
+    const float* from = split.sums + which * each + (int64_t)rank * a.tokens * width + at;
+#pragma unroll 4
+    for (int k = 0; k < split.parts; k++) {
+      Pack8<float> x;
+      x.load_stream(from + 2 * k * each);
+      x.widen(v);
+#pragma unroll
+      for (int i = 0; i < 8; i++) sum[i] += v[i];
+    }
+    Pack8<T> y;
+    y.narrow(sum);
+    y.store((T*)(which == 0 ? a.dk[rank] : a.dv[rank]) + token * (which == 0 ? a.dk_stride : a.dv_stride) + at % width);
   }
 }
 
@@ -522,6 +576,8 @@ template <int DP, int BT>
 constexpr int shared_bytes(int rows, int scores) {
   return (rows * Shape<DP, BT>::kRows + scores * Shape<DP, BT>::kScores) * 4;
 }
+
+int64_t delta_bytes(int nranks, int64_t tokens, int q_heads) { return align_up((int64_t)nranks * tokens * q_heads * 4, 256); }
 
 cudaError_t launch(const void* fn, dim3 grid, int shared, cudaStream_t stream, void** params) {
   int blocks = 0;
@@ -554,12 +610,19 @@ cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
   PromptBwdArgs copy = a;
   void* params[] = {&copy};
   const unsigned kv = (unsigned)a.kv_heads, n = (unsigned)a.nranks;
-  const cudaError_t e = launch((const void*)prompt_bwd_rows_kernel<T, DP, BT>,
+  cudaError_t e = launch((const void*)prompt_bwd_rows_kernel<T, DP, BT>,
                                dim3((unsigned)prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT), kv, n),
-                               shared_bytes<DP, BT>(3, 1), stream, params);
+                               shared_bytes<DP, BT>(kApart<DP> ? 4 : 3, 1), stream, params);
   if (e != cudaSuccess) return e;
-  return launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>,
-                dim3((unsigned)prompt_slots(a.tokens, a.sequences, 1, BT), kv, n), shared_bytes<DP, BT>(3, 2), stream, params);
+  const int64_t slots = prompt_slots(a.tokens, a.sequences, 1, BT);
+  KeyParts split;
+  split.parts = key_parts(slots * a.kv_heads * a.nranks, kPromptParts,
+                          (int64_t)a.tokens / a.sequences * (a.q_heads / a.kv_heads) / (2 * BT));
+  split.sums = (float*)(a.ws + kOpScratchOffset + delta_bytes(a.nranks, a.tokens, a.q_heads));
+  void* key_params[] = {&copy, &split};
+  e = launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>, dim3((unsigned)(slots * split.parts), kv, n),
+             shared_bytes<DP, BT>(kApart<DP> ? 4 : 3, 2), stream, key_params);
+  return e != cudaSuccess || split.parts == 1 ? e : launch_prompt_key_parts(a, split, stream);
 }
 
 // Whether the tensor core form takes the call: a group of heads fills no more than the
@@ -590,6 +653,15 @@ cudaError_t by_size(const PromptBwdArgs& a, cudaStream_t stream) {
   return backward<T, 256, 32>(a, stream);
 }
 
+cudaError_t launch_prompt_key_parts(const PromptBwdArgs& a, const KeyParts& parts, cudaStream_t stream) {
+  PromptBwdArgs copy = a;
+  KeyParts split = parts;
+  void* params[] = {&copy, &split};
+  const void* fn = a.dtype == 0 ? (const void*)prompt_key_parts_kernel<float> : (const void*)prompt_key_parts_kernel<uint16_t>;
+  const int64_t pieces = (int64_t)a.tokens * a.kv_heads * a.head_dim / 8;
+  return launch_op(fn, dim3((unsigned)div_up(pieces, 256), (unsigned)a.nranks), 256, 0, stream, params);
+}
+
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream) {
   if (a.dtype == 0) return by_size<float>(a, stream);
   if (tensor_cores(a, a.k_stride, a.v_stride)) return launch_prompt_attention_tc(a, stream);
@@ -604,7 +676,7 @@ cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t str
 }
 
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
-  const int64_t delta = align_up((int64_t)nranks * tokens * q_heads * 4, 256);
+  const int64_t delta = delta_bytes(nranks, tokens, q_heads);
   // the parts of few items' keys, where they may be split: rows of O, m and l, in either form
   const int group = q_heads / kv_heads, rows = head_dim <= 128 ? 64 : 32;
   const int64_t lanes = (int64_t)kv_heads * nranks, padded = head_dim <= 64 ? 64 : head_dim <= 96 ? 96 : head_dim <= 128 ? 128 : 256;
@@ -612,7 +684,14 @@ int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, 
   if ((tokens * group / rows + 1) * lanes * 2 <= kPromptParts) parts = kPromptParts * rows * (padded + 2) * 4;
   if (group <= 128 && head_dim <= 128 && (tokens / (2 * (128 / group)) + 1) * lanes * 2 <= kPromptSplitBlocks)
     parts = (int64_t)kPromptSplitBlocks * (256 * ((head_dim <= 64 ? 64 : 128) + 2) + kPromptPartInfo) * 4;
-  return delta > parts ? delta : parts;
+  // what parts of the rows leave of dk and dv: a call of more sequences than one has no more of them
+  const int unit = group <= 128 && head_dim <= 128 ? 128 : rows;
+  const int most = group <= 128 && head_dim <= 128 ? key_parts((tokens / unit + 1) * lanes, 152, tokens / (2 * (128 / group)))
+                                                   : 1;
+  const int plain = key_parts((tokens / rows + 1) * lanes, kPromptParts, tokens * group / (2 * rows));
+  const int key_split = most > plain ? most : plain;
+  const int64_t gradient = delta + (key_split > 1 ? key_split * 2 * key_part_floats(nranks, tokens, kv_heads, head_dim) * 4 : 0);
+  return gradient > parts ? gradient : parts;
 }
 
 }  // namespace rar

@@ -41,11 +41,32 @@ struct PromptBwdArgs {
   void* dk[kMaxRanks];
   void* dv[kMaxRanks];
   const int32_t* starts;
-  char* ws;  // scratch: delta, float [ranks, tokens, q_heads]
+  char* ws;  // scratch: delta, float [ranks, tokens, q_heads]; then what parts leave of dk and dv
   int64_t q_stride, k_stride, v_stride, out_stride, dout_stride, dq_stride, dk_stride, dv_stride;
   float scale;
   int nranks, dtype, tokens, sequences, q_heads, kv_heads, head_dim;
 };
+
+// The rows that see a tile of keys may be split into parts, which then leave their sums:
+// float [part, 2 (dk, dv), rank, token, kv_heads, head_dim] behind delta.
+struct KeyParts {
+  int parts;
+  float* sums;
+};
+__host__ __device__ inline int64_t key_part_floats(int nranks, int64_t tokens, int kv_heads, int head_dim) {
+  return (int64_t)nranks * tokens * kv_heads * head_dim;  // of dk, or dv, of a part
+}
+constexpr int kMostKeyParts = 8;
+// Parts for `items` tiles of keys on `blocks` resident blocks, where a key is seen by the rows of `row_tiles` tiles on
+// average. The items of a long sequence differ by the rows that see them: with fewer than two a block the first keys'
+// alone would take twice as long as the mean. A part has eight tiles of rows, for the cost of its sums.
+inline int key_parts(int64_t items, int64_t blocks, int64_t row_tiles) {
+  int64_t parts = 2 * blocks / (items > 0 ? items : 1);
+  if (parts > row_tiles / 8) parts = row_tiles / 8;
+  return parts < 1 ? 1 : parts > kMostKeyParts ? kMostKeyParts : (int)parts;
+}
+// Adds them up, in their order.
+cudaError_t launch_prompt_key_parts(const PromptBwdArgs& a, const KeyParts& parts, cudaStream_t stream);
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream);
 // The forms of bf16 with head sizes up to 128 and groups up to 128 (prompt_attention_tc.cu, prompt_attention_bwd_tc.cu).

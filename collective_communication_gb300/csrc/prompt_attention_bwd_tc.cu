@@ -67,18 +67,21 @@ struct Item {
   int rank, head;        // key head
   int sequence, length;  // the sequence's first token in the step, and its tokens
   int from, count;       // first token or key of the item in the sequence, and how many
+  int part;
 };
 
-// Numbers of items, in tiles of `unit` tokens.
+// Numbers of items, in tiles of `unit` tokens, and what their rows are split into.
 struct Work {
   int64_t slots;
   int unit;
+  KeyParts split;
 };
 
 // Item number n in order, from the last tiles of a sequence on, or from the first; false if there is none (a whole warp).
 __device__ __forceinline__ bool find_item(const PromptBwdArgs& a, const Work& work, bool last_first, int64_t n, Item* item) {
-  const int64_t lanes = (int64_t)a.kv_heads * a.nranks, slot = n / lanes;
-  const int lane_of = (int)(n % lanes);
+  const int64_t lanes = (int64_t)a.kv_heads * a.nranks, whole = n / work.split.parts, slot = whole / lanes;
+  const int lane_of = (int)(whole % lanes);
+  item->part = (int)(n % work.split.parts);
   item->head = lane_of % a.kv_heads;
   item->rank = lane_of / a.kv_heads;
   PromptSequence seq;
@@ -98,7 +101,7 @@ __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& 
                                             uint64_t* full, uint64_t* empty, volatile int* dead) {
   const int lane = threadIdx.x & 31;
   uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
-  const int64_t all = work.slots * a.kv_heads * a.nranks;
+  const int64_t all = work.slots * work.split.parts * a.kv_heads * a.nranks;
   int64_t n = blockIdx.x;
   for (int i = 0;;) {
     Item item;
@@ -126,7 +129,7 @@ __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& 
 
 // What another warp reads of item i; false at the end.
 struct Taken {
-  int rank, head, sequence, length, from, count;
+  int rank, head, sequence, length, from, count, part;
 };
 __device__ __forceinline__ bool take_item(int i, const Item* items, uint64_t* full, uint64_t* empty, volatile int* dead, Taken* t) {
   if (!wait_warp(&full[i % kItemSlots], i / kItemSlots & 1, dead)) return false;
@@ -139,6 +142,7 @@ __device__ __forceinline__ bool take_item(int i, const Item* items, uint64_t* fu
     t->length = uniform(item.length);
     t->from = uniform(item.from);
     t->count = uniform(item.count);
+    t->part = uniform(item.part);
   }
   __syncwarp();
   if (there && (threadIdx.x & 31) == 0) arrive(&empty[i % kItemSlots]);
@@ -159,6 +163,19 @@ struct Quarter {
   __device__ __forceinline__ void load(uint32_t at, int slice) {
     if (DP == 128) tmem_load32(at + slice * 32, o);
     else tmem_load16(at + slice * 16, o);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < DP / 4; i++) o[i] = 0;
+  }
+  __device__ __forceinline__ void store_part(float* row, int slice, float by, int D) const {
+#pragma unroll
+    for (int i = 0; i < DP / 4; i += 4) {
+      const int d = slice * (DP / 4) + i;
+      if (d < D)
+        store4(row + d, __uint_as_float(o[i]) * by, __uint_as_float(o[i + 1]) * by, __uint_as_float(o[i + 2]) * by,
+               __uint_as_float(o[i + 3]) * by);
+    }
   }
   __device__ __forceinline__ void store(uint16_t* row, int slice, float by, int D) const {
 #pragma unroll
@@ -498,13 +515,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   constexpr uint32_t s_at = 0, dp_at = 128, dv_at = 256, dk_at = 384;  // all of tensor memory, from 0 on
   uint8_t *const k_tile = smem, *const v_tile = smem + L::kBytes, *const ring = smem + 2 * L::kBytes;  // a stage: Q, dO
   const int D = a.head_dim, per_tile = kTile / group, steps = (D + 15) / 16;
-  auto first_tile = [&](const Taken& t) { return t.from / per_tile; };  // of rows
-  auto last_tile = [&](const Taken& t) { return (t.length + per_tile - 1) / per_tile; };
+  // tiles of rows, of all that see the item's keys the part's
+  auto tile_of = [&](const Taken& t, int part) {
+    const int first = t.from / per_tile, count = (t.length + per_tile - 1) / per_tile - first;
+    return first + (int)((int64_t)count * part / work.split.parts);
+  };
+  auto first_tile = [&](const Taken& t) { return tile_of(t, t.part); };
+  auto last_tile = [&](const Taken& t) { return tile_of(t, t.part + 1); };
 
   if (warp == kItemWarp) {
     serve_items(a, work, false, items, item_full, item_empty, dead);  // the first keys are seen by the most rows
   } else if (warp == kCopyWarp) {
-    int n = 0;  // tiles of rows so far
+    int n = 0, some = 0;  // tiles of rows, and items that have some, so far
     for (int i = 0;; i++) {
       Taken t;
       if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
@@ -523,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
           }
         }
         if (x == begin) {
-          if (!(fine = wait_warp(&kv_empty, (i & 1) ^ 1, dead))) break;
+          if (!(fine = wait_warp(&kv_empty, (some & 1) ^ 1, dead))) break;
           if (lane == 0) {
             arrive_expect(&kv_full, 2 * L::kBytes);
             for (int h = 0; h < DP / 64; h++) {
@@ -534,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         }
       }
       if (!fine) break;
+      some += begin < end;
     }
   } else if (warp == kNumbersWarp) {
     int n = 0;
@@ -572,11 +595,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   } else if (warp == kProductWarp) {
     const uint32_t k_at = shared_address(k_tile), v_at = shared_address(v_tile), ring_at = shared_address(ring);
     const uint32_t lead = elect_one();
-    int base = 0;  // tiles of rows of the items before
+    int base = 0, some = 0;  // tiles of rows, and items that have some, so far
     for (int i = 0;; i++) {
       Taken t;
       if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
       const int begin = first_tile(t), end = last_tile(t);
+      if (begin == end) continue;
       auto score = [&](int x) {  // S^T of a tile of rows; rows that are none are 0, for the products with P and dS
         const int n = base + x - begin, stage = n % NS;
         if (!wait_warp(&full[stage], n / NS & 1, dead)) return false;
@@ -597,11 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         commit(lead, &dp_full);
         if (x + 1 == end) commit(lead, &kv_empty);
       };
-      bool fine = wait_warp(&kv_full, i & 1, dead) && score(begin);
+      bool fine = wait_warp(&kv_full, some & 1, dead) && score(begin);
       if (!fine) break;
       value(begin);
       // sums of the item before have been read
-      if (i > 0 && !wait_warp(&sums_free, (i - 1) & 1, dead)) break;
+      if (some > 0 && !wait_warp(&sums_free, (some - 1) & 1, dead)) break;
       for (int x = begin; x < end; x++) {
         const int n = base + x - begin, stage = n % NS;
         const bool more = x + 1 < end;
@@ -618,13 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       }
       if (!fine) break;
       base += end - begin;
+      some++;
     }
   } else if (warp < kWeightWarps) {
     const int slice = warp >> 2, c0 = slice * kColumns;
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;
     const int row = threadIdx.x & 127;
     const F2 scale_pair = f2(a.scale * kLog2e, a.scale * kLog2e);
-    int n = 0;
+    int n = 0, some = 0;
     for (int i = 0;; i++) {
       Taken t;
       if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
@@ -682,19 +707,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         arrive_warp(&ds_ready);
         if (lane == 0) arrive(&empty[stage]);  // the rows' numbers have been read
       }
-      if (!fine || !wait(&sums_full, i & 1, dead)) break;
-      fence_after();
+      if (!fine) break;
       Quarter<DP> dk, dv;
-      dk.load(dk_at + quarter, slice);
-      dv.load(dv_at + quarter, slice);
-      loads_done();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) arrive(&sums_free);
+      if (begin < end) {
+        if (!wait(&sums_full, some & 1, dead)) break;
+        some++;
+        fence_after();
+        dk.load(dk_at + quarter, slice);
+        dv.load(dv_at + quarter, slice);
+        loads_done();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(&sums_free);
+      } else {
+        dk.zero();
+        dv.zero();
+      }
       if (row < t.count) {
         const int64_t token = (int64_t)t.sequence + key, at = (int64_t)t.head * D;
-        dk.store((uint16_t*)a.dk[t.rank] + token * a.dk_stride + at, slice, a.scale, D);
-        dv.store((uint16_t*)a.dv[t.rank] + token * a.dv_stride + at, slice, 1.f, D);
+        if (work.split.parts > 1) {
+          const int64_t each = key_part_floats(a.nranks, a.tokens, a.kv_heads, D);
+          float* const to = work.split.sums + 2 * t.part * each + ((int64_t)t.rank * a.tokens + token) * a.kv_heads * D + at;
+          dk.store_part(to, slice, a.scale, D);
+          dv.store_part(to + each, slice, 1.f, D);
+        } else {
+          dk.store((uint16_t*)a.dk[t.rank] + token * a.dk_stride + at, slice, a.scale, D);
+          dv.store((uint16_t*)a.dv[t.rank] + token * a.dv_stride + at, slice, 1.f, D);
+        }
       }
     }
   }
@@ -726,10 +765,15 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
     Work work;
     work.unit = which == 0 ? per_tile : kTile;
     work.slots = prompt_slots(a.tokens, a.sequences, 1, work.unit);
-    const int64_t all = work.slots * a.kv_heads * a.nranks;
+    work.split.parts = 1;
+    if (which == 1)
+      work.split.parts = key_parts(work.slots * a.kv_heads * a.nranks, blocks, (int64_t)a.tokens / a.sequences / (2 * per_tile));
+    work.split.sums = (float*)(a.ws + kOpScratchOffset + align_up((int64_t)a.nranks * a.tokens * a.q_heads * 4, 256));
+    const int64_t all = work.slots * work.split.parts * a.kv_heads * a.nranks;
     void* params[] = {&copy, &maps, &work};
     e = launch_op(which == 0 ? rows : keys, dim3((unsigned)(all < blocks ? all : blocks)), kThreads,
                   which == 0 ? Layout<DP>::kRowsShared : Layout<DP>::kKeysShared, stream, params);
+    if (e == cudaSuccess && work.split.parts > 1) e = launch_prompt_key_parts(a, work.split, stream);
   }
   return e;
 }

@@ -155,6 +155,9 @@ PROMPTS = [
     (1, [90], 2, 2, 256, "f32"), (1, [70], 2, 2, 160, "f32"), (1, [9, 30], 130, 1, 64, "bf16"), (1, [3, 20], 128, 1, 128, "bf16"),
     (1, [11], 100, 1, 64, "f32"), (1, [45], 96, 2, 128, "bf16"), (8, [64, 300, 1, 7], 8, 1, 128, "bf16"),
     (32, [17, 9], 2, 1, 64, "bf16"), (1, [1] * 150, 8, 2, 64, "bf16"), (1, [700, 1300], 3, 1, 64, "bf16"),
+    # few key heads of long sequences, whose rows are split
+    (1, [1100, 30], 16, 2, 128, "bf16"), (2, [1500], 16, 1, 64, "bf16"), (1, [600, 0, 9], 16, 2, 64, "f32"),
+    (1, [400], 8, 1, 192, "bf16"), (1, [333], 16, 1, 96, "f32"),
 ]
 
 
@@ -267,6 +270,25 @@ def test_cached(ranks, new, lens, q_heads, kv_heads, dim, page, dtype):
     starts = starts_of(new)
     out, lse = cached_forward(q, k, v, table, starts, i32(*lens))
     check_forward(q, keys, values, starts, out, lse, before=[a - b for a, b in zip(lens, new)])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cached_not_a_number_in_a_part(dtype):
+    """A query of NaN, and a key of NaN that later rows alone see, where the keys are split over blocks."""
+    new, lens = [6], [4000]
+    g = gen(8)
+    k, v, table, keys, values = paged(g, 1, lens, 1, 64, 16, DT[dtype])
+    q = normal(g, 1, 6, 4, 64, dtype=DT[dtype])
+    want, want_lse = cached_forward(q, k, v, table, starts_of(new), i32(*lens))
+    q[:, 2, 1] = float("nan")
+    page = int(table[0, 3997 // 16])
+    k[:, page, 0, 3997 % 16] = float("nan")
+    out, lse = cached_forward(q, k, v, table, starts_of(new), i32(*lens))
+    bad = torch.zeros(1, 6, 4, dtype=torch.bool, device="cuda")
+    bad[:, 2, 1] = True
+    bad[:, 3:] = True
+    assert torch.equal(out.isnan().all(-1), bad) and torch.equal(out.isnan().any(-1), bad) and torch.equal(lse.isnan(), bad)
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
