@@ -190,6 +190,22 @@ struct Split {
 template <int DP, int BT>
 constexpr int64_t kPartFloats = BT * (DP + 2);
 
+// A block's place: the heads of all ranks side by side, so that the tiles with the most
+// work of every head start first.
+struct Place {
+  int head, rank, part;
+  int64_t slot, slots;
+  template <typename Args>
+  __device__ __forceinline__ Place(const Args& a, int parts) {
+    const unsigned lanes = (unsigned)(a.kv_heads * a.nranks), whole = blockIdx.x / (unsigned)parts;
+    part = (int)(blockIdx.x % (unsigned)parts);
+    head = (int)(whole % lanes) % a.kv_heads;
+    rank = (int)(whole % lanes) / a.kv_heads;
+    slot = whole / lanes;
+    slots = gridDim.x / (unsigned)parts / lanes;
+  }
+};
+
 template <typename T, int DP, int BT>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(const __grid_constant__ PromptArgs a,
                                                                            const __grid_constant__ Split split) {
@@ -199,13 +215,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(con
   __shared__ int64_t key_row[BT];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
-  const int group = a.q_heads / a.kv_heads, head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
+  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
+  const Place place(a, split.parts);
+  const int group = a.q_heads / a.kv_heads, head = place.head, rank = place.rank, part = place.part, D = a.head_dim;
   PromptSequence seq;
   int tile;
   // the last tiles of a sequence see the most keys: they start first
-  const int part = (int)(blockIdx.x % (unsigned)split.parts);
-  const int64_t slots = gridDim.x / (unsigned)split.parts, slot = slots - 1 - blockIdx.x / (unsigned)split.parts;
+  const int64_t slots = place.slots, slot = slots - 1 - place.slot;
   if (!find_sequence(a.starts, a.sequences, a.tokens, group, BT, slot, &seq, &tile)) return;
   const bool paged = a.table != nullptr;
   if (paged) cached_sequence(a, &seq);
@@ -380,11 +396,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
         *sp = sv + S::kRows;  // values and keys may take turns
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
-  const int group = a.q_heads / a.kv_heads, head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
+  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
+  const Place place(a, 1);
+  const int group = a.q_heads / a.kv_heads, head = place.head, rank = place.rank, D = a.head_dim;
   PromptSequence seq;
   int tile;
-  if (!find_sequence(a.starts, a.sequences, a.tokens, group, BT, (int64_t)gridDim.x - 1 - blockIdx.x, &seq, &tile)) return;
+  if (!find_sequence(a.starts, a.sequences, a.tokens, group, BT, place.slots - 1 - place.slot, &seq, &tile)) return;
   const int row0 = tile * BT, rows = min(BT, seq.length * group - row0);
   auto token_of = [&](int r) { return (int64_t)(seq.first + (row0 + r) / group); };
   auto head_of = [&](int r) { return (int64_t)(head * group + (row0 + r) % group); };
@@ -462,12 +479,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
   __shared__ float slse[BT], sdelta[BT];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  const int group = a.q_heads / a.kv_heads, head = blockIdx.y, rank = blockIdx.z, D = a.head_dim;
+  const Place place(a, split.parts);
+  const int group = a.q_heads / a.kv_heads, head = place.head, rank = place.rank, part = place.part, D = a.head_dim;
   PromptSequence seq;
   int tile;
   // the first keys of a sequence are seen by the most rows: they start first
-  const int part = (int)(blockIdx.x % (unsigned)split.parts);
-  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, BT, blockIdx.x / (unsigned)split.parts, &seq, &tile)) return;
+  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, BT, place.slot, &seq, &tile)) return;
   const int j0 = tile * BT, keys = min(BT, seq.length - j0);
   auto key = [&](const void* base, int64_t stride, int r) {
     return r < keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
@@ -599,7 +616,7 @@ cudaError_t forward(const PromptArgs& a, cudaStream_t stream) {
   PromptArgs copy = a;
   void* params[] = {&copy, &split, &slots};
   const cudaError_t e = launch((const void*)prompt_kernel<T, DP, BT>,
-                               dim3((unsigned)(slots * split.parts), (unsigned)a.kv_heads, (unsigned)a.nranks),
+                               dim3((unsigned)(items * split.parts)),
                                shared_bytes<DP, BT>(2, 1), stream, params);
   if (e != cudaSuccess || split.parts == 1) return e;
   return launch_op((const void*)prompt_join_rows_kernel<T, DP, BT>, dim3((unsigned)(items * BT)), 128, 0, stream, params);
@@ -609,18 +626,17 @@ template <typename T, int DP, int BT>
 cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
   PromptBwdArgs copy = a;
   void* params[] = {&copy};
-  const unsigned kv = (unsigned)a.kv_heads, n = (unsigned)a.nranks;
+  const int64_t lanes = (int64_t)a.kv_heads * a.nranks;
   cudaError_t e = launch((const void*)prompt_bwd_rows_kernel<T, DP, BT>,
-                               dim3((unsigned)prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT), kv, n),
+                               dim3((unsigned)(prompt_slots(a.tokens, a.sequences, a.q_heads / a.kv_heads, BT) * lanes)),
                                shared_bytes<DP, BT>(kApart<DP> ? 4 : 3, 1), stream, params);
   if (e != cudaSuccess) return e;
   const int64_t slots = prompt_slots(a.tokens, a.sequences, 1, BT);
   KeyParts split;
-  split.parts = key_parts(slots * a.kv_heads * a.nranks, kPromptParts,
-                          (int64_t)a.tokens / a.sequences * (a.q_heads / a.kv_heads) / (2 * BT));
+  split.parts = key_parts(slots * lanes, kPromptParts, (int64_t)a.tokens * (a.q_heads / a.kv_heads) / (2 * BT));
   split.sums = (float*)(a.ws + kOpScratchOffset + delta_bytes(a.nranks, a.tokens, a.q_heads));
   void* key_params[] = {&copy, &split};
-  e = launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>, dim3((unsigned)(slots * split.parts), kv, n),
+  e = launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>, dim3((unsigned)(slots * lanes * split.parts)),
              shared_bytes<DP, BT>(kApart<DP> ? 4 : 3, 2), stream, key_params);
   return e != cudaSuccess || split.parts == 1 ? e : launch_prompt_key_parts(a, split, stream);
 }
