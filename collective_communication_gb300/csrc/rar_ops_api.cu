@@ -283,7 +283,9 @@ rar_status check_prompt(int nranks, int64_t tokens, int q_heads, int kv_heads, i
                         const int32_t* starts, int sequences, Spans* s) {
   const rar_status st = check_ranks(nranks, dtype);
   if (st != RAR_OK) return st;
-  if (!prompt_sizes_ok(tokens, q_heads, kv_heads, head_dim) || sequences < 0 || sequences > INT32_MAX / 2) return RAR_ERR_ARG;
+  if (!prompt_sizes_ok(tokens, q_heads, kv_heads, head_dim) || sequences < 0) return RAR_ERR_ARG;
+  // blocks of a launch: a tile of 32 rows or more each, and one for every sequence and key head
+  if ((int64_t)sequences > INT32_MAX / 2 / ((int64_t)kv_heads * nranks)) return RAR_ERR_ARG;
   if (starts == nullptr && sequences > 0) return RAR_ERR_ARG;
   if (!aligned(starts, 4)) return RAR_ERR_ALIGN;
   s->read(span(starts, sequences > 0 ? ((int64_t)sequences + 1) * 4 : 0));

@@ -588,7 +588,8 @@ RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const 
  * token attends to key head h / (q_heads / kv_heads) of the tokens of its sequence up
  * to and including itself (q_heads a multiple of kv_heads):
  *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = log sum_j exp(scale * q . k_j)
- * q[r], out[r] are [tokens, q_heads, head_dim]; tokens * q_heads < 2^31. lse: host array
+ * q[r], out[r] are [tokens, q_heads, head_dim]; tokens * q_heads < 2^31, and
+ * num_sequences * kv_heads * nranks < 2^30. lse: host array
  * of nranks pointers to float [tokens, q_heads], or NULL. Rows of tokens in no sequence
  * (ahead of the first, behind the last) are left as they were. Starts that are out of
  * order or range report RAR_ERR_CAPACITY, and the rows concerned are left or written
@@ -606,8 +607,12 @@ RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const 
  *   out and lse of the forward call. dk and dv are sums over the query heads of a group.
  *   No gradient goes through lse. The same bits every time.
  * A key or value of a sequence that is infinite or NaN makes the rows that see it
- * infinite or NaN, and may make those of its earlier tokens NaN; other sequences' rows
- * do not depend on it.
+ * infinite or NaN (a key that gives a score of -inf: no weight), and may make those of its
+ * earlier tokens NaN; likewise a row of dout the gradients of the sequence. Other
+ * sequences' rows do not depend on it.
+ * RAR_BF16 with head_dim up to 128 and groups of up to 128 query heads runs on the tensor
+ * cores, with the weights of values (and score gradients) rounded to bf16; all else in
+ * binary32 on the ordinary arithmetic units.
  */
 RAR_API size_t rar_prompt_attention_workspace_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads,
                                                     int head_dim); /* for all three; 0: bad arguments */
