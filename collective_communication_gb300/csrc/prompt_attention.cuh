@@ -132,9 +132,54 @@ __device__ __forceinline__ bool find_sequence(const int32_t* starts, int sequenc
 __device__ __forceinline__ void cached_sequence(const PromptArgs& a, PromptSequence* seq) {
   const int len = a.lens[seq->index];
   const int room = a.max_blocks << a.page_shift;
-  if ((threadIdx.x & 31) == 0 && (len < 0 || len > room)) op_report(a.ws, kErrCapacity);
+  if (len < 0 || len > room) op_report(a.ws, kErrCapacity);
   seq->before = (len < 0 ? 0 : len) - seq->length;
   seq->keys = len < 0 ? 0 : len < room ? len : room;
 }
+
+// The order in which a kernel's items are taken, where there are at most 32 sequences:
+// those with the most work first, whatever sequence they are of. A warp steps through
+// it, a lane a sequence. An item is `unit` tokens; its work is the keys that its last
+// token sees, or (by_keys) the tokens that see its first one. (In the order of the
+// numbers, sequences of different lengths left SMs with what they happened to get:
+// TIME_LPT.)
+struct ItemOrder {
+  int first, length, before, keys;  // of the lane's sequence
+  int items, left;                  // of them not taken
+  int64_t taken;                    // of all sequences
+  int last_sequence, last_tile;     // the last one taken
+
+  __device__ __forceinline__ bool begin(const int32_t* starts, int sequences, int tokens, int unit) {
+    first = length = before = keys = items = left = last_sequence = last_tile = 0;
+    taken = 0;
+    if (sequences > 32) return false;
+    const int s = (int)(threadIdx.x & 31);
+    if (s < sequences) {
+      const int a = starts[s], b = starts[s + 1];
+      if (a >= 0 && b >= a && b <= tokens) {
+        first = a;
+        length = keys = b - a;
+        items = (length + unit - 1) / unit;
+      }
+    }
+    left = items;
+    return true;
+  }
+  // Item number n, none below the last one asked for; false if there are no more.
+  __device__ __forceinline__ bool advance(int64_t n, int unit, bool by_keys, int* sequence, int* tile) {
+    for (; taken <= n; taken++) {
+      const int i = by_keys ? items - left : left - 1;
+      const int work = left == 0 ? INT32_MIN : by_keys ? length - i * unit : min(before + min((i + 1) * unit, length), keys);
+      const int most = __reduce_max_sync(~0u, work);
+      if (__all_sync(~0u, left == 0)) return false;
+      last_sequence = __ffs(__ballot_sync(~0u, left > 0 && work == most)) - 1;
+      last_tile = __shfl_sync(~0u, i, last_sequence);
+      if ((int)(threadIdx.x & 31) == last_sequence) left--;
+    }
+    *sequence = last_sequence;
+    *tile = last_tile;
+    return true;
+  }
+};
 
 }  // namespace rar

@@ -77,8 +77,9 @@ struct Work {
   KeyParts split;
 };
 
-// Item number n in order, from the last tiles of a sequence on, or from the first; false if there is none (a whole warp).
-__device__ __forceinline__ bool find_item(const PromptBwdArgs& a, const Work& work, bool last_first, int64_t n, Item* item) {
+// Item number n in order; 0 if there is none, -1 if there are no more (a whole warp).
+__device__ __forceinline__ int find_item(const PromptBwdArgs& a, const Work& work, ItemOrder& order, bool ordered, bool by_keys,
+                                         int64_t n, Item* item) {
   const int64_t lanes = (int64_t)a.kv_heads * a.nranks, whole = n / work.split.parts, slot = whole / lanes;
   const int lane_of = (int)(whole % lanes);
   item->part = (int)(n % work.split.parts);
@@ -86,28 +87,36 @@ __device__ __forceinline__ bool find_item(const PromptBwdArgs& a, const Work& wo
   item->rank = lane_of / a.kv_heads;
   PromptSequence seq;
   int tile;
-  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, work.unit, last_first ? work.slots - 1 - slot : slot, &seq, &tile))
-    return false;
+  if (ordered) {
+    if (!order.advance(slot, work.unit, by_keys, &seq.index, &tile)) return -1;
+    seq.first = __shfl_sync(~0u, order.first, seq.index);
+    seq.length = __shfl_sync(~0u, order.length, seq.index);
+  } else if (!find_sequence(a.starts, a.sequences, a.tokens, 1, work.unit, by_keys ? slot : work.slots - 1 - slot, &seq, &tile)) {
+    return 0;
+  }
   item->sequence = seq.first;
   item->length = seq.length;
   item->from = tile * work.unit;
   item->count = min(work.unit, seq.length - item->from);
   item->there = 1;
-  return true;
+  return 1;
 }
 
-// The warp that finds items for the others.
-__device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& work, bool last_first, Item* items,
+// The warp that finds items for the others, from those with the most work on: rows that
+// see many keys, or keys that many rows see.
+__device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& work, bool by_keys, Item* items,
                                             uint64_t* full, uint64_t* empty, volatile int* dead) {
   const int lane = threadIdx.x & 31;
   uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
   const int64_t all = work.slots * work.split.parts * a.kv_heads * a.nranks;
+  ItemOrder order;
+  const bool ordered = order.begin(a.starts, a.sequences, a.tokens, work.unit);
   int64_t n = blockIdx.x;
   for (int i = 0;;) {
     Item item;
-    const bool more = n < all;
-    if (!more) item.there = 0;
-    if (!more || find_item(a, work, last_first, n, &item)) {
+    const int found = n < all ? find_item(a, work, order, ordered, by_keys, n, &item) : -1;
+    if (found < 0) item.there = 0;
+    if (found != 0) {
       if (!wait_warp(&empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, dead)) break;
       if (lane == 0) {
         items[i % kItemSlots] = item;
@@ -115,7 +124,7 @@ __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& 
       }
       i++;
     }
-    if (!more) break;
+    if (found < 0) break;
     uint32_t next = 0;
     if (lane == 0) next = atomicAdd(&counters[kNextItem], 1);
     n = (int64_t)gridDim.x + __shfl_sync(~0u, next, 0);
@@ -306,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   const int group = a.q_heads / a.kv_heads, D = a.head_dim, per_tile = kTile / group, steps = (D + 15) / 16;
 
   if (warp == kItemWarp) {
-    serve_items(a, work, true, items, item_full, item_empty, dead);  // the last rows see the most keys
+    serve_items(a, work, false, items, item_full, item_empty, dead);
   } else if (warp == kCopyWarp) {
     int n = 0;  // tiles of keys so far
     for (int i = 0;; i++) {
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   auto last_tile = [&](const Taken& t) { return tile_of(t, t.part + 1); };
 
   if (warp == kItemWarp) {
-    serve_items(a, work, false, items, item_full, item_empty, dead);  // the first keys are seen by the most rows
+    serve_items(a, work, true, items, item_full, item_empty, dead);
   } else if (warp == kCopyWarp) {
     int n = 0, some = 0;  // tiles of rows, and items that have some, so far
     for (int i = 0;; i++) {

@@ -17,8 +17,8 @@
 // bf16 (2^-8 of themselves, in both directions): their sum l is of the unrounded ones,
 // so the roundings average out over the keys and stay below the result's own.
 //
-// Blocks stay, one an SM, and take items from a counter, those with the most keys first
-// within a sequence. A fourth warp takes them ahead and finds out what they are, so
+// Blocks stay, one an SM, and take items from a counter, those with the most keys
+// first. A fourth warp takes them ahead and finds out what they are, so
 // that queries, keys and values of the next item are copied, and its scores worked out,
 // while the last one's results are still being stored.
 //
@@ -74,6 +74,8 @@ struct Layout {
   static constexpr int kQueries = 3;                     // tiles of queries: the item's, and one of the next
   static constexpr int kStages = DP == 64 ? 8 : 4;       // tiles of keys or values
   static constexpr int kShared = (kQueries + kStages) * kTile + 1024;
+  // With half the columns for O, weights have columns of their own, and the S of the next tile need not wait for P V.
+  static constexpr bool kApart = DP == 64;
 };
 
 struct Split {
@@ -97,23 +99,31 @@ struct Item {
   int64_t index;    // of the item, parts aside
 };
 
-// Item number n in order; false if there is none (a whole warp).
+// Item number n in order; 0 if there is none, -1 if there are no more (a whole warp).
 template <int FORM>
-__device__ __forceinline__ bool find_item(const PromptArgs& a, const Split& split, int64_t n, Item* item) {
+__device__ __forceinline__ int find_item(const PromptArgs& a, const Split& split, ItemOrder& order, bool ordered, int64_t n,
+                                         Item* item) {
   const int per_tile = kRows / (a.q_heads / a.kv_heads);
   item->part = (int)(n % split.parts);
   const int64_t whole = n / split.parts, lanes = (int64_t)a.kv_heads * a.nranks;
   const int lane_of = (int)(whole % lanes);
   item->head = lane_of % a.kv_heads;
   item->rank = lane_of / a.kv_heads;
-  // the last tokens of a sequence see the most keys: they come first
-  const int64_t slot = split.slots - 1 - whole / lanes;
-  item->index = slot * lanes + lane_of;
   PromptSequence seq;
   int pair;
-  if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, slot, &seq, &pair)) return false;
-  if (FORM != kDense) cached_sequence(a, &seq);
+  if (ordered) {
+    if (!order.advance(whole / lanes, 2 * per_tile, false, &seq.index, &pair)) return -1;
+    seq.first = __shfl_sync(~0u, order.first, seq.index);
+    seq.length = __shfl_sync(~0u, order.length, seq.index);
+    seq.before = __shfl_sync(~0u, order.before, seq.index);
+    seq.keys = __shfl_sync(~0u, order.keys, seq.index);
+  } else {
+    // the last tokens of a sequence see the most keys: they come first
+    if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, split.slots - 1 - whole / lanes, &seq, &pair)) return 0;
+    if (FORM != kDense) cached_sequence(a, &seq);
+  }
   const int token0 = pair * 2 * per_tile;  // of the sequence
+  item->index = ((int64_t)seq.first / (2 * per_tile) + seq.index + pair) * lanes + lane_of;  // by number, as the join finds it
   item->sequence = seq.index;
   item->keys = seq.keys;
   item->first = seq.first + token0;
@@ -132,7 +142,7 @@ __device__ __forceinline__ bool find_item(const PromptArgs& a, const Split& spli
 #pragma unroll
   for (int t = 0; t < 2; t++) item->last[t] = max(item->begin, min(tiles[t], item->end));
   item->there = 1;
-  return true;
+  return 1;
 }
 
 template <int DP, int FORM>
@@ -143,7 +153,8 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
   constexpr int NS = L::kStages, NQ = L::kQueries;
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (shared_address(raw) & 1023));
-  __shared__ uint64_t q_full[NQ], q_empty[NQ], full[NS], empty[NS], s_full[2], p_half[2], p_full[2], o_full[2], o_free[2], out_ready[2],
+  __shared__ uint64_t q_full[NQ], q_empty[NQ], full[NS], empty[NS], s_full[2], s_read[2], p_half[2], p_full[2], pv_done[2], o_full[2],
+      o_free[2], out_ready[2],
       item_full[kItemSlots], item_empty[kItemSlots];
   __shared__ Item items[kItemSlots];
   __shared__ uint32_t tmem_at, lost[kLostSlots][4];
@@ -162,6 +173,8 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     }
     for (int i = 0; i < 2; i++) {
       barrier_init(&s_full[i], 1);
+      barrier_init(&s_read[i], 4);
+      barrier_init(&pv_done[i], 1);
       barrier_init(&p_half[i], kRows);
       barrier_init(&p_full[i], kRows);
       barrier_init(&o_full[i], 1);
@@ -189,7 +202,8 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
   constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
-  constexpr uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 384};
+  constexpr uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 256 + DP};
+  constexpr uint32_t p_at[2] = {L::kApart ? tmem + 384 : s_at[0], L::kApart ? tmem + 448 : s_at[1]};
   uint8_t* const ring = smem + NQ * L::kTile;
   const int group = a.q_heads / a.kv_heads, D = a.head_dim;
   const int per_tile = kRows / group;  // tokens of a tile
@@ -202,12 +216,20 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
   if (warp == kItemWarp) {
     uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
     const int64_t all = split.items * split.parts;
+    ItemOrder order;
+    const bool ordered = order.begin(a.starts, a.sequences, a.tokens, 2 * per_tile);
+    if (FORM != kDense && ordered && lane < a.sequences) {
+      PromptSequence seq = {lane, order.first, order.length, 0, order.length};
+      cached_sequence(a, &seq);
+      order.before = seq.before;
+      order.keys = seq.keys;
+    }
     int64_t n = blockIdx.x;
     for (int i = 0;;) {
       Item item;
-      const bool more = n < all;
-      if (!more) item.there = 0;
-      if (!more || find_item<FORM>(a, split, n, &item)) {
+      int found = n < all ? find_item<FORM>(a, split, order, ordered, n, &item) : -1;
+      if (found < 0) item.there = 0;
+      if (found != 0) {
         if (!wait_warp(&item_empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, dead)) break;
         if (lane == 0) {
           items[i % kItemSlots] = item;
@@ -215,7 +237,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         }
         i++;
       }
-      if (!more) break;
+      if (found < 0) break;
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(&counters[kNextItem], 1);
       n = (int64_t)gridDim.x + __shfl_sync(~0u, next, 0);
@@ -505,6 +527,18 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         const uint32_t k_phase = v_phase ^ (k_stage == 0);
         const int next_stage = k_stage + 1 == NS ? 0 : k_stage + 1;
         const uint32_t next_phase = k_phase ^ (next_stage == 0);
+        if (L::kApart && more) {
+          if (!(fine = wait_warp(&full[k_stage], k_phase, dead))) break;
+#pragma unroll
+          for (int t = 0; t < 2; t++) {
+            if (!fine || j + 1 >= last[t]) continue;
+            if (!(fine = wait_warp(&s_read[t], walked[t] & 1, dead))) break;
+            fence_after();
+            score(t, ring_at + k_stage * L::kTile);
+          }
+          if (!fine) break;
+          commit(lead, &empty[k_stage]);
+        }
 #pragma unroll
         for (int t = 0; t < 2; t++) {
           if (j < last[t]) {
@@ -512,27 +546,28 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
             if (j == begin && results[t] > 0 && !(fine = wait_warp(&o_free[t], (results[t] - 1) & 1, dead))) break;
             if (!(fine = wait_warp(&p_half[t], walked[t] & 1, dead))) break;
             fence_after();
-            weights_by_rows<8, 0, 0, 4>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, j > begin, kv_slab, kv_group);
+            weights_by_rows<8, 0, 0, 4>(lead, o_at[t], p_at[t], ring_at + v_stage * L::kTile, n_out, j > begin, kv_slab, kv_group);
             if (!(fine = wait_warp(&p_full[t], walked[t] & 1, dead))) break;
             fence_after();
-            weights_by_rows<8, 0, 4, 8>(lead, o_at[t], s_at[t], ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
+            weights_by_rows<8, 0, 4, 8>(lead, o_at[t], p_at[t], ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
             walked[t]++;
+            if (L::kApart) commit(lead, &pv_done[t]);
             if (j + 1 == last[t]) {
               commit(lead, &o_full[t]);
               results[t]++;
             }
           }
           // what the warp waits for beside the weights, it waits for while products run
-          if (more && t == 0 && !(fine = wait_warp(&full[k_stage], k_phase, dead))) break;
+          if (!L::kApart && more && t == 0 && !(fine = wait_warp(&full[k_stage], k_phase, dead))) break;
           if (more && t == 1 && !(fine = values(j + 1, next_stage, next_phase))) break;
-          if (j + 1 < last[t]) {
+          if (!L::kApart && j + 1 < last[t]) {
             fence_after();
             score(t, ring_at + k_stage * L::kTile);
           }
         }
         if (!fine) break;
         commit(lead, &empty[v_stage]);
-        if (more) commit(lead, &empty[k_stage]);
+        if (!L::kApart && more) commit(lead, &empty[k_stage]);
         // behind the item's last V: the next item's first K
         stage = more ? next_stage : k_stage;
         phase = more ? next_phase : k_phase;
@@ -580,6 +615,11 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) tmem_load32(s_at[t] + quarter + c, s + c);
         loads_done();
+        if (L::kApart) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(&s_read[t]);
+        }
         if (!(a.scale > 0.f)) {
 #pragma unroll
           for (int c = 0; c < kKeys; c++) s[c] = (s[c] ^ turn) & keep_bits;
@@ -603,6 +643,11 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
 #pragma unroll
           for (int i = 0; i < 4; i++) top[i] = fmaxf(top[i], __uint_as_float(s[c + i]));
         const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // the last tile's weights have been read, and O has them
+        if (L::kApart && j > begin) {
+          if (!(fine = wait(&pv_done[t], walked & 1, dead))) break;
+          fence_after();
+        }
         const float high = best * scale2;
         // (rows that are none have no say: what they hold would change how the others are rounded)
         if (__any_sync(~0u, mine && high > m + 8.f)) {
@@ -641,7 +686,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
             s[c / 2] = bf16_pair(x.x, x.y);
             s[c / 2 + 1] = bf16_pair(y.x, y.y);
           }
-          tmem_store32(s_at[t] + quarter + 32 * h, s + 32 * h);
+          tmem_store32(p_at[t] + quarter + 32 * h, s + 32 * h);
           stores_done();
           fence_before();
           arrive(h == 0 ? &p_half[t] : &p_full[t]);
