@@ -633,7 +633,8 @@ cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t slots = prompt_slots(a.tokens, a.sequences, 1, BT);
   KeyParts split;
-  split.parts = key_parts(slots * lanes, kPromptParts, (int64_t)a.tokens * (a.q_heads / a.kv_heads) / (2 * BT));
+  split.parts = key_parts(slots * lanes, kPromptParts, (int64_t)a.tokens * (a.q_heads / a.kv_heads) / (2 * BT),
+                          kLeastPlainRowTiles);
   split.sums = (float*)(a.ws + kOpScratchOffset + delta_bytes(a.nranks, a.tokens, a.q_heads));
   void* key_params[] = {&copy, &split};
   e = launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>, dim3((unsigned)(slots * lanes * split.parts)),
@@ -702,9 +703,9 @@ int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, 
     parts = (int64_t)kPromptSplitBlocks * (256 * ((head_dim <= 64 ? 64 : 128) + 2) + kPromptPartInfo) * 4;
   // what parts of the rows leave of dk and dv: a call of more sequences than one has no more of them
   const int unit = group <= 128 && head_dim <= 128 ? 128 : rows;
-  const int most = group <= 128 && head_dim <= 128 ? key_parts((tokens / unit + 1) * lanes, 152, tokens / (2 * (128 / group)))
+  const int most = group <= 128 && head_dim <= 128 ? key_parts((tokens / unit + 1) * lanes, kPromptSplitBlocks, tokens / (2 * (128 / group)), kLeastRowTiles)
                                                    : 1;
-  const int plain = key_parts((tokens / rows + 1) * lanes, kPromptParts, tokens * group / (2 * rows));
+  const int plain = key_parts((tokens / rows + 1) * lanes, kPromptParts, tokens * group / (2 * rows), kLeastPlainRowTiles);
   const int key_split = most > plain ? most : plain;
   const int64_t gradient = delta + (key_split > 1 ? key_split * 2 * key_part_floats(nranks, tokens, kv_heads, head_dim) * 4 : 0);
   return gradient > parts ? gradient : parts;

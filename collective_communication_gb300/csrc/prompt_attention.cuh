@@ -58,13 +58,18 @@ __host__ __device__ inline int64_t key_part_floats(int nranks, int64_t tokens, i
 }
 constexpr int kMostKeyParts = 8;
 // Parts for `items` tiles of keys on `blocks` resident blocks, where a key is seen by the rows of `row_tiles` tiles on
-// average. The items of a long sequence differ by the rows that see them: with fewer than two a block the first keys'
-// alone would take twice as long as the mean. A part has eight tiles of rows, for the cost of its sums.
-inline int key_parts(int64_t items, int64_t blocks, int64_t row_tiles) {
-  int64_t parts = 2 * blocks / (items > 0 ? items : 1);
-  if (parts > row_tiles / 8) parts = row_tiles / 8;
+// average. Few items are split until there are two a block, into parts of eight tiles of rows or more. The items of a long
+// sequence differ by the rows that see them, so they are split further, into parts of `least` tiles, for eight a
+// block: one of 8192 tokens, 4 key heads of 64, 658 us whole and 554 in four parts; of 4096 tokens, 8 key heads of 128, 64
+// tiles of rows or fewer each, 244 whole and 256 in two, for the cost of the parts' sums.
+inline int key_parts(int64_t items, int64_t blocks, int64_t row_tiles, int64_t least) {
+  if (items < 1) items = 1;
+  const int64_t fill = 2 * blocks / items < row_tiles / 8 ? 2 * blocks / items : row_tiles / 8;
+  const int64_t even = 8 * blocks / items < row_tiles / least ? 8 * blocks / items : row_tiles / least;
+  const int64_t parts = fill > even ? fill : even;
   return parts < 1 ? 1 : parts > kMostKeyParts ? kMostKeyParts : (int)parts;
 }
+constexpr int kLeastRowTiles = 32, kLeastPlainRowTiles = 8;  // on the tensor cores, and on the ordinary arithmetic units
 // Adds them up, in their order.
 cudaError_t launch_prompt_key_parts(const PromptBwdArgs& a, const KeyParts& parts, cudaStream_t stream);
 
