@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kChunks = 8;  // of a block, a warp each
 constexpr int kSortThreads = 512, kMergeThreads = 512;
-constexpr int kMergePairs = 16384;  // of whole tiles, in a merging block's shared memory
+constexpr int kMergePairs = 24576;  // of whole tiles, in a merging block's shared memory
 // Pairs of a tile: bisection in shared memory bounds its sort (8192 took 80 us), and the
 // number of tiles the merge's.
 constexpr int kSmallTile = 1024, kLargeTile = 4096;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
 }
 
 // Tiles to one row of pairs, a thread a pair; tokens that ask for nothing stay behind.
-// Blocks bisect in shared memory, 128 KiB of tiles at a time: in global memory, with a
+// Blocks bisect in shared memory, 192 KiB of tiles at a time: in global memory, with a
 // tenth of the pairs in L1 at first, 17 tiles took 36 us.
 __global__ void __launch_bounds__(kMergeThreads) embed_merge_kernel(const __grid_constant__ EmbedBwdArgs a) {
   extern __shared__ uint64_t pair[];

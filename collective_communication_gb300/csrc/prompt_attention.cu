@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(con
   __shared__ int64_t key_row[BT];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
+  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws, threadIdx.x, kThreads);
   const Place place(a, split.parts);
   const int group = a.q_heads / a.kv_heads, head = place.head, rank = place.rank, part = place.part, D = a.head_dim;
   PromptSequence seq;
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
         *sp = sv + S::kRows;  // values and keys may take turns
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
-  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
+  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws, threadIdx.x, kThreads);
   const Place place(a, 1);
   const int group = a.q_heads / a.kv_heads, head = place.head, rank = place.rank, D = a.head_dim;
   PromptSequence seq;

@@ -95,10 +95,11 @@ struct PromptSequence {
   int keys;                  // tokens with a key
 };
 
-// Every pair of starts, by the threads of one block; true if they are in order.
-__device__ __forceinline__ void check_starts(const int32_t* starts, int sequences, int tokens, char* ws) {
+// Every pair of starts, by `threads` threads from 0 on.
+__device__ __forceinline__ void check_starts(const int32_t* starts, int sequences, int tokens, char* ws, int thread,
+                                             int threads) {
   bool bad = false;
-  for (int s = threadIdx.x; s < sequences; s += blockDim.x) {
+  for (int s = thread; s < sequences; s += threads) {
     const int a = starts[s], b = starts[s + 1];
     bad |= a < 0 || b < a || b > tokens;
   }

@@ -104,14 +104,17 @@ __device__ __forceinline__ int find_item(const PromptBwdArgs& a, const Work& wor
 
 // The warp that finds items for the others, from those with the most work on: rows that
 // see many keys, or keys that many rows see.
-__device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& work, bool by_keys, Item* items,
-                                            uint64_t* full, uint64_t* empty, volatile int* dead) {
+__device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& work, bool by_keys, uint32_t magic,
+                                            Item* items, uint64_t* full, uint64_t* empty, volatile int* dead) {
   const int lane = threadIdx.x & 31;
   uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
   const int64_t all = work.slots * work.split.parts * a.kv_heads * a.nranks;
   ItemOrder order;
   const bool ordered = order.begin(a.starts, a.sequences, a.tokens, work.unit);
-  int64_t n = blockIdx.x;
+  // without a workspace there are no items: the others wait for the first one, not for the header
+  const bool ready = magic == kOpMagic;
+  if (!ready && lane == 0) op_report(a.ws, kErrWorkspace);
+  int64_t n = ready ? blockIdx.x : all;
   for (int i = 0;;) {
     Item item;
     const int found = n < all ? find_item(a, work, order, ordered, by_keys, n, &item) : -1;
@@ -130,7 +133,7 @@ __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& 
     n = (int64_t)gridDim.x + __shfl_sync(~0u, next, 0);
   }
   // the last block to have no more sets the counters back
-  if (lane == 0 && atom_add_acq_rel_u32(&counters[kDoneBlocks], 1) == gridDim.x - 1) {
+  if (ready && lane == 0 && atom_add_acq_rel_u32(&counters[kDoneBlocks], 1) == gridDim.x - 1) {
     counters[kNextItem] = 0;
     counters[kDoneBlocks] = 0;
   }
@@ -305,8 +308,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
     barriers_ready();
   }
   const uint32_t magic = op_start(a.ws);
-  if (!op_ready(a.ws, magic)) return;
-  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
   constexpr uint32_t s_at = 0, dp_at = 256, dq_at = 384;  // all of tensor memory, from 0 on; S: two buffers of 128 columns
@@ -315,7 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   const int group = a.q_heads / a.kv_heads, D = a.head_dim, per_tile = kTile / group, steps = (D + 15) / 16;
 
   if (warp == kItemWarp) {
-    serve_items(a, work, false, items, item_full, item_empty, dead);
+    serve_items(a, work, false, magic, items, item_full, item_empty, dead);
+  } else if (warp == kNumbersWarp) {
+    if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws, lane, 32);
   } else if (warp == kCopyWarp) {
     int n = 0;  // tiles of keys so far
     for (int i = 0;; i++) {
@@ -518,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   }
   if (threadIdx.x < kTile) token_of[threadIdx.x] = (uint8_t)(threadIdx.x / group);
   const uint32_t magic = op_start(a.ws);
-  if (!op_ready(a.ws, magic)) return;
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
   constexpr uint32_t s_at = 0, dp_at = 128, dv_at = 256, dk_at = 384;  // all of tensor memory, from 0 on
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   auto last_tile = [&](const Taken& t) { return tile_of(t, t.part + 1); };
 
   if (warp == kItemWarp) {
-    serve_items(a, work, true, items, item_full, item_empty, dead);
+    serve_items(a, work, true, magic, items, item_full, item_empty, dead);
   } else if (warp == kCopyWarp) {
     int n = 0, some = 0;  // tiles of rows, and items that have some, so far
     for (int i = 0;; i++) {

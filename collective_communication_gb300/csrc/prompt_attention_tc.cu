@@ -197,8 +197,6 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     }
   }
   const uint32_t magic = op_start(a.ws);
-  if (!op_ready(a.ws, magic)) return;
-  if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws);
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
   constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
@@ -224,7 +222,10 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       order.before = seq.before;
       order.keys = seq.keys;
     }
-    int64_t n = blockIdx.x;
+    // without a workspace there are no items: the others wait for the first one, not for the header
+    const bool ready = magic == kOpMagic;
+    if (!ready && lane == 0) op_report(a.ws, kErrWorkspace);
+    int64_t n = ready ? blockIdx.x : all;
     for (int i = 0;;) {
       Item item;
       int found = n < all ? find_item<FORM>(a, split, order, ordered, n, &item) : -1;
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       n = (int64_t)gridDim.x + __shfl_sync(~0u, next, 0);
     }
     // the last block to have no more sets the counters back
-    if (lane == 0 && atom_add_acq_rel_u32(&counters[kDoneBlocks], 1) == gridDim.x - 1) {
+    if (ready && lane == 0 && atom_add_acq_rel_u32(&counters[kDoneBlocks], 1) == gridDim.x - 1) {
       counters[kNextItem] = 0;
       counters[kDoneBlocks] = 0;
     }
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     }
     drain();
   } else if (warp == kStoreWarp) {
+    if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws, lane, 32);
     int queries = 0, results[2] = {0, 0};
     for (int i = 0;; i++) {
       if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;

@@ -695,3 +695,25 @@ def test_embed_nothing():
     assert bool((grads[0] == MARK).all())
     B.embed_tokens_backward(none, rows, grads, ws)
     assert B.get_status(ws) == B.Status.OK and bool((grads[0] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_workspace_that_is_not_initialised(dtype):
+    """The kernels write nothing but the status."""
+    q, k, v, starts = prompt_inputs(1, [300, 20], 4, 2, 64, dtype)
+    ws = workspace(q, 2)
+    ws.buf.zero_()
+    out, lse = torch.full_like(q, MARK), torch.full(q.shape[:3], MARK, device="cuda")
+    B.prompt_attention(q, k, v, starts, out, lse, ws)
+    assert B.get_status(ws) == B.Status.ERR_WORKSPACE
+    grads = [torch.full_like(x, MARK) for x in (q, k, k)]
+    B.prompt_attention_backward(q, k, v, starts, out, lse, q, *grads, ws)
+    assert B.get_status(ws) == B.Status.ERR_WORKSPACE
+    rows, tables = torch.full((20, 64), MARK, device="cuda"), torch.full((1, 9, 64), MARK, device="cuda")
+    tokens = torch.zeros(20, dtype=torch.int32, device="cuda")
+    B.embed_tokens(tokens, torch.zeros_like(tables), rows, ws)
+    assert B.get_status(ws) == B.Status.ERR_WORKSPACE
+    B.embed_tokens_backward(tokens, torch.zeros(20, 64, device="cuda"), tables, ws)
+    assert B.get_status(ws) == B.Status.ERR_WORKSPACE
+    for x in (out, lse, *grads, rows, tables):
+        assert bool((x == MARK).all())
