@@ -5,6 +5,7 @@
 //
 // Both are bound by memory. The lookup takes a warp for 2 KiB of a row: its four
 // 16-byte loads a lane are in flight at once, and a few tokens still make many warps.
+// 16384 tokens of 7168 bf16 elements take 54 us, 6.2 TB/s.
 //
 // The gradient sums in an order that no run changes, with no atomics on values: the
 // pairs (word, t) are sorted, and a warp sums a chunk of 32 (few tokens: 8) sorted
@@ -13,12 +14,13 @@
 // chunks a block, and of words of several blocks in a kernel behind, always in order.
 // A pair is one 64-bit number, no two alike, so any way of sorting gives the same
 // order: blocks sort tiles in shared memory (32 pairs in a warp's lanes, then runs merge by
-// bisection), and if there are several, each
-// pair's place is its place in its tile and its places by bisection in the others.
+// bisection), and if there are several, each pair's place is its place in its tile and
+// its places by bisection in the others.
 // Where the tables are not added to, further warps of that kernel look their words up
 // in the sorted pairs and fill the rows of those that do not occur with zeros: every
 // row is written once. (Filling whole tables beside the sorting blocks, and rows that
-// occur again, took 187 us where that took 170.)
+// occur again, took 187 us where that took 170.) 16385 tokens of 4096 elements, 32008
+// words, take 131 us, 104 of them the sums and zeros at 6.3 TB/s; 300 tokens take 14 us, a chain of three launches.
 #include "op_common.cuh"
 #include "rar_launch.h"
 

@@ -29,6 +29,12 @@
 //   keys:  P(i) ready: dV += P(i) dO, S(i+1) | dS(i) ready: dK += dS(i) Q, dP(i+1) | ...
 // Blocks stay, one an SM, and take items (a tile of rows, or of keys) from a counter;
 // a warp finds the next one while the last is under way, and its first tiles are copied.
+//
+// Measured: 8192 tokens of one sequence, 16 query heads on 4 key heads of 64: 545 us, 0.88
+// PFLOP/s of the seven products. What bounds it is the weights' chain, from scores through
+// two roundings to the last product, as long for half the products of a head size of 128:
+// tensor cores 36 % of the time, issue slots 43 %. 4097 tokens of 9 sequences, 32 query
+// heads on 8 key heads of 128: 141 us, 16 of them delta (cold; out and dout from memory).
 #include <cstdio>
 
 #include "prompt_attention.cuh"

@@ -30,7 +30,17 @@
 // Few rows over many keys (the verification of drafted tokens behind a long context)
 // would leave most SMs idle: where the items would be at most half of the SMs, each
 // one's keys are split over several, which leave O, m and l unscaled as binary32, and a
-// second kernel adds them up in the order of the keys, a warp a row.
+// second kernel adds them up in the order of the keys, a block a row.
+//
+// Measured: 16384 tokens of one sequence, 16 query heads on 2 key heads of 128: 610 us,
+// 1.8 PFLOP/s, where a plain matrix product makes 1.95 in a burst and 1.73 over seconds,
+// with lower clocks; chunks of 2048 tokens behind up to 8192 cached ones, 64 heads on 8,
+// pages of 16: 293 us, tensor cores 68 % of the time. 8192 tokens in 17 sequences: 114 us,
+// tensor cores 42 %: items are over before the chain of their products and weights has
+// filled the SM, and reading and writing rows takes 45 us of it at the memory's rate.
+// Heads of 64 take 550 us for the 16384 tokens: the exponentials bound them, as many
+// for half the products. Five tokens behind 30011 take 21 us, a chain of a block's start,
+// its share of the keys and the join.
 #include <cstdio>
 
 #include "prompt_attention.cuh"

@@ -108,10 +108,6 @@ __device__ __forceinline__ void copy_4d(void* to, const CUtensorMap* m, int x, i
       "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(shared_address(b))
       : "memory");
 }
-__device__ __forceinline__ void prefetch_3d(const CUtensorMap* m, int x, int y, int z) {  // into L2
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
 __device__ __forceinline__ void store_3d(const CUtensorMap* m, int x, int y, int z, const void* from) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x), "r"(y),
                "r"(z), "r"(shared_address(from))
