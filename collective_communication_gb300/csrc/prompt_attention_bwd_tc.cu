@@ -492,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
                                                                      const __grid_constant__ Maps maps,
                                                                      const __grid_constant__ Work work) {
   using L = Layout<DP>;
-  constexpr int NS = L::kRowStages;
+  constexpr int NS = L::kRowStages, SB = DP == 64 ? 2 : 1;  // SB: buffers of scores, what tensor memory has room for
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (shared_address(raw) & 1023));
-  __shared__ uint64_t kv_full, kv_empty, full[NS], empty[NS], s_full, p_ready, dp_full, ds_ready, sums_full, sums_free,
+  __shared__ uint64_t kv_full, kv_empty, full[NS], empty[NS], s_full[SB], p_ready[SB], dp_full, ds_ready, sums_full, sums_free,
       item_full[kItemSlots], item_empty[kItemSlots];
   __shared__ Item items[kItemSlots];
   __shared__ uint32_t tmem_at;
@@ -513,8 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       barrier_init(&full[i], 2);
       barrier_init(&empty[i], 1 + kWeightWarps);
     }
-    barrier_init(&s_full, 1);
-    barrier_init(&p_ready, kWeightWarps);
+    // of each buffer: a warp may be through with the next tile's scores while another has not read these
+    for (int i = 0; i < SB; i++) {
+      barrier_init(&s_full[i], 1);
+      barrier_init(&p_ready[i], kWeightWarps);
+    }
     barrier_init(&dp_full, 1);
     barrier_init(&ds_ready, kWeightWarps);
     barrier_init(&sums_full, 1);
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   const uint32_t magic = op_start(a.ws);
   if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
   __syncthreads();
-  constexpr uint32_t s_at = 0, dp_at = 128, dv_at = 256, dk_at = 384;  // all of tensor memory, from 0 on
+  constexpr uint32_t s_at = 0, dp_at = SB * 128, dv_at = dp_at + 128, dk_at = dv_at + DP;  // all of tensor memory, from 0 on
   uint8_t *const k_tile = smem, *const v_tile = smem + L::kBytes, *const ring = smem + 2 * L::kBytes;  // a stage: Q, dO
   const int D = a.head_dim, per_tile = kTile / group, steps = (D + 15) / 16;
   // tiles of rows, of all that see the item's keys the part's
@@ -629,8 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
           __syncwarp();
         }
         fence_after();
-        rows_by_rows<DP / 16, L::kSlab>(lead, s_at, k_at, ring_at + stage * 2 * L::kBytes, kTile, steps);
-        commit(lead, &s_full);
+        rows_by_rows<DP / 16, L::kSlab>(lead, s_at + n % SB * 128, k_at, ring_at + stage * 2 * L::kBytes, kTile, steps);
+        commit(lead, &s_full[n % SB]);
         return true;
       };
       auto value = [&](int x) {  // V dO^T
@@ -641,15 +644,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       bool fine = wait_warp(&kv_full, some & 1, dead) && score(begin);
       if (!fine) break;
       value(begin);
+      if (SB > 1 && begin + 1 < end && !score(begin + 1)) break;
       // sums of the item before have been read
       if (some > 0 && !wait_warp(&sums_free, (some - 1) & 1, dead)) break;
       for (int x = begin; x < end; x++) {
         const int n = base + x - begin, stage = n % NS;
         const bool more = x + 1 < end;
-        if (!(fine = wait_warp(&p_ready, n & 1, dead))) break;
+        if (!(fine = wait_warp(&p_ready[n % SB], n / SB & 1, dead))) break;
         fence_after();
-        weights_by_rows<2, kColumns>(lead, dv_at, s_at, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, x > begin, L::kSlab);
-        if (more && !(fine = score(x + 1))) break;
+        weights_by_rows<2, kColumns>(lead, dv_at, s_at + n % SB * 128, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, x > begin, L::kSlab);
+        if (x + SB < end && !(fine = score(x + SB))) break;
         if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
         fence_after();
         weights_by_rows<2, kColumns>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, x > begin, L::kSlab);
@@ -675,9 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       for (int x = begin; x < end; x++, n++) {
         const int stage = n % NS;
         if (!(fine = wait(&full[stage], n / NS & 1, dead))) break;  // the rows' numbers
-        if (!(fine = wait(&s_full, n & 1, dead))) break;
+        if (!(fine = wait(&s_full[n % SB], n / SB & 1, dead))) break;
         fence_after();
-        const uint32_t from = s_at + quarter + c0, dp_from = dp_at + quarter + c0;
+        const uint32_t from = s_at + n % SB * 128 + quarter + c0, dp_from = dp_at + quarter + c0;
         uint32_t s[kColumns], w[kColumns / 2];
         tmem_load32(from, s);
         loads_done();
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
 #pragma unroll
         for (int c = 0; c < kColumns; c += 2) w[c / 2] = bf16_pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         tmem_store16(from, w);
-        arrive_warp(&p_ready);
+        arrive_warp(&p_ready[n % SB]);
         if (!(fine = wait(&dp_full, n & 1, dead))) break;
         fence_after();
         uint32_t g[kColumns];
