@@ -16,11 +16,13 @@
 // order: blocks sort tiles in shared memory (32 pairs in a warp's lanes, then runs merge by
 // bisection), and if there are several, each pair's place is its place in its tile and
 // its places by bisection in the others.
-// Where the tables are not added to, further warps of that kernel look their words up
-// in the sorted pairs and fill the rows of those that do not occur with zeros: every
-// row is written once. (Filling whole tables beside the sorting blocks, and rows that
-// occur again, took 187 us where that took 170.) 16385 tokens of 4096 elements, 32008
-// words, take 131 us, 104 of them the sums and zeros at 6.3 TB/s; 300 tokens take 14 us, a chain of three launches.
+// Where the tables are not added to, the rows of words that do not occur are filled with
+// zeros, so that every row is written once: some by blocks beside the sort and the merge,
+// which leave most SMs free, and find their words in the tokens as they are; the others
+// by warps of the sums' kernel, which look their words up in the sorted pairs. (Filling
+// whole tables beside the sorting blocks, and rows that occur again, took 187 us where the
+// warps took 170.) 16385 tokens of 4096 elements, 32008 words, take 130 us, the floor of
+// the bytes 97; 300 tokens of 512 elements, with nothing sorted and in one launch, 5.8.
 #include "op_common.cuh"
 #include "rar_launch.h"
 
@@ -34,6 +36,8 @@ constexpr int kMergePairs = 24576;  // of whole tiles, in a merging block's shar
 // number of tiles the merge's.
 constexpr int kSmallTile = 1024, kLargeTile = 4096;
 constexpr int64_t kManyPairs = 65536;  // with small tiles no more than 64 of them
+constexpr int kClearBlocks = 152;  // that clear rows beside others; twice as many fit beside the sort
+constexpr int kFewTokens = 512;
 constexpr uint64_t kNone = (uint64_t)~0u << 32;  // with the token's number: a token of no word
 
 __device__ __forceinline__ int shard_of(const int64_t* first, int nranks, int64_t word) {
@@ -79,11 +83,54 @@ __global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ Embe
   }
 }
 
-// A block sorts a tile.
+// Rows of 0 for the words from first to end that no token asks for, by block number
+// `block` of `blocks`, from the tokens as they come: a block marks those of its words that
+// occur, so many at a time. Warps take a row each.
+__device__ __forceinline__ void clear_absent(const EmbedBwdArgs& a, int64_t first, int64_t end, int block, int blocks) {
+  constexpr int kWords = 4096;
+  __shared__ uint32_t occurs[kWords / 32];
+  const int64_t to = first + (end - first) * (block + 1) / blocks;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  for (int64_t from = first + (end - first) * block / blocks; from < to; from += kWords) {
+    const int count = (int)min((int64_t)kWords, to - from);
+    for (int i = threadIdx.x; i < kWords / 32; i += blockDim.x) occurs[i] = 0;
+    __syncthreads();
+    constexpr int kAhead = 16;
+    for (int64_t t0 = threadIdx.x; t0 < a.tokens; t0 += kAhead * blockDim.x) {
+      int32_t x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) {
+        const int64_t t = t0 + i * blockDim.x;
+        x[i] = t < a.tokens ? a.tokens_in[t] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) {
+        const int64_t w = x[i] - from;
+        if (w >= 0 && w < count) atomicOr(&occurs[w >> 5], 1u << (w & 31));
+      }
+    }
+    __syncthreads();
+    for (int w = threadIdx.x >> 5; w < count; w += warps) {
+      if (occurs[w >> 5] >> (w & 31) & 1) continue;
+      const int64_t word = from + w;
+      const int r = shard_of(a.first, a.nranks, word);
+      float4* const row = reinterpret_cast<float4*>(a.dtables[r] + (word - a.first[r]) * a.drow_stride[r]);
+#pragma unroll 8
+      for (int d = lane; d < a.hidden / 4; d += 32) row[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+  }
+}
+
+// A block sorts a tile; those behind them clear rows.
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_constant__ EmbedBwdArgs a) {
   extern __shared__ uint64_t pair[];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
+  if ((int)blockIdx.x >= a.tiles) {
+    clear_absent(a, 0, a.clear_first, (int)blockIdx.x - a.tiles, (int)gridDim.x - a.tiles);
+    return;
+  }
   const int64_t at = (int64_t)blockIdx.x * a.tile;
   const int count = (int)min((int64_t)a.tile, a.tokens - at);
   // warps sort 32 pairs each, by exchanges between lanes; then runs merge two by two
@@ -129,12 +176,18 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
 }
 
 // Tiles to one row of pairs, a thread a pair; tokens that ask for nothing stay behind.
+// Blocks behind those that merge clear rows.
 // Blocks bisect in shared memory, 192 KiB of tiles at a time: in global memory, with a
 // tenth of the pairs in L1 at first, 17 tiles took 36 us.
 __global__ void __launch_bounds__(kMergeThreads) embed_merge_kernel(const __grid_constant__ EmbedBwdArgs a) {
   extern __shared__ uint64_t pair[];
   const uint32_t magic = op_start(a.ws);
   if (!op_ready(a.ws, magic)) return;
+  const int blocks = (int)((a.tokens + kMergeThreads - 1) / kMergeThreads);
+  if ((int)blockIdx.x >= blocks) {
+    clear_absent(a, a.clear_first, a.clear_end, (int)blockIdx.x - blocks, (int)gridDim.x - blocks);
+    return;
+  }
   const int64_t i = (int64_t)blockIdx.x * kMergeThreads + threadIdx.x;
   const bool live = i < a.tokens;
   const uint64_t x = live ? a.sorted_tiles[i] : 0;
@@ -206,17 +259,18 @@ __device__ __forceinline__ int64_t first_of(const EmbedBwdArgs& a, uint32_t word
 __device__ __forceinline__ void clear_words(const EmbedBwdArgs& a, int64_t first, int count) {
   const int lane = threadIdx.x & 31;
   const int64_t mine = first + lane;
-  int64_t lo = first_of(a, (uint32_t)first);
-  const int64_t end = first_of(a, (uint32_t)min(first + count, a.first[a.nranks]));
+  const auto number = [](int64_t word) { return (uint32_t)min(word, (int64_t)1 << 31); };  // tokens' are below 2^31
+  int64_t lo = first_of(a, number(first));
+  const int64_t end = first_of(a, number(min(first + count, a.first[a.nranks])));
   bool absent = false;
   if (lane < count && mine < a.first[a.nranks]) {
     int64_t hi = end;  // the first pair of the word or a later one
     while (lo < hi) {
       const int64_t mid = (lo + hi) >> 1;
-      if (word_of(a.sorted[mid]) < (uint32_t)mine) lo = mid + 1;
+      if (word_of(a.sorted[mid]) < number(mine)) lo = mid + 1;
       else hi = mid;
     }
-    absent = lo >= end || word_of(a.sorted[lo]) != (uint32_t)mine;
+    absent = lo >= end || word_of(a.sorted[lo]) != number(mine);
   }
   for (uint32_t left = __ballot_sync(~0u, absent); left != 0; left &= left - 1) {
     const int64_t word = first + __ffs(left) - 1;
@@ -235,7 +289,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const __grid_constant__ 
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   if (blockIdx.x >= a.sum_blocks) {
-    const int64_t first = ((int64_t)(blockIdx.x - a.sum_blocks) * kChunks + warp) * a.clear_rows;
+    const int64_t first = a.clear_end + ((int64_t)(blockIdx.x - a.sum_blocks) * kChunks + warp) * a.clear_rows;
     if (first < a.first[a.nranks]) clear_words(a, first, a.clear_rows);
     return;
   }
@@ -368,6 +422,77 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
   store_sum(a, word, d, sum);
 }
 
+// Few tokens, with nothing sorted: a block a token and 256 columns, which is over if its word
+// has come before, and else finds the word's other tokens and sums their rows, eight warps
+// a part of them each if there are more than eight. Blocks behind these clear rows.
+template <typename T>
+__global__ void __launch_bounds__(256) embed_few_kernel(const __grid_constant__ EmbedBwdArgs a) {
+  __shared__ int same[kFewTokens], found[kFewTokens / 32];
+  __shared__ __align__(16) float part[kChunks][256];
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  if (blockIdx.x >= a.sum_blocks) {
+    clear_absent(a, 0, a.clear_end, (int)(blockIdx.x - a.sum_blocks), (int)(gridDim.x - a.sum_blocks));
+    return;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tokens = (int)a.tokens, i = (int)blockIdx.x / a.spans;
+  const int d = (int)blockIdx.x % a.spans * 256 + lane * 8;
+  const int32_t word = a.tokens_in[i];
+  if (word < 0 || word >= a.first[a.nranks]) return;
+  // warp by warp 32 tokens: which have the word
+  bool before = false;
+  uint32_t mine[kFewTokens / 256];
+#pragma unroll
+  for (int k = 0; k < kFewTokens / 256; k++) {
+    const int j = k * 256 + threadIdx.x;
+    const bool match = j < tokens && a.tokens_in[j] == word;
+    before |= match && j < i;
+    mine[k] = __ballot_sync(~0u, match);
+    if (lane == 0) found[k * kChunks + warp] = __popc(mine[k]);
+  }
+  if (__syncthreads_or(before)) return;
+  int count = 0;
+#pragma unroll
+  for (int k = 0; k < kFewTokens / 32; k++) {
+    if (k % kChunks == warp && (mine[k / kChunks] >> lane & 1) != 0)
+      same[count + __popc(mine[k / kChunks] & ((1u << lane) - 1))] = k * 32 + lane;
+    count += found[k];
+  }
+  __syncthreads();
+  const int warps = count > kChunks ? kChunks : 1;
+  if (warp >= warps) return;
+  const int end = count * (warp + 1) / warps;
+  float sum[8] = {}, v[8];
+  for (int k0 = count * warp / warps; k0 < end; k0 += 8) {
+    Pack8<T> x[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      x[k].zero();
+      if (k0 + k < end && d < a.hidden) x[k].load_stream((const T*)a.dout + (int64_t)same[k0 + k] * a.dout_stride + d);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      x[k].widen(v);
+#pragma unroll
+      for (int j = 0; j < 8; j++) sum[j] += v[j];
+    }
+  }
+  if (warps > 1) {
+    Pack8<float> y;
+    y.narrow(sum);
+    y.store(&part[warp][lane * 8]);
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < kChunks; w++) {
+      y.load(&part[w][lane * 8]);
+      y.widen(v);
+#pragma unroll
+      for (int j = 0; j < 8; j++) sum[j] += v[j];
+    }
+  }
+  if (d < a.hidden) store_sum(a, (uint32_t)word, d, sum);
+}
+
 template <typename T, int C>
 cudaError_t sums(EmbedBwdArgs& a, cudaStream_t stream) {
   void* params[] = {&a};
@@ -376,12 +501,17 @@ cudaError_t sums(EmbedBwdArgs& a, cudaStream_t stream) {
   a.sum_blocks = units;
   // a warp's rows: 32 KiB of them, one at least
   a.clear_rows = (int)(8192 / a.hidden < 1 ? 1 : 8192 / a.hidden > 32 ? 32 : 8192 / a.hidden);
-  const int64_t clears = a.accumulate ? 0 : div_up(a.first[a.nranks], (int64_t)a.clear_rows * kChunks);
+  const int64_t clears = a.accumulate ? 0 : div_up(a.first[a.nranks] - a.clear_end, (int64_t)a.clear_rows * kChunks);
   const cudaError_t e =
       launch_op((const void*)embed_sum_kernel<T, C>, dim3((unsigned)(units + clears)), 32 * kChunks, 0, stream, params);
   if (e != cudaSuccess || a.tokens <= B) return e;
   return launch_op((const void*)embed_join_kernel<B>, dim3((unsigned)div_up(units, 8)), 256, 0, stream, params);
 }
+
+// Every block of few tokens reads them all, and most rows are one block's work: at 1600 blocks
+// (100 tokens of 4096 elements) 31 us where the sort takes 34, at 300 tokens of 512 elements
+// 11 and 18, but at 4096 (256 of 4096) 24 and 22, at 8192 (512 of 4096) 23 and 18.
+bool few_tokens(int64_t tokens, int spans) { return tokens <= kFewTokens && tokens * spans <= 152 * 16; }
 
 // Chunks of 32 tokens leave less to join; of 8, where they would make too few warps.
 bool short_chunks(int64_t tokens, int hidden) { return div_up(tokens, 32) * div_up(hidden, 256) < 152 * 16; }
@@ -409,20 +539,38 @@ cudaError_t launch_embed_tokens_bwd(EmbedBwdArgs& a, cudaStream_t stream) {
   a.tile = a.tokens <= kManyPairs ? kSmallTile : kLargeTile;
   a.tiles = (int)div_up(a.tokens, a.tile);
   a.spans = (int)div_up(a.hidden, 256);
+  if (a.accumulate && a.tokens == 0) return cudaSuccess;
+  const int64_t words = a.first[a.nranks];
+  // Where most words do not occur, rows to clear beside the sort, and half of them beside the
+  // merge: as many as these take; the sums' kernel reads meanwhile, and is better at it
+  // (16385 tokens, 32008 words of 4096 elements: none 142 us, a fifth 139, a third 133, all 154;
+  // 50000 tokens, 2000 words of 1024: none 100 us, a third 104).
+  a.clear_end = a.accumulate || a.tokens > kManyPairs || words <= a.tokens ? 0 : a.tiles > 1 ? words / 3 : words;
+  a.clear_first = a.tiles > 1 ? a.clear_end / 2 : a.clear_end;
+  auto clearing = [&](int64_t rows, int64_t most) {  // blocks, of 16 KiB or more
+    const int64_t n = div_up(rows * a.hidden, 4096);
+    return n < most ? n : most;
+  };
+  void* params[] = {&a};
+  if (few_tokens(a.tokens, a.spans)) {
+    a.clear_end = a.accumulate ? 0 : words;
+    a.sum_blocks = a.tokens * a.spans;
+    return launch_op(a.dtype == 0 ? (const void*)embed_few_kernel<float> : (const void*)embed_few_kernel<uint16_t>,
+                     dim3((unsigned)(a.sum_blocks + clearing(a.clear_end, 8 * kClearBlocks))), 32 * kChunks, 0, stream, params);
+  }
   int blocks = 0;
   cudaError_t e = resident_blocks((const void*)embed_sort_kernel, kSortThreads, 2 * kLargeTile * 8, &blocks);
   if (e != cudaSuccess) return e;
-  if (a.accumulate && a.tokens == 0) return cudaSuccess;
-  void* params[] = {&a};
-  if (a.tokens > 0) {
-    e = launch_op((const void*)embed_sort_kernel, dim3((unsigned)a.tiles), kSortThreads, 2 * a.tile * 8, stream, params);
-    if (e != cudaSuccess) return e;
-  }
+  e = launch_op((const void*)embed_sort_kernel, dim3((unsigned)(a.tiles + clearing(a.clear_first, 2 * kClearBlocks))), kSortThreads,
+                2 * a.tile * 8, stream, params);
+  if (e != cudaSuccess) return e;
   if (a.tiles > 1) {
     e = resident_blocks((const void*)embed_merge_kernel, kMergeThreads, kMergePairs * 8, &blocks);
     if (e != cudaSuccess) return e;
-    e = launch_op((const void*)embed_merge_kernel, dim3((unsigned)div_up(a.tokens, kMergeThreads)), kMergeThreads, kMergePairs * 8,
-                  stream, params);
+    const int64_t merging = div_up(a.tokens, kMergeThreads), others = merging < kClearBlocks / 2 ? merging : kClearBlocks / 2;
+    e = launch_op((const void*)embed_merge_kernel,
+                  dim3((unsigned)(merging + clearing(a.clear_end - a.clear_first, kClearBlocks - others))), kMergeThreads,
+                  kMergePairs * 8, stream, params);
     if (e != cudaSuccess) return e;
   }
   const bool few = short_chunks(a.tokens, a.hidden);

@@ -306,6 +306,7 @@ struct EmbedBwdArgs {
   uint64_t* sorted;
   float* parts;
   int64_t sum_blocks;  // blocks that sum; the warps of those behind them clear rows, so many each
+  int64_t clear_first, clear_end;  // words up to which rows are cleared beside the sort, and beside the merge
   int tile, tiles, spans, clear_rows;
 };
 constexpr int kMaxTop = 32;

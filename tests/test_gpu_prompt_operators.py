@@ -659,6 +659,23 @@ def test_embed_backward_distributions(count, tokens):
     check_table_gradient(token, dout, grads, 1.0)
 
 
+@pytest.mark.parametrize("count,hidden", [(304, 2048), (305, 2048), (512, 64), (513, 64), (1024, 1032), (1025, 1032),
+                                          (65536, 64), (65537, 64), (140001, 8)])
+@pytest.mark.parametrize("words", [9, 70000])
+def test_embed_backward_counts(count, hidden, words):
+    """On both sides of the numbers of tokens at which another form begins; few words, and more than there are tokens."""
+    vocab = [words // 3, words - words // 3]
+    token = torch.randint(-1, words + 1, (count,), generator=gen(count), device="cuda").int()
+    dout = normal(gen(3), count, hidden, dtype=torch.bfloat16)
+    ws = B.OpWorkspace(B.embed_tokens_workspace_bytes(count, hidden))
+    for accumulate in (False, True):
+        grads = [normal(gen(r), v, hidden) for r, v in enumerate(vocab)]
+        base = torch.cat(grads).clone()
+        B.embed_tokens_backward(token, dout, grads, ws, accumulate=accumulate)
+        check_table_gradient(token, dout, grads, 1.0, base if accumulate else None)
+    assert B.get_status(ws) == B.Status.OK
+
+
 def test_embed_layouts():
     """Rows with gaps: tables in one buffer side by side, outputs and gradients strided; infinities and NaN of words that
     no token asks for do not matter, and those of tokens that ask for nothing neither."""
