@@ -714,6 +714,104 @@ def test_embed_nothing():
     assert B.get_status(ws) == B.Status.OK and bool((grads[0] == 0).all())
 
 
+MANY = [
+    ([i * 37 % 190 for i in range(45)], 8, 2, 128, "bf16"), ([i * 37 % 190 for i in range(33)], 3, 1, 64, "bf16"),
+    ([0, 0, 1] * 700, 4, 4, 64, "bf16"), ([i * 37 % 90 for i in range(45)], 4, 2, 64, "f32"), ([0] * 40 + [300] + [0] * 2000, 8, 1, 64, "bf16"),
+]
+
+
+@pytest.mark.parametrize("lens,q_heads,kv_heads,dim,dtype", MANY, ids=lambda x: None if isinstance(x, list) else str(x))
+def test_many_sequences(lens, q_heads, kv_heads, dim, dtype):
+    """More than a warp has lanes, which are taken in another order."""
+    q, k, v, starts = prompt_inputs(2, lens, q_heads, kv_heads, dim, dtype, seed=4, ahead=3)
+    out, lse = forward(q, k, v, starts)
+    check_forward(q, k, v, starts, out, lse)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    check_backward(q, k, v, starts, out, lse, dout, *backward(q, k, v, starts, out, lse, dout))
+
+
+@pytest.mark.parametrize("page,dtype", [(64, "bf16"), (4, "bf16"), (64, "f32")])
+def test_cached_far(page, dtype):
+    """Pages whose elements' numbers pass 32 bits."""
+    d, kv, heads, new, lens = 128, 2, 4, [9, 200], [500, 340]
+    pages = (2 ** 32 + 2 ** 20) // (kv * page * d)
+    g = gen(7)
+    k, v = (torch.empty(1, pages, kv, page, d, dtype=DT[dtype], device="cuda") for _ in range(2))
+    have = [-(-n // page) for n in lens]
+    near, far = list(range(have[0])), [pages - 1 - i for i in range(have[1])]
+    far[1] = pages // 2 - 1
+    keys, values, rows = [], [], []
+    for n, mine in zip(lens, (near, far)):
+        key, value = (normal(g, 1, n, kv, d, dtype=DT[dtype]) for _ in range(2))
+        for c, at in enumerate(mine):
+            m = min(page, n - c * page)
+            k[:, at, :, :m] = key[:, c * page:c * page + m].transpose(1, 2)
+            v[:, at, :, :m] = value[:, c * page:c * page + m].transpose(1, 2)
+        keys.append(key)
+        values.append(value)
+        rows.append(mine + [0] * (max(have) - len(mine)))
+    q = normal(g, 1, sum(new), heads, d, dtype=DT[dtype])
+    starts = starts_of(new)
+    out, lse = cached_forward(q, k, v, i32(*sum(rows, [])).view(2, -1), starts, i32(*lens))
+    check_forward(q, keys, values, starts, out, lse, before=[a - b for a, b in zip(lens, new)])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_far_apart(dtype):
+    """Rows whose elements' numbers pass 32 bits, of all tensors in one buffer."""
+    t, heads, kv, d = 150, 4, 2, 64
+    stride = 2 ** 32 // 140
+    stride -= stride % 8
+    buffer = torch.empty(t * stride, dtype=DT[dtype], device="cuda")
+    q, k, v, starts = prompt_inputs(1, [20, 130], heads, kv, d, dtype)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    out, lse = forward(q, k, v, starts)
+    want = [out, *backward(q, k, v, starts, out, lse, dout)]
+    at = 0
+
+    def place(x):
+        nonlocal at
+        view = buffer.as_strided(x.shape, (t * stride, stride, d, 1), at)
+        at += x.shape[2] * d
+        return view.copy_(x)
+
+    q, k, v, dout = (place(x) for x in (q, k, v, dout))
+    out, dq, dk, dv = (place(torch.full_like(x, MARK)) for x in want)
+    ws = workspace(q, kv)
+    B.prompt_attention(q, k, v, starts, out, lse, ws)
+    B.prompt_attention_backward(q, k, v, starts, out, lse, dout, dq, dk, dv, ws)
+    assert B.get_status(ws) == B.Status.OK
+    for got, w in zip((out, dq, dk, dv), want):
+        assert torch.equal(got, w)
+
+
+def test_embed_far():
+    """A table, outputs and a gradient whose elements' numbers pass 32 bits."""
+    words, hidden = 2 ** 32 // 4096 + 100, 4096
+    table = torch.empty(words, hidden, dtype=torch.bfloat16, device="cuda")
+    tokens = torch.randint(0, words, (3000,), generator=gen(1), device="cuda").int()
+    tokens[:3] = i32(words - 1, words, 0)
+    tokens[7] = words - 1
+    used = tokens[tokens < words].long()
+    table[used] = normal(gen(2), len(used), hidden, dtype=torch.bfloat16)
+    ws = B.OpWorkspace(B.embed_tokens_workspace_bytes(len(tokens), hidden))
+    out = torch.full((len(tokens), hidden), MARK, dtype=torch.bfloat16, device="cuda")
+    B.embed_tokens(tokens, [table], out, ws)
+    want = table[tokens.long().clamp(max=words - 1)]
+    want[1] = 0
+    assert torch.equal(out, want)
+    del table
+    grad = torch.full((words, hidden), MARK, device="cuda")
+    B.embed_tokens_backward(tokens, out, [grad], ws)
+    assert B.get_status(ws) == B.Status.OK
+    row, place = torch.unique(used, return_inverse=True)
+    part = torch.zeros(len(row), hidden, dtype=torch.float64, device="cuda").index_add_(0, place, out[tokens < words].double())
+    size = torch.zeros_like(part).index_add_(0, place, out[tokens < words].double().abs())
+    close(grad[row], part, 5 * U * size, "dtable")
+    grad[row] = 0
+    assert not bool(grad.any())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_workspace_that_is_not_initialised(dtype):
     """The kernels write nothing but the status."""
