@@ -91,10 +91,10 @@ struct Work {
 
 // Item number n in order; 0 if there is none, -1 if there are no more (a whole warp).
 __device__ __forceinline__ int find_item(const PromptBwdArgs& a, const Work& work, ItemOrder& order, bool ordered, bool by_keys,
-                                         int64_t n, Item* item) {
-  const int64_t lanes = (int64_t)a.kv_heads * a.nranks, whole = n / work.split.parts, slot = whole / lanes;
-  const int lane_of = (int)(whole % lanes);
-  item->part = (int)(n % work.split.parts);
+                                         uint32_t n, Item* item) {
+  const uint32_t lanes = (uint32_t)(a.kv_heads * a.nranks), parts = (uint32_t)work.split.parts, whole = n / parts, slot = whole / lanes;
+  const int lane_of = (int)(whole - slot * lanes);
+  item->part = (int)(n - whole * parts);
   item->head = lane_of % a.kv_heads;
   item->rank = lane_of / a.kv_heads;
   PromptSequence seq;
@@ -120,13 +120,13 @@ __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& 
                                             Item* items, uint64_t* full, uint64_t* empty, volatile int* dead) {
   const int lane = threadIdx.x & 31;
   uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
-  const int64_t all = work.slots * work.split.parts * a.kv_heads * a.nranks;
+  const uint32_t all = (uint32_t)(work.slots * work.split.parts * a.kv_heads * a.nranks);
   ItemOrder order;
   const bool ordered = order.begin(a.starts, a.sequences, a.tokens, work.unit);
   // without a workspace there are no items: the others wait for the first one, not for the header
   const bool ready = magic == kOpMagic;
   if (!ready && lane == 0) op_report(a.ws, kErrWorkspace);
-  int64_t n = ready ? blockIdx.x : all;
+  uint32_t n = ready ? blockIdx.x : all;
   for (int i = 0;;) {
     Item item;
     const int found = n < all ? find_item(a, work, order, ordered, by_keys, n, &item) : -1;
@@ -142,7 +142,7 @@ __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& 
     if (found < 0) break;
     uint32_t next = 0;
     if (lane == 0) next = atomicAdd(&counters[kNextItem], 1);
-    n = (int64_t)gridDim.x + __shfl_sync(~0u, next, 0);
+    n = gridDim.x + __shfl_sync(~0u, next, 0);
   }
   // the last block to have no more sets the counters back
   if (ready && lane == 0 && atom_add_acq_rel_u32(&counters[kDoneBlocks], 1) == gridDim.x - 1) {

@@ -110,30 +110,31 @@ struct Item {
 };
 
 // Item number n in order; 0 if there is none, -1 if there are no more (a whole warp).
+// Numbers are below 2^31, and in 32 bits for short prompts: divisions in 64 are half of the time that the first item takes.
 template <int FORM>
-__device__ __forceinline__ int find_item(const PromptArgs& a, const Split& split, ItemOrder& order, bool ordered, int64_t n,
+__device__ __forceinline__ int find_item(const PromptArgs& a, const Split& split, ItemOrder& order, bool ordered, uint32_t n,
                                          Item* item) {
   const int per_tile = kRows / (a.q_heads / a.kv_heads);
-  item->part = (int)(n % split.parts);
-  const int64_t whole = n / split.parts, lanes = (int64_t)a.kv_heads * a.nranks;
-  const int lane_of = (int)(whole % lanes);
+  const uint32_t whole = n / (uint32_t)split.parts, lanes = (uint32_t)(a.kv_heads * a.nranks), slot = whole / lanes;
+  item->part = (int)(n - whole * (uint32_t)split.parts);
+  const int lane_of = (int)(whole - slot * lanes);
   item->head = lane_of % a.kv_heads;
   item->rank = lane_of / a.kv_heads;
   PromptSequence seq;
   int pair;
   if (ordered) {
-    if (!order.advance(whole / lanes, 2 * per_tile, false, &seq.index, &pair)) return -1;
+    if (!order.advance(slot, 2 * per_tile, false, &seq.index, &pair)) return -1;
     seq.first = __shfl_sync(~0u, order.first, seq.index);
     seq.length = __shfl_sync(~0u, order.length, seq.index);
     seq.before = __shfl_sync(~0u, order.before, seq.index);
     seq.keys = __shfl_sync(~0u, order.keys, seq.index);
   } else {
     // the last tokens of a sequence see the most keys: they come first
-    if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, split.slots - 1 - whole / lanes, &seq, &pair)) return 0;
+    if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, split.slots - 1 - slot, &seq, &pair)) return 0;
     if (FORM != kDense) cached_sequence(a, &seq);
   }
   const int token0 = pair * 2 * per_tile;  // of the sequence
-  item->index = ((int64_t)seq.first / (2 * per_tile) + seq.index + pair) * lanes + lane_of;  // by number, as the join finds it
+  item->index = (int64_t)(seq.first / (2 * per_tile) + seq.index + pair) * lanes + lane_of;  // by number, as the join finds it
   item->sequence = seq.index;
   item->keys = seq.keys;
   item->first = seq.first + token0;
@@ -147,8 +148,9 @@ __device__ __forceinline__ int find_item(const PromptArgs& a, const Split& split
     item->tokens[t] = tokens;
   }
   const int most = max(tiles[0], tiles[1]);
-  item->begin = (int)((int64_t)most * item->part / split.parts);
-  item->end = (int)((int64_t)most * (item->part + 1) / split.parts);
+  // (most is below 2^24, parts 152 or fewer)
+  item->begin = (int)((uint32_t)most * (uint32_t)item->part / (uint32_t)split.parts);
+  item->end = (int)((uint32_t)most * (uint32_t)(item->part + 1) / (uint32_t)split.parts);
 #pragma unroll
   for (int t = 0; t < 2; t++) item->last[t] = max(item->begin, min(tiles[t], item->end));
   item->there = 1;
@@ -207,35 +209,41 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     }
   }
   const uint32_t magic = op_start(a.ws);
-  if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
-  __syncthreads();
-  constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
-  constexpr uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 256 + DP};
-  constexpr uint32_t p_at[2] = {L::kApart ? tmem + 384 : s_at[0], L::kApart ? tmem + 448 : s_at[1]};
-  uint8_t* const ring = smem + NQ * L::kTile;
   const int group = a.q_heads / a.kv_heads, D = a.head_dim;
   const int per_tile = kRows / group;  // tokens of a tile
-  // a tile of keys is slab by slab, or where a box holds whole rows of pages, eight rows of both slabs after one another
-  const bool grouped = FORM == kPages && DP == 128 && D == DP;
-  const uint32_t kv_slab = grouped ? kGroup : L::kSlab, kv_group = grouped ? kGroup * (DP / 64) : kGroup;
-  const int steps = (D + 15) / 16;
-
-  if (warp >= kCopyWarp) give_registers<Threads<FORM>::kFew>();
+  if (warp == kCopyWarp) tmem_alloc(&tmem_at, 512);
+  ItemOrder order;
+  bool ordered = false;
   if (warp == kItemWarp) {
-    uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
-    const int64_t all = split.items * split.parts;
-    ItemOrder order;
-    const bool ordered = order.begin(a.starts, a.sequences, a.tokens, 2 * per_tile);
+    ordered = order.begin(a.starts, a.sequences, a.tokens, 2 * per_tile);
     if (FORM != kDense && ordered && lane < a.sequences) {
       PromptSequence seq = {lane, order.first, order.length, 0, order.length};
       cached_sequence(a, &seq);
       order.before = seq.before;
       order.keys = seq.keys;
     }
+  }
+  __syncthreads();
+  constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
+  constexpr uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 256 + DP};
+  constexpr uint32_t p_at[2] = {L::kApart ? tmem + 384 : s_at[0], L::kApart ? tmem + 448 : s_at[1]};
+  uint8_t* const ring = smem + NQ * L::kTile;
+  const uint32_t all = (uint32_t)(split.items * split.parts);
+  // a tile of keys is slab by slab, or where a box holds whole rows of pages, eight rows of both slabs after one another
+  const bool grouped = FORM == kPages && DP == 128 && D == DP;
+  const uint32_t kv_slab = grouped ? kGroup : L::kSlab, kv_group = grouped ? kGroup * (DP / 64) : kGroup;
+  const int steps = (D + 15) / 16;
+  // With one item a block, its softmax warps store the results: a TMA store takes 1 us longer to be done, and there is
+  // nothing to do meanwhile.
+  const bool alone = all <= gridDim.x;
+
+  if (warp >= kCopyWarp) give_registers<Threads<FORM>::kFew>();
+  if (warp == kItemWarp) {
+    uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
     // without a workspace there are no items: the others wait for the first one, not for the header
     const bool ready = magic == kOpMagic;
     if (!ready && lane == 0) op_report(a.ws, kErrWorkspace);
-    int64_t n = ready ? blockIdx.x : all;
+    uint32_t n = ready ? blockIdx.x : all;
     for (int i = 0;;) {
       Item item;
       int found = n < all ? find_item<FORM>(a, split, order, ordered, n, &item) : -1;
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       if (found < 0) break;
       uint32_t next = 0;
       if (lane == 0) next = atomicAdd(&counters[kNextItem], 1);
-      n = (int64_t)gridDim.x + __shfl_sync(~0u, next, 0);
+      n = gridDim.x + __shfl_sync(~0u, next, 0);
     }
     // the last block to have no more sets the counters back
     if (ready && lane == 0 && atom_add_acq_rel_u32(&counters[kDoneBlocks], 1) == gridDim.x - 1) {
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         const int at = queries++ % NQ;
         if (!(fine = wait_warp(&out_ready[t], results[t]++ & 1, dead))) break;
         if (lane == 0) {
-          if (tokens[t] == per_tile && split.parts == 1) {
+          if (tokens[t] == per_tile && split.parts == 1 && !alone) {
             for (int h = 0; h < DP / 64 && h * 64 < D; h++)
               store_3d(&maps.out[rank], h * 64, head * group, first + t * per_tile, smem + at * L::kTile + h * L::kSlab);
             stores_read();
@@ -734,7 +742,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
           }
         } else {
           // to the queries' place in shared memory, from where the store warp's TMA takes a
-          // whole tile; a warp stores its rows of one that the sequence does not fill itself
+          // whole tile; a warp stores its rows of one that the sequence does not fill itself, or of a block's only item
           if (l == 0.f) {  // no weight at all: 0, whatever the values are
 #pragma unroll
             for (int c = 0; c < DP; c++) o[c] = 0;
@@ -753,7 +761,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
             *reinterpret_cast<uint4*>(place + (c >> 6) * L::kSlab + (((c >> 3 & 7) ^ (row & 7)) << 4)) = x;
           }
           stores_to_products();
-          if (tokens != per_tile) {
+          if (tokens != per_tile || alone) {
             __syncwarp();
             constexpr int kPieces = DP / 8, kAtOnce = 32 / kPieces;  // lanes of a row, rows of an instruction
             const int piece = lane % kPieces;
