@@ -384,6 +384,80 @@ __global__ void __launch_bounds__(128) prompt_join_rows_kernel(const __grid_cons
   if (threadIdx.x == 0 && a.lse[rank] != nullptr) a.lse[rank][token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
 
+// The sequence of a token: the last one that begins at or before it. A whole warp looks.
+__device__ __forceinline__ int sequence_of(const int32_t* starts, int sequences, int token) {
+  int lo = 0, hi = sequences;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, probe = lo + (int)(threadIdx.x & 31) * step;
+    const int count = __popc(__ballot_sync(~0u, probe < hi && starts[probe < hi ? probe : lo] <= token));
+    lo += (count > 1 ? count - 1 : 0) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// Few parts of a row's keys, a warp a row of all heads and tokens: lanes have a part's
+// weight each, and pairs of elements.
+template <typename T>
+__global__ void __launch_bounds__(128) prompt_join_few_kernel(const __grid_constant__ PromptArgs a,
+                                                              const __grid_constant__ FewParts f) {
+  const uint32_t magic = op_start(a.ws);
+  if (!op_ready(a.ws, magic)) return;
+  const int group = a.q_heads / a.kv_heads, D = a.head_dim, lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), each = (int64_t)a.tokens * a.q_heads;
+  const int rank = (int)(r / each);
+  if (rank >= a.nranks) return;
+  const int token = (int)(r % each / a.q_heads), query = (int)(r % a.q_heads), head = query / group, in_group = query % group;
+  const int s = sequence_of(a.starts, a.sequences, token), first = a.starts[s], end = a.starts[s + 1];
+  if (first < 0 || end > a.tokens || token < first || token >= end) return;
+  // the item, its tile of rows, and the row in it
+  const int at = token - first;
+  int64_t item;
+  int tile = 0, row;
+  if (f.pairs) {
+    const int per_tile = f.tile_rows / group, unit = 2 * per_tile;
+    item = (int64_t)(first / unit + s + at / unit) * (a.kv_heads * a.nranks) + rank * a.kv_heads + head;
+    tile = at % unit / per_tile;
+    row = at % per_tile * group + in_group;
+  } else {
+    const int64_t slot = (int64_t)first * group / f.tile_rows + s + (at * group + in_group) / f.tile_rows;
+    item = ((int64_t)rank * a.kv_heads + head) * f.slots + slot;
+    row = (at * group + in_group) % f.tile_rows;
+  }
+  const float* const sums = f.sums + item * f.parts * f.part_floats + (int64_t)tile * f.tile_rows * (f.row_floats + 2);
+  const float* const numbers = sums + lane * f.part_floats + f.tile_rows * f.row_floats + row;
+  const float m = lane < f.parts ? numbers[0] : -INFINITY, l = lane < f.parts ? numbers[f.tile_rows] : 0.f;
+  float top = m;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  // below 0: a part with no weight at all has left nothing. (One of NaN scores alone has a sum of NaN, and no maximum.)
+  const float w = l == 0.f ? -1.f : exp2_fast(m - top);
+  float sum = w < 0.f ? 0.f : l * w;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  const float by = sum == 0.f ? 0.f : 1.f / sum;
+  T* const out = (T*)a.out[rank] + (int64_t)token * a.out_stride + (int64_t)query * D;
+  for (int d0 = 0; d0 < D; d0 += 64) {
+    const int d = d0 + lane * 2;
+    float2 x[kFewParts];
+#pragma unroll
+    for (int k = 0; k < kFewParts; k++) {
+      x[k] = make_float2(0.f, 0.f);
+      if (__shfl_sync(~0u, w, k) >= 0.f && d < D) x[k] = *reinterpret_cast<const float2*>(sums + k * f.part_floats + row * f.row_floats + d);
+    }
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kFewParts; k++) {
+      const float y = __shfl_sync(~0u, w, k);
+      if (y < 0.f) continue;
+      v.x = fmaf(x[k].x, y, v.x);
+      v.y = fmaf(x[k].y, y, v.y);
+    }
+    if (d < D) store2(out + d, sum == 0.f ? 0.f : v.x * by, sum == 0.f ? 0.f : v.y * by);
+  }
+  if (lane == 0 && a.lse[rank] != nullptr) a.lse[rank][(int64_t)token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
+}
+
 // Weight and score gradient of a score s that the row sees.
 __device__ __forceinline__ void weigh(float s, float dp, bool seen, float scale2, float lse2, float delta, float* p, float* ds) {
   *p = seen ? exp2_fast(fmaf(s, scale2, -lse2)) : 0.f;
@@ -612,7 +686,7 @@ cudaError_t forward(const PromptArgs& a, cudaStream_t stream) {
   const int64_t items = slots * a.kv_heads * a.nranks;
   Split split = {1, (float*)(a.ws + kOpScratchOffset)};
   if (items * 2 <= kPromptParts) {
-    const int64_t most = a.table != nullptr ? (int64_t)a.max_blocks << a.page_shift : a.tokens;
+    const int64_t most = a.table != nullptr ? (int64_t)a.max_blocks << a.page_shift : likely_keys(a.tokens, a.sequences);
     const int64_t room = kPromptParts / items, wanted = div_up(most, 2 * BT);
     split.parts = (int)(room < wanted ? room : wanted);
   }
@@ -622,6 +696,8 @@ cudaError_t forward(const PromptArgs& a, cudaStream_t stream) {
                                dim3((unsigned)(items * split.parts)),
                                shared_bytes<DP, BT>(2, 1), stream, params);
   if (e != cudaSuccess || split.parts == 1) return e;
+  if (split.parts <= kFewParts)
+    return launch_prompt_join_few(a, {split.sums, split.parts, BT, DP, 0, kPartFloats<DP, BT>, slots}, stream);
   return launch_op((const void*)prompt_join_rows_kernel<T, DP, BT>, dim3((unsigned)(items * BT)), 128, 0, stream, params);
 }
 
@@ -636,8 +712,8 @@ cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t slots = prompt_slots(a.tokens, a.sequences, 1, BT);
   KeyParts split;
-  split.parts = key_parts(slots * lanes, kPromptParts, (int64_t)a.tokens * (a.q_heads / a.kv_heads) / (2 * BT),
-                          kLeastPlainRowTiles);
+  split.parts = key_parts(slots * lanes, kPromptParts, (int64_t)a.tokens / a.sequences * (a.q_heads / a.kv_heads) / (2 * BT),
+                          kLeastPlainRowTilesFew, kLeastPlainRowTiles);
   split.sums = (float*)(a.ws + kOpScratchOffset + delta_bytes(a.nranks, a.tokens, a.q_heads));
   void* key_params[] = {&copy, &split};
   e = launch((const void*)prompt_bwd_keys_kernel<T, DP, BT>, dim3((unsigned)(slots * lanes * split.parts)),
@@ -673,6 +749,14 @@ cudaError_t by_size(const PromptBwdArgs& a, cudaStream_t stream) {
   return backward<T, 256, 32>(a, stream);
 }
 
+cudaError_t launch_prompt_join_few(const PromptArgs& a, const FewParts& parts, cudaStream_t stream) {
+  PromptArgs copy = a;
+  FewParts few = parts;
+  void* params[] = {&copy, &few};
+  const void* fn = a.dtype == 0 ? (const void*)prompt_join_few_kernel<float> : (const void*)prompt_join_few_kernel<uint16_t>;
+  return launch_op(fn, dim3((unsigned)div_up((int64_t)a.nranks * a.tokens * a.q_heads, 4)), 128, 0, stream, params);
+}
+
 cudaError_t launch_prompt_key_parts(const PromptBwdArgs& a, const KeyParts& parts, cudaStream_t stream) {
   PromptBwdArgs copy = a;
   KeyParts split = parts;
@@ -706,9 +790,11 @@ int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, 
     parts = (int64_t)kPromptSplitBlocks * (256 * ((head_dim <= 64 ? 64 : 128) + 2) + kPromptPartInfo) * 4;
   // what parts of the rows leave of dk and dv: a call of more sequences than one has no more of them
   const int unit = group <= 128 && head_dim <= 128 ? 128 : rows;
-  const int most = group <= 128 && head_dim <= 128 ? key_parts((tokens / unit + 1) * lanes, kPromptSplitBlocks, tokens / (2 * (128 / group)), kLeastRowTiles)
+  const int most = group <= 128 && head_dim <= 128 ? key_parts((tokens / unit + 1) * lanes, kPromptSplitBlocks, tokens / (2 * (128 / group)), kLeastRowTilesFew,
+                                                               kLeastRowTiles)
                                                    : 1;
-  const int plain = key_parts((tokens / rows + 1) * lanes, kPromptParts, tokens * group / (2 * rows), kLeastPlainRowTiles);
+  const int plain = key_parts((tokens / rows + 1) * lanes, kPromptParts, tokens * group / (2 * rows), kLeastPlainRowTilesFew,
+                              kLeastPlainRowTiles);
   const int key_split = most > plain ? most : plain;
   const int64_t gradient = delta + (key_split > 1 ? key_split * 2 * key_part_floats(nranks, tokens, kv_heads, head_dim) * 4 : 0);
   return gradient > parts ? gradient : parts;

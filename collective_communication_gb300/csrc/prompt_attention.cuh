@@ -58,18 +58,19 @@ __host__ __device__ inline int64_t key_part_floats(int nranks, int64_t tokens, i
 }
 constexpr int kMostKeyParts = 8;
 // Parts for `items` tiles of keys on `blocks` resident blocks, where a key is seen by the rows of `row_tiles` tiles on
-// average. Few items are split until there are two a block, into parts of eight tiles of rows or more. The items of a long
+// average. Few items are split until there are two a block, into parts of `least_few` tiles of rows or more. The items of a long
 // sequence differ by the rows that see them, so they are split further, into parts of `least` tiles, for eight a
 // block: one of 8192 tokens, 4 key heads of 64, 658 us whole and 554 in four parts; of 4096 tokens, 8 key heads of 128, 64
 // tiles of rows or fewer each, 244 whole and 256 in two, for the cost of the parts' sums.
-inline int key_parts(int64_t items, int64_t blocks, int64_t row_tiles, int64_t least) {
+inline int key_parts(int64_t items, int64_t blocks, int64_t row_tiles, int64_t least_few, int64_t least) {
   if (items < 1) items = 1;
-  const int64_t fill = 2 * blocks / items < row_tiles / 8 ? 2 * blocks / items : row_tiles / 8;
+  const int64_t fill = 2 * blocks / items < row_tiles / least_few ? 2 * blocks / items : row_tiles / least_few;
   const int64_t even = 8 * blocks / items < row_tiles / least ? 8 * blocks / items : row_tiles / least;
   const int64_t parts = fill > even ? fill : even;
   return parts < 1 ? 1 : parts > kMostKeyParts ? kMostKeyParts : (int)parts;
 }
-constexpr int kLeastRowTiles = 32, kLeastPlainRowTiles = 8;  // on the tensor cores, and on the ordinary arithmetic units
+// on the tensor cores, and on the ordinary arithmetic units, where a tile takes 5 to 8 us
+constexpr int kLeastRowTilesFew = 8, kLeastRowTiles = 32, kLeastPlainRowTilesFew = 1, kLeastPlainRowTiles = 8;
 // Adds them up, in their order.
 cudaError_t launch_prompt_key_parts(const PromptBwdArgs& a, const KeyParts& parts, cudaStream_t stream);
 
@@ -82,6 +83,21 @@ constexpr int kPromptParts = 304;        // the same in the form on the ordinary
 constexpr int kPromptPartInfo = 32;      // numbers behind a part's sums
 cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t stream);
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim);
+
+// Where few parts of each row's keys have been left: of item i's part k from sums + (i * parts + k) * part_floats on,
+// with tiles of tile_rows rows of row_floats numbers, then their m and l.
+struct FewParts {
+  const float* sums;
+  int parts, tile_rows, row_floats, pairs;  // pairs: items are two tiles, and the ranks' heads of an item lie together
+  int64_t part_floats, slots;
+};
+constexpr int kFewParts = 16;
+// Joins them, a warp a row: a block a row, most of its threads idle, took 45 us for 500 tokens of 16 heads.
+cudaError_t launch_prompt_join_few(const PromptArgs& a, const FewParts& parts, cudaStream_t stream);
+// Keys that one of the dense sequences may have, as far as the host knows: twice the average.
+inline int64_t likely_keys(int64_t tokens, int sequences) {
+  return sequences < 2 ? tokens : (2 * tokens + sequences - 1) / sequences;
+}
 
 // Numbers that cover any starts of `tokens` tokens in `sequences` sequences.
 inline int64_t prompt_slots(int64_t tokens, int sequences, int per, int unit) {

@@ -923,7 +923,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   split.sums = (float*)(a.ws + kOpScratchOffset);
   split.parts = 1;
   // tiles of keys that an item may have
-  const int64_t most = div_up(FORM != kDense ? (int64_t)a.max_blocks << a.page_shift : a.tokens, kKeys);
+  const int64_t most = div_up(FORM != kDense ? (int64_t)a.max_blocks << a.page_shift : likely_keys(a.tokens, a.sequences), kKeys);
   if (split.items * 2 <= kPromptSplitBlocks) {
     const int64_t room = kPromptSplitBlocks / split.items, wanted = div_up(most, 2);
     split.parts = (int)(room < wanted ? room : wanted);
@@ -933,6 +933,8 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   void* params[] = {&copy, &maps, &split};
   e = launch_op(fn, dim3((unsigned)(all < blocks ? all : blocks)), Threads<FORM>::kCount, Layout<DP>::kShared, stream, params);
   if (e != cudaSuccess || split.parts == 1) return e;
+  if (split.parts <= kFewParts)
+    return launch_prompt_join_few(a, {split.sums, split.parts, kRows, DP, 1, kPartFloats<DP>, split.slots}, stream);
   void* join_params[] = {&copy, &split};
   return launch_op((const void*)prompt_join_kernel<DP>, dim3((unsigned)(split.items * 2 * kRows)), 128, 0, stream, join_params);
 }
