@@ -712,7 +712,7 @@ cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t slots = prompt_slots(a.tokens, a.sequences, 1, BT);
   KeyParts split;
-  split.parts = key_parts(slots * lanes, kPromptParts, (int64_t)a.tokens / a.sequences * (a.q_heads / a.kv_heads) / (2 * BT),
+  split.parts = key_parts(slots * lanes, kPromptParts, likely_keys(a.tokens, a.sequences) * (a.q_heads / a.kv_heads) / (2 * BT),
                           kLeastPlainRowTilesFew, kLeastPlainRowTiles);
   split.sums = (float*)(a.ws + kOpScratchOffset + delta_bytes(a.nranks, a.tokens, a.q_heads));
   void* key_params[] = {&copy, &split};

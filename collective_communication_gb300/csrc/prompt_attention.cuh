@@ -58,19 +58,23 @@ __host__ __device__ inline int64_t key_part_floats(int nranks, int64_t tokens, i
 }
 constexpr int kMostKeyParts = 8;
 // Parts for `items` tiles of keys on `blocks` resident blocks, where a key is seen by the rows of `row_tiles` tiles on
-// average. Few items are split until there are two a block, into parts of `least_few` tiles of rows or more. The items of a long
+// average. Few items are split until there is one a block, into parts of `least_few` tiles of rows or more, or two, of twice
+// as many (1000 tokens, 4 key heads of 64: 71 us whole, 51 in three parts, 55 in seven). The items of a long
 // sequence differ by the rows that see them, so they are split further, into parts of `least` tiles, for eight a
 // block: one of 8192 tokens, 4 key heads of 64, 658 us whole and 554 in four parts; of 4096 tokens, 8 key heads of 128, 64
 // tiles of rows or fewer each, 244 whole and 256 in two, for the cost of the parts' sums.
 inline int key_parts(int64_t items, int64_t blocks, int64_t row_tiles, int64_t least_few, int64_t least) {
   if (items < 1) items = 1;
-  const int64_t fill = 2 * blocks / items < row_tiles / least_few ? 2 * blocks / items : row_tiles / least_few;
-  const int64_t even = 8 * blocks / items < row_tiles / least ? 8 * blocks / items : row_tiles / least;
-  const int64_t parts = fill > even ? fill : even;
-  return parts < 1 ? 1 : parts > kMostKeyParts ? kMostKeyParts : (int)parts;
+  int64_t parts = 1;
+  const int64_t waves[] = {1, 2, 8}, tiles[] = {least_few, 2 * least_few, least};
+  for (int i = 0; i < 3; i++) {
+    const int64_t room = waves[i] * blocks / items, there = row_tiles / tiles[i], n = room < there ? room : there;
+    parts = n > parts ? n : parts;
+  }
+  return parts > kMostKeyParts ? kMostKeyParts : (int)parts;
 }
 // on the tensor cores, and on the ordinary arithmetic units, where a tile takes 5 to 8 us
-constexpr int kLeastRowTilesFew = 8, kLeastRowTiles = 32, kLeastPlainRowTilesFew = 1, kLeastPlainRowTiles = 8;
+constexpr int kLeastRowTilesFew = 2, kLeastRowTiles = 32, kLeastPlainRowTilesFew = 1, kLeastPlainRowTiles = 8;
 // Adds them up, in their order.
 cudaError_t launch_prompt_key_parts(const PromptBwdArgs& a, const KeyParts& parts, cudaStream_t stream);
 

@@ -795,7 +795,7 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
     work.split.parts = 1;
     if (which == 1)
       work.split.parts = key_parts(work.slots * a.kv_heads * a.nranks, blocks < kPromptSplitBlocks ? blocks : kPromptSplitBlocks,
-                                   (int64_t)a.tokens / a.sequences / (2 * per_tile), kLeastRowTilesFew, kLeastRowTiles);
+                                   likely_keys(a.tokens, a.sequences) / (2 * per_tile), kLeastRowTilesFew, kLeastRowTiles);
     work.split.sums = (float*)(a.ws + kOpScratchOffset + align_up((int64_t)a.nranks * a.tokens * a.q_heads * 4, 256));
     const int64_t all = work.slots * work.split.parts * a.kv_heads * a.nranks;
     void* params[] = {&copy, &maps, &work};
