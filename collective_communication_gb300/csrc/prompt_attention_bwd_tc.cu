@@ -786,8 +786,10 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
   PromptBwdArgs copy = a;
   void* delta_params[] = {&copy};
   const int64_t a_block = 8 * 4 * (32 / (DP / 8));  // rows
-  e = launch_op((const void*)prompt_delta_kernel<DP>,
-                dim3((unsigned)div_up((int64_t)a.tokens * a.q_heads, a_block), (unsigned)a.nranks), 256, 0, stream, delta_params);
+  // (no row of 128 tokens or fewer has a second tile of keys: the rows' kernel works out all deltas)
+  if (a.tokens > kTile)
+    e = launch_op((const void*)prompt_delta_kernel<DP>,
+                  dim3((unsigned)div_up((int64_t)a.tokens * a.q_heads, a_block), (unsigned)a.nranks), 256, 0, stream, delta_params);
   for (int which = 0; which < 2 && e == cudaSuccess; which++) {
     Work work;
     work.unit = which == 0 ? per_tile : kTile;

@@ -304,6 +304,18 @@ def test_cached_rows_that_see_nothing(dtype):
     assert bool((out[:, :6] == 0).all()) and bool((lse[:, 10:30] == float("-inf")).all())
 
 
+@pytest.mark.parametrize("new,lens", [([10, 20, 5], [4, 0, 5]), ([30], [11]), ([7], [0]), ([3, 0, 40, 1], [3, 9, 700, 0])])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cached_rows_that_see_nothing_in_parts(new, lens, dtype):
+    """The same where the table has room for many keys, so that rows are joined from parts, most of them of no key."""
+    g = gen(6)
+    k, v, table, keys, values = paged(g, 1, lens, 1, 64, 16, DT[dtype], extra_columns=400)
+    q = normal(g, 1, sum(new), 4, 64, dtype=DT[dtype])
+    starts = starts_of(new)
+    out, lse = cached_forward(q, k, v, table, starts, i32(*lens))
+    check_forward(q, keys, values, starts, out, lse, before=[a - b for a, b in zip(lens, new)])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_cached_bad_numbers(dtype):
     """Pages that are none are left out, lengths past the table row are cut to it; the status says so, later calls run."""
