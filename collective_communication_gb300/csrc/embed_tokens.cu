@@ -514,13 +514,16 @@ cudaError_t sums(EmbedBwdArgs& a, cudaStream_t stream) {
 bool few_tokens(int64_t tokens, int spans) { return tokens <= kFewTokens && tokens * spans <= 152 * 16; }
 
 // Chunks of 32 tokens leave less to join; of 8, where they would make too few warps.
-bool short_chunks(int64_t tokens, int hidden) { return div_up(tokens, 32) * div_up(hidden, 256) < 152 * 16; }
+constexpr int64_t kShortChunks = 152 * 16;
+bool short_chunks(int64_t tokens, int hidden) { return div_up(tokens, 32) * div_up(hidden, 256) < kShortChunks; }
 
 }  // namespace
 
+// Enough for every call of so many tokens or fewer.
 int64_t embed_tokens_scratch_bytes(int64_t tokens, int hidden) {
-  const int chunk = short_chunks(tokens, hidden) ? 8 : 32;
-  return 2 * align_up(tokens * 8, 256) + div_up(tokens, chunk * kChunks) * 2 * hidden * 4;
+  const int64_t few = (int64_t)(kShortChunks - 1) / div_up(hidden, 256) * 32, blocks = div_up(tokens < few ? tokens : few, 8 * kChunks),
+                more = div_up(tokens, 32 * kChunks);
+  return 2 * align_up(tokens * 8, 256) + (blocks > more ? blocks : more) * 2 * hidden * 4;
 }
 
 cudaError_t launch_embed_tokens(EmbedArgs& a, cudaStream_t stream) {

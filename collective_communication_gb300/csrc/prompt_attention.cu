@@ -779,24 +779,42 @@ cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t str
   return by_size<uint16_t>(a, stream);
 }
 
+// The most tokens times parts that a gradient of `tokens` or fewer leaves sums of, 0 if none is split: for each number of
+// parts the most tokens that still have so many. More sequences than one never have more parts.
+template <typename Tiles>
+int64_t most_key_parts(int64_t tokens, int64_t lanes, int64_t unit, int64_t blocks, int64_t least_few, int64_t least, Tiles row_tiles) {
+  int64_t most = 0;
+  for (int parts = 2; parts <= kMostKeyParts; parts++)
+    for (const int64_t waves : {1, 2, 8}) {
+      const int64_t fit = waves * blocks / parts / lanes * unit - 1, t = tokens < fit ? tokens : fit;  // items * parts <= waves * blocks
+      if (t > 0 && key_parts((t / unit + 1) * lanes, blocks, row_tiles(t), least_few, least) >= parts && t * parts > most)
+        most = t * parts;
+    }
+  return most;
+}
+
+// Enough for every call of so many tokens or fewer.
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim) {
   const int64_t delta = delta_bytes(nranks, tokens, q_heads);
   // the parts of few items' keys, where they may be split: rows of O, m and l, in either form
   const int group = q_heads / kv_heads, rows = head_dim <= 128 ? 64 : 32;
   const int64_t lanes = (int64_t)kv_heads * nranks, padded = head_dim <= 64 ? 64 : head_dim <= 96 ? 96 : head_dim <= 128 ? 128 : 256;
+  const bool tensor = group <= 128 && head_dim <= 128;
   int64_t parts = 0;
-  if ((tokens * group / rows + 1) * lanes * 2 <= kPromptParts) parts = kPromptParts * rows * (padded + 2) * 4;
-  if (group <= 128 && head_dim <= 128 && (tokens / (2 * (128 / group)) + 1) * lanes * 2 <= kPromptSplitBlocks)
-    parts = (int64_t)kPromptSplitBlocks * (256 * ((head_dim <= 64 ? 64 : 128) + 2) + kPromptPartInfo) * 4;
-  // what parts of the rows leave of dk and dv: a call of more sequences than one has no more of them
-  const int unit = group <= 128 && head_dim <= 128 ? 128 : rows;
-  const int most = group <= 128 && head_dim <= 128 ? key_parts((tokens / unit + 1) * lanes, kPromptSplitBlocks, tokens / (2 * (128 / group)), kLeastRowTilesFew,
-                                                               kLeastRowTiles)
-                                                   : 1;
-  const int plain = key_parts((tokens / rows + 1) * lanes, kPromptParts, tokens * group / (2 * rows), kLeastPlainRowTilesFew,
-                              kLeastPlainRowTiles);
-  const int key_split = most > plain ? most : plain;
-  const int64_t gradient = delta + (key_split > 1 ? key_split * 2 * key_part_floats(nranks, tokens, kv_heads, head_dim) * 4 : 0);
+  if ((group / rows + 1) * lanes * 2 <= kPromptParts) parts = kPromptParts * rows * (padded + 2) * 4;
+  if (tensor && lanes * 2 <= kPromptSplitBlocks) {
+    const int64_t more = (int64_t)kPromptSplitBlocks * (256 * ((head_dim <= 64 ? 64 : 128) + 2) + kPromptPartInfo) * 4;
+    parts = more > parts ? more : parts;
+  }
+  // what parts of the rows leave of dk and dv
+  int64_t split = most_key_parts(tokens, lanes, rows, kPromptParts, kLeastPlainRowTilesFew, kLeastPlainRowTiles,
+                                 [&](int64_t t) { return t * group / (2 * rows); });
+  if (tensor) {
+    const int64_t most = most_key_parts(tokens, lanes, 128, kPromptSplitBlocks, kLeastRowTilesFew, kLeastRowTiles,
+                                        [&](int64_t t) { return t / (2 * (128 / group)); });
+    split = most > split ? most : split;
+  }
+  const int64_t gradient = delta + 2 * key_part_floats(nranks, split, kv_heads, head_dim) * 4;
   return gradient > parts ? gradient : parts;
 }
 

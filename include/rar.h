@@ -508,7 +508,7 @@ RAR_API rar_status rar_qk_norm_rope_cached(const void* const* qkv, int nranks, i
                                            rar_dtype dtype, float eps, void* const* q_out, int64_t q_stride,
                                            void* const* k_cache, void* const* v_cache, int num_pages, int page_size,
                                            void* workspace, size_t workspaceBytes, void* stream);
-RAR_API size_t rar_qk_norm_rope_workspace_bytes(int nranks, int head_dim); /* of the backward call; 0: bad arguments */
+RAR_API size_t rar_qk_norm_rope_workspace_bytes(int nranks, int head_dim); /* of the backward call, also of fewer tokens; 0: bad arguments */
 RAR_API rar_status rar_qk_norm_rope_backward(const void* const* qkv, int nranks, int64_t tokens, int64_t qkv_stride,
                                              const void* q_weight, const void* k_weight, const float* cos_sin,
                                              int max_pos, int rot_dim, int interleaved, const int32_t* positions,
@@ -615,7 +615,7 @@ RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const 
  * binary32 on the ordinary arithmetic units.
  */
 RAR_API size_t rar_prompt_attention_workspace_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads,
-                                                    int head_dim); /* for all three; 0: bad arguments */
+                                                    int head_dim); /* for all three, also of fewer tokens; 0: bad arguments */
 RAR_API rar_status rar_prompt_attention(const void* const* q, int64_t q_stride, const void* const* k, int64_t k_stride,
                                         const void* const* v, int64_t v_stride, int nranks, int64_t tokens, int q_heads,
                                         int kv_heads, int head_dim, rar_dtype dtype, const int32_t* starts,
@@ -656,7 +656,7 @@ RAR_API rar_status rar_embed_tokens(const int32_t* tokens, int64_t num_tokens, c
                                     const int64_t* vocab, const int64_t* row_strides, int nranks, int hidden,
                                     rar_dtype dtype, float scale, void* out, int64_t out_stride, void* workspace,
                                     size_t workspaceBytes, void* stream);
-RAR_API size_t rar_embed_tokens_workspace_bytes(int64_t num_tokens, int hidden); /* of the backward call; 0: bad arguments */
+RAR_API size_t rar_embed_tokens_workspace_bytes(int64_t num_tokens, int hidden); /* of the backward call, also of fewer tokens; 0: bad arguments */
 RAR_API rar_status rar_embed_tokens_backward(const int32_t* tokens, int64_t num_tokens, const void* dout,
                                              int64_t dout_stride, rar_dtype dtype, float scale, float* const* dtables,
                                              const int64_t* vocab, const int64_t* drow_strides, int nranks, int hidden,

@@ -98,6 +98,17 @@ def test_prompt_workspace_bytes(lib):
     assert f(4, 100000, 32, 8, 128) >= B.OP_WORKSPACE_MIN_BYTES + 4 * 100000 * 32 * 4
 
 
+def test_workspaces_serve_fewer_tokens(lib):
+    """A workspace for the largest call is one for every smaller one, though only small calls are split."""
+    counts = sorted({n + d for k in range(17) for n in (1 << k, 5 << k, 19 * k * k) for d in (-1, 0, 1) if n + d >= 0})
+    for n, heads, kv, dim in ((1, 8, 1, 128), (2, 16, 4, 64), (8, 64, 8, 128), (1, 4, 4, 256), (1, 130, 1, 80), (1, 1, 1, 8), (32, 32, 32, 64)):
+        need = [lib.rar_prompt_attention_workspace_bytes(n, t, heads, kv, dim) for t in counts]
+        assert need == sorted(need) and need[0] >= B.OP_WORKSPACE_MIN_BYTES, (n, heads, kv, dim)
+    for hidden in (8, 64, 512, 4096, 1 << 20):
+        need = [lib.rar_embed_tokens_workspace_bytes(t, hidden) for t in counts]
+        assert need == sorted(need) and need[0] >= B.OP_WORKSPACE_MIN_BYTES, hidden
+
+
 def test_prompt_gradients_side_by_side(lib):
     """dq, dk and dv in one buffer (qkv's gradient) are apart; shifted into one another they are not."""
     parts = dict(dq=ranks(10), dk=(ctypes.c_void_p * 2)(*[at(10) + r * 64 * MIB + 1024 for r in range(2)]),
