@@ -458,10 +458,12 @@ __global__ void __launch_bounds__(128) prompt_join_few_kernel(const __grid_const
   if (lane == 0 && a.lse[rank] != nullptr) a.lse[rank][(int64_t)token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
 
-// Weight and score gradient of a score s that the row sees.
-__device__ __forceinline__ void weigh(float s, float dp, bool seen, float scale2, float lse2, float delta, float* p, float* ds) {
+// Weight and score gradient of a score s that the row sees; one that it sees alone has none (and would have what
+// roundings leave of dp - delta).
+__device__ __forceinline__ void weigh(float s, float dp, bool seen, bool alone, float scale2, float lse2, float delta, float* p,
+                                      float* ds) {
   *p = seen ? exp2_fast(fmaf(s, scale2, -lse2)) : 0.f;
-  *ds = seen ? *p * (dp - delta) : 0.f;
+  *ds = seen && !alone ? *p * (dp - delta) : 0.f;
 }
 
 // dq of BT rows, and delta of each for the other kernel.
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
 #pragma unroll
       for (int j = 0; j < S::MT; j++) {
         float p, ds;
-        weigh(s[i][j], dp[i][j], j0 + tx + 16 * j < sees[i], scale2, lse2[i], delta[i], &p, &ds);
+        weigh(s[i][j], dp[i][j], j0 + tx + 16 * j < sees[i], sees[i] == 1, scale2, lse2[i], delta[i], &p, &ds);
         sp[(ty + 16 * i) * S::LP + tx + 16 * j] = ds;
       }
     __syncwarp();
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
         const int r = tx + 16 * j, c = ty + 16 * i;
         const bool seen = r < rows && c < keys && j0 + c <= (row0 + r) / group;
         float p, ds;
-        weigh(s[i][j], dp[i][j], seen, scale2, slse[r], sdelta[r], &p, &ds);
+        weigh(s[i][j], dp[i][j], seen, row0 + r < group, scale2, slse[r], sdelta[r], &p, &ds);
         sp[c * S::LP + r] = p;
         sd[c * S::LP + r] = ds;
       }

@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         tmem_load32(from, s);
         tmem_load32(dp_at + quarter + slice * kColumns, dp);
         loads_done();
-        const int upto = sees - j * kTile - slice * kColumns;
+        // (the one score of a row that sees one key has no gradient, whatever roundings leave of dp - delta)
+        const int upto = (sees > 1 ? sees : 0) - j * kTile - slice * kColumns;
         const bool cut = (j + 1) * kTile > least;
         const F2 scale_pair = f2(scale2, scale2), lse_pair = f2(-lse2, -lse2);
 #pragma unroll
@@ -720,6 +721,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         uint32_t g[kColumns];
         tmem_load32(dp_from, g);
         loads_done();
+        if (x == 0) {  // rows of the first token, which see one key: its score has no gradient
+#pragma unroll
+          for (int c = 0; c < kColumns; c++)
+            if (c0 + c < group) s[c] = 0;
+        }
 #pragma unroll
         for (int c = 0; c < kColumns; c += 4) {
           const float4 y = d[c / 4];

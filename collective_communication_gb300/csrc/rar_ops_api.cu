@@ -153,7 +153,7 @@ struct Residency {
   std::atomic<const void*> fn;
   std::atomic<int> device, blocks;
 };
-constexpr int kResidencies = 64;
+constexpr int kResidencies = 128;
 Residency g_residency[kResidencies];
 std::atomic<int> g_residencies{0};
 

@@ -418,6 +418,23 @@ def test_backward(ranks, lens, q_heads, kv_heads, dim, dtype):
     check_backward(q, k, v, starts, out, lse, dout, *backward(q, k, v, starts, out, lse, dout))
 
 
+@pytest.mark.parametrize("dim", [64, 80, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_of_one_key(dim, dtype):
+    """A sequence's first token sees one key: no gradient through its score, exactly, and dv is dout."""
+    q, k, v, starts = prompt_inputs(2, [1, 0, 1, 1, 1], 3, 3, dim, dtype, seed=5)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    out, lse = forward(q, k, v, starts)
+    assert torch.equal(out, v)
+    dq, dk, dv = backward(q, k, v, starts, out, lse, dout)
+    assert bool((dq == 0).all()) and bool((dk == 0).all())
+    close(dv, dout.double(), 1e-6 * dout.double().abs())
+    q, k, v, starts = prompt_inputs(1, [300, 40], 6, 2, dim, dtype, seed=5)
+    out, lse = forward(q, k, v, starts)
+    dq = backward(q, k, v, starts, out, lse, normal(gen(9), *q.shape, dtype=q.dtype))[0]
+    assert bool((dq[:, [0, 300]] == 0).all()) and bool((dq[:, [1, 301]] != 0).any())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_backward_rows_in_no_sequence(dtype):
     q, k, v, starts = prompt_inputs(2, [100, 0, 37, 130], 6, 2, 64, dtype, ahead=5, behind=150)
