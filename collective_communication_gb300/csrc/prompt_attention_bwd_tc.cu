@@ -30,7 +30,7 @@
 // Blocks stay, one an SM, and take items (a tile of rows, or of keys) from a counter;
 // a warp finds the next one while the last is under way, and its first tiles are copied.
 //
-// Measured: 8192 tokens of one sequence, 16 query heads on 4 key heads of 64: 527 to 536
+// Measured: 8192 tokens of one sequence, 16 query heads on 4 key heads of 64: 526 to 536
 // us, 220 for the rows and 298 for the keys, 0.9 PFLOP/s of the seven products. What bounds
 // it is the weights' chain, from scores through two roundings to the last product, as long
 // for half the products of a head size of 128: tensor cores 38 % of the time, issue slots
@@ -216,6 +216,8 @@ struct Quarter {
   }
 };
 
+// What the bf16 pair `to` leaves of x and y, as another.
+__device__ __forceinline__ uint32_t bf16_rest(float x, float y, uint32_t to) { return bf16_pair(x - bf16_lo(to), y - bf16_hi(to)); }
 __device__ __forceinline__ void weights_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWeightWarps) : "memory"); }
 // One arrival of the warp, after its lanes' stores to tensor memory.
 __device__ __forceinline__ void arrive_warp(uint64_t* b) {
@@ -281,7 +283,10 @@ __global__ void __launch_bounds__(256) prompt_delta_kernel(const __grid_constant
   }
 }
 
-template <int DP>
+// FEW: a call of up to 128 tokens takes products with what the roundings of P and dS leave as well, which lies behind
+// them: over so few keys and rows the roundings need not average out (2 tokens: dq off by 2.8e-3 of its norm, where its own
+// rounding is 1.7e-3). It costs 1.5 to 3.5 us of 18 to 33; for all calls, it would cost 5 %.
+template <int DP, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __grid_constant__ PromptBwdArgs a,
                                                                      const __grid_constant__ Maps maps,
                                                                      const __grid_constant__ Work work) {
@@ -406,6 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         fence_after();
         if (more && !(fine = value(j + 1))) break;
         weights_by_rows<2, kColumns>(lead, dq_at, s_at + (n & 1) * 128, k_at + n % KS * L::kBytes, steps * 16, j > 0, L::kSlab);
+        if (FEW)
+          weights_by_rows<2, kColumns>(lead, dq_at, s_at + (n & 1) * 128 + kColumns / 2, k_at + n % KS * L::kBytes, steps * 16, true, L::kSlab);
         commit(lead, &k_empty[n % KS]);
         if (!more) commit(lead, &dq_full);
       }
@@ -475,9 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         for (int c = 0; c < kColumns; c += 2) {
           const F2 d = add2(f2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), delta_pair);
           const float2 ds = unpack(mul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), d));
+          if (FEW) dp[c] = __float_as_uint(ds.x), dp[c + 1] = __float_as_uint(ds.y);
           s[c / 2] = bf16_pair(ds.x, ds.y);
         }
         tmem_store16(from, s);
+        if (FEW) {
+#pragma unroll
+          for (int c = 0; c < kColumns; c += 2) s[c / 2] = bf16_rest(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]), s[c / 2]);
+          tmem_store16(from + kColumns / 2, s);
+        }
         arrive_warp(&ds_ready);
       }
       if (!fine || !wait(&dq_full, i & 1, dead)) break;
@@ -494,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   end_block(a.ws, dead, warp);
 }
 
-template <int DP>
+template <int DP, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __grid_constant__ PromptBwdArgs a,
                                                                      const __grid_constant__ Maps maps,
                                                                      const __grid_constant__ Work work) {
@@ -660,10 +673,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         if (!(fine = wait_warp(&p_ready[n % SB], n / SB & 1, dead))) break;
         fence_after();
         weights_by_rows<2, kColumns>(lead, dv_at, s_at + n % SB * 128, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, x > begin, L::kSlab);
+        if (FEW)
+          weights_by_rows<2, kColumns>(lead, dv_at, s_at + n % SB * 128 + kColumns / 2, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, true,
+                                       L::kSlab);
         if (x + SB < end && !(fine = score(x + SB))) break;
         if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
         fence_after();
         weights_by_rows<2, kColumns>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, x > begin, L::kSlab);
+        if (FEW)
+          weights_by_rows<2, kColumns>(lead, dk_at, dp_at + kColumns / 2, ring_at + stage * 2 * L::kBytes, steps * 16, true, L::kSlab);
         commit(lead, &empty[stage]);
         if (!more) commit(lead, &sums_full);
         if (more) value(x + 1);
@@ -715,6 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
 #pragma unroll
         for (int c = 0; c < kColumns; c += 2) w[c / 2] = bf16_pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         tmem_store16(from, w);
+        if (FEW) {
+#pragma unroll
+          for (int c = 0; c < kColumns; c += 2) w[c / 2] = bf16_rest(__uint_as_float(s[c]), __uint_as_float(s[c + 1]), w[c / 2]);
+          tmem_store16(from + kColumns / 2, w);
+        }
         arrive_warp(&p_ready[n % SB]);
         if (!(fine = wait(&dp_full, n & 1, dead))) break;
         fence_after();
@@ -726,15 +749,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
           for (int c = 0; c < kColumns; c++)
             if (c0 + c < group) s[c] = 0;
         }
-#pragma unroll
-        for (int c = 0; c < kColumns; c += 4) {
+        // four of the scores' gradients as bf16 pairs
+        auto gradients = [&](int c, float2* u, float2* v) {
           const float4 y = d[c / 4];
-          const float2 u = unpack(mul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                       add2(f2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), f2(y.x, y.y))));
-          const float2 v = unpack(mul2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
-                                       add2(f2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), f2(y.z, y.w))));
-          w[c / 2] = bf16_pair(u.x, u.y);
-          w[c / 2 + 1] = bf16_pair(v.x, v.y);
+          *u = unpack(mul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                           add2(f2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), f2(y.x, y.y))));
+          *v = unpack(mul2(f2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                           add2(f2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), f2(y.z, y.w))));
+          w[c / 2] = bf16_pair(u->x, u->y);
+          w[c / 2 + 1] = bf16_pair(v->x, v->y);
+        };
+        float2 u, v;
+        if (FEW) {
+#pragma unroll
+          for (int c = 0; c < kColumns; c += 4) {
+            gradients(c, &u, &v);
+            s[c / 2] = bf16_rest(u.x, u.y, w[c / 2]);  // in the place of weights that have had their turn
+            s[c / 2 + 1] = bf16_rest(v.x, v.y, w[c / 2 + 1]);
+          }
+          tmem_store16(dp_from + kColumns / 2, s);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kColumns; c += 4) gradients(c, &u, &v);
         }
         tmem_store16(dp_from, w);
         arrive_warp(&ds_ready);
@@ -773,10 +809,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   end_block(a.ws, dead, warp);
 }
 
-template <int DP>
+template <int DP, bool FEW>
 cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
   const int group = a.q_heads / a.kv_heads, per_tile = kTile / group, D = a.head_dim;
-  const void *rows = (const void*)prompt_rows_tc_kernel<DP>, *keys = (const void*)prompt_keys_tc_kernel<DP>;
+  const void *rows = (const void*)prompt_rows_tc_kernel<DP, FEW>, *keys = (const void*)prompt_keys_tc_kernel<DP, FEW>;
   int blocks = 0;
   cudaError_t e = resident_blocks(rows, kThreads, Layout<DP>::kRowsShared, &blocks);
   if (e == cudaSuccess) e = resident_blocks(keys, kThreads, Layout<DP>::kKeysShared, &blocks);
@@ -793,7 +829,7 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
   void* delta_params[] = {&copy};
   const int64_t a_block = 8 * 4 * (32 / (DP / 8));  // rows
   // (no row of 128 tokens or fewer has a second tile of keys: the rows' kernel works out all deltas)
-  if (a.tokens > kTile)
+  if (!FEW)
     e = launch_op((const void*)prompt_delta_kernel<DP>,
                   dim3((unsigned)div_up((int64_t)a.tokens * a.q_heads, a_block), (unsigned)a.nranks), 256, 0, stream, delta_params);
   for (int which = 0; which < 2 && e == cudaSuccess; which++) {
@@ -817,7 +853,8 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_prompt_attention_bwd_tc(const PromptBwdArgs& a, cudaStream_t stream) {
-  return a.head_dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+  if (a.tokens <= kTile) return a.head_dim <= 64 ? launch<64, true>(a, stream) : launch<128, true>(a, stream);
+  return a.head_dim <= 64 ? launch<64, false>(a, stream) : launch<128, false>(a, stream);
 }
 
 }  // namespace rar

@@ -435,6 +435,37 @@ def test_backward_of_one_key(dim, dtype):
     assert bool((dq[:, [0, 300]] == 0).all()) and bool((dq[:, [1, 301]] != 0).any())
 
 
+@pytest.mark.parametrize("lens", [[2], [3, 1, 32], [17, 0, 9, 31], [128]], ids=str)
+@pytest.mark.parametrize("dim", [64, 80, 128])
+def test_backward_of_few_tokens(lens, dim):
+    """Calls of up to 128 tokens lose nothing to the roundings of weights: what those leave takes part (2^-17 of a
+    weight or a score's gradient is lost), next to sums of 128 binary32 products (2^-17), the exponential of a score below 16
+    (2^-19) and lse's rounding (2^-21): below 2^-15 in all, of terms that are multiplied twice; 2^-13 is allowed."""
+    q, k, v, starts = prompt_inputs(2, lens, 6, 2, dim, "bf16", seed=6)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    out, lse = forward(q, k, v, starts)
+    dq, dk, dv = backward(q, k, v, starts, out, lse, dout)
+    bounds = starts.tolist()
+    for r in range(2):
+        for a, b in zip(bounds, bounds[1:]):
+            if a == b:
+                continue
+            x, key, value, g = (z[r, a:b].double() for z in (q, k, v, dout))
+            x, g = (z.unflatten(1, (2, 3)) for z in (x, g))
+            s, sees, _ = scores(q[r, a:b], k[r, a:b], 0, dim ** -0.5)
+            p = torch.softmax(s.masked_fill(~sees, float("-inf")), -1)
+            dp = torch.einsum("thgd,shd->hgts", g, value)
+            dsize = torch.einsum("thgd,shd->hgts", g.abs(), value.abs())
+            delta = (p * dp).sum(-1, keepdim=True)
+            ds = p * (dp - delta)
+            size = p * (dsize + (p * dsize).sum(-1, keepdim=True)) * 2 ** -13 * dim ** -0.5
+            close(dq[r, a:b], torch.einsum("hgts,shd->thgd", ds, key).flatten(1, 2) * dim ** -0.5,
+                  torch.einsum("hgts,shd->thgd", size, key.abs()).flatten(1, 2), "dq")
+            close(dk[r, a:b], torch.einsum("hgts,thgd->shd", ds, x) * dim ** -0.5,
+                  torch.einsum("hgts,thgd->shd", size, x.abs()), "dk")
+            close(dv[r, a:b], torch.einsum("hgts,thgd->shd", p, g), 2 ** -13 * torch.einsum("hgts,thgd->shd", p, g.abs()), "dv")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_backward_rows_in_no_sequence(dtype):
     q, k, v, starts = prompt_inputs(2, [100, 0, 37, 130], 6, 2, 64, dtype, ahead=5, behind=150)
