@@ -50,7 +50,8 @@ EXPORTED = (
     "rar_decode_attention_workspace_bytes", "rar_decode_attention", "rar_token_logprobs_workspace_bytes",
     "rar_token_logprobs", "rar_token_logprobs_backward", "rar_prompt_attention_workspace_bytes",
     "rar_prompt_attention", "rar_prompt_attention_cached", "rar_prompt_attention_backward", "rar_embed_tokens",
-    "rar_embed_tokens_workspace_bytes", "rar_embed_tokens_backward",
+    "rar_embed_tokens_workspace_bytes", "rar_embed_tokens_backward", "rar_prompt_attention_ex",
+    "rar_prompt_attention_cached_ex", "rar_prompt_attention_backward_ex",
 )
 
 
@@ -128,11 +129,13 @@ def load_library():
     L.rar_token_logprobs.argtypes = [P, P, P, I, I64, I, P, P, P, P, I, P, P, P, SZ, P]
     L.rar_token_logprobs_backward.argtypes = [P, P, P, I, I64, I, P, P, P, P, P, P, P, P, SZ, P]
     L.rar_prompt_attention_workspace_bytes.argtypes = [I, I64, I, I, I]
-    rows = [P, I64]
-    L.rar_prompt_attention.argtypes = rows * 3 + [I, I64, I, I, I, I, P, I, F] + rows + [P, P, SZ, P]
-    L.rar_prompt_attention_cached.argtypes = rows + [P, P, I, I64, I, I, I, I, I, I, P, I64, I, P, P, I, F] + rows + \
-        [P, P, SZ, P]
-    L.rar_prompt_attention_backward.argtypes = rows * 3 + [I, I64, I, I, I, I, P, I, F] + rows + [P] + rows * 4 + [P, SZ, P]
+    for rows, form in (([P, I64], ""), ([P, I64, I64], "_ex")):  # data, then elements from token to token, from head to head
+        f = {name: getattr(L, "rar_prompt_attention" + name + form) for name in ("", "_cached", "_backward")}
+        f[""].argtypes = rows * 3 + [I, I64, I, I, I, I, P, I, F] + rows + [P, P, SZ, P]
+        f["_cached"].argtypes = rows + [P, P, I, I64, I, I, I, I, I, I, P, I64, I, P, P, I, F] + rows + [P, P, SZ, P]
+        f["_backward"].argtypes = rows * 3 + [I, I64, I, I, I, I, P, I, F] + rows + [P] + rows * 4 + [P, SZ, P]
+        for call in f.values():
+            call.restype = I
     L.rar_embed_tokens.argtypes = [P, I64, P, P, P, I, I, I, F, P, I64, P, SZ, P]
     L.rar_embed_tokens_workspace_bytes.argtypes = [I64, I]
     L.rar_embed_tokens_backward.argtypes = [P, I64, P, I64, I, F, P, P, P, I, I, I, P, SZ, P]
@@ -142,8 +145,7 @@ def load_library():
         getattr(L, name).restype = SZ
     for name in ("rar_op_workspace_init", "rar_page_tables", "rar_qk_norm_rope", "rar_qk_norm_rope_cached",
                  "rar_qk_norm_rope_backward", "rar_decode_attention", "rar_token_logprobs",
-                 "rar_token_logprobs_backward", "rar_prompt_attention", "rar_prompt_attention_cached",
-                 "rar_prompt_attention_backward", "rar_embed_tokens", "rar_embed_tokens_backward"):
+                 "rar_token_logprobs_backward", "rar_embed_tokens", "rar_embed_tokens_backward"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -405,8 +407,8 @@ def _op_setup():
                            "collective_communication_gb300/build.py` (or __graft_entry__.build())") from e
     lib = load_library()
     names = ("rar_page_tables", "rar_qk_norm_rope", "rar_qk_norm_rope_cached", "rar_qk_norm_rope_backward",
-             "rar_decode_attention", "rar_token_logprobs", "rar_token_logprobs_backward", "rar_prompt_attention",
-             "rar_prompt_attention_cached", "rar_prompt_attention_backward", "rar_embed_tokens", "rar_embed_tokens_backward")
+             "rar_decode_attention", "rar_token_logprobs", "rar_token_logprobs_backward", "rar_prompt_attention_ex",
+             "rar_prompt_attention_cached_ex", "rar_prompt_attention_backward_ex", "rar_embed_tokens", "rar_embed_tokens_backward")
     _operands.setup(RarError, (torch.float32, torch.bfloat16, torch.int32),
                     tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in names),
                     torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
@@ -500,8 +502,9 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_ent
 def prompt_attention(q, k, v, starts, out, lse, workspace: OpWorkspace, scale: Optional[float] = None,
                      stream=None) -> None:
     """Enqueue causal attention over packed sequences: q, out [tokens, q_heads,
-    head_dim] and k, v [tokens, kv_heads, head_dim] a rank (v may be a view of
-    the projection's output), int32 starts [sequences + 1]; lse float32 [tokens,
+    head_dim] and k, v [tokens, kv_heads, head_dim] a rank, of any strides that keep
+    heads dense and rows apart (v may be a view of the projection's output, out one of
+    [q_heads, tokens, head_dim]), int32 starts [sequences + 1]; lse float32 [tokens,
     q_heads] a rank, or None. scale: head_dim ** -0.5 by default."""
     st = (_ops or _op_setup()).prompt_attention(q, k, v, starts, out, lse, scale, workspace.ptr, workspace.nbytes, stream)
     if st:

@@ -33,9 +33,9 @@ static struct {
   __typeof__(&rar_decode_attention) decode_attention;
   __typeof__(&rar_token_logprobs) token_logprobs;
   __typeof__(&rar_token_logprobs_backward) token_logprobs_backward;
-  __typeof__(&rar_prompt_attention) prompt_attention;
-  __typeof__(&rar_prompt_attention_cached) prompt_attention_cached;
-  __typeof__(&rar_prompt_attention_backward) prompt_attention_backward;
+  __typeof__(&rar_prompt_attention_ex) prompt_attention;
+  __typeof__(&rar_prompt_attention_cached_ex) prompt_attention_cached;
+  __typeof__(&rar_prompt_attention_backward_ex) prompt_attention_backward;
   __typeof__(&rar_embed_tokens) embed_tokens;
   __typeof__(&rar_embed_tokens_backward) embed_tokens_backward;
 } abi;
@@ -123,6 +123,7 @@ typedef struct {
   int ranks, dims, dtype;
   int64_t size[MAX_DIMS]; /* of a rank's tensor */
   int64_t row;            /* elements from row to row; the dimensions after a row's are dense */
+  int64_t head;           /* of rows of heads: from head to head */
   bool dense;             /* no gaps between the rows either */
   void* data[RAR_MAX_RANKS];
 } Ranked;
@@ -140,7 +141,18 @@ static bool lay_out(const int64_t* size, const int64_t* stride, int dims, const 
   return true;
 }
 
-static bool read_ranked(PyObject* x, const char* name, int dims, Ranked* out) {
+/* [tokens, heads, head_dim] of which the last dimension alone is dense. */
+static bool lay_out_heads(const int64_t* size, const int64_t* stride, const char* name, Ranked* out) {
+  if (size[2] != 1 && stride[2] != 1) return refuse(name, "dense in its last dimension");
+  out->dims = 3;
+  for (int i = 0; i < 3; i++) out->size[i] = size[i];
+  out->head = size[1] > 1 ? stride[1] : size[2];
+  out->row = size[0] > 1 ? stride[0] : size[1] * out->head;
+  out->dense = false;
+  return true;
+}
+
+static bool read_laid_out(PyObject* x, const char* name, int dims, bool heads, Ranked* out) {
   Tensor t;
   if (PyList_Check(x) || PyTuple_Check(x)) {
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(x);
@@ -156,7 +168,7 @@ static bool read_ranked(PyObject* x, const char* name, int dims, Ranked* out) {
     }
     out->ranks = (int)n;
     out->dtype = first.dtype;
-    return lay_out(first.size, first.stride, dims, name, out);
+    return heads ? lay_out_heads(first.size, first.stride, name, out) : lay_out(first.size, first.stride, dims, name, out);
   }
   if (!read_tensor(x, name, &t)) return false;
   if (t.dims != dims + 1 || t.size[0] < 1 || t.size[0] > RAR_MAX_RANKS)
@@ -165,8 +177,10 @@ static bool read_ranked(PyObject* x, const char* name, int dims, Ranked* out) {
   out->dtype = t.dtype;
   const int64_t step = t.stride[0] * bytes_of(t.dtype);
   for (int r = 0; r < out->ranks; r++) out->data[r] = t.data == NULL ? NULL : t.data + r * step;
-  return lay_out(t.size + 1, t.stride + 1, dims, name, out);
+  return heads ? lay_out_heads(t.size + 1, t.stride + 1, name, out) : lay_out(t.size + 1, t.stride + 1, dims, name, out);
 }
+static bool read_ranked(PyObject* x, const char* name, int dims, Ranked* out) { return read_laid_out(x, name, dims, false, out); }
+static bool read_heads(PyObject* x, const char* name, Ranked* out) { return read_laid_out(x, name, 3, true, out); }
 
 static bool same_size(const Ranked* a, const Ranked* b) {
   if (a->ranks != b->ranks || a->dims != b->dims) return false;
@@ -527,7 +541,7 @@ typedef struct {
 /* q, starts, scale or None */
 static bool read_prompt(PyObject* q, PyObject* starts, PyObject* scale, Prompt* p) {
   int64_t bounds;
-  if (!read_ranked(q, "q", 3, &p->q) || !floating(p->q.dtype, "q") ||
+  if (!read_heads(q, "q", &p->q) || !floating(p->q.dtype, "q") ||
       !read_flat(starts, "starts", I32, -1, &p->starts, &bounds) || !fits_int(bounds, "starts") ||
       !fits_int(p->q.size[1], "q") || !fits_int(p->q.size[2], "q"))
     return false;
@@ -538,12 +552,12 @@ static bool read_prompt(PyObject* q, PyObject* starts, PyObject* scale, Prompt* 
 }
 /* A tensor as the queries are. */
 static bool read_like(PyObject* x, const char* name, const Ranked* q, Ranked* out) {
-  if (!read_ranked(x, name, 3, out)) return false;
+  if (!read_heads(x, name, out)) return false;
   return (same_size(out, q) && out->dtype == q->dtype) || refuse(name, "as q");
 }
 /* Keys or values: [tokens, kv_heads, head_dim] with the queries' tokens and head_dim. */
 static bool read_keys(PyObject* x, const char* name, const Ranked* q, Ranked* out) {
-  if (!read_ranked(x, name, 3, out)) return false;
+  if (!read_heads(x, name, out)) return false;
   return (out->ranks == q->ranks && out->dtype == q->dtype && out->size[0] == q->size[0] && out->size[2] == q->size[2] &&
           out->size[1] <= INT32_MAX) ||
          refuse(name, "[tokens, kv_heads, head_dim] of q's tokens, head_dim and dtype");
@@ -569,10 +583,10 @@ static PyObject* prompt_attention(PyObject* self, PyObject* const* v, Py_ssize_t
     return NULL;
   }
   if (!read_place(v + 7, &w)) return NULL;
-  CALL(abi.prompt_attention((const void* const*)p.q.data, p.q.row, (const void* const*)k.data, k.row,
-                            (const void* const*)c.data, c.row, p.q.ranks, p.q.size[0], (int)p.q.size[1], (int)k.size[1],
-                            (int)p.q.size[2], (rar_dtype)p.q.dtype, p.starts, p.sequences, p.scale, out.data, out.row,
-                            v[5] != Py_None ? (float* const*)lse.data : NULL, w.data, w.bytes, w.stream));
+  CALL(abi.prompt_attention((const void* const*)p.q.data, p.q.row, p.q.head, (const void* const*)k.data, k.row, k.head,
+                            (const void* const*)c.data, c.row, c.head, p.q.ranks, p.q.size[0], (int)p.q.size[1],
+                            (int)k.size[1], (int)p.q.size[2], (rar_dtype)p.q.dtype, p.starts, p.sequences, p.scale,
+                            out.data, out.row, out.head, v[5] != Py_None ? (float* const*)lse.data : NULL, w.data, w.bytes, w.stream));
 }
 
 /* q, k_cache, v_cache, block_table, starts, lens, out, lse or None, scale or None, place */
@@ -592,10 +606,10 @@ static PyObject* prompt_attention_cached(PyObject* self, PyObject* const* v, Py_
     return NULL;
   }
   if (!read_place(v + 9, &w)) return NULL;
-  CALL(abi.prompt_attention_cached((const void* const*)p.q.data, p.q.row, (const void* const*)k.data,
+  CALL(abi.prompt_attention_cached((const void* const*)p.q.data, p.q.row, p.q.head, (const void* const*)k.data,
                                    (const void* const*)c.data, p.q.ranks, p.q.size[0], (int)p.q.size[1], (int)k.size[1],
                                    (int)p.q.size[2], (rar_dtype)p.q.dtype, (int)k.size[0], (int)k.size[2], table.data,
-                                   table.stride, table.columns, p.starts, lens, p.sequences, p.scale, out.data, out.row,
+                                   table.stride, table.columns, p.starts, lens, p.sequences, p.scale, out.data, out.row, out.head,
                                    v[7] != Py_None ? (float* const*)lse.data : NULL, w.data, w.bytes, w.stream));
 }
 
@@ -614,12 +628,12 @@ static PyObject* prompt_attention_backward(PyObject* self, PyObject* const* v, P
     return NULL;
   }
   if (!read_place(v + 11, &w)) return NULL;
-  CALL(abi.prompt_attention_backward((const void* const*)p.q.data, p.q.row, (const void* const*)k.data, k.row,
-                                     (const void* const*)c.data, c.row, p.q.ranks, p.q.size[0], (int)p.q.size[1],
+  CALL(abi.prompt_attention_backward((const void* const*)p.q.data, p.q.row, p.q.head, (const void* const*)k.data, k.row,
+                                     k.head, (const void* const*)c.data, c.row, c.head, p.q.ranks, p.q.size[0], (int)p.q.size[1],
                                      (int)k.size[1], (int)p.q.size[2], (rar_dtype)p.q.dtype, p.starts, p.sequences, p.scale,
-                                     (const void* const*)out.data, out.row, (const float* const*)lse.data,
-                                     (const void* const*)dout.data, dout.row, dq.data, dq.row, dk.data, dk.row, dv.data,
-                                     dv.row, w.data, w.bytes, w.stream));
+                                     (const void* const*)out.data, out.row, out.head, (const float* const*)lse.data,
+                                     (const void* const*)dout.data, dout.row, dout.head, dq.data, dq.row, dq.head, dk.data,
+                                     dk.row, dk.head, dv.data, dv.row, dv.head, w.data, w.bytes, w.stream));
 }
 
 /* [tokens, width] rows that the ranks share. */

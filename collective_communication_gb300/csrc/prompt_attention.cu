@@ -23,6 +23,8 @@
 // items split, 170 to 197). Over long prompts that is 34 to 40 TFLOP/s forward and 17 to
 // 27 for the gradient, of the 75 that the multiply-adds alone could make: issue slots are
 // 46 % busy, the rest of the time warps wait for shared memory and for the pipes.
+#include <initializer_list>
+
 #include "op_common.cuh"
 #include "prompt_attention.cuh"
 #include "rar_launch.h"
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(con
   auto token_of = [&](int r) { return seq.first + (row0 + r) / group; };
   auto head_of = [&](int r) { return head * group + (row0 + r) % group; };
   load_rows<T, DP, BT>(sq, D, [&](int r) {
-    return r < rows ? q + (int64_t)token_of(r) * a.q_stride + (int64_t)head_of(r) * D : nullptr;
+    return r < rows ? q + (int64_t)token_of(r) * a.q_stride + (int64_t)head_of(r) * a.q_head : nullptr;
   });
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   int sees[S::MT];  // keys that the row sees
@@ -258,16 +260,16 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(con
       find_keys<BT>(a, seq, head, j0, key_row);
       __syncthreads();
     }
-    auto key = [&](const void* base, int64_t stride, int r) -> const T* {
+    auto key = [&](const void* base, int64_t stride, int64_t head_stride, int r) -> const T* {
       if (paged) return key_row[r] < 0 ? nullptr : (const T*)base + key_row[r] * D;
-      return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
+      return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + head * head_stride : nullptr;
     };
-    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
+    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, a.k_head, r); });
     __syncthreads();
     float s[S::MT][S::MT];
     dots<DP, BT>(sq, sk, D, s);
     __syncthreads();
-    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
+    load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.v[rank], a.v_stride, a.v_head, r); });
 #pragma unroll
     for (int i = 0; i < S::MT; i++) {
       float top = m[i];
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) prompt_kernel(con
       }
       continue;
     }
-    o.store_row(i, (T*)a.out[rank] + (int64_t)token_of(r) * a.out_stride + (int64_t)head_of(r) * D, D,
+    o.store_row(i, (T*)a.out[rank] + (int64_t)token_of(r) * a.out_stride + (int64_t)head_of(r) * a.out_head, D,
                 sum == 0.f ? 0.f : 1.f / sum);
     if (a.lse[rank] != nullptr && tx == 0)
       a.lse[rank][(int64_t)token_of(r) * a.q_heads + head_of(r)] = (m[i] + log2f(sum)) / kLog2e;
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(128) prompt_join_rows_kernel(const __grid_cons
       v.y += partial[k][d / 2].y;
     }
     const float by = sum == 0.f ? 0.f : 1.f / sum;
-    store2((T*)a.out[rank] + token * a.out_stride + query * D + d, sum == 0.f ? 0.f : v.x * by, sum == 0.f ? 0.f : v.y * by);
+    store2((T*)a.out[rank] + token * a.out_stride + query * a.out_head + d, sum == 0.f ? 0.f : v.x * by, sum == 0.f ? 0.f : v.y * by);
   }
   if (threadIdx.x == 0 && a.lse[rank] != nullptr) a.lse[rank][token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(128) prompt_join_few_kernel(const __grid_const
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   const float by = sum == 0.f ? 0.f : 1.f / sum;
-  T* const out = (T*)a.out[rank] + (int64_t)token * a.out_stride + (int64_t)query * D;
+  T* const out = (T*)a.out[rank] + (int64_t)token * a.out_stride + query * a.out_head;
   for (int d0 = 0; d0 < D; d0 += 64) {
     const int d = d0 + lane * 2;
     float2 x[kFewParts];
@@ -484,12 +486,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
   const int row0 = tile * BT, rows = min(BT, seq.length * group - row0);
   auto token_of = [&](int r) { return (int64_t)(seq.first + (row0 + r) / group); };
   auto head_of = [&](int r) { return (int64_t)(head * group + (row0 + r) % group); };
-  auto row_of = [&](const void* base, int64_t stride, int r) {
-    return r < rows ? (const T*)base + token_of(r) * stride + head_of(r) * D : nullptr;
+  auto row_of = [&](const void* base, int64_t stride, int64_t head_stride, int r) {
+    return r < rows ? (const T*)base + token_of(r) * stride + head_of(r) * head_stride : nullptr;
   };
-  load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
-  load_rows<T, DP, BT>(sk, D, [&](int r) { return row_of(a.out[rank], a.out_stride, r); });
-  load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
+  load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, a.dout_head, r); });
+  load_rows<T, DP, BT>(sk, D, [&](int r) { return row_of(a.out[rank], a.out_stride, a.out_head, r); });
+  load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, a.q_head, r); });
   __syncthreads();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   int sees[S::MT];
@@ -515,17 +517,17 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
   const float scale2 = a.scale * kLog2e;
   for (int j0 = 0; j0 < most; j0 += BT) {
     __syncthreads();
-    auto key = [&](const void* base, int64_t stride, int r) {
-      return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
+    auto key = [&](const void* base, int64_t stride, int64_t head_stride, int r) {
+      return j0 + r < seq.keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + head * head_stride : nullptr;
     };
     float s[S::MT][S::MT], dp[S::MT][S::MT];
-    load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
-    if (kApart<DP>) load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
+    load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, a.v_head, r); });
+    if (kApart<DP>) load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, a.k_head, r); });
     __syncthreads();
     dots<DP, BT>(sg, sv, D, dp);
     if (!kApart<DP>) {
       __syncthreads();
-      load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
+      load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, a.k_head, r); });
       __syncthreads();
     }
     dots<DP, BT>(sq, sk, D, s);
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
 #pragma unroll
   for (int i = 0; i < S::MT; i++) {
     const int r = ty + 16 * i;
-    if (r < rows) dq.store_row(i, (T*)a.dq[rank] + token_of(r) * a.dq_stride + head_of(r) * D, D, a.scale);
+    if (r < rows) dq.store_row(i, (T*)a.dq[rank] + token_of(r) * a.dq_stride + head_of(r) * a.dq_head, D, a.scale);
   }
 }
 
@@ -565,11 +567,11 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
   // the first keys of a sequence are seen by the most rows: they start first
   if (!find_sequence(a.starts, a.sequences, a.tokens, 1, BT, place.slot, &seq, &tile)) return;
   const int j0 = tile * BT, keys = min(BT, seq.length - j0);
-  auto key = [&](const void* base, int64_t stride, int r) {
-    return r < keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + (int64_t)head * D : nullptr;
+  auto key = [&](const void* base, int64_t stride, int64_t head_stride, int r) {
+    return r < keys ? (const T*)base + (int64_t)(seq.first + j0 + r) * stride + head * head_stride : nullptr;
   };
-  load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, r); });
-  load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, r); });
+  load_rows<T, DP, BT>(sk, D, [&](int r) { return key(a.k[rank], a.k_stride, a.k_head, r); });
+  load_rows<T, DP, BT>(sv, D, [&](int r) { return key(a.v[rank], a.v_stride, a.v_head, r); });
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   Sums<DP, BT> dk, dv;
   dk.zero();
@@ -582,12 +584,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
     const int rows = min(BT, seq.length * group - row0);
     auto token_of = [&](int r) { return (int64_t)(seq.first + (row0 + r) / group); };
     auto head_of = [&](int r) { return (int64_t)(head * group + (row0 + r) % group); };
-    auto row_of = [&](const void* base, int64_t stride, int r) {
-      return r < rows ? (const T*)base + token_of(r) * stride + head_of(r) * D : nullptr;
+    auto row_of = [&](const void* base, int64_t stride, int64_t head_stride, int r) {
+      return r < rows ? (const T*)base + token_of(r) * stride + head_of(r) * head_stride : nullptr;
     };
     __syncthreads();
-    load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
-    if (kApart<DP>) load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
+    load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, a.q_head, r); });
+    if (kApart<DP>) load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, a.dout_head, r); });
     for (int r = threadIdx.x; r < BT; r += kThreads) {
       const int64_t at = r < rows ? token_of(r) * a.q_heads + head_of(r) : 0;
       slse[r] = r < rows ? a.lse[rank][at] * kLog2e : 0.f;
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
     dots<DP, BT>(sk, sq, D, s);
     if (!kApart<DP>) {
       __syncthreads();
-      load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, r); });
+      load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, a.dout_head, r); });
       __syncthreads();
     }
     dots<DP, BT>(sv, sg, D, dp);
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
     dv.add(sp, sg);
     if (!kApart<DP>) {
       __syncthreads();
-      load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, r); });
+      load_rows<T, DP, BT>(sq, D, [&](int r) { return row_of(a.q[rank], a.q_stride, a.q_head, r); });
       __syncthreads();
     }
     dk.add(sd, sq);
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
   for (int i = 0; i < S::MT; i++) {
     const int r = ty + 16 * i;
     if (r >= keys) continue;
-    const int64_t token = seq.first + j0 + r, at = (int64_t)head * D;
+    const int64_t token = seq.first + j0 + r;
     if (split.parts > 1) {
       const int64_t each = key_part_floats(a.nranks, a.tokens, a.kv_heads, D);
       float* const to = split.sums + 2 * part * each + (((int64_t)rank * a.tokens + token) * a.kv_heads + head) * D;
@@ -634,8 +636,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
       dv.store_row(i, to + each, D, 1.f);
       continue;
     }
-    dk.store_row(i, (T*)a.dk[rank] + token * a.dk_stride + at, D, a.scale);
-    dv.store_row(i, (T*)a.dv[rank] + token * a.dv_stride + at, D, 1.f);
+    dk.store_row(i, (T*)a.dk[rank] + token * a.dk_stride + head * a.dk_head, D, a.scale);
+    dv.store_row(i, (T*)a.dv[rank] + token * a.dv_stride + head * a.dv_head, D, 1.f);
   }
 }
 
@@ -664,7 +666,9 @@ __global__ void __launch_bounds__(256) prompt_key_parts_kernel(const __grid_cons
     }
     Pack8<T> y;
     y.narrow(sum);
-    y.store((T*)(which == 0 ? a.dk[rank] : a.dv[rank]) + token * (which == 0 ? a.dk_stride : a.dv_stride) + at % width);
+    const int head = (int)(at % width) / a.head_dim, d = (int)(at % width) % a.head_dim;
+    y.store(which == 0 ? (T*)a.dk[rank] + token * a.dk_stride + head * a.dk_head + d
+                       : (T*)a.dv[rank] + token * a.dv_stride + head * a.dv_head + d);
   }
 }
 
@@ -726,11 +730,10 @@ cudaError_t backward(const PromptBwdArgs& a, cudaStream_t stream) {
 // Whether the tensor core form takes the call: a group of heads fills no more than the
 // 128 rows of a tile, sums of 128 elements a row fit tensor memory beside the scores,
 // and strides are what a TMA map can say.
-template <typename Args>
-bool tensor_cores(const Args& a, int64_t k_stride, int64_t v_stride) {
-  const int64_t most = (int64_t)1 << 38;
-  return a.dtype != 0 && a.head_dim <= 128 && a.q_heads / a.kv_heads <= 128 && a.q_stride < most && a.out_stride < most &&
-         k_stride < most && v_stride < most;
+bool tensor_cores(int dtype, int head_dim, int group, std::initializer_list<int64_t> strides) {
+  for (const int64_t s : strides)
+    if (s >= (int64_t)1 << 38) return false;
+  return dtype != 0 && head_dim <= 128 && group <= 128;
 }
 
 }  // namespace
@@ -770,13 +773,16 @@ cudaError_t launch_prompt_key_parts(const PromptBwdArgs& a, const KeyParts& part
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream) {
   if (a.dtype == 0) return by_size<float>(a, stream);
-  if (tensor_cores(a, a.k_stride, a.v_stride)) return launch_prompt_attention_tc(a, stream);
+  if (tensor_cores(a.dtype, a.head_dim, a.q_heads / a.kv_heads,
+                   {a.q_stride, a.k_stride, a.v_stride, a.out_stride, a.q_head, a.k_head, a.v_head, a.out_head}))
+    return launch_prompt_attention_tc(a, stream);
   return by_size<uint16_t>(a, stream);
 }
 
 cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t stream) {
   if (a.dtype == 0) return by_size<float>(a, stream);
-  if (tensor_cores(a, a.k_stride, a.v_stride) && a.dout_stride < (int64_t)1 << 38)
+  if (tensor_cores(a.dtype, a.head_dim, a.q_heads / a.kv_heads,
+                   {a.q_stride, a.k_stride, a.v_stride, a.dout_stride, a.q_head, a.k_head, a.v_head, a.dout_head}))
     return launch_prompt_attention_bwd_tc(a, stream);
   return by_size<uint16_t>(a, stream);
 }

@@ -26,6 +26,7 @@ struct PromptArgs {
   const int32_t* table;  // null: dense keys
   char* ws;
   int64_t q_stride, k_stride, v_stride, out_stride, table_stride;
+  int64_t q_head, k_head, v_head, out_head;  // elements from head to head of a token
   float scale;
   int nranks, dtype, tokens, sequences, q_heads, kv_heads, head_dim, page_shift, num_pages, max_blocks;
 };
@@ -43,6 +44,7 @@ struct PromptBwdArgs {
   const int32_t* starts;
   char* ws;  // scratch: delta, float [ranks, tokens, q_heads]; then what parts leave of dk and dv
   int64_t q_stride, k_stride, v_stride, out_stride, dout_stride, dq_stride, dk_stride, dv_stride;
+  int64_t q_head, k_head, v_head, out_head, dout_head, dq_head, dk_head, dv_head;
   float scale;
   int nranks, dtype, tokens, sequences, q_heads, kv_heads, head_dim;
 };

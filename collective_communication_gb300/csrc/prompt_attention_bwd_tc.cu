@@ -264,9 +264,9 @@ __global__ void __launch_bounds__(256) prompt_delta_kernel(const __grid_constant
     x[i].zero();
     y[i].zero();
     if (r < rows && d < D) {
-      const int64_t token = r / a.q_heads, in_token = r % a.q_heads * D + d;
-      x[i].load_stream((const uint16_t*)a.out[rank] + token * a.out_stride + in_token);
-      y[i].load_stream((const uint16_t*)a.dout[rank] + token * a.dout_stride + in_token);
+      const int64_t token = r / a.q_heads, head = r % a.q_heads;
+      x[i].load_stream((const uint16_t*)a.out[rank] + token * a.out_stride + head * a.out_head + d);
+      y[i].load_stream((const uint16_t*)a.dout[rank] + token * a.dout_stride + head * a.dout_head + d);
     }
   }
 #pragma unroll
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(&dq_free);
-      if (mine) o.store((uint16_t*)a.dq[t.rank] + at_token * a.dq_stride + (int64_t)query * D, slice, a.scale, D);
+      if (mine) o.store((uint16_t*)a.dq[t.rank] + at_token * a.dq_stride + query * a.dq_head, slice, a.scale, D);
     }
   }
   end_block(a.ws, dead, warp);
@@ -793,15 +793,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         dv.zero();
       }
       if (row < t.count) {
-        const int64_t token = (int64_t)t.sequence + key, at = (int64_t)t.head * D;
+        const int64_t token = (int64_t)t.sequence + key;
         if (work.split.parts > 1) {
           const int64_t each = key_part_floats(a.nranks, a.tokens, a.kv_heads, D);
-          float* const to = work.split.sums + 2 * t.part * each + ((int64_t)t.rank * a.tokens + token) * a.kv_heads * D + at;
+          float* const to = work.split.sums + 2 * t.part * each + (((int64_t)t.rank * a.tokens + token) * a.kv_heads + t.head) * D;
           dk.store_part(to, slice, a.scale, D);
           dv.store_part(to + each, slice, 1.f, D);
         } else {
-          dk.store((uint16_t*)a.dk[t.rank] + token * a.dk_stride + at, slice, a.scale, D);
-          dv.store((uint16_t*)a.dv[t.rank] + token * a.dv_stride + at, slice, 1.f, D);
+          dk.store((uint16_t*)a.dk[t.rank] + token * a.dk_stride + t.head * a.dk_head, slice, a.scale, D);
+          dv.store((uint16_t*)a.dv[t.rank] + token * a.dv_stride + t.head * a.dv_head, slice, 1.f, D);
         }
       }
     }
@@ -818,11 +818,11 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
   if (e == cudaSuccess) e = resident_blocks(keys, kThreads, Layout<DP>::kKeysShared, &blocks);
   static thread_local Maps maps;
   for (int r = 0; r < a.nranks && e == cudaSuccess; r++) {
-    e = make_map(&maps.q[r], a.q[r], D, a.q_heads, a.tokens, D * 2, a.q_stride * 2, group, per_tile);
+    e = make_map(&maps.q[r], a.q[r], D, a.q_heads, a.tokens, a.q_head * 2, a.q_stride * 2, group, per_tile);
     if (e == cudaSuccess)
-      e = make_map(&maps.dout[r], a.dout[r], D, a.q_heads, a.tokens, D * 2, a.dout_stride * 2, group, per_tile);
-    if (e == cudaSuccess) e = make_map(&maps.k[r], a.k[r], D, a.kv_heads, a.tokens, D * 2, a.k_stride * 2, 1, kTile);
-    if (e == cudaSuccess) e = make_map(&maps.v[r], a.v[r], D, a.kv_heads, a.tokens, D * 2, a.v_stride * 2, 1, kTile);
+      e = make_map(&maps.dout[r], a.dout[r], D, a.q_heads, a.tokens, a.dout_head * 2, a.dout_stride * 2, group, per_tile);
+    if (e == cudaSuccess) e = make_map(&maps.k[r], a.k[r], D, a.kv_heads, a.tokens, a.k_head * 2, a.k_stride * 2, 1, kTile);
+    if (e == cudaSuccess) e = make_map(&maps.v[r], a.v[r], D, a.kv_heads, a.tokens, a.v_head * 2, a.v_stride * 2, 1, kTile);
   }
   if (e != cudaSuccess) return e;
   PromptBwdArgs copy = a;

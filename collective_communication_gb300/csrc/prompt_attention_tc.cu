@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         fence_after();
       }
       const float by = l == 0.f ? 0.f : 1.f / l;
-      uint16_t* const out = (uint16_t*)a.out[rank] + at_token * a.out_stride + (int64_t)query * D;
+      uint16_t* const out = (uint16_t*)a.out[rank] + at_token * a.out_stride + query * a.out_head;
       float* const sums = split.sums + (index * split.parts + part) * kPartFloats<DP> + t * kRows * (DP + 2);
       if (!some) {
         for (int c = 0; c < D && mine && split.parts == 1; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
       const float z = (partial[0][d + e] + partial[1][d + e]) + (partial[2][d + e] + partial[3][d + e]);
       y[e] = sum == 0.f ? 0.f : z * by;
     }
-    *reinterpret_cast<uint32_t*>((uint16_t*)a.out[rank] + at_token * a.out_stride + (int64_t)query * D + d) = bf16_pair(y[0], y[1]);
+    *reinterpret_cast<uint32_t*>((uint16_t*)a.out[rank] + at_token * a.out_stride + query * a.out_head + d) = bf16_pair(y[0], y[1]);
   }
   if (threadIdx.x == 0 && a.lse[rank] != nullptr) a.lse[rank][at_token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
@@ -904,14 +904,15 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   static thread_local Maps maps;
   for (int r = 0; r < a.nranks && e == cudaSuccess; r++) {
-    e = make_map(&maps.q[r], a.q[r], D, a.q_heads, a.tokens, D * 2, a.q_stride * 2, group, per_tile);
-    if (e == cudaSuccess) e = make_map(&maps.out[r], a.out[r], D, a.q_heads, a.tokens, D * 2, a.out_stride * 2, group, per_tile);
+    e = make_map(&maps.q[r], a.q[r], D, a.q_heads, a.tokens, a.q_head * 2, a.q_stride * 2, group, per_tile);
+    if (e == cudaSuccess) e = make_map(&maps.out[r], a.out[r], D, a.q_heads, a.tokens, a.out_head * 2, a.out_stride * 2, group, per_tile);
     for (int which = 0; which < 2 && e == cudaSuccess; which++) {
       CUtensorMap* map = which == 0 ? &maps.k[r] : &maps.v[r];
       const void* base = which == 0 ? a.k[r] : a.v[r];
       const int64_t page = (int64_t)1 << a.page_shift, planes = (int64_t)a.num_pages * a.kv_heads, box = page < kKeys ? page : kKeys;
       if (FORM == kDense)
-        e = make_map(map, base, D, a.kv_heads, a.tokens, D * 2, (which == 0 ? a.k_stride : a.v_stride) * 2, 1, kKeys);
+        e = make_map(map, base, D, a.kv_heads, a.tokens, (which == 0 ? a.k_head : a.v_head) * 2,
+                     (which == 0 ? a.k_stride : a.v_stride) * 2, 1, kKeys);
       else if (FORM == kPages && DP == 128 && D == DP)
         e = make_grouped_map(map, base, D, planes * page, (int)box / 8);
       else if (FORM == kPages)

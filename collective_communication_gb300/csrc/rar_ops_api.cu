@@ -24,16 +24,24 @@ rar_status from_cuda(cudaError_t e) {
 
 bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
-// `rows` rows of `width` bytes, `stride` bytes from row to row.
+// `rows` rows of `width` bytes, `stride` bytes from row to row; of their bytes (if `every` is set) those alone that are
+// less than `part` behind the base, or behind a multiple of `every` from there.
 struct Span {
   uintptr_t base;
   int64_t rows, width, stride;
+  int64_t part = 0, every = 0;
 };
 Span span(const void* p, int64_t rows, int64_t width, int64_t stride) {
-  return Span{(uintptr_t)p, rows, width, stride};
+  return Span{(uintptr_t)p, rows, width, stride, 0, 0};
 }
-Span span(const void* p, int64_t bytes) { return Span{(uintptr_t)p, 1, bytes, bytes}; }
+Span span(const void* p, int64_t bytes) { return Span{(uintptr_t)p, 1, bytes, bytes, 0, 0}; }
 
+// Whether parts of two rows of bytes that repeat after `stride` leave each other alone, whatever their number.
+bool interleave(const Span& a, const Span& b, int64_t stride, int64_t a_width, int64_t b_width) {
+  const bool first = a.base <= b.base;
+  const int64_t d = (int64_t)((first ? b.base - a.base : a.base - b.base) % (uintptr_t)stride);
+  return d >= (first ? a_width : b_width) && stride - d >= (first ? b_width : a_width);
+}
 // Whether two spans share a byte. Spans of one stride may interleave (the ranks'
 // heads side by side in one row); spans of different strides must not meet at all.
 bool meet(const Span& a, const Span& b) {
@@ -41,12 +49,8 @@ bool meet(const Span& a, const Span& b) {
   const uintptr_t ae = a.base + (uintptr_t)((a.rows - 1) * a.stride + a.width);
   const uintptr_t be = b.base + (uintptr_t)((b.rows - 1) * b.stride + b.width);
   if (!(a.base < be && b.base < ae)) return false;
-  if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {
-    const Span& lo = a.base <= b.base ? a : b;
-    const Span& hi = a.base <= b.base ? b : a;
-    const int64_t d = (int64_t)((hi.base - lo.base) % (uintptr_t)a.stride);
-    if (d >= lo.width && a.stride - d >= hi.width) return false;
-  }
+  if (a.rows > 1 && b.rows > 1 && a.stride == b.stride && interleave(a, b, a.stride, a.width, b.width)) return false;
+  if (a.every > 0 && a.every == b.every && interleave(a, b, a.every, a.part, b.part)) return false;
   return true;
 }
 
@@ -291,22 +295,36 @@ rar_status check_prompt(int nranks, int64_t tokens, int q_heads, int kv_heads, i
   s->read(span(starts, sequences > 0 ? ((int64_t)sequences + 1) * 4 : 0));
   return RAR_OK;
 }
-// Rows [tokens, heads, head_dim] of each rank.
-rar_status check_rows(const void* const* p, int nranks, int64_t tokens, int64_t width, int64_t stride, int64_t es, bool out,
-                      Spans* s) {
-  rar_status st = check_pointers(p, nranks, tokens, 16);
-  if (st != RAR_OK || (st = check_stride(stride, width, tokens, es)) != RAR_OK) return st;
-  for (int r = 0; r < nranks; r++) {
-    const Span x = span(p[r], tokens, width * es, stride * es);
-    if (out) s->write(x);
-    else s->read(x);
+// Rows [tokens, heads, head_dim] of each rank: elements from token to token, and from head to head.
+struct Rows {
+  const void* const* data;
+  int64_t stride, head;
+};
+// A token's heads may lie within its row, or the tokens within a head's; either way no two rows of head_dim share an element.
+rar_status check_rows(const Rows& x, int nranks, int64_t tokens, int heads, int head_dim, int64_t es, bool out, Spans* s) {
+  rar_status st = check_pointers(x.data, nranks, tokens, 16);
+  if (st != RAR_OK) return st;
+  const int64_t most = INT64_MAX / 32, D = head_dim;
+  if (x.stride < 0 || x.head < 0 || x.stride > most / (tokens > 0 ? tokens : 1) || x.head > most / heads) return RAR_ERR_ARG;
+  const int64_t of_token = (heads - 1) * x.head + D, of_head = (tokens - 1) * x.stride + D;  // a row's elements, with gaps
+  const bool by_token = (heads < 2 || x.head >= D) && (tokens < 2 || x.stride >= of_token);
+  const bool by_head = heads > 1 && tokens > 1 && x.stride >= D && x.head >= of_head;
+  if (!by_token && !by_head) return RAR_ERR_ARG;
+  if (x.stride * es % 16 != 0 || x.head * es % 16 != 0) return RAR_ERR_ALIGN;
+  for (int r = 0; r < nranks && tokens > 0; r++) {
+    Span y = by_token ? span(x.data[r], tokens, of_token * es, x.stride * es) : span(x.data[r], heads, of_head * es, x.head * es);
+    // a head's rows of other tensors may lie between these
+    if (by_token && heads > 1 && (tokens < 2 || x.stride % x.head == 0)) y.part = D * es, y.every = x.head * es;
+    if (!by_token && x.head % x.stride == 0) y.part = D * es, y.every = x.stride * es;
+    if (out) s->write(y);
+    else s->read(y);
   }
   return RAR_OK;
 }
 
-rar_status prompt_forward(PromptArgs& a, void* const* out, float* const* lse, size_t ws_bytes, Spans& s, void* stream) {
-  const int64_t es = a.dtype == RAR_F32 ? 4 : 2, width = (int64_t)a.q_heads * a.head_dim;
-  rar_status st = check_rows((const void* const*)out, a.nranks, a.tokens, width, a.out_stride, es, true, &s);
+rar_status prompt_forward(PromptArgs& a, void* const* out, float* const* lse, size_t ws_bytes, Spans& s) {
+  const Rows rows = {(const void* const*)out, a.out_stride, a.out_head};
+  rar_status st = check_rows(rows, a.nranks, a.tokens, a.q_heads, a.head_dim, size_of((rar_dtype)a.dtype), true, &s);
   if (st != RAR_OK) return st;
   if (lse != nullptr) {
     if ((st = check_pointers((const void* const*)lse, a.nranks, a.tokens, 4)) != RAR_OK) return st;
@@ -716,18 +734,19 @@ size_t rar_prompt_attention_workspace_bytes(int nranks, int64_t tokens, int q_he
   return (size_t)(kOpScratchOffset + prompt_attention_scratch_bytes(nranks, tokens, q_heads, kv_heads, head_dim));
 }
 
-rar_status rar_prompt_attention(const void* const* q, int64_t q_stride, const void* const* k, int64_t k_stride,
-                                const void* const* v, int64_t v_stride, int nranks, int64_t tokens, int q_heads,
-                                int kv_heads, int head_dim, rar_dtype dtype, const int32_t* starts, int num_sequences,
-                                float scale, void* const* out, int64_t out_stride, float* const* lse, void* workspace,
-                                size_t workspaceBytes, void* stream) {
+rar_status rar_prompt_attention_ex(const void* const* q, int64_t q_stride, int64_t q_head_stride, const void* const* k,
+                                   int64_t k_stride, int64_t k_head_stride, const void* const* v, int64_t v_stride,
+                                   int64_t v_head_stride, int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim,
+                                   rar_dtype dtype, const int32_t* starts, int num_sequences, float scale, void* const* out,
+                                   int64_t out_stride, int64_t out_head_stride, float* const* lse, void* workspace,
+                                   size_t workspaceBytes, void* stream) {
   Spans s;
   rar_status st = check_prompt(nranks, tokens, q_heads, kv_heads, head_dim, dtype, starts, num_sequences, &s);
   if (st != RAR_OK) return st;
-  const int64_t es = size_of(dtype), D = head_dim;
-  if ((st = check_rows(q, nranks, tokens, q_heads * D, q_stride, es, false, &s)) != RAR_OK ||
-      (st = check_rows(k, nranks, tokens, kv_heads * D, k_stride, es, false, &s)) != RAR_OK ||
-      (st = check_rows(v, nranks, tokens, kv_heads * D, v_stride, es, false, &s)) != RAR_OK)
+  const int64_t es = size_of(dtype);
+  if ((st = check_rows({q, q_stride, q_head_stride}, nranks, tokens, q_heads, head_dim, es, false, &s)) != RAR_OK ||
+      (st = check_rows({k, k_stride, k_head_stride}, nranks, tokens, kv_heads, head_dim, es, false, &s)) != RAR_OK ||
+      (st = check_rows({v, v_stride, v_head_stride}, nranks, tokens, kv_heads, head_dim, es, false, &s)) != RAR_OK)
     return st;
   PromptArgs a;
   std::memset(&a, 0, sizeof a);
@@ -742,6 +761,10 @@ rar_status rar_prompt_attention(const void* const* q, int64_t q_stride, const vo
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   a.out_stride = out_stride;
+  a.q_head = q_head_stride;
+  a.k_head = k_head_stride;
+  a.v_head = v_head_stride;
+  a.out_head = out_head_stride;
   a.scale = scale;
   a.nranks = nranks;
   a.dtype = (int)dtype;
@@ -750,17 +773,27 @@ rar_status rar_prompt_attention(const void* const* q, int64_t q_stride, const vo
   a.q_heads = q_heads;
   a.kv_heads = kv_heads;
   a.head_dim = head_dim;
-  if ((st = prompt_forward(a, out, lse, workspaceBytes, s, stream)) != RAR_OK || tokens == 0 || num_sequences == 0) return st;
+  if ((st = prompt_forward(a, out, lse, workspaceBytes, s)) != RAR_OK || tokens == 0 || num_sequences == 0) return st;
   return from_cuda(launch_prompt_attention(a, (cudaStream_t)stream));
 }
 
-rar_status rar_prompt_attention_cached(const void* const* q, int64_t q_stride, const void* const* k_cache,
-                                       const void* const* v_cache, int nranks, int64_t tokens, int q_heads, int kv_heads,
-                                       int head_dim, rar_dtype dtype, int num_pages, int page_size,
-                                       const int32_t* block_table, int64_t table_stride, int max_blocks,
-                                       const int32_t* starts, const int32_t* lens, int num_sequences, float scale,
-                                       void* const* out, int64_t out_stride, float* const* lse, void* workspace,
-                                       size_t workspaceBytes, void* stream) {
+rar_status rar_prompt_attention(const void* const* q, int64_t q_stride, const void* const* k, int64_t k_stride,
+                                const void* const* v, int64_t v_stride, int nranks, int64_t tokens, int q_heads,
+                                int kv_heads, int head_dim, rar_dtype dtype, const int32_t* starts, int num_sequences,
+                                float scale, void* const* out, int64_t out_stride, float* const* lse, void* workspace,
+                                size_t workspaceBytes, void* stream) {
+  return rar_prompt_attention_ex(q, q_stride, head_dim, k, k_stride, head_dim, v, v_stride, head_dim, nranks, tokens, q_heads,
+                                 kv_heads, head_dim, dtype, starts, num_sequences, scale, out, out_stride, head_dim, lse,
+                                 workspace, workspaceBytes, stream);
+}
+
+rar_status rar_prompt_attention_cached_ex(const void* const* q, int64_t q_stride, int64_t q_head_stride,
+                                          const void* const* k_cache, const void* const* v_cache, int nranks, int64_t tokens,
+                                          int q_heads, int kv_heads, int head_dim, rar_dtype dtype, int num_pages,
+                                          int page_size, const int32_t* block_table, int64_t table_stride, int max_blocks,
+                                          const int32_t* starts, const int32_t* lens, int num_sequences, float scale,
+                                          void* const* out, int64_t out_stride, int64_t out_head_stride, float* const* lse,
+                                          void* workspace, size_t workspaceBytes, void* stream) {
   Spans s;
   rar_status st = check_prompt(nranks, tokens, q_heads, kv_heads, head_dim, dtype, starts, num_sequences, &s);
   if (st != RAR_OK) return st;
@@ -770,7 +803,7 @@ rar_status rar_prompt_attention_cached(const void* const* q, int64_t q_stride, c
     return RAR_ERR_ARG;
   if ((n > 1 && table_stride < max_blocks) || table_stride < 0 || table_stride > INT64_MAX / 8 / (n > 0 ? n : 1))
     return RAR_ERR_ARG;
-  if ((st = check_rows(q, nranks, tokens, q_heads * D, q_stride, es, false, &s)) != RAR_OK ||
+  if ((st = check_rows({q, q_stride, q_head_stride}, nranks, tokens, q_heads, head_dim, es, false, &s)) != RAR_OK ||
       (st = check_pointers(k_cache, nranks, tokens, 16)) != RAR_OK ||
       (st = check_pointers(v_cache, nranks, tokens, 16)) != RAR_OK)
     return st;
@@ -794,6 +827,8 @@ rar_status rar_prompt_attention_cached(const void* const* q, int64_t q_stride, c
   a.ws = (char*)workspace;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
+  a.q_head = q_head_stride;
+  a.out_head = out_head_stride;
   a.table_stride = table_stride;
   a.scale = scale;
   a.nranks = nranks;
@@ -806,32 +841,44 @@ rar_status rar_prompt_attention_cached(const void* const* q, int64_t q_stride, c
   a.page_shift = shift;
   a.num_pages = num_pages;
   a.max_blocks = max_blocks;
-  if ((st = prompt_forward(a, out, lse, workspaceBytes, s, stream)) != RAR_OK || tokens == 0 || n == 0) return st;
+  if ((st = prompt_forward(a, out, lse, workspaceBytes, s)) != RAR_OK || tokens == 0 || n == 0) return st;
   return from_cuda(launch_prompt_attention(a, (cudaStream_t)stream));
 }
 
-rar_status rar_prompt_attention_backward(const void* const* q, int64_t q_stride, const void* const* k, int64_t k_stride,
-                                         const void* const* v, int64_t v_stride, int nranks, int64_t tokens, int q_heads,
-                                         int kv_heads, int head_dim, rar_dtype dtype, const int32_t* starts,
-                                         int num_sequences, float scale, const void* const* out, int64_t out_stride,
-                                         const float* const* lse, const void* const* dout, int64_t dout_stride,
-                                         void* const* dq, int64_t dq_stride, void* const* dk, int64_t dk_stride,
-                                         void* const* dv, int64_t dv_stride, void* workspace, size_t workspaceBytes,
-                                         void* stream) {
+rar_status rar_prompt_attention_cached(const void* const* q, int64_t q_stride, const void* const* k_cache,
+                                       const void* const* v_cache, int nranks, int64_t tokens, int q_heads, int kv_heads,
+                                       int head_dim, rar_dtype dtype, int num_pages, int page_size,
+                                       const int32_t* block_table, int64_t table_stride, int max_blocks,
+                                       const int32_t* starts, const int32_t* lens, int num_sequences, float scale,
+                                       void* const* out, int64_t out_stride, float* const* lse, void* workspace,
+                                       size_t workspaceBytes, void* stream) {
+  return rar_prompt_attention_cached_ex(q, q_stride, head_dim, k_cache, v_cache, nranks, tokens, q_heads, kv_heads, head_dim,
+                                        dtype, num_pages, page_size, block_table, table_stride, max_blocks, starts, lens,
+                                        num_sequences, scale, out, out_stride, head_dim, lse, workspace, workspaceBytes, stream);
+}
+
+rar_status rar_prompt_attention_backward_ex(const void* const* q, int64_t q_stride, int64_t q_head_stride,
+                                            const void* const* k, int64_t k_stride, int64_t k_head_stride,
+                                            const void* const* v, int64_t v_stride, int64_t v_head_stride, int nranks,
+                                            int64_t tokens, int q_heads, int kv_heads, int head_dim, rar_dtype dtype,
+                                            const int32_t* starts, int num_sequences, float scale, const void* const* out,
+                                            int64_t out_stride, int64_t out_head_stride, const float* const* lse,
+                                            const void* const* dout, int64_t dout_stride, int64_t dout_head_stride,
+                                            void* const* dq, int64_t dq_stride, int64_t dq_head_stride, void* const* dk,
+                                            int64_t dk_stride, int64_t dk_head_stride, void* const* dv, int64_t dv_stride,
+                                            int64_t dv_head_stride, void* workspace, size_t workspaceBytes, void* stream) {
   Spans s;
   rar_status st = check_prompt(nranks, tokens, q_heads, kv_heads, head_dim, dtype, starts, num_sequences, &s);
   if (st != RAR_OK) return st;
-  const int64_t es = size_of(dtype), D = head_dim, qw = q_heads * D, kw = kv_heads * D;
-  if ((st = check_rows(q, nranks, tokens, qw, q_stride, es, false, &s)) != RAR_OK ||
-      (st = check_rows(k, nranks, tokens, kw, k_stride, es, false, &s)) != RAR_OK ||
-      (st = check_rows(v, nranks, tokens, kw, v_stride, es, false, &s)) != RAR_OK ||
-      (st = check_rows(out, nranks, tokens, qw, out_stride, es, false, &s)) != RAR_OK ||
-      (st = check_rows(dout, nranks, tokens, qw, dout_stride, es, false, &s)) != RAR_OK ||
-      (st = check_rows((const void* const*)dq, nranks, tokens, qw, dq_stride, es, true, &s)) != RAR_OK ||
-      (st = check_rows((const void* const*)dk, nranks, tokens, kw, dk_stride, es, true, &s)) != RAR_OK ||
-      (st = check_rows((const void* const*)dv, nranks, tokens, kw, dv_stride, es, true, &s)) != RAR_OK ||
-      (st = check_pointers((const void* const*)lse, nranks, tokens, 4)) != RAR_OK)
-    return st;
+  const Rows of_queries[] = {{q, q_stride, q_head_stride}, {out, out_stride, out_head_stride}, {dout, dout_stride, dout_head_stride},
+                             {(const void* const*)dq, dq_stride, dq_head_stride}};
+  const Rows of_keys[] = {{k, k_stride, k_head_stride}, {v, v_stride, v_head_stride},
+                          {(const void* const*)dk, dk_stride, dk_head_stride}, {(const void* const*)dv, dv_stride, dv_head_stride}};
+  for (int i = 0; i < 4; i++)
+    if ((st = check_rows(of_queries[i], nranks, tokens, q_heads, head_dim, size_of(dtype), i == 3, &s)) != RAR_OK ||
+        (st = check_rows(of_keys[i], nranks, tokens, kv_heads, head_dim, size_of(dtype), i >= 2, &s)) != RAR_OK)
+      return st;
+  if ((st = check_pointers((const void* const*)lse, nranks, tokens, 4)) != RAR_OK) return st;
   PromptBwdArgs a;
   std::memset(&a, 0, sizeof a);
   for (int r = 0; r < nranks; r++) {
@@ -862,6 +909,14 @@ rar_status rar_prompt_attention_backward(const void* const* q, int64_t q_stride,
   a.dq_stride = dq_stride;
   a.dk_stride = dk_stride;
   a.dv_stride = dv_stride;
+  a.q_head = q_head_stride;
+  a.k_head = k_head_stride;
+  a.v_head = v_head_stride;
+  a.out_head = out_head_stride;
+  a.dout_head = dout_head_stride;
+  a.dq_head = dq_head_stride;
+  a.dk_head = dk_head_stride;
+  a.dv_head = dv_head_stride;
   a.scale = scale;
   a.nranks = nranks;
   a.dtype = (int)dtype;
@@ -871,6 +926,20 @@ rar_status rar_prompt_attention_backward(const void* const* q, int64_t q_stride,
   a.kv_heads = kv_heads;
   a.head_dim = head_dim;
   return from_cuda(launch_prompt_attention_bwd(a, (cudaStream_t)stream));
+}
+
+rar_status rar_prompt_attention_backward(const void* const* q, int64_t q_stride, const void* const* k, int64_t k_stride,
+                                         const void* const* v, int64_t v_stride, int nranks, int64_t tokens, int q_heads,
+                                         int kv_heads, int head_dim, rar_dtype dtype, const int32_t* starts,
+                                         int num_sequences, float scale, const void* const* out, int64_t out_stride,
+                                         const float* const* lse, const void* const* dout, int64_t dout_stride,
+                                         void* const* dq, int64_t dq_stride, void* const* dk, int64_t dk_stride,
+                                         void* const* dv, int64_t dv_stride, void* workspace, size_t workspaceBytes,
+                                         void* stream) {
+  return rar_prompt_attention_backward_ex(q, q_stride, head_dim, k, k_stride, head_dim, v, v_stride, head_dim, nranks, tokens,
+                                          q_heads, kv_heads, head_dim, dtype, starts, num_sequences, scale, out, out_stride,
+                                          head_dim, lse, dout, dout_stride, head_dim, dq, dq_stride, head_dim, dk, dk_stride,
+                                          head_dim, dv, dv_stride, head_dim, workspace, workspaceBytes, stream);
 }
 
 rar_status rar_embed_tokens(const int32_t* tokens, int64_t num_tokens, const void* const* tables, const int64_t* vocab,

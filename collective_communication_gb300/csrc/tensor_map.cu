@@ -30,8 +30,9 @@ cudaError_t encode(CUtensorMap* map, const void* base, int rank, const cuuint64_
 cudaError_t make_map(CUtensorMap* map, const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t stride1_bytes,
                      int64_t stride2_bytes, int rows, int planes) {
   const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-  // a single plane's stride means nothing: any valid one will do
-  const cuuint64_t strides[2] = {(cuuint64_t)stride1_bytes, (cuuint64_t)(d2 > 1 ? stride2_bytes : stride1_bytes * d1)};
+  // a single row's or plane's stride means nothing: any valid one will do
+  const cuuint64_t row = (cuuint64_t)(d1 > 1 ? stride1_bytes : d0 * 2);
+  const cuuint64_t strides[2] = {row, d2 > 1 ? (cuuint64_t)stride2_bytes : row};
   const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)planes};
   return encode(map, base, 3, dims, strides, box);
 }

@@ -638,6 +638,43 @@ RAR_API rar_status rar_prompt_attention_backward(const void* const* q, int64_t q
                                                  int64_t dv_stride, void* workspace, size_t workspaceBytes, void* stream);
 
 /*
+ * The same with rows of heads at any distance: each *_head_stride is that from a head to
+ * the next one of the same token, in elements, as each *_stride is that from a token to the
+ * next one of the same head (the calls above: head_dim). Heads lie within their token's
+ * row ([tokens, heads, head_dim], gaps allowed) or tokens within their head's ([heads,
+ * tokens, head_dim]); both distances are multiples of 16 bytes. Results do not depend on it.
+ */
+RAR_API rar_status rar_prompt_attention_ex(const void* const* q, int64_t q_stride, int64_t q_head_stride,
+                                           const void* const* k, int64_t k_stride, int64_t k_head_stride,
+                                           const void* const* v, int64_t v_stride, int64_t v_head_stride, int nranks,
+                                           int64_t tokens, int q_heads, int kv_heads, int head_dim, rar_dtype dtype,
+                                           const int32_t* starts, int num_sequences, float scale, void* const* out,
+                                           int64_t out_stride, int64_t out_head_stride, float* const* lse,
+                                           void* workspace, size_t workspaceBytes, void* stream);
+RAR_API rar_status rar_prompt_attention_cached_ex(const void* const* q, int64_t q_stride, int64_t q_head_stride,
+                                                  const void* const* k_cache, const void* const* v_cache, int nranks,
+                                                  int64_t tokens, int q_heads, int kv_heads, int head_dim,
+                                                  rar_dtype dtype, int num_pages, int page_size,
+                                                  const int32_t* block_table, int64_t table_stride, int max_blocks,
+                                                  const int32_t* starts, const int32_t* lens, int num_sequences,
+                                                  float scale, void* const* out, int64_t out_stride,
+                                                  int64_t out_head_stride, float* const* lse, void* workspace,
+                                                  size_t workspaceBytes, void* stream);
+RAR_API rar_status rar_prompt_attention_backward_ex(const void* const* q, int64_t q_stride, int64_t q_head_stride,
+                                                    const void* const* k, int64_t k_stride, int64_t k_head_stride,
+                                                    const void* const* v, int64_t v_stride, int64_t v_head_stride,
+                                                    int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim,
+                                                    rar_dtype dtype, const int32_t* starts, int num_sequences,
+                                                    float scale, const void* const* out, int64_t out_stride,
+                                                    int64_t out_head_stride, const float* const* lse,
+                                                    const void* const* dout, int64_t dout_stride,
+                                                    int64_t dout_head_stride, void* const* dq, int64_t dq_stride,
+                                                    int64_t dq_head_stride, void* const* dk, int64_t dk_stride,
+                                                    int64_t dk_head_stride, void* const* dv, int64_t dv_stride,
+                                                    int64_t dv_head_stride, void* workspace, size_t workspaceBytes,
+                                                    void* stream);
+
+/*
  * Embedding lookup over vocabulary shards that are never gathered: rank r holds the
  * rows of vocab[r] words, tables[r] [vocab[r], hidden], rows row_strides[r] apart (host
  * arrays); row j of rank r is word vocab[0] + .. + vocab[r-1] + j.

@@ -1,0 +1,93 @@
+"""GPU tests of what the prompt operators do at their edges: tensors laid out in other ways."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from collective_communication_gb300 import binding as B
+from test_gpu_prompt_operators import (DT, MARK, backward, cached_forward, forward, gen, i32, normal, paged, prompt_inputs,
+                                       starts_of, workspace)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.load_library()
+    yield
+
+
+# ---------------------------------------------------------------- layouts
+def by_head(x):
+    """A copy whose heads are apart by all tokens and 16 elements more, with marks between them."""
+    n, t, h, d = x.shape
+    buffer = torch.full((n, h, t * d + 16), MARK, dtype=x.dtype, device="cuda")
+    view = buffer[:, :, :t * d].unflatten(2, (t, d)).transpose(1, 2)
+    view.copy_(x)
+    return view, buffer[:, :, t * d:]
+
+
+def apart(x):
+    """A copy with 8 elements more behind each head, and 24 behind each token."""
+    n, t, h, d = x.shape
+    buffer = torch.full((n, t, h * (d + 8) + 24), MARK, dtype=x.dtype, device="cuda")
+    view = buffer[:, :, :h * (d + 8)].unflatten(2, (h, d + 8))
+    view[..., :d].copy_(x)
+    return view[..., :d], torch.cat([view[..., d:].flatten(), buffer[:, :, h * (d + 8):].flatten()])
+
+
+LAYOUTS = [
+    ([97], 8, 1, 128, "bf16"), ([300, 0, 41], 6, 2, 64, "bf16"), ([1], 4, 2, 64, "bf16"), ([1], 4, 2, 64, "f32"), ([1100, 30], 16, 2, 128, "bf16"),
+    ([140, 5], 6, 3, 80, "bf16"), ([60], 4, 2, 192, "bf16"), ([140, 5], 6, 3, 80, "f32"), ([600], 16, 2, 64, "f32"), ([33, 2], 5, 5, 40, "bf16"),
+]
+
+
+@pytest.mark.parametrize("layout", [by_head, apart])
+@pytest.mark.parametrize("lens,heads,kv,dim,dtype", LAYOUTS, ids=str)
+def test_layouts_change_nothing(lens, heads, kv, dim, dtype, layout):
+    """Heads of any distance give the same bits as dense ones, and what lies between rows is left as it was."""
+    q, k, v, starts = prompt_inputs(2, lens, heads, kv, dim, dtype, behind=2)
+    out, lse = forward(q, k, v, starts)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    want = [out, *backward(q, k, v, starts, out, lse, dout)]
+    q, k, v, dout = (layout(x)[0] for x in (q, k, v, dout))
+    (out, g0), (dq, g1), (dk, g2), (dv, g3) = (layout(torch.full_like(x, MARK)) for x in want)
+    ws = workspace(q, kv)
+    again = torch.full_like(lse, MARK)
+    B.prompt_attention(q, k, v, starts, out, again, ws)
+    B.prompt_attention_backward(q, k, v, starts, out, lse, dout, dq, dk, dv, ws)
+    assert B.get_status(ws) == B.Status.OK and torch.equal(again, lse)
+    for got, w in zip((out, dq, dk, dv), want):
+        assert torch.equal(got, w)
+    assert all(bool((g == MARK).all()) for g in (g0, g1, g2, g3))
+
+
+@pytest.mark.parametrize("layout", [by_head, apart])
+@pytest.mark.parametrize("new,lens,heads,kv,dim,page,dtype", [
+    ([5], [3000], 16, 2, 128, 64, "bf16"), ([40, 130], [300, 400], 6, 2, 80, 16, "bf16"), ([3, 9], [60, 500], 4, 2, 64, 2, "bf16"),
+    ([4], [900], 4, 2, 64, 16, "f32"), ([1], [500], 4, 1, 192, 32, "bf16")], ids=str)
+def test_cached_layouts_change_nothing(new, lens, heads, kv, dim, page, dtype, layout):
+    g = gen(3)
+    k, v, table, _, _ = paged(g, 2, lens, kv, dim, page, DT[dtype])
+    q = normal(g, 2, sum(new) + 1, heads, dim, dtype=DT[dtype])
+    starts, lens = starts_of(new), i32(*lens)
+    want, want_lse = cached_forward(q, k, v, table, starts, lens)
+    q = layout(q)[0]
+    out, gaps = layout(torch.full_like(want, MARK))
+    lse, ws = torch.full_like(want_lse, MARK), workspace(q, kv)
+    B.prompt_attention_cached(q, k, v, table, starts, lens, out, lse, ws)
+    assert B.get_status(ws) == B.Status.OK
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and bool((gaps == MARK).all())
+
+
+def test_forward_result_of_torch():
+    """The gradient takes out as a product of heads leaves it, turned back to tokens, and tensors of different layouts."""
+    q, k, v, starts = prompt_inputs(2, [150], 4, 2, 64, "bf16")
+    out, lse = forward(q, k, v, starts)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    want = backward(q, k, v, starts, out, lse, dout)
+    turned = out.transpose(1, 2).contiguous().transpose(1, 2)
+    assert not turned.is_contiguous()
+    for a, b in zip(want, backward(q, by_head(k)[0], v, starts, turned, lse, apart(dout)[0])):
+        assert torch.equal(a, b)
