@@ -811,7 +811,7 @@ int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, 
   int64_t parts = 0;
   if ((group / rows + 1) * lanes * 2 <= kPromptParts) parts = kPromptParts * rows * (padded + 2) * 4;
   if (tensor && lanes * 2 <= kPromptSplitBlocks) {
-    const int64_t more = (int64_t)kPromptSplitBlocks * (256 * ((head_dim <= 64 ? 64 : 128) + 2) + kPromptPartInfo) * 4;
+    const int64_t more = (int64_t)kPromptSplitBlocks * 256 * ((head_dim <= 64 ? 64 : 128) + 2) * 4;
     parts = more > parts ? more : parts;
   }
   // what parts of the rows leave of dk and dv

@@ -29,6 +29,8 @@ struct PromptArgs {
   int64_t q_head, k_head, v_head, out_head;  // elements from head to head of a token
   float scale;
   int nranks, dtype, tokens, sequences, q_heads, kv_heads, head_dim, page_shift, num_pages, max_blocks;
+  uint64_t wait_ns;  // limit of a wait inside a block
+  int fault;
 };
 
 struct PromptBwdArgs {
@@ -47,6 +49,8 @@ struct PromptBwdArgs {
   int64_t q_head, k_head, v_head, out_head, dout_head, dq_head, dk_head, dv_head;
   float scale;
   int nranks, dtype, tokens, sequences, q_heads, kv_heads, head_dim;
+  uint64_t wait_ns;  // limit of a wait inside a block
+  int fault;
 };
 
 // The rows that see a tile of keys may be split into parts, which then leave their sums:
@@ -86,7 +90,6 @@ cudaError_t launch_prompt_attention_tc(const PromptArgs& a, cudaStream_t stream)
 cudaError_t launch_prompt_attention_bwd_tc(const PromptBwdArgs& a, cudaStream_t stream);
 constexpr int kPromptSplitBlocks = 152;  // blocks among which few tiles' keys are split: the SMs
 constexpr int kPromptParts = 304;        // the same in the form on the ordinary arithmetic units: two blocks an SM
-constexpr int kPromptPartInfo = 32;      // numbers behind a part's sums
 cudaError_t launch_prompt_attention_bwd(const PromptBwdArgs& a, cudaStream_t stream);
 int64_t prompt_attention_scratch_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads, int head_dim);
 

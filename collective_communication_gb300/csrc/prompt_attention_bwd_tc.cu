@@ -41,8 +41,6 @@
 // where an SM has 20 on average. Queries of the next item ahead in a buffer of their own,
 // for fewer tiles of keys and values, took as long, and 800 us where this takes 715 (8192
 // tokens, 16 query heads on 2 key heads of 128).
-#include <cstdio>
-
 #include "prompt_attention.cuh"
 #include "rar_launch.h"
 #include "tensor_core.cuh"
@@ -117,7 +115,7 @@ __device__ __forceinline__ int find_item(const PromptBwdArgs& a, const Work& wor
 // The warp that finds items for the others, from those with the most work on: rows that
 // see many keys, or keys that many rows see.
 __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& work, bool by_keys, uint32_t magic,
-                                            Item* items, uint64_t* full, uint64_t* empty, volatile int* dead) {
+                                            Item* items, uint64_t* full, uint64_t* empty, volatile Limit* limit) {
   const int lane = threadIdx.x & 31;
   uint32_t* const counters = reinterpret_cast<uint32_t*>(a.ws + kHeaderBytes);
   const uint32_t all = (uint32_t)(work.slots * work.split.parts * a.kv_heads * a.nranks);
@@ -132,7 +130,7 @@ __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& 
     const int found = n < all ? find_item(a, work, order, ordered, by_keys, n, &item) : -1;
     if (found < 0) item.there = 0;
     if (found != 0) {
-      if (!wait_warp(&empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, dead)) break;
+      if (!wait_warp(&empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, limit)) break;
       if (lane == 0) {
         items[i % kItemSlots] = item;
         arrive(&full[i % kItemSlots]);
@@ -155,8 +153,8 @@ __device__ __forceinline__ void serve_items(const PromptBwdArgs& a, const Work& 
 struct Taken {
   int rank, head, sequence, length, from, count, part;
 };
-__device__ __forceinline__ bool take_item(int i, const Item* items, uint64_t* full, uint64_t* empty, volatile int* dead, Taken* t) {
-  if (!wait_warp(&full[i % kItemSlots], i / kItemSlots & 1, dead)) return false;
+__device__ __forceinline__ bool take_item(int i, const Item* items, uint64_t* full, uint64_t* empty, volatile Limit* limit, Taken* t) {
+  if (!wait_warp(&full[i % kItemSlots], i / kItemSlots & 1, limit)) return false;
   const Item& item = items[i % kItemSlots];
   const int there = uniform(item.there);
   if (there) {
@@ -218,7 +216,6 @@ struct Quarter {
 
 // What the bf16 pair `to` leaves of x and y, as another.
 __device__ __forceinline__ uint32_t bf16_rest(float x, float y, uint32_t to) { return bf16_pair(x - bf16_lo(to), y - bf16_hi(to)); }
-__device__ __forceinline__ void weights_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWeightWarps) : "memory"); }
 // One arrival of the warp, after its lanes' stores to tensor memory.
 __device__ __forceinline__ void arrive_warp(uint64_t* b) {
   stores_done();
@@ -227,11 +224,11 @@ __device__ __forceinline__ void arrive_warp(uint64_t* b) {
   if ((threadIdx.x & 31) == 0) arrive(b);
 }
 
-__device__ __forceinline__ void end_block(char* ws, volatile int* dead, int warp) {
+__device__ __forceinline__ void end_block(char* ws, volatile Limit* limit, int warp) {
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (*dead) {
+  if (limit->dead) {
     // a wait ran out: copies and products that are still under way have ended by the time this has passed
     const uint64_t until = global_timer_ns() + 10000000ull;
     while (global_timer_ns() < until) {}
@@ -295,15 +292,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + (1024 - (shared_address(raw) & 1023));
   __shared__ uint64_t q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], dp_full, ds_ready, dq_full, dq_free,
+      sums_half, sums_full,
       item_full[kItemSlots], item_empty[kItemSlots];
   __shared__ Item items[kItemSlots];
   __shared__ uint32_t tmem_at;
-  __shared__ int dead_flag;
+  __shared__ Limit limit_at;
+  volatile Limit* const limit = &limit_at;
   __shared__ float sums[2][kTile];
-  volatile int* const dead = &dead_flag;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    dead_flag = 0;
+    limit->dead = 0;
+    limit->ns = a.wait_ns;
     barrier_init(&q_full, 1);
     barrier_init(&q_empty, 1);
     for (int i = 0; i < KS; i++) {
@@ -318,6 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
     barrier_init(&ds_ready, kWeightWarps);
     barrier_init(&dq_full, 1);
     barrier_init(&dq_free, kWeightWarps);
+    barrier_init(&sums_half, kWeightWarps / 2);
+    barrier_init(&sums_full, kWeightWarps / 2);
     for (int i = 0; i < kItemSlots; i++) {
       barrier_init(&item_full[i], 1);
       barrier_init(&item_empty[i], kWeightWarps + 2);
@@ -333,32 +334,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   const int group = a.q_heads / a.kv_heads, D = a.head_dim, per_tile = kTile / group, steps = (D + 15) / 16;
 
   if (warp == kItemWarp) {
-    serve_items(a, work, false, magic, items, item_full, item_empty, dead);
+    serve_items(a, work, false, magic, items, item_full, item_empty, limit);
   } else if (warp == kNumbersWarp) {
     if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws, lane, 32);
   } else if (warp == kCopyWarp) {
     int n = 0;  // tiles of keys so far
     for (int i = 0;; i++) {
       Taken t;
-      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      if (!take_item(i, items, item_full, item_empty, limit, &t)) break;
       const int tiles = (t.from + t.count + kTile - 1) / kTile;
       bool fine = true;
       for (int j = 0; j < tiles && fine; j++, n++) {
         const int k = n % KS, v = n % VS;
-        if (!(fine = wait_warp(&k_empty[k], (n / KS & 1) ^ 1, dead))) break;
+        if (!(fine = wait_warp(&k_empty[k], (n / KS & 1) ^ 1, limit))) break;
         if (lane == 0) {
           arrive_expect(&k_full[k], L::kBytes);
           for (int h = 0; h < DP / 64; h++)
             copy_3d(k_ring + k * L::kBytes + h * L::kSlab, &maps.k[t.rank], h * 64, t.head, t.sequence + j * kTile, &k_full[k]);
         }
-        if (!(fine = wait_warp(&v_empty[v], (n / VS & 1) ^ 1, dead))) break;
+        if (!(fine = wait_warp(&v_empty[v], (n / VS & 1) ^ 1, limit))) break;
         if (lane == 0) {
           arrive_expect(&v_full[v], L::kBytes);
           for (int h = 0; h < DP / 64; h++)
             copy_3d(v_ring + v * L::kBytes + h * L::kSlab, &maps.v[t.rank], h * 64, t.head, t.sequence + j * kTile, &v_full[v]);
         }
         if (j == 0) {
-          if (!(fine = wait_warp(&q_empty, (i & 1) ^ 1, dead))) break;
+          if (!(fine = wait_warp(&q_empty, (i & 1) ^ 1, limit))) break;
           if (lane == 0) {
             arrive_expect(&q_full, (uint32_t)(2 * per_tile * group * 128 * (DP / 64)));
             for (int h = 0; h < DP / 64; h++) {
@@ -377,11 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
     int base = 0;  // tiles of keys of the items before
     for (int i = 0;; i++) {
       Taken t;
-      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      if (!take_item(i, items, item_full, item_empty, limit, &t)) break;
       const int tiles = (t.from + t.count + kTile - 1) / kTile;
       auto score = [&](int j) {  // S of key tile j; keys that are none are 0, for the product with dS
         const int n = base + j, stage = n % KS;
-        if (!wait_warp(&k_full[stage], n / KS & 1, dead)) return false;
+        if (!wait_warp(&k_full[stage], n / KS & 1, limit)) return false;
         if (t.length - j * kTile < kTile) {
           clear_rows<DP>(k_ring + stage * L::kBytes, t.length - j * kTile);
           stores_to_products();
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
       };
       auto value = [&](int j) {  // dO V^T
         const int n = base + j, stage = n % VS;
-        if (!wait_warp(&v_full[stage], n / VS & 1, dead)) return false;
+        if (!wait_warp(&v_full[stage], n / VS & 1, limit)) return false;
         fence_after();
         rows_by_rows<DP / 16, L::kSlab>(lead, dp_at, g_at, v_at + stage * L::kBytes, kTile, steps);
         commit(lead, &dp_full);
@@ -401,13 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         if (j + 1 == tiles) commit(lead, &q_empty);
         return true;
       };
-      bool fine = wait_warp(&q_full, i & 1, dead) && score(0) && value(0);
+      bool fine = wait_warp(&q_full, i & 1, limit) && score(0) && value(0);
       for (int j = 0; j < tiles && fine; j++) {
         const int n = base + j;
         const bool more = j + 1 < tiles;
         if (more && !(fine = score(j + 1))) break;
-        if (j == 0 && i > 0 && !(fine = wait_warp(&dq_free, (i - 1) & 1, dead))) break;  // dQ of the item before has been read
-        if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
+        if (j == 0 && i > 0 && !(fine = wait_warp(&dq_free, (i - 1) & 1, limit))) break;  // dQ of the item before has been read
+        if (!(fine = wait_warp(&ds_ready, n & 1, limit))) break;
         fence_after();
         if (more && !(fine = value(j + 1))) break;
         weights_by_rows<2, kColumns>(lead, dq_at, s_at + (n & 1) * 128, k_at + n % KS * L::kBytes, steps * 16, j > 0, L::kSlab);
@@ -424,10 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
     const int row = threadIdx.x & 127, token = row / group, in_group = row % group;
     const float scale2 = a.scale * kLog2e;
-    int n = 0;
+    int n = 0, summed = 0;  // tiles of keys, and items whose rows see one, so far
     for (int i = 0;; i++) {
       Taken t;
-      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      if (!take_item(i, items, item_full, item_empty, limit, &t) || (a.fault == kFaultWeights && warp == 0)) break;
       const int tiles = (t.from + t.count + kTile - 1) / kTile, query = t.head * group + in_group;
       const bool mine = token < t.count;
       const int64_t at_token = (int64_t)t.sequence + t.from + token, at = at_token * a.q_heads + query;
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
       const int least = __reduce_min_sync(~0u, sees);
       bool fine = true;
       for (int j = 0; j < tiles; j++, n++) {
-        if (!(fine = wait(&dp_full, n & 1, dead))) break;  // S of the tile was issued ahead of it
+        wait_lane(&dp_full, n & 1, limit);  // S of the tile was issued ahead of it
         fence_after();
         const uint32_t from = s_at + (n & 1) * 128 + quarter + slice * kColumns;
         uint32_t s[kColumns], dp[kColumns];
@@ -467,15 +468,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
           float sum = 0.f;
 #pragma unroll
           for (int c = 0; c < kColumns; c++) sum = fmaf(__uint_as_float(s[c]), __uint_as_float(dp[c]), sum);
-          if (slice >= 2) sums[slice - 2][row] = sum;
-          weights_barrier();
-          if (slice < 2) sum += sums[slice][row];
-          weights_barrier();
-          if (slice < 2) sums[slice][row] = sum;
-          weights_barrier();
+          // slices 2 and 3 hand theirs to 0 and 1, and those the two sums to all; the next item's come after dQ of this one,
+          // for which all warps have to be through here
+          if (slice >= 2) {
+            sums[slice - 2][row] = sum;
+            __syncwarp();
+            if (lane == 0) arrive(&sums_half);
+          } else {
+            if (!(fine = wait(&sums_half, summed & 1, limit))) break;
+            sums[slice][row] += sum;
+            __syncwarp();
+            if (lane == 0) arrive(&sums_full);
+          }
+          if (!(fine = wait(&sums_full, summed & 1, limit))) break;
+          summed++;
           delta = sums[0][row] + sums[1][row];
           if (mine && slice == 0) deltas_of(a, t.rank)[at] = delta;
-          weights_barrier();
         }
         const F2 delta_pair = f2(-delta, -delta);
 #pragma unroll
@@ -492,8 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
           tmem_store16(from + kColumns / 2, s);
         }
         arrive_warp(&ds_ready);
+        if (!(fine = !ended_early(limit))) break;
       }
-      if (!fine || !wait(&dq_full, i & 1, dead)) break;
+      if (!fine || !wait(&dq_full, i & 1, limit)) break;
       fence_after();
       Quarter<DP> o;
       o.load(dq_at + quarter, slice);
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
       if (mine) o.store((uint16_t*)a.dq[t.rank] + at_token * a.dq_stride + query * a.dq_head, slice, a.scale, D);
     }
   }
-  end_block(a.ws, dead, warp);
+  end_block(a.ws, limit, warp);
 }
 
 template <int DP, bool FEW>
@@ -519,14 +528,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       item_full[kItemSlots], item_empty[kItemSlots];
   __shared__ Item items[kItemSlots];
   __shared__ uint32_t tmem_at;
-  __shared__ int dead_flag;
+  __shared__ Limit limit_at;
+  volatile Limit* const limit = &limit_at;
   __shared__ __align__(16) float numbers[NS][2][kTile];  // -lse log2(e) and -delta of a tile's rows
   __shared__ uint8_t token_of[kTile];
-  volatile int* const dead = &dead_flag;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int group = a.q_heads / a.kv_heads;
   if (threadIdx.x == 0) {
-    dead_flag = 0;
+    limit->dead = 0;
+    limit->ns = a.wait_ns;
     barrier_init(&kv_full, 1);
     barrier_init(&kv_empty, 1);
     for (int i = 0; i < NS; i++) {
@@ -564,17 +574,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   auto last_tile = [&](const Taken& t) { return tile_of(t, t.part + 1); };
 
   if (warp == kItemWarp) {
-    serve_items(a, work, true, magic, items, item_full, item_empty, dead);
+    serve_items(a, work, true, magic, items, item_full, item_empty, limit);
   } else if (warp == kCopyWarp) {
     int n = 0, some = 0;  // tiles of rows, and items that have some, so far
     for (int i = 0;; i++) {
       Taken t;
-      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      if (!take_item(i, items, item_full, item_empty, limit, &t)) break;
       const int begin = first_tile(t), end = last_tile(t);
       bool fine = true;
       for (int x = begin; x < end && fine; x++, n++) {
         const int stage = n % NS;
-        if (!(fine = wait_warp(&empty[stage], (n / NS & 1) ^ 1, dead))) break;
+        if (!(fine = wait_warp(&empty[stage], (n / NS & 1) ^ 1, limit))) break;
         if (lane == 0) {
           arrive_expect(&full[stage], (uint32_t)(2 * per_tile * group * 128 * (DP / 64)));
           for (int h = 0; h < DP / 64; h++) {
@@ -585,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
           }
         }
         if (x == begin) {
-          if (!(fine = wait_warp(&kv_empty, (some & 1) ^ 1, dead))) break;
+          if (!(fine = wait_warp(&kv_empty, (some & 1) ^ 1, limit))) break;
           if (lane == 0) {
             arrive_expect(&kv_full, 2 * L::kBytes);
             for (int h = 0; h < DP / 64; h++) {
@@ -602,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
     int n = 0;
     for (int i = 0;; i++) {
       Taken t;
-      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      if (!take_item(i, items, item_full, item_empty, limit, &t)) break;
       const int begin = first_tile(t), end = last_tile(t);
       const float *const lse = a.lse[t.rank], *const deltas = deltas_of(a, t.rank);
       float l[4], d[4];
@@ -620,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       bool fine = true;
       for (int x = begin; x < end; x++, n++) {
         const int stage = n % NS;
-        if (!(fine = wait_warp(&empty[stage], (n / NS & 1) ^ 1, dead))) break;
+        if (!(fine = wait_warp(&empty[stage], (n / NS & 1) ^ 1, limit))) break;
 #pragma unroll
         for (int y = 0; y < 4; y++) {
           numbers[stage][0][lane + 32 * y] = l[y];
@@ -638,12 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
     int base = 0, some = 0;  // tiles of rows, and items that have some, so far
     for (int i = 0;; i++) {
       Taken t;
-      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      if (!take_item(i, items, item_full, item_empty, limit, &t)) break;
       const int begin = first_tile(t), end = last_tile(t);
       if (begin == end) continue;
       auto score = [&](int x) {  // S^T of a tile of rows; rows that are none are 0, for the products with P and dS
         const int n = base + x - begin, stage = n % NS;
-        if (!wait_warp(&full[stage], n / NS & 1, dead)) return false;
+        if (!wait_warp(&full[stage], n / NS & 1, limit)) return false;
         const int rows = min(per_tile, t.length - x * per_tile) * group;
         if (rows < kTile) {
           clear_rows<DP>(ring + stage * 2 * L::kBytes, rows);
@@ -661,23 +671,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         commit(lead, &dp_full);
         if (x + 1 == end) commit(lead, &kv_empty);
       };
-      bool fine = wait_warp(&kv_full, some & 1, dead) && score(begin);
+      bool fine = wait_warp(&kv_full, some & 1, limit) && score(begin);
       if (!fine) break;
       value(begin);
       if (SB > 1 && begin + 1 < end && !score(begin + 1)) break;
       // sums of the item before have been read
-      if (some > 0 && !wait_warp(&sums_free, (some - 1) & 1, dead)) break;
+      if (some > 0 && !wait_warp(&sums_free, (some - 1) & 1, limit)) break;
       for (int x = begin; x < end; x++) {
         const int n = base + x - begin, stage = n % NS;
         const bool more = x + 1 < end;
-        if (!(fine = wait_warp(&p_ready[n % SB], n / SB & 1, dead))) break;
+        if (!(fine = wait_warp(&p_ready[n % SB], n / SB & 1, limit))) break;
         fence_after();
         weights_by_rows<2, kColumns>(lead, dv_at, s_at + n % SB * 128, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, x > begin, L::kSlab);
         if (FEW)
           weights_by_rows<2, kColumns>(lead, dv_at, s_at + n % SB * 128 + kColumns / 2, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, true,
                                        L::kSlab);
         if (x + SB < end && !(fine = score(x + SB))) break;
-        if (!(fine = wait_warp(&ds_ready, n & 1, dead))) break;
+        if (!(fine = wait_warp(&ds_ready, n & 1, limit))) break;
         fence_after();
         weights_by_rows<2, kColumns>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, x > begin, L::kSlab);
         if (FEW)
@@ -698,13 +708,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
     int n = 0, some = 0;
     for (int i = 0;; i++) {
       Taken t;
-      if (!take_item(i, items, item_full, item_empty, dead, &t)) break;
+      if (!take_item(i, items, item_full, item_empty, limit, &t) || (a.fault == kFaultWeights && warp == 0)) break;
       const int begin = first_tile(t), end = last_tile(t), key = t.from + row;
       bool fine = true;
       for (int x = begin; x < end; x++, n++) {
         const int stage = n % NS;
-        if (!(fine = wait(&full[stage], n / NS & 1, dead))) break;  // the rows' numbers
-        if (!(fine = wait(&s_full[n % SB], n / SB & 1, dead))) break;
+        // the rows' numbers, and their scores
+        wait_lane(&full[stage], n / NS & 1, limit);
+        wait_lane(&s_full[n % SB], n / SB & 1, limit);
         fence_after();
         const uint32_t from = s_at + n % SB * 128 + quarter + c0, dp_from = dp_at + quarter + c0;
         uint32_t s[kColumns], w[kColumns / 2];
@@ -739,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
           tmem_store16(from + kColumns / 2, w);
         }
         arrive_warp(&p_ready[n % SB]);
-        if (!(fine = wait(&dp_full, n & 1, dead))) break;
+        wait_lane(&dp_full, n & 1, limit);
         fence_after();
         uint32_t g[kColumns];
         tmem_load32(dp_from, g);
@@ -775,11 +786,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         tmem_store16(dp_from, w);
         arrive_warp(&ds_ready);
         if (lane == 0) arrive(&empty[stage]);  // the rows' numbers have been read
+        if (!(fine = !ended_early(limit))) break;
       }
       if (!fine) break;
       Quarter<DP> dk, dv;
       if (begin < end) {
-        if (!wait(&sums_full, some & 1, dead)) break;
+        if (!wait(&sums_full, some & 1, limit)) break;
         some++;
         fence_after();
         dk.load(dk_at + quarter, slice);
@@ -806,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       }
     }
   }
-  end_block(a.ws, dead, warp);
+  end_block(a.ws, limit, warp);
 }
 
 template <int DP, bool FEW>

@@ -43,8 +43,6 @@
 // for half the products. Five tokens behind 30011 take 21 us, a chain of a block's start,
 // its share of the keys and the join; 97 tokens 7.8, a chain of one tile: the first item
 // 1.5 us, copies 0.6, scores 0.4, weights 1.1, the product 0.4, rows 0.6.
-#include <cstdio>
-
 #include "prompt_attention.cuh"
 #include "rar_launch.h"
 #include "tensor_core.cuh"
@@ -93,11 +91,11 @@ struct Layout {
 struct Split {
   int64_t slots, items;
   int parts;    // that an item's keys are split into
-  float* sums;  // per item and part: 2 x 128 rows of DP binary32, then m and l of each, then the item (of part 0)
+  float* sums;  // per item and part: 2 x 128 rows of DP binary32, then m and l of each
 };
-// of 2 x 128 rows with m and l, and 32 numbers behind them
+// of 2 x 128 rows with m and l
 template <int DP>
-constexpr int64_t kPartFloats = 2 * kRows * (DP + 2) + kPromptPartInfo;
+constexpr int64_t kPartFloats = 2 * kRows * (DP + 2);
 
 struct Item {
   int there;        // 0: no more
@@ -172,11 +170,12 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       item_full[kItemSlots], item_empty[kItemSlots];
   __shared__ Item items[kItemSlots];
   __shared__ uint32_t tmem_at, lost[kLostSlots][4];
-  __shared__ int dead_flag;
-  volatile int* const dead = &dead_flag;
+  __shared__ Limit limit_at;
+  volatile Limit* const limit = &limit_at;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    dead_flag = 0;
+    limit->dead = 0;
+    limit->ns = a.wait_ns;
     for (int i = 0; i < NQ; i++) {
       barrier_init(&q_full[i], 1);
       barrier_init(&q_empty[i], 1);
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       int found = n < all ? find_item<FORM>(a, split, order, ordered, n, &item) : -1;
       if (found < 0) item.there = 0;
       if (found != 0) {
-        if (!wait_warp(&item_empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, dead)) break;
+        if (!wait_warp(&item_empty[i % kItemSlots], (i / kItemSlots & 1) ^ 1, limit)) break;
         if (lane == 0) {
           items[i % kItemSlots] = item;
           arrive(&item_full[i % kItemSlots]);
@@ -272,7 +271,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     int stage = 0, queries = 0, seen = 0;  // seen: tiles of keys of the items before
     uint32_t phase = 0;
     for (int i = 0;; i++) {
-      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, limit)) break;
       const Item& item = items[i % kItemSlots];
       const int there = uniform(item.there);
       if (!there) break;
@@ -285,7 +284,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       if (lane == 0) arrive(&item_empty[i % kItemSlots]);
       auto query = [&](int t) {
         const int at = queries % NQ;
-        if (!wait_warp(&q_empty[at], (queries / NQ & 1) ^ 1, dead)) return false;
+        if (!wait_warp(&q_empty[at], (queries / NQ & 1) ^ 1, limit)) return false;
         if (lane == 0) {
           arrive_expect(&q_full[at], (uint32_t)(per_tile * group * 128 * (DP / 64)));
           for (int h = 0; h < DP / 64; h++)
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         const bool copied = (unsigned)page < (unsigned)a.num_pages;
         const int count = FORM == kPages ? __popc(__ballot_sync(~0u, copied)) : 0;
         for (int which = 0; which < 2; which++) {
-          if (!(fine = wait_warp(&empty[stage], phase ^ 1, dead))) break;
+          if (!(fine = wait_warp(&empty[stage], phase ^ 1, limit))) break;
           uint8_t* const to = ring + stage * L::kTile;
           const CUtensorMap* const map = which == 0 ? &maps.k[rank] : &maps.v[rank];
           if (FORM == kDense) {
@@ -397,7 +396,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     };
     for (int i = 0;; i++) {
       if (pending > 0 && !__all_sync(~0u, ended(&item_full[i % kItemSlots], i / kItemSlots & 1))) drain();
-      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, limit)) break;
       const Item& item = items[i % kItemSlots];
       const int there = uniform(item.there);
       if (!there) break;
@@ -424,7 +423,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         for (int which = 0; which < 2; which++) {
           if (!__all_sync(~0u, ended(&empty[stage], phase ^ 1))) {
             drain();  // nobody would make room for what is not there yet
-            if (!(fine = wait_warp(&empty[stage], phase ^ 1, dead))) break;
+            if (!(fine = wait_warp(&empty[stage], phase ^ 1, limit))) break;
           }
           if (which == 0 && lane == 0) lost[(seen + j - begin) % kLostSlots][warp - kCacheWarp] = bad;
           const uint16_t* const from = (which == 0 ? k : v) + piece * 8;
@@ -453,7 +452,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     if (blockIdx.x == 0) check_starts(a.starts, a.sequences, a.tokens, a.ws, lane, 32);
     int queries = 0, results[2] = {0, 0};
     for (int i = 0;; i++) {
-      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, limit)) break;
       const Item& item = items[i % kItemSlots];
       const int there = uniform(item.there);
       if (!there) break;
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       for (int t = 0; t < 2; t++) {
         if (!fine || last[t] <= begin) continue;
         const int at = queries++ % NQ;
-        if (!(fine = wait_warp(&out_ready[t], results[t]++ & 1, dead))) break;
+        if (!(fine = wait_warp(&out_ready[t], results[t]++ & 1, limit))) break;
         if (lane == 0) {
           if (tokens[t] == per_tile && split.parts == 1 && !alone) {
             for (int h = 0; h < DP / 64 && h * 64 < D; h++)
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     int walked[2] = {0, 0}, results[2] = {0, 0};  // tiles of keys, and items, of each tile of rows so far
     uint32_t phase = 0;
     for (int i = 0;; i++) {
-      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      if (!wait_warp(&item_full[i % kItemSlots], i / kItemSlots & 1, limit)) break;
       const Item& item = items[i % kItemSlots];
       const int there = uniform(item.there);
       if (!there) break;
@@ -508,7 +507,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       };
       // V of key tile j is there; rows with no key would be multiplied by weights of 0, and may hold a NaN
       auto values = [&](int j, int stage, uint32_t phase) {
-        if (!wait_warp(&full[stage], phase, dead)) return false;
+        if (!wait_warp(&full[stage], phase, limit)) return false;
         const int left = keys - j * kKeys;
         const uint32_t* const holes_of = lost[(seen + j - begin) % kLostSlots];
         const bool holes = FORM == kPages && __any_sync(~0u, lane < 4 && holes_of[lane & 3] != 0);
@@ -525,12 +524,12 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         return true;
       };
       // stages: K of the first tile, then V of a tile and K of the next in turn
-      bool fine = wait_warp(&full[stage], phase, dead);
+      bool fine = wait_warp(&full[stage], phase, limit);
       const int first_stage = stage;
 #pragma unroll
       for (int t = 0; t < 2; t++) {
         if (!fine || last[t] <= begin) continue;
-        if (!(fine = wait_warp(&q_full[q_slot[t] % NQ], q_slot[t] / NQ & 1, dead))) break;
+        if (!(fine = wait_warp(&q_full[q_slot[t] % NQ], q_slot[t] / NQ & 1, limit))) break;
         fence_after();
         score(t, ring_at + first_stage * L::kTile);
       }
@@ -550,11 +549,11 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         const int next_stage = k_stage + 1 == NS ? 0 : k_stage + 1;
         const uint32_t next_phase = k_phase ^ (next_stage == 0);
         if (L::kApart && more) {
-          if (!(fine = wait_warp(&full[k_stage], k_phase, dead))) break;
+          if (!(fine = wait_warp(&full[k_stage], k_phase, limit))) break;
 #pragma unroll
           for (int t = 0; t < 2; t++) {
             if (!fine || j + 1 >= last[t]) continue;
-            if (!(fine = wait_warp(&s_read[t], walked[t] & 1, dead))) break;
+            if (!(fine = wait_warp(&s_read[t], walked[t] & 1, limit))) break;
             fence_after();
             score(t, ring_at + k_stage * L::kTile);
           }
@@ -565,11 +564,11 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         for (int t = 0; t < 2; t++) {
           if (j < last[t]) {
             // O of the item before has been read
-            if (j == begin && results[t] > 0 && !(fine = wait_warp(&o_free[t], (results[t] - 1) & 1, dead))) break;
-            if (!(fine = wait_warp(&p_half[t], walked[t] & 1, dead))) break;
+            if (j == begin && results[t] > 0 && !(fine = wait_warp(&o_free[t], (results[t] - 1) & 1, limit))) break;
+            if (!(fine = wait_warp(&p_half[t], walked[t] & 1, limit))) break;
             fence_after();
             weights_by_rows<8, 0, 0, 4>(lead, o_at[t], p_at[t], ring_at + v_stage * L::kTile, n_out, j > begin, kv_slab, kv_group);
-            if (!(fine = wait_warp(&p_full[t], walked[t] & 1, dead))) break;
+            if (!(fine = wait_warp(&p_full[t], walked[t] & 1, limit))) break;
             fence_after();
             weights_by_rows<8, 0, 4, 8>(lead, o_at[t], p_at[t], ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
             walked[t]++;
@@ -580,7 +579,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
             }
           }
           // what the warp waits for beside the weights, it waits for while products run
-          if (!L::kApart && more && t == 0 && !(fine = wait_warp(&full[k_stage], k_phase, dead))) break;
+          if (!L::kApart && more && t == 0 && !(fine = wait_warp(&full[k_stage], k_phase, limit))) break;
           if (more && t == 1 && !(fine = values(j + 1, next_stage, next_phase))) break;
           if (!L::kApart && j + 1 < last[t]) {
             fence_after();
@@ -609,9 +608,9 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     const uint32_t turn = a.scale < 0.f ? 0x80000000u : 0u, keep_bits = a.scale == 0.f ? 0u : ~0u;
     int walked = 0, results = 0, seen = 0, queries = 0;  // queries: tiles of queries of both tiles of rows
     for (int i = 0;; i++) {
-      if (!wait(&item_full[i % kItemSlots], i / kItemSlots & 1, dead)) break;
+      if (!wait(&item_full[i % kItemSlots], i / kItemSlots & 1, limit)) break;
       const Item& item = items[i % kItemSlots];
-      if (!item.there) break;
+      if (!item.there || (a.fault == kFaultWeights && warp == 0)) break;
       const int begin = item.begin, end = item.end, last = item.last[t];
       const int q_slot = (queries + (t == 1 && item.last[0] > begin)) % NQ;
       queries += (item.last[0] > begin) + (item.last[1] > begin);
@@ -620,8 +619,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       // rows that are none see what the tile's first row sees: they hold anything, and nobody reads them
       const int sees = min(item.before + t * per_tile + (mine ? token : 0) + 1, item.keys);
       const int query = item.head * group + in_group, rank = item.rank, part = item.part;
-      const int token0 = item.first, both_tokens = item.tokens[0] + item.tokens[1];
-      const int64_t at_token = (int64_t)token0 + t * per_tile + token, index = item.index;
+      const int64_t at_token = (int64_t)item.first + t * per_tile + token, index = item.index;
       __syncwarp();
       if (lane == 0) arrive(&item_empty[i % kItemSlots]);
       int least = sees;  // of the warp
@@ -630,7 +628,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       float m = -INFINITY, l = 0.f;
       bool fine = true;
       for (int j = begin; j < last; j++) {
-        if (!(fine = wait(&s_full[t], walked & 1, dead))) break;
+        if (!(fine = wait(&s_full[t], walked & 1, limit))) break;
         walked++;
         fence_after();
         uint32_t s[kKeys];
@@ -667,7 +665,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // the last tile's weights have been read, and O has them
         if (L::kApart && j > begin) {
-          if (!(fine = wait(&pv_done[t], walked & 1, dead))) break;
+          if (!(fine = wait(&pv_done[t], walked & 1, limit))) break;
           fence_after();
         }
         const float high = best * scale2;
@@ -720,7 +718,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       seen += end - begin;
       const bool some = last > begin;  // O has been written
       if (some) {
-        if (!wait(&o_full[t], results & 1, dead)) break;
+        if (!wait(&o_full[t], results & 1, limit)) break;
         results++;
         fence_after();
       }
@@ -779,11 +777,6 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         }
         arrive(&out_ready[t]);
       }
-      if (split.parts > 1 && part == 0 && threadIdx.x == 0) {
-        int* const info = reinterpret_cast<int*>(sums + 2 * kRows * (DP + 2));
-        info[0] = token0;
-        info[1] = both_tokens;
-      }
       if (mine && split.parts > 1) {
         sums[kRows * DP + row] = m;
         sums[kRows * (DP + 1) + row] = l;
@@ -795,7 +788,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (*dead) {
+  if (limit->dead) {
     // a wait ran out: copies and products that are still under way have ended by the time this has passed
     const uint64_t until = global_timer_ns() + 10000000ull;
     while (global_timer_ns() < until) {}
@@ -820,8 +813,6 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   const int group = a.q_heads / a.kv_heads, D = a.head_dim, per_tile = kRows / group, token = row / group;
   const int64_t index = blockIdx.x / (2 * kRows), lanes = (int64_t)a.kv_heads * a.nranks;
   const float* const sums = split.sums + index * split.parts * kPartFloats<DP> + t * kRows * (DP + 2);
-  // an item of no tokens has left nothing: whether this is one, only the starts say
-  const int* const info = reinterpret_cast<const int*>(split.sums + index * split.parts * kPartFloats<DP> + 2 * kRows * (DP + 2));
   float m[kPromptSplitBlocks / 32 + 1], l[kPromptSplitBlocks / 32 + 1];
 #pragma unroll
   for (int i = 0; i <= kPromptSplitBlocks / 32; i++) {
@@ -829,12 +820,12 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     m[i] = k < split.parts ? sums[k * kPartFloats<DP> + kRows * DP + row] : -INFINITY;
     l[i] = k < split.parts ? sums[k * kPartFloats<DP> + kRows * (DP + 1) + row] : 0.f;
   }
-  const int first = info[0], tokens = info[1];
   PromptSequence seq;
   int pair;
   if (!op_ready(a.ws, magic) || token >= per_tile) return;
   if (!find_sequence(a.starts, a.sequences, a.tokens, 1, 2 * per_tile, index / lanes, &seq, &pair)) return;
-  if (t * per_tile + token >= tokens) return;
+  const int at = pair * 2 * per_tile + t * per_tile + token;  // the row's token in the sequence
+  if (at >= seq.length) return;
   float top = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int i = 0; i <= kPromptSplitBlocks / 32; i++) top = fmaxf(top, m[i]);
@@ -880,7 +871,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
   for (int e = 0; e < E; e++) partial[warp][lane * E + e] = v[e];
   __syncthreads();
   const int lane_of = (int)(index % lanes), head = lane_of % a.kv_heads, rank = lane_of / a.kv_heads;
-  const int64_t at_token = (int64_t)first + t * per_tile + token;
+  const int64_t at_token = (int64_t)seq.first + at;
   const int query = head * group + row % group, d = threadIdx.x * 2;
   const float by = sum == 0.f ? 0.f : 1.f / sum;
   if (d < D) {

@@ -64,8 +64,6 @@ void mark_setup_done(int device, int key) {
   if (device >= 0 && device < kMaxDevices) g_setup[device].fetch_or(1u << key, std::memory_order_release);
 }
 
-namespace {
-
 uint64_t spin_timeout_ns() {
   uint64_t t = g_timeout_ns.load(std::memory_order_relaxed);
   if (t != 0) return t;
@@ -76,6 +74,10 @@ uint64_t spin_timeout_ns() {
   }
   return kDefaultTimeoutNs;
 }
+
+int debug_fault() { return g_fault.load(std::memory_order_relaxed); }
+
+namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -288,7 +290,7 @@ rar_status check_ring_call(int kind, const void* const* sendbufs, void* const* r
   a->conn_offset = kHeaderBytes;
   a->fifo_offset = kHeaderBytes + conn_region_bytes(nranks, g.nchan);
   a->timeout_ns = spin_timeout_ns();
-  a->fault = g_fault.load(std::memory_order_relaxed);
+  a->fault = debug_fault();
   a->ll_flag_max = g.proto == kLL ? g_ll_flag_max.load(std::memory_order_relaxed) : 0u;
   a->direct = direct ? 1 : 0;
   *grid = count == 0 ? 0 : nranks * g.nchan;
@@ -466,7 +468,7 @@ rar_status rar_oneshot_staged(const void* const* sendbufs, void* const* recvbufs
   a.nranks = nranks;
   a.dtype = (int)dtype;
   a.blocks_per_rank = staged_blocks_per_rank(nranks, sms);
-  a.fault = g_fault.load(std::memory_order_relaxed);
+  a.fault = debug_fault();
   a.count = (int64_t)count;
   a.ws = (char*)workspace;
   a.stage_offset = staged_stage_offset(nranks);  // the slot size comes from the workspace header

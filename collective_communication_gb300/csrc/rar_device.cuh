@@ -79,6 +79,7 @@ constexpr uint32_t kErrBounds = 9;  // debug builds: a slice outside its buffers
 constexpr int kFaultNone = 0;
 constexpr int kFaultDropHead = 1;   // receivers never publish their head
 constexpr int kFaultDropAck = 2;    // staged one-shot: ranks never acknowledge their reads
+constexpr int kFaultWeights = 4;    // attention over prompts: a warp that works out weights leaves at its first item
 constexpr int kFaultBoundsView = 3;  // debug builds: the bounds check sees each slice one buffer further on
 
 struct RingArgs {

@@ -99,6 +99,10 @@ int staged_blocks_per_rank(int nranks, int sms);
 // makes every call print its resolved geometry and kernel to stderr.
 bool trace_on();
 
+// The time limit of a wait inside a kernel, and the fault that tests ask for.
+uint64_t spin_timeout_ns();
+int debug_fault();
+
 // The current device and its SM count (cached per device; safe from several
 // host threads).
 cudaError_t current_device_sms(int* device, int* sms);

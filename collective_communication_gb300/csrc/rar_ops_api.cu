@@ -765,6 +765,8 @@ rar_status rar_prompt_attention_ex(const void* const* q, int64_t q_stride, int64
   a.k_head = k_head_stride;
   a.v_head = v_head_stride;
   a.out_head = out_head_stride;
+  a.wait_ns = spin_timeout_ns();
+  a.fault = debug_fault();
   a.scale = scale;
   a.nranks = nranks;
   a.dtype = (int)dtype;
@@ -830,6 +832,8 @@ rar_status rar_prompt_attention_cached_ex(const void* const* q, int64_t q_stride
   a.q_head = q_head_stride;
   a.out_head = out_head_stride;
   a.table_stride = table_stride;
+  a.wait_ns = spin_timeout_ns();
+  a.fault = debug_fault();
   a.scale = scale;
   a.nranks = nranks;
   a.dtype = (int)dtype;
@@ -917,6 +921,8 @@ rar_status rar_prompt_attention_backward_ex(const void* const* q, int64_t q_stri
   a.dq_head = dq_head_stride;
   a.dk_head = dk_head_stride;
   a.dv_head = dv_head_stride;
+  a.wait_ns = spin_timeout_ns();
+  a.fault = debug_fault();
   a.scale = scale;
   a.nranks = nranks;
   a.dtype = (int)dtype;

@@ -326,7 +326,8 @@ RAR_API rar_status rar_allreduce_static(const void* const* sendbufs, void* const
  * Wait for `stream`, then return the device status word of `workspace`
  * (RAR_OK if no kernel reported a failure) and clear it. After
  * RAR_ERR_TIMEOUT the workspace stays aborted (later calls report
- * RAR_ERR_ABORT) until rar_workspace_init.
+ * RAR_ERR_ABORT) until rar_workspace_init; that of an operator serves later
+ * calls as it is, and what the call was to write has no meaning.
  */
 RAR_API rar_status rar_get_status(void* workspace, void* stream);
 
@@ -349,7 +350,10 @@ RAR_API void rar_set_spin_timeout_ns(uint64_t ns);
  * rar_oneshot_staged, no rank acknowledges its reads, so the fifth call's
  * guard (4 slots per rank) waits until the time limit. No GPU fault
  * happens: the waits end, every block leaves, the launch completes, and
- * rar_get_status() reports RAR_ERR_TIMEOUT. 3 = in the debug library
+ * rar_get_status() reports RAR_ERR_TIMEOUT. 4 = in the attention over
+ * prompts and its gradient on the tensor cores, a warp of each block leaves
+ * at its first item, and the others wait for it until the time limit and
+ * leave likewise. 3 = in the debug library
  * (librar_debug.so) only, the device-side bounds check of the ring kernels
  * sees every slice one buffer further on than it is (the slice's own
  * accesses keep their offsets), so the first slice is refused and

@@ -1,4 +1,4 @@
-"""GPU tests of what the prompt operators do at their edges: tensors laid out in other ways."""
+"""GPU tests of what the prompt operators do at their edges: tensors laid out in other ways, waits that run out of time."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -90,4 +90,64 @@ def test_forward_result_of_torch():
     turned = out.transpose(1, 2).contiguous().transpose(1, 2)
     assert not turned.is_contiguous()
     for a, b in zip(want, backward(q, by_head(k)[0], v, starts, turned, lse, apart(dout)[0])):
+        assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- waits that run out
+@pytest.fixture
+def short_limit():
+    """Waits of 20 ms, and a warp of each block that works out weights leaves at its first item: nothing that the others
+    wait for comes, so they leave as well."""
+    B.set_spin_timeout_ns(20_000_000)
+    B.debug_set_fault(4)
+    yield
+    B.debug_set_fault(0)
+    B.set_spin_timeout_ns(0)
+
+
+def run_out(call, ws, outs):
+    """The call ends with its status, and writes no rows of tokens in no sequence (the last two)."""
+    call()
+    assert B.get_status(ws) == B.Status.ERR_TIMEOUT
+    assert all(bool((x[:, -2:] == MARK).all()) for x in outs)
+
+
+@pytest.mark.parametrize("lens,heads,kv,dim", [([700], 8, 1, 128), ([97], 8, 1, 128), ([4000], 4, 1, 64), ([60, 200], 6, 2, 80)], ids=str)
+def test_forward_runs_out_of_time(short_limit, lens, heads, kv, dim):
+    q, k, v, starts = prompt_inputs(2, lens, heads, kv, dim, "bf16", behind=2)
+    ws, out, lse = workspace(q, kv), torch.full_like(q, MARK), torch.full(q.shape[:3], MARK, device="cuda")
+    run_out(lambda: B.prompt_attention(q, k, v, starts, out, lse, ws), ws, (out, lse))
+    B.debug_set_fault(0)
+    want, want_lse = forward(q, k, v, starts)
+    out, lse = forward(q, k, v, starts, ws=ws)  # the same workspace
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("new,lens,dim,page", [([5], [3000], 128, 64), ([300, 20], [700, 20], 128, 16), ([300], [900], 64, 16),
+                                               ([40], [500], 80, 2), ([9, 9], [60, 50], 64, 1)], ids=str)
+def test_cached_runs_out_of_time(short_limit, new, lens, dim, page):
+    k, v, table, _, _ = paged(gen(3), 2, lens, 2, dim, page, torch.bfloat16)
+    q = normal(gen(4), 2, sum(new) + 2, 8, dim, dtype=torch.bfloat16)
+    starts, lens = starts_of(new), i32(*lens)
+    ws, out, lse = workspace(q, 2), torch.full_like(q, MARK), torch.full(q.shape[:3], MARK, device="cuda")
+    run_out(lambda: B.prompt_attention_cached(q, k, v, table, starts, lens, out, lse, ws), ws, (out, lse))
+    B.debug_set_fault(0)
+    want = cached_forward(q, k, v, table, starts, lens)
+    assert all(torch.equal(a, b) for a, b in zip(cached_forward(q, k, v, table, starts, lens, ws), want))
+
+
+@pytest.mark.parametrize("lens,heads,kv,dim", [([700], 8, 1, 128), ([97], 8, 1, 128), ([1500], 16, 1, 64), ([60, 200], 6, 2, 80),
+                                               ([3, 20], 6, 2, 64)], ids=str)
+def test_gradient_runs_out_of_time(short_limit, lens, heads, kv, dim):
+    """Rows that see one tile of keys (among 97 tokens, say) wait for one another's sums as well."""
+    q, k, v, starts = prompt_inputs(2, lens, heads, kv, dim, "bf16", behind=2)
+    B.debug_set_fault(0)
+    out, lse = forward(q, k, v, starts)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    want = backward(q, k, v, starts, out, lse, dout)
+    ws, grads = workspace(q, kv), [torch.full_like(x, MARK) for x in (q, k, k)]
+    B.debug_set_fault(4)
+    run_out(lambda: B.prompt_attention_backward(q, k, v, starts, out, lse, dout, *grads, ws), ws, grads)
+    B.debug_set_fault(0)
+    for a, b in zip(want, backward(q, k, v, starts, out, lse, dout, ws)):
         assert torch.equal(a, b)
