@@ -461,11 +461,11 @@ __global__ void __launch_bounds__(128) prompt_join_few_kernel(const __grid_const
 }
 
 // Weight and score gradient of a score s that the row sees; one that it sees alone has none (and would have what
-// roundings leave of dp - delta).
+// roundings leave of dp - delta), unless it is no number.
 __device__ __forceinline__ void weigh(float s, float dp, bool seen, bool alone, float scale2, float lse2, float delta, float* p,
                                       float* ds) {
   *p = seen ? exp2_fast(fmaf(s, scale2, -lse2)) : 0.f;
-  *ds = seen && !alone ? *p * (dp - delta) : 0.f;
+  *ds = seen ? *p * (dp - delta) * (alone ? 0.f : 1.f) : 0.f;
 }
 
 // dq of BT rows, and delta of each for the other kernel.

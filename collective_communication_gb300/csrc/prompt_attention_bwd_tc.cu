@@ -448,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         tmem_load32(from, s);
         tmem_load32(dp_at + quarter + slice * kColumns, dp);
         loads_done();
-        // (the one score of a row that sees one key has no gradient, whatever roundings leave of dp - delta)
-        const int upto = (sees > 1 ? sees : 0) - j * kTile - slice * kColumns;
+        const int upto = sees - j * kTile - slice * kColumns;
         const bool cut = (j + 1) * kTile > least;
         const F2 scale_pair = f2(scale2, scale2), lse_pair = f2(-lse2, -lse2);
 #pragma unroll
@@ -463,6 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
           for (int c = 0; c < kColumns; c++) {
             if (c >= upto) s[c] = dp[c] = 0;
           }
+          // the one score of a row that sees one key has no gradient, whatever roundings leave of dp - delta; NaN stays
+          if (sees == 1) s[0] = __float_as_uint(__uint_as_float(s[0]) * 0.f);
         }
         if (tiles == 1) {  // all keys of the rows are here
           float sum = 0.f;
@@ -755,10 +756,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         uint32_t g[kColumns];
         tmem_load32(dp_from, g);
         loads_done();
-        if (x == 0) {  // rows of the first token, which see one key: its score has no gradient
+        if (x == 0) {  // rows of the first token, which see one key: its score has no gradient, NaN stays
 #pragma unroll
           for (int c = 0; c < kColumns; c++)
-            if (c0 + c < group) s[c] = 0;
+            if (c0 + c < group) s[c] = __float_as_uint(__uint_as_float(s[c]) * 0.f);
         }
         // four of the scores' gradients as bf16 pairs
         auto gradients = [&](int c, float2* u, float2* v) {

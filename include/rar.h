@@ -609,7 +609,9 @@ RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const 
  *   read, and reports as in rar_decode_attention.
  * rar_prompt_attention_backward: dq, dk and dv from the gradient dout of out, with
  *   out and lse of the forward call. dk and dv are sums over the query heads of a group.
- *   No gradient goes through lse. The same bits every time.
+ *   No gradient goes through lse. The same bits every time. A row that sees one key has
+ *   no gradient through its score, exactly (but NaN where what it sees, or its row of
+ *   dout, is no number).
  * A key or value of a sequence that is infinite or NaN makes the rows that see it
  * infinite or NaN (a key that gives a score of -inf: no weight), and may make those of its
  * earlier tokens NaN; likewise a row of dout the gradients of the sequence. Other

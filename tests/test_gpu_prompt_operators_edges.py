@@ -1,4 +1,5 @@
-"""GPU tests of what the prompt operators do at their edges: tensors laid out in other ways, waits that run out of time."""
+"""GPU tests of what the prompt operators do at their edges: tensors laid out in other ways, waits that run out of
+time, single keys that are no numbers."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -151,3 +152,30 @@ def test_gradient_runs_out_of_time(short_limit, lens, heads, kv, dim):
     B.debug_set_fault(0)
     for a, b in zip(want, backward(q, k, v, starts, out, lse, dout, ws)):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- what is no number
+@pytest.mark.parametrize("bad", ["q", "k", "v", "dout"])
+@pytest.mark.parametrize("lens", [[3, 1, 40], [3, 1, 200]], ids=str)
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (128, "bf16"), (80, "bf16"), (192, "bf16"), (64, "f32"), (128, "f32")], ids=str)
+def test_gradient_of_one_key_that_is_no_number(dim, dtype, lens, bad):
+    """A row that sees one key alone: what is infinite or NaN there shows in every gradient that the formula takes from it
+    (dv takes nothing of v), in every form alike, and in no other sequence."""
+    q, k, v, starts = prompt_inputs(1, lens, 4, 2, dim, dtype, seed=2)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    out, lse = forward(q, k, v, starts)
+    want = backward(q, k, v, starts, out, lse, dout)
+    for value in (float("nan"), float("inf")):
+        x = dict(q=q.clone(), k=k.clone(), v=v.clone(), dout=dout.clone())
+        x[bad][:, 3, 0] = value  # its first head: of a group of two queries, or one of them
+        o, l = forward(x["q"], x["k"], x["v"], starts)
+        dq, dk, dv = backward(x["q"], x["k"], x["v"], starts, o, l, x["dout"])
+        heads = 1 if bad in ("q", "dout") else 2
+        assert not bool(dq[:, 3, :heads].isfinite().any()) and torch.equal(dq[:, 3, heads:], want[0][:, 3, heads:])
+        assert not bool(dk[:, 3, 0].isfinite().any()) and torch.equal(dk[:, 3, 1], want[1][:, 3, 1])
+        if bad == "v":
+            assert torch.equal(dv, want[2])
+        else:
+            assert not bool(dv[:, 3, 0].isfinite().any()) and torch.equal(dv[:, 3, 1], want[2][:, 3, 1])
+        for a, b in zip((dq, dk, dv), want):
+            assert torch.equal(a[:, :3], b[:, :3]) and torch.equal(a[:, 4:], b[:, 4:])
