@@ -41,6 +41,8 @@
 // where an SM has 20 on average. Queries of the next item ahead in a buffer of their own,
 // for fewer tiles of keys and values, took as long, and 800 us where this takes 715 (8192
 // tokens, 16 query heads on 2 key heads of 128).
+#include <type_traits>
+
 #include "prompt_attention.cuh"
 #include "rar_launch.h"
 #include "tensor_core.cuh"
@@ -280,10 +282,14 @@ __global__ void __launch_bounds__(256) prompt_delta_kernel(const __grid_constant
   }
 }
 
-// FEW: a call of up to 128 tokens takes products with what the roundings of P and dS leave as well, which lies behind
-// them: over so few keys and rows the roundings need not average out (2 tokens: dq off by 2.8e-3 of its norm, where its own
-// rounding is 1.7e-3). It costs 1.5 to 3.5 us of 18 to 33; for all calls, it would cost 5 %.
-template <int DP, bool FEW>
+// Products with P and dS may take what their roundings leave as well, which lies behind them. The roundings are as large as
+// the result's, and stay so over any number of keys: dq is off by 2.4e-3 of its norm in long sequences, by 2.8e-3 in one of 2
+// tokens, where its own rounding is 1.66e-3. With the rests that is all there is, but for another three products
+// of seven: 148 -> 178 us for 4097 packed tokens of 128 elements, 550 -> 694 for 8192 of 64. Those have them that are a small
+// part of such a call, and whose products are over before anything else is in a call of their own (1.5 to 3.5 us of 18 to
+// 33): dq of rows that see one tile of keys, dk and dv of sequences of one. What a sequence gets depends on
+// its own length alone, not on what it is packed with.
+template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __grid_constant__ PromptBwdArgs a,
                                                                      const __grid_constant__ Maps maps,
                                                                      const __grid_constant__ Work work) {
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         fence_after();
         if (more && !(fine = value(j + 1))) break;
         weights_by_rows<2, kColumns>(lead, dq_at, s_at + (n & 1) * 128, k_at + n % KS * L::kBytes, steps * 16, j > 0, L::kSlab);
-        if (FEW)
+        if (tiles == 1)
           weights_by_rows<2, kColumns>(lead, dq_at, s_at + (n & 1) * 128 + kColumns / 2, k_at + n % KS * L::kBytes, steps * 16, true, L::kSlab);
         commit(lead, &k_empty[n % KS]);
         if (!more) commit(lead, &dq_full);
@@ -439,8 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
       }
       const int sees = t.from + (mine ? token : 0) + 1;
       const int least = __reduce_min_sync(~0u, sees);
-      bool fine = true;
-      for (int j = 0; j < tiles; j++, n++) {
+      const F2 scale_pair = f2(scale2, scale2), lse_pair = f2(-lse2, -lse2);
+      // the score gradients of key tile j; ONE: it is all that the rows see
+      auto work_out = [&](auto one, int j) {
+        constexpr bool ONE = decltype(one)::value;
         wait_lane(&dp_full, n & 1, limit);  // S of the tile was issued ahead of it
         fence_after();
         const uint32_t from = s_at + (n & 1) * 128 + quarter + slice * kColumns;
@@ -450,7 +458,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         loads_done();
         const int upto = sees - j * kTile - slice * kColumns;
         const bool cut = (j + 1) * kTile > least;
-        const F2 scale_pair = f2(scale2, scale2), lse_pair = f2(-lse2, -lse2);
 #pragma unroll
         for (int c = 0; c < kColumns; c += 2) {
           float2 p = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, lse_pair));
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
           // the one score of a row that sees one key has no gradient, whatever roundings leave of dp - delta; NaN stays
           if (sees == 1) s[0] = __float_as_uint(__uint_as_float(s[0]) * 0.f);
         }
-        if (tiles == 1) {  // all keys of the rows are here
+        if (ONE) {
           float sum = 0.f;
 #pragma unroll
           for (int c = 0; c < kColumns; c++) sum = fmaf(__uint_as_float(s[c]), __uint_as_float(dp[c]), sum);
@@ -476,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
             __syncwarp();
             if (lane == 0) arrive(&sums_half);
           } else {
-            if (!(fine = wait(&sums_half, summed & 1, limit))) break;
+            if (!wait(&sums_half, summed & 1, limit)) return false;
             sums[slice][row] += sum;
             __syncwarp();
             if (lane == 0) arrive(&sums_full);
           }
-          if (!(fine = wait(&sums_full, summed & 1, limit))) break;
+          if (!wait(&sums_full, summed & 1, limit)) return false;
           summed++;
           delta = sums[0][row] + sums[1][row];
           if (mine && slice == 0) deltas_of(a, t.rank)[at] = delta;
@@ -491,18 +498,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         for (int c = 0; c < kColumns; c += 2) {
           const F2 d = add2(f2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), delta_pair);
           const float2 ds = unpack(mul2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), d));
-          if (FEW) dp[c] = __float_as_uint(ds.x), dp[c + 1] = __float_as_uint(ds.y);
+          if (ONE) dp[c] = __float_as_uint(ds.x), dp[c + 1] = __float_as_uint(ds.y);
           s[c / 2] = bf16_pair(ds.x, ds.y);
         }
         tmem_store16(from, s);
-        if (FEW) {
+        if (ONE) {
 #pragma unroll
           for (int c = 0; c < kColumns; c += 2) s[c / 2] = bf16_rest(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]), s[c / 2]);
           tmem_store16(from + kColumns / 2, s);
         }
         arrive_warp(&ds_ready);
-        if (!(fine = !ended_early(limit))) break;
-      }
+        n++;
+        return !ended_early(limit);
+      };
+      bool fine = true;
+      if (tiles == 1) fine = work_out(std::true_type{}, 0);
+      else
+        for (int j = 0; j < tiles && fine; j++) fine = work_out(std::false_type{}, j);
       if (!fine || !wait(&dq_full, i & 1, limit)) break;
       fence_after();
       Quarter<DP> o;
@@ -517,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
   end_block(a.ws, limit, warp);
 }
 
-template <int DP, bool FEW>
+template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __grid_constant__ PromptBwdArgs a,
                                                                      const __grid_constant__ Maps maps,
                                                                      const __grid_constant__ Work work) {
@@ -573,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   };
   auto first_tile = [&](const Taken& t) { return tile_of(t, t.part); };
   auto last_tile = [&](const Taken& t) { return tile_of(t, t.part + 1); };
+  auto rests_of = [&](const Taken& t) { return t.length <= kTile; };
 
   if (warp == kItemWarp) {
     serve_items(a, work, true, magic, items, item_full, item_empty, limit);
@@ -651,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       Taken t;
       if (!take_item(i, items, item_full, item_empty, limit, &t)) break;
       const int begin = first_tile(t), end = last_tile(t);
+      const bool rests = rests_of(t);
       if (begin == end) continue;
       auto score = [&](int x) {  // S^T of a tile of rows; rows that are none are 0, for the products with P and dS
         const int n = base + x - begin, stage = n % NS;
@@ -684,14 +698,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         if (!(fine = wait_warp(&p_ready[n % SB], n / SB & 1, limit))) break;
         fence_after();
         weights_by_rows<2, kColumns>(lead, dv_at, s_at + n % SB * 128, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, x > begin, L::kSlab);
-        if (FEW)
+        if (rests)
           weights_by_rows<2, kColumns>(lead, dv_at, s_at + n % SB * 128 + kColumns / 2, ring_at + (stage * 2 + 1) * L::kBytes, steps * 16, true,
                                        L::kSlab);
         if (x + SB < end && !(fine = score(x + SB))) break;
         if (!(fine = wait_warp(&ds_ready, n & 1, limit))) break;
         fence_after();
         weights_by_rows<2, kColumns>(lead, dk_at, dp_at, ring_at + stage * 2 * L::kBytes, steps * 16, x > begin, L::kSlab);
-        if (FEW)
+        if (rests)
           weights_by_rows<2, kColumns>(lead, dk_at, dp_at + kColumns / 2, ring_at + stage * 2 * L::kBytes, steps * 16, true, L::kSlab);
         commit(lead, &empty[stage]);
         if (!more) commit(lead, &sums_full);
@@ -711,8 +725,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
       Taken t;
       if (!take_item(i, items, item_full, item_empty, limit, &t) || (a.fault == kFaultWeights && warp == 0)) break;
       const int begin = first_tile(t), end = last_tile(t), key = t.from + row;
-      bool fine = true;
-      for (int x = begin; x < end; x++, n++) {
+      // weights and score gradients of a tile of rows
+      auto work_out = [&](auto with_rests, int x) {
+        constexpr bool RESTS = decltype(with_rests)::value;
         const int stage = n % NS;
         // the rows' numbers, and their scores
         wait_lane(&full[stage], n / NS & 1, limit);
@@ -745,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
 #pragma unroll
         for (int c = 0; c < kColumns; c += 2) w[c / 2] = bf16_pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         tmem_store16(from, w);
-        if (FEW) {
+        if (RESTS) {
 #pragma unroll
           for (int c = 0; c < kColumns; c += 2) w[c / 2] = bf16_rest(__uint_as_float(s[c]), __uint_as_float(s[c + 1]), w[c / 2]);
           tmem_store16(from + kColumns / 2, w);
@@ -772,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
           w[c / 2 + 1] = bf16_pair(v->x, v->y);
         };
         float2 u, v;
-        if (FEW) {
+        if (RESTS) {
 #pragma unroll
           for (int c = 0; c < kColumns; c += 4) {
             gradients(c, &u, &v);
@@ -787,8 +802,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         tmem_store16(dp_from, w);
         arrive_warp(&ds_ready);
         if (lane == 0) arrive(&empty[stage]);  // the rows' numbers have been read
-        if (!(fine = !ended_early(limit))) break;
-      }
+        n++;
+        return !ended_early(limit);
+      };
+      bool fine = true;
+      if (rests_of(t))
+        for (int x = begin; x < end && fine; x++) fine = work_out(std::true_type{}, x);
+      else
+        for (int x = begin; x < end && fine; x++) fine = work_out(std::false_type{}, x);
       if (!fine) break;
       Quarter<DP> dk, dv;
       if (begin < end) {
@@ -822,10 +843,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
   end_block(a.ws, limit, warp);
 }
 
-template <int DP, bool FEW>
+template <int DP>
 cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
   const int group = a.q_heads / a.kv_heads, per_tile = kTile / group, D = a.head_dim;
-  const void *rows = (const void*)prompt_rows_tc_kernel<DP, FEW>, *keys = (const void*)prompt_keys_tc_kernel<DP, FEW>;
+  const void *rows = (const void*)prompt_rows_tc_kernel<DP>, *keys = (const void*)prompt_keys_tc_kernel<DP>;
   int blocks = 0;
   cudaError_t e = resident_blocks(rows, kThreads, Layout<DP>::kRowsShared, &blocks);
   if (e == cudaSuccess) e = resident_blocks(keys, kThreads, Layout<DP>::kKeysShared, &blocks);
@@ -842,7 +863,7 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
   void* delta_params[] = {&copy};
   const int64_t a_block = 8 * 4 * (32 / (DP / 8));  // rows
   // (no row of 128 tokens or fewer has a second tile of keys: the rows' kernel works out all deltas)
-  if (!FEW)
+  if (a.tokens > kTile)
     e = launch_op((const void*)prompt_delta_kernel<DP>,
                   dim3((unsigned)div_up((int64_t)a.tokens * a.q_heads, a_block), (unsigned)a.nranks), 256, 0, stream, delta_params);
   for (int which = 0; which < 2 && e == cudaSuccess; which++) {
@@ -866,8 +887,7 @@ cudaError_t launch(const PromptBwdArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_prompt_attention_bwd_tc(const PromptBwdArgs& a, cudaStream_t stream) {
-  if (a.tokens <= kTile) return a.head_dim <= 64 ? launch<64, true>(a, stream) : launch<128, true>(a, stream);
-  return a.head_dim <= 64 ? launch<64, false>(a, stream) : launch<128, false>(a, stream);
+  return a.head_dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
 }
 
 }  // namespace rar

@@ -617,7 +617,8 @@ RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const 
  * earlier tokens NaN; likewise a row of dout the gradients of the sequence. Other
  * sequences' rows do not depend on it.
  * RAR_BF16 with head_dim up to 128 and groups of up to 128 query heads runs on the tensor
- * cores, with the weights of values (and score gradients) rounded to bf16; all else in
+ * cores, with the weights of values (and score gradients) rounded to bf16, but for the
+ * gradients of sequences of up to 128 tokens, which keep what that leaves; all else in
  * binary32 on the ordinary arithmetic units.
  */
 RAR_API size_t rar_prompt_attention_workspace_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads,

@@ -1,12 +1,12 @@
 """GPU tests of what the prompt operators do at their edges: tensors laid out in other ways, waits that run out of
-time, single keys that are no numbers."""
+time, single keys that are no numbers, what the roundings of weights leave."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from collective_communication_gb300 import binding as B
-from test_gpu_prompt_operators import (DT, MARK, backward, cached_forward, forward, gen, i32, normal, paged, prompt_inputs,
-                                       starts_of, workspace)
+from test_gpu_prompt_operators import (DT, MARK, backward, cached_forward, close, forward, gen, i32, normal, paged,
+                                       prompt_inputs, scores, starts_of, workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +179,35 @@ def test_gradient_of_one_key_that_is_no_number(dim, dtype, lens, bad):
             assert not bool(dv[:, 3, 0].isfinite().any()) and torch.equal(dv[:, 3, 1], want[2][:, 3, 1])
         for a, b in zip((dq, dk, dv), want):
             assert torch.equal(a[:, :3], b[:, :3]) and torch.equal(a[:, 4:], b[:, 4:])
+
+
+# ---------------------------------------------------------------- roundings of weights
+@pytest.mark.parametrize("lens", [[2, 300, 17, 1, 128, 129, 90], [5] * 70, [128, 1000, 3]], ids=str)
+@pytest.mark.parametrize("dim", [64, 80, 128])
+def test_gradient_of_short_sequences_among_others(lens, dim):
+    """A sequence of up to 128 tokens loses nothing to the roundings of weights, whatever it is packed with: the bound of
+    a call of its own, 2^-13 of the magnitudes (2^-17 of a weight or a score's gradient is lost with what their
+    roundings leave, sums of 128 binary32 products take 2^-17, the exponential of a score below 16 2^-19, lse's rounding
+    2^-21; below 2^-15 in all, of terms that are multiplied twice)."""
+    q, k, v, starts = prompt_inputs(2, lens, 6, 2, dim, "bf16", seed=6)
+    dout = normal(gen(9), *q.shape, dtype=q.dtype)
+    out, lse = forward(q, k, v, starts)
+    dq, dk, dv = backward(q, k, v, starts, out, lse, dout)
+    bounds = starts.tolist()
+    for r in range(2):
+        for a, b in zip(bounds, bounds[1:]):
+            if b - a > 128:
+                continue
+            x, key, value, g = (z[r, a:b].double() for z in (q, k, v, dout))
+            x, g = (z.unflatten(1, (2, 3)) for z in (x, g))
+            s, sees, _ = scores(q[r, a:b], k[r, a:b], 0, dim ** -0.5)
+            p = torch.softmax(s.masked_fill(~sees, float("-inf")), -1)
+            dp = torch.einsum("thgd,shd->hgts", g, value)
+            dsize = torch.einsum("thgd,shd->hgts", g.abs(), value.abs())
+            ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+            size = p * (dsize + (p * dsize).sum(-1, keepdim=True)) * 2 ** -13 * dim ** -0.5
+            close(dq[r, a:b], torch.einsum("hgts,shd->thgd", ds, key).flatten(1, 2) * dim ** -0.5,
+                  torch.einsum("hgts,shd->thgd", size, key.abs()).flatten(1, 2), "dq")
+            close(dk[r, a:b], torch.einsum("hgts,thgd->shd", ds, x) * dim ** -0.5,
+                  torch.einsum("hgts,thgd->shd", size, x.abs()), "dk")
+            close(dv[r, a:b], torch.einsum("hgts,thgd->shd", p, g), 2 ** -13 * torch.einsum("hgts,thgd->shd", p, g.abs()), "dv")
