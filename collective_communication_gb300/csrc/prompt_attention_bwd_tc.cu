@@ -216,8 +216,6 @@ struct Quarter {
   }
 };
 
-// What the bf16 pair `to` leaves of x and y, as another.
-__device__ __forceinline__ uint32_t bf16_rest(float x, float y, uint32_t to) { return bf16_pair(x - bf16_lo(to), y - bf16_hi(to)); }
 // One arrival of the warp, after its lanes' stores to tensor memory.
 __device__ __forceinline__ void arrive_warp(uint64_t* b) {
   stores_done();

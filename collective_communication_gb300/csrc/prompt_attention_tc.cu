@@ -13,9 +13,14 @@
 // tile's weights are being worked out, the other's products run. S and O are in tensor
 // memory (2 x 128 and 2 x head size columns); P takes the place of the S that it came
 // from, as bf16, and is the left operand of P V from there; products with the first half
-// of a tile's weights run while the second half is worked out. Weights are rounded to
-// bf16 (2^-8 of themselves, in both directions): their sum l is of the unrounded ones,
-// so the roundings average out over the keys and stay below the result's own.
+// of a tile's weights run while the second half is worked out. Weights are rounded to bf16
+// for that product; their sum l is of the unrounded ones. The rounding is as large as the
+// result's own, over few keys or many: out is off by 1.9 to 2.1e-3 of its norm, where its own
+// rounding is 1.6e-3. What it leaves would take a second product: 686 -> 977 us for 16384
+// tokens, 115 -> 147 for 8192 packed ones, 306 -> 422 for chunks. A cached request of one tile of
+// rows (128 / group new tokens: drafts behind a long context) has it (21.3 -> 24 us for five
+// tokens behind 30011, 2.3e-3 -> 1.7e-3), so that these tokens come out as close as one by one from
+// decode_attention.cu, which has it too. The second tile's columns are free there.
 //
 // Blocks stay, one an SM, and take items from a counter, those with the most keys
 // first. A fourth warp takes them ahead and finds out what they are, so
@@ -43,6 +48,8 @@
 // for half the products. Five tokens behind 30011 take 21 us, a chain of a block's start,
 // its share of the keys and the join; 97 tokens 7.8, a chain of one tile: the first item
 // 1.5 us, copies 0.6, scores 0.4, weights 1.1, the product 0.4, rows 0.6.
+#include <type_traits>
+
 #include "prompt_attention.cuh"
 #include "rar_launch.h"
 #include "tensor_core.cuh"
@@ -106,6 +113,7 @@ struct Item {
   int begin, end;   // tiles of keys
   int last[2];      // a tile of rows walks from begin to here
   int part;
+  int rests;        // weights keep what their rounding leaves
   int64_t index;    // of the item, parts aside
 };
 
@@ -134,6 +142,7 @@ __device__ __forceinline__ int find_item(const PromptArgs& a, const Split& split
     if (FORM != kDense) cached_sequence(a, &seq);
   }
   const int token0 = pair * 2 * per_tile;  // of the sequence
+  item->rests = FORM != kDense && seq.length <= per_tile;
   item->index = (int64_t)(seq.first / (2 * per_tile) + seq.index + pair) * lanes + lane_of;  // by number, as the join finds it
   item->sequence = seq.index;
   item->keys = seq.keys;
@@ -228,6 +237,8 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
   constexpr uint32_t tmem = 0;  // all of it, so it begins at 0
   constexpr uint32_t s_at[2] = {tmem, tmem + 128}, o_at[2] = {tmem + 256, tmem + 256 + DP};
   constexpr uint32_t p_at[2] = {L::kApart ? tmem + 384 : s_at[0], L::kApart ? tmem + 448 : s_at[1]};
+  // of the first tile of rows, where there is no second one: the second's place, or the other half of S
+  constexpr uint32_t rest_at = L::kApart ? p_at[1] : p_at[0] + 64;
   uint8_t* const ring = smem + NQ * L::kTile;
   const uint32_t all = (uint32_t)(split.items * split.parts);
   // a tile of keys is slab by slab, or where a box holds whole rows of pages, eight rows of both slabs after one another
@@ -492,7 +503,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       const Item& item = items[i % kItemSlots];
       const int there = uniform(item.there);
       if (!there) break;
-      const int begin = uniform(item.begin), end = uniform(item.end), keys = uniform(item.keys);
+      const int begin = uniform(item.begin), end = uniform(item.end), keys = uniform(item.keys), rests = uniform(item.rests);
       const int last[2] = {uniform(item.last[0]), uniform(item.last[1])};
       __syncwarp();
       if (lane == 0) arrive(&item_empty[i % kItemSlots]);
@@ -568,9 +579,13 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
             if (!(fine = wait_warp(&p_half[t], walked[t] & 1, limit))) break;
             fence_after();
             weights_by_rows<8, 0, 0, 4>(lead, o_at[t], p_at[t], ring_at + v_stage * L::kTile, n_out, j > begin, kv_slab, kv_group);
+            if (FORM != kDense && t == 0 && rests)
+              weights_by_rows<8, 0, 0, 4>(lead, o_at[0], rest_at, ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
             if (!(fine = wait_warp(&p_full[t], walked[t] & 1, limit))) break;
             fence_after();
             weights_by_rows<8, 0, 4, 8>(lead, o_at[t], p_at[t], ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
+            if (FORM != kDense && t == 0 && rests)
+              weights_by_rows<8, 0, 4, 8>(lead, o_at[0], rest_at, ring_at + v_stage * L::kTile, n_out, true, kv_slab, kv_group);
             walked[t]++;
             if (L::kApart) commit(lead, &pv_done[t]);
             if (j + 1 == last[t]) {
@@ -612,6 +627,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
       const Item& item = items[i % kItemSlots];
       if (!item.there || (a.fault == kFaultWeights && warp == 0)) break;
       const int begin = item.begin, end = item.end, last = item.last[t];
+      const bool rests = item.rests;
       const int q_slot = (queries + (t == 1 && item.last[0] > begin)) % NQ;
       queries += (item.last[0] > begin) + (item.last[1] > begin);
       const int tokens = item.tokens[t];
@@ -691,8 +707,9 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         F2 sum = f2(0.f, 0.f), more = f2(0.f, 0.f);
         const F2 scale_pair = f2(scale2, scale2), by_pair = f2(-by, -by);
         // products with the first half of the weights run while the second half is worked out
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
+        auto half = [&](auto with_rests, int h) {
+          constexpr bool RESTS = decltype(with_rests)::value;
+          uint32_t left[RESTS ? 16 : 1];
 #pragma unroll
           for (int c = h * 64; c < h * 64 + 64; c += 4) {
             float2 x = unpack(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), scale_pair, by_pair));
@@ -705,11 +722,23 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
             more = add2(more, f2(y.x, y.y));
             s[c / 2] = bf16_pair(x.x, x.y);
             s[c / 2 + 1] = bf16_pair(y.x, y.y);
+            if (RESTS) {
+              left[c / 2 % 16] = bf16_rest(x.x, x.y, s[c / 2]);
+              left[c / 2 % 16 + 1] = bf16_rest(y.x, y.y, s[c / 2 + 1]);
+              if (c % 32 == 28) tmem_store16(rest_at + quarter + c / 32 * 16, left);
+            }
           }
           tmem_store32(p_at[t] + quarter + 32 * h, s + 32 * h);
           stores_done();
           fence_before();
           arrive(h == 0 ? &p_half[t] : &p_full[t]);
+        };
+        if (FORM != kDense && rests) {
+          half(std::true_type{}, 0);
+          half(std::true_type{}, 1);
+        } else {
+          half(std::false_type{}, 0);
+          half(std::false_type{}, 1);
         }
         const float2 u = unpack(add2(sum, more));
         l += u.x + u.y;

@@ -265,6 +265,9 @@ __device__ __forceinline__ void weights_by_rows(uint32_t lead, uint32_t d, uint3
     multiply_tmem(lead, d, w + k / PER * STRIDE + k % PER * 8, b + k * (group >> 3), high, kind, add || k > 0);
 }
 
+// What the bf16 pair `to` leaves of x and y, as another.
+__device__ __forceinline__ uint32_t bf16_rest(float x, float y, uint32_t to) { return bf16_pair(x - bf16_lo(to), y - bf16_hi(to)); }
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

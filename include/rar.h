@@ -618,8 +618,9 @@ RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const 
  * sequences' rows do not depend on it.
  * RAR_BF16 with head_dim up to 128 and groups of up to 128 query heads runs on the tensor
  * cores, with the weights of values (and score gradients) rounded to bf16, but for the
- * gradients of sequences of up to 128 tokens, which keep what that leaves; all else in
- * binary32 on the ordinary arithmetic units.
+ * gradients of sequences of up to 128 tokens and cached requests of up to 128 / (q_heads /
+ * kv_heads) new ones, which keep what that leaves; all else in binary32 on the ordinary
+ * arithmetic units.
  */
 RAR_API size_t rar_prompt_attention_workspace_bytes(int nranks, int64_t tokens, int q_heads, int kv_heads,
                                                     int head_dim); /* for all three, also of fewer tokens; 0: bad arguments */

@@ -5,7 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from collective_communication_gb300 import binding as B
-from test_gpu_prompt_operators import (DT, MARK, backward, cached_forward, close, forward, gen, i32, normal, paged,
+from test_gpu_prompt_operators import (DT, MARK, attend, backward, cached_forward, close, forward, gen, i32, normal, paged,
                                        prompt_inputs, scores, starts_of, workspace)
 
 pytestmark = pytest.mark.gpu
@@ -186,7 +186,7 @@ def test_gradient_of_one_key_that_is_no_number(dim, dtype, lens, bad):
 @pytest.mark.parametrize("dim", [64, 80, 128])
 def test_gradient_of_short_sequences_among_others(lens, dim):
     """A sequence of up to 128 tokens loses nothing to the roundings of weights, whatever it is packed with: the bound of
-    a call of its own, 2^-13 of the magnitudes (2^-17 of a weight or a score's gradient is lost with what their
+    a call of its own, 2^-13 of the magnitudes (2^-16 of a weight or a score's gradient is lost with what their
     roundings leave, sums of 128 binary32 products take 2^-17, the exponential of a score below 16 2^-19, lse's rounding
     2^-21; below 2^-15 in all, of terms that are multiplied twice)."""
     q, k, v, starts = prompt_inputs(2, lens, 6, 2, dim, "bf16", seed=6)
@@ -211,3 +211,26 @@ def test_gradient_of_short_sequences_among_others(lens, dim):
             close(dk[r, a:b], torch.einsum("hgts,thgd->shd", ds, x) * dim ** -0.5,
                   torch.einsum("hgts,thgd->shd", size, x.abs()), "dk")
             close(dv[r, a:b], torch.einsum("hgts,thgd->shd", p, g), 2 ** -13 * torch.einsum("hgts,thgd->shd", p, g.abs()), "dv")
+
+
+@pytest.mark.parametrize("new,lens,heads,kv,dim,page", [
+    ([5], [3000], 16, 2, 128, 64), ([1, 16, 3], [1, 700, 41], 8, 1, 128, 16), ([9, 128, 40], [900, 128, 1000], 2, 2, 64, 16),
+    ([42, 300, 1], [50, 800, 513], 6, 2, 80, 32), ([7, 2], [300, 9], 8, 2, 64, 4), ([1] * 40, list(range(1, 401, 10)), 4, 2, 64, 16),
+    ([1], [30000], 100, 1, 128, 128)], ids=str)
+def test_cached_requests_of_few_tokens(new, lens, heads, kv, dim, page):
+    """New tokens of one tile of rows lose nothing to the weights' rounding, whatever else is in the call: a weight is off by
+    2^-16 of itself (the rounding of what its rounding leaves), where attend() allows 2^-8 for others."""
+    k, v, table, keys, values = paged(gen(3), 2, lens, kv, dim, page, torch.bfloat16)
+    q = normal(gen(4), 2, sum(new), heads, dim, dtype=torch.bfloat16)
+    starts = starts_of(new)
+    out, lse = cached_forward(q, k, v, table, starts, i32(*lens))
+    bounds = starts.tolist()
+    for r in range(2):
+        for i, (a, b) in enumerate(zip(bounds, bounds[1:])):
+            o, _, slack, _ = attend(q[r, a:b], keys[i][r], values[i][r], lens[i] - (b - a), dim ** -0.5)
+            if b - a <= 128 // (heads // kv):
+                s, sees, _ = scores(q[r, a:b], keys[i][r], lens[i] - (b - a), dim ** -0.5)
+                p = torch.softmax(s.masked_fill(~sees, float("-inf")), -1)
+                mass = torch.einsum("hgts,shd->thgd", p, values[i][r].double().abs()).flatten(1, 2)
+                slack = slack - (2.0 ** -8 - 2.0 ** -16) * mass
+            close(out[r, a:b], o, slack, f"{i}")
