@@ -460,15 +460,19 @@ __global__ void __launch_bounds__(128) prompt_join_few_kernel(const __grid_const
   if (lane == 0 && a.lse[rank] != nullptr) a.lse[rank][(int64_t)token * a.q_heads + query] = (top + log2f(sum)) / kLog2e;
 }
 
-// Weight and score gradient of a score s that the row sees; one that it sees alone has none (and would have what
-// roundings leave of dp - delta), unless it is no number.
-__device__ __forceinline__ void weigh(float s, float dp, bool seen, bool alone, float scale2, float lse2, float delta, float* p,
-                                      float* ds) {
-  *p = seen ? exp2_fast(fmaf(s, scale2, -lse2)) : 0.f;
-  *ds = seen ? *p * (dp - delta) * (alone ? 0.f : 1.f) : 0.f;
+// Weight of a score s. The difference from lse is taken ahead of the base's factor: the weight is off by roundings of the
+// difference, not of scores and lse in another base, and is 1 where the two are the same. (With delta from the same dp, 2
+// tokens of 2 / 1 heads of 128: dq off by 1.5e-7 of its norm, where it was 3.3e-7.)
+__device__ __forceinline__ float weight_of(float s, bool seen, float scale, float lse) {
+  return seen ? exp2_fast(fmaf(s, scale, -lse) * kLog2e) : 0.f;
+}
+// A score that a row sees alone has none (and would have what roundings leave of dp - delta), unless it is no number.
+__device__ __forceinline__ float score_gradient(float p, float dp, bool seen, bool alone, float delta) {
+  return seen ? p * (dp - delta) * (alone ? 0.f : 1.f) : 0.f;
 }
 
-// dq of BT rows, and delta of each for the other kernel.
+// dq of BT rows, and delta of each for the other kernel. Delta by way of the result has the roundings of other sums than
+// dO . v has; over few keys, where the two nearly cancel, they count.
 template <typename T, int DP, int BT>
 __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_kernel(const __grid_constant__ PromptBwdArgs a) {
   using S = Shape<DP, BT>;
@@ -495,9 +499,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
   __syncthreads();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   int sees[S::MT];
-  float lse2[S::MT], delta[S::MT];
+  float lse[S::MT], delta[S::MT];
   Sums<DP, BT> dq;
   dq.zero();
+  const int most = (row0 + rows - 1) / group + 1;
+  const bool whole = most <= BT;  // all keys of the rows are in one tile: delta is the sum of p (dO . v), at hand there
+  float* const deltas = reinterpret_cast<float*>(a.ws + kOpScratchOffset) + (int64_t)rank * a.tokens * a.q_heads;
 #pragma unroll
   for (int i = 0; i < S::MT; i++) {
     const int r = ty + 16 * i;
@@ -505,16 +512,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
     for (int d = tx; d < DP; d += 16) x = fmaf(sg[r * S::LD + d], sk[r * S::LD + d], x);
     delta[i] = sum16(x);
     sees[i] = r < rows ? (row0 + r) / group + 1 : 0;
-    lse2[i] = 0.f;
+    lse[i] = 0.f;
     if (r < rows) {
       const int64_t at = token_of(r) * a.q_heads + head_of(r);
-      lse2[i] = a.lse[rank][at] * kLog2e;
-      if (tx == 0)
-        reinterpret_cast<float*>(a.ws + kOpScratchOffset)[(int64_t)rank * a.tokens * a.q_heads + at] = delta[i];
+      lse[i] = a.lse[rank][at];
+      if (tx == 0 && !whole) deltas[at] = delta[i];
     }
   }
-  const int most = (row0 + rows - 1) / group + 1;
-  const float scale2 = a.scale * kLog2e;
   for (int j0 = 0; j0 < most; j0 += BT) {
     __syncthreads();
     auto key = [&](const void* base, int64_t stride, int64_t head_stride, int r) {
@@ -532,13 +536,23 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_rows_ke
     }
     dots<DP, BT>(sq, sk, D, s);
 #pragma unroll
-    for (int i = 0; i < S::MT; i++)
+    for (int i = 0; i < S::MT; i++) {
+      const int r = ty + 16 * i;
+      float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < S::MT; j++) {
-        float p, ds;
-        weigh(s[i][j], dp[i][j], j0 + tx + 16 * j < sees[i], sees[i] == 1, scale2, lse2[i], delta[i], &p, &ds);
-        sp[(ty + 16 * i) * S::LP + tx + 16 * j] = ds;
+        const bool seen = j0 + tx + 16 * j < sees[i];
+        s[i][j] = weight_of(s[i][j], seen, a.scale, lse[i]);
+        if (seen) sum = fmaf(s[i][j], dp[i][j], sum);
       }
+      if (whole) {
+        delta[i] = sum16(sum);
+        if (r < rows && tx == 0) deltas[token_of(r) * a.q_heads + head_of(r)] = delta[i];
+      }
+#pragma unroll
+      for (int j = 0; j < S::MT; j++)
+        sp[r * S::LP + tx + 16 * j] = score_gradient(s[i][j], dp[i][j], j0 + tx + 16 * j < sees[i], sees[i] == 1, delta[i]);
+    }
     __syncwarp();
     dq.add(sp, sk);
   }
@@ -576,7 +590,6 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
   Sums<DP, BT> dk, dv;
   dk.zero();
   dv.zero();
-  const float scale2 = a.scale * kLog2e;
   const float* deltas = reinterpret_cast<const float*>(a.ws + kOpScratchOffset) + (int64_t)rank * a.tokens * a.q_heads;
   const int64_t tiles = div_up((int64_t)(seq.length - j0) * group, BT);
   const int first = j0 * group + (int)(tiles * part / split.parts) * BT, last = j0 * group + (int)(tiles * (part + 1) / split.parts) * BT;
@@ -592,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
     if (kApart<DP>) load_rows<T, DP, BT>(sg, D, [&](int r) { return row_of(a.dout[rank], a.dout_stride, a.dout_head, r); });
     for (int r = threadIdx.x; r < BT; r += kThreads) {
       const int64_t at = r < rows ? token_of(r) * a.q_heads + head_of(r) : 0;
-      slse[r] = r < rows ? a.lse[rank][at] * kLog2e : 0.f;
+      slse[r] = r < rows ? a.lse[rank][at] : 0.f;
       sdelta[r] = r < rows ? deltas[at] : 0.f;
     }
     __syncthreads();
@@ -610,10 +623,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 96 ? 2 : 1) prompt_bwd_keys_ke
       for (int j = 0; j < S::MT; j++) {
         const int r = tx + 16 * j, c = ty + 16 * i;
         const bool seen = r < rows && c < keys && j0 + c <= (row0 + r) / group;
-        float p, ds;
-        weigh(s[i][j], dp[i][j], seen, row0 + r < group, scale2, slse[r], sdelta[r], &p, &ds);
+        const float p = weight_of(s[i][j], seen, a.scale, slse[r]);
         sp[c * S::LP + r] = p;
-        sd[c * S::LP + r] = ds;
+        sd[c * S::LP + r] = score_gradient(p, dp[i][j], seen, row0 + r < group, sdelta[r]);
       }
     __syncwarp();  // a row's weights are written and read by the same half warp
     dv.add(sp, sg);

@@ -1,12 +1,12 @@
 """GPU tests of what the prompt operators do at their edges: tensors laid out in other ways, waits that run out of
-time, single keys that are no numbers, what the roundings of weights leave."""
+time, single keys that are no numbers, what the roundings of weights leave, weights and gradients of few keys."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
 from collective_communication_gb300 import binding as B
 from test_gpu_prompt_operators import (DT, MARK, attend, backward, cached_forward, close, forward, gen, i32, normal, paged,
-                                       prompt_inputs, scores, starts_of, workspace)
+                                       prompt_inputs, scores, starts_of, U, workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -234,3 +234,37 @@ def test_cached_requests_of_few_tokens(new, lens, heads, kv, dim, page):
                 mass = torch.einsum("hgts,shd->thgd", p, values[i][r].double().abs()).flatten(1, 2)
                 slack = slack - (2.0 ** -8 - 2.0 ** -16) * mass
             close(out[r, a:b], o, slack, f"{i}")
+
+
+PLAIN = [(64, "f32"), (80, "f32"), (128, "f32"), (200, "f32"), (192, "bf16")]  # forms of the ordinary arithmetic units
+
+
+@pytest.mark.parametrize("dim,dtype", PLAIN, ids=str)
+def test_weight_of_a_score_that_is_lse(dim, dtype):
+    """A score and an lse that are the same number leave a weight of 1, exactly, however large they are: dv is dout."""
+    score = torch.tensor([0.0, 1.0, -3.0, 100.0, 123.25, -77.5, 1000.0, 3.0, -4096.0], device="cuda").to(DT[dtype])
+    n = len(score)
+    q, k = (torch.zeros(1, n, 1, dim, dtype=DT[dtype], device="cuda") for _ in range(2))
+    q[0, :, 0, 3], k[0, :, 0, 3] = score, 1.0  # products and sums are exact
+    v, dout = (normal(gen(i), 1, n, 1, dim, dtype=q.dtype) for i in (1, 2))
+    dq, dk, dv = backward(q, k, v, starts_of([1] * n), v, score.float().view(1, n, 1), dout, scale=1.0)
+    assert torch.equal(dv, dout) and bool((dq == 0).all()) and bool((dk == 0).all())
+
+
+@pytest.mark.parametrize("dim,dtype", PLAIN, ids=str)
+def test_gradient_of_keys_that_are_alike(dim, dtype):
+    """Two equal keys of equal values have no gradient. Their dO . v are the same bits x, and so are their weights, 1/2 up to
+    4 U for the exponential, 2 U for its exponent and U for lse: 1/2 (1 + d), d below 8 U. The sum of p x is x (1 + d) up to
+    2 U x, so a score's gradient is below 1/2 (8 + 2 + 1) U |x|: 8 U |x|, where a sum of out . dout is off by some U of the
+    sum of the magnitudes, hundreds of times |x| here. dq and dk of the second token are these, times scale and k, or q."""
+    k = normal(gen(1), 1, 1, 1, dim, dtype=DT[dtype]).expand(1, 2, 1, dim).contiguous()
+    v = normal(gen(2), 1, 1, 1, dim, dtype=DT[dtype]).expand(1, 2, 1, dim).contiguous()
+    q = torch.zeros_like(k)  # scores of 0: lse is the logarithm of 2
+    x = normal(gen(3), dim).double()
+    y = v[0, 0, 0].double()
+    dout = (x - (x @ y) / (y @ y) * y).to(q.dtype).expand(1, 2, 1, dim).contiguous()  # across the value, but for its rounding
+    out, lse = forward(q, k, v, starts_of([2]), scale=0.5)
+    dq, dk, dv = backward(q, k, v, starts_of([2]), out, lse, dout, scale=0.5)
+    dot = abs(float(dout[0, 1, 0].double() @ y)) + 2 * dim * U * float((dout[0, 1, 0].double() * y).abs().sum())
+    assert bool((dq[0, 1, 0].double().abs() <= 2 * 0.5 * 8 * U * dot * k[0, 1, 0].double().abs()).all())
+    assert bool((dk == 0).all())  # queries of 0
