@@ -60,9 +60,9 @@ struct Limit {
   uint64_t ns;
 };
 __device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile Limit* limit) {
-  const uint64_t until = global_timer_ns() + limit->ns;
+  const uint64_t since = global_timer_ns();
   while (!try_wait(b, parity)) {
-    if (global_timer_ns() > until) limit->dead = 1;
+    if (global_timer_ns() - since > limit->ns) limit->dead = 1;
     if (limit->dead) return false;
   }
   return true;
@@ -84,11 +84,11 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile Limi
 // slots of those that work (without it the gradient of 8192 tokens, heads of 64, took 589 us for 562).
 __device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile Limit* limit) {
   if (__all_sync(~0u, try_wait(b, parity))) return true;
-  const uint64_t until = global_timer_ns() + limit->ns;
+  const uint64_t since = global_timer_ns();
 #pragma unroll 1
   while (true) {
     if (__all_sync(~0u, try_wait(b, parity))) return true;
-    const bool late = global_timer_ns() > until;
+    const bool late = global_timer_ns() - since > limit->ns;
     if (late) limit->dead = 1;
     if (__any_sync(~0u, late || limit->dead)) return false;
   }

@@ -154,6 +154,21 @@ def test_gradient_runs_out_of_time(short_limit, lens, heads, kv, dim):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("limit", [2 ** 64 - 1, 2 ** 63])
+def test_no_limit_at_all(limit):
+    """The largest limits are limits like any other."""
+    q, k, v, starts = prompt_inputs(1, [2000, 50], 8, 1, 128, "bf16")
+    want = forward(q, k, v, starts)
+    grads = backward(q, k, v, starts, *want, q)
+    B.set_spin_timeout_ns(limit)
+    try:
+        got = forward(q, k, v, starts)
+        again = backward(q, k, v, starts, *got, q)
+    finally:
+        B.set_spin_timeout_ns(0)
+    assert all(torch.equal(a, b) for a, b in zip((*got, *again), (*want, *grads)))
+
+
 # ---------------------------------------------------------------- what is no number
 @pytest.mark.parametrize("bad", ["q", "k", "v", "dout"])
 @pytest.mark.parametrize("lens", [[3, 1, 40], [3, 1, 200]], ids=str)
