@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
     const int row = threadIdx.x & 127, token = row / group, in_group = row % group;
     // of a negative scale or none, the scores are turned or cleared first, so that the largest is the one that counts
     const float scale2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
-    const uint32_t turn = a.scale < 0.f ? 0x80000000u : 0u, keep_bits = a.scale == 0.f ? 0u : ~0u;
+    const float turn = a.scale < 0.f ? -1.f : 0.f;
     int walked = 0, results = 0, seen = 0, queries = 0;  // queries: tiles of queries of both tiles of rows
     for (int i = 0;; i++) {
       if (!wait(&item_full[i % kItemSlots], i / kItemSlots & 1, limit)) break;
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
         }
         if (!(a.scale > 0.f)) {
 #pragma unroll
-          for (int c = 0; c < kKeys; c++) s[c] = (s[c] ^ turn) & keep_bits;
+          for (int c = 0; c < kKeys; c++) s[c] = __float_as_uint(__uint_as_float(s[c]) * turn);
         }
         const uint32_t* holes_of = lost[(seen + j - begin) % kLostSlots];
         const bool holes = FORM != kDense && (holes_of[0] | holes_of[1] | holes_of[2] | holes_of[3]) != 0;

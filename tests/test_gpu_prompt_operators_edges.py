@@ -196,6 +196,21 @@ def test_gradient_of_one_key_that_is_no_number(dim, dtype, lens, bad):
             assert torch.equal(a[:, :3], b[:, :3]) and torch.equal(a[:, 4:], b[:, 4:])
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.5, 0.5])
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (128, "bf16"), (192, "bf16"), (64, "f32")], ids=str)
+def test_scores_that_are_no_numbers(dim, dtype, scale):
+    """A query or key of NaN shows in the rows that see it, whatever the scale; another sequence's do not change."""
+    q, k, v, starts = prompt_inputs(1, [40, 200, 30], 4, 2, dim, dtype, seed=2)
+    want, want_lse = forward(q, k, v, starts, scale=scale)
+    q[:, 50, 1], k[:, 140, 1, 5] = float("nan"), float("nan")
+    out, lse = forward(q, k, v, starts, scale=scale)
+    bad = torch.zeros(1, 270, 4, dtype=torch.bool, device="cuda")
+    bad[:, 50, 1] = True
+    bad[:, 140:240, 2:] = True
+    assert torch.equal(lse.isnan(), bad) and bool(out[bad].isnan().all())
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
+
+
 # ---------------------------------------------------------------- roundings of weights
 @pytest.mark.parametrize("lens", [[2, 300, 17, 1, 128, 129, 90], [5] * 70, [128, 1000, 3]], ids=str)
 @pytest.mark.parametrize("dim", [64, 80, 128])
