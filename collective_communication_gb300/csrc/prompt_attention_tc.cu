@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(Threads<FORM>::kCount, 1) prompt_tc_kernel(con
   bool ordered = false;
   if (warp == kItemWarp) {
     ordered = order.begin(a.starts, a.sequences, a.tokens, 2 * per_tile);
-    if (FORM != kDense && ordered && lane < a.sequences) {
+    if (FORM != kDense && ordered && order.items > 0) {  // (a request with no new tokens is not looked at)
       PromptSequence seq = {lane, order.first, order.length, 0, order.length};
       cached_sequence(a, &seq);
       order.before = seq.before;

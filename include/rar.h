@@ -606,7 +606,8 @@ RAR_API rar_status rar_token_logprobs_backward(const void* const* logits, const 
  *   starts and lens_out), so its i-th sees those up to position
  *   lens[s] - (starts[s + 1] - starts[s]) + i. A row whose position is negative sees
  *   nothing: out 0, lse -inf. What is past a length or in a page that is none is not
- *   read, and reports as in rar_decode_attention.
+ *   read, and reports as in rar_decode_attention; of a request with no tokens in the call
+ *   nothing is looked at.
  * rar_prompt_attention_backward: dq, dk and dv from the gradient dout of out, with
  *   out and lse of the forward call. dk and dv are sums over the query heads of a group.
  *   No gradient goes through lse. The same bits every time. A row that sees one key has

@@ -94,6 +94,21 @@ def test_forward_result_of_torch():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("requests", [3, 40])
+@pytest.mark.parametrize("dim,page,dtype", [(64, 16, "bf16"), (128, 2, "bf16"), (64, 16, "f32")], ids=str)
+def test_cached_requests_without_tokens(dim, page, dtype, requests):
+    """Whatever the length and pages of a request are that has no tokens in the call: nothing is looked at or reported."""
+    new, lens = [4, 0, 7] + [0] * (requests - 3), [30, 9, 20] + [5] * (requests - 3)
+    k, v, table, _, _ = paged(gen(3), 1, lens, 2, dim, page, DT[dtype])
+    q = normal(gen(4), 1, sum(new), 4, dim, dtype=DT[dtype])
+    starts = starts_of(new)
+    want = cached_forward(q, k, v, table, starts, i32(*lens))
+    for bad in (-1, 2 ** 30):
+        lens[1] = bad
+        table[1] = -5
+        assert all(torch.equal(a, b) for a, b in zip(cached_forward(q, k, v, table, starts, i32(*lens)), want))
+
+
 # ---------------------------------------------------------------- waits that run out
 @pytest.fixture
 def short_limit():
