@@ -18,8 +18,8 @@
 // result's own, over few keys or many: out is off by 1.9 to 2.1e-3 of its norm, where its own
 // rounding is 1.6e-3. What it leaves would take a second product: 686 -> 977 us for 16384
 // tokens, 115 -> 147 for 8192 packed ones, 306 -> 422 for chunks. A cached request of one tile of
-// rows (128 / group new tokens: drafts behind a long context) has it (21.3 -> 24 us for five
-// tokens behind 30011, 2.3e-3 -> 1.7e-3), so that these tokens come out as close as one by one from
+// rows (128 / group new tokens: drafts behind a long context) has it (20.4 -> 22.4 us for five
+// tokens behind 30011, 58 -> 73 for eight such requests; 2.3e-3 -> 1.7e-3), so that these tokens come out as close as one by one from
 // decode_attention.cu, which has it too. The second tile's columns are free there.
 //
 // Blocks stay, one an SM, and take items from a counter, those with the most keys

@@ -266,7 +266,10 @@ __device__ __forceinline__ void weights_by_rows(uint32_t lead, uint32_t d, uint3
 }
 
 // What the bf16 pair `to` leaves of x and y, as another.
-__device__ __forceinline__ uint32_t bf16_rest(float x, float y, uint32_t to) { return bf16_pair(x - bf16_lo(to), y - bf16_hi(to)); }
+__device__ __forceinline__ uint32_t bf16_rest(float x, float y, uint32_t to) {
+  const float2 r = unpack(fma2(f2(bf16_lo(to), bf16_hi(to)), f2(-1.f, -1.f), f2(x, y)));
+  return bf16_pair(r.x, r.y);
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
