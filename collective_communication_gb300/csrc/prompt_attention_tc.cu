@@ -60,10 +60,12 @@ namespace {
 using namespace tc;
 
 // Where keys and values are, and how they are copied: dense, in pages by TMA, or in
-// pages by the lanes of a fourth warpgroup. TMA takes a box or two a page: with pages of
-// fewer than 8 tokens a tile's boxes took longer to issue than its products to run
-// (chunks of 2048 tokens of the largest case, 6.2 GB of copies: pages of 1, 4, 16 and 64
-// tokens 3170, 932, 447 and 350 us by TMA in boxes of 64 elements, 403 us by lanes).
+// pages by the lanes of a fourth warpgroup. TMA takes a box a page (two for heads of 72 to
+// 120), and with small pages a tile's boxes take longer to issue than its products to run;
+// lanes take as long whatever the pages are. Chunks of 2048 tokens of 6 requests behind up to
+// 8192, 64 / 8 heads, us by TMA in pages of 8, 16 and 32 tokens, and by lanes: heads of 40 293,
+// 253, 253 and 285; of 64 293, 260, 258 and 280; of 80 474, 312, 276 and 323; of 120 478, 321,
+// 300 and 350; of 128 328, 301, 300 and 339.
 enum Form { kDense, kPages, kLanes };
 // Two softmax warpgroups, one of which each warp has a part of its own, and the one that
 // copies keys and values. The registers that a block starts with (168 a thread of 384,
@@ -967,7 +969,7 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t stream) {
 cudaError_t launch_prompt_attention_tc(const PromptArgs& a, cudaStream_t stream) {
   const bool small = a.head_dim <= 64;
   if (a.table == nullptr) return small ? launch<64, kDense>(a, stream) : launch<128, kDense>(a, stream);
-  if (a.page_shift >= 3) return small ? launch<64, kPages>(a, stream) : launch<128, kPages>(a, stream);
+  if (a.page_shift >= (a.head_dim == 128 ? 3 : 4)) return small ? launch<64, kPages>(a, stream) : launch<128, kPages>(a, stream);
   return small ? launch<64, kLanes>(a, stream) : launch<128, kLanes>(a, stream);
 }
 

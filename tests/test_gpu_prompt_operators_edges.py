@@ -109,6 +109,21 @@ def test_cached_requests_without_tokens(dim, page, dtype, requests):
         assert all(torch.equal(a, b) for a, b in zip(cached_forward(q, k, v, table, starts, i32(*lens)), want))
 
 
+@pytest.mark.parametrize("new,lens", [([5], [2000]), ([40, 130, 0, 3], [300, 130, 17, 129])], ids=str)
+@pytest.mark.parametrize("dim", [40, 64, 72, 128])
+def test_cached_in_pages_of_any_size(dim, new, lens):
+    """Pages on both sides of the sizes at which they are copied in another way: the same bits."""
+    g = gen(5)
+    q = normal(g, 2, sum(new), 4, dim, dtype=torch.bfloat16)
+    starts, first = starts_of(new), None
+    for page in (4, 8, 16, 32):
+        k, v, table, keys, values = paged(gen(6), 2, lens, 2, dim, page, torch.bfloat16, extra_columns=0)
+        table = torch.cat([table, table.new_full((len(lens), 2048 // page - table.shape[1]), -7)], 1)  # as wide in tokens
+        found = cached_forward(q, k, v, table, starts, i32(*lens))
+        first = first or found
+        assert all(torch.equal(x, y) for x, y in zip(first, found))
+
+
 # ---------------------------------------------------------------- waits that run out
 @pytest.fixture
 def short_limit():
