@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
       // the score gradients of key tile j; ONE: it is all that the rows see
       auto work_out = [&](auto one, int j) {
         constexpr bool ONE = decltype(one)::value;
-        wait_lane(&dp_full, n & 1, limit);  // S of the tile was issued ahead of it
+        if (!wait(&dp_full, n & 1, limit)) return false;  // S of the tile was issued ahead of it
         fence_after();
         const uint32_t from = s_at + (n & 1) * 128 + quarter + slice * kColumns;
         uint32_t s[kColumns], dp[kColumns];
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_rows_tc_kernel(const __gri
         }
         arrive_warp(&ds_ready);
         n++;
-        return !ended_early(limit);
+        return true;
       };
       bool fine = true;
       if (tiles == 1) fine = work_out(std::true_type{}, 0);
@@ -728,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         constexpr bool RESTS = decltype(with_rests)::value;
         const int stage = n % NS;
         // the rows' numbers, and their scores
-        wait_lane(&full[stage], n / NS & 1, limit);
-        wait_lane(&s_full[n % SB], n / SB & 1, limit);
+        if (!wait(&full[stage], n / NS & 1, limit)) return false;
+        if (!wait(&s_full[n % SB], n / SB & 1, limit)) return false;
         fence_after();
         const uint32_t from = s_at + n % SB * 128 + quarter + c0, dp_from = dp_at + quarter + c0;
         uint32_t s[kColumns], w[kColumns / 2];
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
           tmem_store16(from + kColumns / 2, w);
         }
         arrive_warp(&p_ready[n % SB]);
-        wait_lane(&dp_full, n & 1, limit);
+        if (!wait(&dp_full, n & 1, limit)) return false;
         fence_after();
         uint32_t g[kColumns];
         tmem_load32(dp_from, g);
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_keys_tc_kernel(const __gri
         arrive_warp(&ds_ready);
         if (lane == 0) arrive(&empty[stage]);  // the rows' numbers have been read
         n++;
-        return !ended_early(limit);
+        return true;
       };
       bool fine = true;
       if (rests_of(t))

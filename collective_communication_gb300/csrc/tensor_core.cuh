@@ -59,7 +59,10 @@ struct Limit {
   int dead;
   uint64_t ns;
 };
-__device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile Limit* limit) {
+__device__ __forceinline__ bool wait_lane(uint64_t* b, uint32_t parity, volatile Limit* limit) {
+#pragma unroll 1
+  for (int i = 0; i < 16; i++)
+    if (try_wait(b, parity)) return true;
   const uint64_t since = global_timer_ns();
   while (!try_wait(b, parity)) {
     if (global_timer_ns() - since > limit->ns) limit->dead = 1;
@@ -67,16 +70,9 @@ __device__ __forceinline__ bool wait_long(uint64_t* b, uint32_t parity, volatile
   }
   return true;
 }
-// Waits for the phase of `parity` to end. False once any wait of the block has run past the limit: every role then leaves
-// its loops. Lanes may find differently, and what a warp does together needs them all: it goes on, and asks ended_early() later.
-__device__ __forceinline__ bool wait_lane(uint64_t* b, uint32_t parity, volatile Limit* limit) {
-#pragma unroll 1
-  for (int i = 0; i < 16; i++)
-    if (try_wait(b, parity)) return true;
-  return wait_long(b, parity, limit);
-}
-__device__ __forceinline__ bool ended_early(volatile Limit* limit) { return __any_sync(~0u, limit->dead); }
-// The same answer for all lanes of a warp.
+// A warp waits for the phase of `parity` to end. False, for all its lanes, once any wait of the block has run past the
+// limit: every role then leaves its loops. (Lanes that went by what each of them found could part ahead of what a warp does
+// together.)
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile Limit* limit) {
   return __all_sync(~0u, wait_lane(b, parity, limit));
 }
