@@ -30,17 +30,17 @@
 // Blocks stay, one an SM, and take items (a tile of rows, or of keys) from a counter;
 // a warp finds the next one while the last is under way, and its first tiles are copied.
 //
-// Measured: 8192 tokens of one sequence, 16 query heads on 4 key heads of 64: 526 to 536
-// us, 220 for the rows and 298 for the keys, 0.9 PFLOP/s of the seven products. What bounds
-// it is the weights' chain, from scores through two roundings to the last product, as long
-// for half the products of a head size of 128: tensor cores 38 % of the time, issue slots
-// 46 %. Keys have two buffers of scores there, so that the next tile's are ready when the
-// weights are done with this one (one buffer, as tensor memory allows at 128: 561 us).
-// 4097 tokens of 9 sequences, 32 query heads on 8 key heads of 128: 141 us, 16 of them
+// Measured: 8192 tokens of one sequence, 16 query heads on 4 key heads of 64: 542 us, 0.9 PFLOP/s of the
+// seven products. What bounds it is the weights' chain, from scores through two roundings to the last
+// product, as long for half the products of a head size of 128: tensor cores 36 % of the time, issue
+// slots 37 to 48 %. Keys have two buffers of scores there, so that the next tile's are ready when the
+// weights are done with this one (one buffer, as tensor memory allows at 128: 561 us, 536 with two, before
+// warps decided together whether a wait had run out, which costs 2 %).
+// 4097 tokens of 9 sequences, 32 query heads on 8 key heads of 128: 151 us, 16 of them
 // delta (cold; out and dout from memory); the keys that most rows see are 27 tiles of rows
 // where an SM has 20 on average. Queries of the next item ahead in a buffer of their own,
-// for fewer tiles of keys and values, took as long, and 800 us where this takes 715 (8192
-// tokens, 16 query heads on 2 key heads of 128).
+// for fewer tiles of keys and values, took as long, and 800 us for 715 (8192
+// tokens, 16 query heads on 2 key heads of 128; 727 now).
 #include <type_traits>
 
 #include "prompt_attention.cuh"

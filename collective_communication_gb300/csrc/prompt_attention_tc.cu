@@ -38,15 +38,15 @@
 // second kernel adds them up in the order of the keys, a block a row, or a warp a row
 // where there are few parts (prompt_attention.cu).
 //
-// Measured: 16384 tokens of one sequence, 16 query heads on 2 key heads of 128: 610 us,
-// 1.8 PFLOP/s, where a plain matrix product makes 1.95 in a burst and 1.73 over seconds,
-// with lower clocks; chunks of 2048 tokens behind up to 8192 cached ones, 64 heads on 8,
-// pages of 16: 293 us, tensor cores 68 % of the time. 8192 tokens in 17 sequences: 114 us,
-// tensor cores 42 %: items are over before the chain of their products and weights has
+// Measured: 16384 tokens of one sequence, 16 query heads on 2 key heads of 128: 613 us in runs of
+// milliseconds, 650 to 695 in longer ones with lower clocks, 1.58 to 1.79 PFLOP/s, where a plain
+// matrix product makes 1.95 in a burst and 1.73 over seconds; chunks of 2048 tokens behind up to 8192
+// cached ones, 64 heads on 8, pages of 16: 294 to 304 us, tensor cores 70 % of the time. 8192 tokens in
+// 17 sequences: 115 us, tensor cores 41 %: items are over before the chain of their products and weights has
 // filled the SM, and reading and writing rows takes 45 us of it at the memory's rate.
-// Heads of 64 take 550 us for the 16384 tokens: the exponentials bound them, as many
-// for half the products. Five tokens behind 30011 take 21 us, a chain of a block's start,
-// its share of the keys and the join; 97 tokens 7.8, a chain of one tile: the first item
+// Heads of 64 take 515 us for the 16384 tokens: the exponentials bound them, as many
+// for half the products. Five tokens behind 30011 take 23 us, a chain of a block's start,
+// its share of the keys and the join; 97 tokens 8, a chain of one tile: the first item
 // 1.5 us, copies 0.6, scores 0.4, weights 1.1, the product 0.4, rows 0.6.
 #include <type_traits>
 

@@ -512,7 +512,7 @@ RAR_API rar_status rar_qk_norm_rope_cached(const void* const* qkv, int nranks, i
                                            rar_dtype dtype, float eps, void* const* q_out, int64_t q_stride,
                                            void* const* k_cache, void* const* v_cache, int num_pages, int page_size,
                                            void* workspace, size_t workspaceBytes, void* stream);
-RAR_API size_t rar_qk_norm_rope_workspace_bytes(int nranks, int head_dim); /* of the backward call, also of fewer tokens; 0: bad arguments */
+RAR_API size_t rar_qk_norm_rope_workspace_bytes(int nranks, int head_dim); /* of the backward call; 0: bad arguments */
 RAR_API rar_status rar_qk_norm_rope_backward(const void* const* qkv, int nranks, int64_t tokens, int64_t qkv_stride,
                                              const void* q_weight, const void* k_weight, const float* cos_sin,
                                              int max_pos, int rot_dim, int interleaved, const int32_t* positions,
